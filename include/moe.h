@@ -398,6 +398,85 @@ int moe_bwd(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w
  */
 int moe_plan_set_bwd_timing_events(moe_plan* plan, void* const* events);
 
+/* ------------------------------------------------------------------ routing from given logits
+ *
+ * The general router: scores of given logits, an optional balance bias that
+ * takes part in the selection only, expert groups, top-k, and weights that may
+ * or may not be renormalised; with its gradient.  (moe_fwd's built-in router
+ * multiplies x by W_router itself, adds its bias to the logits and always
+ * renormalises.)
+ */
+typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype;
+
+/*
+ *   E            experts, 1..512
+ *   k            experts per token, 1..16, at most topk_group * E / n_group
+ *   n_group      groups of E / n_group consecutive experts, 1..32, dividing E; 1 = no groups
+ *   topk_group   groups kept per token, 1..n_group
+ *   score_fn     moe_score_fn: s = sigmoid(x), or softmax over the E logits
+ *   logits_dtype moe_dtype of the logits and of their gradient
+ *   group_top    a group's score is the sum of its group_top (1 or 2) largest keys
+ *   renormalize  1: w_i = scale s_i / (sum of the selected s); 0: w_i = scale s_i
+ *   scale        factor of the weights, finite
+ */
+typedef struct moe_route_config {
+  int64_t E;
+  int64_t k;
+  int64_t n_group;
+  int64_t topk_group;
+  int32_t score_fn;
+  int32_t logits_dtype;
+  int32_t group_top;
+  int32_t renormalize;
+  float scale;
+} moe_route_config;
+
+typedef struct moe_route_plan moe_route_plan;
+
+/* Validate `cfg` for the current CUDA device and create a plan (host memory
+ * only).  Errors as moe_plan_create. */
+int moe_route_plan_create(const moe_route_config* cfg, moe_route_plan** out);
+int moe_route_plan_destroy(moe_route_plan* plan);
+
+/* Device workspace of moe_route for T tokens, needed only when expert_counts
+ * or prob_sum is asked for (0 on bad input). */
+size_t moe_route_workspace_bytes(const moe_route_plan* plan, int64_t T);
+
+/*
+ * Route T tokens (T = 0: only the sums are written, as zeros).
+ *   logits        [T, E] of logits_dtype, rows logits_stride elements apart (0 = E)
+ *   bias          [E] fp32 or NULL: the selection ranks s + bias (without it the
+ *                 logits' own order); the weights do not see it
+ *   topk_idx      [T, k] int32: the selected experts, ascending id; -1 in the
+ *                 slots of a token with fewer than k experts to select
+ *   topk_w        [T, k] fp32: the weights, same order, 0 in an empty slot
+ *   expert_counts [E] int32 or NULL: routes per expert
+ *   prob_sum      [E] fp32 or NULL: sum over the tokens of s_e / sum_f s_f, the
+ *                 mean score that a load-balance loss is made of
+ * An expert whose logit is -inf or NaN is never selected (a row of them has no
+ * experts).  A NaN makes the row's softmax weights, and prob_sum, NaN.  Ties
+ * go to the lower id, of groups to the lower group.  The selection is that of
+ * exact arithmetic: rows whose keys lie closer than fp32 resolves are decided
+ * in fp64.  No floating-point atomics: two calls give the same bits.
+ * One launch, and a second one for the sums of more than 8 tokens.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
+ */
+int moe_route(const moe_route_plan* plan, int64_t T, const void* logits, int64_t logits_stride, const float* bias,
+              int32_t* topk_idx, float* topk_w, int32_t* expert_counts, float* prob_sum, void* workspace,
+              size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * The gradient of the logits, from dtopk_w = dL/d topk_w [T, k] fp32 and
+ * dprob_sum = dL/d prob_sum [E] fp32 or NULL, for the selection topk_idx that
+ * moe_route wrote (the selection itself has no gradient; a slot outside
+ * [0, E) is empty).  dlogits [T, E] of logits_dtype, every element written.
+ * dlogits must not overlap logits.  One launch, no workspace.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
+ */
+int moe_route_bwd(const moe_route_plan* plan, int64_t T, const void* logits, int64_t logits_stride,
+                  const int32_t* topk_idx, const float* dtopk_w, const float* dprob_sum, void* dlogits,
+                  int64_t dlogits_stride, moe_stream_t stream);
+
 /* Static description of an error code. */
 const char* moe_error_string(int code);
 

@@ -8,7 +8,9 @@ used only to hand over device pointers and streams.
 Entry points keep the C names: ``moe_plan_create``, ``moe_plan_destroy``,
 ``moe_workspace_bytes``, ``moe_quantize_mxfp8``, ``moe_mxfp8_scale_bytes``,
 ``moe_fwd``, ``moe_bwd_workspace_bytes``, ``moe_bwd``, ``moe_get_status``,
-``moe_get_phase_times``, ``moe_route_static``, ``moe_error_string``.
+``moe_get_phase_times``, ``moe_route_static``, ``moe_error_string``; routing from
+given logits: ``moe_route_plan_create``, ``moe_route_plan_destroy``,
+``moe_route_workspace_bytes``, ``moe_route``, ``moe_route_bwd``.
 """
 from __future__ import annotations
 
@@ -39,6 +41,8 @@ MOE_STATUS_OK, MOE_STATUS_TIMEOUT, MOE_STATUS_SCHEDULE_INVALID, MOE_STATUS_STAGI
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_PREC_BF16, MOE_PREC_MXFP8 = 0, 1
 MOE_DISPATCH_RING, MOE_DISPATCH_DIRECT, MOE_DISPATCH_SPREAD = 0, 1, 2
+MOE_DTYPE_FP32, MOE_DTYPE_BF16, MOE_DTYPE_FP16 = 0, 1, 2
+_DTYPES = {"fp32": MOE_DTYPE_FP32, "bf16": MOE_DTYPE_BF16, "fp16": MOE_DTYPE_FP16}
 
 
 class MoEError(RuntimeError):
@@ -72,6 +76,12 @@ class moe_grads(ctypes.Structure):
 class moe_outputs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "out", "topk_idx", "topk_w", "expert_counts", "expert_offsets", "sched", "route_row")]
+
+
+class moe_route_config(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int64), ("k", ctypes.c_int64), ("n_group", ctypes.c_int64),
+                ("topk_group", ctypes.c_int64), ("score_fn", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -114,6 +124,16 @@ def lib():
     L.moe_route_static.restype = ctypes.c_int
     L.moe_route_static_scratch_bytes.argtypes = []
     L.moe_route_static_scratch_bytes.restype = sz
+    L.moe_route_plan_create.argtypes = [ctypes.POINTER(moe_route_config), ctypes.POINTER(vp)]
+    L.moe_route_plan_create.restype = ctypes.c_int
+    L.moe_route_plan_destroy.argtypes = [vp]
+    L.moe_route_plan_destroy.restype = ctypes.c_int
+    L.moe_route_workspace_bytes.argtypes = [vp, i64]
+    L.moe_route_workspace_bytes.restype = sz
+    L.moe_route.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_route.restype = ctypes.c_int
+    L.moe_route_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]
+    L.moe_route_bwd.restype = ctypes.c_int
     L.moe_error_string.argtypes = [ctypes.c_int]
     L.moe_error_string.restype = ctypes.c_char_p
     _lib = L
@@ -318,3 +338,62 @@ def moe_route_static(plan: Plan, T: int, x, W_router, b_router, topk_idx, topk_w
 
 def moe_route_static_scratch_bytes() -> int:
     return int(lib().moe_route_static_scratch_bytes())
+
+
+class RoutePlan:
+    """Owns a moe_route_plan*; released by moe_route_plan_destroy (or garbage collection)."""
+
+    def __init__(self, handle: int, cfg: moe_route_config):
+        self.handle = handle
+        self.cfg = cfg
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.moe_route_plan_destroy(self.handle)
+            self.handle = None
+
+
+def moe_route_plan_create(E, k, score_fn=MOE_SCORE_SIGMOID, logits_dtype=MOE_DTYPE_FP32, n_group=1, topk_group=1,
+                          group_top=2, renormalize=True, scale=1.0) -> RoutePlan:
+    """Plan of the general router (``moe_route``, ``moe_route_bwd``)."""
+    if isinstance(score_fn, str):
+        score_fn = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}[score_fn]
+    if isinstance(logits_dtype, str):
+        logits_dtype = _DTYPES[logits_dtype]
+    cfg = moe_route_config(E, k, n_group, topk_group, score_fn, logits_dtype, group_top, int(renormalize), scale)
+    h = ctypes.c_void_p()
+    rc = lib().moe_route_plan_create(ctypes.byref(cfg), ctypes.byref(h))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_route_plan_create")
+    return RoutePlan(h.value, cfg)
+
+
+def moe_route_plan_destroy(plan: RoutePlan) -> None:
+    if plan.handle:
+        lib().moe_route_plan_destroy(plan.handle)
+        plan.handle = None
+
+
+def moe_route_workspace_bytes(plan: RoutePlan, T: int) -> int:
+    return int(lib().moe_route_workspace_bytes(plan.handle, T))
+
+
+def moe_route(plan: RoutePlan, T: int, logits, bias, topk_idx, topk_w, expert_counts=None, prob_sum=None,
+              workspace=None, workspace_bytes: int | None = None, logits_stride: int = 0, stream=None) -> None:
+    """Scores, selection (bias, groups, top-k) and weights of ``logits`` [T, E];
+    ``expert_counts`` and ``prob_sum`` are the sums a balance bias or loss needs."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = lib().moe_route(plan.handle, T, _ptr(logits), logits_stride, _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
+                         _ptr(expert_counts), _ptr(prob_sum), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_route")
+
+
+def moe_route_bwd(plan: RoutePlan, T: int, logits, topk_idx, dtopk_w, dlogits, dprob_sum=None, logits_stride: int = 0,
+                  dlogits_stride: int = 0, stream=None) -> None:
+    """Gradient of the logits from those of ``topk_w`` and (optionally) ``prob_sum``."""
+    rc = lib().moe_route_bwd(plan.handle, T, _ptr(logits), logits_stride, _ptr(topk_idx), _ptr(dtopk_w),
+                             _ptr(dprob_sum), _ptr(dlogits), dlogits_stride, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_route_bwd")

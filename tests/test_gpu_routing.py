@@ -1,0 +1,424 @@
+"""moe_route and moe_route_bwd against a plain fp64 implementation.
+
+Tolerances: the selection and the counts are exact.  Weights: exp (2 ulp), a
+sum of k terms, a quotient and a product, each half an ulp of fp32 or a few of
+them: 16 * 2^-24 relative covers sigmoid; softmax adds the rounding of x - m,
+|x - m| 2^-24 relative, at most 32 for these logits.  The gradient is rounded
+once to its type, and its terms cancel (a - q sum a): the fp32 error counts
+against the largest term of the row, not against the result."""
+import numpy as np
+import pytest
+import torch
+
+import routing_grouped_expert_gemm_gb300 as rg
+
+DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+U32 = 2.0 ** -24
+HALF_ULP = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+
+
+def scores(x, fn):
+    if fn == "sigmoid":
+        with np.errstate(over="ignore"):
+            return np.where(np.isneginf(x), 0.0, 1.0 / (1.0 + np.exp(-x)))
+    m = x.max(1, keepdims=True)
+    e = np.exp(x - np.where(np.isneginf(m), 0.0, m))
+    z = e.sum(1, keepdims=True)
+    return e / np.where(z == 0, 1.0, z)
+
+
+def log_scores(x, fn):
+    """Up to a constant per row (what a renormalised weight needs, without underflow)."""
+    with np.errstate(over="ignore"):
+        return x if fn == "softmax" else np.where(np.isneginf(x), -np.inf, -np.logaddexp(0.0, -x))
+
+
+def plain_route(x, bias, k, fn, n_group, topk_group, group_top, renorm, scale):
+    """Row by row, from the definition."""
+    T, E = x.shape
+    s, ls = scores(x, fn), log_scores(x, fn)
+    idx = np.full((T, k), -1, np.int32)
+    w = np.zeros((T, k))
+    counts = np.zeros(E, np.int64)
+    gs = E // n_group
+    for t in range(T):
+        live = [e for e in range(E) if x[t, e] > -np.inf]
+        key = x[t] if bias is None else s[t] + bias
+        val = s[t] if bias is None else key
+        if n_group > 1:
+            rank = []
+            for g in range(n_group):
+                v = sorted((val[e] for e in live if e // gs == g), reverse=True)[:group_top]
+                rank.append((-sum(v) if v else np.inf, g))
+            keep = {g for _, g in sorted(rank)[:topk_group]}
+            live = [e for e in live if e // gs in keep]
+        sel = sorted(sorted(live, key=lambda e: (-key[e], e))[:k])
+        for i, e in enumerate(sel):
+            idx[t, i] = e
+            counts[e] += 1
+        if sel:
+            if renorm:
+                l = ls[t, sel]
+                u = np.exp(l - l.max())
+                w[t, :len(sel)] = scale * u / u.sum()
+            else:
+                w[t, :len(sel)] = scale * s[t, sel]
+    l = np.exp(ls - np.where(np.isneginf(ls.max(1, keepdims=True)), 0.0, ls.max(1, keepdims=True)))
+    tot = l.sum(1, keepdims=True)
+    return idx, w, counts, (l / np.where(tot == 0, 1.0, tot)).sum(0)
+
+
+def run_route(x, bias, cfg, sums=True, stride=0, stream=None):
+    T, E = x.shape[0], cfg["E"]
+    plan = rg.moe_route_plan_create(**cfg)
+    k = cfg["k"]
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), float("nan"), device="cuda")
+    cnt = torch.full((E,), -7, dtype=torch.int32, device="cuda") if sums else None
+    ps = torch.full((E,), float("nan"), device="cuda") if sums else None
+    ws = torch.full((rg.moe_route_workspace_bytes(plan, T),), 0xFF, dtype=torch.uint8, device="cuda")
+    rg.moe_route(plan, T, x, bias, idx, w, expert_counts=cnt, prob_sum=ps, workspace=ws, logits_stride=stride, stream=stream)
+    return plan, idx, w, cnt, ps
+
+
+def cfg_of(E, k, fn="sigmoid", dtype="fp32", n_group=1, topk_group=1, group_top=2, renorm=True, scale=1.0):
+    return dict(E=E, k=k, score_fn=fn, logits_dtype=dtype, n_group=n_group, topk_group=topk_group, group_top=group_top,
+                renormalize=renorm, scale=scale)
+
+
+def check_route(x, bias, cfg, stride=0):
+    """x: device logits [T, >= E]."""
+    plan, idx, w, cnt, ps = run_route(x, bias, cfg, stride=stride)
+    xe = x[:, :cfg["E"]].double().cpu().numpy()
+    b = None if bias is None else bias.double().cpu().numpy()
+    ri, rw, rc, rp = plain_route(xe, b, cfg["k"], cfg["score_fn"], cfg["n_group"], cfg["topk_group"], cfg["group_top"],
+                                 cfg["renormalize"], cfg["scale"])
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert np.array_equal(cnt.cpu().numpy(), rc)
+    tol = (16 + 32 * (cfg["score_fn"] == "softmax")) * U32
+    assert np.abs(w.double().cpu().numpy() - rw).max(initial=0.0) <= tol * cfg["scale"]
+    # a sum over T rows in fp32, in runs of at most T / 8 rows per lane and then per CTA
+    assert np.all(np.abs(ps.double().cpu().numpy() - rp) <= (tol + 2e-6) * np.maximum(rp, 1e-3))
+    return idx, w
+
+
+CASES = [
+    # T, E, k, kwargs
+    (1, 256, 8, dict(n_group=8, topk_group=4, scale=2.5)),
+    (1, 1, 1, {}),
+    (3, 2, 2, dict(fn="softmax", renorm=False)),
+    (7, 33, 5, dict(fn="softmax")),
+    (130, 64, 6, dict(fn="softmax", n_group=4, topk_group=2, group_top=1)),
+    (65, 100, 16, dict(n_group=5, topk_group=3)),
+    (50, 100, 6, dict(n_group=25, topk_group=2, group_top=1, fn="softmax", renorm=False, scale=2.5)),
+    (40, 96, 3, dict(n_group=32, topk_group=1)),
+    (200, 256, 8, dict(n_group=8, topk_group=4, renorm=False, scale=2.5)),
+    (77, 384, 8, dict(scale=2.5)),
+    (64, 384, 6, dict(n_group=12, topk_group=5)),
+    (33, 512, 16, dict(fn="softmax", n_group=16, topk_group=16)),
+    (2500, 128, 8, dict(fn="softmax")),
+    (5000, 60, 4, dict(n_group=4, topk_group=2)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T,E,k,kw", CASES)
+def test_route_matches_fp64(T, E, k, kw, with_bias, dtype):
+    g = torch.Generator(device="cuda").manual_seed(T * 1000 + E)
+    x = (torch.randn(T, E, generator=g, device="cuda") * 1.5).to(DTYPES[dtype])
+    bias = (torch.rand(E, generator=g, device="cuda") - 0.5) * 0.2 if with_bias else None
+    check_route(x, bias, cfg_of(E, k, dtype=dtype, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_masked_experts_and_empty_rows(fn, with_bias):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    T, E = 300, 48
+    x = torch.randn(T, E, generator=g, device="cuda")
+    x[torch.rand(T, E, generator=g, device="cuda") < 0.8] = -float("inf")
+    x[::7] = -float("inf")
+    bias = torch.randn(E, generator=g, device="cuda") if with_bias else None
+    for kw in (dict(), dict(n_group=6, topk_group=2), dict(n_group=6, topk_group=3, group_top=1, renorm=False)):
+        idx, w = check_route(x, bias, cfg_of(E, 9, fn=fn, **kw))
+        assert bool((idx[::7] == -1).all()) and bool((w[::7] == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+def test_ties_go_to_the_lowest_id(fn):
+    """Few distinct logits and biases: equal keys everywhere; and biases that
+    make different logits nearly equal in key (decided as in fp64)."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, E = 257, 128
+    x = torch.randint(-2, 3, (T, E), generator=g, device="cuda").float()
+    zero = torch.zeros(E, device="cuda")
+    steps = torch.randint(0, 2, (E,), generator=g, device="cuda").float() * 0.25
+    for bias in (None, zero, steps):
+        for kw in (dict(), dict(n_group=8, topk_group=3), dict(n_group=8, topk_group=3, group_top=1)):
+            check_route(x, bias, cfg_of(E, 8, fn=fn, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("shift", [-30.0, 25.0])
+def test_keys_closer_than_fp32_resolves(fn, shift):
+    """Saturated scores (sigmoid near 0 or 1) whose fp32 values collide, and
+    biases that offset score differences: the selection is fp64's."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    T, E = 400, 64
+    x = torch.randn(T, E, generator=g, device="cuda") + (shift if fn == "sigmoid" else 0.0)
+    b = torch.rand(E, generator=g, device="cuda") * 1e-7 if shift > 0 else torch.zeros(E, device="cuda")
+    for kw in (dict(), dict(n_group=8, topk_group=4)):
+        check_route(x, b, cfg_of(E, 6, fn=fn, **kw))
+    # every row: x_1 = x_0 up to an ulp, the bias making up for the difference in fp32
+    x[:, 1] = torch.nextafter(x[:, 0], x[:, 0] + 1)
+    x[:, :2] += 2.0
+    check_route(x, torch.zeros(E, device="cuda"), cfg_of(E, 1, fn=fn))
+
+
+@pytest.mark.gpu
+def test_very_low_sigmoid_scores_keep_their_weights():
+    x = torch.tensor([[-200.0, -201.0, -202.0, -300.0], [-90.0, -95.0, 3.0, -90.0]], device="cuda")
+    b = torch.tensor([0.0, 0.0, -2.0, -1.0], device="cuda")
+    plan, idx, w, _, _ = run_route(x, b, cfg_of(4, 2))
+    assert idx.tolist() == [[0, 1], [0, 1]]
+    for r, d in ((0, 1.0), (1, 5.0)):
+        want = np.array([1.0, np.exp(-d)]) / (1.0 + np.exp(-d))
+        assert np.abs(w[r].double().cpu().numpy() - want).max() <= 16 * U32
+
+
+@pytest.mark.gpu
+def test_nan_and_infinite_logits():
+    nan, inf = float("nan"), float("inf")
+    x = torch.tensor([[nan, 1.0, 2.0, 3.0], [inf, 1.0, 2.0, 3.0], [0.0, 1.0, 2.0, 3.0]], device="cuda")
+    plan, idx, w, _, _ = run_route(x, None, cfg_of(4, 2, fn="softmax"))
+    assert idx.tolist() == [[2, 3], [0, 3], [2, 3]]
+    assert bool(torch.isnan(w[0]).all()) and w[1].tolist() == [1.0, 0.0] and bool(torch.isfinite(w[2]).all())
+    plan, idx, w, _, _ = run_route(x, None, cfg_of(4, 2, fn="sigmoid", renorm=False))
+    assert idx.tolist() == [[2, 3], [0, 3], [2, 3]] and bool(torch.isfinite(w).all()) and float(w[1, 0]) == 1.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("pad", [1, 8, 13])
+def test_row_strides_and_offset_bases(dtype, pad):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, E = 90, 64
+    big = torch.randn(T, E + pad, generator=g, device="cuda").to(DTYPES[dtype])
+    check_route(big, None, cfg_of(E, 4, dtype=dtype), stride=E + pad)
+    check_route(big[:, 1:], None, cfg_of(E - 1, 4, dtype=dtype), stride=E + pad)  # a base that is not 16-byte aligned
+    # the gradient with strides on both sides writes its rows' E elements only
+    plan, idx, w, _, _ = run_route(big, None, cfg_of(E, 4, dtype=dtype), stride=E + pad)
+    d = torch.full((T, E + pad), 7.0, device="cuda").to(DTYPES[dtype])
+    dw = torch.randn(T, 4, generator=g, device="cuda")
+    rg.moe_route_bwd(plan, T, big, idx, dw, d, logits_stride=E + pad, dlogits_stride=E + pad)
+    d0 = torch.empty(T, E, device="cuda", dtype=DTYPES[dtype])
+    rg.moe_route_bwd(plan, T, big[:, :E].contiguous(), idx, dw, d0)
+    assert bool((d[:, E:] == 7).all()) and torch.equal(d[:, :E], d0)
+
+
+@pytest.mark.gpu
+def test_another_stream_and_no_tokens():
+    T, E = 1000, 64
+    x = torch.randn(T, E, device="cuda")
+    ref = run_route(x, None, cfg_of(E, 4))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = run_route(x, None, cfg_of(E, 4), stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(ref[1:], got[1:]):
+        assert torch.equal(a, b)
+    _, idx, w, cnt, ps = run_route(x[:0], None, cfg_of(E, 4))
+    assert int(cnt.abs().sum()) == 0 and float(ps.abs().sum()) == 0.0
+
+
+def jacobian_bwd(x, idx, dw, dps, fn, renorm, scale):
+    """dL/dx in fp64 by torch's autograd over the definition; and, per element,
+    the sum of the absolute values of the terms that make it up."""
+    x = torch.tensor(x, dtype=torch.float64, requires_grad=True)
+    live = x > -float("inf")
+    xs = torch.where(live, x, torch.zeros_like(x))
+    if fn == "sigmoid":
+        s = torch.where(live, torch.sigmoid(xs), torch.zeros_like(x))
+    else:
+        m = torch.where(live, x, torch.full_like(x, -1e300)).max(1, keepdim=True).values.detach()
+        e = torch.where(live, torch.exp(torch.where(live, x - m, torch.zeros_like(x))), torch.zeros_like(x))
+        s = e / e.sum(1, keepdim=True).clamp_min(1e-300)
+    on = torch.tensor(idx >= 0)
+    at = torch.tensor(np.where(idx >= 0, idx, 0)).long()
+    q = torch.where(on, torch.gather(s, 1, at), torch.zeros_like(dw))
+    w = q / q.sum(1, keepdim=True).clamp_min(1e-300) if renorm else q
+    loss = (w * dw).sum() * scale
+    if dps is not None:
+        loss = loss + ((s / s.sum(1, keepdim=True).clamp_min(1e-300)).sum(0) * dps).sum()
+    loss.backward()
+    return x.grad.numpy()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("sums", [True, False])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,E,k", [(1, 256, 8), (37, 60, 4), (9, 1, 1), (130, 33, 16), (2100, 384, 8), (70, 512, 10)])
+def test_gradient_matches_fp64_autograd(T, E, k, fn, renorm, sums, dtype):
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    k = min(k, E)
+    x = torch.randn(T, E, generator=g, device="cuda") * 1.5
+    x[torch.rand(T, E, generator=g, device="cuda") < 0.1] = -float("inf")
+    if T > 8:
+        x[3] = -float("inf")
+    x = x.to(DTYPES[dtype])
+    plan, idx, w, _, _ = run_route(x, None, cfg_of(E, k, fn=fn, dtype=dtype, renorm=renorm, scale=2.5))
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    dps = torch.randn(E, generator=g, device="cuda") if sums else None
+    d = torch.full((T, E), float("nan"), device="cuda").to(DTYPES[dtype])
+    rg.moe_route_bwd(plan, T, x, idx, dw, d, dprob_sum=dps)
+    ref = jacobian_bwd(x.double().cpu().numpy(), idx.cpu().numpy(), dw.double().cpu(),
+                       None if dps is None else dps.double().cpu(), fn, renorm, 2.5)
+    got = d.double().cpu().numpy()
+    # terms up to (2.5 |dw| + |d|) times a score of at most 1, each with fp32 errors as the weights'; fp16's
+    # smallest step is 2^-24
+    size = 2.5 * dw.abs().max(1, keepdim=True).values.double().cpu().numpy() + (0 if dps is None else float(dps.abs().max()))
+    err32 = 4 * 48 * U32 * size
+    tol = HALF_ULP[dtype] * np.abs(ref) + err32 + (2.0 ** -25 if dtype == "fp16" else 0.0)
+    assert np.all(np.abs(got - ref) <= tol)
+    assert np.all(got[np.isneginf(x.double().cpu().numpy())] == 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_matches_differences(fn, renorm):
+    """Central differences of the fp64 definition with the selection held: step
+    h leaves h^2 / 6 times the third derivative (below 8 for these scores)."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, E, k, h = 5, 24, 3, 1e-3
+    x = torch.randn(T, E, generator=g, device="cuda")
+    plan, idx, w, _, _ = run_route(x, None, cfg_of(E, k, fn=fn, renorm=renorm))
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    dps = torch.randn(E, generator=g, device="cuda")
+    d = torch.empty(T, E, device="cuda")
+    rg.moe_route_bwd(plan, T, x, idx, dw, d, dprob_sum=dps)
+    xn, i, a, b = x.double().cpu().numpy(), idx.cpu().numpy(), dw.double().cpu().numpy(), dps.double().cpu().numpy()
+
+    def loss(v):
+        s = scores(v, fn)
+        q = np.take_along_axis(s, i.astype(np.int64), 1)
+        q = q / q.sum(1, keepdims=True) if renorm else q
+        return (q * a).sum(1) + ((s / s.sum(1, keepdims=True)) * b).sum(1)
+
+    num = np.zeros((T, E))
+    for e in range(E):
+        up, dn = xn.copy(), xn.copy()
+        up[:, e] += h
+        dn[:, e] -= h
+        num[:, e] = (loss(up) - loss(dn)) / (2 * h)
+    size = np.abs(a).max() + np.abs(b).max()
+    assert np.abs(d.double().cpu().numpy() - num).max() <= size * (8 * h * h / 6 + 4 * 48 * U32)
+
+
+@pytest.mark.gpu
+def test_gradient_skips_slots_outside_the_range():
+    T, E, k = 4, 16, 3
+    x = torch.randn(T, E, device="cuda")
+    plan = rg.moe_route_plan_create(E, k)
+    idx = torch.tensor([[-1, -1, -1], [2, 5, 99], [2, 5, -1], [1 << 30, -(1 << 30), 3]], dtype=torch.int32, device="cuda")
+    dw = torch.randn(T, k, device="cuda")
+    dw[2, :2] = dw[1, :2]
+    x[2] = x[1]
+    d = torch.full((T, E), float("nan"), device="cuda")
+    rg.moe_route_bwd(plan, T, x, idx, dw, d)
+    assert bool((d[0] == 0).all()) and torch.equal(d[1], d[2]) and bool(torch.isfinite(d).all())
+
+
+@pytest.mark.gpu
+def test_repeated_calls_and_a_graph_give_the_same_bits():
+    T, E = 3000, 256
+    x = torch.randn(T, E, device="cuda")
+    bias = torch.rand(E, device="cuda") * 0.1
+    cfg = cfg_of(E, 8, n_group=8, topk_group=4)
+    plan, idx, w, cnt, ps = run_route(x, bias, cfg)
+    ws = torch.empty(rg.moe_route_workspace_bytes(plan, T), dtype=torch.uint8, device="cuda")
+    idx2, w2, cnt2, ps2 = (torch.zeros_like(t) for t in (idx, w, cnt, ps))
+    d, d2 = torch.empty_like(x), torch.zeros_like(x)
+    dw = torch.randn(T, 8, device="cuda")
+    rg.moe_route_bwd(plan, T, x, idx, dw, d, dprob_sum=bias)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rg.moe_route(plan, T, x, bias, idx2, w2, cnt2, ps2, ws)
+        rg.moe_route_bwd(plan, T, x, idx2, dw, d2, dprob_sum=bias)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in ((idx, idx2), (w, w2), (cnt, cnt2), (ps, ps2), (d, d2)):
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- refusals (no GPU needed)
+@pytest.fixture(scope="module")
+def L():
+    from routing_grouped_expert_gemm_gb300 import build as rgbuild
+    rgbuild.build()
+    return rg.lib()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(E=0), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(E=513), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(k=0), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(k=17), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(n_group=0), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(n_group=7), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(n_group=64, topk_group=64), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(n_group=8, topk_group=9), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(topk_group=0), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(n_group=32, topk_group=1), rg.MOE_ERR_UNSUPPORTED_SHAPE),  # 8 of 2 experts
+    (dict(score_fn=2), rg.MOE_ERR_INVALID_ARG), (dict(logits_dtype=3), rg.MOE_ERR_INVALID_ARG),
+    (dict(logits_dtype=-1), rg.MOE_ERR_INVALID_ARG), (dict(group_top=3), rg.MOE_ERR_INVALID_ARG),
+    (dict(group_top=0), rg.MOE_ERR_INVALID_ARG), (dict(scale=float("nan")), rg.MOE_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), rg.MOE_ERR_INVALID_ARG), (dict(renormalize=2), rg.MOE_ERR_INVALID_ARG),
+])
+def test_plan_refusals(L, kw, code):
+    with pytest.raises(rg.MoEError) as ei:
+        rg.moe_route_plan_create(**{**dict(E=64, k=8), **kw})
+    assert ei.value.code == code
+
+
+def test_null_plan_refusals(L):
+    assert L.moe_route_plan_create(None, None) == rg.MOE_ERR_INVALID_ARG
+    assert L.moe_route_workspace_bytes(None, 4) == 0
+    assert L.moe_route(None, 1, None, 0, None, None, None, None, None, None, 0, None) == rg.MOE_ERR_INVALID_ARG
+    assert L.moe_route_bwd(None, 1, None, 0, None, None, None, None, 0, None) == rg.MOE_ERR_INVALID_ARG
+    assert L.moe_route_plan_destroy(None) == 0
+
+
+@pytest.mark.gpu
+def test_call_refusals():
+    T, E, k = 100, 64, 8
+    plan = rg.moe_route_plan_create(E, k)
+    x = torch.randn(T, E, device="cuda")
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    cnt = torch.empty(E, dtype=torch.int32, device="cuda")
+
+    def code(f, *a, **kw):
+        with pytest.raises(rg.MoEError) as ei:
+            f(*a, **kw)
+        return ei.value.code
+
+    bad = rg.MOE_ERR_INVALID_ARG
+    assert code(rg.moe_route, plan, -1, x, None, idx, w) == bad
+    assert code(rg.moe_route, plan, T, None, None, idx, w) == bad
+    assert code(rg.moe_route, plan, T, x, None, None, w) == bad
+    assert code(rg.moe_route, plan, T, x, None, idx, None) == bad
+    assert code(rg.moe_route, plan, T, x, None, idx, w, logits_stride=E - 1) == bad
+    assert code(rg.moe_route, plan, T, x.data_ptr() + 2, None, idx, w) == bad
+    assert code(rg.moe_route, plan, T, x, None, idx, w, expert_counts=cnt) == bad  # sums want a workspace
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    assert code(rg.moe_route, plan, T, x, None, idx, w, expert_counts=cnt, workspace=ws) == rg.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert code(rg.moe_route_bwd, plan, T, x, idx, None, x.clone()) == bad
+    assert code(rg.moe_route_bwd, plan, T, x, idx, w, None) == bad
+    assert code(rg.moe_route_bwd, plan, T, x, idx, w, x.clone(), dlogits_stride=E - 1) == bad
