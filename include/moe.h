@@ -477,6 +477,70 @@ int moe_route_bwd(const moe_route_plan* plan, int64_t T, const void* logits, int
                   const int32_t* topk_idx, const float* dtopk_w, const float* dprob_sum, void* dlogits,
                   int64_t dlogits_stride, moe_stream_t stream);
 
+/* ------------------------------------------------------------------ momentum and orthogonalised updates
+ *
+ * The update of a stack of weight matrices as the Muon optimiser makes it from
+ * moe_bwd's gradients:
+ *   M = mu M + G;  U = G + mu M (nesterov) or M;  X = U / |U|_F;
+ *   steps times:  A = X X^T,  X = a X + (b A + c A^2) X     (rows <= cols;
+ *                 A = X^T X,  X = a X + X (b A + c A^2)      otherwise)
+ *   update = scale X
+ * Products run in fp16 operands with fp32 sums; see moe_muon_update.
+ */
+/*
+ *   count, rows, cols  the stack [count, rows, cols]; count 1..65536, rows and cols
+ *                      1..65536, rows * cols up to 2^30
+ *   steps              Newton-Schulz steps, 1..32 (0 = 5)
+ *   grad_dtype         moe_dtype of the gradient
+ *   a, b, c            the step's coefficients, finite (all 0 = 3.4445, -4.7750, 2.0315)
+ *   timeout_ms         limit of every device-side wait (0 = 2000 ms)
+ */
+typedef struct moe_muon_config {
+  int64_t count;
+  int64_t rows;
+  int64_t cols;
+  int32_t steps;
+  int32_t grad_dtype;
+  float a;
+  float b;
+  float c;
+  int32_t timeout_ms;
+} moe_muon_config;
+
+typedef struct moe_muon_plan moe_muon_plan;
+
+/* Validate `cfg` for the current CUDA device and create a plan (host memory
+ * only).  Errors as moe_plan_create. */
+int moe_muon_plan_create(const moe_muon_config* cfg, moe_muon_plan** out);
+int moe_muon_plan_destroy(moe_muon_plan* plan);
+
+/* Device workspace of moe_muon_update (0 on bad input). */
+size_t moe_muon_workspace_bytes(const moe_muon_plan* plan);
+
+/*
+ * One update.
+ *   grad      [count, rows, cols] of grad_dtype, rows grad_row_stride elements
+ *             apart (0 = cols), matrices grad_stride apart (0 = rows * row stride)
+ *   momentum  [count, rows, cols] fp32, updated in place; NULL = no momentum
+ *             (U = G; mu and nesterov are ignored)
+ *   update    [count, rows, cols] bf16
+ *   workspace at least moe_muon_workspace_bytes(plan) bytes, 256-byte aligned,
+ *             no initialisation needed
+ * A matrix of zeros gives zeros; a matrix with an infinity or a NaN gives NaN,
+ * without touching the others.  The step's iterates must stay below 15 in
+ * absolute value (the default coefficients keep them below 1.3).  Two calls on
+ * the same inputs give the same bits.  No host synchronisation; a device-side
+ * wait that ran out is reported by moe_muon_get_status.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
+ */
+int moe_muon_update(const moe_muon_plan* plan, const void* grad, int64_t grad_row_stride, int64_t grad_stride,
+                    float* momentum, float mu, int32_t nesterov, float scale, void* update, void* workspace,
+                    size_t workspace_bytes, moe_stream_t stream);
+
+/* The device status of the last update that used `workspace` (MOE_STATUS_OK or
+ * MOE_STATUS_TIMEOUT); waits for `stream`, as moe_get_status does. */
+int moe_muon_get_status(const moe_muon_plan* plan, const void* workspace, int* device_status, moe_stream_t stream);
+
 /* Static description of an error code. */
 const char* moe_error_string(int code);
 

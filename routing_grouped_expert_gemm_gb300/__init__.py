@@ -10,7 +10,9 @@ Entry points keep the C names: ``moe_plan_create``, ``moe_plan_destroy``,
 ``moe_fwd``, ``moe_bwd_workspace_bytes``, ``moe_bwd``, ``moe_get_status``,
 ``moe_get_phase_times``, ``moe_route_static``, ``moe_error_string``; routing from
 given logits: ``moe_route_plan_create``, ``moe_route_plan_destroy``,
-``moe_route_workspace_bytes``, ``moe_route``, ``moe_route_bwd``.
+``moe_route_workspace_bytes``, ``moe_route``, ``moe_route_bwd``; momentum and
+orthogonalised updates: ``moe_muon_plan_create``, ``moe_muon_plan_destroy``,
+``moe_muon_workspace_bytes``, ``moe_muon_update``, ``moe_muon_get_status``.
 """
 from __future__ import annotations
 
@@ -84,6 +86,12 @@ class moe_route_config(ctypes.Structure):
                 ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class moe_muon_config(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("steps", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("timeout_ms", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -134,6 +142,16 @@ def lib():
     L.moe_route.restype = ctypes.c_int
     L.moe_route_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]
     L.moe_route_bwd.restype = ctypes.c_int
+    L.moe_muon_plan_create.argtypes = [ctypes.POINTER(moe_muon_config), ctypes.POINTER(vp)]
+    L.moe_muon_plan_create.restype = ctypes.c_int
+    L.moe_muon_plan_destroy.argtypes = [vp]
+    L.moe_muon_plan_destroy.restype = ctypes.c_int
+    L.moe_muon_workspace_bytes.argtypes = [vp]
+    L.moe_muon_workspace_bytes.restype = sz
+    L.moe_muon_update.argtypes = [vp, vp, i64, i64, vp, ctypes.c_float, ctypes.c_int32, ctypes.c_float, vp, vp, sz, vp]
+    L.moe_muon_update.restype = ctypes.c_int
+    L.moe_muon_get_status.argtypes = [vp, vp, i32p, vp]
+    L.moe_muon_get_status.restype = ctypes.c_int
     L.moe_error_string.argtypes = [ctypes.c_int]
     L.moe_error_string.restype = ctypes.c_char_p
     _lib = L
@@ -397,3 +415,59 @@ def moe_route_bwd(plan: RoutePlan, T: int, logits, topk_idx, dtopk_w, dlogits, d
                              _ptr(dprob_sum), _ptr(dlogits), dlogits_stride, _stream(stream))
     if rc != MOE_OK:
         raise MoEError(rc, "moe_route_bwd")
+
+
+class MuonPlan:
+    """Owns a moe_muon_plan*; released by moe_muon_plan_destroy (or garbage collection)."""
+
+    def __init__(self, handle: int, cfg: moe_muon_config):
+        self.handle = handle
+        self.cfg = cfg
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.moe_muon_plan_destroy(self.handle)
+            self.handle = None
+
+
+def moe_muon_plan_create(count, rows, cols, steps=5, grad_dtype=MOE_DTYPE_BF16, coefficients=(3.4445, -4.7750, 2.0315),
+                         timeout_ms=0) -> MuonPlan:
+    """Plan of ``moe_muon_update`` for a stack of ``count`` matrices of rows x cols."""
+    if isinstance(grad_dtype, str):
+        grad_dtype = _DTYPES[grad_dtype]
+    cfg = moe_muon_config(count, rows, cols, steps, grad_dtype, *coefficients, timeout_ms)
+    h = ctypes.c_void_p()
+    rc = lib().moe_muon_plan_create(ctypes.byref(cfg), ctypes.byref(h))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_muon_plan_create")
+    return MuonPlan(h.value, cfg)
+
+
+def moe_muon_plan_destroy(plan: MuonPlan) -> None:
+    if plan.handle:
+        lib().moe_muon_plan_destroy(plan.handle)
+        plan.handle = None
+
+
+def moe_muon_workspace_bytes(plan: MuonPlan) -> int:
+    return int(lib().moe_muon_workspace_bytes(plan.handle))
+
+
+def moe_muon_update(plan: MuonPlan, grad, momentum, update, workspace, workspace_bytes: int | None = None, mu=0.95,
+                    nesterov=True, scale=1.0, grad_row_stride: int = 0, grad_stride: int = 0, stream=None) -> None:
+    """Advance ``momentum`` (fp32, in place; None = no momentum) by ``grad`` and
+    write the orthogonalised update of every matrix, times ``scale``, to ``update`` (bf16)."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().moe_muon_update(plan.handle, _ptr(grad), grad_row_stride, grad_stride, _ptr(momentum), mu, int(nesterov),
+                               scale, _ptr(update), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_muon_update")
+
+
+def moe_muon_get_status(plan: MuonPlan, workspace, stream=None) -> int:
+    st = ctypes.c_int(-1)
+    rc = lib().moe_muon_get_status(plan.handle, _ptr(workspace), ctypes.byref(st), _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_muon_get_status")
+    return st.value

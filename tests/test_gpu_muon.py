@@ -1,0 +1,257 @@
+"""moe_muon_update against a plain fp64 implementation.
+
+Tolerances, relative to the Frobenius norm of the result.  Operands of a
+product are rounded to fp16 (relative 2^-11 at most, 2^-11 / sqrt(3) in the
+root mean square over a binade's worst end): X's hi in both products, A and B
+once each, four roundings a step, each multiplied by what the step does to its
+operand (|a| + |b| + |c| = 10.3 at worst, the terms cancelling to 1); errors of
+one step pass the next ones with factors near 1.  Five steps of four roundings
+add as independent errors: sqrt(20) * 2^-11 / sqrt(3) = 1.3e-3 at unit gain,
+and twice that is allowed; then the result's own rounding to bf16 (2^-8 at
+most per element, below 2^-9 in the root mean square)."""
+import numpy as np
+import pytest
+import torch
+
+import routing_grouped_expert_gemm_gb300 as rg
+
+COEFS = (3.4445, -4.7750, 2.0315)
+DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+TOL = 2 * np.sqrt(20.0) * 2.0 ** -11 / np.sqrt(3.0) + 2.0 ** -9
+
+
+def plain(grad, mom, mu=0.95, nesterov=True, steps=5, coefs=COEFS, scale=1.0):
+    """fp64, matrix by matrix; returns (update, momentum)."""
+    a, b, c = (float(np.float32(v)) for v in coefs)
+    mu, scale = float(np.float32(mu)), float(np.float32(scale))
+    g = grad.double()
+    m = None
+    if mom is not None:
+        m = mu * mom.double() + g
+        g = g + mu * m if nesterov else m
+    out = torch.zeros_like(g)
+    for i in range(g.shape[0]):
+        n = torch.linalg.matrix_norm(g[i])
+        if float(n) == 0.0:
+            continue
+        x = g[i] / n
+        for _ in range(steps):
+            y = x @ x.T if x.shape[0] <= x.shape[1] else x.T @ x
+            p = b * y + c * (y @ y)
+            x = a * x + (p @ x if x.shape[0] <= x.shape[1] else x @ p)
+        out[i] = scale * x
+    return out, m
+
+
+def stack(count, rows, cols, kind, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if kind == "flat":
+        return torch.randn(count, rows, cols, generator=g, device="cuda")
+    r = max(1, min(rows, cols) // 4)
+    u = torch.randn(count, rows, r, generator=g, device="cuda")
+    v = torch.randn(count, r, cols, generator=g, device="cuda")
+    if kind == "low rank":
+        return u @ v
+    d = torch.arange(1, r + 1, device="cuda", dtype=torch.float32) ** -1.0
+    return (u * d) @ v + 1e-2 * torch.randn(count, rows, cols, generator=g, device="cuda")
+
+
+def run(grad, mom, dtype, count, rows, cols, **kw):
+    plan_kw = {k: kw.pop(k) for k in ("steps", "coefficients", "timeout_ms") if k in kw}
+    plan = rg.moe_muon_plan_create(count, rows, cols, grad_dtype=dtype, **plan_kw)
+    ws = torch.full((rg.moe_muon_workspace_bytes(plan),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN in every type
+    out = torch.full((count, rows, cols), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rg.moe_muon_update(plan, grad, mom, out, ws, **kw)
+    assert rg.moe_muon_get_status(plan, ws) == rg.MOE_STATUS_OK
+    return out
+
+
+def rel(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+SHAPES = [(1, 1, 1), (2, 1, 9), (2, 7, 1), (5, 8, 8), (3, 33, 65), (2, 64, 64), (4, 100, 30), (2, 128, 256), (2, 255, 257),
+          (1, 257, 255), (3, 300, 200), (1, 512, 1000), (1, 1031, 517), (700, 16, 24), (1, 24, 5000), (1, 5000, 24)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["flat", "decaying", "low rank"])
+@pytest.mark.parametrize("count,rows,cols", SHAPES)
+def test_update_matches_fp64(count, rows, cols, kind):
+    grad = stack(count, rows, cols, kind, rows * 7 + cols)
+    mom = stack(count, rows, cols, kind, rows + cols + 1) * 3
+    ref, rm = plain(grad, mom, scale=0.2)
+    out = run(grad, mom, "fp32", count, rows, cols, scale=0.2)
+    assert rel(out, ref) <= TOL
+    # one product and one sum in fp32
+    assert float((mom.double() - rm).abs().max()) <= 2 ** -23 * float(rm.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("nesterov", [True, False])
+@pytest.mark.parametrize("momentum", [True, False])
+def test_types_and_momentum_forms(dtype, nesterov, momentum):
+    count, rows, cols = 3, 160, 120
+    grad = (stack(count, rows, cols, "decaying", 1) * 1e-2).to(DTYPES[dtype])
+    mom = stack(count, rows, cols, "flat", 2) * 1e-2 if momentum else None
+    ref, rm = plain(grad, mom, mu=0.9, nesterov=nesterov)
+    out = run(grad, mom, dtype, count, rows, cols, mu=0.9, nesterov=nesterov)
+    assert rel(out, ref) <= TOL
+    if momentum:
+        assert float((mom.double() - rm).abs().max()) <= 2 ** -23 * float(rm.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps,coefs", [(1, COEFS), (2, COEFS), (3, (1.875, -1.25, 0.375)), (10, (1.5, -0.5, 0.0))])
+def test_steps_and_coefficients(steps, coefs):
+    grad = stack(2, 90, 140, "flat", 4)
+    ref, _ = plain(grad, None, steps=steps, coefs=coefs)
+    out = run(grad, None, "fp32", 2, 90, 140, steps=steps, coefficients=coefs)
+    # these coefficients damp errors (no gain above 1.9 a step); more steps add more roundings
+    assert rel(out, ref) <= 2 * np.sqrt(4.0 * steps) * 2.0 ** -11 / np.sqrt(3.0) + 2.0 ** -9
+
+
+@pytest.mark.gpu
+def test_strided_gradients():
+    count, rows, cols = 3, 48, 72
+    for pad, extra, off in ((0, 0, 1), (8, 0, 0), (5, 3, 2), (24, 1, 4)):
+        base = torch.randn(count * (rows + extra) * (cols + pad) + off, device="cuda").bfloat16()
+        view = base[off:].view(count, rows + extra, cols + pad)[:, :rows, :cols]
+        ref = run(view.contiguous(), None, "bf16", count, rows, cols)
+        out = run(view.data_ptr(), None, "bf16", count, rows, cols, grad_row_stride=cols + pad,
+                  grad_stride=(rows + extra) * (cols + pad))
+        assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+def test_zero_infinite_and_nan_matrices_keep_to_themselves():
+    count, rows, cols = 5, 70, 90
+    grad = stack(count, rows, cols, "flat", 8)
+    ref = run(grad, None, "fp32", count, rows, cols)
+    bad = grad.clone()
+    bad[1] = 0
+    bad[2, 3, 4] = float("inf")
+    bad[3, 69, 89] = float("nan")
+    out = run(bad, None, "fp32", count, rows, cols)
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[4], ref[4])
+    assert bool((out[1] == 0).all()) and bool(torch.isnan(out[2]).all()) and bool(torch.isnan(out[3]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [-140, -100, 60, 110])
+def test_magnitudes_outside_the_squares_range(power):
+    """Squares of these overflow or underflow fp32; the direction does not change
+    (powers of two, though -140 leaves few bits: subnormal inputs)."""
+    grad = torch.randint(-8, 9, (2, 40, 56), device="cuda").float()
+    ref = run(grad, None, "fp32", 2, 40, 56)
+    out = run(torch.ldexp(grad, torch.tensor(power, device="cuda")), None, "fp32", 2, 40, 56)
+    assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+def test_one_large_element_does_not_overflow():
+    grad = torch.zeros(1, 64, 64, device="cuda")
+    grad[0, 5, 9] = 3.0
+    out = run(grad, None, "fp32", 1, 64, 64)
+    want = 1.0
+    for _ in range(5):
+        want = COEFS[0] * want + COEFS[1] * want ** 3 + COEFS[2] * want ** 5
+    assert abs(float(out[0, 5, 9]) - want) <= TOL * abs(want)
+    assert int((out != 0).sum()) == 1
+
+
+@pytest.mark.gpu
+def test_repeats_streams_and_graphs_give_the_same_bits():
+    count, rows, cols = 4, 300, 520
+    grad = stack(count, rows, cols, "flat", 3).bfloat16()
+    mom0 = stack(count, rows, cols, "flat", 5)
+    mom = mom0.clone()
+    ref = run(grad, mom, "bf16", count, rows, cols)
+    plan = rg.moe_muon_plan_create(count, rows, cols)
+    ws = torch.zeros(rg.moe_muon_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(ref)
+    m2 = mom0.clone()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    rg.moe_muon_update(plan, grad, m2, out, ws, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(m2, mom)
+    m2.copy_(mom0)
+    out.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rg.moe_muon_update(plan, grad, m2, out, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(m2, mom)
+
+
+@pytest.mark.gpu
+def test_several_chunks_equal_single_matrices():
+    """A stack larger than what is in flight at once."""
+    count, rows, cols = 650, 20, 28
+    grad = stack(count, rows, cols, "flat", 6)
+    out = run(grad, None, "fp32", count, rows, cols)
+    for i in (0, 607, 608, 649):
+        assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), None, "fp32", 1, rows, cols)[0])
+
+
+# ---------------------------------------------------------------- refusals (no GPU needed)
+@pytest.fixture(scope="module")
+def L():
+    from routing_grouped_expert_gemm_gb300 import build as rgbuild
+    rgbuild.build()
+    return rg.lib()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(count=0), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(count=65537), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(rows=0), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(cols=0), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(rows=65537), rg.MOE_ERR_UNSUPPORTED_SHAPE), (dict(rows=65536, cols=32768), rg.MOE_ERR_UNSUPPORTED_SHAPE),
+    (dict(steps=-1), rg.MOE_ERR_INVALID_ARG), (dict(steps=33), rg.MOE_ERR_INVALID_ARG),
+    (dict(grad_dtype=3), rg.MOE_ERR_INVALID_ARG), (dict(grad_dtype=-1), rg.MOE_ERR_INVALID_ARG),
+    (dict(coefficients=(1.0, float("nan"), 0.0)), rg.MOE_ERR_INVALID_ARG),
+    (dict(coefficients=(float("inf"), 0.0, 0.0)), rg.MOE_ERR_INVALID_ARG),
+])
+def test_plan_refusals(L, kw, code):
+    with pytest.raises(rg.MoEError) as ei:
+        rg.moe_muon_plan_create(**{**dict(count=2, rows=16, cols=16), **kw})
+    assert ei.value.code == code
+
+
+def test_null_refusals(L):
+    assert L.moe_muon_plan_create(None, None) == rg.MOE_ERR_INVALID_ARG
+    assert L.moe_muon_workspace_bytes(None) == 0
+    assert L.moe_muon_update(None, None, 0, 0, None, 0.9, 1, 1.0, None, None, 0, None) == rg.MOE_ERR_INVALID_ARG
+    assert L.moe_muon_get_status(None, None, None, None) == rg.MOE_ERR_INVALID_ARG
+    assert L.moe_muon_plan_destroy(None) == 0
+
+
+@pytest.mark.gpu
+def test_call_refusals():
+    plan = rg.moe_muon_plan_create(2, 16, 24)
+    g = torch.zeros(2, 16, 24, dtype=torch.bfloat16, device="cuda")
+    m = torch.zeros(2, 16, 24, device="cuda")
+    u = torch.zeros_like(g)
+    ws = torch.zeros(rg.moe_muon_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+
+    def code(*a, **kw):
+        with pytest.raises(rg.MoEError) as ei:
+            rg.moe_muon_update(plan, *a, **kw)
+        return ei.value.code
+
+    bad = rg.MOE_ERR_INVALID_ARG
+    assert code(None, m, u, ws) == bad
+    assert code(g, m, None, ws) == bad
+    assert code(g, m, u, None, workspace_bytes=1 << 30) == bad
+    assert code(g, m, u, ws, grad_row_stride=23) == bad
+    assert code(g, m, u, ws, grad_stride=-1) == bad
+    assert code(g.data_ptr() + 1, m, u, ws) == bad
+    assert code(g, m.data_ptr() + 2, u, ws) == bad
+    assert code(g, m, u, ws.data_ptr() + 16, workspace_bytes=1 << 30) == bad
+    assert code(g, m, u, ws, mu=float("nan")) == bad
+    assert code(g, m, u, ws, scale=float("inf")) == bad
+    assert code(g, m, u, ws, nesterov=2) == bad
+    assert code(g, m, u, ws, workspace_bytes=ws.numel() - 1) == rg.MOE_ERR_WORKSPACE_TOO_SMALL
