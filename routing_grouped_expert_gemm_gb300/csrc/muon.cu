@@ -13,9 +13,15 @@
 // all directions grows against the small ones: rounding X itself to fp16 each
 // step costs 1e-2 on decaying spectra.  X is therefore held as hi + lo, two
 // fp16 numbers (22 bits); the term a X is taken from both, and only B X, which
-// lies in the directions of the large singular values, from hi.  That leaves
-// 2e-4 to 1.7e-3 against fp64 (relative Frobenius norm, over flat, decaying
-// and rank-deficient spectra) before the result's own rounding to bf16.
+// lies in the directions of the large singular values, from hi.  The diagonals
+// of A and B, which carry most of them where the rows are nearly orthogonal,
+// are kept in fp32 beside fp16 matrices without a diagonal (A = D + O gives
+// A^2 = O^2 + D O + O D + D^2) and are applied to the fp32 sums.  B's diagonal
+// multiplies hi in the early steps, so that it cancels against the other
+// elements' share in the small directions, and hi + lo in the last two, after
+// which nothing grows any more.  Left against fp64 (relative Frobenius norm,
+// over flat, decaying and rank-deficient spectra, 16 to 2048 rows): 2e-4 to
+// 1.4e-3, before the result's own rounding to bf16 (1.7e-3).
 //
 // Scales.  fp16 has 5 exponent bits, so X_0 is U 2^k with |U 2^k|_F in
 // [2^14, 2^15): no element overflows and those 2^-28 of the norm keep their
@@ -33,19 +39,22 @@
 
 namespace moe {
 
-constexpr int NS_THREADS = 192;       // producer, MMA issuer, four epilogue warps
+constexpr int NS_THREADS = 224;       // producer, MMA issuer, four epilogue warps, the epilogue's loads and stores
 constexpr int NS_TILE = 256;          // of a CTA pair: 256 x 256, 128 rows in each CTA
 constexpr int NS_BOX = 8192;          // one {64, 64} fp16 box
 constexpr int NS_STAGE = 4 * NS_BOX;  // per CTA: 128 rows of A and half of B's 256, 64 of K
-constexpr int NS_STAGES = 6;
-constexpr int NS_SMEM = NS_STAGES * NS_STAGE + 1024 + 256;
+constexpr int NS_STAGES = 5;
+constexpr int NS_EBUF = 4 * NS_BOX;   // epilogue buffer: two tiles of 128 rows x 64 columns
+constexpr int NS_SMEM = NS_STAGES * NS_STAGE + 2 * NS_EBUF + 1024 + 256;
 constexpr float NS_S = 4096.0f;       // scale of the held iterates, A and B
 constexpr int NS_PREP_BLOCKS = 256;   // partial sums per matrix, at most
 
 enum : int { NS_GRAM = 0, NS_POLY = 1, NS_STEP = 2 };
 
 struct NsMaps {
-  CUtensorMap a, b;
+  CUtensorMap a, b;         // operands
+  CUtensorMap in0, in1;     // box {64, 128}: POLY: A; STEP: X's hi and lo
+  CUtensorMap out0, out1;   // box {64, 128}: A or B, and (box {64, 64}) its transposed tiles; STEP: hi and lo, or the update
 };
 
 struct NsParams {
@@ -53,19 +62,26 @@ struct NsParams {
   int nb;                  // matrices
   int tiles_n, n_tiles;    // column tiles; tiles per matrix (symmetric: the lower ones)
   int first, last;         // Newton-Schulz step
-  int out_vec;             // final rows are 16-byte aligned vectors of 8
-  int64_t ld;              // elements between rows of in and out (STEP: X; else A, B)
-  float ca, cb;            // out = ca in + cb sum
+  int diag_full;           // STEP: B's diagonal multiplies hi + lo, not hi
+  int tall;                // STEP: X B, B's diagonal belongs to the columns
+  int out_vec;             // the update goes out through its tensor map (16-byte aligned rows)
+  int ldd;                 // matrix stride of the diagonals
+  float ca, cb;            // POLY: B = ca A + cb A^2; STEP: X <- ca X + diag(B) X + cb sum
   float scale;             // of the final update
   const float* rho;        // [nb] 1 / |U 2^k|_F
-  const __half* in_hi;     // POLY: A; STEP: X
-  const __half* in_lo;
-  __half* out_hi;
-  __half* out_lo;
+  float* diag_a;           // [nb, ldd] A's diagonal times NS_S
+  float* diag_b;           // [nb, ldd] B's diagonal
   bf16* out_final;
   int* status;
   long long timeout_ns;
 };
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 
 __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {  // MN-major, {64, 64} boxes 8192 B apart
   uint64_t d = 0;
@@ -120,64 +136,105 @@ __device__ __forceinline__ uint4 pack8(const __half* h) {
                     (uint32_t)__half_as_ushort(h[6]) | ((uint32_t)__half_as_ushort(h[7]) << 16));
 }
 
-// 32 columns (from c) of one row of a tile.  Columns past N inside the row's
-// padding (ld is a multiple of 8) hold values that nothing reads: the tensor
-// maps end at the matrix.
+// One row (TMEM lane) of an epilogue chunk, 64 columns: `main` holds this row's
+// inputs and takes its outputs in place (POLY: A -> B; STEP: hi), `aux` is lo,
+// or takes the chunk transposed (symmetric products' tiles below the
+// diagonal).  Rows of 128 bytes, 16-byte pieces swizzled as the tensor maps'.
 template <int KIND>
-__device__ __forceinline__ void ns_store32(const NsParams& p, const NsTile& t, int r, int c, bool mirror, float rho,
-                                           const uint32_t (&acc)[32]) {
-  const size_t base = (size_t)t.mat * (size_t)p.M * p.ld + (size_t)r * p.ld;
-  if (KIND == NS_GRAM) rho = p.first ? rho * rho * NS_S : 1.0f / NS_S;
+__device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uint8_t* main, uint8_t* aux, int rl, int r,
+                                         int c0, float rho, uint32_t taddr) {
+  uint32_t acc[2][32];
+  tmem_ld_32x32b_x32(taddr, acc[0]);
+  tmem_ld_32x32b_x32(taddr + 32u, acc[1]);
+  tmem_ld_wait();
+  const bool mirror = KIND != NS_STEP && t.m0 != t.n0;
+  const float* da = p.diag_a + (size_t)t.mat * p.ldd;
+  const float* db = p.diag_b + (size_t)t.mat * p.ldd;
+  float f = 1.0f, g = 0.0f, cb = p.cb;
+  if (KIND == NS_GRAM) f = p.first ? rho * rho * NS_S : 1.0f / NS_S;
+  if (KIND == NS_POLY) g = da[r];
+  if (KIND == NS_STEP) {
+    if (p.first) f = NS_S * rho, cb = rho;
+    if (!p.tall) g = db[r];
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c8 = c + 8 * i;
-    if (c8 >= p.N) break;
+  for (int i = 0; i < 8; ++i) {
+    const int c = c0 + 8 * i;
+    uint4* at = reinterpret_cast<uint4*>(main + rl * 128 + ((i ^ (rl & 7)) << 4));
     float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[i / 4][(8 * i + j) & 31]);
+    __half h[8];
     if (KIND == NS_GRAM) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[8 * i + j]) * rho;
-    } else {
-      float x[8];
-      unpack8(*reinterpret_cast<const uint4*>(p.in_hi + base + c8), x);
-      float ca = p.ca, cb = p.cb;
-      if (KIND == NS_STEP) {
-        float lo[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.in_lo + base + c8), lo);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] += lo[j];
-        ca = p.first ? ca * NS_S * rho : ca;
-        cb = p.first ? rho : cb;
+      for (int j = 0; j < 8; ++j) {
+        v[j] *= f;
+        if (c + j == r) {
+          if (r < p.M) p.diag_a[(size_t)t.mat * p.ldd + r] = v[j];
+          v[j] = 0.0f;
+        }
+        h[j] = __float2half_rn(v[j]);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = ca * x[j] + cb * __uint_as_float(acc[8 * i + j]);
-    }
-    if (KIND == NS_STEP && p.last) {
-      bf16* o = p.out_final + (size_t)t.mat * (size_t)p.M * p.N + (size_t)r * p.N + c8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= p.scale;
-      if (p.out_vec) {
-        *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                                  pack_bf16x2(v[6], v[7]));
+    } else {
+      float x[8], d[8];
+      unpack8(*at, x);
+      if (KIND == NS_POLY || p.tall) {  // the columns' diagonal: the same 32 bytes for the whole warp
+        const float4* s4 = reinterpret_cast<const float4*>((KIND == NS_POLY ? da : db) + c);
+        const float4 w0 = s4[0], w1 = s4[1];
+        d[0] = w0.x, d[1] = w0.y, d[2] = w0.z, d[3] = w0.w, d[4] = w1.x, d[5] = w1.y, d[6] = w1.z, d[7] = w1.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c8 + j < p.N) o[j] = __float2bfloat16_rn(v[j]);
+        for (int j = 0; j < 8; ++j) d[j] = g;
       }
-      continue;
+      if (KIND == NS_POLY) {  // b O + c (O^2 + (D_r + D_c) O); on the diagonal b D + c (O^2 + D^2)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (c + j == r) {
+            if (r < p.M) p.diag_b[(size_t)t.mat * p.ldd + r] = (p.ca * g + cb * (v[j] + g * g)) / NS_S;
+            h[j] = __float2half_rn(0.0f);
+          } else {
+            h[j] = __float2half_rn(p.ca * x[j] + cb * (v[j] + (g + d[j]) * x[j]));
+          }
+        }
+      } else {
+        uint4* al = reinterpret_cast<uint4*>(aux + rl * 128 + ((i ^ (rl & 7)) << 4));
+        float lo[8];
+        unpack8(*al, lo);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float both = x[j] + lo[j], y = p.diag_full ? both : x[j];
+          v[j] = f * (p.ca * both + d[j] * y) + cb * v[j];
+        }
+        if (p.last) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= p.scale;
+          if (p.out_vec) {
+            *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7]));
+          } else if (r < p.M) {
+            bf16* o = p.out_final + (size_t)t.mat * (size_t)p.M * p.N + (size_t)r * p.N + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (c + j < p.N) o[j] = __float2bfloat16_rn(v[j]);
+          }
+          continue;
+        }
+        __half l[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[j] = __float2half_rn(v[j]);
+          l[j] = __float2half_rn(v[j] - __half2float(h[j]));
+        }
+        *al = pack8(l);
+      }
     }
-    __half h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(v[j]);
-    *reinterpret_cast<uint4*>(p.out_hi + base + c8) = pack8(h);
-    if (KIND == NS_STEP) {
-      __half l[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) l[j] = __float2half_rn(v[j] - __half2float(h[j]));
-      *reinterpret_cast<uint4*>(p.out_lo + base + c8) = pack8(l);
-    } else if (mirror) {  // a warp's 32 rows are 64 consecutive bytes of the transposed row
+    *at = pack8(h);
+    if (mirror) {  // element (r, c) goes to row c, column r; two 64-column boxes
+      uint8_t* b = aux + (rl >> 6) * NS_BOX;
+      const int rc = rl & 63;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (c8 + j < p.N) p.out_hi[(size_t)t.mat * (size_t)p.M * p.ld + (size_t)(c8 + j) * p.ld + r] = h[j];
+        *reinterpret_cast<__half*>(b + (8 * i + j) * 128 + (((rc >> 3) ^ j) << 4) + (rc & 7) * 2) = h[j];
     }
   }
 }
@@ -185,20 +242,27 @@ __device__ __forceinline__ void ns_store32(const NsParams& p, const NsTile& t, i
 // Persistent CTA pairs, one per SM pair; pair u takes tiles u, u + pairs, ...
 // Warp 0: TMA producer of this CTA's operands (counted on the even CTA's full
 // barrier); warp 1 of the even CTA: tcgen05.mma for both; warps 2-5: epilogue
-// of this CTA's 128 rows.  Two 256-column accumulators in TMEM alternate, so a
-// tile's epilogue runs under the next tile's products.
+// of this CTA's 128 rows, 64 columns at a time; warp 6: loads the epilogue's
+// inputs into the two epilogue buffers and stores its outputs from them, both
+// by TMA, the loads ahead of the accumulator.  Two 256-column accumulators in
+// TMEM alternate, so a tile's epilogue runs under the next tile's products.
+// (Rows read and written by the threads themselves, 32 rows of 16 bytes at a
+// time, took 30 us a tile of X against 12 us of products.)
 template <int KIND, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_gemm(const __grid_constant__ NsMaps mp, const NsParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS_STAGES * NS_STAGE);  // [NS_STAGES]
+  uint8_t* ebuf = smem + NS_STAGES * NS_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ebuf + 2 * NS_EBUF);           // [NS_STAGES]
   uint64_t* empty = full + NS_STAGES;                                         // [NS_STAGES]
   uint64_t* tfull = empty + NS_STAGES;                                        // [2]
   uint64_t* tempty = tfull + 2;                                               // [2]
-  uint64_t* drain = tempty + 2;
+  uint64_t* eload = tempty + 2;                                               // [2] inputs landed (or buffer free)
+  uint64_t* edone = eload + 2;                                                // [2] outputs written
+  uint64_t* drain = edone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  static_assert((2 * NS_STAGES + 5) * 8 + 4 <= 256, "barrier area");
+  static_assert((2 * NS_STAGES + 9) * 8 + 4 <= 256, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)(cluster_ctarank() & 1u);
@@ -206,6 +270,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int n_units = p.nb * p.n_tiles;
   const int nk = (p.K + BK - 1) / BK;
+  // epilogue chunks of this CTA's part of a tile
+  auto chunks = [&](const NsTile& t) { return t.m0 + rank * 128 < p.M ? (min(NS_TILE, p.N - t.n0) + 63) / 64 : 0; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS_STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -214,6 +280,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 8);  // one arrival per epilogue warp of both CTAs
+      mbar_init(&eload[a], 1);
+      mbar_init(&edone[a], 4);   // one per epilogue warp
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -298,30 +366,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       mbar_wait_drain(drain, 0, p.timeout_ns);  // every MMA issued has completed before TMEM is freed
     }
     __syncwarp();
-  } else {
-    const int q = warp & 3;
+  } else if (warp < 6) {
+    const int q = warp & 3, rl = q * 32 + lane;
     const uint32_t tempty_even = mapa_shared(tempty, 0);
-    int i = 0;
-    for (int u = pair; u < n_units; u += pairs, ++i) {
+    int i = 0, n = 0;
+    bool ok = true;
+    for (int u = pair; u < n_units && ok; u += pairs, ++i) {
       const NsTile t = ns_tile<KIND>(p, u);
       const uint32_t acc = (uint32_t)i & 1u;
-      const int r = t.m0 + rank * 128 + q * 32 + lane;
+      const int nc = chunks(t);
       const float rho = p.first ? p.rho[t.mat] : 0.0f;
       if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tfull[acc], ((uint32_t)i >> 1) & 1u, p.status, p.timeout_ns))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * 256u;
 #pragma unroll 1
-      for (int c = 0; c < NS_TILE; c += 32) {
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(taddr + (uint32_t)c, v);
-        tmem_ld_wait();
-        if (r < p.M) ns_store32<KIND>(p, t, r, t.n0 + c, t.m0 != t.n0, rho, v);
+      for (int c = 0; c < nc; ++c, ++n) {
+        const int b = n & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&eload[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns))) { ok = false; break; }
+        uint8_t* e = ebuf + b * NS_EBUF;
+        ns_chunk<KIND>(p, t, e, e + 2 * NS_BOX, rl, t.m0 + rank * 128 + rl, t.n0 + 64 * c, rho, taddr + 64u * (uint32_t)c);
+        fence_proxy_async_smem();  // these writes, before the TMA store that follows the arrival
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&edone[b]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty_even + acc * 8u);
+      if (lane == 0 && ok) mbar_arrive_remote(tempty_even + acc * 8u);
     }
+  } else if (lane == 0) {
+    // chunk n uses buffer n & 1: loaded two chunks ahead, once the chunk before
+    // in that buffer has been stored
+    int lu = pair, lc = 0, ln = 0;  // next chunk to load: unit, chunk of its tile, number
+    auto load_next = [&]() {
+      while (lu < n_units) {
+        const NsTile t = ns_tile<KIND>(p, lu);
+        if (lc >= chunks(t)) {
+          lu += pairs;
+          lc = 0;
+          continue;
+        }
+        const int b = ln & 1, row = t.m0 + rank * 128, col = t.n0 + 64 * lc;
+        uint8_t* e = ebuf + b * NS_EBUF;
+        if (KIND == NS_GRAM) {
+          mbar_arrive(&eload[b]);
+        } else {
+          mbar_arrive_expect_tx(&eload[b], (KIND == NS_STEP ? 4u : 2u) * NS_BOX);
+          tma_load_3d(e, &mp.in0, &eload[b], col, row, t.mat);
+          if (KIND == NS_STEP) tma_load_3d(e + 2 * NS_BOX, &mp.in1, &eload[b], col, row, t.mat);
+        }
+        ++lc;
+        ++ln;
+        return;
+      }
+    };
+    load_next();
+    load_next();
+    int n = 0;
+    bool ok = true;
+    for (int u = pair; u < n_units && ok; u += pairs) {
+      const NsTile t = ns_tile<KIND>(p, u);
+      const int nc = chunks(t), row = t.m0 + rank * 128;
+      for (int c = 0; c < nc; ++c, ++n) {
+        const int b = n & 1, col = t.n0 + 64 * c;
+        if (!mbar_wait(&edone[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns)) { ok = false; break; }
+        const uint8_t* e = ebuf + b * NS_EBUF;
+        if (KIND == NS_STEP) {
+          if (!p.last || p.out_vec) tma_store_3d(&mp.out0, e, col, row, t.mat);
+          if (!p.last) tma_store_3d(&mp.out1, e + 2 * NS_BOX, col, row, t.mat);
+        } else {
+          tma_store_3d(&mp.out0, e, col, row, t.mat);
+          if (t.m0 != t.n0) {
+            tma_store_3d(&mp.out1, e + 2 * NS_BOX, row, col, t.mat);
+            if (row + 64 < p.M) tma_store_3d(&mp.out1, e + 3 * NS_BOX, row + 64, col, t.mat);
+          }
+        }
+        bulk_commit_group();
+        bulk_wait_group_read<0>();
+        load_next();
+      }
+    }
+    bulk_wait_group_all();
+    // (after a wait that ran out: the inputs still on their way have landed)
+    for (int k = ln > 2 ? ln - 2 : 0; k < ln; ++k) mbar_wait_drain(&eload[k & 1], ((uint32_t)k >> 1) & 1u, p.timeout_ns);
   }
+  __syncwarp();
   settle_after_abort(p.status);
   tc_fence_before();
   __syncthreads();
@@ -521,8 +649,8 @@ int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 bool ns_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 struct NsLayout {
-  size_t rho, part, hi[2], lo[2], a, b, total;
-  int64_t m, n, ldx, lda;
+  size_t rho, part, hi[2], lo[2], a, b, da, db, total;
+  int64_t m, n, ldx, lda, ldd;
 };
 
 NsLayout ns_layout(const moe_muon_plan* pl) {
@@ -532,6 +660,7 @@ NsLayout ns_layout(const moe_muon_plan* pl) {
   L.n = c.rows < c.cols ? c.cols : c.rows;
   L.ldx = up(c.cols, 8);
   L.lda = up(L.m, 8);
+  L.ldd = up(L.m, NS_TILE);  // the epilogue reads whole tiles' diagonals
   size_t off = 256;  // status word
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -546,18 +675,20 @@ NsLayout ns_layout(const moe_muon_plan* pl) {
   }
   L.a = take(sizeof(__half) * pl->chunk * L.m * L.lda);
   L.b = take(sizeof(__half) * pl->chunk * L.m * L.lda);
+  L.da = take(sizeof(float) * pl->chunk * L.ldd);
+  L.db = take(sizeof(float) * pl->chunk * L.ldd);
   L.total = off;
   return L;
 }
 
-// [nb, rows, cols] fp16, rows ld apart; box {64, box_rows, 1}; elements outside a matrix read as zero
-int ns_encode(const moe_muon_plan* pl, CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int64_t ld,
-              uint32_t box_rows) {
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)pl->chunk};
+// [nb, rows, cols] of 16-bit elements, rows ld apart; box {64, box_rows, 1}; elements outside a matrix read as zero
+int ns_encode(const moe_muon_plan* pl, CUtensorMap* m, const void* ptr, int64_t nb, int64_t rows, int64_t cols, int64_t ld,
+              uint32_t box_rows, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)nb};
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * rows) * 2};
   cuuint32_t box[3] = {64, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = pl->encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+  CUresult r = pl->encode(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_INVALID_ARG;
@@ -645,15 +776,19 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
   const bool tall = c.rows > c.cols;
   auto half_at = [&](size_t o) { return reinterpret_cast<__half*>(ws + o); };
 
-  // K-major operands are loaded 128 rows at a time, MN-major ones as {64, 64} boxes
-  CUtensorMap xk[2], xm[2], ak, bk;
+  // K-major operands and the epilogue's tiles are 128 rows at a time, MN-major
+  // operands and transposed tiles {64, 64} boxes
+  CUtensorMap xk[2], xm[2], xl[2], ak, am, bk, bm, uk;
   int rc = MOE_OK;
   for (int i = 0; i < 2; ++i) {
-    rc |= ns_encode(pl, &xk[i], half_at(L.hi[i]), c.rows, c.cols, L.ldx, 128);
-    rc |= ns_encode(pl, &xm[i], half_at(L.hi[i]), c.rows, c.cols, L.ldx, 64);
+    rc |= ns_encode(pl, &xk[i], half_at(L.hi[i]), pl->chunk, c.rows, c.cols, L.ldx, 128);
+    rc |= ns_encode(pl, &xm[i], half_at(L.hi[i]), pl->chunk, c.rows, c.cols, L.ldx, 64);
+    rc |= ns_encode(pl, &xl[i], half_at(L.lo[i]), pl->chunk, c.rows, c.cols, L.ldx, 128);
   }
-  rc |= ns_encode(pl, &ak, half_at(L.a), L.m, L.m, L.lda, 128);
-  rc |= ns_encode(pl, &bk, half_at(L.b), L.m, L.m, L.lda, 128);
+  rc |= ns_encode(pl, &ak, half_at(L.a), pl->chunk, L.m, L.m, L.lda, 128);
+  rc |= ns_encode(pl, &am, half_at(L.a), pl->chunk, L.m, L.m, L.lda, 64);
+  rc |= ns_encode(pl, &bk, half_at(L.b), pl->chunk, L.m, L.m, L.lda, 128);
+  rc |= ns_encode(pl, &bm, half_at(L.b), pl->chunk, L.m, L.m, L.lda, 64);
   if (rc != MOE_OK) return MOE_ERR_INVALID_ARG;
 
   PrepParams pp{};
@@ -680,6 +815,10 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
   g.status = reinterpret_cast<int*>(ws);
   g.timeout_ns = (long long)c.timeout_ms * 1000000LL;
   g.scale = scale / NS_S;
+  g.tall = tall;
+  g.ldd = (int)L.ldd;
+  g.diag_a = reinterpret_cast<float*>(ws + L.da);
+  g.diag_b = reinterpret_cast<float*>(ws + L.db);
   const int64_t mt = up(L.m, NS_TILE) / NS_TILE;
   for (int64_t c0 = 0; c0 < c.count; c0 += pl->chunk) {
     const int nb = (int)(c.count - c0 < pl->chunk ? c.count - c0 : pl->chunk);
@@ -697,48 +836,41 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
     }
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     g.nb = nb;
+    g.out_final = out;
+    g.out_vec = c.cols % 8 == 0 && ns_aligned(out, 16);
+    uk = xk[0];
+    if (g.out_vec && ns_encode(pl, &uk, out, nb, c.rows, c.cols, c.cols, 128, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) != MOE_OK)
+      return MOE_ERR_INVALID_ARG;
     for (int s = 0; s < c.steps; ++s) {
       const int x = s & 1;
-      NsMaps mp;
       cudaError_t err;
       g.first = s == 0;
       g.last = s == c.steps - 1;
+      g.diag_full = s >= c.steps - 2;
       // A = X X^T or X^T X
       g.M = g.N = (int)L.m;
       g.K = (int)L.n;
-      g.ld = L.lda;
       g.tiles_n = (int)mt;
       g.n_tiles = (int)(mt * (mt + 1) / 2);
-      g.out_hi = half_at(L.a);
-      mp.a = mp.b = tall ? xm[x] : xk[x];
-      err = tall ? ns_launch<NS_GRAM, true, true>(pl, mp, g, st) : ns_launch<NS_GRAM, false, false>(pl, mp, g, st);
+      const CUtensorMap& xx = tall ? xm[x] : xk[x];
+      const NsMaps gram = {xx, xx, ak, ak, ak, am};
+      err = tall ? ns_launch<NS_GRAM, true, true>(pl, gram, g, st) : ns_launch<NS_GRAM, false, false>(pl, gram, g, st);
       if (err != cudaSuccess) return MOE_ERR_CUDA;
       // B = b A + c A^2
       g.K = (int)L.m;
-      g.in_hi = half_at(L.a);
-      g.out_hi = half_at(L.b);
       g.ca = c.b;
       g.cb = c.c / NS_S;
-      mp.a = mp.b = ak;
-      if (ns_launch<NS_POLY, false, false>(pl, mp, g, st) != cudaSuccess) return MOE_ERR_CUDA;
+      const NsMaps poly = {ak, ak, ak, ak, bk, bm};
+      if (ns_launch<NS_POLY, false, false>(pl, poly, g, st) != cudaSuccess) return MOE_ERR_CUDA;
       // X <- a X + B X or a X + X B
       g.M = (int)c.rows;
       g.N = (int)c.cols;
-      g.K = (int)L.m;
-      g.ld = L.ldx;
       g.tiles_n = (int)(up(c.cols, NS_TILE) / NS_TILE);
       g.n_tiles = (int)(up(c.rows, NS_TILE) / NS_TILE) * g.tiles_n;
-      g.in_hi = half_at(L.hi[x]);
-      g.in_lo = half_at(L.lo[x]);
-      g.out_hi = half_at(L.hi[x ^ 1]);
-      g.out_lo = half_at(L.lo[x ^ 1]);
-      g.out_final = out;
-      g.out_vec = c.cols % 8 == 0 && ns_aligned(out, 16);
       g.ca = c.a;
       g.cb = 1.0f / NS_S;
-      mp.a = tall ? xk[x] : bk;
-      mp.b = tall ? bk : xm[x];
-      err = tall ? ns_launch<NS_STEP, false, false>(pl, mp, g, st) : ns_launch<NS_STEP, false, true>(pl, mp, g, st);
+      const NsMaps step = {tall ? xk[x] : bk, tall ? bk : xm[x], xk[x], xl[x], g.last ? uk : xk[x ^ 1], xl[x ^ 1]};
+      err = tall ? ns_launch<NS_STEP, false, false>(pl, step, g, st) : ns_launch<NS_STEP, false, true>(pl, step, g, st);
       if (err != cudaSuccess) return MOE_ERR_CUDA;
     }
   }
