@@ -8,18 +8,22 @@
 // largest keys are largest; the weights come from s alone.
 //
 // The selection is that of exact arithmetic.  Keys are computed in fp32 with a
-// known error; where a value on the losing side of the border (of the kept
-// groups, or of the k-th key) lies within that error of the border, and is not
-// an exact tie (the same logit and bias, decided by the lower id), the warp
-// decides the row again in fp64.  About one row in 1000 is that close with
-// fp32 logits, so the fp64 units do not show in the time; fp32 alone would
-// pick another expert in some rows of a large batch.
+// known error; where values on both sides of a border (of the kept groups, or
+// of the k-th key) lie within that error of it, and are not exact ties (the
+// same logit and bias, decided by the lower id), the warp decides that border
+// again in fp64, computing the few keys that lie in the band (all of them for
+// groups).  A row in some thousands is that close with fp32 logits; fp32 alone
+// would pick another expert in some rows of a large batch.
 //
-// One warp per row, 8 rows in flight per CTA, lane l holding the V consecutive
-// experts l V .. l V + V - 1 in registers: a row is read once, in 16-byte
-// loads, and nothing but the results is written.  Consecutive experts per lane
-// make "lowest id" the same as "lowest lane", so a tie costs nothing, and make
-// a group a set of neighbouring lanes.
+// One warp per row, lane l holding the V consecutive experts l V .. l V + V - 1
+// in registers: a row is read once, in 16-byte loads, and nothing but the
+// results is written.  Consecutive experts per lane make "lowest id" the same
+// as "lowest lane", and a group a set of neighbouring lanes.  The kernel is
+// bound by instruction issue, not by memory, so what a row costs is counted in
+// instructions: keys become integers in the floats' order, the k largest come
+// out by one redux.sync maximum each from the two largest of every lane (a
+// lane that holds three or more of them looks again), and the selected set is
+// then read off by comparing every key with the k-th.
 #include <cuda_fp16.h>
 
 #include <new>
@@ -31,13 +35,13 @@
 namespace moe {
 
 constexpr int ROUTE_WARPS = 8;          // rows in flight per CTA
-constexpr int ROUTE_CTAS_PER_SM = 4;    // of the persistent grid that sums over tokens
+constexpr int ROUTE_CTAS_PER_SM = 3;    // of the persistent grid that sums over tokens
 constexpr float ROUTE_TINY = 1e-36f;    // keys below this have lost their relative precision (fp32 underflow)
 
 struct RouteParams {
   const void* logits;
   int64_t ld, T;  // row stride in elements
-  int E, k, dtype, vec;
+  int E, k, dtype, vec, bvec;
   const float* bias;
   int n_group, topk_group, group_top, gs, renorm;
   float scale;
@@ -133,113 +137,156 @@ __device__ __forceinline__ float sum16(float v) {  // both halves of the warp al
 __device__ __forceinline__ float max32(float v) {  // NaN operands are passed over
   return ord_to(__reduce_max_sync(0xffffffffu, ord_of(v == v ? v : -INFINITY)));
 }
+__device__ __forceinline__ int add32(int v) { return __reduce_add_sync(0xffffffffu, v); }
+// e^x = 2^(x log2 e) for x in [-inf, 88], the rounding of the product carried
+// along (log2 e to 48 bits): relative error below 2^-21.9, flushed to 0 below 2^-126
+__device__ __forceinline__ float exp_fast(float x) {
+  x = fmaxf(x, -200.0f);
+  const float t = x * 1.44269502f;
+  const float r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+  return fmaf(y, r * 0.693147182f, y);
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp_fast(fminf(-x, 88.0f))); }
 // x - m where an infinite maximum is its own limit (0), not NaN
 __device__ __forceinline__ float below(float x, float m) { return x == m ? 0.0f : x - m; }
 
-// ------------------------------------------------------------------ the decision in fp64
-__device__ __forceinline__ double shfl_xor_d(double v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-__device__ __forceinline__ double max32d(double v) {
+// ------------------------------------------------------------------ decisions in fp64
+__device__ __forceinline__ unsigned long long ord_of64(double f) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(f + 0.0);
+  return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double ord_to64(unsigned long long u) {
+  return __longlong_as_double((long long)(u & 0x8000000000000000ull ? u ^ 0x8000000000000000ull : ~u));
+}
+__device__ __forceinline__ unsigned long long max32_64(unsigned long long v) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((unsigned long long)hi << 32) | lo;
+}
+__device__ __forceinline__ double sum32d(double v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmax(v, shfl_xor_d(v, o));
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Which of this lane's V experts are selected, as bits, computed in fp64 from
-// the row in memory.  Whole warp.
+// Softmax's maximum and sum over a row, in fp64.  Whole warp.
+template <int V>
+__device__ __forceinline__ void softmax_stats64(const RouteParams& p, const void* row, int lane, double* m, double* z) {
+  double x[V], lm = -INFINITY, lz = 0.0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float f = lane * V + j < p.E ? load_logit(row, p.dtype, lane * V + j) : -INFINITY;
+    x[j] = f == f ? (double)f : -INFINITY;
+    lm = fmax(lm, x[j]);
+  }
+  *m = ord_to64(max32_64(ord_of64(lm)));
+#pragma unroll
+  for (int j = 0; j < V; ++j) lz += x[j] > -INFINITY ? exp(x[j] == *m ? 0.0 : x[j] - *m) : 0.0;
+  *z = sum32d(lz);
+}
+// one expert's key (value, for groups without a bias); -inf if it is not to be selected
+template <bool kSoft>
+__device__ __forceinline__ double key64(const RouteParams& p, const void* row, int e, double m, double z) {
+  const double x = (double)load_logit(row, p.dtype, e);
+  if (!(x > -INFINITY)) return -INFINITY;
+  double s = kSoft ? exp(x == m ? 0.0 : x - m) / z : 1.0 / (1.0 + exp(-x));
+  if (p.bias) s += (double)p.bias[e];
+  return s > -INFINITY ? s : -INFINITY;
+}
+
+// The kept groups, as bits.  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ uint32_t select_fp64(const RouteParams& p, const void* row) {
+__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
-  double key[V];
-  uint32_t live = 0;
-  double m = -INFINITY;
+  double m = 0.0, z = 1.0;
+  if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
+  unsigned long long key[V];
+#pragma unroll
   for (int j = 0; j < V; ++j) {
-    const double x = e0 + j < p.E ? (double)load_logit(row, p.dtype, e0 + j) : -INFINITY;
-    key[j] = x;
-    if (x > -INFINITY) {
-      live |= 1u << j;
-      m = fmax(m, x);
-    }
+    const double v = e0 + j < p.E ? key64<kSoft>(p, row, e0 + j, m, z) : -INFINITY;
+    key[j] = v > -INFINITY ? ord_of64(v) : 0ull;
   }
-  m = max32d(m);
-  double z = 0.0;
-  for (int j = 0; j < V; ++j) {
-    if (!((live >> j) & 1)) continue;
-    if (kSoft) {
-      key[j] = exp(key[j] == m ? 0.0 : key[j] - m);
-      z += key[j];
-    } else {
-      key[j] = 1.0 / (1.0 + exp(-key[j]));
+  unsigned long long mine = 0;  // lane g: the score of group g
+  for (int g = 0; g < p.n_group; ++g) {
+    const int lo = g * p.gs - e0, hi = lo + p.gs;
+    unsigned long long b1 = 0, b2 = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const unsigned long long v = j >= lo && j < hi ? key[j] : 0ull;
+      b2 = max(b2, min(b1, v));
+      b1 = max(b1, v);
     }
+    const unsigned long long t1 = max32_64(b1);
+    const unsigned own = __ballot_sync(0xffffffffu, b1 == t1);
+    const unsigned long long t2 = max32_64(lane == __ffs(own) - 1 ? b2 : b1);
+    unsigned long long sc = t1;
+    if (p.group_top > 1 && t2) sc = ord_of64(ord_to64(t1) + ord_to64(t2));
+    if (lane == g) mine = sc;
   }
-  if (kSoft)
-    for (int o = 16; o > 0; o >>= 1) z += shfl_xor_d(z, o);
-  for (int j = 0; j < V; ++j) {
-    if (!((live >> j) & 1)) continue;
-    if (kSoft) key[j] /= z;
-    if (p.bias) key[j] += (double)p.bias[e0 + j];
-    if (!(key[j] > -INFINITY)) live &= ~(1u << j);
+  int rank = 0;
+  for (int g = 0; g < p.n_group; ++g) {
+    const unsigned long long v = __shfl_sync(0xffffffffu, mine, g);
+    rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
   }
-  if (p.n_group > 1) {
-    double mine = -INFINITY;  // lane g: the score of group g
-    for (int g = 0; g < p.n_group; ++g) {
-      double b1 = -INFINITY, b2 = -INFINITY;
-      for (int j = 0; j < V; ++j) {
-        if (!((live >> j) & 1) || (e0 + j) / p.gs != g) continue;
-        if (key[j] > b1) b2 = b1, b1 = key[j];
-        else if (key[j] > b2) b2 = key[j];
-      }
-      const double t1 = max32d(b1);
-      const unsigned own = __ballot_sync(0xffffffffu, b1 == t1);
-      const double t2 = max32d(lane == __ffs(own) - 1 ? b2 : b1);
-      const double s = p.group_top > 1 && t2 > -INFINITY ? t1 + t2 : t1;
-      if (lane == g) mine = s;
-    }
-    int rank = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      const double s = __shfl_sync(0xffffffffu, mine, g);
-      rank += (s > mine || (s == mine && g < lane)) ? 1 : 0;
-    }
-    const unsigned kept = __ballot_sync(0xffffffffu, lane < p.n_group && rank < p.topk_group);
-    for (int j = 0; j < V; ++j)
-      if (e0 + j < p.E && !((kept >> ((e0 + j) / p.gs)) & 1u)) live &= ~(1u << j);
-    if (!p.bias)  // without a bias the order is the logits'
-      for (int j = 0; j < V; ++j)
-        if ((live >> j) & 1) key[j] = (double)load_logit(row, p.dtype, e0 + j);
-  }
+  return __ballot_sync(0xffffffffu, lane < p.n_group && rank < p.topk_group);
+}
+
+// The `need` largest keys among the candidates (bits of this lane's experts),
+// as bits.  Whole warp.
+template <int V, bool kSoft>
+__device__ __noinline__ uint32_t band_fp64(const RouteParams& p, const void* row, uint32_t cand, int need) {
+  const int lane = threadIdx.x & 31, e0 = lane * V;
+  double m = 0.0, z = 1.0;
+  if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
   uint32_t sel = 0;
-  for (int i = 0; i < p.k; ++i) {
-    double b = -INFINITY;
-    int bj = -1;
-    for (int j = 0; j < V; ++j)
-      if (((live >> j) & 1) && (bj < 0 || key[j] > b)) b = key[j], bj = j;
-    const double t = max32d(b);
-    const unsigned own = __ballot_sync(0xffffffffu, bj >= 0 && b == t);
-    if (!own) break;
-    if (lane == __ffs(own) - 1) {
-      sel |= 1u << bj;
-      live &= ~(1u << bj);
+  unsigned long long best = 0;
+  int bj = 0;
+  auto scan = [&]() {  // (candidates are few: their keys are computed again rather than held)
+    best = 0;
+    for (uint32_t c = cand; c; c &= c - 1) {
+      const int j = __ffs(c) - 1;
+      const unsigned long long v = ord_of64(key64<kSoft>(p, row, e0 + j, m, z));
+      if (v > best) best = v, bj = j;
     }
+  };
+  scan();
+  for (int i = 0; i < need; ++i) {
+    const unsigned long long t = max32_64(best);
+    if (!t) break;
+    if (lane == __ffs(__ballot_sync(0xffffffffu, best == t)) - 1) {
+      sel |= 1u << bj;
+      cand &= ~(1u << bj);
+      scan();
+    }
+    __syncwarp();
   }
   return sel;
 }
 
 // ------------------------------------------------------------------ forward
-// A row without a border close enough to matter is decided in fp32.  Error of
-// a key: sigmoid, 4 ulp of s (expf 2, sum and quotient 1 each) plus the
-// rounding of s + b: below 2^-20 (|key| + max |b|) for both sides of a
-// comparison.  Softmax adds the rounding of x - m, (m - x) 2^-24 relative and
-// at most 104 before exp underflows: below 2^-16.
+// Relative error of fp32 keys, both sides of a comparison together.  Sigmoid:
+// e^-x 2^-21.9, 1 + e^-x 2^-24, the reciprocal 2^-23, s + b 2^-24: below 2^-20
+// each, of s and of |key|, so 2^-19 (|key| + max |b|).  Softmax adds the
+// rounding of x - m, (m - x) 2^-24, at most 104 before e^x is flushed, and the
+// row sum's: below 2^-16.
 template <int V, bool kSoft>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RouteParams p) {
-  constexpr float REL = kSoft ? 1.0f / 65536 : 1.0f / 1048576;
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
+  constexpr float REL = kSoft ? 1.0f / 65536 : 1.0f / 524288;
   __shared__ int s_hist[E_MAX];
   __shared__ int s_e[ROUTE_WARPS][TOPK_MAX];
-  __shared__ float s_x[ROUTE_WARPS][TOPK_MAX];
-  __shared__ float s_p[ROUTE_WARPS][E_MAX];
+  __shared__ float s_p[ROUTE_WARPS][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const bool sums = p.prob_sum != nullptr, grouped = p.n_group > 1;
-  const bool with_keys = p.bias != nullptr;                                // the order is s + b's, not x's
-  const bool group_scores = grouped && (with_keys || p.group_top > 1);     // groups are ranked by computed values
+  const bool with_keys = p.bias != nullptr;                             // the order is s + b's, not x's
+  const bool group_scores = grouped && (with_keys || p.group_top > 1);  // groups are ranked by computed values
+  const bool scored = with_keys || sums || group_scores || (kSoft && !p.renorm);
   // groups made of whole, aligned sets of lanes are ranked by butterflies
   const int glanes = p.gs / V;
   const bool aligned_groups = grouped && p.gs % V == 0 && (glanes & (glanes - 1)) == 0 && glanes <= 32;
@@ -247,12 +294,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
   }
-  float b[V], bmax = 0.0f, acc[V];
+  float bmax = 0.0f, acc[V];
+  uint32_t gid[(V + 3) / 4];  // the experts' groups, a byte each
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    b[j] = with_keys && e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
-    bmax = fmaxf(bmax, fabsf(b[j]));
+    if (with_keys && e0 + j < p.E) bmax = fmaxf(bmax, fabsf(p.bias[e0 + j]));
     acc[j] = 0.0f;
+    if (j % 4 == 0) gid[j / 4] = 0;
+    gid[j / 4] |= (uint32_t)min((e0 + j) / p.gs, 31) << (8 * (j % 4));
   }
   bmax = max32(bmax);
   const size_t row_bytes = (size_t)p.ld * (p.dtype == MOE_DTYPE_FP32 ? 4 : 2);
@@ -262,7 +311,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
     float x[V];
     load_row<V>(row, p.dtype, p.vec, lane, p.E, x);
 
-    // scores: s (sigmoid) or e^(x - m) (softmax; z is the row's sum), where anything needs them
+    // scores, where anything needs them: s (sigmoid) or e^(x - m) (softmax), z the row's sum
     float s[V];
     float m = 0.0f, z = 1.0f;
     bool nan_row = false;
@@ -277,29 +326,31 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
       m = max32(lm);
       nan_row = __any_sync(0xffffffffu, nan);
     }
-    if (kSoft ? (with_keys || sums || group_scores || !p.renorm) : (with_keys || sums || group_scores)) {
-      float lz = 0.0f;
+    if (scored) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        s[j] = 0.0f;
-        if (x[j] > -INFINITY) s[j] = kSoft ? expf(below(x[j], m)) : 1.0f / (1.0f + expf(-x[j]));
-        lz += s[j];
+      for (int j = 0; j < V; ++j)
+        s[j] = x[j] > -INFINITY ? (kSoft ? exp_fast(below(x[j], m)) : sigmoid_fast(x[j])) : 0.0f;
+      if (kSoft || sums) {
+        float lz = 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) lz += s[j];
+        z = sum32(lz);
       }
-      if (kSoft || sums) z = sum32(lz);
     }
+    const float inv_z = z > 0.0f ? 1.0f / z : 0.0f;
     if (sums) {  // normalised scores, s over the row's sum
       if (!kSoft && m < -20.0f && m > -INFINITY) {  // e^x to fp32 precision: shifted, so that it does not underflow
         float u[V], lz = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          u[j] = x[j] > -INFINITY ? expf(x[j] - m) : 0.0f;
+          u[j] = x[j] > -INFINITY ? exp_fast(x[j] - m) : 0.0f;
           lz += u[j];
         }
-        const float inv = 1.0f / sum32(lz);
+        const float inv = nan_row ? NAN : 1.0f / sum32(lz);
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += u[j] * inv;
       } else {
-        const float inv = nan_row ? NAN : (z > 0.0f ? 1.0f / z : 0.0f);
+        const float inv = nan_row ? NAN : inv_z;
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += s[j] * inv;
       }
@@ -307,27 +358,31 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
 
     // order of the experts as integers, 0 = not to be selected
     uint32_t key[V];
-    const float inv_z = kSoft ? (z > 0.0f ? 1.0f / z : 0.0f) : 1.0f;
+    if (with_keys) {  // (the bias stays in L1, not in registers)
+      float b[V];
+      load_row<V>(p.bias, MOE_DTYPE_FP32, p.bvec, lane, p.E, b);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float f = x[j];
-      if (with_keys) f = (kSoft ? s[j] * inv_z : s[j]) + b[j];
-      key[j] = x[j] > -INFINITY && f > -INFINITY ? ord_of(f) : 0u;
+      for (int j = 0; j < V; ++j) {
+        const float f = x[j] > -INFINITY ? (kSoft ? s[j] * inv_z : s[j]) + b[j] : -INFINITY;
+        key[j] = f > -INFINITY ? ord_of(f) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) key[j] = x[j] > -INFINITY ? ord_of(x[j]) : 0u;
     }
 
-    bool close = false;  // some border is within the keys' error
+    uint32_t a1 = 0, a2 = 0;  // this lane's two largest keys
     if (grouped) {
-      // the two largest of each group; without a bias the (order-keeping) scores, or for the maximum alone x itself
-      uint32_t gk[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) gk[j] = group_scores && !with_keys ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
-      uint32_t g1 = 0, g2 = 0;  // lane g: the largest two of group g
+      // each group's two largest; without a bias of the (order-keeping) scores, or, for the maximum alone, of x
+      const bool by_score = group_scores && !with_keys;
+      uint32_t g1 = 0, g2 = 0;  // lane g: those of group g
       if (aligned_groups) {
         uint32_t t1 = 0, t2 = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          t2 = max(t2, min(t1, gk[j]));
-          t1 = max(t1, gk[j]);
+          const uint32_t v = by_score ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
+          t2 = max(t2, min(t1, v));
+          t1 = max(t1, v);
         }
         for (int o = 1; o < glanes; o <<= 1) {
           const uint32_t u1 = __shfl_xor_sync(0xffffffffu, t1, o), u2 = __shfl_xor_sync(0xffffffffu, t2, o);
@@ -344,7 +399,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
           uint32_t t1 = 0, t2 = 0;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const uint32_t v = j >= lo && j < hi ? gk[j] : 0u;
+            uint32_t v = by_score ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
+            v = j >= lo && j < hi ? v : 0u;
             t2 = max(t2, min(t1, v));
             t1 = max(t1, v);
           }
@@ -363,83 +419,110 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
         rank += (v > score || (v == score && g < lane)) ? 1 : 0;
       }
       const bool in = lane < p.n_group && rank < p.topk_group;
-      const unsigned kept = __ballot_sync(0xffffffffu, in);
+      unsigned kept = __ballot_sync(0xffffffffu, in);
       if (group_scores && p.topk_group < p.n_group) {
         const uint32_t lo = __reduce_min_sync(0xffffffffu, in ? score : 0xffffffffu);
         const uint32_t hi = __reduce_max_sync(0xffffffffu, in || lane >= p.n_group ? 0u : score);
         if (hi) {
           const float fl = ord_to(lo), fh = ord_to(hi);
-          close = !(fl - fh > REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY);
+          if (!(fl - fh > REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY)) kept = groups_fp64<V, kSoft>(p, row);
         }
       }
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (e0 + j < p.E && !((kept >> ((e0 + j) / p.gs)) & 1u)) key[j] = 0;
+        if (!((kept >> ((gid[j / 4] >> (8 * (j % 4))) & 31u)) & 1u)) key[j] = 0;
     }
-
-    // the k largest, the lowest id first among equals
-    uint32_t sel = 0, lbest = 0, last = 0;
-    int lj = 0, owner = 0;
-    int n_sel = 0;
-    auto scan = [&]() {
-      lbest = 0;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (key[j] > lbest && !((sel >> j) & 1u)) lbest = key[j], lj = j;
-    };
-    scan();
-    for (; n_sel < p.k; ++n_sel) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, lbest);
-      if (!best) break;
-      last = best;
-      owner = __ffs(__ballot_sync(0xffffffffu, lbest == best)) - 1;
-      if (lane == owner) {
-        sel |= 1u << lj;
-        scan();
-      }
-    }
-    if (with_keys && n_sel == p.k) {
-      // keys within the error of the k-th: unless all of them are the same logit and bias, it is too close
-      const float fk = ord_to(last), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
-      float lx = 0.0f, lb = 0.0f;
-      bool some = false, mixed = false;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (key[j] && !(fabsf(ord_to(key[j]) - fk) > tol)) {
-          mixed |= some && (x[j] != lx || b[j] != lb);
-          lx = x[j], lb = b[j], some = true;
-        }
-      }
-      const unsigned who = __ballot_sync(0xffffffffu, some);
-      const int first = __ffs(who) - 1;  // (the k-th itself is among them)
-      const float rx = __shfl_sync(0xffffffffu, lx, first), rb = __shfl_sync(0xffffffffu, lb, first);
-      close |= __any_sync(0xffffffffu, mixed || (some && (lx != rx || lb != rb)));
-    }
-    if (close) sel = select_fp64<V, kSoft>(p, row);
-
-    // slots in ascending id: one lane per slot
-    const int mine = __popc(sel);
-    int before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += n;
-    }
-    n_sel = __shfl_sync(0xffffffffu, before, 31);
-    before -= mine;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      if ((sel >> j) & 1u) {
-        s_e[warp][before] = e0 + j;
-        s_x[warp][before] = x[j];
-        ++before;
+      a2 = max(a2, min(a1, key[j]));
+      a1 = max(a1, key[j]);
+    }
+
+    // the k-th largest key
+    uint32_t kth = 0;
+    int n = 0, taken = 0;
+    for (; n < p.k; ++n) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, a1);
+      if (!best) break;
+      kth = best;
+      if (lane == __ffs(__ballot_sync(0xffffffffu, a1 == best)) - 1) {
+        ++taken;
+        a1 = a2;
+        a2 = 0;
+        if (!a1) {  // both are gone: the next one, counting equal keys
+          int ge = 0;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            ge += key[j] >= best ? 1 : 0;
+            a1 = max(a1, key[j] < best ? key[j] : 0u);
+          }
+          if (ge > taken) a1 = best;
+        }
       }
     }
+    // the selected: keys above it, and as many equal ones, lowest ids first, as there is room for
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      gt |= key[j] > kth ? 1u << j : 0u;
+      eq |= key[j] == kth && kth ? 1u << j : 0u;
+    }
+    int room = n - add32(__popc(gt));
+    uint32_t sel = gt | eq;
+    if (add32(__popc(eq)) > room) {
+      int before = __popc(eq);
+      const int mine = before;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      room -= before - mine;
+      sel = gt;
+      for (; eq && room > 0; eq &= eq - 1, --room) sel |= eq & -eq;
+    }
+    if (with_keys && n == p.k) {
+      // keys within the error of the k-th: unless all of them are one logit with one bias, they are compared in fp64
+      const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
+      const uint32_t lo = ord_of(fk - tol), hi = ord_of(fk + tol);
+      uint32_t band = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) band |= key[j] >= lo && key[j] <= hi ? 1u << j : 0u;
+      if (add32(__popc(band)) > 1) {
+        float lx = 0.0f, lb = 0.0f;
+        bool some = false, mixed = false;
+        for (uint32_t c = band; c; c &= c - 1) {
+          const int e = e0 + __ffs(c) - 1;
+          const float xe = load_logit(row, p.dtype, e), be = p.bias[e];
+          mixed |= some && (xe != lx || be != lb);
+          lx = xe, lb = be, some = true;
+        }
+        const int first = __ffs(__ballot_sync(0xffffffffu, some)) - 1;
+        const float rx = __shfl_sync(0xffffffffu, lx, first), rb = __shfl_sync(0xffffffffu, lb, first);
+        if (__any_sync(0xffffffffu, mixed || (some && (lx != rx || lb != rb)))) {
+          sel = 0;
+#pragma unroll
+          for (int j = 0; j < V; ++j) sel |= key[j] > hi ? 1u << j : 0u;
+          sel |= band_fp64<V, kSoft>(p, row, band, p.k - add32(__popc(sel)));
+        }
+      }
+    }
+
+    // slots in ascending id, one lane each
+    int before = __popc(sel);
+    const int mine = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    before -= mine;
+    for (uint32_t c = sel; c; c &= c - 1) s_e[warp][before++] = e0 + __ffs(c) - 1;
     __syncwarp();
-    const bool on = lane < n_sel;
+    const bool on = lane < n;
     const int e = on ? s_e[warp][lane] : -1;
-    const float xs = on ? s_x[warp][lane] : -INFINITY;
     __syncwarp();
+    const float xs = on ? load_logit(row, p.dtype, e) : -INFINITY;
     float w = 0.0f;
     if (p.renorm) {  // over the selected: a common factor cancels, so scores that underflow are shifted
       const float ms = max32(xs);
@@ -460,8 +543,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_kernel(const RoutePara
   if (p.counts || sums) {
     if (sums) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (e0 + j < p.E) s_p[warp][e0 + j] = acc[j];
+      for (int j = 0; j < V; ++j) s_p[warp][e0 + j] = acc[j];
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
@@ -531,7 +613,7 @@ struct RouteBwdParams {
 // lane, meet the row's through shared memory.  Renormalised weights without
 // prob_sum need the selected logits only, so the row itself is not read.
 template <int V, bool kSoft>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const RouteBwdParams p) {
+__global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __grid_constant__ RouteBwdParams p) {
   __shared__ __align__(16) float s_a[ROUTE_WARPS][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const bool sums = p.dprob_sum != nullptr, dense = sums || (kSoft && !p.renorm);
@@ -764,6 +846,7 @@ int moe_route(const moe_route_plan* pl, int64_t T, const void* logits, int64_t l
   p.dtype = c.logits_dtype;
   p.vec = route_aligned(logits, 16) && logits_stride * (int64_t)dtype_size(c.logits_dtype) % 16 == 0;
   p.bias = bias;
+  p.bvec = route_aligned(bias, 16);
   p.n_group = (int)c.n_group;
   p.topk_group = (int)c.topk_group;
   p.group_top = c.group_top;
