@@ -20,10 +20,11 @@
 // results is written.  Consecutive experts per lane make "lowest id" the same
 // as "lowest lane", and a group a set of neighbouring lanes.  The kernel is
 // bound by instruction issue, not by memory, so what a row costs is counted in
-// instructions: keys become integers in the floats' order, the k largest come
-// out by one redux.sync maximum each from the two largest of every lane (a
-// lane that holds three or more of them looks again), and the selected set is
-// then read off by comparing every key with the k-th.
+// instructions.  Keys become integers in the floats' order.  The k-th largest
+// of the lanes' maxima (k redux.sync maxima) is a lower bound for the k-th
+// key; the keys above it, little more than k, move to one lane each, where a
+// row's worth of ranking, ties, checks and weights is a few instructions for
+// the whole warp.
 #include <cuda_fp16.h>
 
 #include <new>
@@ -116,10 +117,11 @@ __device__ __forceinline__ void load_row(const void* row, int dtype, int vec, in
 }
 
 // Floats in the order of unsigned integers; nothing finite or infinite maps to 0.
-__device__ __forceinline__ uint32_t ord_of(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);  // -0 equals +0
+__device__ __forceinline__ uint32_t ord_bits(float f) {
+  const uint32_t u = __float_as_uint(f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t ord_of(float f) { return ord_bits(f + 0.0f); }  // -0 equals +0
 __device__ __forceinline__ float ord_to(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
@@ -138,22 +140,20 @@ __device__ __forceinline__ float max32(float v) {  // NaN operands are passed ov
   return ord_to(__reduce_max_sync(0xffffffffu, ord_of(v == v ? v : -INFINITY)));
 }
 __device__ __forceinline__ int add32(int v) { return __reduce_add_sync(0xffffffffu, v); }
-// e^x = 2^(x log2 e) for x in [-inf, 88], the rounding of the product carried
-// along (log2 e to 48 bits): relative error below 2^-21.9, flushed to 0 below 2^-126
-__device__ __forceinline__ float exp_fast(float x) {
-  x = fmaxf(x, -200.0f);
-  const float t = x * 1.44269502f;
-  const float r = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -t));
+// e^x = 2^(x log2 e): relative error (|x| + 3) 2^-24, flushed to 0 below 2^-126, infinite above 2^128
+__device__ __forceinline__ float exp2_fast(float t) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
-  return fmaf(y, r * 0.693147182f, y);
+  return y;
 }
+constexpr float LOG2E = 1.44269504f;
 __device__ __forceinline__ float rcp_fast(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp_fast(fminf(-x, 88.0f))); }
+// 0 at -inf, 1 at +inf
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(x * -LOG2E)); }
 // x - m where an infinite maximum is its own limit (0), not NaN
 __device__ __forceinline__ float below(float x, float m) { return x == m ? 0.0f : x - m; }
 
@@ -201,54 +201,82 @@ __device__ __forceinline__ double key64(const RouteParams& p, const void* row, i
   return s > -INFINITY ? s : -INFINITY;
 }
 
-// The kept groups, as bits.  Whole warp.
+// The kept groups, as bits.  state, for lane g's group: 2 kept, 0 not kept, 1
+// to be decided by the candidates' keys (bits of this lane's experts, which
+// hold the largest of every such group).  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row) {
+__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row, uint32_t cand, int state, uint2* buf) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
   double m = 0.0, z = 1.0;
   if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
-  unsigned long long key[V];
+  unsigned long long score = state == 2 ? ~0ull : 0ull, best1 = 0, best2 = 0;  // lane g: of group g so far
+  // the candidates, one per lane, 32 at a time
+  int before = __popc(cand);
+  const int mine = before;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const double v = e0 + j < p.E ? key64<kSoft>(p, row, e0 + j, m, z) : -INFINITY;
-    key[j] = v > -INFINITY ? ord_of64(v) : 0ull;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
   }
-  unsigned long long mine = 0;  // lane g: the score of group g
-  for (int g = 0; g < p.n_group; ++g) {
-    const int lo = g * p.gs - e0, hi = lo + p.gs;
-    unsigned long long b1 = 0, b2 = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const unsigned long long v = j >= lo && j < hi ? key[j] : 0ull;
-      b2 = max(b2, min(b1, v));
-      b1 = max(b1, v);
+  const int total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
+  for (int c0 = 0; c0 < total; c0 += 32) {
+    for (uint32_t c = cand, at = (uint32_t)before; c; c &= c - 1, ++at)
+      if ((int)at >= c0 && (int)at < c0 + 32) buf[at - c0].x = (uint32_t)(e0 + __ffs(c) - 1);
+    __syncwarp();
+    const int n = min(32, total - c0);
+    unsigned long long key = 0ull;
+    int g = -1;
+    if (lane < n) {
+      const int e = (int)buf[lane].x;
+      const double v = key64<kSoft>(p, row, e, m, z);
+      key = v > -INFINITY ? ord_of64(v) : 0ull;
+      g = e / p.gs;
     }
-    const unsigned long long t1 = max32_64(b1);
-    const unsigned own = __ballot_sync(0xffffffffu, b1 == t1);
-    const unsigned long long t2 = max32_64(lane == __ffs(own) - 1 ? b2 : b1);
-    unsigned long long sc = t1;
-    if (p.group_top > 1 && t2) sc = ord_of64(ord_to64(t1) + ord_to64(t2));
-    if (lane == g) mine = sc;
+    __syncwarp();
+    for (int i = 0; i < n; ++i) {
+      const unsigned long long v = __shfl_sync(0xffffffffu, key, i);
+      const int vg = __shfl_sync(0xffffffffu, g, i);
+      if (vg == lane) {
+        best2 = max(best2, min(best1, v));
+        best1 = max(best1, v);
+      }
+    }
   }
+  if (state == 1) score = p.group_top > 1 && best2 ? ord_of64(ord_to64(best1) + ord_to64(best2)) : best1;
   int rank = 0;
   for (int g = 0; g < p.n_group; ++g) {
-    const unsigned long long v = __shfl_sync(0xffffffffu, mine, g);
-    rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
+    const unsigned long long v = __shfl_sync(0xffffffffu, score, g);
+    rank += (v > score || (v == score && g < lane)) ? 1 : 0;
   }
   return __ballot_sync(0xffffffffu, lane < p.n_group && rank < p.topk_group);
 }
 
-// The `need` largest keys among the candidates (bits of this lane's experts),
-// as bits.  Whole warp.
+// Whether this lane's candidate (expert e, -1 for none; ids ascend with the
+// lanes) is one of the `need` with the largest keys.  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ uint32_t band_fp64(const RouteParams& p, const void* row, uint32_t cand, int need) {
+__device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, int e, int need) {
+  const int lane = threadIdx.x & 31;
+  double m = 0.0, z = 1.0;
+  if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
+  const unsigned long long key = e >= 0 ? ord_of64(key64<kSoft>(p, row, e, m, z)) : 0ull;
+  int rank = 0;
+  for (int i = 0; i < 32; ++i) {
+    const unsigned long long v = __shfl_sync(0xffffffffu, key, i);
+    rank += (v > key || (v == key && i < lane)) ? 1 : 0;
+  }
+  return e >= 0 && rank < need;
+}
+// The same for candidates as bits of each lane's experts.
+template <int V, bool kSoft>
+__device__ __noinline__ uint32_t wide_band_fp64(const RouteParams& p, const void* row, uint32_t cand, int need) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
   double m = 0.0, z = 1.0;
   if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
   uint32_t sel = 0;
   unsigned long long best = 0;
   int bj = 0;
-  auto scan = [&]() {  // (candidates are few: their keys are computed again rather than held)
+  auto scan = [&]() {
     best = 0;
     for (uint32_t c = cand; c; c &= c - 1) {
       const int j = __ffs(c) - 1;
@@ -257,6 +285,7 @@ __device__ __noinline__ uint32_t band_fp64(const RouteParams& p, const void* row
     }
   };
   scan();
+  __syncwarp();
   for (int i = 0; i < need; ++i) {
     const unsigned long long t = max32_64(best);
     if (!t) break;
@@ -271,16 +300,17 @@ __device__ __noinline__ uint32_t band_fp64(const RouteParams& p, const void* row
 }
 
 // ------------------------------------------------------------------ forward
-// Relative error of fp32 keys, both sides of a comparison together.  Sigmoid:
-// e^-x 2^-21.9, 1 + e^-x 2^-24, the reciprocal 2^-23, s + b 2^-24: below 2^-20
-// each, of s and of |key|, so 2^-19 (|key| + max |b|).  Softmax adds the
-// rounding of x - m, (m - x) 2^-24, at most 104 before e^x is flushed, and the
-// row sum's: below 2^-16.
+// REL: relative error of fp32 keys, both sides of a comparison together.
+// Sigmoid: e^-x, the sum 2^-24, the reciprocal 2^-23; e^-x is off by
+// (|x| + 3) 2^-24 and weighs 1 - s: for keys above ROUTE_TINY (x > -83) below
+// 2^-17.3 of s and, with the rounding of s + b, 2^-16 (|key| + max |b|) for the
+// two sides.  Softmax: (m - x + 3) 2^-24, at most 104 before e^x is flushed,
+// the row sum and its reciprocal: below 2^-16 as well.
 template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
-  constexpr float REL = kSoft ? 1.0f / 65536 : 1.0f / 524288;
+  constexpr float REL = 1.0f / 65536;
   __shared__ int s_hist[E_MAX];
-  __shared__ int s_e[ROUTE_WARPS][TOPK_MAX];
+  __shared__ uint2 s_c[ROUTE_WARPS][32];  // candidates: key, expert
   __shared__ float s_p[ROUTE_WARPS][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const bool sums = p.prob_sum != nullptr, grouped = p.n_group > 1;
@@ -295,13 +325,22 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
     __syncthreads();
   }
   float bmax = 0.0f, acc[V];
-  uint32_t gid[(V + 3) / 4];  // the experts' groups, a byte each
+  uint32_t gid[(V + 3) / 4];  // the experts' groups, a byte each (aligned groups: the lane's, once)
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (with_keys && e0 + j < p.E) bmax = fmaxf(bmax, fabsf(p.bias[e0 + j]));
-    acc[j] = 0.0f;
-    if (j % 4 == 0) gid[j / 4] = 0;
-    gid[j / 4] |= (uint32_t)min((e0 + j) / p.gs, 31) << (8 * (j % 4));
+  for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < (V + 3) / 4; ++j) gid[j] = 0;
+  if (aligned_groups) {
+    gid[0] = (uint32_t)min(lane / glanes, 31);
+  } else if (grouped) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) gid[j / 4] |= (uint32_t)min((e0 + j) / p.gs, 31) << (8 * (j % 4));
+  }
+  if (with_keys) {
+    float b[V];
+    load_row<V>(p.bias, MOE_DTYPE_FP32, p.bvec, lane, p.E, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) bmax = fmaxf(bmax, e0 + j < p.E ? fabsf(b[j]) : 0.0f);
   }
   bmax = max32(bmax);
   const size_t row_bytes = (size_t)p.ld * (p.dtype == MOE_DTYPE_FP32 ? 4 : 2);
@@ -317,36 +356,54 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
     bool nan_row = false;
     if (kSoft || sums) {
       float lm = -INFINITY;
-      bool nan = false;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        lm = fmaxf(lm, x[j]);
-        nan |= x[j] != x[j];
-      }
+      for (int j = 0; j < V; ++j) lm = fmaxf(lm, x[j]);
       m = max32(lm);
-      nan_row = __any_sync(0xffffffffu, nan);
     }
     if (scored) {
+      if (kSoft) {
+        // an infinite maximum is its own limit: those logits share the row
+        const float mm = m * LOG2E;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        s[j] = x[j] > -INFINITY ? (kSoft ? exp_fast(below(x[j], m)) : sigmoid_fast(x[j])) : 0.0f;
+        for (int j = 0; j < V; ++j) s[j] = x[j] == m ? 1.0f : exp2_fast(fmaf(x[j], LOG2E, -mm));
+        if (m == -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[j] = x[j] != x[j] ? x[j] : 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] = sigmoid_fast(x[j]);
+      }
       if (kSoft || sums) {
         float lz = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) lz += s[j];
         z = sum32(lz);
+        nan_row = z != z;
+        if (kSoft && nan_row) {  // the NaNs are not selected; the others keep their order
+          lz = 0.0f;
+#pragma unroll
+          for (int j = 0; j < V; ++j) lz += x[j] > -INFINITY ? s[j] : 0.0f;
+          z = sum32(lz);
+        }
       }
     }
-    const float inv_z = z > 0.0f ? 1.0f / z : 0.0f;
+    if (kSoft && !scored) {
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < V; ++j) nan |= x[j] != x[j];
+      nan_row = __any_sync(0xffffffffu, nan);
+    }
+    const float inv_z = z > 0.0f ? rcp_fast(z) : 0.0f;
     if (sums) {  // normalised scores, s over the row's sum
       if (!kSoft && m < -20.0f && m > -INFINITY) {  // e^x to fp32 precision: shifted, so that it does not underflow
         float u[V], lz = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          u[j] = x[j] > -INFINITY ? exp_fast(x[j] - m) : 0.0f;
+          u[j] = exp2_fast((x[j] - m) * LOG2E);
           lz += u[j];
         }
-        const float inv = nan_row ? NAN : 1.0f / sum32(lz);
+        const float inv = rcp_fast(sum32(lz));
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += u[j] * inv;
       } else {
@@ -363,15 +420,14 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
       load_row<V>(p.bias, MOE_DTYPE_FP32, p.bvec, lane, p.E, b);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float f = x[j] > -INFINITY ? (kSoft ? s[j] * inv_z : s[j]) + b[j] : -INFINITY;
-        key[j] = f > -INFINITY ? ord_of(f) : 0u;
+        const float f = kSoft ? fmaf(s[j], inv_z, b[j]) : s[j] + b[j];  // (never -0)
+        key[j] = x[j] > -INFINITY && f > -INFINITY ? ord_bits(f) : 0u;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) key[j] = x[j] > -INFINITY ? ord_of(x[j]) : 0u;
     }
 
-    uint32_t a1 = 0, a2 = 0;  // this lane's two largest keys
     if (grouped) {
       // each group's two largest; without a bias of the (order-keeping) scores, or, for the maximum alone, of x
       const bool by_score = group_scores && !with_keys;
@@ -424,33 +480,112 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
         const uint32_t lo = __reduce_min_sync(0xffffffffu, in ? score : 0xffffffffu);
         const uint32_t hi = __reduce_max_sync(0xffffffffu, in || lane >= p.n_group ? 0u : score);
         if (hi) {
-          const float fl = ord_to(lo), fh = ord_to(hi);
-          if (!(fl - fh > REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY)) kept = groups_fp64<V, kSoft>(p, row);
+          const float fl = ord_to(lo), fh = ord_to(hi), tol = REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY;
+          if (!(fl - fh > tol)) {
+            // groups that may lie on either side, and in them the keys that may be among their largest
+            const bool band = lane < p.n_group && score && ord_to(score) >= fh - tol && ord_to(score) <= fl + tol;
+            uint32_t least = 0xffffffffu;
+            if (band) least = p.group_top > 1 && g2 ? g2 : g1;
+            if (band) {
+              const float f = ord_to(least);
+              least = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
+            }
+            uint32_t cand = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const int g = aligned_groups ? (int)gid[0] : (int)((gid[j / 4] >> (8 * (j % 4))) & 31u);
+              const uint32_t from = __shfl_sync(0xffffffffu, least, g);
+              const uint32_t v = by_score ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
+              cand |= v && v >= from ? 1u << j : 0u;
+            }
+            // (lane g: 2 its group is in, 0 it is out, 1 to be decided)
+            kept = groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, &s_c[warp][0]);
+          }
         }
       }
+      if (aligned_groups) {
+        const bool keep = (kept >> gid[0]) & 1u;  // all of a lane's experts are in one group
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = keep ? key[j] : 0u;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (!((kept >> ((gid[j / 4] >> (8 * (j % 4))) & 31u)) & 1u)) key[j] = 0;
+      }
+    }
+    uint32_t a1 = 0;  // this lane's largest key
+#pragma unroll
+    for (int j = 0; j < V; ++j) a1 = max(a1, key[j]);
+
+    // k lanes' maxima at least reach `floor`, so the k-th key does too (0: fewer lanes have keys)
+    uint32_t floor = 0xffffffffu;
+    {
+      uint32_t a = a1;
+      for (int i = 0; i < p.k && floor; ++i) {
+        floor = __reduce_max_sync(0xffffffffu, a);
+        a = a == floor ? 0u : a;
+      }
+    }
+    // candidates: the keys from there up, and those that their error might lift there
+    if (with_keys && floor) {
+      const float f = ord_to(floor);
+      floor = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
+    }
+    floor = max(floor, 1u);
+    uint32_t cand = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) cand |= key[j] >= floor ? 1u << j : 0u;
+    int before = __popc(cand);
+    const int mine = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    const int n_cand = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    int e = -1;  // this lane's selected expert; ids ascend with the lanes
+    if (n_cand <= 32) {
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (!((kept >> ((gid[j / 4] >> (8 * (j % 4))) & 31u)) & 1u)) key[j] = 0;
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      a2 = max(a2, min(a1, key[j]));
-      a1 = max(a1, key[j]);
-    }
-
-    // the k-th largest key
-    uint32_t kth = 0;
-    int n = 0, taken = 0;
-    for (; n < p.k; ++n) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, a1);
-      if (!best) break;
-      kth = best;
-      if (lane == __ffs(__ballot_sync(0xffffffffu, a1 == best)) - 1) {
-        ++taken;
-        a1 = a2;
-        a2 = 0;
-        if (!a1) {  // both are gone: the next one, counting equal keys
-          int ge = 0;
+        if ((cand >> j) & 1u) s_c[warp][before++] = make_uint2(key[j], (uint32_t)(e0 + j));
+      __syncwarp();
+      uint2 c = make_uint2(0u, 0u);
+      if (lane < n_cand) c = s_c[warp][lane];
+      int rank = 0;
+      for (int i = 0; i < n_cand; ++i) {
+        const uint32_t v = __shfl_sync(0xffffffffu, c.x, i);
+        rank += (v > c.x || (v == c.x && i < lane)) ? 1 : 0;
+      }
+      bool in = lane < n_cand && rank < p.k;
+      if (with_keys && n_cand > p.k) {
+        // candidates within the error of the k-th: unless all of them are one logit with one bias, fp64 decides
+        const uint32_t kth = __shfl_sync(0xffffffffu, c.x, __ffs(__ballot_sync(0xffffffffu, lane < n_cand && rank == p.k - 1)) - 1);
+        const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY, fc = ord_to(c.x);
+        const bool close = lane < n_cand && !(fabsf(fc - fk) > tol);
+        const unsigned band = __ballot_sync(0xffffffffu, close);
+        if (__popc(band) > 1 && __ballot_sync(0xffffffffu, close && !in)) {
+          const float xe = close ? load_logit(row, p.dtype, (int)c.y) : 0.0f, be = close ? p.bias[c.y] : 0.0f;
+          const int first = __ffs(band) - 1;
+          const float rx = __shfl_sync(0xffffffffu, xe, first), rb = __shfl_sync(0xffffffffu, be, first);
+          if (__any_sync(0xffffffffu, close && (xe != rx || be != rb))) {
+            in = in && !close;
+            in |= band_fp64<V, kSoft>(p, row, close ? (int)c.y : -1, p.k - __popc(__ballot_sync(0xffffffffu, in)));
+          }
+        }
+      }
+      e = in ? (int)c.y : -1;
+    } else {
+      // many equal keys, or few lanes that hold many: one maximum after the other
+      uint32_t kth = 0;
+      int n = 0, taken = 0;
+      for (; n < p.k; ++n) {
+        const uint32_t best = __reduce_max_sync(0xffffffffu, a1);
+        kth = best;  // (not 0: there are more than 32 candidates)
+        if (lane == __ffs(__ballot_sync(0xffffffffu, a1 == best)) - 1) {
+          ++taken;
+          int ge = 0;  // the next one of this lane, counting equal keys
+          a1 = 0;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             ge += key[j] >= best ? 1 : 0;
@@ -458,85 +593,93 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
           }
           if (ge > taken) a1 = best;
         }
+        __syncwarp();
       }
-    }
-    // the selected: keys above it, and as many equal ones, lowest ids first, as there is room for
-    uint32_t gt = 0, eq = 0;
+      // the selected: keys above the k-th, and as many equal ones, lowest ids first, as there is room for
+      uint32_t gt = 0, eq = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      gt |= key[j] > kth ? 1u << j : 0u;
-      eq |= key[j] == kth && kth ? 1u << j : 0u;
-    }
-    int room = n - add32(__popc(gt));
-    uint32_t sel = gt | eq;
-    if (add32(__popc(eq)) > room) {
-      int before = __popc(eq);
-      const int mine = before;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
+      for (int j = 0; j < V; ++j) {
+        gt |= key[j] > kth ? 1u << j : 0u;
+        eq |= key[j] == kth ? 1u << j : 0u;
       }
-      room -= before - mine;
-      sel = gt;
-      for (; eq && room > 0; eq &= eq - 1, --room) sel |= eq & -eq;
-    }
-    if (with_keys && n == p.k) {
-      // keys within the error of the k-th: unless all of them are one logit with one bias, they are compared in fp64
-      const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
-      const uint32_t lo = ord_of(fk - tol), hi = ord_of(fk + tol);
       uint32_t band = 0;
+      bool decide = false;
+      if (with_keys) {
+        const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
+        const uint32_t lo = ord_of(fk - tol), hi = ord_of(fk + tol);
+        uint32_t over = 0;
 #pragma unroll
-      for (int j = 0; j < V; ++j) band |= key[j] >= lo && key[j] <= hi ? 1u << j : 0u;
-      if (add32(__popc(band)) > 1) {
+        for (int j = 0; j < V; ++j) {
+          over |= key[j] > hi ? 1u << j : 0u;
+          band |= key[j] >= lo && key[j] <= hi ? 1u << j : 0u;
+        }
         float lx = 0.0f, lb = 0.0f;
         bool some = false, mixed = false;
         for (uint32_t c = band; c; c &= c - 1) {
-          const int e = e0 + __ffs(c) - 1;
-          const float xe = load_logit(row, p.dtype, e), be = p.bias[e];
+          const int ee = e0 + __ffs(c) - 1;
+          const float xe = load_logit(row, p.dtype, ee), be = p.bias[ee];
           mixed |= some && (xe != lx || be != lb);
           lx = xe, lb = be, some = true;
         }
+        __syncwarp();
         const int first = __ffs(__ballot_sync(0xffffffffu, some)) - 1;
         const float rx = __shfl_sync(0xffffffffu, lx, first), rb = __shfl_sync(0xffffffffu, lb, first);
-        if (__any_sync(0xffffffffu, mixed || (some && (lx != rx || lb != rb)))) {
-          sel = 0;
-#pragma unroll
-          for (int j = 0; j < V; ++j) sel |= key[j] > hi ? 1u << j : 0u;
-          sel |= band_fp64<V, kSoft>(p, row, band, p.k - add32(__popc(sel)));
-        }
+        decide = __any_sync(0xffffffffu, mixed || (some && (lx != rx || lb != rb)));
+        if (decide) gt = over, eq = band;
       }
-    }
-
-    // slots in ascending id, one lane each
-    int before = __popc(sel);
-    const int mine = before;
+      const int room = p.k - add32(__popc(gt));
+      uint32_t sel = gt;
+      if (decide) {
+        sel |= wide_band_fp64<V, kSoft>(p, row, eq, room);
+      } else {
+        int b4 = __popc(eq);
+        const int own = b4;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, b4, o);
+          if (lane >= o) b4 += v;
+        }
+        for (int left = room - (b4 - own); eq && left > 0; eq &= eq - 1, --left) sel |= eq & -eq;
+      }
+      __syncwarp();
+      int at = __popc(sel);
+      const int own = at;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      at -= own;
+      for (; sel; sel &= sel - 1) s_c[warp][at++] = make_uint2(0u, (uint32_t)(e0 + __ffs(sel) - 1));
+      __syncwarp();
+      if (lane < p.k) e = (int)s_c[warp][lane].y;
     }
-    before -= mine;
-    for (uint32_t c = sel; c; c &= c - 1) s_e[warp][before++] = e0 + __ffs(c) - 1;
     __syncwarp();
-    const bool on = lane < n;
-    const int e = on ? s_e[warp][lane] : -1;
-    __syncwarp();
+
+    // weights of the selected, one lane each
+    const bool on = e >= 0;
+    const unsigned who = __ballot_sync(0xffffffffu, on);
     const float xs = on ? load_logit(row, p.dtype, e) : -INFINITY;
     float w = 0.0f;
     if (p.renorm) {  // over the selected: a common factor cancels, so scores that underflow are shifted
       const float ms = max32(xs);
       if (on) w = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
-      const float tot = sum16(w);
-      if (on) w = w / tot * p.scale;
+      const float tot = sum32(w);
+      if (on) w = __fdividef(w, tot) * p.scale;
     } else if (on) {
       w = (kSoft ? expf(below(xs, m)) * inv_z : 1.0f / (1.0f + expf(-xs))) * p.scale;
     }
     if (kSoft && nan_row && on) w = NAN;
-    if (lane < p.k) {
-      p.topk_idx[t * p.k + lane] = e;
-      p.topk_w[t * p.k + lane] = w;
-      if (p.counts && on) atomicAdd(&s_hist[e], 1);  // (integers: any order gives the same)
+    if (on) {
+      const int64_t o = t * p.k + __popc(who & ((1u << lane) - 1u));
+      p.topk_idx[o] = e;
+      p.topk_w[o] = w;
+      if (p.counts) atomicAdd(&s_hist[e], 1);  // (integers: any order gives the same)
+    }
+    const int n = __popc(who);
+    if (lane >= n && lane < p.k) {  // fewer than k to select
+      p.topk_idx[t * p.k + lane] = -1;
+      p.topk_w[t * p.k + lane] = 0.0f;
     }
   }
 
@@ -559,20 +702,25 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
   }
 }
 
-// Sums over the CTAs' partials in a fixed order: a CTA per 32 experts, its
-// warps taking every 8th partial, then the warps in turn.
-__global__ void __launch_bounds__(256) route_sums_kernel(const int* pc, const float* pp, int n, int E, int* counts,
-                                                         float* prob_sum) {
-  __shared__ int s_c[8][32];
-  __shared__ float s_f[8][32];
+// Sums over the CTAs' partials in a fixed order: a CTA per 32 experts, its 32
+// warps taking every 32nd partial, then the warps in turn.  Launched while
+// route_kernel still runs (programmatic dependency), it waits for it here.
+__global__ void __launch_bounds__(1024) route_sums_kernel(const int* pc, const float* pp, int n, int E, int* counts,
+                                                          float* prob_sum) {
+  __shared__ int s_c[32][32];
+  __shared__ float s_f[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
   int c = 0;
   float f = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (e < E) {
-#pragma unroll 4
-    for (int i = warp; i < n; i += 8) {
-      if (pc) c += pc[(size_t)i * E + e];
-      if (pp) f += pp[(size_t)i * E + e];
+    if (pc) {
+#pragma unroll 8
+      for (int i = warp; i < n; i += 32) c += pc[(size_t)i * E + e];
+    }
+    if (pp) {
+#pragma unroll 8
+      for (int i = warp; i < n; i += 32) f += pp[(size_t)i * E + e];
     }
   }
   s_c[warp][lane] = c;
@@ -582,7 +730,7 @@ __global__ void __launch_bounds__(256) route_sums_kernel(const int* pc, const fl
     c = 0;
     f = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < 32; ++w) {
       c += s_c[w][lane];
       f += s_f[w][lane];
     }
@@ -868,9 +1016,18 @@ int moe_route(const moe_route_plan* pl, int64_t T, const void* logits, int64_t l
   const cudaError_t err = c.score_fn == MOE_SCORE_SOFTMAX ? launch(std::true_type{}) : launch(std::false_type{});
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   if (split) {
-    route_sums_kernel<<<(unsigned)((c.E + 31) / 32), 256, 0, stream>>>(expert_counts ? pc : nullptr, prob_sum ? pp : nullptr,
-                                                                     (int)grid, p.E, expert_counts, prob_sum);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)((c.E + 31) / 32));
+    lc.blockDim = dim3(1024);
+    lc.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, route_sums_kernel, expert_counts ? (const int*)pc : nullptr,
+                           prob_sum ? (const float*)pp : nullptr, (int)grid, p.E, (int*)expert_counts, prob_sum) != cudaSuccess)
+      return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }

@@ -422,3 +422,23 @@ def test_call_refusals():
     assert code(rg.moe_route_bwd, plan, T, x, idx, None, x.clone()) == bad
     assert code(rg.moe_route_bwd, plan, T, x, idx, w, None) == bad
     assert code(rg.moe_route_bwd, plan, T, x, idx, w, x.clone(), dlogits_stride=E - 1) == bad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_many_equal_or_crowded_keys(fn, with_bias):
+    """More equal (or nearly equal) keys than one lane each can hold: all logits
+    the same; the large ones all in a few neighbouring experts; logits so close
+    that a whole row is within fp32's error."""
+    g = torch.Generator(device="cuda").manual_seed(21)
+    T, E = 64, 512
+    flat = torch.full((T, E), 0.25, device="cuda")
+    crowd = torch.randn(T, E, generator=g, device="cuda") - 20.0
+    crowd[:, 32:80] += 20.0
+    near = 0.5 + torch.randint(0, 3, (T, E), generator=g, device="cuda") * 2.0 ** -23
+    for x in (flat, crowd, near):
+        for bias in ((torch.zeros(E, device="cuda"), torch.randint(0, 3, (E,), generator=g, device="cuda") * 2.0 ** -25)
+                     if with_bias else (None,)):
+            for kw in (dict(), dict(n_group=16, topk_group=2), dict(n_group=2, topk_group=1, group_top=1)):
+                check_route(x, bias, cfg_of(E, 16, fn=fn, **kw))
