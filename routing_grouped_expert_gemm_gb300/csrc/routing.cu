@@ -42,9 +42,10 @@ constexpr float ROUTE_TINY = 1e-36f;    // keys below this have lost their relat
 struct RouteParams {
   const void* logits;
   int64_t ld, T;  // row stride in elements
-  int E, k, dtype, vec, bvec;
+  int E, k, dtype, vec;
   const float* bias;
   int n_group, topk_group, group_top, gs, renorm;
+  int rows, ks;     // rows per warp; log2 of the lanes of a row's slots (k rounded up)
   float scale;
   int* topk_idx;
   float* topk_w;
@@ -116,12 +117,13 @@ __device__ __forceinline__ void load_row(const void* row, int dtype, int vec, in
   for (int i = 0; i < V; ++i) x[i] = e0 + i < E ? load_logit(row, dtype, e0 + i) : -INFINITY;
 }
 
-// Floats in the order of unsigned integers; nothing finite or infinite maps to 0.
+// Floats (no NaN) in the order of unsigned integers.
 __device__ __forceinline__ uint32_t ord_bits(float f) {
   const uint32_t u = __float_as_uint(f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint32_t ord_of(float f) { return ord_bits(f + 0.0f); }  // -0 equals +0
+constexpr uint32_t ORD_NONE = 0x007fffffu;  // -inf: keys up to this are not to be selected
 __device__ __forceinline__ float ord_to(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
@@ -205,7 +207,7 @@ __device__ __forceinline__ double key64(const RouteParams& p, const void* row, i
 // to be decided by the candidates' keys (bits of this lane's experts, which
 // hold the largest of every such group).  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row, uint32_t cand, int state, uint2* buf) {
+__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row, uint32_t cand, int state, int* buf) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
   double m = 0.0, z = 1.0;
   if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
@@ -222,13 +224,13 @@ __device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* r
   before -= mine;
   for (int c0 = 0; c0 < total; c0 += 32) {
     for (uint32_t c = cand, at = (uint32_t)before; c; c &= c - 1, ++at)
-      if ((int)at >= c0 && (int)at < c0 + 32) buf[at - c0].x = (uint32_t)(e0 + __ffs(c) - 1);
+      if ((int)at >= c0 && (int)at < c0 + 32) buf[at - c0] = e0 + __ffs(c) - 1;
     __syncwarp();
     const int n = min(32, total - c0);
     unsigned long long key = 0ull;
     int g = -1;
     if (lane < n) {
-      const int e = (int)buf[lane].x;
+      const int e = buf[lane];
       const double v = key64<kSoft>(p, row, e, m, z);
       key = v > -INFINITY ? ord_of64(v) : 0ull;
       g = e / p.gs;
@@ -310,8 +312,13 @@ template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
   constexpr float REL = 1.0f / 65536;
   __shared__ int s_hist[E_MAX];
-  __shared__ uint2 s_c[ROUTE_WARPS][32];  // candidates: key, expert
+  __shared__ __align__(16) uint32_t s_key[ROUTE_WARPS][32];  // candidates: key and expert
+  __shared__ int s_id[ROUTE_WARPS][32];
+  __shared__ int s_sel[ROUTE_WARPS][32];        // selected experts of up to 32 >> ks rows
+  __shared__ float s_row[ROUTE_WARPS][32][2];   // softmax: the row's maximum and 1 / sum (NaN: the row has one)
   __shared__ float s_p[ROUTE_WARPS][32 * V];
+  __shared__ __align__(16) float s_bias[32 * V];                   // NaN as -inf: never selected
+  __shared__ __align__(16) uint32_t s_keys[ROUTE_WARPS][32 * V];  // the row's keys
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const bool sums = p.prob_sum != nullptr, grouped = p.n_group > 1;
   const bool with_keys = p.bias != nullptr;                             // the order is s + b's, not x's
@@ -320,6 +327,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
   // groups made of whole, aligned sets of lanes are ranked by butterflies
   const int glanes = p.gs / V;
   const bool aligned_groups = grouped && p.gs % V == 0 && (glanes & (glanes - 1)) == 0 && glanes <= 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sums' kernel may take its place and wait
   if (p.counts) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) s_hist[e] = 0;
     __syncthreads();
@@ -336,17 +344,29 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
 #pragma unroll
     for (int j = 0; j < V; ++j) gid[j / 4] |= (uint32_t)min((e0 + j) / p.gs, 31) << (8 * (j % 4));
   }
-  if (with_keys) {
-    float b[V];
-    load_row<V>(p.bias, MOE_DTYPE_FP32, p.bvec, lane, p.E, b);
+  float* bias = s_bias + e0;
+  if (with_keys) {  // every warp writes the same
 #pragma unroll
-    for (int j = 0; j < V; ++j) bmax = fmaxf(bmax, e0 + j < p.E ? fabsf(b[j]) : 0.0f);
+    for (int j = 0; j < V; ++j) {
+      const float v = e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
+      bmax = fmaxf(bmax, fabsf(v) < INFINITY ? fabsf(v) : 0.0f);
+      bias[j] = v == v ? v : -INFINITY;
+    }
+    __syncwarp();
   }
   bmax = max32(bmax);
   const size_t row_bytes = (size_t)p.ld * (p.dtype == MOE_DTYPE_FP32 ? 4 : 2);
 
-  for (int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + warp; t < p.T; t += (int64_t)gridDim.x * ROUTE_WARPS) {
-    const void* row = static_cast<const uint8_t*>(p.logits) + (size_t)t * row_bytes;
+  const uint32_t lt = (1u << lane) - 1u;
+  const int64_t t_from = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * p.rows;
+  const int64_t t_to = min(t_from + p.rows, p.T);
+  for (int64_t tb = t_from; tb < t_to; tb += 32 >> p.ks) {
+  // select for as many rows as have their slots in one warp, then weigh them together
+  const int n_rows = (int)min((int64_t)(32 >> p.ks), t_to - tb);
+  s_sel[warp][lane] = -1;
+  __syncwarp();
+  for (int r = 0; r < n_rows; ++r) {
+    const void* row = static_cast<const uint8_t*>(p.logits) + (size_t)(tb + r) * row_bytes;
     float x[V];
     load_row<V>(row, p.dtype, p.vec, lane, p.E, x);
 
@@ -354,12 +374,13 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
     float s[V];
     float m = 0.0f, z = 1.0f;
     bool nan_row = false;
-    if (kSoft || sums) {
+    auto row_max = [&]() {
       float lm = -INFINITY;
 #pragma unroll
       for (int j = 0; j < V; ++j) lm = fmaxf(lm, x[j]);
-      m = max32(lm);
-    }
+      return max32(lm);
+    };
+    if (kSoft && (scored || !p.renorm)) m = row_max();
     if (scored) {
       if (kSoft) {
         // an infinite maximum is its own limit: those logits share the row
@@ -396,7 +417,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
     }
     const float inv_z = z > 0.0f ? rcp_fast(z) : 0.0f;
     if (sums) {  // normalised scores, s over the row's sum
-      if (!kSoft && m < -20.0f && m > -INFINITY) {  // e^x to fp32 precision: shifted, so that it does not underflow
+      if (!kSoft && z < 1e-6f) m = row_max();  // (larger sums have no score that underflows and counts)
+      if (!kSoft && z < 1e-6f && m < -20.0f && m > -INFINITY) {  // e^x to fp32 precision: shifted against underflow
         float u[V], lz = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -413,19 +435,17 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
       }
     }
 
-    // order of the experts as integers, 0 = not to be selected
+    // order of the experts as integers
     uint32_t key[V];
-    if (with_keys) {  // (the bias stays in L1, not in registers)
-      float b[V];
-      load_row<V>(p.bias, MOE_DTYPE_FP32, p.bvec, lane, p.E, b);
+    if (with_keys) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float f = kSoft ? fmaf(s[j], inv_z, b[j]) : s[j] + b[j];  // (never -0)
-        key[j] = x[j] > -INFINITY && f > -INFINITY ? ord_bits(f) : 0u;
+        const float f = kSoft ? fmaf(s[j], inv_z, bias[j]) : s[j] + bias[j];  // (never -0)
+        key[j] = ord_bits(x[j] > -INFINITY ? f : -INFINITY);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) key[j] = x[j] > -INFINITY ? ord_of(x[j]) : 0u;
+      for (int j = 0; j < V; ++j) key[j] = ord_bits(x[j] > -INFINITY ? x[j] + 0.0f : -INFINITY);
     }
 
     if (grouped) {
@@ -434,12 +454,18 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
       uint32_t g1 = 0, g2 = 0;  // lane g: those of group g
       if (aligned_groups) {
         uint32_t t1 = 0, t2 = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const uint32_t v = by_score ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
+        auto take = [&](uint32_t v) {
           t2 = max(t2, min(t1, v));
           t1 = max(t1, v);
+        };
+        if (by_score) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) take(key[j] > ORD_NONE ? ord_of(s[j]) : 0u);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) take(key[j]);
         }
+#pragma unroll 2
         for (int o = 1; o < glanes; o <<= 1) {
           const uint32_t u1 = __shfl_xor_sync(0xffffffffu, t1, o), u2 = __shfl_xor_sync(0xffffffffu, t2, o);
           t2 = max(max(t2, u2), min(t1, u1));
@@ -455,7 +481,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
           uint32_t t1 = 0, t2 = 0;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            uint32_t v = by_score ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
+            uint32_t v = by_score ? (key[j] > ORD_NONE ? ord_of(s[j]) : 0u) : key[j];
             v = j >= lo && j < hi ? v : 0u;
             t2 = max(t2, min(t1, v));
             t1 = max(t1, v);
@@ -466,26 +492,38 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
           if (lane == g) g1 = w1, g2 = w2;
         }
       }
-      // rank of lane g's group; a group without an expert ranks last
-      uint32_t score = g1;
-      if (group_scores && p.group_top > 1 && g2) score = ord_of(ord_to(g1) + ord_to(g2));
-      int rank = 0;
-      for (int g = 0; g < p.n_group; ++g) {
-        const uint32_t v = __shfl_sync(0xffffffffu, score, g);
-        rank += (v > score || (v == score && g < lane)) ? 1 : 0;
+      // the topk_group largest scores, the lowest group first among equals; a group without an expert has 0
+      uint32_t score = g1 > ORD_NONE ? g1 : 0u;
+      if (group_scores && p.group_top > 1 && g2 > ORD_NONE) score = ord_of(ord_to(g1) + ord_to(g2));
+      s_key[warp][lane] = score;
+      __syncwarp();
+      int rank = 0;  // the number of larger scores
+      for (int g = 0; g < p.n_group; g += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&s_key[warp][g]);
+        rank += v.x > score ? 1 : 0;
+        rank += v.y > score ? 1 : 0;
+        rank += v.z > score ? 1 : 0;
+        rank += v.w > score ? 1 : 0;
       }
-      const bool in = lane < p.n_group && rank < p.topk_group;
+      __syncwarp();
+      bool in = score && rank < p.topk_group;
       unsigned kept = __ballot_sync(0xffffffffu, in);
-      if (group_scores && p.topk_group < p.n_group) {
-        const uint32_t lo = __reduce_min_sync(0xffffffffu, in ? score : 0xffffffffu);
-        const uint32_t hi = __reduce_max_sync(0xffffffffu, in || lane >= p.n_group ? 0u : score);
+      const uint32_t thr = __reduce_min_sync(0xffffffffu, in ? score : 0xffffffffu);
+      const bool tied = __popc(kept) > p.topk_group;
+      if (tied) {  // equal scores across the border: the lowest groups
+        const unsigned over = __ballot_sync(0xffffffffu, in && score > thr), same = kept & ~over;
+        in = in && (score > thr || __popc(same & lt) < p.topk_group - __popc(over));
+        kept = __ballot_sync(0xffffffffu, in);
+      }
+      if (group_scores && kept) {
+        const uint32_t hi = tied ? thr : __reduce_max_sync(0xffffffffu, in ? 0u : score);
         if (hi) {
-          const float fl = ord_to(lo), fh = ord_to(hi), tol = REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY;
+          const float fl = ord_to(thr), fh = ord_to(hi), tol = REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY;
           if (!(fl - fh > tol)) {
             // groups that may lie on either side, and in them the keys that may be among their largest
             const bool band = lane < p.n_group && score && ord_to(score) >= fh - tol && ord_to(score) <= fl + tol;
             uint32_t least = 0xffffffffu;
-            if (band) least = p.group_top > 1 && g2 ? g2 : g1;
+            if (band) least = p.group_top > 1 && g2 > ORD_NONE ? g2 : g1;
             if (band) {
               const float f = ord_to(least);
               least = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
@@ -495,11 +533,11 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
             for (int j = 0; j < V; ++j) {
               const int g = aligned_groups ? (int)gid[0] : (int)((gid[j / 4] >> (8 * (j % 4))) & 31u);
               const uint32_t from = __shfl_sync(0xffffffffu, least, g);
-              const uint32_t v = by_score ? (key[j] ? ord_of(s[j]) : 0u) : key[j];
-              cand |= v && v >= from ? 1u << j : 0u;
+              const uint32_t v = by_score ? ord_of(s[j]) : key[j];
+              cand |= key[j] > ORD_NONE && v >= from ? 1u << j : 0u;
             }
             // (lane g: 2 its group is in, 0 it is out, 1 to be decided)
-            kept = groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, &s_c[warp][0]);
+            kept = groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, s_id[warp]);
           }
         }
       }
@@ -517,21 +555,22 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
 #pragma unroll
     for (int j = 0; j < V; ++j) a1 = max(a1, key[j]);
 
-    // k lanes' maxima at least reach `floor`, so the k-th key does too (0: fewer lanes have keys)
-    uint32_t floor = 0xffffffffu;
+    // k lanes' maxima at least reach `floor`, so the k-th key does too (not above ORD_NONE: fewer lanes have keys)
+    uint32_t floor = 0;
     {
       uint32_t a = a1;
-      for (int i = 0; i < p.k && floor; ++i) {
+#pragma unroll 4
+      for (int i = 0; i < p.k; ++i) {
         floor = __reduce_max_sync(0xffffffffu, a);
         a = a == floor ? 0u : a;
       }
     }
     // candidates: the keys from there up, and those that their error might lift there
-    if (with_keys && floor) {
+    if (with_keys && floor > ORD_NONE) {
       const float f = ord_to(floor);
       floor = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
     }
-    floor = max(floor, 1u);
+    floor = max(floor, ORD_NONE + 1u);
     uint32_t cand = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) cand |= key[j] >= floor ? 1u << j : 0u;
@@ -544,37 +583,49 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
     }
     const int n_cand = __shfl_sync(0xffffffffu, before, 31);
     before -= mine;
-    int e = -1;  // this lane's selected expert; ids ascend with the lanes
-    if (n_cand <= 32) {
+    if (n_cand <= 32) {  // one lane each, ids ascending with the lanes
+      uint32_t* keys = s_keys[warp] + e0;
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if ((cand >> j) & 1u) s_c[warp][before++] = make_uint2(key[j], (uint32_t)(e0 + j));
+      for (int j = 0; j < V; ++j) keys[j] = key[j];
+      for (uint32_t c = cand; c; c &= c - 1) s_id[warp][before++] = e0 + __ffs(c) - 1;
       __syncwarp();
-      uint2 c = make_uint2(0u, 0u);
-      if (lane < n_cand) c = s_c[warp][lane];
-      int rank = 0;
-      for (int i = 0; i < n_cand; ++i) {
-        const uint32_t v = __shfl_sync(0xffffffffu, c.x, i);
-        rank += (v > c.x || (v == c.x && i < lane)) ? 1 : 0;
+      const int e = s_id[warp][lane];
+      const uint32_t c = lane < n_cand ? s_keys[warp][e] : 0u;
+      s_key[warp][lane] = c;
+      __syncwarp();
+      int rank = 0;  // of a key, the number of larger ones; 0 is no key
+      for (int i = 0; i < n_cand; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&s_key[warp][i]);
+        rank += v.x > c ? 1 : 0;
+        rank += v.y > c ? 1 : 0;
+        rank += v.z > c ? 1 : 0;
+        rank += v.w > c ? 1 : 0;
       }
-      bool in = lane < n_cand && rank < p.k;
+      bool in = c && rank < p.k;
+      unsigned who = __ballot_sync(0xffffffffu, in);
+      const uint32_t kth = __reduce_min_sync(0xffffffffu, in ? c : 0xffffffffu);
+      if (__popc(who) > p.k) {  // equal keys across the border: the lowest ids
+        const unsigned over = __ballot_sync(0xffffffffu, in && c > kth), same = who & ~over;
+        in = in && (c > kth || __popc(same & lt) < p.k - __popc(over));
+        who = __ballot_sync(0xffffffffu, in);
+      }
       if (with_keys && n_cand > p.k) {
         // candidates within the error of the k-th: unless all of them are one logit with one bias, fp64 decides
-        const uint32_t kth = __shfl_sync(0xffffffffu, c.x, __ffs(__ballot_sync(0xffffffffu, lane < n_cand && rank == p.k - 1)) - 1);
-        const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY, fc = ord_to(c.x);
-        const bool close = lane < n_cand && !(fabsf(fc - fk) > tol);
+        const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
+        const bool close = c && !(fabsf(ord_to(c) - fk) > tol);
         const unsigned band = __ballot_sync(0xffffffffu, close);
-        if (__popc(band) > 1 && __ballot_sync(0xffffffffu, close && !in)) {
-          const float xe = close ? load_logit(row, p.dtype, (int)c.y) : 0.0f, be = close ? p.bias[c.y] : 0.0f;
+        if (band & ~who) {
+          const float xe = close ? load_logit(row, p.dtype, e) : 0.0f, be = close ? p.bias[e] : 0.0f;
           const int first = __ffs(band) - 1;
           const float rx = __shfl_sync(0xffffffffu, xe, first), rb = __shfl_sync(0xffffffffu, be, first);
           if (__any_sync(0xffffffffu, close && (xe != rx || be != rb))) {
             in = in && !close;
-            in |= band_fp64<V, kSoft>(p, row, close ? (int)c.y : -1, p.k - __popc(__ballot_sync(0xffffffffu, in)));
+            in |= band_fp64<V, kSoft>(p, row, close ? e : -1, p.k - __popc(__ballot_sync(0xffffffffu, in)));
+            who = __ballot_sync(0xffffffffu, in);
           }
         }
       }
-      e = in ? (int)c.y : -1;
+      if (in) s_sel[warp][(r << p.ks) + __popc(who & lt)] = e;
     } else {
       // many equal keys, or few lanes that hold many: one maximum after the other
       uint32_t kth = 0;
@@ -650,37 +701,40 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
         if (lane >= o) at += v;
       }
       at -= own;
-      for (; sel; sel &= sel - 1) s_c[warp][at++] = make_uint2(0u, (uint32_t)(e0 + __ffs(sel) - 1));
-      __syncwarp();
-      if (lane < p.k) e = (int)s_c[warp][lane].y;
+      for (; sel; sel &= sel - 1) s_sel[warp][(r << p.ks) + at++] = e0 + __ffs(sel) - 1;
+    }
+    if (kSoft && lane == 0) {
+      s_row[warp][r][0] = m;
+      s_row[warp][r][1] = nan_row ? NAN : inv_z;
     }
     __syncwarp();
+  }
 
-    // weights of the selected, one lane each
-    const bool on = e >= 0;
-    const unsigned who = __ballot_sync(0xffffffffu, on);
-    const float xs = on ? load_logit(row, p.dtype, e) : -INFINITY;
-    float w = 0.0f;
-    if (p.renorm) {  // over the selected: a common factor cancels, so scores that underflow are shifted
-      const float ms = max32(xs);
-      if (on) w = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
-      const float tot = sum32(w);
-      if (on) w = __fdividef(w, tot) * p.scale;
-    } else if (on) {
-      w = (kSoft ? expf(below(xs, m)) * inv_z : 1.0f / (1.0f + expf(-xs))) * p.scale;
-    }
-    if (kSoft && nan_row && on) w = NAN;
-    if (on) {
-      const int64_t o = t * p.k + __popc(who & ((1u << lane) - 1u));
-      p.topk_idx[o] = e;
-      p.topk_w[o] = w;
-      if (p.counts) atomicAdd(&s_hist[e], 1);  // (integers: any order gives the same)
-    }
-    const int n = __popc(who);
-    if (lane >= n && lane < p.k) {  // fewer than k to select
-      p.topk_idx[t * p.k + lane] = -1;
-      p.topk_w[t * p.k + lane] = 0.0f;
-    }
+  // weights, one lane per slot of the rows
+  const int r = lane >> p.ks, slot = lane & ((1 << p.ks) - 1);
+  const int64_t t = tb + r;
+  const int e = r < n_rows ? s_sel[warp][lane] : -1;
+  const bool on = e >= 0;
+  const float xs = on ? load_logit(static_cast<const uint8_t*>(p.logits) + (size_t)t * row_bytes, p.dtype, e) : -INFINITY;
+  const float nan = kSoft && on ? s_row[warp][r][1] : 0.0f;
+  float w = 0.0f;
+  if (p.renorm) {  // over the selected: a common factor cancels, so scores that underflow are shifted
+    float ms = xs;
+    for (int o = 1 << p.ks >> 1; o > 0; o >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o));
+    if (on) w = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
+    float tot = w;
+    for (int o = 1 << p.ks >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    if (on) w = __fdividef(w, tot) * p.scale;
+  } else if (on) {
+    w = (kSoft ? expf(below(xs, s_row[warp][r][0])) * nan : 1.0f / (1.0f + expf(-xs))) * p.scale;
+  }
+  if (nan != nan) w = nan;
+  if (r < n_rows && slot < p.k) {
+    p.topk_idx[t * p.k + slot] = e;
+    p.topk_w[t * p.k + slot] = w;
+    if (p.counts && on) atomicAdd(&s_hist[e], 1);  // (integers: any order gives the same)
+  }
+  __syncwarp();
   }
 
   if (p.counts || sums) {
@@ -776,7 +830,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __gri
   __syncwarp();
   for (int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + warp; t < p.T; t += (int64_t)gridDim.x * ROUTE_WARPS) {
     const void* row = static_cast<const uint8_t*>(p.logits) + (size_t)t * p.ld * size;
-    float x[V], s[V];
+    float x[V], s[V], c1[V];  // c1: 1 - s
     int e = -1;
     float dw = 0.0f, xs = -INFINITY;
     if (lane < p.k) {
@@ -798,8 +852,10 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __gri
       shifted = kSoft || (m < -20.0f && m > -INFINITY);  // sigmoid = e^x there: its share without underflow
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        s[j] = 0.0f;
-        if (!(x[j] == -INFINITY)) s[j] = shifted ? expf(below(x[j], m)) : 1.0f / (1.0f + expf(-x[j]));
+        const float y = exp2_fast(-fabsf(x[j]) * LOG2E), r = rcp_fast(1.0f + y);  // e^-|x|: both s and 1 - s keep their bits
+        if (!kSoft) c1[j] = x[j] >= 0.0f ? y * r : r;
+        s[j] = shifted ? (x[j] == m ? 1.0f : exp2_fast((x[j] - m) * LOG2E)) : x[j] >= 0.0f ? r : y * r;
+        if (x[j] == -INFINITY) s[j] = 0.0f;
         lz += s[j];
       }
       z = sum32(lz);
@@ -838,7 +894,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __gri
         const float pe = s[j] * inv_z;
         o[j] -= kSoft ? pe * asum : 0.0f;
         if (sums) o[j] += pe * (d[j] - ld);
-        if (!kSoft) o[j] *= 1.0f / (1.0f + expf(x[j]));  // 1 - s
+        if (!kSoft) o[j] *= c1[j];
         if (x[j] == -INFINITY) o[j] = 0.0f;
       }
     }
@@ -994,12 +1050,13 @@ int moe_route(const moe_route_plan* pl, int64_t T, const void* logits, int64_t l
   p.dtype = c.logits_dtype;
   p.vec = route_aligned(logits, 16) && logits_stride * (int64_t)dtype_size(c.logits_dtype) % 16 == 0;
   p.bias = bias;
-  p.bvec = route_aligned(bias, 16);
   p.n_group = (int)c.n_group;
   p.topk_group = (int)c.topk_group;
   p.group_top = c.group_top;
   p.gs = (int)(c.E / c.n_group);
   p.renorm = c.renormalize;
+  p.rows = (int)((T + grid * ROUTE_WARPS - 1) / (grid * ROUTE_WARPS));
+  while ((1 << p.ks) < p.k) ++p.ks;
   p.scale = c.scale;
   p.topk_idx = topk_idx;
   p.topk_w = topk_w;
