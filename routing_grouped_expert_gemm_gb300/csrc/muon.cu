@@ -32,6 +32,7 @@
 
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "common.cuh"
@@ -297,6 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   cluster_sync_all();  // the other CTA's barriers exist before anything targets them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs are the last launch's results
 
   if (warp == 0) {
     if (lane == 0) {
@@ -470,164 +472,536 @@ struct PrepParams {
   int64_t ld;              // of the first iterate
   float mu;
   float* momentum;         // or NULL
-  double* part;            // [nb, NS_PREP_BLOCKS, 3]
+  float* part;             // [nb, NS_PREP_BLOCKS, 4]
   float* rho;              // [nb]
   __half* hi;
   __half* lo;
   int* status;             // cleared by the call's first launch (NULL in the others)
 };
 
-__device__ __forceinline__ float load_grad(const void* g, int dtype, size_t i) {
-  if (dtype == MOE_DTYPE_FP32) return static_cast<const float*>(g)[i];
-  if (dtype == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const bf16*>(g)[i]);
-  return __half2float(static_cast<const __half*>(g)[i]);
-}
-// The V values U (V = 4: 16 or 8 bytes of the gradient at once) at row r,
-// columns c .. c + V - 1; `advance` takes the momentum one step first.
+// V consecutive values of the gradient (V = 8: 16-byte loads) or of fp32 memory
 template <int V>
-__device__ __forceinline__ void load_u(const PrepParams& p, int mat, int r, int c, bool advance, float (&u)[V]) {
-  const size_t gi = (size_t)mat * p.gms + (size_t)r * p.grs + c;
-  if constexpr (V == 4) {
-    if (p.dtype == MOE_DTYPE_FP32) {
-      const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.grad) + gi);
-      u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.grad) + gi);
-      const uint16_t h[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        u[j] = p.dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)h[j] << 16) : __half2float(__ushort_as_half(h[j]));
-    }
+__device__ __forceinline__ void load_f32(const float* s, float (&v)[V]) {
+  if constexpr (V == 8) {
+    const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    u[0] = load_grad(p.grad, p.dtype, gi);
+    v[0] = *s;
   }
-  if (!p.momentum) return;
-  float* mp = p.momentum + ((size_t)mat * p.R + r) * p.C + c;
-  float m[V];
-  if constexpr (V == 4) {
-    const float4 w = *reinterpret_cast<const float4*>(mp);
-    m[0] = w.x, m[1] = w.y, m[2] = w.z, m[3] = w.w;
+}
+template <int V>
+__device__ __forceinline__ void load_grad(const void* g, int dtype, size_t i, float (&v)[V]) {
+  if (dtype == MOE_DTYPE_FP32) {
+    load_f32<V>(static_cast<const float*>(g) + i, v);
+    return;
+  }
+  const uint16_t* s = static_cast<const uint16_t*>(g) + i;
+  uint32_t w[(V + 1) / 2];
+  if constexpr (V == 8) {
+    const uint4 q = *reinterpret_cast<const uint4*>(s);
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
   } else {
-    m[0] = *mp;
+    w[0] = *s;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if (advance) m[j] = p.mu * m[j] + u[j];
-    u[j] = p.nesterov ? u[j] + p.mu * m[j] : m[j];
-  }
-  if (advance) {
-    if constexpr (V == 4) *reinterpret_cast<float4*>(mp) = make_float4(m[0], m[1], m[2], m[3]);
-    else *mp = m[0];
+    const uint16_t h = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+    v[j] = dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
   }
 }
+constexpr int NS_PREP_U = 2;  // vectors of a thread in flight (4 were no faster: 1 to 4% slower on large stacks)
 
-// Advance the momentum and sum U's squares: fp32 runs of at most a few hundred
-// per thread, fp64 across threads.  Values far from 1 are summed in scaled
-// form in sums of their own, so that no finite matrix has an infinite norm and
-// none that is not zero has a zero one.
-template <int V>
-__global__ void __launch_bounds__(256) ns_prep_norm(const PrepParams p) {
-  __shared__ double s[3][8];
-  const int mat = blockIdx.y, cv = p.C / V;
-  const int n = p.R * cv;
-  if (p.status && blockIdx.x == 0 && mat == 0 && threadIdx.x == 0) p.status[0] = 0;
-  double tot[3] = {0.0, 0.0, 0.0};
-  float f[3] = {0.0f, 0.0f, 0.0f};
-  int run = 0;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int r = (int)i / cv, c = ((int)i - r * cv) * V;
-    float u[V];
-    load_u<V>(p, mat, r, c, true, u);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float a = fabsf(u[j]);
-      const bool big = a >= 0x1p50f, small = a < 0x1p-50f;
-      const float v = u[j] * (big ? 0x1p-80f : small ? 0x1p100f : 1.0f);
-      f[0] += small ? v * v : 0.0f;
-      f[1] += big || small ? 0.0f : v * v;
-      f[2] += big ? v * v : 0.0f;
-    }
-    if (++run == 64) {
-#pragma unroll
-      for (int q = 0; q < 3; ++q) tot[q] += (double)f[q], f[q] = 0.0f;
-      run = 0;
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    tot[q] += (double)f[q];
-    for (int o = 16; o > 0; o >>= 1) tot[q] += __shfl_xor_sync(0xffffffffu, tot[q], o);
-    if ((threadIdx.x & 31) == 0) s[q][threadIdx.x >> 5] = tot[q];
-  }
-  __syncthreads();
-  if (threadIdx.x < 3) {
-    double v = 0.0;
-    for (int w = 0; w < 8; ++w) v += s[threadIdx.x][w];
-    p.part[((size_t)mat * NS_PREP_BLOCKS + blockIdx.x) * 3 + threadIdx.x] = v;
-  }
+// Sums of squares in three sums of their own: values far from 1 are squared
+// in scaled form, so that no finite matrix has an infinite norm and none that
+// is not zero has a zero one.
+__device__ __forceinline__ void add_square(float (&f)[3], float u) {
+  const float a = fabsf(u);
+  const bool big = a >= 0x1p50f, small = a < 0x1p-50f;
+  const float v = u * (big ? 0x1p-80f : small ? 0x1p100f : 1.0f);
+  f[0] += small ? v * v : 0.0f;
+  f[1] += big || small ? 0.0f : v * v;
+  f[2] += big ? v * v : 0.0f;
 }
-
-// X_0 = U 2^k as hi + lo, |U 2^k|_F in [2^14, 2^15); rho = 1 / |U 2^k|_F (0 for
-// a matrix of zeros, NaN where the norm is not finite, which makes every
-// element of that matrix's result NaN).
-template <int V>
-__global__ void __launch_bounds__(256) ns_prep_first(const PrepParams p) {
-  __shared__ double s[3][8];
-  __shared__ float s_f[2];
-  const int mat = blockIdx.y, cv = p.C / V;
-  const int n = p.R * cv;
+// The three sums over the block (256 threads), valid in thread 0, in a fixed order.
+__device__ __forceinline__ void block_sum3(float (&f)[3], float (*s)[8]) {
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    double v = (int)threadIdx.x < p.nblk ? p.part[((size_t)mat * NS_PREP_BLOCKS + threadIdx.x) * 3 + q] : 0.0;
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) s[q][threadIdx.x >> 5] = v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) f[q] += __shfl_xor_sync(0xffffffffu, f[q], o);
+    if ((threadIdx.x & 31) == 0) s[q][threadIdx.x >> 5] = f[q];
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    double v[3];
-    for (int q = 0; q < 3; ++q) {
-      v[q] = 0.0;
-      for (int w = 0; w < 8; ++w) v[q] += s[q][w];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) f[q] = ((s[q][0] + s[q][1]) + (s[q][2] + s[q][3])) + ((s[q][4] + s[q][5]) + (s[q][6] + s[q][7]));
+  }
+}
+// U 2^k = (u f1) f2 has a norm in [2^14, 2^15); rho = 1 / that norm (0 for a
+// matrix of zeros, NaN where the norm is not finite, which makes every element
+// of that matrix's result NaN).
+__device__ __forceinline__ void norm_scale(const float (&f)[3], float* f1, float* f2, float* rho) {
+  const double norm = sqrt((double)f[0] * 0x1p-200 + (double)f[1] + (double)f[2] * 0x1p160);
+  *f1 = *f2 = *rho = 0.0f;
+  if (!(norm < (double)INFINITY)) {
+    *rho = NAN;
+  } else if (norm > 0.0) {
+    int e;
+    const double m = frexp(norm, &e);  // norm = m 2^e, m in [0.5, 1)
+    const int k = 15 - e;
+    *f1 = ldexpf(1.0f, k / 2);
+    *f2 = ldexpf(1.0f, k - k / 2);
+    *rho = (float)(0x1p-15 / m);
+  }
+}
+
+// Advance the momentum and sum U's squares.
+template <int V>
+__global__ void __launch_bounds__(256) ns_prep_norm(const PrepParams p) {
+  __shared__ float s[3][8];
+  const int mat = blockIdx.y, cv = p.C / V, n = p.R * cv;
+  const bool flat = p.grs == p.C;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.status && blockIdx.x == 0 && mat == 0 && threadIdx.x == 0) p.status[0] = 0;
+  float* mom = p.momentum ? p.momentum + (size_t)mat * p.R * p.C : nullptr;
+  float f[3] = {0.0f, 0.0f, 0.0f};
+  for (int64_t i0 = (int64_t)blockIdx.x * (256 * NS_PREP_U) + threadIdx.x; i0 < n; i0 += (int64_t)gridDim.x * (256 * NS_PREP_U)) {
+    float u[NS_PREP_U][V], m[NS_PREP_U][V];
+#pragma unroll
+    for (int q = 0; q < NS_PREP_U; ++q) {
+      const int64_t i = i0 + 256 * q;
+      if (i < n) {
+        const size_t o = flat ? (size_t)i * V : (size_t)((int)i / cv) * p.grs + (size_t)((int)i % cv) * V;
+        load_grad<V>(p.grad, p.dtype, (size_t)mat * p.gms + o, u[q]);
+        if (mom) load_f32<V>(mom + (size_t)i * V, m[q]);
+      }
     }
-    const double norm = sqrt(v[0] * 0x1p-200 + v[1] + v[2] * 0x1p160);
-    float f1 = 0.0f, f2 = 0.0f, rho = 0.0f;
-    if (!(norm < (double)INFINITY)) {
-      rho = NAN;
-    } else if (norm > 0.0) {
-      int e;
-      frexp(norm, &e);  // norm = [0.5, 1) 2^e
-      const int k = 15 - e;
-      f1 = ldexpf(1.0f, k / 2);
-      f2 = ldexpf(1.0f, k - k / 2);
-      rho = (float)(1.0 / ldexp(norm, k));
+#pragma unroll
+    for (int q = 0; q < NS_PREP_U; ++q) {
+      const int64_t i = i0 + 256 * q;
+      if (i >= n) break;
+      if (mom) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          m[q][j] = p.mu * m[q][j] + u[q][j];
+          u[q][j] = p.nesterov ? u[q][j] + p.mu * m[q][j] : m[q][j];
+        }
+        float* d = mom + (size_t)i * V;
+        if constexpr (V == 8) {
+          reinterpret_cast<float4*>(d)[0] = make_float4(m[q][0], m[q][1], m[q][2], m[q][3]);
+          reinterpret_cast<float4*>(d)[1] = make_float4(m[q][4], m[q][5], m[q][6], m[q][7]);
+        } else {
+          d[0] = m[q][0];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) add_square(f, u[q][j]);
     }
-    s_f[0] = f1;
-    s_f[1] = f2;
+  }
+  block_sum3(f, s);
+  if (threadIdx.x == 0)
+    *reinterpret_cast<float4*>(p.part + ((size_t)mat * NS_PREP_BLOCKS + blockIdx.x) * 4) = make_float4(f[0], f[1], f[2], 0.0f);
+}
+
+// X_0 = U 2^k as hi + lo.
+template <int V>
+__global__ void __launch_bounds__(256) ns_prep_first(const PrepParams p) {
+  __shared__ float s[3][8];
+  __shared__ float s_f[2];
+  const int mat = blockIdx.y, cv = p.C / V, n = p.R * cv;
+  const bool flat = p.grs == p.C;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float f[3] = {0.0f, 0.0f, 0.0f};
+  if ((int)threadIdx.x < p.nblk) {
+    const float4 w = *reinterpret_cast<const float4*>(p.part + ((size_t)mat * NS_PREP_BLOCKS + threadIdx.x) * 4);
+    f[0] = w.x, f[1] = w.y, f[2] = w.z;
+  }
+  block_sum3(f, s);
+  if (threadIdx.x == 0) {
+    float rho;
+    norm_scale(f, &s_f[0], &s_f[1], &rho);
     if (blockIdx.x == 0) p.rho[mat] = rho;
   }
   __syncthreads();
   const float f1 = s_f[0], f2 = s_f[1];
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int r = (int)i / cv, c = ((int)i - r * cv) * V;
-    float u[V];
-    load_u<V>(p, mat, r, c, false, u);
-    __half h[V], l[V];
+  const float* mom = p.momentum ? p.momentum + (size_t)mat * p.R * p.C : nullptr;
+  for (int64_t i0 = (int64_t)blockIdx.x * (256 * NS_PREP_U) + threadIdx.x; i0 < n; i0 += (int64_t)gridDim.x * (256 * NS_PREP_U)) {
+    float u[NS_PREP_U][V], m[NS_PREP_U][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float x = u[j] * f1 * f2;
-      h[j] = __float2half_rn(x);
-      l[j] = __float2half_rn(x - __half2float(h[j]));
+    for (int q = 0; q < NS_PREP_U; ++q) {
+      const int64_t i = i0 + 256 * q;
+      if (i < n) {
+        const size_t o = flat ? (size_t)i * V : (size_t)((int)i / cv) * p.grs + (size_t)((int)i % cv) * V;
+        if (!mom || p.nesterov) load_grad<V>(p.grad, p.dtype, (size_t)mat * p.gms + o, u[q]);
+        if (mom) load_f32<V>(mom + (size_t)i * V, m[q]);
+      }
     }
-    const size_t o = ((size_t)mat * p.R + r) * p.ld + c;
-    if constexpr (V == 4) {
-      *reinterpret_cast<uint2*>(p.hi + o) = make_uint2((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
-                                                       (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16));
-      *reinterpret_cast<uint2*>(p.lo + o) = make_uint2((uint32_t)__half_as_ushort(l[0]) | ((uint32_t)__half_as_ushort(l[1]) << 16),
-                                                       (uint32_t)__half_as_ushort(l[2]) | ((uint32_t)__half_as_ushort(l[3]) << 16));
+#pragma unroll
+    for (int q = 0; q < NS_PREP_U; ++q) {
+      const int64_t i = i0 + 256 * q;
+      if (i >= n) break;
+      __half h[8], l[8];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float x = (mom ? p.nesterov ? u[q][j] + p.mu * m[q][j] : m[q][j] : u[q][j]) * f1 * f2;
+        h[j] = __float2half_rn(x);
+        l[j] = __float2half_rn(x - __half2float(h[j]));
+      }
+      if constexpr (V == 8) {  // (rows of multiples of 8 are not padded)
+        const size_t o = (size_t)mat * p.R * p.C + (size_t)i * V;
+        *reinterpret_cast<uint4*>(p.hi + o) = pack8(h);
+        *reinterpret_cast<uint4*>(p.lo + o) = pack8(l);
+      } else {
+        const size_t o = ((size_t)mat * p.R + (int)i / cv) * p.ld + (int)i % cv;
+        p.hi[o] = h[0];
+        p.lo[o] = l[0];
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ small matrices: one launch
+// min(rows, cols) <= 128: a cluster of CTAs keeps one matrix on chip from the
+// gradient to the update.  Held as m x n with m the smaller side (so a tall
+// matrix transposed), CTA r has columns r W .. r W + W - 1: x in registers
+// (fp32, one row of 4 W / 16 columns per thread), its hi part in shared memory
+// as the operand of both products -- K-major for X X^T, and, the same bytes,
+// MN-major for B X.  The parts of A = X X^T are summed over the cluster through
+// distributed shared memory, each CTA reducing 1 / cluster of the matrix and
+// writing the sums to all; everything else is local.  (As launches of their
+// own, 3 a step, such stacks take 11 us a launch whatever their size.)
+constexpr int SM_THREADS = 512;
+constexpr int SM_BLK = 16384;                       // 128 rows x 64 fp16, swizzled
+constexpr int SM_PITCH = 132;                       // floats per row of a CTA's part of A
+constexpr int SM_BYTES = 4 * SM_BLK + 2 * SM_BLK + 128 * SM_PITCH * 4 + 4096 + 1024;  // X, A or B, part; one CTA per SM
+
+struct SmallParams {
+  PrepParams in;
+  bf16* out;
+  int steps, tall, m, n, mp;  // mp: m rounded up to 16
+  float a, b, c, scale;
+  int* status;
+  long long timeout_ns;
+};
+
+__device__ __forceinline__ uint32_t sw_at(int r, int c) {  // byte of element (r, c) in 64-column blocks
+  return (uint32_t)((c >> 6) * SM_BLK + r * 128 + ((((c & 63) >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+}
+__device__ __forceinline__ uint64_t sdesc_mn_blocks(uint32_t smem_addr) {  // MN-major, 64-wide blocks SM_BLK apart
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(SM_BLK >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+// 32 lanes x 16 consecutive 32-bit columns (lane base in taddr)
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_cluster_u4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// WC: columns per thread (W = 4 WC)
+template <int WC>
+__global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant__ SmallParams p) {
+  constexpr int W = 4 * WC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* xs = smem;                                                   // hi of X: W / 64 blocks
+  uint8_t* ab = smem + 4 * SM_BLK;                                      // A, then B, without diagonals
+  float* part = reinterpret_cast<float*>(ab + 2 * SM_BLK);              // [128, SM_PITCH]
+  float* s_da = part + 128 * SM_PITCH;                                  // [128] A's diagonal times NS_S
+  float* s_db = s_da + 128;                                             // [128] B's diagonal
+  float* s_sum = s_db + 128;                                            // [16][4] sums of squares by CTA
+  float(*s_red)[16] = reinterpret_cast<float(*)[16]>(s_sum + 64);       // [3][16]
+  float* s_f = s_sum + 64 + 48;                                         // f1, f2, rho
+  uint64_t* bar = reinterpret_cast<uint64_t*>(s_f + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t cs, rank;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+  rank = cluster_ctarank();
+  const int mat = blockIdx.x / cs;
+  const int i = (warp & 3) * 32 + lane;      // row of the m x n matrix
+  const int j0 = (warp >> 2) * WC;           // first column in the slab
+  const int g0 = (int)rank * W + j0;         // ... and in the matrix
+  const bool tall = p.tall != 0;
+  uint32_t phase = 0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar, 1);
+    fence_barrier_init();
+    if (blockIdx.x == 0) p.status[0] = 0;
+  }
+  if (warp == 0) {
+    tmem_alloc<512>(tmem_slot);
+    tmem_relinquish();
+  }
+  // gradient and momentum -> U, in registers
+  float x[WC];
+  float f[3] = {0.0f, 0.0f, 0.0f};
+  {
+    const PrepParams& in = p.in;
+    float* mom = in.momentum ? in.momentum + (size_t)mat * in.R * in.C : nullptr;
+    const size_t gs = tall ? (size_t)in.grs : 1, ms = tall ? (size_t)in.C : 1;
+    const size_t gi = (size_t)mat * in.gms + (tall ? (size_t)g0 * in.grs + i : (size_t)i * in.grs + g0);
+    const size_t mi = tall ? (size_t)g0 * in.C + i : (size_t)i * in.C + g0;
+#pragma unroll
+    for (int c = 0; c < WC; c += 8) {
+      float u[8], m[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool on = i < p.m && g0 + c + j < p.n;
+        u[j] = m[j] = 0.0f;
+        if (on) {
+          float v[1];
+          load_grad<1>(in.grad, in.dtype, gi + (size_t)(c + j) * gs, v);
+          u[j] = v[0];
+          if (mom) m[j] = mom[mi + (size_t)(c + j) * ms];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (mom) {
+          m[j] = in.mu * m[j] + u[j];
+          if (i < p.m && g0 + c + j < p.n) mom[mi + (size_t)(c + j) * ms] = m[j];
+          u[j] = in.nesterov ? u[j] + in.mu * m[j] : m[j];
+        }
+        add_square(f, u[j]);
+        x[c + j] = u[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) f[q] += __shfl_xor_sync(0xffffffffu, f[q], o);
+    if (lane == 0) s_red[q][warp] = f[q];
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // every CTA runs: its shared memory may be written
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x < 3 * cs) {  // this CTA's sums, to every CTA
+    const uint32_t q = threadIdx.x % 3, to = threadIdx.x / 3;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v += s_red[q][w];
+    st_shared_cluster_u32(mapa_shared(s_sum + rank * 4 + q, to), __float_as_uint(v));
+  }
+  cluster_sync_all();
+  if (threadIdx.x == 0) {
+    float v[3] = {0.0f, 0.0f, 0.0f};
+    for (uint32_t r = 0; r < cs; ++r)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) v[q] += s_sum[r * 4 + q];
+    norm_scale(v, &s_f[0], &s_f[1], &s_f[2]);
+  }
+  __syncthreads();
+  const float f1 = s_f[0], f2 = s_f[1], rho = s_f[2];
+  auto put_hi = [&]() {  // X's hi part as operand
+#pragma unroll
+    for (int c = 0; c < WC; c += 8) {
+      __half h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(x[c + j]);
+      *reinterpret_cast<uint4*>(xs + sw_at(i, j0 + c)) = pack8(h);
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < WC; ++c) x[c] = x[c] * f1 * f2;
+  put_hi();
+
+  const uint32_t xa = smem_u32(xs), aa = smem_u32(ab);
+  const uint32_t row_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const int c32 = (warp >> 2) * 32;  // this thread's columns of A and B: c32 .. c32 + 31
+  // what all threads wrote is the tensor core's to read; then the products, then everyone
+  auto products = [&](auto issue) {
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      tc_fence_after();
+      fence_proxy_async_all();
+      issue();
+      mma_commit(bar);
+    }
+    __syncwarp();
+    // (on a time limit the status says so and the barriers below go on; the
+    // status word is not read here: another CTA may not have cleared it yet)
+    if (!mbar_wait_drain(bar, phase, p.timeout_ns)) raise_status(p.status, STATUS_TIMEOUT);
+    phase ^= 1u;
+    __syncwarp();
+    tc_fence_after();
+  };
+  constexpr uint32_t ID = (1u << 4) | (8u << 24);  // fp16 x fp16 -> fp32, M = 128
+  for (int s = 0; s < p.steps; ++s) {
+    const bool first = s == 0, last = s == p.steps - 1;
+    // A = X X^T: this CTA's columns' part
+    products([&]() {
+      for (int k = 0; k < W; k += 16) {
+        const uint64_t d = sdesc_kmajor_sw128(xa + (uint32_t)((k >> 6) * SM_BLK + (k & 63) * 2));
+        mma_bf16_ss(tmem, d, d, ID | ((uint32_t)(p.mp >> 3) << 17), k != 0 ? 1u : 0u);
+      }
+    });
+    const float fa = first ? rho * rho * NS_S : 1.0f / NS_S;
+    // one row of 8 columns of A: the diagonal apart, the rest as operand, in CTA `to` (-1: here)
+    auto put_a = [&](int r, int c, float (&v)[8], int to) {
+      __half h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] *= fa;
+        h[j] = __float2half_rn(c + j == r ? 0.0f : v[j]);
+      }
+      const uint4 w = pack8(h);
+      float d = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d = c + j == r ? v[j] : d;
+      const bool on_diag = r >= c && r < c + 8;
+      if (to < 0) {
+        *reinterpret_cast<uint4*>(ab + sw_at(r, c)) = w;
+        if (on_diag) s_da[r] = d;
+      } else {
+        for (uint32_t q = 0; q < cs; ++q) {
+          st_cluster_u4(mapa_shared(ab + sw_at(r, c), q), w);
+          if (on_diag) st_shared_cluster_u32(mapa_shared(s_da + r, q), __float_as_uint(d));
+        }
+      }
+    };
+    if (c32 < p.mp) {
+      uint32_t acc[32];
+      tmem_ld_32x32b_x32(row_tmem + (uint32_t)c32, acc);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        if (c32 + c >= p.mp) break;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[c + j]);
+        if (cs == 1) {
+          put_a(i, c32 + c, v, -1);
+        } else if (i < p.mp) {
+          float4* d = reinterpret_cast<float4*>(part + i * SM_PITCH + c32 + c);
+          d[0] = make_float4(v[0], v[1], v[2], v[3]);
+          d[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
+    }
+    if (cs > 1) {
+      __syncwarp();
+      cluster_sync_all();
+      const int per_row = p.mp / 8, units = p.mp * per_row;
+      for (int u = (int)rank + (int)cs * (int)threadIdx.x; u < units; u += (int)cs * SM_THREADS) {
+        const int r = u / per_row, c = (u - r * per_row) * 8;
+        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        for (uint32_t q = 0; q < cs; ++q) {  // in the CTAs' order, whoever sums
+          const uint32_t at = mapa_shared(part + r * SM_PITCH + c, q);
+          const float4 w0 = ld_cluster_f4(at), w1 = ld_cluster_f4(at + 16);
+          v[0] += w0.x, v[1] += w0.y, v[2] += w0.z, v[3] += w0.w;
+          v[4] += w1.x, v[5] += w1.y, v[6] += w1.z, v[7] += w1.w;
+        }
+        put_a(r, c, v, 0);
+      }
+      fence_proxy_async_all();
+      __syncwarp();
+      cluster_sync_all();
+    }
+    // B = b A + c A^2, with A = D + O: A^2 = O^2 + D O + O D + D^2
+    products([&]() {
+      for (int k = 0; k < p.mp; k += 16) {
+        const uint64_t d = sdesc_kmajor_sw128(aa + (uint32_t)((k >> 6) * SM_BLK + (k & 63) * 2));
+        mma_bf16_ss(tmem + 128u, d, d, ID | ((uint32_t)(p.mp >> 3) << 17), k != 0 ? 1u : 0u);
+      }
+    });
+    if (c32 < p.mp) {
+      uint32_t acc[32];
+      tmem_ld_32x32b_x32(row_tmem + 128u + (uint32_t)c32, acc);
+      tmem_ld_wait();
+      const float di = s_da[i], cb = p.c / NS_S;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        if (c32 + c >= p.mp || i >= p.mp) break;
+        uint4* at = reinterpret_cast<uint4*>(ab + sw_at(i, c32 + c));
+        float o[8];
+        unpack8(*at, o);
+        __half h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int cc = c32 + c + j;
+          const float v = __uint_as_float(acc[c + j]);
+          if (cc == i) {
+            s_db[i] = (p.b * di + cb * (v + di * di)) / NS_S;
+            h[j] = __float2half_rn(0.0f);
+          } else {
+            h[j] = __float2half_rn(p.b * o[j] + cb * (v + (di + s_da[cc]) * o[j]));
+          }
+        }
+        *at = pack8(h);
+      }
+    }
+    // X <- a X + B X
+    products([&]() {
+      for (int k = 0; k < p.mp; k += 16)
+        mma_bf16_ss(tmem + 256u, sdesc_kmajor_sw128(aa + (uint32_t)((k >> 6) * SM_BLK + (k & 63) * 2)),
+                    sdesc_mn_blocks(xa + (uint32_t)k * 128u), ID | (1u << 16) | ((uint32_t)(W >> 3) << 17), k != 0 ? 1u : 0u);
+    });
+    const float db = i < p.mp ? s_db[i] : 0.0f, fx = first ? NS_S * rho : 1.0f, cb = first ? rho : 1.0f / NS_S;
+    const bool diag_full = s >= p.steps - 2;
+#pragma unroll
+    for (int c = 0; c < WC; c += 16) {
+      uint32_t acc[16];
+      tmem_ld_32x32b_x16(row_tmem + 256u + (uint32_t)(j0 + c), acc);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float v = x[c + j], y = diag_full ? v : __half2float(__float2half_rn(v));
+        x[c + j] = fx * (p.a * v + db * y) + cb * __uint_as_float(acc[j]);
+      }
+    }
+    if (!last) put_hi();
+  }
+
+  // the update, in the matrix's own orientation
+  bf16* out = p.out + (size_t)mat * p.m * p.n;
+  const bool vec = !tall && p.n % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
+#pragma unroll
+  for (int c = 0; c < WC; c += 8) {
+    if (i >= p.m || g0 + c >= p.n) break;
+    if (vec) {
+      *reinterpret_cast<uint4*>(out + (size_t)i * p.n + g0 + c) =
+          make_uint4(pack_bf16x2(x[c] * p.scale, x[c + 1] * p.scale), pack_bf16x2(x[c + 2] * p.scale, x[c + 3] * p.scale),
+                     pack_bf16x2(x[c + 4] * p.scale, x[c + 5] * p.scale), pack_bf16x2(x[c + 6] * p.scale, x[c + 7] * p.scale));
     } else {
-      p.hi[o] = h[0];
-      p.lo[o] = l[0];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (g0 + c + j < p.n)
+          out[tall ? (size_t)(g0 + c + j) * p.m + i : (size_t)i * p.n + g0 + c + j] = __float2bfloat16_rn(x[c + j] * p.scale);
+      }
     }
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while another may still read its shared memory
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -640,6 +1014,7 @@ struct moe_muon_plan {
   moe_muon_config cfg;
   int device, num_sms;
   int64_t chunk;  // matrices in flight
+  int small_cs, small_wc;  // the one-launch form: CTAs per matrix (0: not used) and columns per thread
   encode_tiled_fn encode;
 };
 
@@ -656,6 +1031,10 @@ struct NsLayout {
 NsLayout ns_layout(const moe_muon_plan* pl) {
   const moe_muon_config& c = pl->cfg;
   NsLayout L{};
+  if (pl->small_cs) {  // on chip but for the status word
+    L.total = 256;
+    return L;
+  }
   L.m = c.rows < c.cols ? c.rows : c.cols;
   L.n = c.rows < c.cols ? c.cols : c.rows;
   L.ldx = up(c.cols, 8);
@@ -668,7 +1047,7 @@ NsLayout ns_layout(const moe_muon_plan* pl) {
     return at;
   };
   L.rho = take(sizeof(float) * pl->chunk);
-  L.part = take(sizeof(double) * 3 * NS_PREP_BLOCKS * pl->chunk);
+  L.part = take(sizeof(float) * 4 * NS_PREP_BLOCKS * pl->chunk);
   for (int i = 0; i < 2; ++i) {
     L.hi[i] = take(sizeof(__half) * pl->chunk * c.rows * L.ldx);
     L.lo[i] = take(sizeof(__half) * pl->chunk * c.rows * L.ldx);
@@ -694,13 +1073,73 @@ int ns_encode(const moe_muon_plan* pl, CUtensorMap* m, const void* ptr, int64_t 
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
+// Launch; `early`: the grid may be set up while the launch before it on the
+// stream still runs (the kernels wait for that one's results themselves)
+template <typename P, typename... A>
+cudaError_t launch_after(void (*kernel)(P, A...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool early,
+                         const std::remove_const_t<P>& p, const std::remove_const_t<A>&... a) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&lc, kernel, p, a...);
+}
+
+// The one-launch form's shape for a plan, if it applies: m <= 128 and up to 16
+// CTAs of at most 256 columns.
+using SmallKernel = void (*)(SmallParams);
+SmallKernel small_kernel(int wc) { return wc == 16 ? ns_small<16> : wc == 32 ? ns_small<32> : ns_small<64>; }
+cudaLaunchConfig_t small_launch(const moe_muon_plan* pl, cudaLaunchAttribute* at, cudaStream_t st) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(pl->cfg.count * pl->small_cs));
+  lc.blockDim = dim3(SM_THREADS);
+  lc.dynamicSmemBytes = SM_BYTES;
+  lc.stream = st;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)pl->small_cs;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return lc;
+}
+int small_prepare(moe_muon_plan* pl) {
+  const moe_muon_config& c = pl->cfg;
+  const int64_t m = c.rows < c.cols ? c.rows : c.cols, n = c.rows < c.cols ? c.cols : c.rows;
+  pl->small_cs = pl->small_wc = 0;
+  if (m > 128 || n > 16 * 256) return MOE_OK;
+  int wc = 64, cs = 1;
+  while (cs * 256 < n) cs *= 2;
+  while (wc > 16 && (int64_t)cs * 2 * wc >= n) wc /= 2;  // (as narrow as the columns are)
+  pl->small_cs = cs;
+  pl->small_wc = wc;
+  const SmallKernel k = small_kernel(wc);
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES) != cudaSuccess ||
+      cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t lc = small_launch(pl, at, nullptr);
+  int fit = 0;
+  if (cudaOccupancyMaxActiveClusters(&fit, k, &lc) != cudaSuccess) return MOE_ERR_CUDA;
+  if (fit < 1) pl->small_cs = 0;  // no room for a cluster of that size on this GPU
+  return MOE_OK;
+}
+
+template <int KIND, bool A_MN, bool B_MN>
+cudaError_t ns_prepare() {
+  return cudaFuncSetAttribute(ns_gemm<KIND, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM);
+}
 template <int KIND, bool A_MN, bool B_MN>
 cudaError_t ns_launch(const moe_muon_plan* pl, const NsMaps& mp, const NsParams& p, cudaStream_t st) {
-  cudaError_t err = cudaFuncSetAttribute(ns_gemm<KIND, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM);
-  if (err != cudaSuccess) return err;
   const int64_t units = (int64_t)p.nb * p.n_tiles, pairs = pl->num_sms / 2;
-  ns_gemm<KIND, A_MN, B_MN><<<(unsigned)(2 * (units < pairs ? units : pairs)), NS_THREADS, NS_SMEM, st>>>(mp, p);
-  return cudaGetLastError();
+  return launch_after(ns_gemm<KIND, A_MN, B_MN>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), NS_THREADS, NS_SMEM,
+                      st, true, mp, p);
 }
 
 }  // namespace
@@ -731,6 +1170,10 @@ int moe_muon_plan_create(const moe_muon_config* cfg, moe_muon_plan** out) {
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
       q != cudaDriverEntryPointSuccess || !fn)
     return MOE_ERR_CUDA;
+  if (ns_prepare<NS_GRAM, false, false>() != cudaSuccess || ns_prepare<NS_GRAM, true, true>() != cudaSuccess ||
+      ns_prepare<NS_POLY, false, false>() != cudaSuccess || ns_prepare<NS_STEP, false, false>() != cudaSuccess ||
+      ns_prepare<NS_STEP, false, true>() != cudaSuccess)
+    return MOE_ERR_CUDA;
   moe_muon_plan* pl = new (std::nothrow) moe_muon_plan;
   if (!pl) return MOE_ERR_INVALID_ARG;
   pl->cfg = c;
@@ -743,6 +1186,11 @@ int moe_muon_plan_create(const moe_muon_config* cfg, moe_muon_plan** out) {
   const int64_t mt = up(c.rows < c.cols ? c.rows : c.cols, NS_TILE) / NS_TILE, tiles = mt * (mt + 1) / 2;
   const int64_t want = (8 * (int64_t)(sms / 2) + tiles - 1) / tiles;
   pl->chunk = want < c.count ? want : c.count;
+  const int rc = small_prepare(pl);
+  if (rc != MOE_OK) {
+    delete pl;
+    return rc;
+  }
   *out = pl;
   return MOE_OK;
 }
@@ -774,6 +1222,35 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
   cudaStream_t st = (cudaStream_t)stream_;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const bool tall = c.rows > c.cols;
+  PrepParams pp{};
+  pp.grad = grad;
+  pp.grs = grad_row_stride;
+  pp.gms = grad_stride;
+  pp.dtype = c.grad_dtype;
+  pp.R = (int)c.rows;
+  pp.C = (int)c.cols;
+  pp.nesterov = nesterov;
+  pp.mu = mu;
+  pp.momentum = momentum;
+  if (pl->small_cs) {
+    SmallParams sp{};
+    sp.in = pp;
+    sp.out = static_cast<bf16*>(update);
+    sp.steps = c.steps;
+    sp.tall = tall;
+    sp.m = (int)(tall ? c.cols : c.rows);
+    sp.n = (int)(tall ? c.rows : c.cols);
+    sp.mp = (int)up(sp.m, 16);
+    sp.a = c.a;
+    sp.b = c.b;
+    sp.c = c.c;
+    sp.scale = scale / NS_S;
+    sp.status = reinterpret_cast<int*>(ws);
+    sp.timeout_ns = (long long)c.timeout_ms * 1000000LL;
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t lc = small_launch(pl, at, st);
+    return cudaLaunchKernelEx(&lc, small_kernel(pl->small_wc), sp) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
   auto half_at = [&](size_t o) { return reinterpret_cast<__half*>(ws + o); };
 
   // K-major operands and the epilogue's tiles are 128 rows at a time, MN-major
@@ -791,23 +1268,14 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
   rc |= ns_encode(pl, &bm, half_at(L.b), pl->chunk, L.m, L.m, L.lda, 64);
   if (rc != MOE_OK) return MOE_ERR_INVALID_ARG;
 
-  PrepParams pp{};
-  pp.grs = grad_row_stride;
-  pp.gms = grad_stride;
-  pp.dtype = c.grad_dtype;
-  pp.R = (int)c.rows;
-  pp.C = (int)c.cols;
-  pp.nesterov = nesterov;
   pp.ld = L.ldx;
-  pp.mu = mu;
-  pp.part = reinterpret_cast<double*>(ws + L.part);
+  pp.part = reinterpret_cast<float*>(ws + L.part);
   pp.rho = reinterpret_cast<float*>(ws + L.rho);
   pp.hi = half_at(L.hi[0]);
   pp.lo = half_at(L.lo[0]);
-  const bool vec = c.cols % 4 == 0 && grad_row_stride % 4 == 0 && grad_stride % 4 == 0 && ns_aligned(grad, 4 * gsize) &&
+  const bool vec = c.cols % 8 == 0 && grad_row_stride % 8 == 0 && grad_stride % 8 == 0 && ns_aligned(grad, 16) &&
                    ns_aligned(momentum, 16);
-  const int64_t nvec = c.rows * c.cols / (vec ? 4 : 1);
-  const int64_t nblk = up(nvec, 2048) / 2048;
+  const int64_t nblk = up(c.rows * c.cols / (vec ? 8 : 1), 256 * NS_PREP_U) / (256 * NS_PREP_U);
   pp.nblk = (int)(nblk < NS_PREP_BLOCKS ? nblk : NS_PREP_BLOCKS);
 
   NsParams g{};
@@ -827,14 +1295,10 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
     pp.momentum = momentum ? momentum + (size_t)c0 * c.rows * c.cols : nullptr;
     bf16* out = static_cast<bf16*>(update) + (size_t)c0 * c.rows * c.cols;
     const dim3 pgrid((unsigned)pp.nblk, (unsigned)nb);
-    if (vec) {
-      ns_prep_norm<4><<<pgrid, 256, 0, st>>>(pp);
-      ns_prep_first<4><<<pgrid, 256, 0, st>>>(pp);
-    } else {
-      ns_prep_norm<1><<<pgrid, 256, 0, st>>>(pp);
-      ns_prep_first<1><<<pgrid, 256, 0, st>>>(pp);
-    }
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    // (the first launch of the call waits for what is on the stream before it as usual)
+    if (launch_after(vec ? ns_prep_norm<8> : ns_prep_norm<1>, pgrid, 256, 0, st, c0 > 0, pp) != cudaSuccess ||
+        launch_after(vec ? ns_prep_first<8> : ns_prep_first<1>, pgrid, 256, 0, st, true, pp) != cudaSuccess)
+      return MOE_ERR_CUDA;
     g.nb = nb;
     g.out_final = out;
     g.out_vec = c.cols % 8 == 0 && ns_aligned(out, 16);

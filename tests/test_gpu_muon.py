@@ -198,6 +198,32 @@ def test_several_chunks_equal_single_matrices():
         assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), None, "fp32", 1, rows, cols)[0])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("count,rows,cols", [(3, 128, 64), (2, 128, 129), (2, 64, 256), (2, 20, 257), (2, 257, 20), (2, 100, 600),
+                                             (1, 1500, 128), (3, 24, 1788), (2, 117, 3051), (2, 3051, 117), (1, 128, 4096),
+                                             (1, 4097, 16), (1, 129, 1000), (40, 96, 512)])
+def test_shapes_around_the_small_form(count, rows, cols):
+    """Widths of a CTA's columns, cluster sizes, and the sizes beyond which the
+    steps are launches of their own."""
+    grad = stack(count, rows, cols, "decaying", rows + 3 * cols).bfloat16()
+    mom = stack(count, rows, cols, "flat", rows * 2 + cols)
+    m2 = mom.clone()
+    ref, rm = plain(grad, mom)
+    out = run(grad, mom, "bf16", count, rows, cols)
+    assert rel(out, ref) <= TOL
+    assert float((mom.double() - rm).abs().max()) <= 2 ** -23 * float(rm.abs().max())
+    assert torch.equal(out, run(grad, m2, "bf16", count, rows, cols))
+
+
+@pytest.mark.gpu
+def test_several_chunks_of_the_general_form():
+    count, rows, cols = 612, 129, 136
+    grad = stack(count, rows, cols, "flat", 6).bfloat16()
+    out = run(grad, None, "bf16", count, rows, cols)
+    for i in (0, 607, 608, 611):
+        assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), None, "bf16", 1, rows, cols)[0])
+
+
 # ---------------------------------------------------------------- refusals (no GPU needed)
 @pytest.fixture(scope="module")
 def L():
