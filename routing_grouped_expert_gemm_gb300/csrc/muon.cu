@@ -680,6 +680,7 @@ struct SmallParams {
   PrepParams in;
   bf16* out;
   int steps, tall, m, n, mp;  // mp: m rounded up to 16
+  int vec;                    // rows of the stored matrix are 16-byte aligned vectors of 8
   float a, b, c, scale;
   int* status;
   long long timeout_ns;
@@ -752,39 +753,81 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
     tmem_alloc<512>(tmem_slot);
     tmem_relinquish();
   }
-  // gradient and momentum -> U, in registers
+  // gradient and momentum -> U: read in the matrix's own order, 8 values a
+  // thread, and turned to this thread's row of columns through shared memory
   float x[WC];
   float f[3] = {0.0f, 0.0f, 0.0f};
   {
+    constexpr int PITCH = W + 4;
+    float* stage = reinterpret_cast<float*>(smem);  // [128][PITCH], before X and A are there
     const PrepParams& in = p.in;
     float* mom = in.momentum ? in.momentum + (size_t)mat * in.R * in.C : nullptr;
-    const size_t gs = tall ? (size_t)in.grs : 1, ms = tall ? (size_t)in.C : 1;
-    const size_t gi = (size_t)mat * in.gms + (tall ? (size_t)g0 * in.grs + i : (size_t)i * in.grs + g0);
-    const size_t mi = tall ? (size_t)g0 * in.C + i : (size_t)i * in.C + g0;
+    const int s0 = (int)rank * W;                                // the slab's first column
+    const int lead = tall ? min(W, p.n - s0) : p.m;              // rows of the stored matrix to read ...
+    const int cols = tall ? p.m : min(W, p.n - s0);              // ... and columns of each
+    const int r_at = tall ? s0 : 0, c_at = tall ? 0 : s0;
+    const int per = cols > 0 ? (cols + 7) / 8 : 0, units = lead > 0 ? lead * per : 0;
+    for (int u = threadIdx.x; u < 128 * PITCH / 4; u += SM_THREADS) reinterpret_cast<float4*>(stage)[u] = make_float4(0, 0, 0, 0);
+    __syncthreads();
+    const bool vec = p.vec != 0;
+    for (int u0 = threadIdx.x; u0 < units; u0 += 2 * SM_THREADS) {
+      float g[2][8], m[2][8];
 #pragma unroll
-    for (int c = 0; c < WC; c += 8) {
-      float u[8], m[8];
+      for (int q = 0; q < 2; ++q) {
+        const int u = u0 + q * SM_THREADS;
+        if (u < units) {
+          const int r = u / per, c = (u - r * per) * 8;
+          const size_t gi = (size_t)mat * in.gms + (size_t)(r_at + r) * in.grs + c_at + c;
+          const float* mi = mom + (size_t)(r_at + r) * in.C + c_at + c;
+          if (vec) {
+            load_grad<8>(in.grad, in.dtype, gi, g[q]);
+            if (mom) load_f32<8>(mi, m[q]);
+          } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool on = i < p.m && g0 + c + j < p.n;
-        u[j] = m[j] = 0.0f;
-        if (on) {
-          float v[1];
-          load_grad<1>(in.grad, in.dtype, gi + (size_t)(c + j) * gs, v);
-          u[j] = v[0];
-          if (mom) m[j] = mom[mi + (size_t)(c + j) * ms];
+            for (int j = 0; j < 8; ++j) {
+              float v[1] = {0.0f};
+              if (c + j < cols) load_grad<1>(in.grad, in.dtype, gi + j, v);
+              g[q][j] = v[0];
+              m[q][j] = mom && c + j < cols ? mi[j] : 0.0f;
+            }
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (mom) {
-          m[j] = in.mu * m[j] + u[j];
-          if (i < p.m && g0 + c + j < p.n) mom[mi + (size_t)(c + j) * ms] = m[j];
-          u[j] = in.nesterov ? u[j] + in.mu * m[j] : m[j];
+      for (int q = 0; q < 2; ++q) {
+        const int u = u0 + q * SM_THREADS;
+        if (u < units) {
+          const int r = u / per, c = (u - r * per) * 8;
+          if (mom) {
+            float* mi = mom + (size_t)(r_at + r) * in.C + c_at + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              m[q][j] = in.mu * m[q][j] + g[q][j];
+              g[q][j] = in.nesterov ? g[q][j] + in.mu * m[q][j] : m[q][j];
+            }
+            if (vec) {
+              reinterpret_cast<float4*>(mi)[0] = make_float4(m[q][0], m[q][1], m[q][2], m[q][3]);
+              reinterpret_cast<float4*>(mi)[1] = make_float4(m[q][4], m[q][5], m[q][6], m[q][7]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (c + j < cols) mi[j] = m[q][j];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (c + j >= cols) break;
+            add_square(f, g[q][j]);
+            stage[tall ? (c + j) * PITCH + r : r * PITCH + c + j] = g[q][j];
+          }
         }
-        add_square(f, u[j]);
-        x[c + j] = u[j];
       }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < WC; c += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(stage + i * PITCH + j0 + c);
+      x[c] = v.x, x[c + 1] = v.y, x[c + 2] = v.z, x[c + 3] = v.w;
     }
   }
 #pragma unroll
@@ -910,6 +953,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
       for (int u = (int)rank + (int)cs * (int)threadIdx.x; u < units; u += (int)cs * SM_THREADS) {
         const int r = u / per_row, c = (u - r * per_row) * 8;
         float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
         for (uint32_t q = 0; q < cs; ++q) {  // in the CTAs' order, whoever sums
           const uint32_t at = mapa_shared(part + r * SM_PITCH + c, q);
           const float4 w0 = ld_cluster_f4(at), w1 = ld_cluster_f4(at + 16);
@@ -1241,6 +1285,7 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
     sp.m = (int)(tall ? c.cols : c.rows);
     sp.n = (int)(tall ? c.rows : c.cols);
     sp.mp = (int)up(sp.m, 16);
+    sp.vec = c.cols % 8 == 0 && grad_row_stride % 8 == 0 && grad_stride % 8 == 0 && ns_aligned(grad, 16) && ns_aligned(momentum, 16);
     sp.a = c.a;
     sp.b = c.b;
     sp.c = c.c;
