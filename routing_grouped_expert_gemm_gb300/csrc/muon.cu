@@ -1161,6 +1161,10 @@ int small_prepare(moe_muon_plan* pl) {
   int wc = 64, cs = 1;
   while (cs * 256 < n) cs *= 2;
   while (wc > 16 && (int64_t)cs * 2 * wc >= n) wc /= 2;  // (as narrow as the columns are)
+  // Few small matrices: more CTAs with fewer columns each, while every cluster
+  // still runs at once and A is small to exchange (4 x 49 x 657: 4 CTAs 68 us,
+  // 8 54 us; 20 x 16 x 247: 1 35 us, 4 27 us; with m = 128 no gain, 92 and 95)
+  while (m <= 64 && wc > 16 && cs < 8 && c.count * cs * 2 <= pl->num_sms) cs *= 2, wc /= 2;
   pl->small_cs = cs;
   pl->small_wc = wc;
   const SmallKernel k = small_kernel(wc);
@@ -1171,7 +1175,11 @@ int small_prepare(moe_muon_plan* pl) {
   const cudaLaunchConfig_t lc = small_launch(pl, at, nullptr);
   int fit = 0;
   if (cudaOccupancyMaxActiveClusters(&fit, k, &lc) != cudaSuccess) return MOE_ERR_CUDA;
-  if (fit < 1) pl->small_cs = 0;  // no room for a cluster of that size on this GPU
+  // Few clusters of 16 run at once (SMs of one GPC), in rounds of 100 us: from
+  // the fourth round on the general form, whose launches hardly notice another
+  // matrix, is ahead (9 x 117 x 3051: 302 us in three, 335 us).  Up to 8 the
+  // one launch stays ahead (90 x 100 x 600: 238 us, 361 us).
+  if (fit < 1 || (cs > 8 && c.count > 3 * (int64_t)fit)) pl->small_cs = 0;
   return MOE_OK;
 }
 
