@@ -40,8 +40,8 @@
 
 namespace moe {
 
-constexpr int NS_THREADS = 224;       // producer, MMA issuer, four epilogue warps, the epilogue's loads and stores
-constexpr int NS_TILE = 256;          // of a CTA pair: 256 x 256, 128 rows in each CTA
+constexpr int NS_THREADS = 352;       // producer, MMA issuer, eight epilogue warps, the epilogue's loads and stores
+constexpr int NS_TILE = 256;          // of a CTA pair: 256 x TN (256 or 128), 128 rows in each CTA
 constexpr int NS_BOX = 8192;          // one {64, 64} fp16 box
 constexpr int NS_STAGE = 4 * NS_BOX;  // per CTA: 128 rows of A and half of B's 256, 64 of K
 constexpr int NS_STAGES = 5;
@@ -94,15 +94,18 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {  // MN-
   return d;
 }
 // .kind::f16 with fp16 A and B (format 0), fp32 D
-constexpr uint32_t ns_idesc(bool a_mn, bool b_mn) {
-  return (1u << 4) | ((NS_TILE >> 3) << 17) | ((NS_TILE >> 4) << 24) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+constexpr uint32_t ns_idesc(int tn, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((uint32_t)(tn >> 3) << 17) | ((NS_TILE >> 4) << 24) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
 struct NsTile {
   int mat, m0, n0;
 };
-template <int KIND>
+// Symmetric products: the tiles that reach the diagonal or lie below it, row
+// by row -- (i + 1) F of them in row i of 256, F = 256 / TN columns of tiles each.
+template <int KIND, int TN>
 __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int u) {
+  constexpr int F = NS_TILE / TN;
   NsTile t;
   t.mat = u / p.n_tiles;
   const int v = u - t.mat * p.n_tiles;
@@ -110,14 +113,14 @@ __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int u) {
   if (KIND == NS_STEP) {
     i = v / p.tiles_n;
     j = v - i * p.tiles_n;
-  } else {  // lower triangle, row by row
-    i = (int)((sqrtf(8.0f * (float)v + 1.0f) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > v) --i;
-    while ((i + 1) * (i + 2) / 2 <= v) ++i;
-    j = v - i * (i + 1) / 2;
+  } else {
+    i = (int)((sqrtf(8.0f / F * (float)v + 1.0f) - 1.0f) * 0.5f);
+    while (F * i * (i + 1) / 2 > v) --i;
+    while (F * (i + 1) * (i + 2) / 2 <= v) ++i;
+    j = v - F * i * (i + 1) / 2;
   }
   t.m0 = i * NS_TILE;
-  t.n0 = j * NS_TILE;
+  t.n0 = j * TN;
   return t;
 }
 
@@ -137,18 +140,18 @@ __device__ __forceinline__ uint4 pack8(const __half* h) {
                     (uint32_t)__half_as_ushort(h[6]) | ((uint32_t)__half_as_ushort(h[7]) << 16));
 }
 
-// One row (TMEM lane) of an epilogue chunk, 64 columns: `main` holds this row's
-// inputs and takes its outputs in place (POLY: A -> B; STEP: hi), `aux` is lo,
-// or takes the chunk transposed (symmetric products' tiles below the
-// diagonal).  Rows of 128 bytes, 16-byte pieces swizzled as the tensor maps'.
+// One row (TMEM lane) of half an epilogue chunk (32 of 64 columns, from i0 * 8):
+// `main` holds this row's inputs and takes its outputs in place (POLY: A -> B;
+// STEP: hi), `aux` is lo, or takes the chunk transposed (symmetric products'
+// tiles below the diagonal).  Rows of 128 bytes, 16-byte pieces swizzled as the
+// tensor maps'.
 template <int KIND>
 __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uint8_t* main, uint8_t* aux, int rl, int r,
-                                         int c0, float rho, uint32_t taddr) {
-  uint32_t acc[2][32];
-  tmem_ld_32x32b_x32(taddr, acc[0]);
-  tmem_ld_32x32b_x32(taddr + 32u, acc[1]);
+                                         int c0, int i0, float rho, uint32_t taddr) {
+  uint32_t acc[32];
+  tmem_ld_32x32b_x32(taddr + 8u * (uint32_t)i0, acc);
   tmem_ld_wait();
-  const bool mirror = KIND != NS_STEP && t.m0 != t.n0;
+  const bool mirror = KIND != NS_STEP && t.n0 < t.m0;
   const float* da = p.diag_a + (size_t)t.mat * p.ldd;
   const float* db = p.diag_b + (size_t)t.mat * p.ldd;
   float f = 1.0f, g = 0.0f, cb = p.cb;
@@ -159,12 +162,12 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
     if (!p.tall) g = db[r];
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = c0 + 8 * i;
+  for (int ii = 0; ii < 4; ++ii) {
+    const int i = i0 + ii, c = c0 + 8 * i;
     uint4* at = reinterpret_cast<uint4*>(main + rl * 128 + ((i ^ (rl & 7)) << 4));
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[i / 4][(8 * i + j) & 31]);
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[8 * ii + j]);
     __half h[8];
     if (KIND == NS_GRAM) {
 #pragma unroll
@@ -242,14 +245,15 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
 
 // Persistent CTA pairs, one per SM pair; pair u takes tiles u, u + pairs, ...
 // Warp 0: TMA producer of this CTA's operands (counted on the even CTA's full
-// barrier); warp 1 of the even CTA: tcgen05.mma for both; warps 2-5: epilogue
-// of this CTA's 128 rows, 64 columns at a time; warp 6: loads the epilogue's
-// inputs into the two epilogue buffers and stores its outputs from them, both
-// by TMA, the loads ahead of the accumulator.  Two 256-column accumulators in
-// TMEM alternate, so a tile's epilogue runs under the next tile's products.
+// barrier); warp 1 of the even CTA: tcgen05.mma for both; warps 2-9: epilogue
+// of this CTA's 128 rows, 64 columns at a time, two warps to 32 rows; warp 10:
+// loads the epilogue's inputs into the two epilogue buffers and stores its
+// outputs from them, both by TMA, the loads ahead of the accumulator.  Two
+// accumulators of TN columns in TMEM alternate, so a tile's epilogue runs under
+// the next tile's products.
 // (Rows read and written by the threads themselves, 32 rows of 16 bytes at a
 // time, took 30 us a tile of X against 12 us of products.)
-template <int KIND, bool A_MN, bool B_MN>
+template <int KIND, int TN, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_gemm(const __grid_constant__ NsMaps mp, const NsParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -272,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const int n_units = p.nb * p.n_tiles;
   const int nk = (p.K + BK - 1) / BK;
   // epilogue chunks of this CTA's part of a tile
-  auto chunks = [&](const NsTile& t) { return t.m0 + rank * 128 < p.M ? (min(NS_TILE, p.N - t.n0) + 63) / 64 : 0; };
+  auto chunks = [&](const NsTile& t) { return t.m0 + rank * 128 < p.M ? (min(TN, p.N - t.n0) + 63) / 64 : 0; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS_STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -280,9 +284,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 8);  // one arrival per epilogue warp of both CTAs
+      mbar_init(&tempty[a], 16);  // one arrival per epilogue warp of both CTAs
       mbar_init(&eload[a], 1);
-      mbar_init(&edone[a], 4);   // one per epilogue warp
+      mbar_init(&edone[a], 8);    // one per epilogue warp
     }
     mbar_init(drain, 1);
     fence_barrier_init();
@@ -290,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     prefetch_tensormap(&mp.b);
   }
   if (warp == 1) {
-    tmem_alloc_pair<512>(tmem_slot);
+    tmem_alloc_pair<2 * TN>(tmem_slot);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -307,13 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       int issued = 0;
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += pairs) {
-        const NsTile t = ns_tile<KIND>(p, u);
-        const int ar = t.m0 + rank * 128, br = t.n0 + rank * 128;
+        const NsTile t = ns_tile<KIND, TN>(p, u);
+        const int ar = t.m0 + rank * 128, br = t.n0 + rank * (TN / 2);
         for (int s = 0; s < nk; ++s) {
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, p.status, p.timeout_ns)) { ok = false; break; }
           uint8_t* sa = smem + stage * NS_STAGE;
           uint8_t* sb = sa + 2 * NS_BOX;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * NS_STAGE);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * (2 + TN / 128) * NS_BOX);
           const uint32_t fb = full_even + 8u * stage;
           if (A_MN) {
             tma_load_3d_pair(sa, &mp.a, fb, ar, s * BK, t.mat);
@@ -323,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           }
           if (B_MN) {
             tma_load_3d_pair(sb, &mp.b, fb, br, s * BK, t.mat);
-            tma_load_3d_pair(sb + NS_BOX, &mp.b, fb, br + 64, s * BK, t.mat);
+            if (TN == 256) tma_load_3d_pair(sb + NS_BOX, &mp.b, fb, br + 64, s * BK, t.mat);
           } else {
             tma_load_3d_pair(sb, &mp.b, fb, s * BK, br, t.mat);
           }
@@ -347,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
         const uint32_t acc = (uint32_t)i & 1u;
         if (!mbar_wait_cluster(&tempty[acc], (((uint32_t)i >> 1) & 1u) ^ 1u, p.status, p.timeout_ns)) break;
         tc_fence_after();
-        const uint32_t d = tmem + acc * 256u;
+        const uint32_t d = tmem + acc * TN;
         for (int s = 0; s < nk; ++s) {
           if (!mbar_wait_cluster(&full[stage], phase, p.status, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
@@ -357,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = A_MN ? sdesc_mn_sw128(a_addr + kk * 2048) : sdesc_kmajor_sw128(a_addr + kk * 32);
             const uint64_t bd = B_MN ? sdesc_mn_sw128(b_addr + kk * 2048) : sdesc_kmajor_sw128(b_addr + kk * 32);
-            mma_bf16_pair(d, ad, bd, ns_idesc(A_MN, B_MN), (s | kk) != 0 ? 1u : 0u);
+            mma_bf16_pair(d, ad, bd, ns_idesc(TN, A_MN, B_MN), (s | kk) != 0 ? 1u : 0u);
           }
           mma_commit_pair(&empty[stage], 0x3);
           if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
@@ -368,25 +372,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       mbar_wait_drain(drain, 0, p.timeout_ns);  // every MMA issued has completed before TMEM is freed
     }
     __syncwarp();
-  } else if (warp < 6) {
-    const int q = warp & 3, rl = q * 32 + lane;
+  } else if (warp < 10) {
+    const int q = warp & 3, rl = q * 32 + lane, half = (warp - 2) >> 2;
     const uint32_t tempty_even = mapa_shared(tempty, 0);
     int i = 0, n = 0;
     bool ok = true;
     for (int u = pair; u < n_units && ok; u += pairs, ++i) {
-      const NsTile t = ns_tile<KIND>(p, u);
+      const NsTile t = ns_tile<KIND, TN>(p, u);
       const uint32_t acc = (uint32_t)i & 1u;
       const int nc = chunks(t);
       const float rho = p.first ? p.rho[t.mat] : 0.0f;
       if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tfull[acc], ((uint32_t)i >> 1) & 1u, p.status, p.timeout_ns))) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * 256u;
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * TN;
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const int b = n & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&eload[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns))) { ok = false; break; }
         uint8_t* e = ebuf + b * NS_EBUF;
-        ns_chunk<KIND>(p, t, e, e + 2 * NS_BOX, rl, t.m0 + rank * 128 + rl, t.n0 + 64 * c, rho, taddr + 64u * (uint32_t)c);
+        ns_chunk<KIND>(p, t, e, e + 2 * NS_BOX, rl, t.m0 + rank * 128 + rl, t.n0 + 64 * c, 4 * half, rho,
+                       taddr + 64u * (uint32_t)c);
         fence_proxy_async_smem();  // these writes, before the TMA store that follows the arrival
         __syncwarp();
         if (lane == 0) mbar_arrive(&edone[b]);
@@ -401,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     int lu = pair, lc = 0, ln = 0;  // next chunk to load: unit, chunk of its tile, number
     auto load_next = [&]() {
       while (lu < n_units) {
-        const NsTile t = ns_tile<KIND>(p, lu);
+        const NsTile t = ns_tile<KIND, TN>(p, lu);
         if (lc >= chunks(t)) {
           lu += pairs;
           lc = 0;
@@ -426,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     int n = 0;
     bool ok = true;
     for (int u = pair; u < n_units && ok; u += pairs) {
-      const NsTile t = ns_tile<KIND>(p, u);
+      const NsTile t = ns_tile<KIND, TN>(p, u);
       const int nc = chunks(t), row = t.m0 + rank * 128;
       for (int c = 0; c < nc; ++c, ++n) {
         const int b = n & 1, col = t.n0 + 64 * c;
@@ -437,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           if (!p.last) tma_store_3d(&mp.out1, e + 2 * NS_BOX, col, row, t.mat);
         } else {
           tma_store_3d(&mp.out0, e, col, row, t.mat);
-          if (t.m0 != t.n0) {
+          if (t.n0 < t.m0) {
             tma_store_3d(&mp.out1, e + 2 * NS_BOX, row, col, t.mat);
             if (row + 64 < p.M) tma_store_3d(&mp.out1, e + 3 * NS_BOX, row + 64, col, t.mat);
           }
@@ -460,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(tmem, 2 * TN);
   }
 }
 
@@ -1184,14 +1189,29 @@ int small_prepare(moe_muon_plan* pl) {
 }
 
 template <int KIND, bool A_MN, bool B_MN>
-cudaError_t ns_prepare() {
-  return cudaFuncSetAttribute(ns_gemm<KIND, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM);
+bool ns_prepare() {
+  return cudaFuncSetAttribute(ns_gemm<KIND, 256, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM) == cudaSuccess &&
+         cudaFuncSetAttribute(ns_gemm<KIND, 128, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM) == cudaSuccess;
 }
+// One product of every matrix, M and N of one given.  Tiles of 256 x 256, or
+// 256 x 128 where those leave CTA pairs idle: a narrow tile takes about 2/3 of
+// a wide one's time, so it is taken where its rounds over the pairs are fewer
+// than 3/2 of the wide tiles' (2 x 700 x 650: 259 us wide, 189 us by this rule;
+// 8 x 1024 x 4096, two rounds of wide tiles or three of narrow: 833 and 846 us).  b64: the second operand with boxes of 64 rows.
 template <int KIND, bool A_MN, bool B_MN>
-cudaError_t ns_launch(const moe_muon_plan* pl, const NsMaps& mp, const NsParams& p, cudaStream_t st) {
-  const int64_t units = (int64_t)p.nb * p.n_tiles, pairs = pl->num_sms / 2;
-  return launch_after(ns_gemm<KIND, A_MN, B_MN>, dim3((unsigned)(2 * (units < pairs ? units : pairs))), NS_THREADS, NS_SMEM,
-                      st, true, mp, p);
+cudaError_t ns_launch(const moe_muon_plan* pl, NsMaps mp, const CUtensorMap& b64, NsParams p, cudaStream_t st) {
+  const int64_t pairs = pl->num_sms / 2, mt = up(p.M, NS_TILE) / NS_TILE, sym = mt * (mt + 1) / 2;
+  auto tiles = [&](int tn) { return KIND == NS_STEP ? mt * (up(p.N, tn) / tn) : sym * (NS_TILE / tn); };
+  auto rounds = [&](int tn) { return (p.nb * tiles(tn) + pairs - 1) / pairs; };
+  const bool narrow = 2 * rounds(128) < 3 * rounds(256);
+  const int tn = narrow ? 128 : 256;
+  p.tiles_n = (int)(up(p.N, tn) / tn);
+  p.n_tiles = (int)tiles(tn);
+  if (narrow) mp.b = b64;
+  const int64_t units = (int64_t)p.nb * p.n_tiles;
+  const dim3 grid((unsigned)(2 * (units < pairs ? units : pairs)));
+  return narrow ? launch_after(ns_gemm<KIND, 128, A_MN, B_MN>, grid, NS_THREADS, NS_SMEM, st, true, mp, p)
+                : launch_after(ns_gemm<KIND, 256, A_MN, B_MN>, grid, NS_THREADS, NS_SMEM, st, true, mp, p);
 }
 
 }  // namespace
@@ -1222,9 +1242,8 @@ int moe_muon_plan_create(const moe_muon_config* cfg, moe_muon_plan** out) {
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
       q != cudaDriverEntryPointSuccess || !fn)
     return MOE_ERR_CUDA;
-  if (ns_prepare<NS_GRAM, false, false>() != cudaSuccess || ns_prepare<NS_GRAM, true, true>() != cudaSuccess ||
-      ns_prepare<NS_POLY, false, false>() != cudaSuccess || ns_prepare<NS_STEP, false, false>() != cudaSuccess ||
-      ns_prepare<NS_STEP, false, true>() != cudaSuccess)
+  if (!ns_prepare<NS_GRAM, false, false>() || !ns_prepare<NS_GRAM, true, true>() || !ns_prepare<NS_POLY, false, false>() ||
+      !ns_prepare<NS_STEP, false, false>() || !ns_prepare<NS_STEP, false, true>())
     return MOE_ERR_CUDA;
   moe_muon_plan* pl = new (std::nothrow) moe_muon_plan;
   if (!pl) return MOE_ERR_INVALID_ARG;
@@ -1340,7 +1359,6 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
   g.ldd = (int)L.ldd;
   g.diag_a = reinterpret_cast<float*>(ws + L.da);
   g.diag_b = reinterpret_cast<float*>(ws + L.db);
-  const int64_t mt = up(L.m, NS_TILE) / NS_TILE;
   for (int64_t c0 = 0; c0 < c.count; c0 += pl->chunk) {
     const int nb = (int)(c.count - c0 < pl->chunk ? c.count - c0 : pl->chunk);
     pp.grad = static_cast<const uint8_t*>(grad) + (size_t)c0 * grad_stride * gsize;
@@ -1367,27 +1385,25 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
       // A = X X^T or X^T X
       g.M = g.N = (int)L.m;
       g.K = (int)L.n;
-      g.tiles_n = (int)mt;
-      g.n_tiles = (int)(mt * (mt + 1) / 2);
       const CUtensorMap& xx = tall ? xm[x] : xk[x];
       const NsMaps gram = {xx, xx, ak, ak, ak, am};
-      err = tall ? ns_launch<NS_GRAM, true, true>(pl, gram, g, st) : ns_launch<NS_GRAM, false, false>(pl, gram, g, st);
+      err = tall ? ns_launch<NS_GRAM, true, true>(pl, gram, xm[x], g, st)
+                 : ns_launch<NS_GRAM, false, false>(pl, gram, xm[x], g, st);
       if (err != cudaSuccess) return MOE_ERR_CUDA;
       // B = b A + c A^2
       g.K = (int)L.m;
       g.ca = c.b;
       g.cb = c.c / NS_S;
       const NsMaps poly = {ak, ak, ak, ak, bk, bm};
-      if (ns_launch<NS_POLY, false, false>(pl, poly, g, st) != cudaSuccess) return MOE_ERR_CUDA;
+      if (ns_launch<NS_POLY, false, false>(pl, poly, am, g, st) != cudaSuccess) return MOE_ERR_CUDA;
       // X <- a X + B X or a X + X B
       g.M = (int)c.rows;
       g.N = (int)c.cols;
-      g.tiles_n = (int)(up(c.cols, NS_TILE) / NS_TILE);
-      g.n_tiles = (int)(up(c.rows, NS_TILE) / NS_TILE) * g.tiles_n;
       g.ca = c.a;
       g.cb = 1.0f / NS_S;
       const NsMaps step = {tall ? xk[x] : bk, tall ? bk : xm[x], xk[x], xl[x], g.last ? uk : xk[x ^ 1], xl[x ^ 1]};
-      err = tall ? ns_launch<NS_STEP, false, false>(pl, step, g, st) : ns_launch<NS_STEP, false, true>(pl, step, g, st);
+      err = tall ? ns_launch<NS_STEP, false, false>(pl, step, bm, g, st)
+                 : ns_launch<NS_STEP, false, true>(pl, step, xm[x], g, st);
       if (err != cudaSuccess) return MOE_ERR_CUDA;
     }
   }
