@@ -53,7 +53,8 @@ typedef enum moe_error {
 typedef enum moe_device_status {
   MOE_STATUS_OK = 0,
   MOE_STATUS_TIMEOUT = 1,          /* a device-side wait exceeded its limit; outputs are invalid */
-  MOE_STATUS_SCHEDULE_INVALID = 2, /* an expert index out of range or route counts inconsistent */
+  MOE_STATUS_SCHEDULE_INVALID = 2, /* an expert index out of range or route counts inconsistent
+                                      (moe_fwd_routed: an index out of range or given twice for a token) */
   MOE_STATUS_STAGING_OVERFLOW = 3  /* the forward completed, but an expert output left the fp16 range of
                                       the staging rows (|v| > 65504, or NaN) and was saturated: the
                                       output is finite but not the layer's value */
@@ -274,6 +275,24 @@ int moe_fwd(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w
             void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /*
+ * The forward pass with the routing given instead of made by the built-in
+ * router (moe_route makes one):
+ *   topk_idx [T, k] int32, topk_w [T, k] fp32 (device): expert and router
+ *   weight g of every slot; an index of -1 is an empty slot.
+ *   out = f_shared(x) + sum over the slots of g f_idx(x).
+ * W_router and b_router are ignored (may be NULL).  Every token takes up k
+ * routes: an empty slot runs the lowest expert that the token does not use,
+ * with weight 0 (it shows as such in o->topk_idx, o->topk_w, the counts and
+ * the schedule), so x must be finite in tokens without experts too.  An index
+ * out of [-1, E), or a second slot of a token with the same expert, is run as
+ * an empty slot and reported as MOE_STATUS_SCHEDULE_INVALID.
+ * Otherwise as moe_fwd (bf16 and MXFP8 plans).
+ */
+int moe_fwd_routed(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w, const int32_t* topk_idx,
+                   const float* topk_w, const moe_outputs* o, void* workspace, size_t workspace_bytes,
+                   moe_stream_t stream);
+
+/*
  * Read the device status of the last forward that used `workspace` (a
  * moe_device_status: a failure if one was recorded, else
  * MOE_STATUS_STAGING_OVERFLOW if that warning was raised, else MOE_STATUS_OK).
@@ -389,6 +408,18 @@ int moe_bwd(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w
             moe_stream_t stream);
 
 /*
+ * The backward pass after moe_fwd_routed: every gradient of moe_grads but the
+ * router's (dW_router and db_router are ignored, dx is without the router's
+ * term), and instead
+ *   dtopk_w [T, k] fp32 (device, required): dL/d topk_w; 0 in an empty slot
+ * which moe_route_bwd takes on to the logits.  Otherwise as moe_bwd; launches
+ * six kernels.
+ */
+int moe_bwd_routed(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w, const void* dO,
+                   const void* fwd_workspace, const moe_grads* grads, float* dtopk_w, void* workspace,
+                   size_t workspace_bytes, moe_stream_t stream);
+
+/*
  * Optional per-phase timing of moe_bwd for profiling harnesses: with events
  * != NULL, every later moe_bwd with this plan records events[0] before its
  * first launch, events[1] after the gather of the routes' x and dO rows,
@@ -404,7 +435,7 @@ int moe_plan_set_bwd_timing_events(moe_plan* plan, void* const* events);
  * takes part in the selection only, expert groups, top-k, and weights that may
  * or may not be renormalised; with its gradient.  (moe_fwd's built-in router
  * multiplies x by W_router itself, adds its bias to the logits and always
- * renormalises.)
+ * renormalises; moe_fwd_routed runs the experts on the routing made here.)
  */
 typedef enum moe_dtype { MOE_DTYPE_FP32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_FP16 = 2 } moe_dtype;
 

@@ -8,8 +8,8 @@ used only to hand over device pointers and streams.
 Entry points keep the C names: ``moe_plan_create``, ``moe_plan_destroy``,
 ``moe_workspace_bytes``, ``moe_quantize_mxfp8``, ``moe_mxfp8_scale_bytes``,
 ``moe_fwd``, ``moe_bwd_workspace_bytes``, ``moe_bwd``, ``moe_get_status``,
-``moe_get_phase_times``, ``moe_route_static``, ``moe_error_string``; routing from
-given logits: ``moe_route_plan_create``, ``moe_route_plan_destroy``,
+``moe_get_phase_times``, ``moe_route_static``, ``moe_error_string``; the layer on a
+given routing: ``moe_fwd_routed``, ``moe_bwd_routed``; routing from given logits: ``moe_route_plan_create``, ``moe_route_plan_destroy``,
 ``moe_route_workspace_bytes``, ``moe_route``, ``moe_route_bwd``; momentum and
 orthogonalised updates: ``moe_muon_plan_create``, ``moe_muon_plan_destroy``,
 ``moe_muon_workspace_bytes``, ``moe_muon_update``, ``moe_muon_get_status``.
@@ -132,6 +132,12 @@ def lib():
     L.moe_route_static.restype = ctypes.c_int
     L.moe_route_static_scratch_bytes.argtypes = []
     L.moe_route_static_scratch_bytes.restype = sz
+    L.moe_fwd_routed.argtypes = [vp, i64, vp, ctypes.POINTER(moe_weights), vp, vp, ctypes.POINTER(moe_outputs), vp, sz,
+                                 vp]
+    L.moe_fwd_routed.restype = ctypes.c_int
+    L.moe_bwd_routed.argtypes = [vp, i64, vp, ctypes.POINTER(moe_weights), vp, vp, ctypes.POINTER(moe_grads), vp, vp, sz,
+                                 vp]
+    L.moe_bwd_routed.restype = ctypes.c_int
     L.moe_route_plan_create.argtypes = [ctypes.POINTER(moe_route_config), ctypes.POINTER(vp)]
     L.moe_route_plan_create.restype = ctypes.c_int
     L.moe_route_plan_destroy.argtypes = [vp]
@@ -204,7 +210,8 @@ def _ptr(v) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        # the current stream's handle without a Stream object (0.2 us a call instead of 3)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -299,6 +306,35 @@ def moe_bwd(plan: Plan, T: int, x, weights: dict, dO, fwd_workspace, grads: dict
                        _ptr(workspace), workspace_bytes, _stream(stream))
     if rc != MOE_OK:
         raise MoEError(rc, "moe_bwd")
+
+
+def moe_fwd_routed(plan: Plan, T: int, x, weights: dict, topk_idx, topk_w, out, workspace,
+                   workspace_bytes: int | None = None, expert_counts=None, expert_offsets=None, sched=None,
+                   route_row=None, stream=None) -> None:
+    """The forward with its routing given: ``topk_idx`` [T, k] int32 (-1: an
+    empty slot) and ``topk_w`` [T, k] fp32, as ``moe_route`` writes them."""
+    w = moe_weights(**{k: _ptr(v) for k, v in weights.items()})
+    o = moe_outputs(_ptr(out), None, None, _ptr(expert_counts), _ptr(expert_offsets), _ptr(sched), _ptr(route_row))
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().moe_fwd_routed(plan.handle, T, _ptr(x), ctypes.byref(w), _ptr(topk_idx), _ptr(topk_w), ctypes.byref(o),
+                              _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_fwd_routed")
+
+
+def moe_bwd_routed(plan: Plan, T: int, x, weights: dict, dO, fwd_workspace, grads: dict, dtopk_w, workspace,
+                   workspace_bytes: int | None = None, stream=None) -> None:
+    """Backward of ``moe_fwd_routed``: ``grads`` as for ``moe_bwd`` without the
+    router's, and the gradient of ``topk_w`` in ``dtopk_w`` [T, k] fp32."""
+    w = moe_weights(**{k: _ptr(v) for k, v in weights.items()})
+    g = moe_grads(**{k: _ptr(v) for k, v in grads.items()})
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().moe_bwd_routed(plan.handle, T, _ptr(x), ctypes.byref(w), _ptr(dO), _ptr(fwd_workspace), ctypes.byref(g),
+                              _ptr(dtopk_w), _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_bwd_routed")
 
 
 def moe_get_status(plan: Plan, workspace, stream=None) -> int:

@@ -14,6 +14,7 @@
 namespace moe {
 cudaError_t launch_router(const RouterMaps& maps, const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_schedule(const FwdParams& p, cudaStream_t stream);
+cudaError_t launch_given_routes(const FwdParams& p, const int* topk_idx, const float* topk_w, cudaStream_t stream);
 cudaError_t launch_megakernel(const TensorMaps& maps, const FwdParams& p, int grid, cudaStream_t stream);
 int megakernel_smem_bytes();
 int megakernel_pair_max_ctas(bool mx);
@@ -306,12 +307,17 @@ int moe_quantize_mxfp8(const moe_plan* plan, const void* W, int64_t rows, int64_
              : MOE_ERR_CUDA;
 }
 
-int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const moe_outputs* o,
-            void* workspace, size_t workspace_bytes, moe_stream_t stream_) {
-  if (!pl || !w || !o || T < 0 || T > pl->cfg.T_max) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
+}  // extern "C"
+
+namespace {
+
+// The forward; with `idx` and `wt` the routing is given and the router kernel
+// is replaced by one that takes it over.
+int forward(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const int32_t* idx, const float* wt,
+            const moe_outputs* o, void* workspace, size_t workspace_bytes, moe_stream_t stream_) {
+  const bool given = idx != nullptr;
   const moe_config& c = pl->cfg;
-  if (!x || !w->W_router || !w->W_up || !w->W_gate || !w->W_down || !o->out || !workspace)
+  if (!x || (!given && !w->W_router) || !w->W_up || !w->W_gate || !w->W_down || !o->out || !workspace)
     return MOE_ERR_INVALID_ARG;
   const bool shared = w->Ws_up || w->Ws_gate || w->Ws_down;
   if (shared && (!w->Ws_up || !w->Ws_gate || !w->Ws_down || c.I_s == 0)) return MOE_ERR_INVALID_ARG;
@@ -319,7 +325,7 @@ int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, 
   if (mx && (!w->W_up_scale || !w->W_gate_scale || !w->W_down_scale)) return MOE_ERR_INVALID_ARG;
   if (mx && (!aligned16(w->W_up_scale) || !aligned16(w->W_gate_scale) || !aligned16(w->W_down_scale)))
     return MOE_ERR_INVALID_ARG;
-  const void* ptrs[] = {x, w->W_router, w->W_up, w->W_gate, w->W_down, o->out, workspace};
+  const void* ptrs[] = {x, given ? x : w->W_router, w->W_up, w->W_gate, w->W_down, o->out, workspace};
   for (const void* p : ptrs)
     if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
   if (shared && (!aligned16(w->Ws_up) || !aligned16(w->Ws_gate) || !aligned16(w->Ws_down))) return MOE_ERR_INVALID_ARG;
@@ -370,7 +376,7 @@ int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, 
   p.plain_launch = c.plain_launch;
   p.half_tiles = c.mma_pair && c.precision == MOE_PREC_BF16 && !c.pad_odd_tiles ? 1 : 0;
   p.x = static_cast<const bf16*>(x);
-  p.b_router = w->b_router;
+  p.b_router = given ? nullptr : w->b_router;
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.stamps = reinterpret_cast<unsigned long long*>(ws + L.status + 8);
   p.counters = reinterpret_cast<int*>(ws + L.counters);
@@ -418,7 +424,7 @@ int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, 
   const uint32_t down_box = c.mma_pair ? 128u : (uint32_t)BN_DOWN;  // pairs: each CTA loads half the columns
   int rc = MOE_OK;
   rc |= encode_bf16_2d(pl, &rm.x, x, T, c.D, BM);
-  rc |= encode_bf16_2d(pl, &rm.wr, w->W_router, c.E, c.D, wr_box);
+  if (!given) rc |= encode_bf16_2d(pl, &rm.wr, w->W_router, c.E, c.D, wr_box);
   rc |= encode_bf16_2d(pl, &tm.x, x, T, c.D, BM);
   if (p.direct) {  // one-row boxes for tile::gather4 from x (bf16) or its E4M3 copy
     if (mx)
@@ -461,7 +467,7 @@ int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, 
   if (rc != MOE_OK) return MOE_ERR_INVALID_ARG;
 
   if (pl->timed && cudaEventRecord(pl->timing[0], stream) != cudaSuccess) return MOE_ERR_CUDA;
-  if (launch_router(rm, p, stream) != cudaSuccess) return MOE_ERR_CUDA;
+  if ((given ? launch_given_routes(p, idx, wt, stream) : launch_router(rm, p, stream)) != cudaSuccess) return MOE_ERR_CUDA;
   if (pl->timed && cudaEventRecord(pl->timing[1], stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (launch_schedule(p, stream) != cudaSuccess) return MOE_ERR_CUDA;
   if (pl->timed && cudaEventRecord(pl->timing[2], stream) != cudaSuccess) return MOE_ERR_CUDA;
@@ -479,13 +485,37 @@ int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, 
   return MOE_OK;
 }
 
+}  // namespace
+
+extern "C" {
+
+int moe_fwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const moe_outputs* o,
+            void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  if (!pl || !w || !o || T < 0 || T > pl->cfg.T_max) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  return forward(pl, T, x, w, nullptr, nullptr, o, workspace, workspace_bytes, stream);
+}
+
+int moe_fwd_routed(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const int32_t* topk_idx,
+                   const float* topk_w, const moe_outputs* o, void* workspace, size_t workspace_bytes,
+                   moe_stream_t stream) {
+  if (!pl || !w || !o || T < 0 || T > pl->cfg.T_max) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!topk_idx || !topk_w || (reinterpret_cast<uintptr_t>(topk_idx) & 3u) || (reinterpret_cast<uintptr_t>(topk_w) & 3u))
+    return MOE_ERR_INVALID_ARG;
+  return forward(pl, T, x, w, topk_idx, topk_w, o, workspace, workspace_bytes, stream);
+}
+
 int moe_get_status(const moe_plan* plan, const void* workspace, int* device_status, moe_stream_t stream) {
   if (!plan || !workspace || !device_status) return MOE_ERR_INVALID_ARG;
   int v[2] = {0, 0};  // the status word and the warning bits after it
   if (cudaMemcpyAsync(v, workspace, sizeof(v), cudaMemcpyDeviceToHost, (cudaStream_t)stream) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
-  *device_status = v[0] != STATUS_OK ? v[0] : ((v[1] & FLAG_STAGING_OVERFLOW) ? MOE_STATUS_STAGING_OVERFLOW : MOE_STATUS_OK);
+  *device_status = v[0] != STATUS_OK                    ? v[0]
+                   : (v[1] & FLAG_ROUTES_INVALID)       ? MOE_STATUS_SCHEDULE_INVALID
+                   : (v[1] & FLAG_STAGING_OVERFLOW)     ? MOE_STATUS_STAGING_OVERFLOW
+                                                        : MOE_STATUS_OK;
   return MOE_OK;
 }
 

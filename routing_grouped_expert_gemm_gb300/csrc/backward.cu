@@ -97,7 +97,8 @@ struct BwdParams {
   // inputs
   const bf16* x;
   const bf16* dO;
-  const bf16* w_router;
+  const bf16* w_router;   // NULL: the routing was given, the router has no gradient here
+  float* dtopk_w;         // ... but its weights have
   // workspace
   int* status;
   int* counters;          // [0] phase-A claims, [1] phase-B claims
@@ -859,6 +860,10 @@ __global__ void __launch_bounds__(256) bwd_router_dl(BwdParams p) {
     g = p.topk_w[j];
     if (p.score_fn == MOE_SCORE_SIGMOID) sv = 1.0f / (1.0f + expf(-p.topk_logit[j]));
   }
+  if (p.dtopk_w) {  // the routing was given (its empty slots are marked in topk_logit)
+    if (on) p.dtopk_w[j] = p.topk_logit[j] != 0.0f ? 0.0f : dg;
+    return;
+  }
   const float c = warp_sum_bfly(on ? g * dg : 0.0f);
   float dl;
   if (p.score_fn == MOE_SCORE_SIGMOID) {
@@ -946,7 +951,7 @@ __global__ void __launch_bounds__(256) bwd_dx_combine(BwdParams p) {
   int ex[TOPK_MAX];
 #pragma unroll
   for (int s = 0; s < TOPK_MAX; ++s) {
-    dl[s] = s < p.k ? p.dl[(size_t)t * p.k + s] : 0.0f;
+    dl[s] = s < p.k && p.w_router ? p.dl[(size_t)t * p.k + s] : 0.0f;
     ex[s] = s < p.k ? p.topk_idx[(size_t)t * p.k + s] : 0;
   }
   const __half* ys = p.dxs + (size_t)t * p.kY * p.D;
@@ -964,7 +969,7 @@ __global__ void __launch_bounds__(256) bwd_dx_combine(BwdParams p) {
     };
     if (sh) add_f16(ys + (size_t)p.k * p.D);
     for (int s = 0; s < p.k; ++s) add_f16(ys + (size_t)s * p.D);
-    for (int s = 0; s < p.k; ++s) {
+    for (int s = 0; s < (p.w_router ? p.k : 0); ++s) {
       const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.w_router + (size_t)ex[s] * p.D) + v);
       const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
 #pragma unroll
@@ -1072,11 +1077,13 @@ extern "C" size_t moe_bwd_workspace_bytes(const moe_plan* plan, int64_t T) {
   return bwd_layout(plan->cfg, T).total;
 }
 
-extern "C" int moe_bwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const void* dO,
-                       const void* fwd_workspace, const moe_grads* gr, void* workspace, size_t workspace_bytes,
-                       moe_stream_t stream_) {
-  if (!pl || !w || !gr || T < 0 || T > pl->cfg.T_max) return MOE_ERR_INVALID_ARG;
-  if (T == 0) return MOE_OK;
+namespace {
+
+// The backward; with `dtopk_w` after a forward whose routing was given.
+int backward(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const void* dO,
+             const void* fwd_workspace, const moe_grads* gr, float* dtopk_w, void* workspace, size_t workspace_bytes,
+             moe_stream_t stream_) {
+  const bool given = dtopk_w != nullptr;
   const moe_config& c = pl->cfg;
   if (!bwd_shape_ok(c)) return MOE_ERR_UNSUPPORTED_SHAPE;
   const bool shared = w->Ws_up || w->Ws_gate || w->Ws_down;
@@ -1084,8 +1091,8 @@ extern "C" int moe_bwd(const moe_plan* pl, int64_t T, const void* x, const moe_w
   if (shared != (gr->dWs_up != nullptr) || (gr->dWs_up != nullptr) != (gr->dWs_gate != nullptr) ||
       (gr->dWs_up != nullptr) != (gr->dWs_down != nullptr))
     return MOE_ERR_INVALID_ARG;
-  const void* req[] = {x, dO, fwd_workspace, workspace, w->W_router, w->W_up, w->W_gate, w->W_down,
-                       gr->dx, gr->dW_router, gr->dW_up, gr->dW_gate, gr->dW_down};
+  const void* req[] = {x, dO, fwd_workspace, workspace, given ? x : w->W_router, w->W_up, w->W_gate, w->W_down,
+                       gr->dx, given ? gr->dx : gr->dW_router, gr->dW_up, gr->dW_gate, gr->dW_down};
   for (const void* q : req)
     if (!q || !al16(q)) return MOE_ERR_INVALID_ARG;
   if (shared) {
@@ -1128,7 +1135,8 @@ extern "C" int moe_bwd(const moe_plan* pl, int64_t T, const void* x, const moe_w
   p.sched = fv.sched;
   p.x = static_cast<const bf16*>(x);
   p.dO = static_cast<const bf16*>(dO);
-  p.w_router = static_cast<const bf16*>(w->W_router);
+  p.w_router = given ? nullptr : static_cast<const bf16*>(w->W_router);
+  p.dtopk_w = dtopk_w;
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.counters = reinterpret_cast<int*>(ws + L.counters);
   p.meta = reinterpret_cast<int*>(ws + L.meta);
@@ -1255,9 +1263,30 @@ extern "C" int moe_bwd(const moe_plan* pl, int64_t T, const void* x, const moe_w
   bwd_router_dl<<<tok_blocks, 256, 0, st>>>(p);
   ok = ok && gemm(1) == cudaSuccess;
   ok = ok && mark(3);
-  bwd_router_wr<<<(unsigned)L.n_wc_max, 256, 0, st>>>(p);
-  bwd_router_fin<<<(unsigned)c.E, 256, 0, st>>>(p);
+  if (!given) {
+    bwd_router_wr<<<(unsigned)L.n_wc_max, 256, 0, st>>>(p);
+    bwd_router_fin<<<(unsigned)c.E, 256, 0, st>>>(p);
+  }
   bwd_dx_combine<<<tok_blocks, 256, 0, st>>>(p);
   ok = ok && mark(4);
   return ok && cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" int moe_bwd(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const void* dO,
+                       const void* fwd_workspace, const moe_grads* gr, void* workspace, size_t workspace_bytes,
+                       moe_stream_t stream) {
+  if (!pl || !w || !gr || T < 0 || T > pl->cfg.T_max) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  return backward(pl, T, x, w, dO, fwd_workspace, gr, nullptr, workspace, workspace_bytes, stream);
+}
+
+extern "C" int moe_bwd_routed(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, const void* dO,
+                              const void* fwd_workspace, const moe_grads* gr, float* dtopk_w, void* workspace,
+                              size_t workspace_bytes, moe_stream_t stream) {
+  if (!pl || !w || !gr || T < 0 || T > pl->cfg.T_max) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!dtopk_w || (reinterpret_cast<uintptr_t>(dtopk_w) & 3u) != 0) return MOE_ERR_INVALID_ARG;
+  return backward(pl, T, x, w, dO, fwd_workspace, gr, dtopk_w, workspace, workspace_bytes, stream);
 }

@@ -55,7 +55,7 @@ constexpr int E_MAX = 512;
 enum : int { STATUS_OK = 0, STATUS_TIMEOUT = 1, STATUS_SCHEDULE_INVALID = 2 };
 // sticky warning bits in the word after the status word: they do not stop the
 // forward (the status word does), they only qualify its result
-enum : int { FLAG_STAGING_OVERFLOW = 1 };
+enum : int { FLAG_STAGING_OVERFLOW = 1, FLAG_ROUTES_INVALID = 2 };
 
 // phase stamps of one persistent-kernel launch (ns of %globaltimer), for
 // per-phase bandwidth figures: the first CTA's start, the last ring fill, the

@@ -935,6 +935,100 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __gri
   }
 }
 
+// ------------------------------------------------------------------ routing given to the layer
+// What the built-in router leaves for the schedule, from a given routing: the
+// experts and weights of every slot, the route histogram of every 128-token
+// chunk, and the persistent kernel's counters and stamps as they start.  One
+// thread per token.  Every slot gets an expert of its own, since the layer
+// takes k distinct routes per token: an empty slot (or one whose index is out
+// of range or a repetition) the lowest expert that the token does not use,
+// with weight 0 and a mark in topk_logit.
+__global__ void __launch_bounds__(BM) given_routes_kernel(const __grid_constant__ FwdParams p, const int* idx, const float* wt) {
+  __shared__ int s_hist[E_MAX];
+  const int t = blockIdx.x * BM + threadIdx.x;
+  for (int i = blockIdx.x * BM + threadIdx.x; i < p.n_counters; i += gridDim.x * BM) p.counters[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.stamps) {
+    p.stamps[STAMP_START] = p.stamps[STAMP_COMBINE_START] = ~0ull;
+    p.stamps[STAMP_LAST_FILL] = p.stamps[STAMP_COMBINE_END] = 0ull;
+  }
+  for (int e = threadIdx.x; e < p.E; e += BM) s_hist[e] = 0;
+  __syncthreads();
+  if (t < p.T) {
+    int ex[TOPK_MAX];
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < TOPK_MAX; ++s) {
+      ex[s] = -1;
+      if (s < p.k) {
+        const int e = idx[(size_t)t * p.k + s];
+        bool ok = e >= 0 && e < p.E;
+        bad |= !ok && e != -1;
+#pragma unroll
+        for (int q = 0; q < s; ++q)
+          if (ok && ex[q] == e) ok = false, bad = true;
+        ex[s] = ok ? e : -1;
+      }
+    }
+    int next = 0;  // the lowest expert not looked at yet (k <= E: one is always left)
+#pragma unroll
+    for (int s = 0; s < TOPK_MAX; ++s) {
+      if (s >= p.k) break;
+      const bool fill = ex[s] < 0;
+      if (fill) {
+        for (bool used = true; used; ++next) {
+          used = false;
+#pragma unroll
+          for (int q = 0; q < TOPK_MAX; ++q) used |= ex[q] == next;
+        }
+        ex[s] = next - 1;
+      }
+      const size_t o = (size_t)t * p.k + s;
+      p.topk_idx[o] = ex[s];
+      p.topk_w[o] = fill ? 0.0f : wt[o];
+      p.topk_logit[o] = fill ? 1.0f : 0.0f;
+      atomicAdd(&s_hist[ex[s]], 1);
+    }
+    if (bad) atomicOr(p.status + 1, FLAG_ROUTES_INVALID);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += BM) p.chunk_counts[(size_t)blockIdx.x * p.E + e] = s_hist[e];
+}
+
+// MXFP8 plans: x in 32-element blocks (OCP MX E4M3 codes, E8M0 scales), as the
+// router pass leaves it; a thread per block.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const bf16* x, int64_t blocks, uint8_t* xq, uint8_t* xs) {
+  for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < blocks; b += (int64_t)gridDim.x * blockDim.x) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(x + b * 32) + i);
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __bfloat1622float2(h[j]);
+        v[8 * i + 2 * j] = f.x;
+        v[8 * i + 2 * j + 1] = f.y;
+      }
+    }
+    uint32_t c[8];
+    xs[b] = (uint8_t)mx_quantize32(v, c);
+    uint4* d = reinterpret_cast<uint4*>(xq + b * 32);
+    d[0] = make_uint4(c[0], c[1], c[2], c[3]);
+    d[1] = make_uint4(c[4], c[5], c[6], c[7]);
+  }
+}
+
+cudaError_t launch_given_routes(const FwdParams& p, const int* topk_idx, const float* topk_w, cudaStream_t stream) {
+  cudaError_t err = cudaMemsetAsync(p.status, 0, 2 * sizeof(int), stream);  // status and warning bits
+  if (err != cudaSuccess) return err;
+  given_routes_kernel<<<p.n_chunks, BM, 0, stream>>>(p, topk_idx, topk_w);
+  err = cudaGetLastError();
+  if (err != cudaSuccess || !p.xq) return err;
+  const int64_t blocks = (int64_t)p.T * p.D / 32, grid = (blocks + 255) / 256;
+  quantize_rows_kernel<<<(unsigned)(grid < 152 * 16 ? grid : 152 * 16), 256, 0, stream>>>(p.x, blocks, p.xq, p.xs);
+  return cudaGetLastError();
+}
+
 }  // namespace moe
 
 // ------------------------------------------------------------------ C ABI
