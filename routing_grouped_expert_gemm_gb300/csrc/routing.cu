@@ -36,7 +36,7 @@
 namespace moe {
 
 constexpr int ROUTE_WARPS = 8;          // rows in flight per CTA
-constexpr int ROUTE_CTAS_PER_SM = 3;    // of the persistent grid that sums over tokens
+constexpr int route_ctas_per_sm(int V) { return V <= 8 ? 3 : 2; }  // what registers allow
 constexpr float ROUTE_TINY = 1e-36f;    // keys below this have lost their relative precision (fp32 underflow)
 
 struct RouteParams {
@@ -133,11 +133,6 @@ __device__ __forceinline__ float sum32(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float sum16(float v) {  // both halves of the warp alike
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 __device__ __forceinline__ float max32(float v) {  // NaN operands are passed over
   return ord_to(__reduce_max_sync(0xffffffffu, ord_of(v == v ? v : -INFINITY)));
 }
@@ -207,10 +202,11 @@ __device__ __forceinline__ double key64(const RouteParams& p, const void* row, i
 // to be decided by the candidates' keys (bits of this lane's experts, which
 // hold the largest of every such group).  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row, uint32_t cand, int state, int* buf) {
+__device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* row, uint32_t cand, int state, float m32,
+                                             int* buf) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
-  double m = 0.0, z = 1.0;
-  if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
+  double m = m32, z = 1.0;
+  if (kSoft && p.bias) softmax_stats64<V>(p, row, lane, &m, &z);  // (without a bias the row's sum cancels)
   unsigned long long score = state == 2 ? ~0ull : 0ull, best1 = 0, best2 = 0;  // lane g: of group g so far
   // the candidates, one per lane, 32 at a time
   int before = __popc(cand);
@@ -255,19 +251,35 @@ __device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* r
 }
 
 // Whether this lane's candidate (expert e, -1 for none; ids ascend with the
-// lanes) is one of the `need` with the largest keys.  Whole warp.
+// lanes) is one of the `need` with the largest keys.  Softmax: z32, the row's
+// sum in fp32 (off by less than 2^-20), scales all of the candidates' scores
+// alike, so it decides unless the border is within 2^-20 of how far they lie
+// apart; the sum in fp64 costs more than all the rest.  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, int e, int need) {
+__device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, int e, int need, float m32, float z32) {
   const int lane = threadIdx.x & 31;
-  double m = 0.0, z = 1.0;
-  if (kSoft) softmax_stats64<V>(p, row, lane, &m, &z);
-  const unsigned long long key = e >= 0 ? ord_of64(key64<kSoft>(p, row, e, m, z)) : 0ull;
-  int rank = 0;
-  for (int i = 0; i < 32; ++i) {
-    const unsigned long long v = __shfl_sync(0xffffffffu, key, i);
-    rank += (v > key || (v == key && i < lane)) ? 1 : 0;
+  double m = m32, z = z32;
+  bool in = false;
+  for (int pass = 0; pass < (kSoft ? 2 : 1); ++pass) {
+    if (pass == 1) softmax_stats64<V>(p, row, lane, &m, &z);
+    const double k = e >= 0 ? key64<kSoft>(p, row, e, m, z) : -INFINITY;
+    const unsigned long long key = e >= 0 ? ord_of64(k) : 0ull;
+    int rank = 0;
+    for (unsigned left = __ballot_sync(0xffffffffu, e >= 0); left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const unsigned long long v = __shfl_sync(0xffffffffu, key, i);
+      rank += (v > key || (v == key && i < lane)) ? 1 : 0;
+    }
+    in = e >= 0 && rank < need;
+    if (kSoft && pass == 0) {
+      const float s32 = e >= 0 ? (float)(k - (p.bias ? (double)p.bias[e] : 0.0)) : 0.0f;
+      const float far = max32(e >= 0 ? s32 : -INFINITY) + max32(e >= 0 ? -s32 : -INFINITY);  // largest less smallest
+      const double lo = ord_to64(~max32_64(in ? ~key : 0ull));
+      const unsigned long long out = max32_64(e >= 0 && !in ? key : 0ull);
+      if (!out || lo - ord_to64(out) > 9.6e-7 * (double)far + 1e-15) break;
+    }
   }
-  return e >= 0 && rank < need;
+  return in;
 }
 // The same for candidates as bits of each lane's experts.
 template <int V, bool kSoft>
@@ -309,7 +321,7 @@ __device__ __noinline__ uint32_t wide_band_fp64(const RouteParams& p, const void
 // two sides.  Softmax: (m - x + 3) 2^-24, at most 104 before e^x is flushed,
 // the row sum and its reciprocal: below 2^-16 as well.
 template <int V, bool kSoft>
-__global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_kernel(const __grid_constant__ RouteParams p) {
   constexpr float REL = 1.0f / 65536;
   __shared__ int s_hist[E_MAX];
   __shared__ __align__(16) uint32_t s_key[ROUTE_WARPS][32];  // candidates: key and expert
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
               cand |= key[j] > ORD_NONE && v >= from ? 1u << j : 0u;
             }
             // (lane g: 2 its group is in, 0 it is out, 1 to be decided)
-            kept = groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, s_id[warp]);
+            kept = groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, m, s_id[warp]);
           }
         }
       }
@@ -620,7 +632,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, V <= 8 ? 3 : 2) route_kernel
           const float rx = __shfl_sync(0xffffffffu, xe, first), rb = __shfl_sync(0xffffffffu, be, first);
           if (__any_sync(0xffffffffu, close && (xe != rx || be != rb))) {
             in = in && !close;
-            in |= band_fp64<V, kSoft>(p, row, close ? e : -1, p.k - __popc(__ballot_sync(0xffffffffu, in)));
+            in |= band_fp64<V, kSoft>(p, row, close ? e : -1, p.k - __popc(__ballot_sync(0xffffffffu, in)), m, z);
             who = __ballot_sync(0xffffffffu, in);
           }
         }
@@ -768,13 +780,10 @@ __global__ void __launch_bounds__(1024) route_sums_kernel(const int* pc, const f
   float f = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (e < E) {
-    if (pc) {
 #pragma unroll 8
-      for (int i = warp; i < n; i += 32) c += pc[(size_t)i * E + e];
-    }
-    if (pp) {
-#pragma unroll 8
-      for (int i = warp; i < n; i += 32) f += pp[(size_t)i * E + e];
+    for (int i = warp; i < n; i += 32) {
+      if (pc) c += pc[(size_t)i * E + e];
+      if (pp) f += pp[(size_t)i * E + e];
     }
   }
   s_c[warp][lane] = c;
@@ -799,6 +808,7 @@ struct RouteBwdParams {
   void* dlogits;
   int64_t ld, dld, T;
   int E, k, dtype, vec, dvec, renorm;
+  int rows, ks;  // as in RouteParams
   float scale;
   const int* topk_idx;
   const float* dtopk_w;
@@ -811,15 +821,18 @@ struct RouteBwdParams {
 //   sigmoid: dx_e = (a_e + c_e) (1 - s_e)
 //   softmax: dx_e = a_e + c_e, less s_e sum_i a_i where not renormalised
 // (a and c are ds_e times s_e, so nothing is divided by a small score.)
-// A row is read once and written once; the selected experts' terms, one per
-// lane, meet the row's through shared memory.  Renormalised weights without
+// A row is read once and written once.  The selected experts' terms are made
+// for several rows at once, one lane per slot (32 >> ks rows), and meet the
+// row's through shared memory.  Renormalised weights, and sigmoid ones, without
 // prob_sum need the selected logits only, so the row itself is not read.
 template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __grid_constant__ RouteBwdParams p) {
   __shared__ __align__(16) float s_a[ROUTE_WARPS][32 * V];
+  __shared__ float s_ai[ROUTE_WARPS][32];
+  __shared__ int s_e[ROUTE_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const bool sums = p.dprob_sum != nullptr, dense = sums || (kSoft && !p.renorm);
-  const int size = p.dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  const int size = p.dtype == MOE_DTYPE_FP32 ? 4 : 2, slots = 1 << p.ks;
   float* a = s_a[warp];
   float d[V];
 #pragma unroll
@@ -828,110 +841,150 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __gri
     d[j] = sums && e0 + j < p.E ? p.dprob_sum[e0 + j] : 0.0f;
   }
   __syncwarp();
-  for (int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + warp; t < p.T; t += (int64_t)gridDim.x * ROUTE_WARPS) {
-    const void* row = static_cast<const uint8_t*>(p.logits) + (size_t)t * p.ld * size;
-    float x[V], s[V], c1[V];  // c1: 1 - s
-    int e = -1;
-    float dw = 0.0f, xs = -INFINITY;
-    if (lane < p.k) {
-      e = p.topk_idx[t * p.k + lane];
-      if (e < 0 || e >= p.E) e = -1;
-    }
-    if (e >= 0) {
-      dw = p.dtopk_w[t * p.k + lane] * p.scale;
-      xs = load_logit(row, p.dtype, e);
-    }
-    float m = 0.0f, z = 1.0f;
-    bool shifted = false;
-    if (dense) {
-      load_row<V>(row, p.dtype, p.vec, lane, p.E, x);
-      float lm = -INFINITY, lz = 0.0f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) lm = fmaxf(lm, x[j]);
-      m = max32(lm);
-      shifted = kSoft || (m < -20.0f && m > -INFINITY);  // sigmoid = e^x there: its share without underflow
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float y = exp2_fast(-fabsf(x[j]) * LOG2E), r = rcp_fast(1.0f + y);  // e^-|x|: both s and 1 - s keep their bits
-        if (!kSoft) c1[j] = x[j] >= 0.0f ? y * r : r;
-        s[j] = shifted ? (x[j] == m ? 1.0f : exp2_fast((x[j] - m) * LOG2E)) : x[j] >= 0.0f ? r : y * r;
-        if (x[j] == -INFINITY) s[j] = 0.0f;
-        lz += s[j];
+  const int64_t t_from = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * p.rows, t_to = min(t_from + p.rows, p.T);
+  for (int64_t tb = t_from; tb < t_to; tb += 32 >> p.ks) {
+    const int n_rows = (int)min((int64_t)(32 >> p.ks), t_to - tb);
+    {  // the selected experts' a (softmax not renormalised: dw, the row's scores follow below)
+      const int r = lane >> p.ks, slot = lane & (slots - 1);
+      int e = -1;
+      float dw = 0.0f, xs = -INFINITY;
+      if (r < n_rows && slot < p.k) {
+        e = p.topk_idx[(tb + r) * p.k + slot];
+        if (e < 0 || e >= p.E) e = -1;
       }
-      z = sum32(lz);
-    }
-    const float inv_z = z == 0.0f ? 0.0f : 1.0f / z;
-
-    // the selected experts' terms
-    float ai = 0.0f;
-    if (p.renorm) {
-      const float ms = max32(xs);
-      float q = 0.0f;
-      if (e >= 0 && !(xs == -INFINITY)) q = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
-      const float tot = sum16(q);
-      q = tot == 0.0f ? 0.0f : q / tot;
-      ai = q * (dw - sum16(q * dw));
-    } else if (e >= 0 && !(xs == -INFINITY)) {
-      ai = dw * (kSoft ? expf(below(xs, m)) * inv_z : 1.0f / (1.0f + expf(-xs)));
-    }
-    const float asum = kSoft && !p.renorm ? sum32(ai) : 0.0f;
-    if (!kSoft && e >= 0 && !dense) ai *= 1.0f / (1.0f + expf(xs));  // 1 - s
-    if (e >= 0) a[e] = ai;
-    __syncwarp();
-
-    float o[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = a[e0 + j];
-    if (dense) {
-      float ld = 0.0f;
-      if (sums) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) ld += s[j] * d[j];
-        ld = sum32(ld) * inv_z;
+      if (e >= 0) {
+        dw = p.dtopk_w[(tb + r) * p.k + slot] * p.scale;
+        xs = load_logit(static_cast<const uint8_t*>(p.logits) + (size_t)(tb + r) * p.ld * size, p.dtype, e);
       }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float pe = s[j] * inv_z;
-        o[j] -= kSoft ? pe * asum : 0.0f;
-        if (sums) o[j] += pe * (d[j] - ld);
-        if (!kSoft) o[j] *= c1[j];
-        if (x[j] == -INFINITY) o[j] = 0.0f;
+      const bool on = e >= 0 && !(xs == -INFINITY);
+      float ai = 0.0f;
+      if (p.renorm) {
+        float ms = xs;
+        for (int o = slots >> 1; o > 0; o >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o));
+        float q = 0.0f;
+        if (on) q = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
+        float tot = q;
+        for (int o = slots >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+        q = tot == 0.0f ? 0.0f : __fdividef(q, tot);
+        float qd = q * dw;
+        for (int o = slots >> 1; o > 0; o >>= 1) qd += __shfl_xor_sync(0xffffffffu, qd, o);
+        ai = q * (dw - qd);
+      } else if (on) {
+        ai = kSoft ? dw : dw / (1.0f + expf(-xs));
       }
+      if (!kSoft && !dense && on) ai /= 1.0f + expf(xs);  // times 1 - s
+      s_ai[warp][lane] = ai;
+      s_e[warp][lane] = e;
+      __syncwarp();
     }
-    // one rounding to the logits' type
-    uint8_t* out = static_cast<uint8_t*>(p.dlogits) + (size_t)t * p.dld * size;
-    if (p.dtype == MOE_DTYPE_FP32) {
-      float* dst = reinterpret_cast<float*>(out) + e0;
-      if (V % 4 == 0 && p.dvec && e0 + V <= p.E) {
+    for (int r = 0; r < n_rows; ++r) {
+      const int64_t t = tb + r;
+      const int e = lane < p.k ? s_e[warp][(r << p.ks) + lane] : -1;
+      if (e >= 0) a[e] = s_ai[warp][(r << p.ks) + lane];
+      __syncwarp();
+      float o[V];
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-          reinterpret_cast<float4*>(dst)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      for (int j = 0; j < V; ++j) o[j] = a[e0 + j];
+      if (dense) {
+        float x[V], s[V], c1[V];  // c1: 1 - s
+        load_row<V>(static_cast<const uint8_t*>(p.logits) + (size_t)t * p.ld * size, p.dtype, p.vec, lane, p.E, x);
+        auto row_max = [&]() {
+          float lm = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < V; ++j) lm = fmaxf(lm, x[j]);
+          return max32(lm);
+        };
+        float z = 0.0f;
+        if (kSoft) {
+          const float m = row_max();
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            s[j] = x[j] == m ? 1.0f : exp2_fast((x[j] - m) * LOG2E);
+            if (x[j] == -INFINITY) s[j] = 0.0f;
+            z += s[j];
+          }
+          z = sum32(z);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float y = exp2_fast(-fabsf(x[j]) * LOG2E), h = rcp_fast(1.0f + y);  // e^-|x|: s and 1 - s keep their bits
+            s[j] = x[j] >= 0.0f ? h : y * h;
+            c1[j] = x[j] >= 0.0f ? y * h : h;
+            z += s[j];
+          }
+          z = sum32(z);
+          if (z < 1e-6f) {  // scores that may underflow: e^x there, so the share is softmax's
+            const float m = row_max();
+            if (m < -20.0f && m > -INFINITY) {
+              z = 0.0f;
+#pragma unroll
+              for (int j = 0; j < V; ++j) {
+                s[j] = exp2_fast((x[j] - m) * LOG2E);
+                z += s[j];
+              }
+              z = sum32(z);
+            }
+          }
+        }
+        const float inv_z = z == 0.0f ? 0.0f : rcp_fast(z);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] *= inv_z;  // normalised
+        if (kSoft && !p.renorm) {
+          float asum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < V; ++j) asum += o[j] * s[j];
+          asum = sum32(asum);
+#pragma unroll
+          for (int j = 0; j < V; ++j) o[j] = s[j] * (o[j] - asum);
+        }
+        if (sums) {
+          float ld = 0.0f;
+#pragma unroll
+          for (int j = 0; j < V; ++j) ld += s[j] * d[j];
+          ld = sum32(ld);
+#pragma unroll
+          for (int j = 0; j < V; ++j) o[j] += s[j] * (d[j] - ld);
+        }
+        if (!kSoft) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) o[j] *= c1[j];
+        }
+      }
+      // one rounding to the logits' type
+      uint8_t* out = static_cast<uint8_t*>(p.dlogits) + (size_t)t * p.dld * size;
+      if (p.dtype == MOE_DTYPE_FP32) {
+        float* dst = reinterpret_cast<float*>(out) + e0;
+        if (V % 4 == 0 && p.dvec && e0 + V <= p.E) {
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<float4*>(dst)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (e0 + j < p.E) dst[j] = o[j];
+        }
       } else {
+        uint16_t h[V + 1];
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          if (e0 + j < p.E) dst[j] = o[j];
+          h[j] = p.dtype == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[j]))
+                                           : __half_as_ushort(__float2half_rn(o[j]));
+        uint16_t* dst = reinterpret_cast<uint16_t*>(out) + e0;
+        if (V % 4 == 0 && p.dvec && e0 + V <= p.E) {
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i)
+            reinterpret_cast<uint2*>(dst)[i] = make_uint2((uint32_t)h[4 * i] | ((uint32_t)h[4 * i + 1] << 16),
+                                                          (uint32_t)h[4 * i + 2] | ((uint32_t)h[4 * i + 3] << 16));
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (e0 + j < p.E) dst[j] = h[j];
+        }
       }
-    } else {
-      uint16_t h[V + 1];
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        h[j] = p.dtype == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(o[j]))
-                                         : __half_as_ushort(__float2half_rn(o[j]));
-      uint16_t* dst = reinterpret_cast<uint16_t*>(out) + e0;
-      if (V % 4 == 0 && p.dvec && e0 + V <= p.E) {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-          reinterpret_cast<uint2*>(dst)[i] = make_uint2((uint32_t)h[4 * i] | ((uint32_t)h[4 * i + 1] << 16),
-                                                        (uint32_t)h[4 * i + 2] | ((uint32_t)h[4 * i + 3] << 16));
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (e0 + j < p.E) dst[j] = h[j];
-      }
+      __syncwarp();
+      if (e >= 0) a[e] = 0.0f;
+      __syncwarp();
     }
-    __syncwarp();
-    if (e >= 0) a[e] = 0.0f;
-    __syncwarp();
   }
 }
 
@@ -1047,7 +1100,7 @@ bool route_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t
 // CTAs of a forward over T rows: enough for every row, at most what the GPU
 // keeps resident (each CTA's sums over its rows are one partial result)
 int64_t route_grid(const moe_route_plan* pl, int64_t T) {
-  const int64_t need = (T + ROUTE_WARPS - 1) / ROUTE_WARPS, most = (int64_t)pl->num_sms * ROUTE_CTAS_PER_SM;
+  const int64_t need = (T + ROUTE_WARPS - 1) / ROUTE_WARPS, most = (int64_t)pl->num_sms * route_ctas_per_sm((int)(pl->cfg.E + 31) / 32);
   return need < most ? need : most;
 }
 
@@ -1218,8 +1271,10 @@ int moe_route_bwd(const moe_route_plan* pl, int64_t T, const void* logits, int64
   p.dtopk_w = dtopk_w;
   p.dprob_sum = dprob_sum;
   int64_t grid = (T + ROUTE_WARPS - 1) / ROUTE_WARPS;
-  const int64_t most = (int64_t)pl->num_sms * 8;
+  const int64_t most = (int64_t)pl->num_sms * (p.E <= 128 ? 5 : 3);  // what registers allow
   if (grid > most) grid = most;
+  p.rows = (int)((T + grid * ROUTE_WARPS - 1) / (grid * ROUTE_WARPS));
+  while ((1 << p.ks) < p.k) ++p.ks;
   auto launch = [&](auto soft) {
     return by_width(p.E, [&](auto v) {
       route_bwd_kernel<decltype(v)::value, decltype(soft)::value><<<(unsigned)grid, ROUTE_WARPS * 32, 0, stream>>>(p);
