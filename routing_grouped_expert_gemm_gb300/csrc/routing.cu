@@ -36,8 +36,9 @@
 namespace moe {
 
 constexpr int ROUTE_WARPS = 8;          // rows in flight per CTA
-constexpr int route_ctas_per_sm(int V) { return V <= 8 ? 3 : 2; }  // what registers allow
+constexpr int route_ctas_per_sm(int V) { return V <= 12 ? 3 : 2; }  // what registers allow
 constexpr float ROUTE_TINY = 1e-36f;    // keys below this have lost their relative precision (fp32 underflow)
+constexpr float ROUTE_REL = 1.0f / 65536;  // relative error of keys, see route_kernel
 
 struct RouteParams {
   const void* logits;
@@ -313,8 +314,142 @@ __device__ __noinline__ uint32_t wide_band_fp64(const RouteParams& p, const void
   return sel;
 }
 
+// This lane's V keys of a row again, from the same bits as in route_kernel
+// (-inf: not to be selected); by_score: the scores in place of x.
+template <int V, bool kSoft>
+__device__ __forceinline__ void keys_again(const RouteParams& p, const void* row, float m, float inv_z, bool by_score,
+                                           uint32_t (&key)[V]) {
+  const int e0 = (threadIdx.x & 31) * V;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float x = e0 + j < p.E ? load_logit(row, p.dtype, e0 + j) : -INFINITY;
+    float f = x + 0.0f;
+    if (p.bias || by_score) {
+      const float b = p.bias && e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
+      const float s = kSoft ? (x == m ? 1.0f : exp2_fast(fmaf(x, LOG2E, -(m * LOG2E)))) : sigmoid_fast(x);
+      f = by_score ? s : kSoft ? fmaf(s, inv_z, b) : s + b;
+    }
+    key[j] = ord_bits(x > -INFINITY && f > -INFINITY ? f : -INFINITY);
+  }
+}
+
+// Groups whose scores are too close to the border: lane g has group g's score
+// (0: none), its smaller key that counts, and whether it ranks as kept; scores
+// in [lo, hi] may lie on either side.  The kept groups, as bits.  Whole warp.
+template <int V, bool kSoft>
+__device__ __noinline__ unsigned decide_groups(const RouteParams& p, const void* row, uint32_t score, uint32_t least, bool in,
+                                               float lo, float hi, float m, float inv_z, float bmax, int* buf) {
+  const int lane = threadIdx.x & 31, e0 = lane * V;
+  uint32_t key[V], cand = 0;
+  keys_again<V, kSoft>(p, row, m, inv_z, !p.bias && p.group_top > 1, key);
+  const bool band = lane < p.n_group && score && ord_to(score) >= lo && ord_to(score) <= hi;
+  // in those groups, the keys that may be among their largest
+  uint32_t from = 0xffffffffu;
+  if (band) {
+    const float f = ord_to(least);
+    from = ord_of(f - (ROUTE_REL * (fabsf(f) + bmax) + ROUTE_TINY));
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t v = __shfl_sync(0xffffffffu, from, min((e0 + j) / p.gs, 31));
+    cand |= key[j] > ORD_NONE && key[j] >= v ? 1u << j : 0u;
+  }
+  return groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, m, buf);
+}
+
+// The k largest of a row with more than 32 candidates -- many equal keys, or
+// few lanes that hold many: one maximum after the other.  Whole warp.
+template <int V, bool kSoft>
+__device__ __noinline__ void select_wide(const RouteParams& p, const void* row, float m, float inv_z, unsigned kept, float bmax,
+                                         int* sel_out) {
+  constexpr float REL = ROUTE_REL;
+  const int lane = threadIdx.x & 31, e0 = lane * V;
+  const bool with_keys = p.bias != nullptr;
+  uint32_t key[V], a1 = 0;
+  keys_again<V, kSoft>(p, row, m, inv_z, false, key);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (key[j] <= ORD_NONE || (p.n_group > 1 && !((kept >> min((e0 + j) / p.gs, 31)) & 1u))) key[j] = 0;
+    a1 = max(a1, key[j]);
+  }
+  uint32_t kth = 0;
+  int n = 0, taken = 0;
+  for (; n < p.k; ++n) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, a1);
+    kth = best;  // (not 0: there are more than 32 candidates)
+    if (lane == __ffs(__ballot_sync(0xffffffffu, a1 == best)) - 1) {
+      ++taken;
+      int ge = 0;  // the next one of this lane, counting equal keys
+      a1 = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        ge += key[j] >= best ? 1 : 0;
+        a1 = max(a1, key[j] < best ? key[j] : 0u);
+      }
+      if (ge > taken) a1 = best;
+    }
+    __syncwarp();
+  }
+  // the selected: keys above the k-th, and as many equal ones, lowest ids first, as there is room for
+  uint32_t gt = 0, eq = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    gt |= key[j] > kth ? 1u << j : 0u;
+    eq |= key[j] == kth ? 1u << j : 0u;
+  }
+  uint32_t band = 0;
+  bool decide = false;
+  if (with_keys) {
+    const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
+    const uint32_t lo = ord_of(fk - tol), hi = ord_of(fk + tol);
+    uint32_t over = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      over |= key[j] > hi ? 1u << j : 0u;
+      band |= key[j] >= lo && key[j] <= hi ? 1u << j : 0u;
+    }
+    float lx = 0.0f, lb = 0.0f;
+    bool some = false, mixed = false;
+    for (uint32_t c = band; c; c &= c - 1) {
+      const int ee = e0 + __ffs(c) - 1;
+      const float xe = load_logit(row, p.dtype, ee), be = p.bias[ee];
+      mixed |= some && (xe != lx || be != lb);
+      lx = xe, lb = be, some = true;
+    }
+    __syncwarp();
+    const int first = __ffs(__ballot_sync(0xffffffffu, some)) - 1;
+    const float rx = __shfl_sync(0xffffffffu, lx, first), rb = __shfl_sync(0xffffffffu, lb, first);
+    decide = __any_sync(0xffffffffu, mixed || (some && (lx != rx || lb != rb)));
+    if (decide) gt = over, eq = band;
+  }
+  const int room = p.k - add32(__popc(gt));
+  uint32_t sel = gt;
+  if (decide) {
+    sel |= wide_band_fp64<V, kSoft>(p, row, eq, room);
+  } else {
+    int b4 = __popc(eq);
+    const int own = b4;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, b4, o);
+      if (lane >= o) b4 += v;
+    }
+    for (int left = room - (b4 - own); eq && left > 0; eq &= eq - 1, --left) sel |= eq & -eq;
+  }
+  __syncwarp();
+  int at = __popc(sel);
+  const int own = at;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  at -= own;
+  for (; sel; sel &= sel - 1) sel_out[at++] = e0 + __ffs(sel) - 1;
+}
+
 // ------------------------------------------------------------------ forward
-// REL: relative error of fp32 keys, both sides of a comparison together.
+// ROUTE_REL: relative error of fp32 keys, both sides of a comparison together.
 // Sigmoid: e^-x, the sum 2^-24, the reciprocal 2^-23; e^-x is off by
 // (|x| + 3) 2^-24 and weighs 1 - s: for keys above ROUTE_TINY (x > -83) below
 // 2^-17.3 of s and, with the rounding of s + b, 2^-16 (|key| + max |b|) for the
@@ -322,7 +457,7 @@ __device__ __noinline__ uint32_t wide_band_fp64(const RouteParams& p, const void
 // the row sum and its reciprocal: below 2^-16 as well.
 template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_kernel(const __grid_constant__ RouteParams p) {
-  constexpr float REL = 1.0f / 65536;
+  constexpr float REL = ROUTE_REL;
   __shared__ int s_hist[E_MAX];
   __shared__ __align__(16) uint32_t s_key[ROUTE_WARPS][32];  // candidates: key and expert
   __shared__ int s_id[ROUTE_WARPS][32];
@@ -460,6 +595,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       for (int j = 0; j < V; ++j) key[j] = ord_bits(x[j] > -INFINITY ? x[j] + 0.0f : -INFINITY);
     }
 
+    unsigned kept_groups = ~0u;
     if (grouped) {
       // each group's two largest; without a bias of the (order-keeping) scores, or, for the maximum alone, of x
       const bool by_score = group_scores && !with_keys;
@@ -532,27 +668,12 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
         if (hi) {
           const float fl = ord_to(thr), fh = ord_to(hi), tol = REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY;
           if (!(fl - fh > tol)) {
-            // groups that may lie on either side, and in them the keys that may be among their largest
-            const bool band = lane < p.n_group && score && ord_to(score) >= fh - tol && ord_to(score) <= fl + tol;
-            uint32_t least = 0xffffffffu;
-            if (band) least = p.group_top > 1 && g2 > ORD_NONE ? g2 : g1;
-            if (band) {
-              const float f = ord_to(least);
-              least = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
-            }
-            uint32_t cand = 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              const int g = aligned_groups ? (int)gid[0] : (int)((gid[j / 4] >> (8 * (j % 4))) & 31u);
-              const uint32_t from = __shfl_sync(0xffffffffu, least, g);
-              const uint32_t v = by_score ? ord_of(s[j]) : key[j];
-              cand |= key[j] > ORD_NONE && v >= from ? 1u << j : 0u;
-            }
-            // (lane g: 2 its group is in, 0 it is out, 1 to be decided)
-            kept = groups_fp64<V, kSoft>(p, row, cand, band ? 1 : in ? 2 : 0, m, s_id[warp]);
+            kept = decide_groups<V, kSoft>(p, row, score, p.group_top > 1 && g2 > ORD_NONE ? g2 : g1, in, fh - tol, fl + tol, m,
+                                           inv_z, bmax, s_id[warp]);
           }
         }
       }
+      kept_groups = kept;
       if (aligned_groups) {
         const bool keep = (kept >> gid[0]) & 1u;  // all of a lane's experts are in one group
 #pragma unroll
@@ -639,81 +760,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       }
       if (in) s_sel[warp][(r << p.ks) + __popc(who & lt)] = e;
     } else {
-      // many equal keys, or few lanes that hold many: one maximum after the other
-      uint32_t kth = 0;
-      int n = 0, taken = 0;
-      for (; n < p.k; ++n) {
-        const uint32_t best = __reduce_max_sync(0xffffffffu, a1);
-        kth = best;  // (not 0: there are more than 32 candidates)
-        if (lane == __ffs(__ballot_sync(0xffffffffu, a1 == best)) - 1) {
-          ++taken;
-          int ge = 0;  // the next one of this lane, counting equal keys
-          a1 = 0;
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            ge += key[j] >= best ? 1 : 0;
-            a1 = max(a1, key[j] < best ? key[j] : 0u);
-          }
-          if (ge > taken) a1 = best;
-        }
-        __syncwarp();
-      }
-      // the selected: keys above the k-th, and as many equal ones, lowest ids first, as there is room for
-      uint32_t gt = 0, eq = 0;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        gt |= key[j] > kth ? 1u << j : 0u;
-        eq |= key[j] == kth ? 1u << j : 0u;
-      }
-      uint32_t band = 0;
-      bool decide = false;
-      if (with_keys) {
-        const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
-        const uint32_t lo = ord_of(fk - tol), hi = ord_of(fk + tol);
-        uint32_t over = 0;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          over |= key[j] > hi ? 1u << j : 0u;
-          band |= key[j] >= lo && key[j] <= hi ? 1u << j : 0u;
-        }
-        float lx = 0.0f, lb = 0.0f;
-        bool some = false, mixed = false;
-        for (uint32_t c = band; c; c &= c - 1) {
-          const int ee = e0 + __ffs(c) - 1;
-          const float xe = load_logit(row, p.dtype, ee), be = p.bias[ee];
-          mixed |= some && (xe != lx || be != lb);
-          lx = xe, lb = be, some = true;
-        }
-        __syncwarp();
-        const int first = __ffs(__ballot_sync(0xffffffffu, some)) - 1;
-        const float rx = __shfl_sync(0xffffffffu, lx, first), rb = __shfl_sync(0xffffffffu, lb, first);
-        decide = __any_sync(0xffffffffu, mixed || (some && (lx != rx || lb != rb)));
-        if (decide) gt = over, eq = band;
-      }
-      const int room = p.k - add32(__popc(gt));
-      uint32_t sel = gt;
-      if (decide) {
-        sel |= wide_band_fp64<V, kSoft>(p, row, eq, room);
-      } else {
-        int b4 = __popc(eq);
-        const int own = b4;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, b4, o);
-          if (lane >= o) b4 += v;
-        }
-        for (int left = room - (b4 - own); eq && left > 0; eq &= eq - 1, --left) sel |= eq & -eq;
-      }
-      __syncwarp();
-      int at = __popc(sel);
-      const int own = at;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += v;
-      }
-      at -= own;
-      for (; sel; sel &= sel - 1) s_sel[warp][(r << p.ks) + at++] = e0 + __ffs(sel) - 1;
+      select_wide<V, kSoft>(p, row, m, inv_z, kept_groups, bmax, &s_sel[warp][r << p.ks]);
     }
     if (kSoft && lane == 0) {
       s_row[warp][r][0] = m;

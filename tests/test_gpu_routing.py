@@ -442,3 +442,125 @@ def test_many_equal_or_crowded_keys(fn, with_bias):
                      if with_bias else (None,)):
             for kw in (dict(), dict(n_group=16, topk_group=2), dict(n_group=2, topk_group=1, group_top=1)):
                 check_route(x, bias, cfg_of(E, 16, fn=fn, **kw))
+
+
+def plain_route_rows(x, bias, k, fn, n_group, topk_group, group_top, renorm, scale):
+    """plain_route for many rows at once (sorted keys, stable: ties to the lower id)."""
+    T, E = x.shape
+    s, ls = scores(x, fn), log_scores(x, fn)
+    live = x > -np.inf
+    key = np.where(live, x if bias is None else s + bias, -np.inf)
+    if n_group > 1:
+        val = np.where(live, s if bias is None else s + bias, -np.inf).reshape(T, n_group, -1)
+        top = -np.sort(-val, axis=2)[:, :, :group_top]
+        none = np.isneginf(top[:, :, 0])
+        gs = np.where(none, -np.inf, np.where(np.isneginf(top), 0.0, top).sum(2))
+        place = np.argsort(np.argsort(-gs, axis=1, kind="stable"), axis=1, kind="stable")
+        key = np.where(np.repeat((place < topk_group) & ~none, E // n_group, axis=1), key, -np.inf)
+    first = np.argsort(-key, axis=1, kind="stable")[:, :k]
+    ok = ~np.isneginf(np.take_along_axis(key, first, 1))
+    idx = np.sort(np.where(ok, first, E), axis=1)
+    got = idx < E
+    at = np.where(got, idx, 0)
+    if renorm:
+        l = np.where(got, np.take_along_axis(ls, at, 1), -np.inf)
+        u = np.exp(l - np.where(got.any(1, keepdims=True), l.max(1, keepdims=True), 0.0))
+        w = scale * u / np.maximum(u.sum(1, keepdims=True), 1e-300)
+    else:
+        w = np.where(got, scale * np.take_along_axis(s, at, 1), 0.0)
+    lm = ls.max(1, keepdims=True)
+    l = np.exp(ls - np.where(np.isneginf(lm), 0.0, lm))
+    tot = l.sum(1, keepdims=True)
+    return (np.where(got, idx, -1).astype(np.int32), w, np.bincount(idx[got], minlength=E),
+            (l / np.where(tot == 0, 1.0, tot)).sum(0))
+
+
+def check_rows(x, bias, cfg):
+    plan, idx, w, cnt, ps = run_route(x, bias, cfg)
+    b = None if bias is None else bias.double().cpu().numpy()
+    args = (x.double().cpu().numpy(), b, cfg["k"], cfg["score_fn"], cfg["n_group"], cfg["topk_group"], cfg["group_top"],
+            cfg["renormalize"], cfg["scale"])
+    ri, rw, rc, rp = plain_route_rows(*args)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert np.array_equal(cnt.cpu().numpy(), rc)
+    tol = (16 + 32 * (cfg["score_fn"] == "softmax")) * U32
+    assert np.abs(w.double().cpu().numpy() - rw).max() <= tol * cfg["scale"]
+    assert np.all(np.abs(ps.double().cpu().numpy() - rp) <= (tol + 2e-6) * np.maximum(rp, 1e-3))
+    _, i2, w2, _, _ = run_route(x, bias, cfg, sums=False)  # (a kernel of its own)
+    assert torch.equal(i2, idx) and torch.equal(w2, w)
+
+
+def test_the_two_plain_forms_agree():
+    r = np.random.default_rng(0)
+    x = r.standard_normal((40, 24))
+    x[r.random((40, 24)) < 0.3] = -np.inf
+    x[3] = -np.inf
+    x = np.round(x * 2) / 2
+    for fn in ("sigmoid", "softmax"):
+        for b in (None, np.round(r.standard_normal(24) * 4) / 8):
+            for a in ((5, fn, 1, 1, 2, True, 1.0), (5, fn, 4, 2, 2, False, 2.5), (4, fn, 6, 2, 1, True, 1.0)):
+                u, v = plain_route(x, b, *a), plain_route_rows(x, b, *a)
+                assert np.array_equal(u[0], v[0]) and np.array_equal(u[2], v[2])
+                assert np.allclose(u[1], v[1], rtol=1e-12) and np.allclose(u[3], v[3], rtol=1e-12)
+
+
+MANY = [(9728, 256, 8, dict(n_group=8, topk_group=4, scale=2.5)), (9731, 256, 8, {}), (9800, 200, 16, dict(renorm=False)),
+        (9733, 64, 6, {}), (9730, 60, 4, dict(n_group=4, topk_group=2)), (9999, 128, 8, dict(n_group=4, topk_group=2)),
+        (9729, 128, 3, dict(n_group=8, topk_group=1, group_top=1)), (10001, 33, 1, {}), (9728, 16, 4, dict(n_group=2)),
+        (4864, 384, 8, dict(scale=2.5)), (4865, 384, 6, dict(n_group=8, topk_group=3)), (5001, 300, 10, {}),
+        (4867, 512, 16, dict(n_group=16, topk_group=5)), (5003, 512, 10, dict(renorm=False)), (20003, 256, 5, {})]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T,E,k,kw", MANY)
+def test_many_rows_match_fp64(T, E, k, kw, with_bias, fn):
+    """Row counts from which several rows share a warp, and odd ones."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    dtype = ("fp32", "bf16", "fp16")[(T + E + with_bias) % 3]
+    x = torch.randn(T, E, generator=g, device="cuda") * 1.5
+    if T % 2:
+        x[torch.rand(T, E, generator=g, device="cuda") < 0.2] = -float("inf")
+        x[::97] = -float("inf")
+    bias = (torch.rand(E, generator=g, device="cuda") - 0.5) * 0.2 if with_bias else None
+    check_rows(x.to(DTYPES[dtype]), bias, cfg_of(E, k, fn=fn, dtype=dtype, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_many_rows_with_ties_and_crowds(fn, with_bias):
+    """Rows that several to a warp cannot hold, beside ones that they can."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    T, E = 9728, 256
+    x = torch.randn(T, E, generator=g, device="cuda") * 1.5
+    few = torch.randint(-2, 3, (T, E), generator=g, device="cuda").float()
+    x[::3] = few[::3]                       # ties everywhere
+    x[1::7] = x[1::7] - 20.0
+    x[1::7, 40:64] += 20.0                  # the large ones side by side
+    x[2::11] = 0.25                         # one value
+    x[5::13] -= 60.0                        # sigmoid scores of 1e-26
+    x[6::17] = 0.5 + torch.randint(0, 3, (len(x[6::17]), E), generator=g, device="cuda") * 2.0 ** -23
+    bias = torch.zeros(E, device="cuda") if with_bias else None
+    for kw in (dict(n_group=8, topk_group=4), dict(), dict(n_group=8, topk_group=2, group_top=1, renorm=False)):
+        check_rows(x, bias, cfg_of(E, 8, fn=fn, **kw))
+        if with_bias:
+            check_rows(x, torch.randint(0, 3, (E,), generator=g, device="cuda") * 2.0 ** -25, cfg_of(E, 8, fn=fn, **kw))
+
+
+@pytest.mark.gpu
+def test_many_rows_with_nan():
+    T, E = 9728, 256
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(T, E, generator=g, device="cuda")
+    _, i0, w0, _, _ = run_route(x, None, cfg_of(E, 8, fn="softmax"))
+    y = x.clone()
+    y[5, 17] = float("nan")
+    y[6, 0] = float("inf")
+    _, i1, w1, _, ps = run_route(y, None, cfg_of(E, 8, fn="softmax"))
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[5:7] = False
+    assert torch.equal(i0[keep], i1[keep]) and torch.equal(w0[keep], w1[keep])
+    assert bool(torch.isnan(w1[5]).all()) and 17 not in i1[5].tolist() and bool(torch.isnan(ps).all())
+    assert i1[6, 0] == 0 and float(w1[6, 0]) == 1.0 and float(w1[6, 1:].abs().sum()) == 0.0
