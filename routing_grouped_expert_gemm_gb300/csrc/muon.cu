@@ -212,15 +212,7 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
         if (p.last) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] *= p.scale;
-          if (p.out_vec) {
-            *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                             pack_bf16x2(v[6], v[7]));
-          } else if (r < p.M) {
-            bf16* o = p.out_final + (size_t)t.mat * (size_t)p.M * p.N + (size_t)r * p.N + c;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (c + j < p.N) o[j] = __float2bfloat16_rn(v[j]);
-          }
+          *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
           continue;
         }
         __half l[8];
@@ -239,6 +231,21 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         *reinterpret_cast<__half*>(b + (8 * i + j) * 128 + (((rc >> 3) ^ j) << 4) + (rc & 7) * 2) = h[j];
+    }
+  }
+  if (KIND == NS_STEP && p.last && !p.out_vec) {
+    // rows that no tensor map can describe: from shared memory, a row of the
+    // warp's 32 at a time (each thread storing its own row took 35 us more for
+    // 3 x 777 x 1001)
+    __syncwarp();
+    const int col = 8 * i0 + (int)lane_id(), rl0 = rl & ~31, r0 = r - (rl & 31);
+    bf16* o = p.out_final + (size_t)t.mat * (size_t)p.M * p.N + c0 + col;
+#pragma unroll 4
+    for (int k = 0; k < 32; ++k) {
+      const int q = rl0 + k;
+      if (r0 + k < p.M && c0 + col < p.N)
+        o[(size_t)(r0 + k) * p.N] =
+            *reinterpret_cast<const bf16*>(main + q * 128 + (((col >> 3) ^ (q & 7)) << 4) + (col & 7) * 2);
     }
   }
 }
@@ -514,7 +521,8 @@ __device__ __forceinline__ void load_grad(const void* g, int dtype, size_t i, fl
     v[j] = dtype == MOE_DTYPE_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
   }
 }
-constexpr int NS_PREP_U = 2;  // vectors of a thread in flight (4 were no faster: 1 to 4% slower on large stacks)
+// vectors of a thread in flight (of 8 values: 4 were 1 to 4% slower on large stacks)
+__host__ __device__ constexpr int prep_unroll(int V) { return V == 8 ? 2 : 8; }
 
 // Sums of squares in three sums of their own: values far from 1 are squared
 // in scaled form, so that no finite matrix has an infinite norm and none that
@@ -562,6 +570,7 @@ __device__ __forceinline__ void norm_scale(const float (&f)[3], float* f1, float
 // Advance the momentum and sum U's squares.
 template <int V>
 __global__ void __launch_bounds__(256) ns_prep_norm(const PrepParams p) {
+  constexpr int NS_PREP_U = prep_unroll(V);
   __shared__ float s[3][8];
   const int mat = blockIdx.y, cv = p.C / V, n = p.R * cv;
   const bool flat = p.grs == p.C;
@@ -611,6 +620,7 @@ __global__ void __launch_bounds__(256) ns_prep_norm(const PrepParams p) {
 // X_0 = U 2^k as hi + lo.
 template <int V>
 __global__ void __launch_bounds__(256) ns_prep_first(const PrepParams p) {
+  constexpr int NS_PREP_U = prep_unroll(V);
   __shared__ float s[3][8];
   __shared__ float s_f[2];
   const int mat = blockIdx.y, cv = p.C / V, n = p.R * cv;
@@ -1347,7 +1357,7 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
   pp.lo = half_at(L.lo[0]);
   const bool vec = c.cols % 8 == 0 && grad_row_stride % 8 == 0 && grad_stride % 8 == 0 && ns_aligned(grad, 16) &&
                    ns_aligned(momentum, 16);
-  const int64_t nblk = up(c.rows * c.cols / (vec ? 8 : 1), 256 * NS_PREP_U) / (256 * NS_PREP_U);
+  const int64_t per = 256 * prep_unroll(vec ? 8 : 1), nblk = up(c.rows * c.cols / (vec ? 8 : 1), per) / per;
   // blocks per matrix: 256, more where few matrices would leave SMs idle (1 x
   // 1500 x 2500: 337 us with 256, 319 with 1024; 8 x 1024 x 4096: 836 and 859 us)
   int64_t most = 8 * (int64_t)pl->num_sms / pl->chunk;
