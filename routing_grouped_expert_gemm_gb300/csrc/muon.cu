@@ -133,6 +133,10 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* v) {
     v[2 * q + 1] = f.y;
   }
 }
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ uint4 pack8(const __half* h) {
   return make_uint4((uint32_t)__half_as_ushort(h[0]) | ((uint32_t)__half_as_ushort(h[1]) << 16),
                     (uint32_t)__half_as_ushort(h[2]) | ((uint32_t)__half_as_ushort(h[3]) << 16),
@@ -145,69 +149,74 @@ __device__ __forceinline__ uint4 pack8(const __half* h) {
 // STEP: hi), `aux` is lo, or takes the chunk transposed (symmetric products'
 // tiles below the diagonal).  Rows of 128 bytes, 16-byte pieces swizzled as the
 // tensor maps'.
+// g: the row's diagonal element (POLY: A's; STEP, not tall: B's).
 template <int KIND>
 __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uint8_t* main, uint8_t* aux, int rl, int r,
-                                         int c0, int i0, float rho, uint32_t taddr) {
+                                         int c0, int i0, float rho, float g, uint32_t taddr) {
+  const int cw = c0 + 8 * i0;  // this warp's columns: cw .. cw + 31
+  // the columns' diagonal (the same for the whole warp), on its way while TMEM is read
+  float4 dv[KIND == NS_GRAM ? 1 : 8];
+  const bool by_column = KIND == NS_POLY || (KIND == NS_STEP && p.tall);
+  if (by_column) {
+    const float4* d4 = reinterpret_cast<const float4*>((KIND == NS_POLY ? p.diag_a : p.diag_b) + (size_t)t.mat * p.ldd + cw);
+#pragma unroll
+    for (int i = 0; i < (KIND == NS_GRAM ? 1 : 8); ++i) dv[i] = d4[i];
+  }
   uint32_t acc[32];
   tmem_ld_32x32b_x32(taddr + 8u * (uint32_t)i0, acc);
   tmem_ld_wait();
   const bool mirror = KIND != NS_STEP && t.n0 < t.m0;
-  const float* da = p.diag_a + (size_t)t.mat * p.ldd;
-  const float* db = p.diag_b + (size_t)t.mat * p.ldd;
-  float f = 1.0f, g = 0.0f, cb = p.cb;
+  // the diagonal crosses a warp's 32 x 32 elements from corner to corner or not at all
+  const int lane = rl & 31, diag = KIND != NS_STEP && r - lane == cw ? lane : -1;
+  float f = 1.0f, cb = p.cb;
   if (KIND == NS_GRAM) f = p.first ? rho * rho * NS_S : 1.0f / NS_S;
-  if (KIND == NS_POLY) g = da[r];
-  if (KIND == NS_STEP) {
-    if (p.first) f = NS_S * rho, cb = rho;
-    if (!p.tall) g = db[r];
-  }
+  if (KIND == NS_STEP && p.first) f = NS_S * rho, cb = rho;
+  const float fa = KIND == NS_POLY ? p.ca + cb * g : f * p.ca;
 #pragma unroll
   for (int ii = 0; ii < 4; ++ii) {
-    const int i = i0 + ii, c = c0 + 8 * i;
+    const int i = i0 + ii;
     uint4* at = reinterpret_cast<uint4*>(main + rl * 128 + ((i ^ (rl & 7)) << 4));
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[8 * ii + j]);
-    __half h[8];
     if (KIND == NS_GRAM) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] *= f;
-        if (c + j == r) {
-          if (r < p.M) p.diag_a[(size_t)t.mat * p.ldd + r] = v[j];
-          v[j] = 0.0f;
-        }
-        h[j] = __float2half_rn(v[j]);
+      for (int j = 0; j < 8; ++j) v[j] *= f;
+      if (diag >= 8 * ii && diag < 8 * ii + 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (8 * ii + j == diag) {
+            if (r < p.M) p.diag_a[(size_t)t.mat * p.ldd + r] = v[j];
+            v[j] = 0.0f;
+          }
       }
     } else {
       float x[8], d[8];
       unpack8(*at, x);
-      if (KIND == NS_POLY || p.tall) {  // the columns' diagonal: the same 32 bytes for the whole warp
-        const float4* s4 = reinterpret_cast<const float4*>((KIND == NS_POLY ? da : db) + c);
-        const float4 w0 = s4[0], w1 = s4[1];
+      if (by_column) {
+        const float4 w0 = dv[KIND == NS_GRAM ? 0 : 2 * ii], w1 = dv[KIND == NS_GRAM ? 0 : 2 * ii + 1];
         d[0] = w0.x, d[1] = w0.y, d[2] = w0.z, d[3] = w0.w, d[4] = w1.x, d[5] = w1.y, d[6] = w1.z, d[7] = w1.w;
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = g;
       }
       if (KIND == NS_POLY) {  // b O + c (O^2 + (D_r + D_c) O); on the diagonal b D + c (O^2 + D^2)
+        float on = 0.0f;
+        if (diag >= 8 * ii && diag < 8 * ii + 8) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (c + j == r) {
-            if (r < p.M) p.diag_b[(size_t)t.mat * p.ldd + r] = (p.ca * g + cb * (v[j] + g * g)) / NS_S;
-            h[j] = __float2half_rn(0.0f);
-          } else {
-            h[j] = __float2half_rn(p.ca * x[j] + cb * (v[j] + (g + d[j]) * x[j]));
-          }
+          for (int j = 0; j < 8; ++j) on = 8 * ii + j == diag ? v[j] : on;
+          if (r < p.M) p.diag_b[(size_t)t.mat * p.ldd + r] = (p.ca * g + cb * (on + g * g)) / NS_S;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 8 * ii + j == diag ? 0.0f : x[j] * (fa + cb * d[j]) + cb * v[j];
       } else {
         uint4* al = reinterpret_cast<uint4*>(aux + rl * 128 + ((i ^ (rl & 7)) << 4));
         float lo[8];
         unpack8(*al, lo);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float both = x[j] + lo[j], y = p.diag_full ? both : x[j];
-          v[j] = f * (p.ca * both + d[j] * y) + cb * v[j];
+          const float both = x[j] + lo[j];
+          v[j] = both * fa + ((p.diag_full ? both : x[j]) * (f * d[j]) + cb * v[j]);
         }
         if (p.last) {
 #pragma unroll
@@ -215,22 +224,26 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
           *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
           continue;
         }
-        __half l[8];
+        uint32_t l[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[j] = __float2half_rn(v[j]);
-          l[j] = __float2half_rn(v[j] - __half2float(h[j]));
+        for (int j = 0; j < 4; ++j) {
+          const float2 h = __half22float2(__floats2half2_rn(v[2 * j], v[2 * j + 1]));
+          l[j] = pack_half2(v[2 * j] - h.x, v[2 * j + 1] - h.y);
         }
-        *al = pack8(l);
+        *al = make_uint4(l[0], l[1], l[2], l[3]);
       }
     }
-    *at = pack8(h);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] = pack_half2(v[2 * j], v[2 * j + 1]);
+    *at = make_uint4(h[0], h[1], h[2], h[3]);
     if (mirror) {  // element (r, c) goes to row c, column r; two 64-column boxes
       uint8_t* b = aux + (rl >> 6) * NS_BOX;
       const int rc = rl & 63;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<__half*>(b + (8 * i + j) * 128 + (((rc >> 3) ^ j) << 4) + (rc & 7) * 2) = h[j];
+        *reinterpret_cast<uint16_t*>(b + (8 * i + j) * 128 + (((rc >> 3) ^ j) << 4) + (rc & 7) * 2) =
+            (uint16_t)(h[j / 2] >> (16 * (j & 1)));
     }
   }
   if (KIND == NS_STEP && p.last && !p.out_vec) {
@@ -310,6 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the inputs are the last launch's results
+  int failed = 0;  // a wait of this thread ran out
 
   if (warp == 0) {
     if (lane == 0) {
@@ -321,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
         const NsTile t = ns_tile<KIND, TN>(p, u);
         const int ar = t.m0 + rank * 128, br = t.n0 + rank * (TN / 2);
         for (int s = 0; s < nk; ++s) {
-          if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, p.status, p.timeout_ns)) { ok = false; break; }
+          if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, p.status, p.timeout_ns)) { ok = false; failed = 1; break; }
           uint8_t* sa = smem + stage * NS_STAGE;
           uint8_t* sb = sa + 2 * NS_BOX;
           if (leader) mbar_arrive_expect_tx(&full[stage], 2u * (2 + TN / 128) * NS_BOX);
@@ -356,11 +370,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += pairs, ++i) {
         const uint32_t acc = (uint32_t)i & 1u;
-        if (!mbar_wait_cluster(&tempty[acc], (((uint32_t)i >> 1) & 1u) ^ 1u, p.status, p.timeout_ns)) break;
+        if (!mbar_wait_cluster(&tempty[acc], (((uint32_t)i >> 1) & 1u) ^ 1u, p.status, p.timeout_ns)) { failed = 1; break; }
         tc_fence_after();
         const uint32_t d = tmem + acc * TN;
         for (int s = 0; s < nk; ++s) {
-          if (!mbar_wait_cluster(&full[stage], phase, p.status, p.timeout_ns)) { ok = false; break; }
+          if (!mbar_wait_cluster(&full[stage], phase, p.status, p.timeout_ns)) { ok = false; failed = 1; break; }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(smem + stage * NS_STAGE);
           const uint32_t b_addr = a_addr + 2 * NS_BOX;
@@ -389,15 +403,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       const uint32_t acc = (uint32_t)i & 1u;
       const int nc = chunks(t);
       const float rho = p.first ? p.rho[t.mat] : 0.0f;
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tfull[acc], ((uint32_t)i >> 1) & 1u, p.status, p.timeout_ns))) break;
+      float g = 0.0f;
+      if (KIND == NS_POLY) g = p.diag_a[(size_t)t.mat * p.ldd + t.m0 + rank * 128 + rl];
+      if (KIND == NS_STEP && !p.tall) g = p.diag_b[(size_t)t.mat * p.ldd + t.m0 + rank * 128 + rl];
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tfull[acc], ((uint32_t)i >> 1) & 1u, p.status, p.timeout_ns))) { failed = 1; break; }
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * TN;
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const int b = n & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&eload[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait(&eload[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns))) { ok = false; failed = 1; break; }
         uint8_t* e = ebuf + b * NS_EBUF;
-        ns_chunk<KIND>(p, t, e, e + 2 * NS_BOX, rl, t.m0 + rank * 128 + rl, t.n0 + 64 * c, 4 * half, rho,
+        ns_chunk<KIND>(p, t, e, e + 2 * NS_BOX, rl, t.m0 + rank * 128 + rl, t.n0 + 64 * c, 4 * half, rho, g,
                        taddr + 64u * (uint32_t)c);
         fence_proxy_async_smem();  // these writes, before the TMA store that follows the arrival
         __syncwarp();
@@ -442,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       const int nc = chunks(t), row = t.m0 + rank * 128;
       for (int c = 0; c < nc; ++c, ++n) {
         const int b = n & 1, col = t.n0 + 64 * c;
-        if (!mbar_wait(&edone[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns)) { ok = false; break; }
+        if (!mbar_wait(&edone[b], ((uint32_t)n >> 1) & 1u, p.status, p.timeout_ns)) { ok = false; failed = 1; break; }
         const uint8_t* e = ebuf + b * NS_EBUF;
         if (KIND == NS_STEP) {
           if (!p.last || p.out_vec) tma_store_3d(&mp.out0, e, col, row, t.mat);
@@ -464,9 +481,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     for (int k = ln > 2 ? ln - 2 : 0; k < ln; ++k) mbar_wait_drain(&eload[k & 1], ((uint32_t)k >> 1) & 1u, p.timeout_ns);
   }
   __syncwarp();
-  settle_after_abort(p.status);
   tc_fence_before();
-  __syncthreads();
+  // (the status word is read only if a wait of this CTA ran out: 0.7 us a launch)
+  if (__syncthreads_or(failed)) settle_after_abort(p.status);
   // neither CTA frees TMEM or leaves while the other may still issue into its
   // TMEM, arrive on its barriers or load into its shared memory
   cluster_sync_all();
