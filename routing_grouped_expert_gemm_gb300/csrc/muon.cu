@@ -182,14 +182,13 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
     if (KIND == NS_GRAM) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= f;
-      if (diag >= 8 * ii && diag < 8 * ii + 8) {
+      float on = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (8 * ii + j == diag) {
-            if (r < p.M) p.diag_a[(size_t)t.mat * p.ldd + r] = v[j];
-            v[j] = 0.0f;
-          }
+      for (int j = 0; j < 8; ++j) {
+        on = 8 * ii + j == diag ? v[j] : on;
+        v[j] = 8 * ii + j == diag ? 0.0f : v[j];
       }
+      if (diag >> 3 == ii && r < p.M) p.diag_a[(size_t)t.mat * p.ldd + r] = on;
     } else {
       float x[8], d[8];
       unpack8(*at, x);
@@ -202,11 +201,9 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
       }
       if (KIND == NS_POLY) {  // b O + c (O^2 + (D_r + D_c) O); on the diagonal b D + c (O^2 + D^2)
         float on = 0.0f;
-        if (diag >= 8 * ii && diag < 8 * ii + 8) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) on = 8 * ii + j == diag ? v[j] : on;
-          if (r < p.M) p.diag_b[(size_t)t.mat * p.ldd + r] = (p.ca * g + cb * (on + g * g)) / NS_S;
-        }
+        for (int j = 0; j < 8; ++j) on = 8 * ii + j == diag ? v[j] : on;
+        if (diag >> 3 == ii && r < p.M) p.diag_b[(size_t)t.mat * p.ldd + r] = (p.ca * g + cb * (on + g * g)) / NS_S;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 8 * ii + j == diag ? 0.0f : x[j] * (fa + cb * d[j]) + cb * v[j];
       } else {

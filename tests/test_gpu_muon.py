@@ -224,6 +224,20 @@ def test_several_chunks_of_the_general_form():
         assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), None, "bf16", 1, rows, cols)[0])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("count,rows,cols", [(65536, 128, 300), (9000, 520, 512)])
+def test_offsets_beyond_31_bits(count, rows, cols):
+    """More than 2^31 values in the stack: the last matrices are those of calls of their own."""
+    grad = torch.empty(count, rows, cols, dtype=torch.bfloat16, device="cuda")
+    grad.uniform_(-1.0, 1.0)
+    mom = torch.zeros(count, rows, cols, device="cuda")
+    out = run(grad, mom, "bf16", count, rows, cols)
+    for i in (0, count - 1):
+        m1 = torch.zeros(1, rows, cols, device="cuda")
+        assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), m1, "bf16", 1, rows, cols)[0])
+        assert torch.equal(mom[i], m1[0])
+
+
 # ---------------------------------------------------------------- refusals (no GPU needed)
 @pytest.fixture(scope="module")
 def L():

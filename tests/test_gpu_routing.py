@@ -564,3 +564,22 @@ def test_many_rows_with_nan():
     assert torch.equal(i0[keep], i1[keep]) and torch.equal(w0[keep], w1[keep])
     assert bool(torch.isnan(w1[5]).all()) and 17 not in i1[5].tolist() and bool(torch.isnan(ps).all())
     assert i1[6, 0] == 0 and float(w1[6, 0]) == 1.0 and float(w1[6, 1:].abs().sum()) == 0.0
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes of logits: the last rows are those of a call of their own."""
+    T, E, k = (1 << 22) + 37, 264, 8
+    x = torch.empty(T, E, device="cuda")
+    x.uniform_(-3.0, 3.0)
+    bias = torch.rand(E, device="cuda") * 0.1
+    plan, idx, w, cnt, ps = run_route(x, bias, cfg_of(E, k, n_group=8, topk_group=4))
+    tail = slice(T - 100, T)
+    _, i2, w2, _, _ = run_route(x[tail].contiguous(), bias, cfg_of(E, k, n_group=8, topk_group=4))
+    assert torch.equal(idx[tail], i2) and torch.equal(w[tail], w2) and int(cnt.long().sum()) == T * k
+    dw = torch.randn(T, k, device="cuda")
+    d = torch.empty_like(x)
+    rg.moe_route_bwd(plan, T, x, idx, dw, d, dprob_sum=bias)
+    d2 = torch.empty(100, E, device="cuda")
+    rg.moe_route_bwd(plan, 100, x[tail].contiguous(), i2, dw[tail].contiguous(), d2, dprob_sum=bias)
+    assert torch.equal(d[tail], d2)
