@@ -41,7 +41,7 @@
 namespace moe {
 
 constexpr int NS_THREADS = 352;       // producer, MMA issuer, eight epilogue warps, the epilogue's loads and stores
-constexpr int NS_TILE = 256;          // of a CTA pair: 256 x TN (256 or 128), 128 rows in each CTA
+constexpr int NS_TILE = 256;          // of a CTA pair: 256 x 256, or 256 x 128 (narrow), 128 rows in each CTA
 constexpr int NS_BOX = 8192;          // one {64, 64} fp16 box
 constexpr int NS_STAGE = 4 * NS_BOX;  // per CTA: 128 rows of A and half of B's 256, 64 of K
 constexpr int NS_STAGES = 5;
@@ -53,7 +53,7 @@ constexpr int NS_PREP_BLOCKS = 1024;  // partial sums per matrix, at most
 enum : int { NS_GRAM = 0, NS_POLY = 1, NS_STEP = 2 };
 
 struct NsMaps {
-  CUtensorMap a, b;         // operands
+  CUtensorMap a, b, b64;    // operands; b64: the second for narrow tiles (box of 64 rows; MN-major the same as b)
   CUtensorMap in0, in1;     // box {64, 128}: POLY: A; STEP: X's hi and lo
   CUtensorMap out0, out1;   // box {64, 128}: A or B, and (box {64, 64}) its transposed tiles; STEP: hi and lo, or the update
 };
@@ -62,6 +62,7 @@ struct NsParams {
   int M, N, K;             // of one matrix's product
   int nb;                  // matrices
   int tiles_n, n_tiles;    // column tiles; tiles per matrix (symmetric: the lower ones)
+  int n_wide, n_units;     // the first tiles of the launch, whole; and with the others' halves
   int first, last;         // Newton-Schulz step
   int diag_full;           // STEP: B's diagonal multiplies hi + lo, not hi
   int tall;                // STEP: X B, B's diagonal belongs to the columns
@@ -99,28 +100,30 @@ constexpr uint32_t ns_idesc(int tn, bool a_mn, bool b_mn) {
 }
 
 struct NsTile {
-  int mat, m0, n0;
+  int mat, m0, n0, w;  // w: columns, 256 or 128
 };
-// Symmetric products: the tiles that reach the diagonal or lie below it, row
-// by row -- (i + 1) F of them in row i of 256, F = 256 / TN columns of tiles each.
-template <int KIND, int TN>
+// Unit u: a whole tile, or from n_wide on half of one.  Symmetric products: the
+// tiles on and below the diagonal, row by row.
+template <int KIND>
 __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int u) {
-  constexpr int F = NS_TILE / TN;
   NsTile t;
-  t.mat = u / p.n_tiles;
-  const int v = u - t.mat * p.n_tiles;
+  const bool wide = u < p.n_wide;
+  const int g = wide ? u : p.n_wide + (u - p.n_wide) / 2;
+  t.mat = g / p.n_tiles;
+  const int v = g - t.mat * p.n_tiles;
   int i, j;
   if (KIND == NS_STEP) {
     i = v / p.tiles_n;
     j = v - i * p.tiles_n;
   } else {
-    i = (int)((sqrtf(8.0f / F * (float)v + 1.0f) - 1.0f) * 0.5f);
-    while (F * i * (i + 1) / 2 > v) --i;
-    while (F * (i + 1) * (i + 2) / 2 <= v) ++i;
-    j = v - F * i * (i + 1) / 2;
+    i = (int)((sqrtf(8.0f * (float)v + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > v) --i;
+    while ((i + 1) * (i + 2) / 2 <= v) ++i;
+    j = v - i * (i + 1) / 2;
   }
   t.m0 = i * NS_TILE;
-  t.n0 = j * TN;
+  t.n0 = j * NS_TILE + (wide ? 0 : ((u - p.n_wide) & 1) * 128);
+  t.w = wide ? 256 : 128;
   return t;
 }
 
@@ -165,7 +168,7 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
   uint32_t acc[32];
   tmem_ld_32x32b_x32(taddr + 8u * (uint32_t)i0, acc);
   tmem_ld_wait();
-  const bool mirror = KIND != NS_STEP && t.n0 < t.m0;
+  const bool mirror = KIND != NS_STEP && t.n0 < t.m0;  // (the halves of a diagonal tile are both computed)
   // the diagonal crosses a warp's 32 x 32 elements from corner to corner or not at all
   const int lane = rl & 31, diag = KIND != NS_STEP && r - lane == cw ? lane : -1;
   float f = 1.0f, cb = p.cb;
@@ -266,11 +269,11 @@ __device__ __forceinline__ void ns_chunk(const NsParams& p, const NsTile& t, uin
 // of this CTA's 128 rows, 64 columns at a time, two warps to 32 rows; warp 10:
 // loads the epilogue's inputs into the two epilogue buffers and stores its
 // outputs from them, both by TMA, the loads ahead of the accumulator.  Two
-// accumulators of TN columns in TMEM alternate, so a tile's epilogue runs under
+// accumulators of 256 columns in TMEM alternate, so a tile's epilogue runs under
 // the next tile's products.
 // (Rows read and written by the threads themselves, 32 rows of 16 bytes at a
 // time, took 30 us a tile of X against 12 us of products.)
-template <int KIND, int TN, bool A_MN, bool B_MN>
+template <int KIND, bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_gemm(const __grid_constant__ NsMaps mp, const NsParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -290,10 +293,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const int rank = (int)(cluster_ctarank() & 1u);
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int n_units = p.nb * p.n_tiles;
+  const int n_units = p.n_units;
   const int nk = (p.K + BK - 1) / BK;
   // epilogue chunks of this CTA's part of a tile
-  auto chunks = [&](const NsTile& t) { return t.m0 + rank * 128 < p.M ? (min(TN, p.N - t.n0) + 63) / 64 : 0; };
+  auto chunks = [&](const NsTile& t) { return t.m0 + rank * 128 < p.M ? (min(t.w, p.N - t.n0) + 63) / 64 : 0; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS_STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -309,9 +312,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     fence_barrier_init();
     prefetch_tensormap(&mp.a);
     prefetch_tensormap(&mp.b);
+    prefetch_tensormap(&mp.b64);
   }
   if (warp == 1) {
-    tmem_alloc_pair<2 * TN>(tmem_slot);
+    tmem_alloc_pair<512>(tmem_slot);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -329,13 +333,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       int issued = 0;
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += pairs) {
-        const NsTile t = ns_tile<KIND, TN>(p, u);
-        const int ar = t.m0 + rank * 128, br = t.n0 + rank * (TN / 2);
+        const NsTile t = ns_tile<KIND>(p, u);
+        const int ar = t.m0 + rank * 128, br = t.n0 + rank * (t.w / 2);
+        const bool wide = t.w == 256;
         for (int s = 0; s < nk; ++s) {
           if (!mbar_wait_cluster(&empty[stage], phase ^ 1u, p.status, p.timeout_ns)) { ok = false; failed = 1; break; }
           uint8_t* sa = smem + stage * NS_STAGE;
           uint8_t* sb = sa + 2 * NS_BOX;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * (2 + TN / 128) * NS_BOX);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * (wide ? 4u : 3u) * NS_BOX);
           const uint32_t fb = full_even + 8u * stage;
           if (A_MN) {
             tma_load_3d_pair(sa, &mp.a, fb, ar, s * BK, t.mat);
@@ -345,9 +350,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           }
           if (B_MN) {
             tma_load_3d_pair(sb, &mp.b, fb, br, s * BK, t.mat);
-            if (TN == 256) tma_load_3d_pair(sb + NS_BOX, &mp.b, fb, br + 64, s * BK, t.mat);
+            if (wide) tma_load_3d_pair(sb + NS_BOX, &mp.b, fb, br + 64, s * BK, t.mat);
           } else {
-            tma_load_3d_pair(sb, &mp.b, fb, s * BK, br, t.mat);
+            tma_load_3d_pair(sb, wide ? &mp.b : &mp.b64, fb, s * BK, br, t.mat);
           }
           ++issued;
           if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
@@ -367,9 +372,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += pairs, ++i) {
         const uint32_t acc = (uint32_t)i & 1u;
+        const uint32_t id = u < p.n_wide ? ns_idesc(256, A_MN, B_MN) : ns_idesc(128, A_MN, B_MN);
         if (!mbar_wait_cluster(&tempty[acc], (((uint32_t)i >> 1) & 1u) ^ 1u, p.status, p.timeout_ns)) { failed = 1; break; }
         tc_fence_after();
-        const uint32_t d = tmem + acc * TN;
+        const uint32_t d = tmem + acc * 256u;
         for (int s = 0; s < nk; ++s) {
           if (!mbar_wait_cluster(&full[stage], phase, p.status, p.timeout_ns)) { ok = false; failed = 1; break; }
           tc_fence_after();
@@ -379,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           for (int kk = 0; kk < BK / 16; ++kk) {
             const uint64_t ad = A_MN ? sdesc_mn_sw128(a_addr + kk * 2048) : sdesc_kmajor_sw128(a_addr + kk * 32);
             const uint64_t bd = B_MN ? sdesc_mn_sw128(b_addr + kk * 2048) : sdesc_kmajor_sw128(b_addr + kk * 32);
-            mma_bf16_pair(d, ad, bd, ns_idesc(TN, A_MN, B_MN), (s | kk) != 0 ? 1u : 0u);
+            mma_bf16_pair(d, ad, bd, id, (s | kk) != 0 ? 1u : 0u);
           }
           mma_commit_pair(&empty[stage], 0x3);
           if (++stage == NS_STAGES) { stage = 0; phase ^= 1u; }
@@ -396,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     int i = 0, n = 0;
     bool ok = true;
     for (int u = pair; u < n_units && ok; u += pairs, ++i) {
-      const NsTile t = ns_tile<KIND, TN>(p, u);
+      const NsTile t = ns_tile<KIND>(p, u);
       const uint32_t acc = (uint32_t)i & 1u;
       const int nc = chunks(t);
       const float rho = p.first ? p.rho[t.mat] : 0.0f;
@@ -405,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       if (KIND == NS_STEP && !p.tall) g = p.diag_b[(size_t)t.mat * p.ldd + t.m0 + rank * 128 + rl];
       if (!__all_sync(0xffffffffu, mbar_wait_cluster(&tfull[acc], ((uint32_t)i >> 1) & 1u, p.status, p.timeout_ns))) { failed = 1; break; }
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * TN;
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * 256u;
 #pragma unroll 1
       for (int c = 0; c < nc; ++c, ++n) {
         const int b = n & 1;
@@ -427,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     int lu = pair, lc = 0, ln = 0;  // next chunk to load: unit, chunk of its tile, number
     auto load_next = [&]() {
       while (lu < n_units) {
-        const NsTile t = ns_tile<KIND, TN>(p, lu);
+        const NsTile t = ns_tile<KIND>(p, lu);
         if (lc >= chunks(t)) {
           lu += pairs;
           lc = 0;
@@ -452,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     int n = 0;
     bool ok = true;
     for (int u = pair; u < n_units && ok; u += pairs) {
-      const NsTile t = ns_tile<KIND, TN>(p, u);
+      const NsTile t = ns_tile<KIND>(p, u);
       const int nc = chunks(t), row = t.m0 + rank * 128;
       for (int c = 0; c < nc; ++c, ++n) {
         const int b = n & 1, col = t.n0 + 64 * c;
@@ -486,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 2 * TN);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -1214,28 +1220,23 @@ int small_prepare(moe_muon_plan* pl) {
 
 template <int KIND, bool A_MN, bool B_MN>
 bool ns_prepare() {
-  return cudaFuncSetAttribute(ns_gemm<KIND, 256, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM) == cudaSuccess &&
-         cudaFuncSetAttribute(ns_gemm<KIND, 128, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM) == cudaSuccess;
+  return cudaFuncSetAttribute(ns_gemm<KIND, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, NS_SMEM) == cudaSuccess;
 }
-// One product of every matrix, M and N of one given.  Tiles of 256 x 256, or
-// 256 x 128 where those leave CTA pairs idle: a narrow tile takes about 2/3 of
-// a wide one's time, so it is taken where its rounds over the pairs are fewer
-// than 3/2 of the wide tiles' (2 x 700 x 650: 259 us wide, 189 us by this rule;
-// 8 x 1024 x 4096, two rounds of wide tiles or three of narrow: 833 and 846 us).  b64: the second operand with boxes of 64 rows.
+// One product of every matrix, M and N of one given.  Every CTA pair takes
+// whole tiles, round by round; tiles that would fill less than half of a last
+// round are halved for it, a half taking about 0.6 of a tile's time (2 x 700 x
+// 650, all of them halves: 189 us, whole 259 us; 8 x 1024 x 4096, whose A has 80
+// tiles for 76 pairs: 748 us, two whole rounds 777 us).
 template <int KIND, bool A_MN, bool B_MN>
-cudaError_t ns_launch(const moe_muon_plan* pl, NsMaps mp, const CUtensorMap& b64, NsParams p, cudaStream_t st) {
-  const int64_t pairs = pl->num_sms / 2, mt = up(p.M, NS_TILE) / NS_TILE, sym = mt * (mt + 1) / 2;
-  auto tiles = [&](int tn) { return KIND == NS_STEP ? mt * (up(p.N, tn) / tn) : sym * (NS_TILE / tn); };
-  auto rounds = [&](int tn) { return (p.nb * tiles(tn) + pairs - 1) / pairs; };
-  const bool narrow = 2 * rounds(128) < 3 * rounds(256);
-  const int tn = narrow ? 128 : 256;
-  p.tiles_n = (int)(up(p.N, tn) / tn);
-  p.n_tiles = (int)tiles(tn);
-  if (narrow) mp.b = b64;
-  const int64_t units = (int64_t)p.nb * p.n_tiles;
-  const dim3 grid((unsigned)(2 * (units < pairs ? units : pairs)));
-  return narrow ? launch_after(ns_gemm<KIND, 128, A_MN, B_MN>, grid, NS_THREADS, NS_SMEM, st, true, mp, p)
-                : launch_after(ns_gemm<KIND, 256, A_MN, B_MN>, grid, NS_THREADS, NS_SMEM, st, true, mp, p);
+cudaError_t ns_launch(const moe_muon_plan* pl, const NsMaps& mp, NsParams p, cudaStream_t st) {
+  const int64_t pairs = pl->num_sms / 2, mt = up(p.M, NS_TILE) / NS_TILE;
+  p.tiles_n = (int)(up(p.N, NS_TILE) / NS_TILE);
+  p.n_tiles = (int)(KIND == NS_STEP ? mt * p.tiles_n : mt * (mt + 1) / 2);
+  const int64_t tiles = (int64_t)p.nb * p.n_tiles, rest = tiles % pairs;
+  p.n_wide = (int)(2 * rest <= pairs ? tiles - rest : tiles);
+  p.n_units = (int)(p.n_wide + 2 * (tiles - p.n_wide));
+  const int64_t grid = p.n_units < pairs ? p.n_units : pairs;
+  return launch_after(ns_gemm<KIND, A_MN, B_MN>, dim3((unsigned)(2 * grid)), NS_THREADS, NS_SMEM, st, true, mp, p);
 }
 
 }  // namespace
@@ -1414,24 +1415,22 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
       g.M = g.N = (int)L.m;
       g.K = (int)L.n;
       const CUtensorMap& xx = tall ? xm[x] : xk[x];
-      const NsMaps gram = {xx, xx, ak, ak, ak, am};
-      err = tall ? ns_launch<NS_GRAM, true, true>(pl, gram, xm[x], g, st)
-                 : ns_launch<NS_GRAM, false, false>(pl, gram, xm[x], g, st);
+      const NsMaps gram = {xx, xx, xm[x], ak, ak, ak, am};
+      err = tall ? ns_launch<NS_GRAM, true, true>(pl, gram, g, st) : ns_launch<NS_GRAM, false, false>(pl, gram, g, st);
       if (err != cudaSuccess) return MOE_ERR_CUDA;
       // B = b A + c A^2
       g.K = (int)L.m;
       g.ca = c.b;
       g.cb = c.c / NS_S;
-      const NsMaps poly = {ak, ak, ak, ak, bk, bm};
-      if (ns_launch<NS_POLY, false, false>(pl, poly, am, g, st) != cudaSuccess) return MOE_ERR_CUDA;
+      const NsMaps poly = {ak, ak, am, ak, ak, bk, bm};
+      if (ns_launch<NS_POLY, false, false>(pl, poly, g, st) != cudaSuccess) return MOE_ERR_CUDA;
       // X <- a X + B X or a X + X B
       g.M = (int)c.rows;
       g.N = (int)c.cols;
       g.ca = c.a;
       g.cb = 1.0f / NS_S;
-      const NsMaps step = {tall ? xk[x] : bk, tall ? bk : xm[x], xk[x], xl[x], g.last ? uk : xk[x ^ 1], xl[x ^ 1]};
-      err = tall ? ns_launch<NS_STEP, false, false>(pl, step, bm, g, st)
-                 : ns_launch<NS_STEP, false, true>(pl, step, xm[x], g, st);
+      const NsMaps step = {tall ? xk[x] : bk, tall ? bk : xm[x], tall ? bm : xm[x], xk[x], xl[x], g.last ? uk : xk[x ^ 1], xl[x ^ 1]};
+      err = tall ? ns_launch<NS_STEP, false, false>(pl, step, g, st) : ns_launch<NS_STEP, false, true>(pl, step, g, st);
       if (err != cudaSuccess) return MOE_ERR_CUDA;
     }
   }
