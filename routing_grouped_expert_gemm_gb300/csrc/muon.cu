@@ -704,8 +704,11 @@ __global__ void __launch_bounds__(256) ns_prep_first(const PrepParams p) {
 // as the operand of both products -- K-major for X X^T, and, the same bytes,
 // MN-major for B X.  The parts of A = X X^T are summed over the cluster through
 // distributed shared memory, each CTA reducing 1 / cluster of the matrix and
-// writing the sums to all; everything else is local.  (As launches of their
-// own, 3 a step, such stacks take 11 us a launch whatever their size.)
+// writing the sums to all; everything else is local.  16 x 128 x 256: 48 us,
+// 10 of them for the gradient and the momentum and 6.5 a step, against 111 us
+// in the general form's 17 launches.  What bounds it is the chain of a step:
+// three products (1 us each from the barrier to the sums in TMEM) and what
+// follows each of them.
 constexpr int SM_THREADS = 512;
 constexpr int SM_BLK = 16384;                       // 128 rows x 64 fp16, swizzled
 constexpr int SM_PITCH = 132;                       // floats per row of a CTA's part of A
@@ -747,8 +750,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
-__device__ __forceinline__ void st_cluster_u4(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
@@ -756,6 +759,9 @@ __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.pr
 template <int WC>
 __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant__ SmallParams p) {
   constexpr int W = 4 * WC;
+  // sums over the columns (the norm, A) are made of slabs of 128 columns, then of pairs of slabs, whatever W is: a
+  // matrix's update does not depend on how many CTAs share it
+  constexpr int HB = W == 256 ? 2 : 1, HW = W / HB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xs = smem;                                                   // hi of X: W / 64 blocks
@@ -763,9 +769,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
   float* part = reinterpret_cast<float*>(ab + 2 * SM_BLK);              // [128, SM_PITCH]
   float* s_da = part + 128 * SM_PITCH;                                  // [128] A's diagonal times NS_S
   float* s_db = s_da + 128;                                             // [128] B's diagonal
-  float* s_sum = s_db + 128;                                            // [16][4] sums of squares by CTA
-  float(*s_red)[16] = reinterpret_cast<float(*)[16]>(s_sum + 64);       // [3][16]
-  float* s_f = s_sum + 64 + 48;                                         // f1, f2, rho
+  float* s_sum = s_db + 128;                                            // [32][4] sums of squares by slab
+  float(*s_red)[16] = reinterpret_cast<float(*)[16]>(s_sum + 128);      // [3 HB][16]
+  float* s_f = s_sum + 128 + 96;                                        // f1, f2, rho
   uint64_t* bar = reinterpret_cast<uint64_t*>(s_f + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -775,7 +781,6 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
   const int mat = blockIdx.x / cs;
   const int i = (warp & 3) * 32 + lane;      // row of the m x n matrix
   const int j0 = (warp >> 2) * WC;           // first column in the slab
-  const int g0 = (int)rank * W + j0;         // ... and in the matrix
   const bool tall = p.tall != 0;
   uint32_t phase = 0;
 
@@ -791,24 +796,30 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
   // gradient and momentum -> U: read in the matrix's own order, 8 values a
   // thread, and turned to this thread's row of columns through shared memory
   float x[WC];
-  float f[3] = {0.0f, 0.0f, 0.0f};
+  float f[HB][3];
   {
     constexpr int PITCH = W + 4;
     float* stage = reinterpret_cast<float*>(smem);  // [128][PITCH], before X and A are there
     const PrepParams& in = p.in;
     float* mom = in.momentum ? in.momentum + (size_t)mat * in.R * in.C : nullptr;
-    const int s0 = (int)rank * W;                                // the slab's first column
-    const int lead = tall ? min(W, p.n - s0) : p.m;              // rows of the stored matrix to read ...
-    const int cols = tall ? p.m : min(W, p.n - s0);              // ... and columns of each
-    const int r_at = tall ? s0 : 0, c_at = tall ? 0 : s0;
-    const int per = cols > 0 ? (cols + 7) / 8 : 0, units = lead > 0 ? lead * per : 0;
-    for (int u = threadIdx.x; u < 128 * PITCH / 4; u += SM_THREADS) reinterpret_cast<float4*>(stage)[u] = make_float4(0, 0, 0, 0);
-    __syncthreads();
+    const int s0 = (int)rank * W;  // the first column
+    if (p.m < 128 || p.n - s0 < W) {
+      for (int u = threadIdx.x; u < 128 * PITCH / 4; u += SM_THREADS) reinterpret_cast<float4*>(stage)[u] = make_float4(0, 0, 0, 0);
+      __syncthreads();
+    }
     const bool vec = p.vec != 0;
-    for (int u0 = threadIdx.x; u0 < units; u0 += 2 * SM_THREADS) {
-      float g[2][8], m[2][8];
+    constexpr int U = 4;  // units of a thread in flight
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+    for (int h = 0; h < HB; ++h) {
+    f[h][0] = f[h][1] = f[h][2] = 0.0f;
+    const int first = s0 + h * HW, width = min(HW, p.n - first);                     // the slab
+    const int lead = tall ? width : p.m, cols = tall ? p.m : width;                  // rows of the stored matrix, columns
+    const int r_at = tall ? first : 0, c_at = tall ? 0 : first;
+    const int per = cols > 0 ? (cols + 7) / 8 : 0, units = lead > 0 ? lead * per : 0;
+    for (int u0 = threadIdx.x; u0 < units; u0 += U * SM_THREADS) {
+      float g[U][8], m[U][8];
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
         const int u = u0 + q * SM_THREADS;
         if (u < units) {
           const int r = u / per, c = (u - r * per) * 8;
@@ -829,7 +840,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
         }
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < U; ++q) {
         const int u = u0 + q * SM_THREADS;
         if (u < units) {
           const int r = u / per, c = (u - r * per) * 8;
@@ -852,11 +863,12 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if (c + j >= cols) break;
-            add_square(f, g[q][j]);
-            stage[tall ? (c + j) * PITCH + r : r * PITCH + c + j] = g[q][j];
+            add_square(f[h], g[q][j]);
+            stage[tall ? (c + j) * PITCH + h * HW + r : r * PITCH + h * HW + c + j] = g[q][j];
           }
         }
       }
+    }
     }
     __syncthreads();
 #pragma unroll
@@ -866,27 +878,30 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
     }
   }
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
+  for (int h = 0; h < HB; ++h)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) f[q] += __shfl_xor_sync(0xffffffffu, f[q], o);
-    if (lane == 0) s_red[q][warp] = f[q];
-  }
+    for (int q = 0; q < 3; ++q) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) f[h][q] += __shfl_xor_sync(0xffffffffu, f[h][q], o);
+      if (lane == 0) s_red[3 * h + q][warp] = f[h][q];
+    }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // every CTA runs: its shared memory may be written
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (threadIdx.x < 3 * cs) {  // this CTA's sums, to every CTA
-    const uint32_t q = threadIdx.x % 3, to = threadIdx.x / 3;
+  if (threadIdx.x < 3 * HB * cs) {  // this CTA's sums, to every CTA
+    const uint32_t q = threadIdx.x % (3 * HB), to = threadIdx.x / (3 * HB);
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) v += s_red[q][w];
-    st_shared_cluster_u32(mapa_shared(s_sum + rank * 4 + q, to), __float_as_uint(v));
+    st_shared_cluster_u32(mapa_shared(s_sum + (rank * HB + q / 3) * 4 + q % 3, to), __float_as_uint(v));
   }
+  __syncwarp();
   cluster_sync_all();
   if (threadIdx.x == 0) {
     float v[3] = {0.0f, 0.0f, 0.0f};
-    for (uint32_t r = 0; r < cs; ++r)
+    for (uint32_t r = 0; r < cs * HB; ++r)
 #pragma unroll
       for (int q = 0; q < 3; ++q) v[q] += s_sum[r * 4 + q];
     norm_scale(v, &s_f[0], &s_f[1], &s_f[2]);
@@ -896,10 +911,9 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
   auto put_hi = [&]() {  // X's hi part as operand
 #pragma unroll
     for (int c = 0; c < WC; c += 8) {
-      __half h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(x[c + j]);
-      *reinterpret_cast<uint4*>(xs + sw_at(i, j0 + c)) = pack8(h);
+      *reinterpret_cast<uint4*>(xs + sw_at(i, j0 + c)) =
+          make_uint4(pack_half2(x[c], x[c + 1]), pack_half2(x[c + 2], x[c + 3]), pack_half2(x[c + 4], x[c + 5]),
+                     pack_half2(x[c + 6], x[c + 7]));
     }
   };
 #pragma unroll
@@ -935,37 +949,34 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
     products([&]() {
       for (int k = 0; k < W; k += 16) {
         const uint64_t d = sdesc_kmajor_sw128(xa + (uint32_t)((k >> 6) * SM_BLK + (k & 63) * 2));
-        mma_bf16_ss(tmem, d, d, ID | ((uint32_t)(p.mp >> 3) << 17), k != 0 ? 1u : 0u);
+        mma_bf16_ss(tmem + (uint32_t)(k / HW) * 128u, d, d, ID | ((uint32_t)(p.mp >> 3) << 17), k % HW != 0 ? 1u : 0u);
       }
     });
     const float fa = first ? rho * rho * NS_S : 1.0f / NS_S;
-    // one row of 8 columns of A: the diagonal apart, the rest as operand, in CTA `to` (-1: here)
-    auto put_a = [&](int r, int c, float (&v)[8], int to) {
-      __half h[8];
+    // one row of 8 columns of A: the diagonal apart, the rest as operand
+    auto put_a = [&](int r, int c, float (&v)[8]) {
+      float d = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[j] *= fa;
-        h[j] = __float2half_rn(c + j == r ? 0.0f : v[j]);
+        d = c + j == r ? v[j] : d;
+        v[j] = c + j == r ? 0.0f : v[j];
       }
-      const uint4 w = pack8(h);
-      float d = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d = c + j == r ? v[j] : d;
-      const bool on_diag = r >= c && r < c + 8;
-      if (to < 0) {
-        *reinterpret_cast<uint4*>(ab + sw_at(r, c)) = w;
-        if (on_diag) s_da[r] = d;
-      } else {
-        for (uint32_t q = 0; q < cs; ++q) {
-          st_cluster_u4(mapa_shared(ab + sw_at(r, c), q), w);
-          if (on_diag) st_shared_cluster_u32(mapa_shared(s_da + r, q), __float_as_uint(d));
-        }
-      }
+      *reinterpret_cast<uint4*>(ab + sw_at(r, c)) =
+          make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+      if ((r & ~7) == c) s_da[r] = d;
     };
     if (c32 < p.mp) {
       uint32_t acc[32];
       tmem_ld_32x32b_x32(row_tmem + (uint32_t)c32, acc);
       tmem_ld_wait();
+      if (HB == 2) {
+        uint32_t more[32];
+        tmem_ld_32x32b_x32(row_tmem + 128u + (uint32_t)c32, more);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) acc[c] = __float_as_uint(__uint_as_float(acc[c]) + __uint_as_float(more[c]));
+      }
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
         if (c32 + c >= p.mp) break;
@@ -973,7 +984,7 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(acc[c + j]);
         if (cs == 1) {
-          put_a(i, c32 + c, v, -1);
+          put_a(i, c32 + c, v);
         } else if (i < p.mp) {
           float4* d = reinterpret_cast<float4*>(part + i * SM_PITCH + c32 + c);
           d[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -984,18 +995,33 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
     if (cs > 1) {
       __syncwarp();
       cluster_sync_all();
-      const int per_row = p.mp / 8, units = p.mp * per_row;
-      for (int u = (int)rank + (int)cs * (int)threadIdx.x; u < units; u += (int)cs * SM_THREADS) {
-        const int r = u / per_row, c = (u - r * per_row) * 8;
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      // 4 columns a thread, consecutive threads side by side (no bank conflicts), CTA r the r-th share
+      const int per_row = p.mp / 4, share = (p.mp * per_row + (int)cs - 1) / (int)cs;
+      const int u_to = min(p.mp * per_row, ((int)rank + 1) * share);
+      for (int u = (int)rank * share + (int)threadIdx.x; u < u_to; u += SM_THREADS) {
+        const int r = u / per_row, c = (u - r * per_row) * 4;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-        for (uint32_t q = 0; q < cs; ++q) {  // in the CTAs' order, whoever sums
-          const uint32_t at = mapa_shared(part + r * SM_PITCH + c, q);
-          const float4 w0 = ld_cluster_f4(at), w1 = ld_cluster_f4(at + 16);
-          v[0] += w0.x, v[1] += w0.y, v[2] += w0.z, v[3] += w0.w;
-          v[4] += w1.x, v[5] += w1.y, v[6] += w1.z, v[7] += w1.w;
+        for (uint32_t q = 0; q < cs; q += 3 - HB) {  // in the CTAs' order, whoever sums
+          float4 w = ld_cluster_f4(mapa_shared(part + r * SM_PITCH + c, q));
+          if (HB == 1) {  // (clusters are even)
+            const float4 w1 = ld_cluster_f4(mapa_shared(part + r * SM_PITCH + c, q + 1));
+            w.x += w1.x, w.y += w1.y, w.z += w1.z, w.w += w1.w;
+          }
+          v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
         }
-        put_a(r, c, v, 0);
+        float d = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] *= fa;
+          d = c + j == r ? v[j] : d;
+          v[j] = c + j == r ? 0.0f : v[j];
+        }
+        const uint32_t h0 = pack_half2(v[0], v[1]), h1 = pack_half2(v[2], v[3]);
+        for (uint32_t q = 0; q < cs; ++q) {
+          st_cluster_u2(mapa_shared(ab + sw_at(r, c), q), h0, h1);
+          if ((r & ~3) == c) st_shared_cluster_u32(mapa_shared(s_da + r, q), __float_as_uint(d));
+        }
       }
       fence_proxy_async_all();
       __syncwarp();
@@ -1019,19 +1045,16 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
         uint4* at = reinterpret_cast<uint4*>(ab + sw_at(i, c32 + c));
         float o[8];
         unpack8(*at, o);
-        __half h[8];
+        float on = 0.0f, v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int cc = c32 + c + j;
-          const float v = __uint_as_float(acc[c + j]);
-          if (cc == i) {
-            s_db[i] = (p.b * di + cb * (v + di * di)) / NS_S;
-            h[j] = __float2half_rn(0.0f);
-          } else {
-            h[j] = __float2half_rn(p.b * o[j] + cb * (v + (di + s_da[cc]) * o[j]));
-          }
+          const float w = __uint_as_float(acc[c + j]);
+          const bool diag = c32 + c + j == i;
+          on = diag ? w : on;
+          v[j] = diag ? 0.0f : o[j] * (p.b + cb * (di + s_da[c32 + c + j])) + cb * w;
         }
-        *at = pack8(h);
+        if ((i & ~7) == c32 + c) s_db[i] = (p.b * di + cb * (on + di * di)) / NS_S;
+        *at = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
       }
     }
     // X <- a X + B X
@@ -1056,21 +1079,36 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
     if (!last) put_hi();
   }
 
-  // the update, in the matrix's own orientation
-  bf16* out = p.out + (size_t)mat * p.m * p.n;
-  const bool vec = !tall && p.n % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
+  // the update, through shared memory into the matrix's own order: this CTA's
+  // part is `lead` rows of `cols` values, rows `pitch` apart in the matrix
+  {
+    const int s0 = (int)rank * W, width = min(W, p.n - s0);
+    const int lead = tall ? width : p.m, cols = tall ? p.m : width, pitch = tall ? p.m : p.n;
+    bf16* out = p.out + (size_t)mat * p.m * p.n + (tall ? (size_t)s0 * p.m : (size_t)s0);
+    constexpr int SP = (W > 128 ? W : 128) + 8;  // elements between rows in shared memory
+    bf16* stage = reinterpret_cast<bf16*>(smem);
 #pragma unroll
-  for (int c = 0; c < WC; c += 8) {
-    if (i >= p.m || g0 + c >= p.n) break;
-    if (vec) {
-      *reinterpret_cast<uint4*>(out + (size_t)i * p.n + g0 + c) =
-          make_uint4(pack_bf16x2(x[c] * p.scale, x[c + 1] * p.scale), pack_bf16x2(x[c + 2] * p.scale, x[c + 3] * p.scale),
-                     pack_bf16x2(x[c + 4] * p.scale, x[c + 5] * p.scale), pack_bf16x2(x[c + 6] * p.scale, x[c + 7] * p.scale));
+    for (int c = 0; c < WC; c += 8) {
+      if (tall) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage[(j0 + c + j) * SP + i] = __float2bfloat16_rn(x[c + j] * p.scale);
+      } else {
+        *reinterpret_cast<uint4*>(stage + i * SP + j0 + c) =
+            make_uint4(pack_bf16x2(x[c] * p.scale, x[c + 1] * p.scale), pack_bf16x2(x[c + 2] * p.scale, x[c + 3] * p.scale),
+                       pack_bf16x2(x[c + 4] * p.scale, x[c + 5] * p.scale), pack_bf16x2(x[c + 6] * p.scale, x[c + 7] * p.scale));
+      }
+    }
+    __syncthreads();
+    if (cols % 8 == 0 && pitch % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0) {
+      const int per = cols / 8;
+      for (int u = threadIdx.x; u < lead * per; u += SM_THREADS) {
+        const int r = u / per, c = (u - r * per) * 8;
+        *reinterpret_cast<uint4*>(out + (size_t)r * pitch + c) = *reinterpret_cast<const uint4*>(stage + r * SP + c);
+      }
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (g0 + c + j < p.n)
-          out[tall ? (size_t)(g0 + c + j) * p.m + i : (size_t)i * p.n + g0 + c + j] = __float2bfloat16_rn(x[c + j] * p.scale);
+      for (int u = threadIdx.x; u < lead * cols; u += SM_THREADS) {
+        const int r = u / cols, c = u - r * cols;
+        out[(size_t)r * pitch + c] = stage[r * SP + c];
       }
     }
   }
@@ -1196,10 +1234,11 @@ int small_prepare(moe_muon_plan* pl) {
   int wc = 64, cs = 1;
   while (cs * 256 < n) cs *= 2;
   while (wc > 16 && (int64_t)cs * 2 * wc >= n) wc /= 2;  // (as narrow as the columns are)
-  // Few small matrices: more CTAs with fewer columns each, while every cluster
-  // still runs at once and A is small to exchange (4 x 49 x 657: 4 CTAs 68 us,
-  // 8 54 us; 20 x 16 x 247: 1 35 us, 4 27 us; with m = 128 no gain, 92 and 95)
-  while (m <= 64 && wc > 16 && cs < 8 && c.count * cs * 2 <= pl->num_sms) cs *= 2, wc /= 2;
+  // Twice the CTAs with half the columns each, where all of them still run at
+  // once: less work per CTA for the same exchanges (2 x 128 x 1024: 4 CTAs 64
+  // us, 8 54 us; 8 x 100 x 600: 60 and 50 us).  A CTA that needs no exchange
+  // stays alone (16 x 128 x 256: 47.5 us, two CTAs 48.8 us).  Both give the same bits.
+  if (cs > 1 && cs < 8 && wc == 64 && c.count * cs * 2 <= pl->num_sms) cs *= 2, wc = 32;
   pl->small_cs = cs;
   pl->small_wc = wc;
   const SmallKernel k = small_kernel(wc);
@@ -1210,11 +1249,11 @@ int small_prepare(moe_muon_plan* pl) {
   const cudaLaunchConfig_t lc = small_launch(pl, at, nullptr);
   int fit = 0;
   if (cudaOccupancyMaxActiveClusters(&fit, k, &lc) != cudaSuccess) return MOE_ERR_CUDA;
-  // Few clusters of 16 run at once (SMs of one GPC), in rounds of 100 us: from
-  // the fourth round on the general form, whose launches hardly notice another
-  // matrix, is ahead (9 x 117 x 3051: 302 us in three, 335 us).  Up to 8 the
-  // one launch stays ahead (90 x 100 x 600: 238 us, 361 us).
-  if (fit < 1 || (cs > 8 && c.count > 3 * (int64_t)fit)) pl->small_cs = 0;
+  // Few clusters of 16 run at once (SMs of one GPC), so with many matrices the
+  // general form catches up (n x 117 x 3051: 9 matrices 151 us and 205 us, 40
+  // 449 and 477, 80 1011 and 943).  The form goes by the matrices' size alone
+  // all the same, so that a matrix's update does not depend on the others.
+  if (fit < 1) pl->small_cs = 0;
   return MOE_OK;
 }
 

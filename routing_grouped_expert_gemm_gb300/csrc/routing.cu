@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
     if (on) w = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
     float tot = w;
     for (int o = 1 << p.ks >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    if (on) w = __fdividef(w, tot) * p.scale;
+    if (on) w = w / tot * p.scale;  // (one expert: exactly scale)
   } else if (on) {
     w = (kSoft ? expf(below(xs, s_row[warp][r][0])) * nan : 1.0f / (1.0f + expf(-xs))) * p.scale;
   }
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32) route_bwd_kernel(const __gri
         if (on) q = kSoft || ms < -20.0f ? expf(below(xs, ms)) : 1.0f / (1.0f + expf(-xs));
         float tot = q;
         for (int o = slots >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-        q = tot == 0.0f ? 0.0f : __fdividef(q, tot);
+        q = tot == 0.0f ? 0.0f : q / tot;  // (one expert: exactly 1, so that its gradient is 0)
         float qd = q * dw;
         for (int o = slots >> 1; o > 0; o >>= 1) qd += __shfl_xor_sync(0xffffffffu, qd, o);
         ai = q * (dw - qd);

@@ -295,3 +295,18 @@ def test_call_refusals():
     assert code(g, m, u, ws, scale=float("inf")) == bad
     assert code(g, m, u, ws, nesterov=2) == bad
     assert code(g, m, u, ws, workspace_bytes=ws.numel() - 1) == rg.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(128, 300), (60, 1000), (700, 90), (33, 2000), (100, 256), (300, 520)])
+def test_a_matrix_does_not_depend_on_its_stack(rows, cols):
+    """Alone, or among so many that another split over the SMs is chosen."""
+    count = 90
+    grad = stack(count, rows, cols, "decaying", 12).bfloat16()
+    mom = stack(count, rows, cols, "flat", 13)
+    m0 = mom.clone()
+    out = run(grad, mom, "bf16", count, rows, cols)
+    for i in (0, 41, 89):
+        m1 = m0[i:i + 1].clone()
+        assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), m1, "bf16", 1, rows, cols)[0])
+        assert torch.equal(mom[i], m1[0])

@@ -583,3 +583,19 @@ def test_offsets_beyond_32_bits():
     d2 = torch.empty(100, E, device="cuda")
     rg.moe_route_bwd(plan, 100, x[tail].contiguous(), i2, dw[tail].contiguous(), d2, dprob_sum=bias)
     assert torch.equal(d[tail], d2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+def test_one_renormalised_expert_has_a_constant_weight(fn):
+    """k = 1, or one expert left: the weight is scale itself and its gradient 0."""
+    T, E = 300, 48
+    x = torch.randn(T, E, device="cuda") * 3
+    for k, keep in ((1, E), (3, 1)):
+        y = x.clone()
+        y[:, keep:] = -float("inf")
+        plan, idx, w, _, _ = run_route(y, None, cfg_of(E, k, fn=fn, scale=2.5))
+        assert bool((w[:, 0] == 2.5).all()) and bool((w[:, 1:] == 0).all())
+        d = torch.full_like(y, float("nan"))
+        rg.moe_route_bwd(plan, T, y, idx, torch.randn(T, k, device="cuda"), d)
+        assert bool((d == 0).all())
