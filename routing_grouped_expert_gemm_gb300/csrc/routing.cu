@@ -129,6 +129,7 @@ __device__ __forceinline__ uint32_t ord_bits(float f) {
 }
 __device__ __forceinline__ uint32_t ord_of(float f) { return ord_bits(f + 0.0f); }  // -0 equals +0
 constexpr uint32_t ORD_NONE = 0x007fffffu;  // -inf: keys up to this are not to be selected
+constexpr uint32_t ORD_INF = 0xff800000u;   // +inf (a bias may be): exact, so without an error's band
 __device__ __forceinline__ float ord_to(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
@@ -351,7 +352,7 @@ __device__ __noinline__ unsigned decide_groups(const RouteParams& p, const void*
   uint32_t from = 0xffffffffu;
   if (band) {
     const float f = ord_to(least);
-    from = ord_of(f - (ROUTE_REL * (fabsf(f) + bmax) + ROUTE_TINY));
+    from = least < ORD_INF ? ord_of(f - (ROUTE_REL * (fabsf(f) + bmax) + ROUTE_TINY)) : ORD_INF;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       }
     }
     // candidates: the keys from there up, and those that their error might lift there
-    if (with_keys && floor > ORD_NONE) {
+    if (with_keys && floor > ORD_NONE && floor < ORD_INF) {
       const float f = ord_to(floor);
       floor = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
     }

@@ -599,3 +599,17 @@ def test_one_renormalised_expert_has_a_constant_weight(fn):
         d = torch.full_like(y, float("nan"))
         rg.moe_route_bwd(plan, T, y, idx, torch.randn(T, k, device="cuda"), d)
         assert bool((d == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n_inf", [1, 3, 4, 9, 40])
+def test_a_bias_of_plus_infinity_forces_its_experts(fn, n_inf):
+    """Fewer of them than slots, as many, more; equal keys, so the lowest ids win."""
+    T, E = 70, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, E, generator=g, device="cuda")
+    bias = torch.rand(E, generator=g, device="cuda") * 0.1
+    bias[torch.randperm(E, generator=g, device="cuda")[:n_inf]] = float("inf")
+    for kw in (dict(), dict(n_group=8, topk_group=3), dict(n_group=8, topk_group=3, group_top=1, renorm=False)):
+        check_route(x, bias, cfg_of(E, 4, fn=fn, **kw))
