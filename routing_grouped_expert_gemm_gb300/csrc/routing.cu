@@ -12,12 +12,14 @@
 // of the k-th key) lie within that error of it, and are not exact ties (the
 // same logit and bias, decided by the lower id), the warp decides that border
 // again in fp64, computing the few keys that lie in the band (all of them for
-// groups).  A row in some thousands is that close with fp32 logits; fp32 alone
-// would pick another expert in some rows of a large batch.
+// groups).  With fp32 logits one row of some thousands is that close (16384 x
+// 256 in 8 groups: 2 rows at the k-th key, 0.7 at the groups' border, which takes
+// the warp 2 to 3 us); fp32 alone would pick another expert in some rows of a
+// large batch.
 //
-// 16384 x 256 fp32 in 8 groups: 20.3 us, with the sums 25.5 us (17 MB at the
+// 16384 x 256 fp32 in 8 groups: 17.1 us, with the sums 21.2 us (17 MB at the
 // copy rate would be 2.6 us; DRAM is at 8%, instruction issue at 56 to 68%);
-// 32768 x 384 bf16: 27 us; one row: 4.3 us.
+// 32768 x 384 bf16: 26.9 us; one row: 4.3 us.
 //
 // One warp per row, lane l holding the V consecutive experts l V .. l V + V - 1
 // in registers: a row is read once, in 16-byte loads, and nothing but the
@@ -42,7 +44,8 @@ namespace moe {
 constexpr int ROUTE_WARPS = 8;          // rows in flight per CTA
 constexpr int route_ctas_per_sm(int V) { return V <= 12 ? 3 : 2; }  // what registers allow
 constexpr float ROUTE_TINY = 1e-36f;    // keys below this have lost their relative precision (fp32 underflow)
-constexpr float ROUTE_REL = 1.0f / 65536;  // relative error of keys, see route_kernel
+constexpr float ROUTE_REL = 1.0f / 32768;  // relative error of keys, see key_tol
+constexpr float ROUTE_U = 1.0f / 8388608;  // 2^-23: fp32's half ulp, two sides of a comparison
 
 struct RouteParams {
   const void* logits;
@@ -50,7 +53,7 @@ struct RouteParams {
   int E, k, dtype, vec;
   const float* bias;
   int n_group, topk_group, group_top, gs, renorm;
-  int rows, ks;     // rows per warp; log2 of the lanes of a row's slots (k rounded up)
+  int rows, more, ks;  // rows per warp, one more in the first `more` warps; log2 of the lanes of a row's slots (k rounded up)
   float scale;
   int* topk_idx;
   float* topk_w;
@@ -157,6 +160,31 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 // 0 at -inf, 1 at +inf
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(x * -LOG2E)); }
+// How far apart two fp32 keys near f have to be for their order to be exact.  In
+// units of 2^-24, one side:
+// Sigmoid: e^-x is off by 1.22 |x| + 3 relative (the product, log2 e's rounding,
+// ex2) and weighs 1 - s; the sum 1, the reciprocal 2: s ((1 - s) (1.22 |x| + 3) +
+// 3), so at most 0.82 + 3 s, and relative to s at most 107 above ROUTE_TINY (x >
+// -83).  Softmax, d = m - x: e^-d is off by 2.22 d + 3; the row's sum by the
+// scores' mean of that (their mean d is at most ln 512) and its roundings, 38; the
+// reciprocal 2: s (2.22 d + 43), so at most 0.82 + 43 s, relative at most 228.
+// Then the rounding of s + b.  s is at most |key| + max |b|.
+template <bool kSoft>
+__device__ __forceinline__ float key_tol(float f, float bmax) {
+  const float a = fabsf(f) + bmax;
+  return fminf(ROUTE_REL * a + ROUTE_TINY, ROUTE_U * (1.0f + (kSoft ? 45.0f : 5.0f) * a));
+}
+// The same for sums of two keys (of the scores, 43 or 3 times |f| + 2 max |b|; of
+// the keys' sizes |f| + 4 max |b|; of the sum itself).
+template <bool kSoft>
+__device__ __forceinline__ float group_tol(float f, float bmax) {
+  const float a = fabsf(f) + 4.0f * bmax;
+  return fminf(ROUTE_REL * a + ROUTE_TINY, ROUTE_U * (2.0f + (kSoft ? 46.0f : 6.0f) * a));
+}
+// e^(x - m), m the row's maximum; an infinite one is its own limit, those logits share the row
+__device__ __forceinline__ float soft_score(float x, float m) {
+  return m == INFINITY ? (x == m ? 1.0f : x != x ? x : 0.0f) : exp2_fast((x - m) * LOG2E);
+}
 // x - m where an infinite maximum is its own limit (0), not NaN
 __device__ __forceinline__ float below(float x, float m) { return x == m ? 0.0f : x - m; }
 
@@ -258,8 +286,8 @@ __device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* r
 
 // Whether this lane's candidate (expert e, -1 for none; ids ascend with the
 // lanes) is one of the `need` with the largest keys.  Softmax: z32, the row's
-// sum in fp32 (off by less than 2^-20), scales all of the candidates' scores
-// alike, so it decides unless the border is within 2^-20 of how far they lie
+// sum in fp32 (off by less than 2.4e-6), scales all of the candidates' scores
+// alike, so it decides unless the border is within that of how far they lie
 // apart; the sum in fp64 costs more than all the rest.  Whole warp.
 template <int V, bool kSoft>
 __device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, int e, int need, float m32, float z32) {
@@ -282,7 +310,7 @@ __device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, in
       const float far = max32(e >= 0 ? s32 : -INFINITY) + max32(e >= 0 ? -s32 : -INFINITY);  // largest less smallest
       const double lo = ord_to64(~max32_64(in ? ~key : 0ull));
       const unsigned long long out = max32_64(e >= 0 && !in ? key : 0ull);
-      if (!out || lo - ord_to64(out) > 9.6e-7 * (double)far + 1e-15) break;
+      if (!out || lo - ord_to64(out) > 2.4e-6 * (double)far + 1e-15) break;
     }
   }
   return in;
@@ -331,7 +359,7 @@ __device__ __forceinline__ void keys_again(const RouteParams& p, const void* row
     float f = x + 0.0f;
     if (p.bias || by_score) {
       const float b = p.bias && e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
-      const float s = kSoft ? (x == m ? 1.0f : exp2_fast(fmaf(x, LOG2E, -(m * LOG2E)))) : sigmoid_fast(x);
+      const float s = kSoft ? soft_score(x, m) : sigmoid_fast(x);
       f = by_score ? s : kSoft ? fmaf(s, inv_z, b) : s + b;
     }
     key[j] = ord_bits(x > -INFINITY && f > -INFINITY ? f : -INFINITY);
@@ -352,7 +380,7 @@ __device__ __noinline__ unsigned decide_groups(const RouteParams& p, const void*
   uint32_t from = 0xffffffffu;
   if (band) {
     const float f = ord_to(least);
-    from = least < ORD_INF ? ord_of(f - (ROUTE_REL * (fabsf(f) + bmax) + ROUTE_TINY)) : ORD_INF;
+    from = least < ORD_INF ? ord_of(f - key_tol<kSoft>(f, bmax)) : ORD_INF;
   }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -367,7 +395,6 @@ __device__ __noinline__ unsigned decide_groups(const RouteParams& p, const void*
 template <int V, bool kSoft>
 __device__ __noinline__ void select_wide(const RouteParams& p, const void* row, float m, float inv_z, unsigned kept, float bmax,
                                          int* sel_out) {
-  constexpr float REL = ROUTE_REL;
   const int lane = threadIdx.x & 31, e0 = lane * V;
   const bool with_keys = p.bias != nullptr;
   uint32_t key[V], a1 = 0;
@@ -405,7 +432,7 @@ __device__ __noinline__ void select_wide(const RouteParams& p, const void* row, 
   uint32_t band = 0;
   bool decide = false;
   if (with_keys) {
-    const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
+    const float fk = ord_to(kth), tol = key_tol<kSoft>(fk, bmax);
     const uint32_t lo = ord_of(fk - tol), hi = ord_of(fk + tol);
     uint32_t over = 0;
 #pragma unroll
@@ -454,15 +481,8 @@ __device__ __noinline__ void select_wide(const RouteParams& p, const void* row, 
 }
 
 // ------------------------------------------------------------------ forward
-// ROUTE_REL: relative error of fp32 keys, both sides of a comparison together.
-// Sigmoid: e^-x, the sum 2^-24, the reciprocal 2^-23; e^-x is off by
-// (|x| + 3) 2^-24 and weighs 1 - s: for keys above ROUTE_TINY (x > -83) below
-// 2^-17.3 of s and, with the rounding of s + b, 2^-16 (|key| + max |b|) for the
-// two sides.  Softmax: (m - x + 3) 2^-24, at most 104 before e^x is flushed,
-// the row sum and its reciprocal: below 2^-16 as well.
 template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_kernel(const __grid_constant__ RouteParams p) {
-  constexpr float REL = ROUTE_REL;
   __shared__ int s_hist[E_MAX];
   __shared__ __align__(16) uint32_t s_key[ROUTE_WARPS][32];  // candidates: key and expert
   __shared__ int s_id[ROUTE_WARPS][32];
@@ -510,8 +530,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
   const size_t row_bytes = (size_t)p.ld * (p.dtype == MOE_DTYPE_FP32 ? 4 : 2);
 
   const uint32_t lt = (1u << lane) - 1u;
-  const int64_t t_from = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * p.rows;
-  const int64_t t_to = min(t_from + p.rows, p.T);
+  const int wid = blockIdx.x * ROUTE_WARPS + warp;
+  const int64_t t_from = (int64_t)wid * p.rows + min(wid, p.more), t_to = t_from + p.rows + (wid < p.more ? 1 : 0);
   for (int64_t tb = t_from; tb < t_to; tb += 32 >> p.ks) {
   // select for as many rows as have their slots in one warp, then weigh them together
   const int n_rows = (int)min((int64_t)(32 >> p.ks), t_to - tb);
@@ -535,10 +555,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
     if (kSoft && (scored || !p.renorm)) m = row_max();
     if (scored) {
       if (kSoft) {
-        // an infinite maximum is its own limit: those logits share the row
-        const float mm = m * LOG2E;
 #pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = x[j] == m ? 1.0f : exp2_fast(fmaf(x[j], LOG2E, -mm));
+        for (int j = 0; j < V; ++j) s[j] = soft_score(x[j], m);
         if (m == -INFINITY) {
 #pragma unroll
           for (int j = 0; j < V; ++j) s[j] = x[j] != x[j] ? x[j] : 0.0f;
@@ -671,7 +689,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       if (group_scores && kept) {
         const uint32_t hi = tied ? thr : __reduce_max_sync(0xffffffffu, in ? 0u : score);
         if (hi) {
-          const float fl = ord_to(thr), fh = ord_to(hi), tol = REL * (fabsf(fl) + 4.0f * bmax) + ROUTE_TINY;
+          const float fl = ord_to(thr), fh = ord_to(hi), tol = group_tol<kSoft>(fl, bmax);
           if (!(fl - fh > tol)) {
             kept = decide_groups<V, kSoft>(p, row, score, p.group_top > 1 && g2 > ORD_NONE ? g2 : g1, in, fh - tol, fl + tol, m,
                                            inv_z, bmax, s_id[warp]);
@@ -706,7 +724,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
     // candidates: the keys from there up, and those that their error might lift there
     if (with_keys && floor > ORD_NONE && floor < ORD_INF) {
       const float f = ord_to(floor);
-      floor = ord_of(f - (REL * (fabsf(f) + bmax) + ROUTE_TINY));
+      floor = ord_of(f - key_tol<kSoft>(f, bmax));
     }
     floor = max(floor, ORD_NONE + 1u);
     uint32_t cand = 0;
@@ -749,7 +767,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       }
       if (with_keys && n_cand > p.k) {
         // candidates within the error of the k-th: unless all of them are one logit with one bias, fp64 decides
-        const float fk = ord_to(kth), tol = REL * (fabsf(fk) + bmax) + ROUTE_TINY;
+        const float fk = ord_to(kth), tol = key_tol<kSoft>(fk, bmax);
         const bool close = c && !(fabsf(ord_to(c) - fk) > tol);
         const unsigned band = __ballot_sync(0xffffffffu, close);
         if (band & ~who) {
@@ -831,11 +849,21 @@ __global__ void __launch_bounds__(1024) route_sums_kernel(const int* pc, const f
   int c = 0;
   float f = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // partials in flight; 16 need the registers of a whole SM, so that the launch cannot take its place early (1 us more),
+  // and a loop without bounds checks has its last few one after the other (1.1 us more)
+  constexpr int B = 8;
   if (e < E) {
-#pragma unroll 8
-    for (int i = warp; i < n; i += 32) {
-      if (pc) c += pc[(size_t)i * E + e];
-      if (pp) f += pp[(size_t)i * E + e];
+    for (int i0 = warp; i0 < n; i0 += 32 * B) {
+      int vc[B];
+      float vf[B];
+#pragma unroll
+      for (int q = 0; q < B; ++q) {
+        const int i = i0 + 32 * q;
+        vc[q] = pc && i < n ? pc[(size_t)i * E + e] : 0;
+        vf[q] = pp && i < n ? pp[(size_t)i * E + e] : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < B; ++q) c += vc[q], f += vf[q];
     }
   }
   s_c[warp][lane] = c;
@@ -860,7 +888,7 @@ struct RouteBwdParams {
   void* dlogits;
   int64_t ld, dld, T;
   int E, k, dtype, vec, dvec, renorm;
-  int rows, ks;  // as in RouteParams
+  int rows, more, ks;  // as in RouteParams
   float scale;
   const int* topk_idx;
   const float* dtopk_w;
@@ -896,7 +924,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
     d[j] = sums && e0 + j < p.E ? p.dprob_sum[e0 + j] : 0.0f;
   }
   __syncwarp();
-  const int64_t t_from = ((int64_t)blockIdx.x * ROUTE_WARPS + warp) * p.rows, t_to = min(t_from + p.rows, p.T);
+  const int wid = blockIdx.x * ROUTE_WARPS + warp;
+  const int64_t t_from = (int64_t)wid * p.rows + min(wid, p.more), t_to = t_from + p.rows + (wid < p.more ? 1 : 0);
   for (int64_t tb = t_from; tb < t_to; tb += 32 >> p.ks) {
     const int n_rows = (int)min((int64_t)(32 >> p.ks), t_to - tb);
     {  // the selected experts' a (softmax not renormalised: dw, the row's scores follow below)
@@ -1257,7 +1286,8 @@ int moe_route(const moe_route_plan* pl, int64_t T, const void* logits, int64_t l
   p.group_top = c.group_top;
   p.gs = (int)(c.E / c.n_group);
   p.renorm = c.renormalize;
-  p.rows = (int)((T + grid * ROUTE_WARPS - 1) / (grid * ROUTE_WARPS));
+  p.rows = (int)(T / (grid * ROUTE_WARPS));
+  p.more = (int)(T % (grid * ROUTE_WARPS));
   while ((1 << p.ks) < p.k) ++p.ks;
   p.scale = c.scale;
   p.topk_idx = topk_idx;
@@ -1328,7 +1358,8 @@ int moe_route_bwd(const moe_route_plan* pl, int64_t T, const void* logits, int64
   int64_t grid = (T + ROUTE_WARPS - 1) / ROUTE_WARPS;
   const int64_t most = (int64_t)pl->num_sms * (p.E <= 128 ? 5 : route_ctas_per_sm((p.E + 31) / 32));  // what stays resident
   if (grid > most) grid = most;
-  p.rows = (int)((T + grid * ROUTE_WARPS - 1) / (grid * ROUTE_WARPS));
+  p.rows = (int)(T / (grid * ROUTE_WARPS));
+  p.more = (int)(T % (grid * ROUTE_WARPS));
   while ((1 << p.ks) < p.k) ++p.ks;
   auto launch = [&](auto soft) {
     return by_width(p.E, [&](auto v) {

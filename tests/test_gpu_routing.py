@@ -613,3 +613,31 @@ def test_a_bias_of_plus_infinity_forces_its_experts(fn, n_inf):
     bias[torch.randperm(E, generator=g, device="cuda")[:n_inf]] = float("inf")
     for kw in (dict(), dict(n_group=8, topk_group=3), dict(n_group=8, topk_group=3, group_top=1, renorm=False)):
         check_route(x, bias, cfg_of(E, 4, fn=fn, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [-5000.0, 300.0, 5000.0, 1e30])
+def test_softmax_of_large_logits(shift):
+    """The row's maximum is subtracted, not its rounded product with log2 e."""
+    T, E = 300, 64
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn(T, E, generator=g, device="cuda") + shift
+    bias = torch.rand(E, generator=g, device="cuda") * 0.1
+    for b in (None, bias):
+        for kw in (dict(), dict(n_group=8, topk_group=3), dict(renorm=False)):
+            check_route(x, b, cfg_of(E, 6, fn="softmax", **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("spread", [0.5, 3.0, 20.0])
+def test_many_near_borders(fn, spread):
+    """Biases that cancel the scores but for a few units of fp32's rounding: each row's border is close."""
+    T, E = 500, 96
+    g = torch.Generator(device="cuda").manual_seed(6)
+    base = torch.randn(E, generator=g, device="cuda") * spread
+    x = base[None, :] + (torch.randint(-2, 3, (T, E), generator=g, device="cuda") * 2.0 ** -22) * base.abs()[None, :]
+    s = torch.sigmoid(base.double()) if fn == "sigmoid" else torch.softmax(base.double(), 0)
+    bias = (0.5 - s).float()
+    for kw in (dict(), dict(n_group=8, topk_group=4), dict(n_group=12, topk_group=5, group_top=1)):
+        check_route(x, bias, cfg_of(E, 8, fn=fn, **kw))
