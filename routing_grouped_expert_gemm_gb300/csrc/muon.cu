@@ -794,12 +794,13 @@ __global__ void __launch_bounds__(SM_THREADS, 1) ns_small(const __grid_constant_
   if (threadIdx.x == 0) {
     mbar_init(bar, 1);
     fence_barrier_init();
-    if (blockIdx.x == 0) p.status[0] = 0;
   }
   if (warp == 0) {
     tmem_alloc<512>(tmem_slot);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what is before this launch on the stream
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.status[0] = 0;
   // gradient and momentum -> U: read in the matrix's own order, 8 values a
   // thread, and turned to this thread's row of columns through shared memory
   float x[WC];
@@ -1197,10 +1198,10 @@ int ns_encode(const moe_muon_plan* pl, CUtensorMap* m, const void* ptr, int64_t 
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
-// Launch; `early`: the grid may be set up while the launch before it on the
-// stream still runs (the kernels wait for that one's results themselves)
+// Launch; the grid may be set up while the launch before it on the stream still
+// runs (the kernels wait for that one's results themselves)
 template <typename P, typename... A>
-cudaError_t launch_after(void (*kernel)(P, A...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool early,
+cudaError_t launch_after(void (*kernel)(P, A...), dim3 grid, int threads, size_t smem, cudaStream_t st,
                          const std::remove_const_t<P>& p, const std::remove_const_t<A>&... a) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = grid;
@@ -1211,7 +1212,7 @@ cudaError_t launch_after(void (*kernel)(P, A...), dim3 grid, int threads, size_t
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
-  lc.numAttrs = early ? 1 : 0;
+  lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, kernel, p, a...);
 }
 
@@ -1219,7 +1220,7 @@ cudaError_t launch_after(void (*kernel)(P, A...), dim3 grid, int threads, size_t
 // CTAs of at most 256 columns.
 using SmallKernel = void (*)(SmallParams);
 SmallKernel small_kernel(int wc) { return wc == 16 ? ns_small<16> : wc == 32 ? ns_small<32> : ns_small<64>; }
-cudaLaunchConfig_t small_launch(const moe_muon_plan* pl, cudaLaunchAttribute* at, cudaStream_t st) {
+cudaLaunchConfig_t small_launch(const moe_muon_plan* pl, cudaLaunchAttribute (&at)[2], cudaStream_t st) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(pl->cfg.count * pl->small_cs));
   lc.blockDim = dim3(SM_THREADS);
@@ -1229,8 +1230,10 @@ cudaLaunchConfig_t small_launch(const moe_muon_plan* pl, cudaLaunchAttribute* at
   at[0].val.clusterDim.x = (unsigned)pl->small_cs;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = at;
-  lc.numAttrs = 1;
+  lc.numAttrs = 2;
   return lc;
 }
 int small_prepare(moe_muon_plan* pl) {
@@ -1252,7 +1255,7 @@ int small_prepare(moe_muon_plan* pl) {
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SM_BYTES) != cudaSuccess ||
       cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return MOE_ERR_CUDA;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   const cudaLaunchConfig_t lc = small_launch(pl, at, nullptr);
   int fit = 0;
   if (cudaOccupancyMaxActiveClusters(&fit, k, &lc) != cudaSuccess) return MOE_ERR_CUDA;
@@ -1282,7 +1285,7 @@ cudaError_t ns_launch(const moe_muon_plan* pl, const NsMaps& mp, NsParams p, cud
   p.n_wide = (int)(2 * rest <= pairs ? tiles - rest : tiles);
   p.n_units = (int)(p.n_wide + 2 * (tiles - p.n_wide));
   const int64_t grid = p.n_units < pairs ? p.n_units : pairs;
-  return launch_after(ns_gemm<KIND, A_MN, B_MN>, dim3((unsigned)(2 * grid)), NS_THREADS, NS_SMEM, st, true, mp, p);
+  return launch_after(ns_gemm<KIND, A_MN, B_MN>, dim3((unsigned)(2 * grid)), NS_THREADS, NS_SMEM, st, mp, p);
 }
 
 }  // namespace
@@ -1390,7 +1393,7 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
     sp.scale = scale / NS_S;
     sp.status = reinterpret_cast<int*>(ws);
     sp.timeout_ns = (long long)c.timeout_ms * 1000000LL;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     const cudaLaunchConfig_t lc = small_launch(pl, at, st);
     return cudaLaunchKernelEx(&lc, small_kernel(pl->small_wc), sp) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
@@ -1441,9 +1444,8 @@ int moe_muon_update(const moe_muon_plan* pl, const void* grad, int64_t grad_row_
     pp.momentum = momentum ? momentum + (size_t)c0 * c.rows * c.cols : nullptr;
     bf16* out = static_cast<bf16*>(update) + (size_t)c0 * c.rows * c.cols;
     const dim3 pgrid((unsigned)pp.nblk, (unsigned)nb);
-    // (the first launch of the call waits for what is on the stream before it as usual)
-    if (launch_after(vec ? ns_prep_norm<8> : ns_prep_norm<1>, pgrid, 256, 0, st, c0 > 0, pp) != cudaSuccess ||
-        launch_after(vec ? ns_prep_first<8> : ns_prep_first<1>, pgrid, 256, 0, st, true, pp) != cudaSuccess)
+    if (launch_after(vec ? ns_prep_norm<8> : ns_prep_norm<1>, pgrid, 256, 0, st, pp) != cudaSuccess ||
+        launch_after(vec ? ns_prep_first<8> : ns_prep_first<1>, pgrid, 256, 0, st, pp) != cudaSuccess)
       return MOE_ERR_CUDA;
     g.nb = nb;
     g.out_final = out;
