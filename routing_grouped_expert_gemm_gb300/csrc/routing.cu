@@ -17,20 +17,21 @@
 // the warp 2 to 3 us); fp32 alone would pick another expert in some rows of a
 // large batch.
 //
-// 16384 x 256 fp32 in 8 groups: 17.1 us, with the sums 21.2 us (17 MB at the
+// 16384 x 256 fp32 in 8 groups: 15.4 us, with the sums 19.5 us (17 MB at the
 // copy rate would be 2.6 us; DRAM is at 8%, instruction issue at 56 to 68%);
-// 32768 x 384 bf16: 26.9 us; one row: 4.3 us.
+// 32768 x 384 bf16: 25.5 us; one row: 4.3 us.
 //
 // One warp per row, lane l holding the V consecutive experts l V .. l V + V - 1
 // in registers: a row is read once, in 16-byte loads, and nothing but the
 // results is written.  Consecutive experts per lane make "lowest id" the same
 // as "lowest lane", and a group a set of neighbouring lanes.  The kernel is
 // bound by instruction issue, not by memory, so what a row costs is counted in
-// instructions.  Keys become integers in the floats' order.  The k-th largest
+// instructions (740 a row with groups, bias and sums).  The k-th largest
 // of the lanes' maxima (k redux.sync maxima) is a lower bound for the k-th
 // key; the keys above it, little more than k, move to one lane each, where a
 // row's worth of ranking, ties, checks and weights is a few instructions for
 // the whole warp.
+#include <cfloat>
 #include <cuda_fp16.h>
 
 #include <new>
@@ -143,9 +144,17 @@ __device__ __forceinline__ float sum32(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float max32(float v) {  // NaN operands are passed over
-  return ord_to(__reduce_max_sync(0xffffffffu, ord_of(v == v ? v : -INFINITY)));
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
+__device__ __forceinline__ float redux_min(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float max32(float v) { return redux_max(v == v ? v : -INFINITY); }  // NaN operands are passed over
 __device__ __forceinline__ int add32(int v) { return __reduce_add_sync(0xffffffffu, v); }
 // e^x = 2^(x log2 e): relative error (|x| + 3) 2^-24, flushed to 0 below 2^-126, infinite above 2^128
 __device__ __forceinline__ float exp2_fast(float t) {
@@ -485,13 +494,13 @@ __device__ __noinline__ void select_wide(const RouteParams& p, const void* row, 
 template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_kernel(const __grid_constant__ RouteParams p) {
   __shared__ int s_hist[E_MAX];
-  __shared__ __align__(16) uint32_t s_key[ROUTE_WARPS][32];  // candidates: key and expert
+  __shared__ __align__(16) float s_key[ROUTE_WARPS][32];  // candidates: key and expert
   __shared__ int s_id[ROUTE_WARPS][32];
   __shared__ int s_sel[ROUTE_WARPS][32];        // selected experts of up to 32 >> ks rows
   __shared__ float s_row[ROUTE_WARPS][32][2];   // softmax: the row's maximum and 1 / sum (NaN: the row has one)
   __shared__ float s_p[ROUTE_WARPS][32 * V];
   __shared__ __align__(16) float s_bias[32 * V];                   // NaN as -inf: never selected
-  __shared__ __align__(16) uint32_t s_keys[ROUTE_WARPS][32 * V];  // the row's keys
+  __shared__ __align__(16) float s_keys[ROUTE_WARPS][32 * V];  // the row's keys
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const bool sums = p.prob_sum != nullptr, grouped = p.n_group > 1;
   const bool with_keys = p.bias != nullptr;                             // the order is s + b's, not x's
@@ -609,94 +618,102 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       }
     }
 
-    // order of the experts as integers
-    uint32_t key[V];
+    // the order of the experts: -inf is not to be selected
+    float key[V];
     if (with_keys) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float f = kSoft ? fmaf(s[j], inv_z, bias[j]) : s[j] + bias[j];  // (never -0)
-        key[j] = ord_bits(x[j] > -INFINITY ? f : -INFINITY);
+        const float f = kSoft ? fmaf(s[j], inv_z, bias[j]) : s[j] + bias[j];
+        key[j] = x[j] > -INFINITY ? f : -INFINITY;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) key[j] = ord_bits(x[j] > -INFINITY ? x[j] + 0.0f : -INFINITY);
+      for (int j = 0; j < V; ++j) key[j] = fmaxf(x[j], -INFINITY);  // (NaN too)
     }
 
     unsigned kept_groups = ~0u;
     if (grouped) {
       // each group's two largest; without a bias of the (order-keeping) scores, or, for the maximum alone, of x
       const bool by_score = group_scores && !with_keys;
-      uint32_t g1 = 0, g2 = 0;  // lane g: those of group g
+      float g1 = -INFINITY, g2 = -INFINITY;  // lane g: those of group g
       if (aligned_groups) {
-        uint32_t t1 = 0, t2 = 0;
-        auto take = [&](uint32_t v) {
-          t2 = max(t2, min(t1, v));
-          t1 = max(t1, v);
+        float t1 = -INFINITY, t2 = -INFINITY;
+        auto take = [&](float v) {
+          t2 = fmaxf(t2, fminf(t1, v));
+          t1 = fmaxf(t1, v);
         };
         if (by_score) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) take(key[j] > ORD_NONE ? ord_of(s[j]) : 0u);
+          for (int j = 0; j < V; ++j) take(key[j] > -INFINITY ? s[j] : -INFINITY);
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j) take(key[j]);
         }
 #pragma unroll 2
         for (int o = 1; o < glanes; o <<= 1) {
-          const uint32_t u1 = __shfl_xor_sync(0xffffffffu, t1, o), u2 = __shfl_xor_sync(0xffffffffu, t2, o);
-          t2 = max(max(t2, u2), min(t1, u1));
-          t1 = max(t1, u1);
+          const float u1 = __shfl_xor_sync(0xffffffffu, t1, o), u2 = __shfl_xor_sync(0xffffffffu, t2, o);
+          t2 = fmaxf(fmaxf(t2, u2), fminf(t1, u1));
+          t1 = fmaxf(t1, u1);
         }
         const int from = (lane * glanes) & 31;
         g1 = __shfl_sync(0xffffffffu, t1, from);
         g2 = __shfl_sync(0xffffffffu, t2, from);
-        if (lane >= p.n_group) g1 = g2 = 0;
+        if (lane >= p.n_group) g1 = g2 = -INFINITY;
       } else {
         for (int g = 0; g < p.n_group; ++g) {
           const int lo = g * p.gs - e0, hi = lo + p.gs;
-          uint32_t t1 = 0, t2 = 0;
+          float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            uint32_t v = by_score ? (key[j] > ORD_NONE ? ord_of(s[j]) : 0u) : key[j];
-            v = j >= lo && j < hi ? v : 0u;
-            t2 = max(t2, min(t1, v));
-            t1 = max(t1, v);
+            float v = by_score ? (key[j] > -INFINITY ? s[j] : -INFINITY) : key[j];
+            v = j >= lo && j < hi ? v : -INFINITY;
+            t2 = fmaxf(t2, fminf(t1, v));
+            t1 = fmaxf(t1, v);
           }
-          const uint32_t w1 = __reduce_max_sync(0xffffffffu, t1);
+          const float w1 = redux_max(t1);
           const unsigned own = __ballot_sync(0xffffffffu, t1 == w1);
-          const uint32_t w2 = __reduce_max_sync(0xffffffffu, lane == __ffs(own) - 1 ? t2 : t1);
+          const float w2 = redux_max(lane == __ffs(own) - 1 ? t2 : t1);
           if (lane == g) g1 = w1, g2 = w2;
         }
       }
-      // the topk_group largest scores, the lowest group first among equals; a group without an expert has 0
-      uint32_t score = g1 > ORD_NONE ? g1 : 0u;
-      if (group_scores && p.group_top > 1 && g2 > ORD_NONE) score = ord_of(ord_to(g1) + ord_to(g2));
-      s_key[warp][lane] = score;
-      __syncwarp();
-      int rank = 0;  // the number of larger scores
-      for (int g = 0; g < p.n_group; g += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(&s_key[warp][g]);
-        rank += v.x > score ? 1 : 0;
-        rank += v.y > score ? 1 : 0;
-        rank += v.z > score ? 1 : 0;
-        rank += v.w > score ? 1 : 0;
+      // the topk_group largest scores, the lowest group first among equals; a group without an expert has -inf
+      float score = g1;
+      if (group_scores && p.group_top > 1 && g2 > -INFINITY) score = fmaxf(g1 + g2, -FLT_MAX);
+      float thr = -INFINITY;
+      {
+        float a = score;
+#pragma unroll 4
+        for (int i = 0; i < p.topk_group; ++i) {
+          thr = redux_max(a);
+          a = a == thr ? -INFINITY : a;
+        }
       }
-      __syncwarp();
-      bool in = score && rank < p.topk_group;
+      bool in = score > -INFINITY && score >= thr, tied = false;
       unsigned kept = __ballot_sync(0xffffffffu, in);
-      const uint32_t thr = __reduce_min_sync(0xffffffffu, in ? score : 0xffffffffu);
-      const bool tied = __popc(kept) > p.topk_group;
-      if (tied) {  // equal scores across the border: the lowest groups
-        const unsigned over = __ballot_sync(0xffffffffu, in && score > thr), same = kept & ~over;
-        in = in && (score > thr || __popc(same & lt) < p.topk_group - __popc(over));
+      if (__popc(kept) > p.topk_group) {  // (equal scores count once above)
+        s_key[warp][lane] = score;
+        __syncwarp();
+        int rank = 0;  // the number of larger scores
+        for (int g = 0; g < p.n_group; ++g) rank += s_key[warp][g] > score ? 1 : 0;
+        __syncwarp();
+        in = in && rank < p.topk_group;
         kept = __ballot_sync(0xffffffffu, in);
+        thr = redux_min(in ? score : INFINITY);
+        tied = __popc(kept) > p.topk_group;
+        if (tied) {  // equal scores across the border: the lowest groups
+          const unsigned over = __ballot_sync(0xffffffffu, in && score > thr), same = kept & ~over;
+          in = in && (score > thr || __popc(same & lt) < p.topk_group - __popc(over));
+          kept = __ballot_sync(0xffffffffu, in);
+        }
       }
-      if (group_scores && kept) {
-        const uint32_t hi = tied ? thr : __reduce_max_sync(0xffffffffu, in ? 0u : score);
-        if (hi) {
-          const float fl = ord_to(thr), fh = ord_to(hi), tol = group_tol<kSoft>(fl, bmax);
-          if (!(fl - fh > tol)) {
-            kept = decide_groups<V, kSoft>(p, row, score, p.group_top > 1 && g2 > ORD_NONE ? g2 : g1, in, fh - tol, fl + tol, m,
-                                           inv_z, bmax, s_id[warp]);
+      if (group_scores) {
+        const float hi = tied ? thr : redux_max(in ? -INFINITY : score);
+        if (hi > -INFINITY) {
+          const float tol = group_tol<kSoft>(thr, bmax);
+          if (!(thr - hi > tol)) {
+            kept = decide_groups<V, kSoft>(p, row, score > -INFINITY ? ord_of(score) : 0u,
+                                           ord_of(p.group_top > 1 && g2 > -INFINITY ? g2 : g1), in, hi - tol, thr + tol, m, inv_z,
+                                           bmax, s_id[warp]);
           }
         }
       }
@@ -704,33 +721,30 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       if (aligned_groups) {
         const bool keep = (kept >> gid[0]) & 1u;  // all of a lane's experts are in one group
 #pragma unroll
-        for (int j = 0; j < V; ++j) key[j] = keep ? key[j] : 0u;
+        for (int j = 0; j < V; ++j) key[j] = keep ? key[j] : -INFINITY;
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j)
-          if (!((kept >> ((gid[j / 4] >> (8 * (j % 4))) & 31u)) & 1u)) key[j] = 0;
+          if (!((kept >> ((gid[j / 4] >> (8 * (j % 4))) & 31u)) & 1u)) key[j] = -INFINITY;
       }
     }
-    uint32_t a1 = 0;  // this lane's largest key
+    float a1 = -INFINITY;  // this lane's largest key
 #pragma unroll
-    for (int j = 0; j < V; ++j) a1 = max(a1, key[j]);
+    for (int j = 0; j < V; ++j) a1 = fmaxf(a1, key[j]);
 
-    // k lanes' maxima at least reach `floor`, so the k-th key does too (not above ORD_NONE: fewer lanes have keys)
-    uint32_t floor = 0;
+    // k lanes' maxima at least reach `floor`, so the k-th key does too (-inf: fewer lanes have keys)
+    float floor = -INFINITY;
     {
-      uint32_t a = a1;
+      float a = a1;
 #pragma unroll 4
       for (int i = 0; i < p.k; ++i) {
-        floor = __reduce_max_sync(0xffffffffu, a);
-        a = a == floor ? 0u : a;
+        floor = redux_max(a);
+        a = a == floor ? -INFINITY : a;
       }
     }
-    // candidates: the keys from there up, and those that their error might lift there
-    if (with_keys && floor > ORD_NONE && floor < ORD_INF) {
-      const float f = ord_to(floor);
-      floor = ord_of(f - key_tol<kSoft>(f, bmax));
-    }
-    floor = max(floor, ORD_NONE + 1u);
+    // candidates: the keys from there up, and those that their error might lift there (an infinite bias is exact)
+    if (with_keys && fabsf(floor) < INFINITY) floor -= key_tol<kSoft>(floor, bmax);
+    floor = fmaxf(floor, -FLT_MAX);
     uint32_t cand = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) cand |= key[j] >= floor ? 1u << j : 0u;
@@ -744,26 +758,26 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
     const int n_cand = __shfl_sync(0xffffffffu, before, 31);
     before -= mine;
     if (n_cand <= 32) {  // one lane each, ids ascending with the lanes
-      uint32_t* keys = s_keys[warp] + e0;
+      float* keys = s_keys[warp] + e0;
 #pragma unroll
       for (int j = 0; j < V; ++j) keys[j] = key[j];
       for (uint32_t c = cand; c; c &= c - 1) s_id[warp][before++] = e0 + __ffs(c) - 1;
       __syncwarp();
       const int e = s_id[warp][lane];
-      const uint32_t c = lane < n_cand ? s_keys[warp][e] : 0u;
+      const float c = lane < n_cand ? s_keys[warp][e] : -INFINITY;
       s_key[warp][lane] = c;
       __syncwarp();
-      int rank = 0;  // of a key, the number of larger ones; 0 is no key
+      int rank = 0;  // of a key, the number of larger ones
       for (int i = 0; i < n_cand; i += 4) {
-        const uint4 v = *reinterpret_cast<const uint4*>(&s_key[warp][i]);
+        const float4 v = *reinterpret_cast<const float4*>(&s_key[warp][i]);
         rank += v.x > c ? 1 : 0;
         rank += v.y > c ? 1 : 0;
         rank += v.z > c ? 1 : 0;
         rank += v.w > c ? 1 : 0;
       }
-      bool in = c && rank < p.k;
+      bool in = c > -INFINITY && rank < p.k;
       unsigned who = __ballot_sync(0xffffffffu, in);
-      const uint32_t kth = __reduce_min_sync(0xffffffffu, in ? c : 0xffffffffu);
+      const float kth = redux_min(in ? c : INFINITY);
       if (__popc(who) > p.k) {  // equal keys across the border: the lowest ids
         const unsigned over = __ballot_sync(0xffffffffu, in && c > kth), same = who & ~over;
         in = in && (c > kth || __popc(same & lt) < p.k - __popc(over));
@@ -771,8 +785,8 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
       }
       if (with_keys && n_cand > p.k) {
         // candidates within the error of the k-th: unless all of them are one logit with one bias, fp64 decides
-        const float fk = ord_to(kth), tol = key_tol<kSoft>(fk, bmax);
-        const bool close = c && !(fabsf(ord_to(c) - fk) > tol);
+        const float tol = key_tol<kSoft>(kth, bmax);
+        const bool close = c > -INFINITY && !(fabsf(c - kth) > tol);
         const unsigned band = __ballot_sync(0xffffffffu, close);
         if (band & ~who) {
           const float xe = close ? load_logit(row, p.dtype, e) : 0.0f, be = close ? p.bias[e] : 0.0f;
@@ -909,9 +923,9 @@ struct RouteBwdParams {
 // for several rows at once, one lane per slot (32 >> ks rows), and meet the
 // row's through shared memory.  Renormalised weights, and sigmoid ones, without
 // prob_sum need the selected logits only, so the row itself is not read.
-// 16384 x 256 fp32 with prob_sum: 10.3 us (33.5 MB at the copy rate would be
+// 16384 x 256 fp32 with prob_sum: 9.5 us (33.5 MB at the copy rate would be
 // 5.1 us; what is left is the latency of a row's load and reductions, four to
-// five rows a warp), without 7.2 us; 32768 x 384 bf16: 19.5 us (7.8).
+// five rows a warp), without 6.4 us; 32768 x 384 bf16: 19.0 us (7.8).
 template <int V, bool kSoft>
 __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_bwd_kernel(const __grid_constant__ RouteBwdParams p) {
   __shared__ __align__(16) float s_a[ROUTE_WARPS][32 * V];
