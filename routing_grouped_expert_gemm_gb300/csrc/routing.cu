@@ -14,7 +14,7 @@
 // again in fp64, computing the few keys that lie in the band (all of them for
 // groups).  With fp32 logits one row of some thousands is that close (16384 x
 // 256 in 8 groups: 2 rows at the k-th key, 0.7 at the groups' border, which takes
-// the warp 2 to 3 us); fp32 alone would pick another expert in some rows of a
+// the warp 4 us and a call 2 to 3); fp32 alone would pick another expert in some rows of a
 // large batch.
 //
 // 16384 x 256 fp32 in 8 groups: 15.4 us, with the sums 19.5 us (17 MB at the
