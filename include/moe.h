@@ -54,7 +54,8 @@ typedef enum moe_device_status {
   MOE_STATUS_OK = 0,
   MOE_STATUS_TIMEOUT = 1,          /* a device-side wait exceeded its limit; outputs are invalid */
   MOE_STATUS_SCHEDULE_INVALID = 2, /* an expert index out of range or route counts inconsistent
-                                      (moe_fwd_routed: an index out of range or given twice for a token) */
+                                      (moe_fwd_routed: an index out of range or given twice for a token;
+                                      a backward: its forward was of the other kind) */
   MOE_STATUS_STAGING_OVERFLOW = 3  /* the forward completed, but an expert output left the fp16 range of
                                       the staging rows (|v| > 65504, or NaN) and was saturated: the
                                       output is finite but not the layer's value */
@@ -399,7 +400,9 @@ size_t moe_bwd_workspace_bytes(const moe_plan* plan, int64_t T);
  *   dO         [T, D] bf16 (device)
  *   workspace  at least moe_bwd_workspace_bytes(plan, T) bytes, 256-byte aligned
  * Launches eight kernels on `stream`; no host synchronisation; device-side
- * failures are reported through moe_get_status on `workspace`.
+ * failures are reported through moe_get_status on `workspace`.  After a forward
+ * whose routing was given (moe_fwd_routed) there is no router gradient: the
+ * status is MOE_STATUS_SCHEDULE_INVALID, and dW_router, db_router and dx are NaN.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE,
  * MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
  */
@@ -412,8 +415,9 @@ int moe_bwd(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w
  * router's (dW_router and db_router are ignored, dx is without the router's
  * term), and instead
  *   dtopk_w [T, k] fp32 (device, required): dL/d topk_w; 0 in an empty slot
- * which moe_route_bwd takes on to the logits.  Otherwise as moe_bwd; launches
- * six kernels.
+ * which moe_route_bwd takes on to the logits.  After a forward that routed by
+ * itself (moe_fwd) the status is MOE_STATUS_SCHEDULE_INVALID and dtopk_w NaN.
+ * Otherwise as moe_bwd; launches six kernels.
  */
 int moe_bwd_routed(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w, const void* dO,
                    const void* fwd_workspace, const moe_grads* grads, float* dtopk_w, void* workspace,

@@ -140,6 +140,7 @@ int fwd_routing_views(const moe_plan* pl, int64_t T, const void* workspace, FwdR
   v->topk_idx = reinterpret_cast<const int*>(ws + L.topk_idx);
   v->topk_w = reinterpret_cast<const float*>(ws + L.topk_w);
   v->topk_logit = reinterpret_cast<const float*>(ws + L.topk_logit);
+  v->status = reinterpret_cast<const int*>(ws + L.status);
   v->M = reinterpret_cast<const int*>(ws + L.M);
   v->S = reinterpret_cast<const int*>(ws + L.S);
   v->sched = reinterpret_cast<const int*>(ws + L.sched);

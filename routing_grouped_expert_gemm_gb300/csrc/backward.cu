@@ -91,6 +91,7 @@ struct BwdParams {
   const int* topk_idx;
   const float* topk_w;
   const float* topk_logit;
+  const int* fwd_status;  // its status word and FLAG_* bits
   const int* M;
   const int* S;
   const int* sched;
@@ -150,6 +151,14 @@ __device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t smem_addr) {
 constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
 // ------------------------------------------------------------------ prep
+// topk_logit holds logits after a forward with the built-in router and marks of
+// the empty slots after one with a given routing.  A backward of the other kind
+// is reported (FLAG_ROUTES_INVALID) and its router gradient, or gradient of the
+// weights, is NaN.
+__device__ __forceinline__ bool other_forward(const BwdParams& p) {
+  return ((p.fwd_status[1] & FLAG_ROUTES_GIVEN) != 0) != (p.dtopk_w != nullptr);
+}
+
 // One CTA: padded segment starts Sp (each expert's routes rounded up to 64),
 // the 128-row M-tiles over them, the experts by descending route count (ties:
 // lower id first) and the router-gradient chunks; zeroes the claim counters
@@ -159,7 +168,7 @@ __global__ void __launch_bounds__(512, 1) bwd_prep(BwdParams p) {
   const int E = p.E, tid = threadIdx.x;
   if (tid == 0) {
     p.status[0] = 0;
-    p.status[1] = 0;
+    p.status[1] = other_forward(p) ? FLAG_ROUTES_INVALID : 0;
     p.counters[0] = 0;
     p.counters[1] = 0;
   }
@@ -860,8 +869,9 @@ __global__ void __launch_bounds__(256) bwd_router_dl(BwdParams p) {
     g = p.topk_w[j];
     if (p.score_fn == MOE_SCORE_SIGMOID) sv = 1.0f / (1.0f + expf(-p.topk_logit[j]));
   }
+  const bool wrong = other_forward(p);
   if (p.dtopk_w) {  // the routing was given (its empty slots are marked in topk_logit)
-    if (on) p.dtopk_w[j] = p.topk_logit[j] != 0.0f ? 0.0f : dg;
+    if (on) p.dtopk_w[j] = wrong ? NAN : p.topk_logit[j] != 0.0f ? 0.0f : dg;
     return;
   }
   const float c = warp_sum_bfly(on ? g * dg : 0.0f);
@@ -872,7 +882,7 @@ __global__ void __launch_bounds__(256) bwd_router_dl(BwdParams p) {
   } else {
     dl = g * (dg - c);
   }
-  if (on) p.dl[j] = dl;
+  if (on) p.dl[j] = wrong ? NAN : dl;
 }
 
 // dW_r and db partial sums over chunks of WR_CHUNK consecutive routes of one
@@ -1130,6 +1140,7 @@ int backward(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w,
   p.topk_idx = fv.topk_idx;
   p.topk_w = fv.topk_w;
   p.topk_logit = fv.topk_logit;
+  p.fwd_status = fv.status;
   p.M = fv.M;
   p.S = fv.S;
   p.sched = fv.sched;

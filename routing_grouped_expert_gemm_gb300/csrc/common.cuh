@@ -54,8 +54,10 @@ constexpr int E_MAX = 512;
 // device status codes (written to the workspace status word)
 enum : int { STATUS_OK = 0, STATUS_TIMEOUT = 1, STATUS_SCHEDULE_INVALID = 2 };
 // sticky warning bits in the word after the status word: they do not stop the
-// forward (the status word does), they only qualify its result
-enum : int { FLAG_STAGING_OVERFLOW = 1, FLAG_ROUTES_INVALID = 2 };
+// forward (the status word does), they only qualify its result.
+// FLAG_ROUTES_GIVEN is no warning: the forward's routing was given, so that the
+// backward can tell whether it belongs to that forward
+enum : int { FLAG_STAGING_OVERFLOW = 1, FLAG_ROUTES_INVALID = 2, FLAG_ROUTES_GIVEN = 4 };
 
 // phase stamps of one persistent-kernel launch (ns of %globaltimer), for
 // per-phase bandwidth figures: the first CTA's start, the last ring fill, the

@@ -15,6 +15,7 @@ struct FwdRoutingViews {
   const int* topk_idx;
   const float* topk_w;
   const float* topk_logit;
+  const int* status;  // status word and FLAG_* bits
   const int* M;
   const int* S;
   const int* sched;

@@ -1107,6 +1107,7 @@ __global__ void __launch_bounds__(BM) given_routes_kernel(const __grid_constant_
     p.stamps[STAMP_START] = p.stamps[STAMP_COMBINE_START] = ~0ull;
     p.stamps[STAMP_LAST_FILL] = p.stamps[STAMP_COMBINE_END] = 0ull;
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status + 1, FLAG_ROUTES_GIVEN);
   for (int e = threadIdx.x; e < p.E; e += BM) s_hist[e] = 0;
   __syncthreads();
   if (t < p.T) {

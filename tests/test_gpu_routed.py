@@ -196,3 +196,41 @@ def test_refusals():
     inp, layer, x = bwd_layer(0)
     gr = grads_of(layer, inp.T)
     assert code(rg.moe_bwd_routed, layer.plan, inp.T, x, layer.w, x, layer.ws, gr, None, layer.ws) == bad
+
+
+@pytest.mark.parametrize("pair", [0, 1])
+def test_a_backward_of_the_other_forward_is_reported(pair):
+    """moe_bwd after moe_fwd_routed, and moe_bwd_routed after moe_fwd: the status
+    says so, and what would be wrong is NaN."""
+    inp, layer, x = bwd_layer(pair)
+    s, T = inp.shape, inp.T
+    dO = torch.randn(T, s.D, device="cuda").bfloat16()
+    bws = torch.zeros(rg.moe_bwd_workspace_bytes(layer.plan, T), dtype=torch.uint8, device="cuda")
+
+    def built_in():
+        gr = grads_of(layer, T)
+        gr["dW_router"] = torch.zeros(s.E, s.D, device="cuda")
+        rg.moe_bwd(layer.plan, T, x, layer.w, dO, layer.ws, gr, bws)
+        return rg.moe_get_status(layer.plan, bws), gr
+
+    def routed():
+        gr, dw = grads_of(layer, T), torch.zeros(T, s.k, device="cuda")
+        rg.moe_bwd_routed(layer.plan, T, x, layer.w, dO, layer.ws, gr, dw, bws)
+        return rg.moe_get_status(layer.plan, bws), dw
+
+    res = layer.run(x)
+    status, ref = built_in()
+    assert status == rg.MOE_STATUS_OK
+    status, dw = routed()
+    assert status == rg.MOE_STATUS_SCHEDULE_INVALID and bool(torch.isnan(dw).all())
+    fwd_routed(layer, x, res["topk_idx"], res["topk_w"])
+    status, gr = built_in()
+    assert status == rg.MOE_STATUS_SCHEDULE_INVALID
+    hit = torch.bincount(res["topk_idx"].flatten().long(), minlength=s.E) > 0
+    assert bool(torch.isnan(gr["dW_router"][hit]).all()) and bool(torch.isnan(gr["dx"]).all())
+    status, dw = routed()
+    assert status == rg.MOE_STATUS_OK and bool(torch.isfinite(dw).all())
+    # the next forward decides again
+    layer.run(x)
+    status, again = built_in()
+    assert status == rg.MOE_STATUS_OK and all(torch.equal(ref[k], again[k]) for k in ref)
