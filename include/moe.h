@@ -284,7 +284,8 @@ int moe_fwd(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w
  * W_router and b_router are ignored (may be NULL).  Every token takes up k
  * routes: an empty slot runs the lowest expert that the token does not use,
  * with weight 0 (it shows as such in o->topk_idx, o->topk_w, the counts and
- * the schedule), so x must be finite in tokens without experts too.  An index
+ * the schedule; what it makes reaches neither out nor the status).  For
+ * moe_bwd_routed x must be finite in tokens without experts too.  An index
  * out of [-1, E), or a second slot of a token with the same expert, is run as
  * an empty slot and reported as MOE_STATUS_SCHEDULE_INVALID.
  * Otherwise as moe_fwd (bf16 and MXFP8 plans).

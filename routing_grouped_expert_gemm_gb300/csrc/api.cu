@@ -378,6 +378,7 @@ int forward(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, 
   p.half_tiles = c.mma_pair && c.precision == MOE_PREC_BF16 && !c.pad_odd_tiles ? 1 : 0;
   p.x = static_cast<const bf16*>(x);
   p.b_router = given ? nullptr : w->b_router;
+  p.given = given ? 1 : 0;
   p.status = reinterpret_cast<int*>(ws + L.status);
   p.stamps = reinterpret_cast<unsigned long long*>(ws + L.status + 8);
   p.counters = reinterpret_cast<int*>(ws + L.counters);

@@ -111,6 +111,7 @@ struct FwdParams {
   int n_counters;
   int l2_prefetch;      // K steps ahead that the producer prefetches into L2 (0 = off)
   int test_unfilled;    // test hook: 0 off; m + 1 = minibatch m is never marked gathered
+  int given;            // 1: the routing was given; topk_logit marks the empty slots (not 0), which concern nobody
   int clc;              // 1: GEMM CTAs get their work tokens from cluster launch control (one-CTA kernel)
   long long timeout_ns;
   // inputs
@@ -123,7 +124,8 @@ struct FwdParams {
   int* meta;
   int* topk_idx;      // [T,k]
   float* topk_w;      // [T,k]
-  float* topk_logit;  // [T,k] the selected experts' biased fp32 logits (kept for the backward pass), or null
+  float* topk_logit;  // [T,k] the selected experts' biased fp32 logits (kept for the backward pass), or null;
+                      // given routing: 1 in an empty slot, else 0
   int* chunk_counts;  // [n_chunks, E]
   int* M;             // [E]
   int* S;             // [E+1]

@@ -497,14 +497,17 @@ __device__ void epilogue_swiglu_mx(uint32_t taddr, uint8_t* dst_row, uint8_t* sf
 // row's 256-column segment.  The buffer is handed back after the last TMEM
 // read (with two accumulator buffers the MMA issuer rarely waits for it).
 // A value outside the fp16 range (or NaN) is saturated and raises
-// FLAG_STAGING_OVERFLOW in flags (the forward goes on; its status says so).
+// FLAG_STAGING_OVERFLOW in flags (the forward goes on; its status says so),
+// unless *empty, looked up only then, says that this thread's row (route) is an
+// empty slot of a given routing (NULL: it is not).
 // ncols of the warp's 32 TMEM lanes (from taddr) are output columns col0 .. col0 + ncols - 1 of
 // its rows: all 256 columns, or (a split tile: lanes 0-63 columns 0-127, lanes 64-127 columns
 // 128-255 of the same 64 rows) 128 of them
 __device__ void epilogue_copy_f16_staged(uint32_t taddr, EpiStage& st, __half* Y, long long y_mine, int nrows,
-                                         const AccRelease& rel, int* flags, int ncols = BN_DOWN, int col0 = 0) {
+                                         const AccRelease& rel, int* flags, const float* empty, int ncols = BN_DOWN,
+                                         int col0 = 0) {
   const int lane = threadIdx.x & 31;
-  bool ovf = false;
+  uint32_t ovf = 0;  // rows
 #pragma unroll 1
   for (int c = 0; c < ncols; c += 32) {
     uint32_t r[32];
@@ -523,14 +526,15 @@ __device__ void epilogue_copy_f16_staged(uint32_t taddr, EpiStage& st, __half* Y
       if (rr < nrows) {
         const float4 f = staged4(st, rr, cc);
         const float a = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
-        ovf |= !(a <= 65504.0f) || f.x != f.x || f.y != f.y || f.z != f.z || f.w != f.w;
+        ovf |= !(a <= 65504.0f) || f.x != f.x || f.y != f.y || f.z != f.z || f.w != f.w ? 1u << rr : 0u;
         *reinterpret_cast<uint2*>(Y + yr + col0 + c + cc) =
             make_uint2(pack_f16x2_sat(f.x, f.y), pack_f16x2_sat(f.z, f.w));
       }
     }
     __syncwarp();
   }
-  if (__any_sync(0xffffffffu, ovf) && lane == 0) atomicOr(flags, FLAG_STAGING_OVERFLOW);
+  ovf = __reduce_or_sync(0xffffffffu, ovf);
+  if ((ovf >> lane & 1u) && !(empty && *empty != 0.0f)) atomicOr(flags, FLAG_STAGING_OVERFLOW);
 }
 
 // BF16 CTA pairs store their epilogue rows from registers: lane l holds 32
@@ -566,9 +570,10 @@ __device__ void epilogue_swiglu_direct(uint32_t taddr, bf16* dst, bool live, con
 
 // Down-projection tile -> fp16 staging row: ncols TMEM columns from taddr are
 // output columns 0 .. ncols - 1 from yrow (all 256, or 128 for a split tile);
-// saturation at the fp16 maximum and NaN are flagged as in the staged form.
+// saturation at the fp16 maximum and NaN are flagged as in the staged form (empty
+// as there).
 __device__ void epilogue_copy_f16_direct(uint32_t taddr, __half* yrow, bool live, const AccRelease& rel, int* flags,
-                                         int ncols) {
+                                         int ncols, const float* empty) {
   bool ovf = false;
 #pragma unroll 1
   for (int c = 0; c < ncols; c += 32) {
@@ -589,7 +594,7 @@ __device__ void epilogue_copy_f16_direct(uint32_t taddr, __half* yrow, bool live
       st_global_v8(yrow + c + 16, w + 8);
     }
   }
-  if (__any_sync(0xffffffffu, ovf && live) && (threadIdx.x & 31) == 0) atomicOr(flags, FLAG_STAGING_OVERFLOW);
+  if (ovf && live && !(empty && *empty != 0.0f)) atomicOr(flags, FLAG_STAGING_OVERFLOW);
 }
 
 // ------------------------------------------------------------------ combine
@@ -1386,14 +1391,15 @@ __device__ __forceinline__ void mega_body(const TensorMaps& maps, const FwdParam
           } else if (t.kind == TASK_R2 && t.half) {
             const int j = hrow < t.rows ? p.sched[(size_t)(t.p0 + hrow) * 3 + 2] : 0;
             epilogue_copy_f16_direct(taddr, p.Y + y_offset(p, j / p.k, j % p.k, t.n) + (q >> 1) * (BN_DOWN / 2),
-                                     store_ok && hrow < t.rows, rel, p.status + 1, BN_DOWN / 2);
+                                     store_ok && hrow < t.rows, rel, p.status + 1, BN_DOWN / 2,
+                                     p.given ? p.topk_logit + j : nullptr);
           } else if (t.kind == TASK_R2) {
             const int j = row < t.rows ? p.sched[(size_t)(t.p0 + row) * 3 + 2] : 0;
             epilogue_copy_f16_direct(taddr, p.Y + y_offset(p, j / p.k, j % p.k, t.n), store_ok && row < t.rows, rel,
-                                     p.status + 1, BN_DOWN);
+                                     p.status + 1, BN_DOWN, p.given ? p.topk_logit + j : nullptr);
           } else {  // the shared expert's output: staging slot k of its tokens
             epilogue_copy_f16_direct(taddr, p.Y + y_offset(p, t.out_row + row, p.k, t.n), store_ok && row < t.rows,
-                                     rel, p.status + 1, BN_DOWN);
+                                     rel, p.status + 1, BN_DOWN, nullptr);
           }
         } else {
         EpiStage& st = epi[q];
@@ -1407,10 +1413,10 @@ __device__ __forceinline__ void mega_body(const TensorMaps& maps, const FwdParam
         } else if (t.kind == TASK_R2) {
           const int j = row < t.rows ? p.sched[(size_t)(t.p0 + row) * 3 + 2] : 0;
           epilogue_copy_f16_staged(taddr, st, p.Y, (long long)y_offset(p, j / p.k, j % p.k, t.n), nrows, rel,
-                                   p.status + 1);
+                                   p.status + 1, p.given ? p.topk_logit + j : nullptr);
         } else {  // the shared expert's output: staging slot k of its tokens
           epilogue_copy_f16_staged(taddr, st, p.Y, (long long)y_offset(p, t.out_row + row, p.k, t.n), nrows, rel,
-                                   p.status + 1);
+                                   p.status + 1, nullptr);
         }
         }
         // h tiles are read back by TMA (async proxy); Y and out only by plain loads

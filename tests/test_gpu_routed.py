@@ -234,3 +234,30 @@ def test_a_backward_of_the_other_forward_is_reported(pair):
     layer.run(x)
     status, again = built_in()
     assert status == rg.MOE_STATUS_OK and all(torch.equal(ref[k], again[k]) for k in ref)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(mma_pair=1, dispatch="spread"), dict(dispatch="direct", gather_ctas=0)])
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+def test_an_empty_slots_expert_does_not_reach_the_status(precision, kw):
+    """Expert 0 runs in every empty slot; its outputs leave fp16's range, which
+    concerns only tokens that were routed to it."""
+    inp, layer, x = layer_of(mi.custom_shape(300, 256, 128, 16, 4, 128, precision=precision), **kw)
+    s, T = inp.shape, inp.T
+    g = torch.Generator(device="cuda").manual_seed(4)
+    idx = 1 + torch.rand(T, s.E - 1, generator=g, device="cuda").argsort(1)[:, :s.k].to(torch.int32)
+    idx[torch.rand(T, s.k, generator=g, device="cuda") < 0.3] = -1
+    w = torch.rand(T, s.k, generator=g, device="cuda") + 0.1
+    ref, status = fwd_routed(layer, x, idx, w)
+    assert status == rg.MOE_STATUS_OK
+    if precision == "mxfp8":
+        big = layer.w_bf16["W_down"].clone()
+        big[0] *= 2.0 ** 40
+        rg.moe_quantize_mxfp8(layer.plan, big, s.E * s.D, s.I, layer.w["W_down"], layer.w["W_down_scale"])
+    else:
+        layer.w["W_down"][0] *= 2.0 ** 40
+    out, status = fwd_routed(layer, x, idx, w)
+    assert status == rg.MOE_STATUS_OK and torch.equal(out, ref)
+    for t in (0, 130, T - 1):  # one route to expert 0 is enough
+        i2 = idx.clone()
+        i2[t, 1] = 0
+        assert fwd_routed(layer, x, i2, w)[1] == rg.MOE_STATUS_STAGING_OVERFLOW
