@@ -178,18 +178,26 @@ __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + 
 // -83).  Softmax, d = m - x: e^-d is off by 2.22 d + 3; the row's sum by the
 // scores' mean of that (their mean d is at most ln 512) and its roundings, 38; the
 // reciprocal 2: s (2.22 d + 43), so at most 0.82 + 43 s, relative at most 228.
-// Then the rounding of s + b.  s is at most |key| + max |b|.
+// Then the rounding of s + b, |f|.
+// Bounds of s: it is at most 1, and at most |f| + |b|.  Of keys up to 2 in size
+// (with a neighbour this side of 3) the biases are at most 4: bmax is the largest
+// |b| of those only, so that an expert held out or forced by a large bias does
+// not make every row's border a close one (16384 x 256 with one expert at -1e4:
+// 1.0 to 2.5 ms in place of 14 to 28 us).
+constexpr float ROUTE_BIAS = 4.0f;
 template <bool kSoft>
 __device__ __forceinline__ float key_tol(float f, float bmax) {
-  const float a = fabsf(f) + bmax;
-  return fminf(ROUTE_REL * a + ROUTE_TINY, ROUTE_U * (1.0f + (kSoft ? 45.0f : 5.0f) * a));
+  const float a = fminf(fabsf(f), FLT_MAX);  // (an infinite key is exact, and far from every finite one)
+  const float s = a > 2.0f ? 1.0f : fminf(a + bmax, 1.0f);
+  return fminf(ROUTE_REL * s + ROUTE_TINY, ROUTE_U * (1.0f + (kSoft ? 44.0f : 4.0f) * s)) + 1.25f * ROUTE_U * a;
 }
-// The same for sums of two keys (of the scores, 43 or 3 times |f| + 2 max |b|; of
-// the keys' sizes |f| + 4 max |b|; of the sum itself).
+// How far a group's score, the sum of its keys f1 and f2 (0 for none), may be off:
+// each key's error as above, and the sum's rounding.
 template <bool kSoft>
-__device__ __forceinline__ float group_tol(float f, float bmax) {
-  const float a = fabsf(f) + 4.0f * bmax;
-  return fminf(ROUTE_REL * a + ROUTE_TINY, ROUTE_U * (2.0f + (kSoft ? 46.0f : 6.0f) * a));
+__device__ __forceinline__ float group_err(float score, float f1, float f2, float bmax) {
+  const float a = fabsf(f1) + fabsf(f2), s = a > 2.0f ? 2.0f : fminf(a + 2.0f * bmax, 2.0f);
+  const float of_scores = fminf(0.5f * ROUTE_REL * s + ROUTE_TINY, ROUTE_U * (1.0f + (kSoft ? 22.0f : 2.0f) * s));
+  return of_scores + 0.625f * ROUTE_U * fminf(a + fabsf(score), FLT_MAX);
 }
 // e^(x - m), m the row's maximum; an infinite one is its own limit, those logits share the row
 __device__ __forceinline__ float soft_score(float x, float m) {
@@ -298,7 +306,8 @@ __device__ __noinline__ unsigned groups_fp64(const RouteParams& p, const void* r
 // lanes) is one of the `need` with the largest keys.  Softmax: z32, the row's
 // sum in fp32 (off by less than 2.4e-6), scales all of the candidates' scores
 // alike, so it decides unless the border is within that of how far they lie
-// apart; the sum in fp64 costs more than all the rest.  Whole warp.
+// apart (and the keys' own roundings); the sum in fp64 costs more than all the
+// rest.  Whole warp.
 template <int V, bool kSoft>
 __device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, int e, int need, float m32, float z32) {
   const int lane = threadIdx.x & 31;
@@ -320,7 +329,7 @@ __device__ __noinline__ bool band_fp64(const RouteParams& p, const void* row, in
       const float far = max32(e >= 0 ? s32 : -INFINITY) + max32(e >= 0 ? -s32 : -INFINITY);  // largest less smallest
       const double lo = ord_to64(~max32_64(in ? ~key : 0ull));
       const unsigned long long out = max32_64(e >= 0 && !in ? key : 0ull);
-      if (!out || lo - ord_to64(out) > 2.4e-6 * (double)far + 1e-15) break;
+      if (!out || lo - ord_to64(out) > 2.4e-6 * (double)far + 1e-15 + 4.5e-16 * fabs(lo)) break;
     }
   }
   return in;
@@ -376,16 +385,15 @@ __device__ __forceinline__ void keys_again(const RouteParams& p, const void* row
   }
 }
 
-// Groups whose scores are too close to the border: lane g has group g's score
-// (0: none), its smaller key that counts, and whether it ranks as kept; scores
-// in [lo, hi] may lie on either side.  The kept groups, as bits.  Whole warp.
+// Groups whose scores are too close to the border: lane g has group g's smaller
+// key that counts, whether it ranks as kept and whether it may lie on either
+// side.  The kept groups, as bits.  Whole warp.
 template <int V, bool kSoft>
-__device__ __noinline__ unsigned decide_groups(const RouteParams& p, const void* row, uint32_t score, uint32_t least, bool in,
-                                               float lo, float hi, float m, float inv_z, float bmax, int* buf) {
+__device__ __noinline__ unsigned decide_groups(const RouteParams& p, const void* row, uint32_t least, bool in, bool band,
+                                               float m, float inv_z, float bmax, int* buf) {
   const int lane = threadIdx.x & 31, e0 = lane * V;
   uint32_t key[V], cand = 0;
   keys_again<V, kSoft>(p, row, m, inv_z, !p.bias && p.group_top > 1, key);
-  const bool band = lane < p.n_group && score && ord_to(score) >= lo && ord_to(score) <= hi;
   // in those groups, the keys that may be among their largest
   uint32_t from = 0xffffffffu;
   if (band) {
@@ -534,7 +542,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const float v = e0 + j < p.E ? p.bias[e0 + j] : 0.0f;
-      bmax = fmaxf(bmax, fabsf(v) < INFINITY ? fabsf(v) : 0.0f);
+      bmax = fmaxf(bmax, fabsf(v) <= ROUTE_BIAS ? fabsf(v) : 0.0f);
       bias[j] = v == v ? v : -INFINITY;
     }
     __syncwarp();
@@ -688,7 +696,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
           a = a == thr ? -INFINITY : a;
         }
       }
-      bool in = score > -INFINITY && score >= thr, tied = false;
+      bool in = score > -INFINITY && score >= thr;
       unsigned kept = __ballot_sync(0xffffffffu, in);
       if (__popc(kept) > p.topk_group) {  // (equal scores count once above)
         s_key[warp][lane] = score;
@@ -699,22 +707,20 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32, route_ctas_per_sm(V)) route_
         in = in && rank < p.topk_group;
         kept = __ballot_sync(0xffffffffu, in);
         thr = redux_min(in ? score : INFINITY);
-        tied = __popc(kept) > p.topk_group;
-        if (tied) {  // equal scores across the border: the lowest groups
+        if (__popc(kept) > p.topk_group) {  // equal scores across the border: the lowest groups
           const unsigned over = __ballot_sync(0xffffffffu, in && score > thr), same = kept & ~over;
           in = in && (score > thr || __popc(same & lt) < p.topk_group - __popc(over));
           kept = __ballot_sync(0xffffffffu, in);
         }
       }
       if (group_scores) {
-        const float hi = tied ? thr : redux_max(in ? -INFINITY : score);
-        if (hi > -INFINITY) {
-          const float tol = group_tol<kSoft>(thr, bmax);
-          if (!(thr - hi > tol)) {
-            kept = decide_groups<V, kSoft>(p, row, score > -INFINITY ? ord_of(score) : 0u,
-                                           ord_of(p.group_top > 1 && g2 > -INFINITY ? g2 : g1), in, hi - tol, thr + tol, m, inv_z,
-                                           bmax, s_id[warp]);
-          }
+        // each group's own error: one of large biases may be far off without its being near the border
+        const bool two = p.group_top > 1 && g2 > -INFINITY;
+        const float err = group_err<kSoft>(score, g1, two ? g2 : 0.0f, bmax);
+        const float hi = redux_max(in ? -INFINITY : score + err), lo = redux_min(in ? score - err : INFINITY);
+        if (hi > -INFINITY && !(lo > hi)) {
+          const bool band = score > -INFINITY && (in ? score - err <= hi : score + err >= lo);
+          kept = decide_groups<V, kSoft>(p, row, ord_of(two ? g2 : g1), in, band, m, inv_z, bmax, s_id[warp]);
         }
       }
       kept_groups = kept;

@@ -641,3 +641,62 @@ def test_many_near_borders(fn, spread):
     bias = (0.5 - s).float()
     for kw in (dict(), dict(n_group=8, topk_group=4), dict(n_group=12, topk_group=5, group_top=1)):
         check_route(x, bias, cfg_of(E, 8, fn=fn, **kw))
+
+
+FMAX = float(torch.finfo(torch.float32).max)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("out", [-1e4, -1e9, 1e9, -FMAX, float("inf")])
+@pytest.mark.parametrize("kw", [dict(), dict(n_group=8, topk_group=4)])
+def test_a_few_far_biases_do_not_slow_every_row(fn, out, kw):
+    """Experts held out or forced by a bias: the rows' borders are as far from
+    fp32's error as before, so a call takes as long (within half of it)."""
+    T, E = 16384, 256
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, E, generator=g, device="cuda") * 1.5
+    bias = (torch.rand(E, generator=g, device="cuda") - 0.5) * 0.1
+    far = bias.clone()
+    far[[3, 77, 130, 131]] = out
+    plan = rg.moe_route_plan_create(**cfg_of(E, 8, fn=fn, **kw))
+    idx = torch.empty(T, 8, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, 8, device="cuda")
+
+    def ms(b):
+        best = float("inf")
+        for _ in range(5):
+            a, z = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(20):
+                rg.moe_route(plan, T, x, b, idx, w)
+            z.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(z) / 20)
+        return best
+
+    ms(bias)
+    assert ms(far) <= 1.5 * ms(bias)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [3.0, 1e4, 1e9, FMAX])
+@pytest.mark.parametrize("sign", [-1, 1, 0])
+def test_biases_far_outside_the_scores_range(fn, size, sign):
+    """Experts held out (or forced) by a large finite bias, or some of both (sign
+    0): few of them, and so many that held-out ones must be selected too."""
+    T, E = 120, 96
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(T, E, generator=g, device="cuda") * 1.5
+    x[::5] = torch.randint(-2, 3, (len(x[::5]), E), generator=g, device="cuda").float()
+    for n_out in (2, 40, 92):
+        bias = (torch.rand(E, generator=g, device="cuda") - 0.5) * 0.1
+        out = torch.randperm(E, generator=g, device="cuda")[:n_out]
+        how = torch.full((n_out,), float(sign or 1), device="cuda")
+        if sign == 0:
+            how[::2] = -1.0
+        bias[out] = size * how
+        for kw in (dict(), dict(n_group=8, topk_group=3), dict(n_group=8, topk_group=3, group_top=1),
+                   dict(n_group=12, topk_group=5)):
+            check_route(x, bias, cfg_of(E, 6, fn=fn, **kw))
