@@ -528,7 +528,11 @@ int moe_route_bwd(const moe_route_plan* plan, int64_t T, const void* logits, int
  *                      1..65536, rows * cols up to 2^30
  *   steps              Newton-Schulz steps, 1..32 (0 = 5)
  *   grad_dtype         moe_dtype of the gradient
- *   a, b, c            the step's coefficients, finite (all 0 = 3.4445, -4.7750, 2.0315)
+ *   a, b, c            the step's coefficients, finite (all 0 = 3.4445, -4.7750, 2.0315).
+ *                      Iterates, A and b A + c A^2 are held in fp16 and must stay
+ *                      below 16: coefficients with which the singular values 0..1
+ *                      of X can lead out of that (or within 1% a step of it) are
+ *                      refused (MOE_ERR_INVALID_ARG)
  *   timeout_ms         limit of every device-side wait (0 = 2000 ms)
  */
 typedef struct moe_muon_config {
@@ -563,10 +567,9 @@ size_t moe_muon_workspace_bytes(const moe_muon_plan* plan);
  *   workspace at least moe_muon_workspace_bytes(plan) bytes, 256-byte aligned,
  *             no initialisation needed
  * A matrix of zeros gives zeros; a matrix with an infinity or a NaN gives NaN,
- * without touching the others.  The step's iterates must stay below 15 in
- * absolute value (the default coefficients keep them below 1.3).  Two calls on
- * the same inputs give the same bits.  No host synchronisation; a device-side
- * wait that ran out is reported by moe_muon_get_status.
+ * without touching the others.  Two calls on the same inputs give the same
+ * bits.  No host synchronisation; a device-side wait that ran out is reported by
+ * moe_muon_get_status.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
  */
 int moe_muon_update(const moe_muon_plan* plan, const void* grad, int64_t grad_row_stride, int64_t grad_stride,

@@ -25,11 +25,13 @@
 //
 // Scales.  fp16 has 5 exponent bits, so X_0 is U 2^k with |U 2^k|_F in
 // [2^14, 2^15): no element overflows, and those down to 2^-28 of the norm keep
-// their 11 bits.  Later iterates, A and B are held times 2^12 (|X|_2 < 1.3 for the
-// default coefficients, so below 16 on their side too); the factors, and what
-// is left of 1 / |U|_F, are applied to the fp32 sums.
+// their 11 bits.  Later iterates, A and B are held times 2^12, so they must stay
+// below 16 (|X|_2 < 1.3 for the default coefficients; others are checked when the
+// plan is made, ns_in_range); the factors, and what is left of 1 / |U|_F, are
+// applied to the fp32 sums.
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <cstring>
 #include <new>
 #include <type_traits>
@@ -1145,6 +1147,35 @@ struct moe_muon_plan {
 
 namespace {
 
+// Whether every iterate, A and B stay in range: held as fp16 times 4096, they
+// must not reach 16.  A singular value of X is at most 1 at the start and goes
+// through s -> a s + b s^3 + c s^5 each step; an element of X is at most the
+// largest, one of A or B beside the diagonal (which is kept in fp32) half of the
+// spread of the eigenvalues.  1% a step for the products' own errors, and 15 of 16.
+bool ns_in_range(const moe_muon_config& cfg) {
+  const double a = cfg.a, b = cfg.b, c = cfg.c, most = 15.0;
+  double S = 1.01;  // bound of the singular values
+  for (int i = 0; i < cfg.steps; ++i) {
+    const double t = S * S;  // of A's eigenvalues, 0 .. t
+    auto poly = [&](double u) { return u * (b + c * u); };  // of B's
+    const double turn = c != 0.0 ? -b / (2.0 * c) : -1.0, inner = turn > 0.0 && turn < t ? poly(turn) : 0.0;
+    const double hi = fmax(fmax(0.0, poly(t)), inner), lo = fmin(fmin(0.0, poly(t)), inner);
+    if (!(t <= 2.0 * most) || !(hi - lo <= 2.0 * most)) return false;
+    // |s (a + b u + c u^2)|, u = s^2: at the end, or where a + 3 b u + 5 c u^2 = 0
+    auto at = [&](double u) { return u > 0.0 && u < t ? fabs(sqrt(u) * (a + u * (b + c * u))) : 0.0; };
+    double next = fabs(S * (a + t * (b + c * t)));
+    if (c != 0.0) {
+      const double d = 9.0 * b * b - 20.0 * a * c;
+      if (d >= 0.0) next = fmax(next, fmax(at((-3.0 * b + sqrt(d)) / (10.0 * c)), at((-3.0 * b - sqrt(d)) / (10.0 * c))));
+    } else if (b != 0.0) {
+      next = fmax(next, at(-a / (3.0 * b)));
+    }
+    S = 1.01 * next;
+    if (i + 1 < cfg.steps && !(S <= most)) return false;  // (the last one is the update, in bf16)
+  }
+  return true;
+}
+
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 bool ns_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -1301,6 +1332,7 @@ int moe_muon_plan_create(const moe_muon_config* cfg, moe_muon_plan** out) {
   if (c.a == 0.0f && c.b == 0.0f && c.c == 0.0f) c.a = 3.4445f, c.b = -4.7750f, c.c = 2.0315f;
   if (c.grad_dtype < MOE_DTYPE_FP32 || c.grad_dtype > MOE_DTYPE_FP16 || c.steps < 1 || c.steps > 32) return MOE_ERR_INVALID_ARG;
   if (!(c.a - c.a == 0.0f) || !(c.b - c.b == 0.0f) || !(c.c - c.c == 0.0f)) return MOE_ERR_INVALID_ARG;  // finite
+  if (!ns_in_range(c)) return MOE_ERR_INVALID_ARG;
   if (c.count < 1 || c.count > 65536 || c.rows < 1 || c.rows > 65536 || c.cols < 1 || c.cols > 65536 ||
       c.rows * c.cols > (int64_t)1 << 30)
     return MOE_ERR_UNSUPPORTED_SHAPE;

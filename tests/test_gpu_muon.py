@@ -310,3 +310,38 @@ def test_a_matrix_does_not_depend_on_its_stack(rows, cols):
         m1 = m0[i:i + 1].clone()
         assert torch.equal(out[i], run(grad[i:i + 1].contiguous(), m1, "bf16", 1, rows, cols)[0])
         assert torch.equal(mom[i], m1[0])
+
+
+# ---------------------------------------------------------------- the coefficients' range
+@pytest.mark.parametrize("steps,coefs", [
+    (2, (6.0, 0.0, 0.0)),      # |X|_2 6 after a step: A's elements up to 18
+    (1, (1.0, 40.0, 0.0)),     # B's elements up to 20
+    (1, (1.0, 0.0, -40.0)),
+    (3, (3.0, 0.0, 0.0)),      # 9 after two steps
+    (32, (1.2, 0.0, 0.0)),
+    (1, (1.0, 3e38, 3e38)),
+    (32, (3e38, 3e38, 3e38)),
+])
+def test_coefficients_whose_iterates_leave_fp16_are_refused(L, steps, coefs):
+    with pytest.raises(rg.MoEError) as ei:
+        rg.moe_muon_plan_create(2, 16, 16, steps=steps, coefficients=coefs)
+    assert ei.value.code == rg.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols", [(64, 96), (96, 64), (200, 264), (264, 200)])
+@pytest.mark.parametrize("steps,coefs", [(2, (5.2, 0.0, 0.0)), (1, (1.0, 28.0, 0.0)), (1, (100.0, 0.0, 0.0)),
+                                         (3, (2.2, 0.0, 0.0))])
+def test_coefficients_near_the_limit(rows, cols, steps, coefs):
+    """One direction only, two of the short side's indices sharing it: the
+    largest element that A and B can have beside their diagonals.  Nothing cancels
+    here (all terms have one sign), so the file's tolerance holds."""
+    short = torch.zeros(min(rows, cols), device="cuda")
+    short[3] = short[min(rows, cols) - 5] = 1.0
+    long = torch.randn(max(rows, cols), device="cuda")
+    m = torch.outer(short, long) if rows <= cols else torch.outer(long, short)
+    grad = torch.stack([m, torch.randn(rows, cols, device="cuda")])
+    ref, _ = plain(grad, None, steps=steps, coefs=coefs)
+    out = run(grad, None, "fp32", 2, rows, cols, steps=steps, coefficients=coefs)
+    for i in range(2):
+        assert rel(out[i], ref[i]) <= TOL
