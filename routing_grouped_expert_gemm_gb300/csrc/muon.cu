@@ -552,11 +552,12 @@ __host__ __device__ constexpr int prep_unroll(int V) { return V == 8 ? 2 : 8; }
 
 // Sums of squares in three sums of their own: values far from 1 are squared
 // in scaled form, so that no finite matrix has an infinite norm and none that
-// is not zero has a zero one.
+// is not zero has a zero one.  (Squares up to 2^96, and up to 2^30 of them: below
+// 2^126.  The smallest, of 2^-149, is 2^-106.)
 __device__ __forceinline__ void add_square(float (&f)[3], float u) {
   const float a = fabsf(u);
-  const bool big = a >= 0x1p50f, small = a < 0x1p-50f;
-  const float v = u * (big ? 0x1p-80f : small ? 0x1p100f : 1.0f);
+  const bool big = a >= 0x1p48f, small = a < 0x1p-48f;
+  const float v = u * (big ? 0x1p-80f : small ? 0x1p96f : 1.0f);
   f[0] += small ? v * v : 0.0f;
   f[1] += big || small ? 0.0f : v * v;
   f[2] += big ? v * v : 0.0f;
@@ -579,7 +580,7 @@ __device__ __forceinline__ void block_sum3(float (&f)[3], float (*s)[8]) {
 // matrix of zeros, NaN where the norm is not finite, which makes every element
 // of that matrix's result NaN).
 __device__ __forceinline__ void norm_scale(const float (&f)[3], float* f1, float* f2, float* rho) {
-  const double norm = sqrt((double)f[0] * 0x1p-200 + (double)f[1] + (double)f[2] * 0x1p160);
+  const double norm = sqrt((double)f[0] * 0x1p-192 + (double)f[1] + (double)f[2] * 0x1p160);
   *f1 = *f2 = *rho = 0.0f;
   if (!(norm < (double)INFINITY)) {
     *rho = NAN;

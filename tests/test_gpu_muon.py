@@ -345,3 +345,16 @@ def test_coefficients_near_the_limit(rows, cols, steps, coefs):
     out = run(grad, None, "fp32", 2, rows, cols, steps=steps, coefficients=coefs)
     for i in range(2):
         assert rel(out[i], ref[i]) <= TOL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [50, -50])
+def test_norms_of_large_matrices_do_not_overflow(power):
+    """2^28 and more elements just below 2^50, or 2^-50: the squares' sums reach
+    2^128 where the elements are taken as they are (or times 2^100)."""
+    rows, cols = 16384, 16640
+    grad = (torch.randint(0, 2, (1, rows, cols), device="cuda", dtype=torch.int8) * 2 - 1).bfloat16() * (1 - 2.0 ** -8)
+    assert float(grad[0, 0].abs().max()) < 1.0
+    ref = run(grad, None, "bf16", 1, rows, cols, steps=1)
+    out = run(grad * 2.0 ** power, None, "bf16", 1, rows, cols, steps=1)
+    assert bool(torch.isfinite(ref).all()) and torch.equal(out, ref)
