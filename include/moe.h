@@ -492,8 +492,12 @@ size_t moe_route_workspace_bytes(const moe_route_plan* plan, int64_t T);
  * An expert whose logit is -inf or NaN is never selected (a row of them has no
  * experts).  A NaN makes the row's softmax weights, and prob_sum, NaN.  Ties
  * go to the lower id, of groups to the lower group.  The selection is that of
- * exact arithmetic: rows whose keys lie closer than fp32 resolves are decided
- * in fp64.  No floating-point atomics: two calls give the same bits.
+ * keys and groups' scores computed in fp64 from the logits and biases: where
+ * they lie closer than fp32 resolves they are, elsewhere fp32 gives the same.
+ * So keys that fp64 does not tell apart are ties -- sigmoid scores of logits
+ * above 37 (all 1), or scores added to a bias some 1e16 times their size -- also
+ * with a bias of zeros, whereas without a bias the logits themselves decide.
+ * No floating-point atomics: two calls give the same bits.
  * One launch, and a second one for the sums of more than 8 tokens.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
  */

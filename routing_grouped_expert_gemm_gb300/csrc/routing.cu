@@ -7,15 +7,15 @@
 // keep in order), inside the topk_group groups whose sums of the group_top
 // largest keys are largest; the weights come from s alone.
 //
-// The selection is that of exact arithmetic.  Keys are computed in fp32 with a
-// known error; where values on both sides of a border (of the kept groups, or
-// of the k-th key) lie within that error of it, and are not exact ties (the
-// same logit and bias, decided by the lower id), the warp decides that border
-// again in fp64, computing the few keys that lie in the band (all of them for
-// groups).  With fp32 logits one row of some thousands is that close (16384 x
-// 256 in 8 groups: 2 rows at the k-th key, 0.7 at the groups' border, which takes
-// the warp 4 us and a call 2 to 3); fp32 alone would pick another expert in some rows of a
-// large batch.
+// The selection is that of fp64 keys (equal ones: the lower id).  Keys are
+// computed in fp32 with a known error; where values on both sides of a border
+// (of the kept groups, or of the k-th key) lie within that error of it, and are
+// not exact ties (the same logit and bias), the warp decides that border again
+// in fp64, computing the few keys that lie in the band (for groups those that
+// may be among the largest of a group in the band).  With fp32 logits one row of
+// some thousands is that close (16384 x 256 in 8 groups: 2 rows at the k-th key,
+// 0.7 at the groups' border, which takes the warp 4 us and a call 2 to 3); fp32
+// alone would pick another expert in some rows of a large batch.
 //
 // 16384 x 256 fp32 in 8 groups: 15.4 us, with the sums 19.5 us (17 MB at the
 // copy rate would be 2.6 us; DRAM is at 8%, instruction issue at 56 to 68%);

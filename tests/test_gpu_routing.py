@@ -700,3 +700,13 @@ def test_biases_far_outside_the_scores_range(fn, size, sign):
         for kw in (dict(), dict(n_group=8, topk_group=3), dict(n_group=8, topk_group=3, group_top=1),
                    dict(n_group=12, topk_group=5)):
             check_route(x, bias, cfg_of(E, 6, fn=fn, **kw))
+
+
+@pytest.mark.gpu
+def test_saturated_scores_tie_as_in_fp64():
+    """The keys are those of fp64: 1 / (1 + e^-40) and 1 / (1 + e^-41) are both 1
+    there, so with a bias the lower id wins; without one the logits decide."""
+    x = torch.tensor([[40.0, 41.0, 0.0], [41.0, 40.0, 0.0], [-800.0, -790.0, -900.0]], device="cuda")
+    for bias, want in ((torch.zeros(3, device="cuda"), [[0], [0], [0]]), (None, [[1], [0], [1]])):
+        _, idx, _, _, _ = run_route(x, bias, cfg_of(3, 1))
+        assert idx.tolist() == want
