@@ -358,3 +358,110 @@ def test_norms_of_large_matrices_do_not_overflow(power):
     ref = run(grad, None, "bf16", 1, rows, cols, steps=1)
     out = run(grad * 2.0 ** power, None, "bf16", 1, rows, cols, steps=1)
     assert bool(torch.isfinite(ref).all()) and torch.equal(out, ref)
+
+
+# ---------------------------------------------------------------- both forms
+# (rows, cols, one launch): a cluster per matrix on chip, or the steps as launches of their own
+FORMS = [(70, 90, True), (90, 70, True), (67, 131, True), (200, 264, False), (264, 200, False), (257, 131, False), (131, 257, False)]
+
+
+def assert_form(rows, cols, one_launch, count=2, **kw):
+    """The one-launch form's workspace holds the status only."""
+    plan = rg.moe_muon_plan_create(count, rows, cols, **kw)
+    assert (rg.moe_muon_workspace_bytes(plan) == 256) == one_launch
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,one_launch", FORMS)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("nesterov,momentum", [(True, True), (False, True), (True, False)])
+def test_types_and_momentum_in_both_forms(rows, cols, one_launch, dtype, nesterov, momentum):
+    assert_form(rows, cols, one_launch, 3)
+    grad = (stack(3, rows, cols, "decaying", 1) * 1e-2).to(DTYPES[dtype])
+    mom = stack(3, rows, cols, "flat", 2) * 1e-2 if momentum else None
+    ref, rm = plain(grad, mom, mu=0.9, nesterov=nesterov)
+    out = run(grad, mom, dtype, 3, rows, cols, mu=0.9, nesterov=nesterov)
+    assert rel(out, ref) <= TOL
+    if momentum:
+        assert float((mom.double() - rm).abs().max()) <= 2 ** -23 * float(rm.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,one_launch", FORMS)
+@pytest.mark.parametrize("steps,coefs", [(1, COEFS), (2, COEFS), (4, COEFS), (3, (1.875, -1.25, 0.375)), (10, (1.5, -0.5, 0.0))])
+def test_steps_and_coefficients_in_both_forms(rows, cols, one_launch, steps, coefs):
+    assert_form(rows, cols, one_launch)
+    grad = stack(2, rows, cols, "flat", 4)
+    ref, _ = plain(grad, None, steps=steps, coefs=coefs, scale=0.3)
+    out = run(grad, None, "fp32", 2, rows, cols, steps=steps, coefficients=coefs, scale=0.3)
+    # as in test_steps_and_coefficients
+    assert rel(out, ref) <= 2 * np.sqrt(4.0 * steps) * 2.0 ** -11 / np.sqrt(3.0) + 2.0 ** -9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,one_launch", FORMS)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_strides_in_both_forms(rows, cols, one_launch, dtype):
+    assert_form(rows, cols, one_launch, 3)
+    mom0 = stack(3, rows, cols, "flat", 2)
+    for pad, extra, off in ((0, 0, 1), (8, 0, 0), (5, 3, 2), (24, 1, 8)):
+        base = torch.randn(3 * (rows + extra) * (cols + pad) + off, device="cuda").to(DTYPES[dtype])
+        view = base[off:].view(3, rows + extra, cols + pad)[:, :rows, :cols]
+        mom = mom0.clone()
+        ref, rm = plain(view, mom)
+        out = run(view.data_ptr(), mom, dtype, 3, rows, cols, grad_row_stride=cols + pad,
+                  grad_stride=(rows + extra) * (cols + pad))
+        assert rel(out, ref) <= TOL
+        assert float((mom.double() - rm).abs().max()) <= 2 ** -23 * float(rm.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,one_launch", FORMS)
+def test_bad_matrices_keep_to_themselves_in_both_forms(rows, cols, one_launch):
+    assert_form(rows, cols, one_launch, 5)
+    grad = stack(5, rows, cols, "flat", 8)
+    ref = run(grad, None, "fp32", 5, rows, cols)
+    bad = grad.clone()
+    bad[1] = 0
+    bad[2, 3, 4] = float("-inf")
+    bad[3, rows - 1, cols - 1] = float("nan")
+    out = run(bad, None, "fp32", 5, rows, cols)
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[4], ref[4])
+    assert bool((out[1] == 0).all()) and bool(torch.isnan(out[2]).all()) and bool(torch.isnan(out[3]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,one_launch", FORMS)
+@pytest.mark.parametrize("power", [-140, -100, 45, 60, 110])
+def test_magnitudes_in_both_forms(rows, cols, one_launch, power):
+    """As test_magnitudes_outside_the_squares_range."""
+    assert_form(rows, cols, one_launch)
+    grad = torch.randint(-8, 9, (2, rows, cols), device="cuda").float()
+    ref = run(grad, None, "fp32", 2, rows, cols)
+    out = run(torch.ldexp(grad, torch.tensor(power, device="cuda")), None, "fp32", 2, rows, cols)
+    assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,one_launch", FORMS)
+def test_one_element_in_both_forms(rows, cols, one_launch):
+    assert_form(rows, cols, one_launch, 1)
+    grad = torch.zeros(1, rows, cols, device="cuda")
+    grad[0, rows - 2, cols - 3] = 3.0
+    out = run(grad, None, "fp32", 1, rows, cols)
+    want = 1.0
+    for _ in range(5):
+        want = COEFS[0] * want + COEFS[1] * want ** 3 + COEFS[2] * want ** 5
+    assert abs(float(out[0, rows - 2, cols - 3]) - want) <= TOL * abs(want)
+    assert int((out != 0).sum()) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,kind", [(2048, 7168, "decaying"), (7168, 2048, "flat"), (2049, 3333, "low rank")])
+def test_large_matrices_match_fp64(rows, cols, kind):
+    grad = stack(2, rows, cols, kind, 5).bfloat16()
+    mom = stack(2, rows, cols, kind, 6)
+    ref, rm = plain(grad, mom, scale=0.2)
+    out = run(grad, mom, "bf16", 2, rows, cols, scale=0.2)
+    assert rel(out, ref) <= TOL
+    assert float((mom.double() - rm).abs().max()) <= 2 ** -23 * float(rm.abs().max())

@@ -710,3 +710,76 @@ def test_saturated_scores_tie_as_in_fp64():
     for bias, want in ((torch.zeros(3, device="cuda"), [[0], [0], [0]]), (None, [[1], [0], [1]])):
         _, idx, _, _, _ = run_route(x, bias, cfg_of(3, 1))
         assert idx.tolist() == want
+
+
+def rare_experts(T, E, seed):
+    """Logits whose experts' popularity falls by up to e^-20."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T, E, generator=g, device="cuda") * 1.5
+    return x - torch.linspace(0.0, 20.0, E, device="cuda")[torch.randperm(E, generator=g, device="cuda")]
+
+
+def score_error(xn, fn):
+    """Relative error of a score or its share of the row: the exponential's
+    2.22 d + 3 units of 2^-24 (d its argument), the row's sum and reciprocal 40."""
+    d = (xn.max(1, keepdims=True) - xn).max() if fn == "softmax" else np.abs(xn).max()
+    return (2.22 * d + 43) * U32
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E", [(600, 160), (5000, 96)])
+def test_sums_and_weights_of_rare_experts(fn, T, E):
+    """Element by element, relative to the element: all terms are positive.  The
+    sums over the tokens add 64 units at most (runs of a few rows, 8 warps, up to
+    15 partials in each of 32 warps); a weight adds exp's 2, |x - m| and 4."""
+    x = rare_experts(T, E, 17)
+    xn = x.double().cpu().numpy()
+    plan, idx, w, _, ps = run_route(x, None, cfg_of(E, 9, fn=fn, renorm=False, scale=2.5))
+    _, rw, _, rp = plain_route_rows(xn, None, 9, fn, 1, 1, 2, False, 2.5)
+    err = score_error(xn, fn)
+    assert np.all(np.abs(ps.double().cpu().numpy() - rp) <= (err + 64 * U32) * rp)
+    assert np.all(np.abs(w.double().cpu().numpy() - rw) <= (err + 16 * U32) * rw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("sums", [True, False])
+def test_gradients_of_rare_experts(fn, renorm, sums):
+    """Element by element, relative to the terms that make the element up (which
+    cancel): a score times (the gradient of it, and the row's mean of those); both
+    scores' errors, 64 units for the mean's sum and the products."""
+    T, E, k, scale = 600, 160, 9, 2.5
+    x = rare_experts(T, E, 18)
+    g = torch.Generator(device="cuda").manual_seed(19)
+    plan, idx, w, _, _ = run_route(x, None, cfg_of(E, k, fn=fn, renorm=renorm, scale=scale))
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    dps = torch.randn(E, generator=g, device="cuda") if sums else None
+    d = torch.full((T, E), float("nan"), device="cuda")
+    rg.moe_route_bwd(plan, T, x, idx, dw, d, dprob_sum=dps)
+    xn, i, a = x.double().cpu().numpy(), idx.cpu().numpy().astype(np.int64), dw.double().cpu().numpy()
+    s = scores(xn, fn)
+    share = s / s.sum(1, keepdims=True)
+    q = np.take_along_axis(s, i, 1)
+    if renorm:
+        q = q / q.sum(1, keepdims=True)
+    # the formula itself (the other tests hold it against autograd and differences, whose own rounding is far above
+    # these elements), and beside it its terms' sizes
+    part = scale * q * (a - ((q * a).sum(1, keepdims=True) if renorm else 0.0))
+    most = scale * q * (np.abs(a) + ((q * np.abs(a)).sum(1, keepdims=True) if renorm else 0.0))
+    ref, size = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(ref, i, part, 1)
+    np.put_along_axis(size, i, most, 1)
+    if fn == "softmax" and not renorm:
+        ref -= s * part.sum(1, keepdims=True)
+        size += s * most.sum(1, keepdims=True)
+    if sums:
+        b = dps.double().cpu().numpy()
+        ref += share * (b - (share * b).sum(1, keepdims=True))
+        size += share * (np.abs(b) + (share * np.abs(b)).sum(1, keepdims=True))
+    if fn == "sigmoid":
+        ref /= 1.0 + np.exp(xn)
+        size /= 1.0 + np.exp(xn)
+    tol = (2 * score_error(xn, fn) + 64 * U32) * size
+    assert np.all(np.abs(d.double().cpu().numpy() - ref) <= tol)
