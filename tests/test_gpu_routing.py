@@ -783,3 +783,41 @@ def test_gradients_of_rare_experts(fn, renorm, sums):
         size /= 1.0 + np.exp(xn)
     tol = (2 * score_error(xn, fn) + 64 * U32) * size
     assert np.all(np.abs(d.double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40, 3000])
+def test_logits_written_just_before_the_call(T):
+    """The launch is set up while the kernels before it run: it must see what they
+    write, call after call into the same buffers."""
+    E, k = 256, 8
+    cfg = cfg_of(E, k, n_group=8, topk_group=4)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    xs = torch.randn(8, T, E, generator=g, device="cuda")
+    bias = torch.rand(E, generator=g, device="cuda") * 0.1
+    dw = torch.randn(T, k, generator=g, device="cuda")
+    plan = rg.moe_route_plan_create(**cfg)
+    ws = torch.empty(rg.moe_route_workspace_bytes(plan, T), dtype=torch.uint8, device="cuda")
+
+    def call(x, idx, w, cnt, ps, d):
+        rg.moe_route(plan, T, x, bias, idx, w, cnt, ps, ws)
+        rg.moe_route_bwd(plan, T, x, idx, dw, d, dprob_sum=bias)
+
+    def outputs():
+        return (torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda"),
+                torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E, device="cuda"), torch.empty(T, E, device="cuda"))
+
+    want = []
+    for i in range(8):
+        torch.cuda.synchronize()
+        want.append(outputs())
+        call(xs[i], *want[-1])
+    torch.cuda.synchronize()
+    x, out = torch.empty_like(xs[0]), outputs()
+    for rep in range(40):
+        i = rep % 8
+        x.copy_(xs[i])
+        call(x, *out)
+        x.mul_(2.0)  # (after them: reads of this call must not see it)
+        same = [torch.equal(a, b) for a, b in zip(out, want[i])] if rep >= 32 else None
+        assert same is None or all(same), same
