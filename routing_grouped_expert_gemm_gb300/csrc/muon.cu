@@ -1292,8 +1292,8 @@ int small_prepare(moe_muon_plan* pl) {
   int fit = 0;
   if (cudaOccupancyMaxActiveClusters(&fit, k, &lc) != cudaSuccess) return MOE_ERR_CUDA;
   // Few clusters of 16 run at once (SMs of one GPC), so with many matrices the
-  // general form catches up (n x 117 x 3051: 9 matrices 151 us and 205 us, 40
-  // 449 and 477, 80 1011 and 943).  The form goes by the matrices' size alone
+  // general form catches up and passes it (n x 117 x 3051: 9 matrices 151 us and
+  // 205 us, 40 449 and 477, 80 1011 and 943).  The form goes by the matrices' size alone
   // all the same, so that a matrix's update does not depend on the others.
   if (fit < 1) pl->small_cs = 0;
   return MOE_OK;

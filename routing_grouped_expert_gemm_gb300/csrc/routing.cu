@@ -17,16 +17,16 @@
 // 0.7 at the groups' border, which takes the warp 4 us and a call 2 to 3); fp32
 // alone would pick another expert in some rows of a large batch.
 //
-// 16384 x 256 fp32 in 8 groups: 15.4 us, with the sums 19.5 us (17 MB at the
-// copy rate would be 2.6 us; DRAM is at 8%, instruction issue at 56 to 68%);
-// 32768 x 384 bf16: 25.5 us; one row: 4.3 us.
+// 16384 x 256 fp32 in 8 groups: 15.6 us, with the sums 19.8 us (17 MB at the
+// copy rate would be 2.6 us; DRAM is at 9%, instruction issue at 57%), by softmax
+// with the sums 31 us; 32768 x 384 bf16: 25.6 us; one row: 4.0 us a call in a chain.
 //
 // One warp per row, lane l holding the V consecutive experts l V .. l V + V - 1
 // in registers: a row is read once, in 16-byte loads, and nothing but the
 // results is written.  Consecutive experts per lane make "lowest id" the same
 // as "lowest lane", and a group a set of neighbouring lanes.  The kernel is
 // bound by instruction issue, not by memory, so what a row costs is counted in
-// instructions (740 a row with groups, bias and sums).  The k-th largest
+// instructions (760 a row with groups, bias and sums).  The k-th largest
 // of the lanes' maxima (k redux.sync maxima) is a lower bound for the k-th
 // key; the keys above it, little more than k, move to one lane each, where a
 // row's worth of ranking, ties, checks and weights is a few instructions for
@@ -932,7 +932,7 @@ struct RouteBwdParams {
 // for several rows at once, one lane per slot (32 >> ks rows), and meet the
 // row's through shared memory.  Renormalised weights, and sigmoid ones, without
 // prob_sum need the selected logits only, so the row itself is not read.
-// 16384 x 256 fp32 with prob_sum: 9.5 us (33.5 MB at the copy rate would be
+// 16384 x 256 fp32 with prob_sum: 9.6 us (33.5 MB at the copy rate would be
 // 5.1 us; what is left is the latency of a row's load and reductions, four to
 // five rows a warp), without 6.4 us; 32768 x 384 bf16: 19.0 us (7.8).
 template <int V, bool kSoft>
@@ -1230,7 +1230,7 @@ cudaError_t by_width(int E, F&& f) {
 
 // Launch; the grid is set up while what is before it on the stream still runs,
 // and waits for that itself (a chain of single-token calls: 6.15 us a call
-// without, 3.7 us, the host's time, with).
+// without, 4.5 us with; 4.0 us in a graph, where the host's 3.8 us do not count).
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st, const A&... a) {
   cudaLaunchConfig_t lc = {};
