@@ -584,6 +584,120 @@ int moe_muon_update(const moe_muon_plan* plan, const void* grad, int64_t grad_ro
  * MOE_STATUS_TIMEOUT); waits for `stream`, as moe_get_status does. */
 int moe_muon_get_status(const moe_muon_plan* plan, const void* workspace, int* device_status, moe_stream_t stream);
 
+/* ------------------------------------------------------------------ norms around a block
+ *
+ * What stands between two blocks of a decoder, in one pass over the rows:
+ *   z = N(o; post_weight, post_bias)        norm of the block's output
+ *   y = x_scale x + o_scale (gate * z)      gate and scaled residual
+ *   h = N(y; pre_weight, pre_bias)          norm of the next block's input
+ * with N(v) = (v - m) / sqrt(mean((v - m)^2) + eps) * (weight_offset + weight) + bias
+ * over the D elements of a row, m = 0 (MOE_NORM_RMS) or the row's mean
+ * (MOE_NORM_LAYER).  Either norm may be left out of the plan (z = o; no h), the
+ * gate, the residual x or the block's output o out of a call.
+ */
+typedef enum moe_norm_kind { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+
+/*
+ *   D             elements of a row, 1..16384
+ *   kind          moe_norm_kind
+ *   post, pre     1: with the norm of the block's output, of the next block's input
+ *   stream_dtype  moe_dtype of the residual stream x, y and of dy, dx
+ *   branch_dtype  moe_dtype of o, h, a gate per row, do and dh: the stream's, or
+ *                 any beside an fp32 stream
+ *   param_dtype   moe_dtype of the weights, biases and a gate per channel
+ *   eps           > 0;  weight_offset, x_scale, o_scale  finite
+ */
+typedef struct moe_norm_config {
+  int64_t D;
+  int32_t kind;
+  int32_t post;
+  int32_t pre;
+  int32_t stream_dtype;
+  int32_t branch_dtype;
+  int32_t param_dtype;
+  float eps;
+  float weight_offset;
+  float x_scale;
+  float o_scale;
+} moe_norm_config;
+
+typedef struct moe_norm_plan moe_norm_plan;
+
+/*
+ * Parameters (device pointers), each may be NULL.
+ *   post_weight, pre_weight  [D]: NULL = ones (weight_offset is not added then)
+ *   post_bias, pre_bias      [D]: layer norms only
+ *   gate         [D] of param_dtype (gate_stride 0), or [T, D] of branch_dtype with
+ *                rows gate_stride elements apart; NULL = 1
+ */
+typedef struct moe_norm_params {
+  const void* post_weight;
+  const void* post_bias;
+  const void* pre_weight;
+  const void* pre_bias;
+  const void* gate;
+  int64_t gate_stride;
+} moe_norm_params;
+
+/* Validate `cfg` for the current CUDA device and create a plan (host memory
+ * only).  Errors as moe_plan_create. */
+int moe_norm_plan_create(const moe_norm_config* cfg, moe_norm_plan** out);
+int moe_norm_plan_destroy(moe_norm_plan* plan);
+
+/*
+ * The forward (T = 0 does nothing).  Rows [T, D] lie `_stride` elements apart (0 = D);
+ * what is between D and the stride is neither read nor written.
+ *   x      the residual stream, or NULL: y = o_scale (gate * z)
+ *   o      the block's output, or NULL: y = x_scale x (a plan without a post norm, no gate)
+ *   y      the new residual stream, or NULL: not written (with a pre norm only).
+ *          It may be x itself (the same pointer and stride)
+ *   h      the next block's input, with a pre norm (else NULL).  It may be o itself
+ *   stats  [T, 4] fp32 or NULL: m and 1 / sqrt(mean((v - m)^2) + eps) of o, then of y, for
+ *          moe_norm_bwd; 0 where a norm is left out
+ * h is the norm of y as it is written, so the fused call gives the bits of the
+ * separate ones.  Sums are fp32; rows whose squares leave fp32's range come out
+ * as zeros or NaN.  A row's result does not depend on the other rows.  One launch.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_CUDA.
+ */
+int moe_norm(const moe_norm_plan* plan, int64_t T, const moe_norm_params* params, const void* x, int64_t x_stride,
+             const void* o, int64_t o_stride, void* y, int64_t y_stride, void* h, int64_t h_stride, float* stats,
+             moe_stream_t stream);
+
+/*
+ * Gradients of the parameters, written by moe_norm_bwd (device pointers, each
+ * may be NULL): fp32 [D], summed over the T rows; of a gate per row [T, D] of
+ * branch_dtype, rows gate_stride elements apart (0 = D).
+ */
+typedef struct moe_norm_grads {
+  float* post_weight;
+  float* post_bias;
+  float* pre_weight;
+  float* pre_bias;
+  void* gate;
+  int64_t gate_stride;
+} moe_norm_grads;
+
+/* Device workspace of moe_norm_bwd for T rows (0 on bad input). */
+size_t moe_norm_workspace_bytes(const moe_norm_plan* plan, int64_t T);
+
+/*
+ * The gradients, from dy = dL/dy (the part that reaches y past the pre norm) and
+ * dh = dL/dh, for a forward on the same o and parameters that wrote y and stats.
+ *   o    needed with a post norm or for the gate's gradient;  y, dh  with a pre norm
+ *   dy   or NULL: 0 (with a pre norm only)
+ *   dx   or NULL: not written; it may be dy itself
+ *   d_o  or NULL: not written; it may be dh itself
+ *   workspace  at least moe_norm_workspace_bytes(plan, T) bytes, 256-byte aligned,
+ *              no initialisation needed
+ * With T = 0 the summed gradients are zeros.  No floating-point atomics: two
+ * calls give the same bits.  One launch, and a second one for the sums.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
+ */
+int moe_norm_bwd(const moe_norm_plan* plan, int64_t T, const moe_norm_params* params, const float* stats, const void* o,
+                 int64_t o_stride, const void* y, int64_t y_stride, const void* dy, int64_t dy_stride, const void* dh,
+                 int64_t dh_stride, void* dx, int64_t dx_stride, void* d_o, int64_t d_o_stride,
+                 const moe_norm_grads* grads, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* Static description of an error code. */
 const char* moe_error_string(int code);
 

@@ -12,7 +12,9 @@ Entry points keep the C names: ``moe_plan_create``, ``moe_plan_destroy``,
 given routing: ``moe_fwd_routed``, ``moe_bwd_routed``; routing from given logits: ``moe_route_plan_create``, ``moe_route_plan_destroy``,
 ``moe_route_workspace_bytes``, ``moe_route``, ``moe_route_bwd``; momentum and
 orthogonalised updates: ``moe_muon_plan_create``, ``moe_muon_plan_destroy``,
-``moe_muon_workspace_bytes``, ``moe_muon_update``, ``moe_muon_get_status``.
+``moe_muon_workspace_bytes``, ``moe_muon_update``, ``moe_muon_get_status``; norms
+around a block: ``moe_norm_plan_create``, ``moe_norm_plan_destroy``, ``moe_norm``,
+``moe_norm_workspace_bytes``, ``moe_norm_bwd``.
 """
 from __future__ import annotations
 
@@ -44,6 +46,7 @@ MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_PREC_BF16, MOE_PREC_MXFP8 = 0, 1
 MOE_DISPATCH_RING, MOE_DISPATCH_DIRECT, MOE_DISPATCH_SPREAD = 0, 1, 2
 MOE_DTYPE_FP32, MOE_DTYPE_BF16, MOE_DTYPE_FP16 = 0, 1, 2
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
 _DTYPES = {"fp32": MOE_DTYPE_FP32, "bf16": MOE_DTYPE_BF16, "fp16": MOE_DTYPE_FP16}
 
 
@@ -90,6 +93,21 @@ class moe_muon_config(ctypes.Structure):
     _fields_ = [("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("steps", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
                 ("c", ctypes.c_float), ("timeout_ms", ctypes.c_int32)]
+
+
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int64), ("kind", ctypes.c_int32), ("post", ctypes.c_int32), ("pre", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32), ("branch_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("x_scale", ctypes.c_float),
+                ("o_scale", ctypes.c_float)]
+
+
+class moe_norm_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("post_weight", "post_bias", "pre_weight", "pre_bias", "gate")] + [
+        ("gate_stride", ctypes.c_int64)]
+
+
+moe_norm_grads = moe_norm_params  # the same fields: gradients of the parameters
 
 
 _lib = None
@@ -158,6 +176,17 @@ def lib():
     L.moe_muon_update.restype = ctypes.c_int
     L.moe_muon_get_status.argtypes = [vp, vp, i32p, vp]
     L.moe_muon_get_status.restype = ctypes.c_int
+    L.moe_norm_plan_create.argtypes = [ctypes.POINTER(moe_norm_config), ctypes.POINTER(vp)]
+    L.moe_norm_plan_create.restype = ctypes.c_int
+    L.moe_norm_plan_destroy.argtypes = [vp]
+    L.moe_norm_plan_destroy.restype = ctypes.c_int
+    L.moe_norm_workspace_bytes.argtypes = [vp, i64]
+    L.moe_norm_workspace_bytes.restype = sz
+    L.moe_norm.argtypes = [vp, i64, ctypes.POINTER(moe_norm_params)] + [vp, i64] * 4 + [vp, vp]
+    L.moe_norm.restype = ctypes.c_int
+    L.moe_norm_bwd.argtypes = [vp, i64, ctypes.POINTER(moe_norm_params), vp] + [vp, i64] * 6 + [
+        ctypes.POINTER(moe_norm_grads), vp, sz, vp]
+    L.moe_norm_bwd.restype = ctypes.c_int
     L.moe_error_string.argtypes = [ctypes.c_int]
     L.moe_error_string.restype = ctypes.c_char_p
     _lib = L
@@ -513,3 +542,92 @@ def moe_muon_get_status(plan: MuonPlan, workspace, stream=None) -> int:
     if rc != MOE_OK:
         raise MoEError(rc, "moe_muon_get_status")
     return st.value
+
+
+class NormPlan:
+    """Owns a moe_norm_plan*; released by moe_norm_plan_destroy (or garbage collection)."""
+
+    def __init__(self, handle: int, cfg: moe_norm_config):
+        self.handle = handle
+        self.cfg = cfg
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.moe_norm_plan_destroy(self.handle)
+            self.handle = None
+
+
+def moe_norm_plan_create(D, kind=MOE_NORM_RMS, post=True, pre=True, stream_dtype=MOE_DTYPE_BF16, branch_dtype=MOE_DTYPE_BF16,
+                         param_dtype=MOE_DTYPE_FP32, eps=1e-6, weight_offset=0.0, x_scale=1.0, o_scale=1.0) -> NormPlan:
+    """Plan of ``moe_norm`` and ``moe_norm_bwd`` for rows of D elements."""
+    if isinstance(kind, str):
+        kind = {"rms": MOE_NORM_RMS, "layer": MOE_NORM_LAYER}[kind]
+    stream_dtype, branch_dtype, param_dtype = (_DTYPES[d] if isinstance(d, str) else d
+                                               for d in (stream_dtype, branch_dtype, param_dtype))
+    cfg = moe_norm_config(D, kind, int(post), int(pre), stream_dtype, branch_dtype, param_dtype, eps, weight_offset,
+                          x_scale, o_scale)
+    h = ctypes.c_void_p()
+    rc = lib().moe_norm_plan_create(ctypes.byref(cfg), ctypes.byref(h))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_norm_plan_create")
+    return NormPlan(h.value, cfg)
+
+
+def moe_norm_plan_destroy(plan: NormPlan) -> None:
+    if plan.handle:
+        lib().moe_norm_plan_destroy(plan.handle)
+        plan.handle = None
+
+
+def moe_norm_workspace_bytes(plan: NormPlan, T: int) -> int:
+    return int(lib().moe_norm_workspace_bytes(plan.handle, T))
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows of a tensor [T, D]: 0 (rows of D) where it is
+    contiguous or only a pointer, else its stride."""
+    if t is None or isinstance(t, int) or t.is_contiguous():
+        return 0
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) <= 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "rows of a tensor that is neither contiguous nor [T, D] with a row stride")
+    return t.stride(0)
+
+
+def _gate_stride(gate, D: int) -> int:
+    """0: one gate per channel; else the stride of a gate per row."""
+    if gate is None or isinstance(gate, int) or gate.dim() == 1:
+        return 0
+    return _row_stride(gate) or D
+
+
+def _norm_args(plan: NormPlan, params: dict) -> moe_norm_params:
+    get = params.get
+    gate = get("gate")
+    return moe_norm_params(_ptr(get("post_weight")), _ptr(get("post_bias")), _ptr(get("pre_weight")), _ptr(get("pre_bias")),
+                           _ptr(gate), get("gate_stride") or _gate_stride(gate, plan.cfg.D))
+
+
+def moe_norm(plan: NormPlan, T: int, params: dict, x=None, o=None, y=None, h=None, stats=None, stream=None) -> None:
+    """z = N(o), y = x_scale x + o_scale gate z, h = N(y).  ``params``: post_weight,
+    post_bias, pre_weight, pre_bias and gate ([D], or [T, D] for a gate per row),
+    each optional.  Rows may be further apart than D (a view of a wider tensor);
+    ``stats`` [T, 4] fp32 keeps what ``moe_norm_bwd`` needs."""
+    q = _norm_args(plan, params)
+    rc = lib().moe_norm(plan.handle, T, q, _ptr(x), _row_stride(x), _ptr(o), _row_stride(o), _ptr(y), _row_stride(y),
+                        _ptr(h), _row_stride(h), _ptr(stats), _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_norm")
+
+
+def moe_norm_bwd(plan: NormPlan, T: int, params: dict, stats, grads: dict, o=None, y=None, dy=None, dh=None, dx=None,
+                 do=None, workspace=None, workspace_bytes: int | None = None, stream=None) -> None:
+    """The gradients of ``moe_norm``: of the rows in ``dx`` and ``do``, of the parameters
+    in ``grads`` (the keys of ``params``: fp32 [D]; a gate per row: [T, D] of the branch's type)."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    q, g = _norm_args(plan, params), _norm_args(plan, grads)
+    rc = lib().moe_norm_bwd(plan.handle, T, q, _ptr(stats), _ptr(o), _row_stride(o), _ptr(y), _row_stride(y), _ptr(dy),
+                            _row_stride(dy), _ptr(dh), _row_stride(dh), _ptr(dx), _row_stride(dx), _ptr(do),
+                            _row_stride(do), g, _ptr(workspace), workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_norm_bwd")
