@@ -584,6 +584,50 @@ int moe_muon_update(const moe_muon_plan* plan, const void* grad, int64_t grad_ro
  * MOE_STATUS_TIMEOUT); waits for `stream`, as moe_get_status does. */
 int moe_muon_get_status(const moe_muon_plan* plan, const void* workspace, int* device_status, moe_stream_t stream);
 
+/* ------------------------------------------------------------------ the layer for a few tokens
+ *
+ * moe_fwd's layer for T <= MOE_DECODE_MAX_TOKENS tokens (the decode steps of a
+ * server), in one launch that streams the weights of the experts that have a
+ * token, each once: the router, the selected experts, the shared expert and the
+ * weighted sum.  The same plan and weights as moe_fwd (the ring, gather, pair and
+ * raster settings do not matter here); for MXFP8 plans x and h are quantised as
+ * there.  Products are summed in fp32 and h is held in bf16 (or MXFP8) as there,
+ * but the experts' outputs stay fp32 (moe_fwd holds them in fp16), so
+ * results agree with moe_fwd's up to roundings, not bit for bit.
+ */
+#define MOE_DECODE_MAX_TOKENS 64
+
+/* Device workspace of moe_decode and moe_decode_routed for T tokens (0 on bad input). */
+size_t moe_decode_workspace_bytes(const moe_plan* plan, int64_t T);
+
+/*
+ *   x          [T, D] bf16 (device), 0 <= T <= min(T_max, MOE_DECODE_MAX_TOKENS); T = 0 does nothing
+ *   out        [T, D] bf16
+ *   topk_idx   [T, k] int32 or NULL: the selected experts, ascending id per token
+ *   topk_w     [T, k] fp32 or NULL: their weights g
+ *   workspace  at least moe_decode_workspace_bytes(plan, T) bytes, 256-byte
+ *              aligned, no initialisation needed; not to be shared by calls that overlap
+ * The selection is that of exact logits (with the bias; ties to the lower id):
+ * where fp32 sums cannot tell the k-th logit from the next, fp64 sums decide.
+ * The launch is cooperative.  Two calls on the same inputs give the same bits; a
+ * token's last bits may depend on which other tokens are in the call.  moe_get_status reads
+ * the call's status from `workspace` (MOE_STATUS_TIMEOUT: a wait inside ran out).
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.
+ */
+int moe_decode(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w, void* out, int32_t* topk_idx,
+               float* topk_w, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * The same on a routing that is given: topk_idx [T, k] int32, topk_w [T, k] fp32
+ * (device) as moe_route writes them.  W_router and b_router are ignored.  An
+ * empty slot (-1) costs nothing and its weight is not looked at; an index out of
+ * [-1, E), or a second slot of a token with the same expert, is taken for an empty
+ * slot and reported as MOE_STATUS_SCHEDULE_INVALID.  A token without experts gets the shared
+ * expert's output, or zeros.
+ */
+int moe_decode_routed(const moe_plan* plan, int64_t T, const void* x, const moe_weights* w, const int32_t* topk_idx,
+                      const float* topk_w, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------------ norms around a block
  *
  * What stands between two blocks of a decoder, in one pass over the rows:

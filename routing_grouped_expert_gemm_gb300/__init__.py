@@ -12,7 +12,8 @@ Entry points keep the C names: ``moe_plan_create``, ``moe_plan_destroy``,
 given routing: ``moe_fwd_routed``, ``moe_bwd_routed``; routing from given logits: ``moe_route_plan_create``, ``moe_route_plan_destroy``,
 ``moe_route_workspace_bytes``, ``moe_route``, ``moe_route_bwd``; momentum and
 orthogonalised updates: ``moe_muon_plan_create``, ``moe_muon_plan_destroy``,
-``moe_muon_workspace_bytes``, ``moe_muon_update``, ``moe_muon_get_status``; norms
+``moe_muon_workspace_bytes``, ``moe_muon_update``, ``moe_muon_get_status``; the layer
+for a few tokens: ``moe_decode_workspace_bytes``, ``moe_decode``, ``moe_decode_routed``; norms
 around a block: ``moe_norm_plan_create``, ``moe_norm_plan_destroy``, ``moe_norm``,
 ``moe_norm_workspace_bytes``, ``moe_norm_bwd``.
 """
@@ -41,6 +42,7 @@ MOE_ERR_CUDA = -4
 MOE_ERR_UNSUPPORTED_DEVICE = -5
 MOE_ERR_STATIC_SCRATCH_TOO_SMALL = -6
 MOE_ROUTE_STATIC_MAX_TOKENS = 16384
+MOE_DECODE_MAX_TOKENS = 64
 MOE_STATUS_OK, MOE_STATUS_TIMEOUT, MOE_STATUS_SCHEDULE_INVALID, MOE_STATUS_STAGING_OVERFLOW = 0, 1, 2, 3
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_PREC_BF16, MOE_PREC_MXFP8 = 0, 1
@@ -176,6 +178,12 @@ def lib():
     L.moe_muon_update.restype = ctypes.c_int
     L.moe_muon_get_status.argtypes = [vp, vp, i32p, vp]
     L.moe_muon_get_status.restype = ctypes.c_int
+    L.moe_decode_workspace_bytes.argtypes = [vp, i64]
+    L.moe_decode_workspace_bytes.restype = sz
+    L.moe_decode.argtypes = [vp, i64, vp, ctypes.POINTER(moe_weights), vp, vp, vp, vp, sz, vp]
+    L.moe_decode.restype = ctypes.c_int
+    L.moe_decode_routed.argtypes = [vp, i64, vp, ctypes.POINTER(moe_weights), vp, vp, vp, vp, sz, vp]
+    L.moe_decode_routed.restype = ctypes.c_int
     L.moe_norm_plan_create.argtypes = [ctypes.POINTER(moe_norm_config), ctypes.POINTER(vp)]
     L.moe_norm_plan_create.restype = ctypes.c_int
     L.moe_norm_plan_destroy.argtypes = [vp]
@@ -542,6 +550,34 @@ def moe_muon_get_status(plan: MuonPlan, workspace, stream=None) -> int:
     if rc != MOE_OK:
         raise MoEError(rc, "moe_muon_get_status")
     return st.value
+
+
+def moe_decode_workspace_bytes(plan: Plan, T: int) -> int:
+    return int(lib().moe_decode_workspace_bytes(plan.handle, T))
+
+
+def moe_decode(plan: Plan, T: int, x, weights: dict, out, workspace, workspace_bytes: int | None = None, topk_idx=None,
+               topk_w=None, stream=None) -> None:
+    """``moe_fwd``'s layer for at most MOE_DECODE_MAX_TOKENS tokens, in one launch bound by the experts' weights."""
+    w = moe_weights(**{k: _ptr(v) for k, v in weights.items()})
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().moe_decode(plan.handle, T, _ptr(x), w, _ptr(out), _ptr(topk_idx), _ptr(topk_w), _ptr(workspace),
+                          workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_decode")
+
+
+def moe_decode_routed(plan: Plan, T: int, x, weights: dict, topk_idx, topk_w, out, workspace,
+                      workspace_bytes: int | None = None, stream=None) -> None:
+    """``moe_decode`` with its routing given: ``topk_idx`` [T, k] int32 (-1: an empty slot) and ``topk_w`` [T, k] fp32."""
+    w = moe_weights(**{k: _ptr(v) for k, v in weights.items()})
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    rc = lib().moe_decode_routed(plan.handle, T, _ptr(x), w, _ptr(topk_idx), _ptr(topk_w), _ptr(out), _ptr(workspace),
+                                 workspace_bytes, _stream(stream))
+    if rc != MOE_OK:
+        raise MoEError(rc, "moe_decode_routed")
 
 
 class NormPlan:
