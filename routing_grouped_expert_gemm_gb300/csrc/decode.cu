@@ -12,17 +12,18 @@
 //     of 128 weight rows (the M side) by the tokens of that expert (the N side, 16
 //     to 64 columns): a step is 128 rows x 128 bytes (16 KB of weights) and its
 //     tokens' 128 bytes each, eight to eleven steps in flight on an SM.
-//   - The steps of a phase lie in one line (expert, tile, K) and every CTA takes an
-//     equal stretch of it, so that SMs finish together whatever the number of
-//     experts; a tile cut by a border leaves fp32 partial sums (a few KB beside
-//     hundreds of KB of weights) that its CTAs add in CTA order, so results do not
-//     depend on timing.
+//   - Work is cut into units: some steps of one weight tile for one expert, a few
+//     hundred KB. SMs are not equally fast at reading memory, so units are claimed
+//     from a counter, in order. A unit leaves its fp32 sums (512 bytes a token beside
+//     those hundreds of KB) in a place of its own; when all of a phase are there every
+//     CTA adds its share of them in a fixed order, so results do not depend on timing.
+//     (With the deep queue of loads that fills the memory system a round trip to L2
+//     takes microseconds: units must not wait for one, a phase may.)
 //   - Three phases: the shared expert's up/gate projections, which need no
-//     routing and stream while the router works; the routed experts' up/gate
-//     projections; all down projections, one output tile at a time over all its
-//     experts, so that a token's weighted sum ends in one place.  Weights do not
-//     depend on anything, so the loads of the next phase start while its inputs are
-//     still being made.
+//     routing and stream while the router works (dealt out, not claimed); the routed
+//     experts' up/gate projections; all down projections, one output tile at a time
+//     over its experts. Weights do not depend on anything, so the loads of the next
+//     phase start while its inputs are still being made.
 //   - The router's products (T E D) run on the CUDA cores of all SMs first, with a bound
 //     of its error beside every logit; where the k-th and the next logit are
 //     closer than fp32 sums can tell apart, the undecided experts are decided in
@@ -43,8 +44,22 @@ constexpr int DEC_MAX_R = DEC_MAX_T * TOPK_MAX;     // routes
 constexpr int DEC_MAX_STAGES = 12;
 constexpr int DEC_THREADS = 256;
 constexpr int DEC_A_BYTES = 128 * 128;              // weights of a step
-constexpr int DEC_MIN_STEPS = 4;                    // of a CTA's stretch: fewer and partial sums outweigh the steps
-constexpr int DEC_SLOTS = 3;                        // partial sums of a CTA: its first, its last and a whole tile
+enum : int { CTR_TOPK = 0, CTR_CLAIMS, CTR_UP /* units done */, CTR_H /* CTAs whose share of h is written */, CTR_DOWN, DEC_COUNTERS };
+constexpr int DEC_EARLY = 5;                        // steps loaded before the grid's barrier
+constexpr int DEC_QUEUE = 4;                        // claimed units on their way to the roles of a CTA
+
+// Steps of a unit, for `total` steps on `ctas` CTAs: a CTA's share in 32 units,
+// though not so many that a unit is below 12 steps (4.5 us of an SM's loads), or where
+// the share is small, 8 units of at least 4; and its sums (ncap columns) stay below an
+// eighth of its weights.
+__host__ __device__ inline int dec_unit_steps(int total, int ctas, int ncap) {
+  const int share = (total + ctas - 1) / ctas;
+  int q = share / 8;
+  q = q < 4 ? 4 : q > 12 ? 12 : q;
+  if (q < share / 32) q = share / 32;
+  if (q < ncap / 4) q = ncap / 4;
+  return q;
+}
 
 struct DecodeParams {
   int T, D, I, E, k, I_s;
@@ -61,7 +76,7 @@ struct DecodeParams {
   int* out_idx;         // exports, or null
   float* out_w;
   int* status;
-  int* counters;        // [3 gridDim + 2]
+  int* counters;        // [DEC_COUNTERS]
   float2* logits;       // [T, E] logit, what it may be off by
   int* topk_idx;        // [T, k]
   float* topk_w;
@@ -70,8 +85,12 @@ struct DecodeParams {
   void* h;              // [R, I] bf16, or codes
   uint8_t* hs;          // [R, I / 32]
   bf16* h_s;            // [64, I_s]
-  float* slots;         // [gridDim][DEC_SLOTS][ncap][256]
-  float* slots_s;       // the same for the shared expert's up/gate phase
+  float* sums_s;        // sums of the shared up/gate units: [tile][part][piece][T][128]
+  float* sums_u;        // of the routed ones: [tile][part][piece][T k rows][128]
+  float* sums_d;        // of the down units: [tile][piece][T k rows][128]
+  float* sums_ds;       // of the shared expert's: [tile][piece][T][128]
+  int q_s, q_ds;        // steps of a unit of the shared expert's up/gate and (where it has no others) down projections
+  int most_u, most_d;   // pieces that there is room for
   const uint8_t* sf_up;
   const uint8_t* sf_gate;
   const uint8_t* sf_down;
@@ -96,84 +115,96 @@ struct DecodeSched {
   uint16_t act_e[E_MAX];           // experts with a token
   int scan[4];
   int n_act;
+  // the units of the claimed phases
+  int m_u, q_u;         // pieces of a routed up/gate part, steps of a piece
+  int m_d, q_d, m_ds;   // pieces of a down projection, steps of a piece, pieces of the shared expert's
+  int n_u, n_d;         // units of the two phases
+  int n_rows;           // rows: routes that are not empty
 };
 
 constexpr int dec_smem_fixed() { return (int)sizeof(DecodeSched) + 1024 /* alignment */ + 512 /* barriers */; }
 
-// One phase of the step line
-struct Phase {
-  int L;      // steps of a tile
-  int total;  // steps of the phase
-  int q;      // of a CTA's stretch
-  __device__ __forceinline__ int owner(int step) const { return step / q; }
-};
-__device__ __forceinline__ Phase make_phase(int tiles, int L) {
-  Phase f;
-  f.L = L;
-  f.total = tiles * L;
-  f.q = max((f.total + (int)gridDim.x - 1) / (int)gridDim.x, DEC_MIN_STEPS);
-  return f;
-}
-
 enum : int { PH_SHARED = 0, PH_UP = 1, PH_DOWN = 2 };
 
-// A run of steps with one weight matrix and one set of tokens: one accumulator
-struct Seg {
-  int phase, tile;
-  int part;    // PH_SHARED, PH_UP: 0 up rows, 1 gate rows; PH_DOWN: -1 the shared expert, else index of the active expert
-  int act;     // index of the active expert (PH_UP, routed part of PH_DOWN)
-  int k0, k1;  // steps of the part
-  bool first, last;  // of the tile in this CTA
+struct Unit {
+  int phase;
+  int tile;    // 128 rows: of the expert's up/gate matrices, or of the output
+  int part;    // up/gate: 0 up rows, 1 gate rows
+  int piece;
+  int act;     // index of the active expert, -1: the shared expert
+  int e;       // that expert
+  int k0, k1;  // steps
+  int n, off;  // its tokens and their first row
 };
 
-// The segments of this CTA in order.  Every role of the CTA walks them by itself.
-struct Walk {
-  int phase = -1, pos = 0, hi = 0, lo = 0;
-  Phase f{1, 0, 1};
-  __device__ __forceinline__ Phase phase_of(const DecodeParams& p, int ph, int n_act) const {
-    const int kd = p.D / (p.mx ? BK_MX : BK);
-    if (ph == PH_SHARED) return make_phase(p.I_s / 128, 2 * (p.D / BK));
-    if (ph == PH_UP) return make_phase(n_act * (p.I / 128), 2 * kd);
-    return make_phase(p.D / 128, p.I_s / BK + n_act * (p.I / (p.mx ? BK_MX : BK)));
+__device__ __forceinline__ void unit_expert(const DecodeParams& p, const DecodeSched& s, Unit& u) {
+  if (u.act >= 0) {
+    u.e = s.act_e[u.act];
+    u.n = __popcll(s.mask[u.e]);
+    u.off = s.off[u.e];
+  } else {
+    u.e = u.off = 0;
+    u.n = p.T;
   }
-  __device__ __forceinline__ void enter(const DecodeParams& p, int ph, int n_act) {
-    phase = ph;
-    f = phase_of(p, ph, n_act);
-    lo = min(f.total, (int)blockIdx.x * f.q);
-    hi = min(f.total, lo + f.q);
-    pos = lo;
-  }
-  __device__ __forceinline__ bool next(const DecodeParams& p, Seg& s) {
-    if (pos >= hi) return false;
-    s.phase = phase;
-    s.tile = pos / f.L;
-    int r = pos - s.tile * f.L, len;
-    s.first = pos == lo || r == 0;
-    if (phase != PH_DOWN) {
-      const int half = f.L / 2;
-      s.part = r >= half;
-      s.act = phase == PH_UP ? s.tile / (p.I / 128) : -1;
-      s.k0 = r - s.part * half;
-      len = half - s.k0;
+}
+// Unit i of the shared expert's up/gate phase
+__device__ __forceinline__ int shared_pieces(const DecodeParams& p) { return (p.D / BK + p.q_s - 1) / p.q_s; }
+__device__ __forceinline__ int shared_units(const DecodeParams& p) { return p.I_s / 128 * 2 * shared_pieces(p); }
+__device__ __forceinline__ Unit shared_unit(const DecodeParams& p, int i) {
+  const int m = shared_pieces(p);
+  Unit u;
+  u.phase = PH_SHARED;
+  u.piece = i % m;
+  u.part = i / m & 1;
+  u.tile = i / (2 * m);
+  u.act = -1, u.e = 0, u.n = p.T, u.off = 0;
+  u.k0 = u.piece * p.q_s;
+  u.k1 = min(p.D / BK, u.k0 + p.q_s);
+  return u;
+}
+// Claimed unit i
+__device__ __forceinline__ Unit claimed_unit(const DecodeParams& p, const DecodeSched& s, int i) {
+  Unit u;
+  if (i < s.n_u) {
+    u.phase = PH_UP;
+    u.piece = i % s.m_u;
+    i /= s.m_u;
+    u.part = i & 1;
+    i >>= 1;
+    u.tile = i % (p.I / 128);
+    u.act = i / (p.I / 128);
+    u.k0 = u.piece * s.q_u;
+    u.k1 = min(p.D / (p.mx ? BK_MX : BK), u.k0 + s.q_u);
+  } else {
+    i -= s.n_u;
+    const int per = s.m_ds + s.n_act * s.m_d;
+    u.phase = PH_DOWN;
+    u.part = 0;
+    u.tile = i / per;
+    i -= u.tile * per;
+    int k;
+    if (i < s.m_ds) {
+      u.act = -1, u.piece = i;
+      k = p.I_s / BK;
     } else {
-      const int ks = p.I_s / BK, ki = p.I / (p.mx ? BK_MX : BK);
-      if (r < ks) {
-        s.part = s.act = -1;
-        s.k0 = r;
-        len = ks - r;
-      } else {
-        s.part = s.act = (r - ks) / ki;
-        s.k0 = r - ks - s.act * ki;
-        len = ki - s.k0;
-      }
+      i -= s.m_ds;
+      u.act = i / s.m_d, u.piece = i % s.m_d;
+      k = p.I / (p.mx ? BK_MX : BK);
     }
-    len = min(len, hi - pos);
-    s.k1 = s.k0 + len;
-    pos += len;
-    s.last = pos == hi || pos == (s.tile + 1) * f.L;
-    return true;
+    u.k0 = u.piece * s.q_d;
+    u.k1 = min(k, u.k0 + s.q_d);
   }
-};
+  unit_expert(p, s, u);
+  return u;
+}
+// Where a unit's sums go: [n][128] floats
+__device__ __forceinline__ float* unit_sums(const DecodeParams& p, const DecodeSched& s, const Unit& u) {
+  const size_t R = (size_t)p.T * p.k;
+  if (u.phase == PH_SHARED) return p.sums_s + ((size_t)((u.tile * 2 + u.part) * shared_pieces(p) + u.piece) * p.T) * 128;
+  if (u.phase == PH_UP) return p.sums_u + ((size_t)((u.tile * 2 + u.part) * s.m_u + u.piece) * R + u.off) * 128;
+  if (u.act < 0) return p.sums_ds + ((size_t)(u.tile * s.m_ds + u.piece) * p.T) * 128;
+  return p.sums_d + ((size_t)(u.tile * s.m_d + u.piece) * R + u.off) * 128;
+}
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -185,10 +216,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 
 // ------------------------------------------------------------------ router
-// Logits of all tokens, four warps per expert and group of 8 tokens, each a
-// quarter of D in chunks of 256 (8 elements a lane).  Beside a logit what fp32 may be off by:
-// a product passes through at most `depth` additions, each of half an ulp (2^-24) of
-// a sum that is at most the sum of magnitudes, and the bias through one.
+// Logits of all tokens: a team of four warps takes four experts (so that x comes from
+// L2 once for them; one where that leaves teams without work) and 8 tokens, each warp a quarter of D in chunks
+// of 256 (8 elements a lane).  Beside a logit what fp32 may be off by: a product
+// passes through at most `depth` additions, each of half an ulp (2^-24) of a sum that
+// is at most the sum of magnitudes, which is at most |x| |w|; and the bias through one.
+// (1 + 2^-8 covers the norms' own roundings.)
+constexpr int RT_E = 4, RT_T = 8;
 __device__ __forceinline__ float dec_depth(int D) { return (float)((D / 256 + 3) / 4 * 8 + 8 + 4); }
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
@@ -197,62 +231,68 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
   for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
 
-__device__ void router_logits(const DecodeParams& p, float2* red /* [2][4][8] */) {
+__device__ void router_logits(const DecodeParams& p, float* red /* [2][4][RT_E RT_T + RT_E + RT_T] */) {
+  constexpr int NV = RT_E * RT_T + RT_E + RT_T;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp >> 2, quarter = warp & 3;
-  const int groups = (p.T + 7) / 8, items = p.E * groups, chunks = p.D / 256;
-  for (int first = blockIdx.x * 2; first < items; first += gridDim.x * 2) {
-    const int item = first + team;
+  const int groups = (p.T + RT_T - 1) / RT_T, chunks = p.D / 256;
+  const int per = p.E * groups <= 4 * (int)gridDim.x ? 1 : RT_E, items = (p.E + per - 1) / per * groups;
+  for (int first = blockIdx.x; first < items; first += 2 * gridDim.x) {
+    const int item = first + team * (int)gridDim.x;
     const bool on = item < items;
-    const int e = on ? item / groups : 0, t0 = on ? (item % groups) * 8 : 0;
-    float acc[8], mag[8];
+    const int e0 = on ? item / groups * per : 0, t0 = on ? item % groups * RT_T : 0;
+    const int ne = min(per, p.E - e0), nt = min(RT_T, p.T - t0);
+    float v[NV];  // logits, then |w|^2, then |x|^2
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = mag[i] = 0.0f;
+    for (int i = 0; i < NV; ++i) v[i] = 0.0f;
     if (on) {
-      const uint4* w = reinterpret_cast<const uint4*>(p.w_router + (size_t)e * p.D) + lane;
+      const uint4* w = reinterpret_cast<const uint4*>(p.w_router + (size_t)e0 * p.D) + lane;
       const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)t0 * p.D) + lane;
-      for (int c0 = quarter; c0 < chunks; c0 += 32) {
-        uint4 wq[8];
+#pragma unroll 4
+      for (int c = quarter; c < chunks; c += 4) {
+        float wf[RT_E][8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c0 + 4 * c < chunks) wq[c] = __ldg(w + (c0 + 4 * c) * 32);
+        for (int e = 0; e < RT_E; ++e) {
+          unpack8(e < ne ? __ldg(w + (size_t)e * (p.D / 8) + c * 32) : make_uint4(0u, 0u, 0u, 0u), wf[e]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c0 + 4 * c >= chunks) break;
-          float wf[8];
-          unpack8(wq[c], wf);
+          for (int j = 0; j < 8; ++j) v[RT_E * RT_T + e] = fmaf(wf[e][j], wf[e][j], v[RT_E * RT_T + e]);
+        }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (t0 + i >= p.T) break;
-            float xf[8];
-            unpack8(__ldg(x + (size_t)i * (p.D / 8) + (c0 + 4 * c) * 32), xf);
+        for (int t = 0; t < RT_T; ++t) {
+          if (t >= nt) break;
+          float xf[8];
+          unpack8(__ldg(x + (size_t)t * (p.D / 8) + c * 32), xf);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i] = fmaf(xf[j], wf[j], acc[i]), mag[i] = fmaf(fabsf(xf[j]), fabsf(wf[j]), mag[i]);
+          for (int j = 0; j < 8; ++j) {
+            v[RT_E * RT_T + RT_E + t] = fmaf(xf[j], xf[j], v[RT_E * RT_T + RT_E + t]);
+#pragma unroll
+            for (int e = 0; e < RT_E; ++e) v[t * RT_E + e] = fmaf(xf[j], wf[e][j], v[t * RT_E + e]);
           }
         }
       }
     }
+    float* mine = red + (team * 4 + quarter) * NV;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (t0 + i >= p.T) break;
+    for (int i = 0; i < NV; ++i) {
+      if (i < RT_E * RT_T && i / RT_E >= nt) continue;  // (of tokens past the end)
 #pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) {
-        acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
-        mag[i] += __shfl_xor_sync(0xffffffffu, mag[i], m);
-      }
-      if (lane == 0) red[(team * 4 + quarter) * 8 + i] = make_float2(acc[i], mag[i]);
+      for (int m = 16; m >= 1; m >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+      if (lane == 0) mine[i] = v[i];
     }
     named_bar_sync(1 + team, 128);
-    if (quarter == 0 && lane < 8 && on && t0 + lane < p.T) {
-      float2 s = red[team * 32 + lane];
+    if (quarter == 0 && on && lane / RT_E < nt && lane % RT_E < ne) {  // lane: a token and an expert
+      const int t = lane / RT_E, e = lane % RT_E;
+      const float* r = red + team * 4 * NV;
+      float2 s = make_float2(0.0f, 0.0f);
+      float ww = 0.0f, xx = 0.0f;
 #pragma unroll
-      for (int q = 1; q < 4; ++q) s.x += red[(team * 4 + q) * 8 + lane].x, s.y += red[(team * 4 + q) * 8 + lane].y;
-      s.y *= dec_depth(p.D) * (1.0f / 16777216.0f);
+      for (int q = 0; q < 4; ++q) s.x += r[q * NV + lane], ww += r[q * NV + RT_E * RT_T + e], xx += r[q * NV + RT_E * RT_T + RT_E + t];
+      s.y = sqrtf(ww) * sqrtf(xx) * dec_depth(p.D) * (257.0f / 256.0f / 16777216.0f);
       if (p.b_router) {
-        s.x += p.b_router[e];
+        s.x += p.b_router[e0 + e];
         s.y += fabsf(s.x) * (1.0f / 16777216.0f);
       }
       if (!(s.x - s.x == 0.0f)) s.y = 0.0f;  // infinite or NaN: nothing to decide
-      p.logits[(size_t)(t0 + lane) * p.E + e] = s;
+      p.logits[(size_t)(t0 + t) * p.E + e0 + e] = s;
     }
     named_bar_sync(1 + team, 128);
   }
@@ -299,7 +339,7 @@ __device__ __noinline__ uint32_t decide_fp64(const DecodeParams& p, int t, uint3
 }
 
 // Experts and weights of token t, one warp
-__device__ void token_topk(const DecodeParams& p, int t) {
+__device__ void token_topk(const DecodeParams& p, int t, float* logit /* [k], shared memory of the warp */) {
   const int lane = threadIdx.x & 31, k = p.k;
   float v[E_MAX / 32], err[E_MAX / 32];
   uint32_t left = 0u, key[E_MAX / 32];
@@ -320,8 +360,10 @@ __device__ void token_topk(const DecodeParams& p, int t) {
     uint32_t b = 0u;
     int id = 1 << 20;
 #pragma unroll
-    for (int i = 0; i < E_MAX / 32; ++i)
+    for (int i = 0; i < E_MAX / 32; ++i) {
+      if (32 * i >= p.E) break;
       if ((left >> i & 1) && (id == 1 << 20 || key[i] > b)) b = key[i], id = lane + 32 * i;
+    }
     const uint32_t m = __reduce_max_sync(0xffffffffu, b);
     id = (int)__reduce_min_sync(0xffffffffu, b == m ? (unsigned)id : 1u << 20);
     if ((id & 31) == lane) left &= ~(1u << (id >> 5)), sel |= 1u << (id >> 5);
@@ -359,7 +401,7 @@ __device__ void token_topk(const DecodeParams& p, int t) {
     if (sel >> i & 1) {
       const int s = slot + __popc(row & ((1u << lane) - 1u));
       p.topk_idx[(size_t)t * k + s] = lane + 32 * i;
-      p.topk_w[(size_t)t * k + s] = v[i];  // the logit, for now
+      logit[s] = v[i];
       if (p.out_idx) p.out_idx[(size_t)t * k + s] = lane + 32 * i;
     }
     slot += __popc(row);
@@ -367,7 +409,7 @@ __device__ void token_topk(const DecodeParams& p, int t) {
   __syncwarp();
   // weights over their sum.  Softmax: exp(l - m); sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)), both factors scaled so
   // that the largest is near 1 (logits far below 0 leave fp32's range otherwise)
-  const float l = lane < k ? *(volatile float*)(p.topk_w + (size_t)t * k + lane) : -INFINITY;
+  const float l = lane < k ? logit[lane] : -INFINITY;
   const bool soft = p.score_fn == MOE_SCORE_SOFTMAX;
   const float a = soft ? l : fminf(l, 0.0f);
   float m = a;
@@ -445,7 +487,22 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
       rows += n;
     }
   }
-  if (tid == 127) s.n_act = act;
+  if (tid == 127) {
+    s.n_act = act;
+    s.n_rows = rows;
+    const int kd = p.D / (p.mx ? BK_MX : BK), ki = p.I / (p.mx ? BK_MX : BK), ks = p.I_s / BK;
+    const int q = dec_unit_steps(act * (p.I / 128) * 2 * kd, gridDim.x, p.ncap);
+    s.m_u = min(max((kd + q - 1) / q, 1), p.most_u);
+    s.q_u = (kd + s.m_u - 1) / s.m_u;
+    s.m_u = (kd + s.q_u - 1) / s.q_u;
+    s.n_u = act * (p.I / 128) * 2 * s.m_u;
+    const int r = dec_unit_steps(p.D / 128 * (ks + act * ki), gridDim.x, p.ncap);
+    s.m_d = min(max((ki + r - 1) / r, 1), p.most_d);
+    s.q_d = max((ki + s.m_d - 1) / s.m_d, p.q_ds);
+    s.m_d = (ki + s.q_d - 1) / s.q_d;
+    s.m_ds = (ks + s.q_d - 1) / s.q_d;
+    s.n_d = p.D / 128 * (s.m_ds + act * s.m_d);
+  }
   named_bar_sync(3, 128);
   for (int r = tid; r < R; r += 128) {
     const uint16_t e = s.idx[r];
@@ -453,63 +510,76 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
   }
 }
 
-// ------------------------------------------------------------------ sums of cut tiles
-// A CTA's partial sums of a tile: slot 0 if it is its first of the phase, 1 if its last, else 2
-__device__ __forceinline__ float* slot_of(const DecodeParams& p, float* slots, const Phase& f, int cta, int tile) {
-  const int lo = cta * f.q, hi = min(f.total, lo + f.q);
-  const int s = tile == lo / f.L ? 0 : tile == (hi - 1) / f.L ? 1 : 2;
-  return slots + ((size_t)cta * DEC_SLOTS + s) * p.ncap * 256;
-}
-
+// ------------------------------------------------------------------ finished tiles
 __device__ __forceinline__ float4 ldcg4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
+__device__ __forceinline__ void fma4(float4& a, float g, const float4& b) {
+  a.x = fmaf(g, b.x, a.x), a.y = fmaf(g, b.y, a.y), a.z = fmaf(g, b.z, a.z), a.w = fmaf(g, b.w, a.w);
+}
 
-// Up/gate tile: sums over its CTAs in order, SwiGLU, h.  This CTA takes every
-// nc-th of the tile's n rows (nc CTAs share it), a warp a row, a lane 4 columns.
-__device__ void finish_up(const DecodeParams& p, const Phase& f, int tile, float* slots, bool shared, int n, int row0, int ew) {
-  const int lane = threadIdx.x & 31;
-  const int b = tile * f.L, half = f.L / 2;
-  const int c0 = f.owner(b), c1 = f.owner(b + half - 1), d0 = f.owner(b + half), d1 = f.owner(b + f.L - 1);
-  const int nc = d1 - c0 + 1, me = (int)blockIdx.x - c0;
-  const int width = shared ? p.I_s : p.I, col = (tile % (width / 128)) * 128 + 4 * lane;
-  for (int r = me + nc * ew; r < n; r += nc * 4) {
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), g = u;
-    for (int c = c0; c <= c1; ++c) add4(u, ldcg4(slot_of(p, slots, f, c, tile) + r * 256 + 4 * lane));
-    for (int c = d0; c <= d1; ++c) add4(g, ldcg4(slot_of(p, slots, f, c, tile) + r * 256 + 128 + 4 * lane));
-    const float h[4] = {silu_f32(g.x) * u.x, silu_f32(g.y) * u.y, silu_f32(g.z) * u.z, silu_f32(g.w) * u.w};
+// h of all rows, this CTA's share: an item is a row (token) and 128 columns, a warp
+// takes an item, a lane 4 columns: the sums of its pieces in order, SwiGLU.
+__device__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) {
+  const int lane = threadIdx.x & 31, tiles_s = p.I_s / 128, tiles_u = p.I / 128;
+  const int of_s = p.T * tiles_s, items = of_s + sc.n_rows * tiles_u;
+  for (int it = blockIdx.x + ew * gridDim.x; it < items; it += 4 * gridDim.x) {
+    const bool shared = it < of_s;
+    const int tiles = shared ? tiles_s : tiles_u, r = (shared ? it : it - of_s) / tiles, tile = (shared ? it : it - of_s) % tiles;
+    const int m = shared ? shared_pieces(p) : sc.m_u, col = tile * 128 + 4 * lane;
+    const size_t rows = shared ? p.T : (size_t)p.T * p.k;
+    const float* su = (shared ? p.sums_s : p.sums_u) + ((size_t)tile * 2 * m * rows + r) * 128 + 4 * lane;
+    const float* sg = su + (size_t)m * rows * 128;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), g = a;
+#pragma unroll 4
+    for (int c = 0; c < m; ++c) {
+      add4(a, ldcg4(su + c * rows * 128));
+      add4(g, ldcg4(sg + c * rows * 128));
+    }
+    const float h[4] = {silu_f32(g.x) * a.x, silu_f32(g.y) * a.y, silu_f32(g.z) * a.z, silu_f32(g.w) * a.w};
     if (shared || !p.mx) {
-      bf16* to = shared ? p.h_s + (size_t)r * p.I_s + col : static_cast<bf16*>(p.h) + (size_t)(row0 + r) * p.I + col;
+      bf16* to = shared ? p.h_s + (size_t)r * p.I_s + col : static_cast<bf16*>(p.h) + (size_t)r * p.I + col;
       *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
     } else {  // MX blocks of 32 columns = 8 lanes
-      float m = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
+      float most = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
 #pragma unroll
-      for (int d = 4; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      for (int d = 4; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
       uint32_t code = 0u, scale = 0u;
-      if (m != 0.0f) {
-        const uint32_t eb = (__float_as_uint(m) >> 23) & 0xFFu;
-        int se = (eb != 0u ? (int)eb - 127 : ilogbf(m)) - 8;
+      if (most != 0.0f) {
+        const uint32_t eb = (__float_as_uint(most) >> 23) & 0xFFu;
+        int se = (eb != 0u ? (int)eb - 127 : ilogbf(most)) - 8;
         se = max(-127, min(127, se));
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = ldexpf(h[i], -se);
-        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
-        code = a | c << 16;
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+        code = lo | hi << 16;
         scale = (uint32_t)(se + 127);
       }
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.h) + (size_t)(row0 + r) * p.I + col) = code;
-      if ((lane & 7) == 0) p.hs[(size_t)(row0 + r) * (p.I / 32) + col / 32] = (uint8_t)scale;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.h) + (size_t)r * p.I + col) = code;
+      if ((lane & 7) == 0) p.hs[(size_t)r * (p.I / 32) + col / 32] = (uint8_t)scale;
     }
   }
 }
 
-// Output tile: sums over its CTAs in order, this CTA taking every nc-th token
-__device__ void finish_down(const DecodeParams& p, const Phase& f, int tile, int ew) {
-  const int lane = threadIdx.x & 31;
-  const int c0 = f.owner(tile * f.L), c1 = f.owner((tile + 1) * f.L - 1), nc = c1 - c0 + 1, me = (int)blockIdx.x - c0;
-  for (int t = me + nc * ew; t < p.T; t += nc * 4) {
+// The output, this CTA's share: a token's outputs of the shared expert and of its
+// slots, in that order, weighted.  An item is a token and 128 columns.
+__device__ void finish_down(const DecodeParams& p, const DecodeSched& sc, int ew) {
+  const int lane = threadIdx.x & 31, tiles = p.D / 128;
+  const size_t R = (size_t)p.T * p.k;
+  for (int it = blockIdx.x + ew * gridDim.x; it < p.T * tiles; it += 4 * gridDim.x) {
+    const int t = it / tiles, tile = it % tiles;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) add4(s, ldcg4(slot_of(p, p.slots, f, c, tile) + t * 128 + 4 * lane));
+    for (int c = 0; c < sc.m_ds; ++c) add4(s, ldcg4(p.sums_ds + ((size_t)(tile * sc.m_ds + c) * p.T + t) * 128 + 4 * lane));
+#pragma unroll 4
+    for (int j = 0; j < p.k; ++j) {
+      const int r = t * p.k + j, e = sc.idx[r];
+      if (e == 0xffff) continue;
+      const int row = sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull));
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < sc.m_d; ++c) add4(y, ldcg4(p.sums_d + ((size_t)(tile * sc.m_d + c) * R + row) * 128 + 4 * lane));
+      fma4(s, sc.w[r], y);
+    }
     *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + tile * 128 + 4 * lane) =
         make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
@@ -528,8 +598,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
   DecodeSched& sched = *reinterpret_cast<DecodeSched*>(after);
   uint64_t* bars = reinterpret_cast<uint64_t*>(after + sizeof(DecodeSched));
   uint64_t *full = bars, *empty = bars + DEC_MAX_STAGES, *acc_full = bars + 2 * DEC_MAX_STAGES,
-           *acc_empty = acc_full + 2, *ready = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ready + 1);
+           *acc_empty = acc_full + 2, *ready = acc_empty + 2, *q_full = ready + 1, *q_empty = q_full + DEC_QUEUE;
+  int* queue = reinterpret_cast<int*>(q_empty + DEC_QUEUE);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + DEC_QUEUE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int FULL_ARRIVALS = MX ? 3 : 2;  // weights, tokens (and the tokens' scales)
 
@@ -543,6 +614,10 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
       mbar_init(&acc_empty[i], 128);
     }
     mbar_init(ready, 128);
+    for (int i = 0; i < DEC_QUEUE; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], MX ? 4 : 3);  // tokens, (scales,) products, epilogue
+    }
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -554,9 +629,33 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // ---- before the grid's barrier: counters and status to zero, logits, x as codes
+  // Loads of one step: 128 rows of weights; the rows of x or h of the unit's tokens
+  auto load_weights = [&](const Unit& u, int k, int stage, const CUtensorMap* m, int row, const uint8_t* scales) {
+    const bool mx = MX && scales;
+    mbar_arrive_expect_tx(&full[stage], DEC_A_BYTES + (mx ? SF_BLOCK_BYTES : 0));
+    tma_load_2d(smem + stage * p.stage_bytes, m, &full[stage], k * (mx ? BK_MX : BK), row);
+    if (mx) bulk_load(sf + stage * 2 * SF_BLOCK_BYTES, scales + (size_t)k * SF_BLOCK_BYTES, SF_BLOCK_BYTES, &full[stage]);
+  };
+  auto load_x = [&](int k, int stage) {
+    mbar_arrive_expect_tx(&full[stage], (uint32_t)p.ncap * 128);
+    tma_load_2d(smem + stage * p.stage_bytes + DEC_A_BYTES, &maps.x, &full[stage], k * BK, 0);
+  };
+
+  // ---- before the grid's barrier: the first loads of the shared expert's weights (they wait for nothing);
+  // counters and status to zero, logits, x as codes
+  const int n_shared = shared_units(p), early_most = min(NST, DEC_EARLY);
+  if (threadIdx.x == 0) {
+    int stage = 0;
+    for (int i = blockIdx.x; i < n_shared && stage < early_most; i += gridDim.x) {
+      const Unit u = shared_unit(p, i);
+      for (int k = u.k0; k < u.k1 && stage < early_most; ++k, ++stage) {
+        load_weights(u, k, stage, u.part ? &maps.ws_gate : &maps.ws_up, u.tile * 128, nullptr);
+        load_x(k, stage);
+      }
+    }
+  }
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
-  for (int i = blockIdx.x * DEC_THREADS + threadIdx.x; i < 3 * (int)gridDim.x + 2; i += gridDim.x * DEC_THREADS) p.counters[i] = 0;
+  for (int i = blockIdx.x * DEC_THREADS + threadIdx.x; i < DEC_COUNTERS; i += gridDim.x * DEC_THREADS) p.counters[i] = 0;
   if (MX) {
     const int blocks = p.T * (p.D / 32);
     for (int b = blockIdx.x * DEC_THREADS + threadIdx.x; b < blocks; b += gridDim.x * DEC_THREADS) {
@@ -570,12 +669,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     }
     fence_proxy_async_global();  // read by TMA
   }
-  if (!p.given) router_logits(p, reinterpret_cast<float2*>(&sched));
+  __syncwarp();
+  if (!p.given) router_logits(p, reinterpret_cast<float*>(&sched));
   cooperative_groups::this_grid().sync();
   if (MX) fence_proxy_async_global();
 
-  int* const topk_done = p.counters + 3 * gridDim.x;
-  int* const h_done = topk_done + 1;
   // the epilogue's 128 threads go on together or not at all
   auto agree = [](bool v) {
     uint32_t all;
@@ -584,153 +682,195 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     return all != 0;
   };
   auto wait_bar = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, p.status, p.timeout_ns); };
+  // the next claimed unit (one thread of a role; others are told by it); -1 at the end, -2 when waiting was given up
+  auto pop = [&](int i) {
+    if (!wait_bar(&q_full[i % DEC_QUEUE], (uint32_t)(i / DEC_QUEUE) & 1u)) return -2;
+    const int v = queue[i % DEC_QUEUE];
+    mbar_arrive(&q_empty[i % DEC_QUEUE]);
+    return v;
+  };
+  // position in the ring of stages
+  int stage = 0;
+  uint32_t parity = 0;
+  auto advance = [&]() {
+    if (++stage == NST) stage = 0, parity ^= 1u;
+  };
 
   if (warp == 0) {
-    // ---------------- weights
+    // ---------------- weights, and claims
     if (elect_one()) {
-      int stage = 0;
-      uint32_t parity = 1;
       bool ok = true;
-      Walk w;
-      for (int ph = PH_SHARED; ph <= PH_DOWN && ok; ++ph) {
-        if (ph == PH_UP && !wait_bar(ready, 0)) break;
-        w.enter(p, ph, ph == PH_SHARED ? 0 : sched.n_act);
-        Seg s;
-        while (ok && w.next(p, s)) {
+      int early = 0;  // steps issued before the barrier
+      for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) {
+        const Unit u = shared_unit(p, i);
+        for (int k = u.k0; k < u.k1; ++k, advance()) {
+          if (early < early_most) { ++early; continue; }
+          if (!(ok = wait_bar(&empty[stage], parity ^ 1u))) break;
+          load_weights(u, k, stage, u.part ? &maps.ws_gate : &maps.ws_up, u.tile * 128, nullptr);
+        }
+      }
+      ok = ok && wait_bar(ready, 0);
+      if (ok) {
+        const int units = sched.n_u + sched.n_d;
+        int next = atomicAdd(p.counters + CTR_CLAIMS, 1);
+        for (int i = 0;; ++i) {
+          const int id = next < units ? next : -1;
+          if (id >= 0) next = atomicAdd(p.counters + CTR_CLAIMS, 1);  // (its answer is not needed before this unit's loads are issued)
+          if (!wait_bar(&q_empty[i % DEC_QUEUE], ((uint32_t)(i / DEC_QUEUE) & 1u) ^ 1u)) break;
+          queue[i % DEC_QUEUE] = id;
+          mbar_arrive(&q_full[i % DEC_QUEUE]);
+          if (id < 0) break;
+          const Unit u = claimed_unit(p, sched, id);
           const CUtensorMap* m;
           const uint8_t* scales = nullptr;
           int row;
-          bool mx = MX;
-          if (ph == PH_SHARED) {
-            m = s.part ? &maps.ws_gate : &maps.ws_up, row = s.tile * 128, mx = false;
-          } else if (ph == PH_UP) {
-            m = s.part ? &maps.w_gate : &maps.w_up;
-            row = sched.act_e[s.act] * p.I + (s.tile % (p.I / 128)) * 128;
-            if (MX) scales = (s.part ? p.sf_gate : p.sf_up) + (size_t)(row / 128) * (p.D / BK_MX) * SF_BLOCK_BYTES;
-          } else if (s.part < 0) {
-            m = &maps.ws_down, row = s.tile * 128, mx = false;
+          if (u.phase == PH_UP) {
+            m = u.part ? &maps.w_gate : &maps.w_up;
+            row = u.e * p.I + u.tile * 128;
+            if (MX) scales = (u.part ? p.sf_gate : p.sf_up) + (size_t)(row / 128) * (p.D / BK_MX) * SF_BLOCK_BYTES;
+          } else if (u.act < 0) {
+            m = &maps.ws_down, row = u.tile * 128;
           } else {
-            m = &maps.w_down, row = sched.act_e[s.act] * p.D + s.tile * 128;
+            m = &maps.w_down, row = u.e * p.D + u.tile * 128;
             if (MX) scales = p.sf_down + (size_t)(row / 128) * (p.I / BK_MX) * SF_BLOCK_BYTES;
           }
-          for (int k = s.k0; k < s.k1; ++k) {
-            if (!wait_bar(&empty[stage], parity)) { ok = false; break; }
-            mbar_arrive_expect_tx(&full[stage], DEC_A_BYTES + (MX && mx ? SF_BLOCK_BYTES : 0));
-            tma_load_2d(smem + stage * p.stage_bytes, m, &full[stage], k * (MX && mx ? BK_MX : BK), row);
-            if (MX && mx) bulk_load(sf + stage * 2 * SF_BLOCK_BYTES, scales + (size_t)k * SF_BLOCK_BYTES, SF_BLOCK_BYTES, &full[stage]);
-            if (++stage == NST) stage = 0, parity ^= 1u;
+          for (int k = u.k0; k < u.k1; ++k, advance()) {
+            if (!(ok = wait_bar(&empty[stage], parity ^ 1u))) break;
+            load_weights(u, k, stage, m, row, scales);
           }
+          if (!ok) break;
         }
       }
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ---------------- tokens: the rows of x or h of a segment's tokens
-    int stage = 0;
-    uint32_t parity = 1;
+    // ---------------- tokens
     bool ok = true;
-    Walk w;
-    for (int ph = PH_SHARED; ph <= PH_DOWN && ok; ++ph) {
-      if (ph == PH_UP) ok = wait_bar(ready, 0);
-      if (ph == PH_DOWN && ok) {
+    int early = 0;
+    for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) {
+      const Unit u = shared_unit(p, i);
+      for (int k = u.k0; k < u.k1; ++k, advance()) {
+        if (early < early_most) { ++early; continue; }
         int go = 1;
-        if (lane == 0) go = wait_counter_ge(h_done, (int)gridDim.x, p.status, p.timeout_ns);
+        if (lane == 0) {
+          go = wait_bar(&empty[stage], parity ^ 1u);
+          if (go) load_x(k, stage);
+        }
+        if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+      }
+    }
+    int go = ok ? 1 : 0;
+    if (lane == 0 && ok) go = wait_bar(ready, 0);
+    ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+    __syncwarp();
+    bool have_h = false;
+    for (int i = 0; ok; ++i) {
+      int id = 0;
+      if (lane == 0) id = pop(i);
+      id = __shfl_sync(0xffffffffu, id, 0);
+      if (id < 0) break;
+      const Unit u = claimed_unit(p, sched, id);
+      if (u.phase == PH_DOWN && !have_h) {
+        go = 1;
+        if (lane == 0) go = wait_counter_ge(p.counters + CTR_H, (int)gridDim.x, p.status, p.timeout_ns);
         ok = __shfl_sync(0xffffffffu, go, 0) != 0;
         __syncwarp();
+        if (!ok) break;
         fence_proxy_async_global();
+        have_h = true;
       }
-      if (!ok) break;
-      w.enter(p, ph, ph == PH_SHARED ? 0 : sched.n_act);
-      Seg s;
-      while (ok && w.next(p, s)) {
-        const bool routed = s.act >= 0, mx = MX && routed;
-        const int e = routed ? sched.act_e[s.act] : 0;
-        const int n = routed ? __popcll(sched.mask[e]) : p.T, off = routed ? sched.off[e] : 0;
-        // lane l: the l-th load of every step
-        int t[4] = {0, 0, 0, 0}, loads;
-        uint32_t bytes;
-        if (ph == PH_SHARED) {
-          loads = 1, bytes = (uint32_t)p.ncap * 128;
-        } else if (ph == PH_UP) {
-          loads = (n + 3) / 4, bytes = (uint32_t)loads * 512;
+      // lane l: the l-th load of every step
+      const bool routed = u.act >= 0, mx = MX && routed;
+      int t[4] = {0, 0, 0, 0}, loads;
+      uint32_t bytes;
+      if (u.phase == PH_UP) {
+        loads = (u.n + 3) / 4, bytes = (uint32_t)loads * 512;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t[j] = sched.row[off + min(4 * lane + j, n - 1)] / p.k;
-        } else {
-          loads = (n + 15) / 16, bytes = (uint32_t)loads * 2048;
+        for (int j = 0; j < 4; ++j) t[j] = sched.row[u.off + min(4 * lane + j, u.n - 1)] / p.k;
+      } else {
+        loads = (u.n + 15) / 16, bytes = (uint32_t)loads * 2048;
+      }
+      for (int k = u.k0; k < u.k1; ++k, advance()) {
+        go = 1;
+        if (lane == 0) {
+          go = wait_bar(&empty[stage], parity ^ 1u);
+          if (go) mbar_arrive_expect_tx(&full[stage], bytes);
         }
-        for (int k = s.k0; k < s.k1; ++k) {
-          int go = 1;
-          if (lane == 0) {
-            go = wait_bar(&empty[stage], parity);
-            if (go) mbar_arrive_expect_tx(&full[stage], bytes);
-          }
-          if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
-          uint8_t* b = smem + stage * p.stage_bytes + DEC_A_BYTES;
-          const int kc = k * (mx ? BK_MX : BK);
-          if (lane < loads) {
-            if (ph == PH_SHARED) tma_load_2d(b, &maps.x, &full[stage], kc, 0);
-            else if (ph == PH_UP) tma_gather4(b + lane * 512, &maps.x_rows, &full[stage], kc, t[0], t[1], t[2], t[3]);
-            else tma_load_2d(b + lane * 2048, routed ? &maps.h : &maps.h_s, &full[stage], kc, off + lane * 16);
-          }
-          __syncwarp();
-          if (++stage == NST) stage = 0, parity ^= 1u;
+        if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+        uint8_t* b = smem + stage * p.stage_bytes + DEC_A_BYTES;
+        const int kc = k * (mx ? BK_MX : BK);
+        if (lane < loads) {
+          if (u.phase == PH_UP) tma_gather4(b + lane * 512, &maps.x_rows, &full[stage], kc, t[0], t[1], t[2], t[3]);
+          else tma_load_2d(b + lane * 2048, routed ? &maps.h : &maps.h_s, &full[stage], kc, u.off + lane * 16);
         }
+        __syncwarp();
       }
     }
   } else if (warp == 3) {
     // ---------------- MXFP8: the scale block of a step's tokens, lane l rows l and l + 32
     if (MX) {
-      int stage = 0;
-      uint32_t parity = 1;
       bool ok = true;
-      Walk w;
-      for (int ph = PH_SHARED; ph <= PH_DOWN && ok; ++ph) {
-        if (ph == PH_UP) ok = wait_bar(ready, 0);
-        if (ph == PH_DOWN && ok) {
-          int go = 1;
-          if (lane == 0) go = wait_counter_ge(h_done, (int)gridDim.x, p.status, p.timeout_ns);
+      int go = 1;
+      for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) {  // no scales: only the arrivals
+        const Unit u = shared_unit(p, i);
+        for (int k = u.k0; k < u.k1; ++k, advance()) {
+          if (lane == 0) {
+            go = wait_bar(&empty[stage], parity ^ 1u);
+            if (go) mbar_arrive(&full[stage]);
+          }
+          if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+        }
+      }
+      if (lane == 0 && ok) go = wait_bar(ready, 0);
+      ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+      __syncwarp();
+      bool have_h = false;
+      for (int i = 0; ok; ++i) {
+        int id = 0;
+        if (lane == 0) id = pop(i);
+        id = __shfl_sync(0xffffffffu, id, 0);
+        if (id < 0) break;
+        const Unit u = claimed_unit(p, sched, id);
+        if (u.phase == PH_DOWN && !have_h) {
+          go = 1;
+          if (lane == 0) go = wait_counter_ge(p.counters + CTR_H, (int)gridDim.x, p.status, p.timeout_ns);
           ok = __shfl_sync(0xffffffffu, go, 0) != 0;
           __syncwarp();
+          if (!ok) break;
+          have_h = true;
         }
-        if (!ok) break;
-        w.enter(p, ph, ph == PH_SHARED ? 0 : sched.n_act);
-        Seg s;
-        while (ok && w.next(p, s)) {
-          const bool routed = s.act >= 0;
-          const uint32_t* src[2] = {nullptr, nullptr};
-          if (routed) {
-            const int e = sched.act_e[s.act], n = __popcll(sched.mask[e]), off = sched.off[e];
+        const uint32_t* src[2] = {nullptr, nullptr};
+        if (u.act >= 0) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = lane + 32 * j;
+            if (r < u.n)
+              src[j] = reinterpret_cast<const uint32_t*>(u.phase == PH_UP ? p.xs + (size_t)(sched.row[u.off + r] / p.k) * (p.D / 32)
+                                                                         : p.hs + (size_t)(u.off + r) * (p.I / 32));
+          }
+        }
+        uint32_t ahead[4][2];  // four steps' words
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) ahead[d][j] = src[j] && u.k0 + d < u.k1 ? __ldcg(src[j] + u.k0 + d) : 0u;
+        for (int k = u.k0; ok && k < u.k1; k += 4) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            if (k + d >= u.k1 || !ok) break;
+            go = 1;
+            if (lane == 0) go = wait_bar(&empty[stage], parity ^ 1u);
+            if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+            uint8_t* to = sf + stage * 2 * SF_BLOCK_BYTES + SF_BLOCK_BYTES + lane * 16;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int r = lane + 32 * j;
-              if (r < n)
-                src[j] = reinterpret_cast<const uint32_t*>(ph == PH_UP ? p.xs + (size_t)(sched.row[off + r] / p.k) * (p.D / 32)
-                                                                      : p.hs + (size_t)(off + r) * (p.I / 32));
+              *reinterpret_cast<uint32_t*>(to + 4 * j) = ahead[d][j];
+              ahead[d][j] = src[j] && k + d + 4 < u.k1 ? __ldcg(src[j] + k + d + 4) : 0u;
             }
-          }
-          uint32_t ahead[4][2];  // four steps' words
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) ahead[d][j] = src[j] && s.k0 + d < s.k1 ? __ldcg(src[j] + s.k0 + d) : 0u;
-          for (int k = s.k0; k < s.k1; k += 4) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              if (k + d >= s.k1 || !ok) break;
-              int go = 1;
-              if (lane == 0) go = wait_bar(&empty[stage], parity);
-              if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
-              uint8_t* to = sf + stage * 2 * SF_BLOCK_BYTES + SF_BLOCK_BYTES + lane * 16;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                *reinterpret_cast<uint32_t*>(to + 4 * j) = ahead[d][j];
-                ahead[d][j] = src[j] && k + d + 4 < s.k1 ? __ldcg(src[j] + k + d + 4) : 0u;
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&full[stage]);
-              if (++stage == NST) stage = 0, parity ^= 1u;
-            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[stage]);
+            advance();
           }
         }
       }
@@ -738,158 +878,119 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
   } else if (warp == 1) {
     // ---------------- products
     if (elect_one()) {
-      int stage = 0, acc = 0;
-      uint32_t parity = 0, acc_parity = 1;
-      bool ok = true;
-      Walk w;
-      for (int ph = PH_SHARED; ph <= PH_DOWN && ok; ++ph) {
-        if (ph == PH_UP && !wait_bar(ready, 0)) break;
-        w.enter(p, ph, ph == PH_SHARED ? 0 : sched.n_act);
-        Seg s;
-        while (ok && w.next(p, s)) {
-          const bool routed = s.act >= 0, mx = MX && routed;
-          const uint32_t n = routed ? (uint32_t)(__popcll(sched.mask[sched.act_e[s.act]]) + 15) & ~15u : (uint32_t)p.ncap;
-          const uint32_t idesc = mx ? idesc_mxf8_e4m3(128, n) : idesc_bf16_f32(128, n);
-          if (!wait_bar(&acc_empty[acc], acc_parity)) { ok = false; break; }
+      int acc = 0;
+      uint32_t acc_parity = 1;
+      auto multiply = [&](const Unit& u) {
+        const bool mx = MX && u.act >= 0;
+        const uint32_t n = (uint32_t)(u.n + 15) & ~15u;
+        const uint32_t idesc = mx ? idesc_mxf8_e4m3(128, n) : idesc_bf16_f32(128, n);
+        if (!wait_bar(&acc_empty[acc], acc_parity)) return false;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * DEC_MAX_T, sfa = tmem + 2 * DEC_MAX_T, sfb = sfa + 4;
+        for (int k = u.k0; k < u.k1; ++k, advance()) {
+          if (!wait_bar(&full[stage], parity)) return false;
           tc_fence_after();
-          const uint32_t d = tmem + acc * DEC_MAX_T, sfa = tmem + 2 * DEC_MAX_T, sfb = sfa + 4;
-          for (int k = s.k0; k < s.k1; ++k) {
-            if (!wait_bar(&full[stage], parity)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t a = smem_u32(smem + stage * p.stage_bytes), b = a + DEC_A_BYTES;
-            if (mx) {
-              const uint32_t f = smem_u32(sf + stage * 2 * SF_BLOCK_BYTES);
-              tmem_cp_32x128b_warpx4(sfa, sdesc_sf_block(f));
-              tmem_cp_32x128b_warpx4(sfb, sdesc_sf_block(f + SF_BLOCK_BYTES));
+          const uint32_t a = smem_u32(smem + stage * p.stage_bytes), b = a + DEC_A_BYTES;
+          if (mx) {
+            const uint32_t f = smem_u32(sf + stage * 2 * SF_BLOCK_BYTES);
+            tmem_cp_32x128b_warpx4(sfa, sdesc_sf_block(f));
+            tmem_cp_32x128b_warpx4(sfb, sdesc_sf_block(f + SF_BLOCK_BYTES));
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_mxf8_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32),
-                            idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), sfa, sfb, k != s.k0 || kk ? 1u : 0u);
-            } else {
+            for (int kk = 0; kk < 4; ++kk)
+              mma_mxf8_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32),
+                          idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), sfa, sfb, k != u.k0 || kk ? 1u : 0u);
+          } else {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32), idesc, k != s.k0 || kk ? 1u : 0u);
-            }
-            mma_commit(&empty[stage]);
-            if (++stage == NST) stage = 0, parity ^= 1u;
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32), idesc, k != u.k0 || kk ? 1u : 0u);
           }
-          if (!ok) break;
-          mma_commit(&acc_full[acc]);
-          acc ^= 1;
-          if (!acc) acc_parity ^= 1u;
+          mma_commit(&empty[stage]);
         }
+        mma_commit(&acc_full[acc]);
+        acc ^= 1;
+        if (!acc) acc_parity ^= 1u;
+        return true;
+      };
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) ok = multiply(shared_unit(p, i));
+      ok = ok && wait_bar(ready, 0);
+      for (int i = 0; ok; ++i) {
+        const int id = pop(i);
+        if (id < 0) break;
+        ok = multiply(claimed_unit(p, sched, id));
       }
     }
     __syncwarp();
   } else {
     // ---------------- routing, then the accumulators (TMEM lanes 32 ew .. 32 ew + 31)
-    const int ew = warp - 4, tid = threadIdx.x - 128, col = tid;
+    const int ew = warp - 4, tid = threadIdx.x - 128;
     bool ok = true;
     if (!p.given) {
       for (int t = blockIdx.x + ew * gridDim.x; t < p.T; t += 4 * gridDim.x) {
-        token_topk(p, t);
+        token_topk(p, t, sched.w + ew * 32);
         __syncwarp();
-        if (lane == 0) red_release_add_gpu(topk_done, 1);
+        if (lane == 0) red_release_add_gpu(p.counters + CTR_TOPK, 1);
       }
-      ok = agree(wait_counter_ge(topk_done, p.T, p.status, p.timeout_ns));
+      // (one thread asks: the others' loads would be in the way of those that work)
+      ok = agree(tid != 0 || wait_counter_ge(p.counters + CTR_TOPK, p.T, p.status, p.timeout_ns));
     }
     if (ok) build_schedule(p, sched, tid);
-    if (ok) mbar_arrive(ready);
-    const int n_act = ok ? sched.n_act : 0;
     named_bar_sync(3, 128);
+    if (ok) mbar_arrive(ready);
 
     int acc = 0;
     uint32_t acc_parity = 0;
-    Walk w;
-    for (int ph = PH_SHARED; ph <= PH_DOWN && ok; ++ph) {
-      w.enter(p, ph, ph == PH_SHARED ? 0 : n_act);
-      const Phase f = w.f;
-      float* slots = ph == PH_SHARED ? p.slots_s : p.slots;
-      int* ctr = p.counters + ph * gridDim.x;
-      Seg s;
-      while (w.next(p, s)) {
-        const bool routed = s.act >= 0;
-        const int e = routed ? sched.act_e[s.act] : 0;
-        const int n = routed ? __popcll(sched.mask[e]) : p.T, off = routed ? sched.off[e] : 0;
-        float* slot = slot_of(p, slots, f, blockIdx.x, s.tile);
-        if (ph == PH_DOWN && s.first)
-          for (int t = 0; t < p.T; ++t) slot[t * 128 + col] = 0.0f;
-        ok = agree(wait_bar(&acc_full[acc], acc_parity));
+    // one unit's sums out of TMEM; the last of a tile finishes it
+    auto take = [&](const Unit& u) {
+      float* to = unit_sums(p, sched, u) + tid;
+      if (!agree(wait_bar(&acc_full[acc], acc_parity))) return false;
+      tc_fence_after();
+      const uint32_t taddr = tmem + acc * DEC_MAX_T + ((uint32_t)(32 * ew) << 16);
+      for (int n0 = 0; n0 < u.n; n0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + n0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (n0 + j < u.n) to[(n0 + j) * 128] = __uint_as_float(v[j]);
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[acc]);
+      acc ^= 1;
+      if (!acc) acc_parity ^= 1u;
+      return true;
+    };
+    // all units of a phase are done: `mine` of them here.  (One thread asks.)
+    auto all_done = [&](int ctr, int mine, int all) {
+      named_bar_sync(3, 128);
+      if (tid == 0) red_release_add_gpu(p.counters + ctr, mine);
+      return agree(tid != 0 || wait_counter_ge(p.counters + ctr, all, p.status, p.timeout_ns));
+    };
+    int up_units = 0, down_units = 0;
+    bool have_h = false;
+    for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x, ++up_units) ok = take(shared_unit(p, i));
+    for (int i = 0; ok; ++i) {
+      // thread 0 takes the unit from the queue and tells the others
+      if (tid == 0) sched.scan[0] = pop(i);
+      named_bar_sync(3, 128);
+      const int id = sched.scan[0];
+      if (id == -2) ok = false;
+      if (ok && !have_h && (id < 0 || id >= sched.n_u)) {  // the last of this CTA's up/gate units is done
+        ok = all_done(CTR_UP, up_units, n_shared + sched.n_u);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem + acc * DEC_MAX_T + ((uint32_t)(32 * ew) << 16);
-        for (int n0 = 0; n0 < n; n0 += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(taddr + n0, v);
-          tmem_ld_wait();
-          if (ph != PH_DOWN) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (n0 + j < n) slot[(n0 + j) * 256 + s.part * 128 + col] = __uint_as_float(v[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (n0 + j < n) {
-                const int r = routed ? sched.row[off + n0 + j] : 0;
-                const int t = routed ? r / p.k : n0 + j;
-                const float g = routed ? sched.w[r] : 1.0f;
-                slot[t * 128 + col] = fmaf(g, __uint_as_float(v[j]), slot[t * 128 + col]);
-              }
-          }
-        }
-        tc_fence_before();
-        mbar_arrive(&acc_empty[acc]);
-        acc ^= 1;
-        if (!acc) acc_parity ^= 1u;
-        if (s.last) {
-          const int b = s.tile * f.L, c0 = f.owner(b), c1 = f.owner(b + f.L - 1);
-          named_bar_sync(3, 128);
-          if (c0 != c1) {  // cut: counted under its first CTA
-            if (tid == 0) red_release_add_gpu(ctr + c0, 1);
-          } else if (ph == PH_DOWN) {
-            finish_down(p, f, s.tile, ew);
-            named_bar_sync(3, 128);
-          } else {
-            finish_up(p, f, s.tile, slots, ph == PH_SHARED, n, off, ew);
-            named_bar_sync(3, 128);
-          }
-        }
-      }
-      if (!ok) break;
-      if (ph == PH_SHARED) continue;
-      // the cut tiles that this CTA has a part of, of this phase (after the up/gate phase: of the shared expert's too)
-      for (int q = ph == PH_UP ? PH_SHARED : PH_DOWN; q <= ph && ok; ++q) {
-        Walk v;
-        v.enter(p, q, q == PH_SHARED ? 0 : n_act);
-        if (v.lo >= v.hi) continue;
-        const int t0 = v.lo / v.f.L, t1 = (v.hi - 1) / v.f.L;
-        for (int i = 0; i < (t0 == t1 ? 1 : 2) && ok; ++i) {
-          const int tile = i ? t1 : t0;
-          const int c0 = v.f.owner(tile * v.f.L), c1 = v.f.owner((tile + 1) * v.f.L - 1);
-          if (c0 == c1) continue;
-          int* const flag = p.counters + q * gridDim.x + c0;
-          ok = agree(wait_counter_ge(flag, c1 - c0 + 1, p.status, p.timeout_ns));
-          if (!ok) break;
-          if (q == PH_DOWN) {
-            finish_down(p, v.f, tile, ew);
-          } else {
-            const int e = q == PH_UP ? sched.act_e[tile / (p.I / 128)] : 0;
-            finish_up(p, v.f, tile, q == PH_SHARED ? p.slots_s : p.slots, q == PH_SHARED,
-                      q == PH_UP ? __popcll(sched.mask[e]) : p.T, q == PH_UP ? sched.off[e] : 0, ew);
-          }
-        }
-      }
-      if (ph == PH_UP) {  // h is read by TMA of every CTA; slots are used again only after all have read them
-        fence_proxy_async_global();
+        finish_up(p, sched, ew);
+        fence_proxy_async_global();  // h is read by TMA
         named_bar_sync(3, 128);
-        if (tid == 0 && ok) red_release_add_gpu(h_done, 1);
-        ok = agree(ok && wait_counter_ge(h_done, (int)gridDim.x, p.status, p.timeout_ns));
-      } else if (w.f.total == 0) {  // no expert and no shared expert: zeros
-        for (int tile = blockIdx.x; tile < p.D / 128; tile += gridDim.x)
-          for (int t = ew; t < p.T; t += 4)
-            *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + tile * 128 + 4 * lane) = make_uint2(0u, 0u);
+        if (tid == 0) red_release_add_gpu(p.counters + CTR_H, 1);
+        have_h = true;
       }
+      if (id < 0) break;
+      ok = take(claimed_unit(p, sched, id));
+      if (id < sched.n_u) ++up_units;
+      else ++down_units;
     }
+    if (ok) ok = all_done(CTR_DOWN, down_units, sched.n_d);
+    if (ok) finish_down(p, sched, ew);  // (without any expert: zeros)
   }
   tc_fence_before();
   __syncthreads();
@@ -907,7 +1008,8 @@ namespace {
 constexpr size_t dec_align(size_t v) { return (v + 255) / 256 * 256; }
 
 struct DecodeLayout {
-  size_t status, counters, logits, topk_idx, topk_w, xq, xs, h, hs, h_s, slots, slots_s, total;
+  size_t status, counters, logits, topk_idx, topk_w, xq, xs, h, hs, h_s, sums_s, sums_u, sums_d, sums_ds, total;
+  int q_s, q_ds, most_u, most_d;
 };
 DecodeLayout decode_layout(const moe_plan* pl, int64_t T) {
   const moe_config& c = pl->cfg;
@@ -921,7 +1023,16 @@ DecodeLayout decode_layout(const moe_plan* pl, int64_t T) {
     return here;
   };
   L.status = take(STATUS_AREA_BYTES);
-  L.counters = take(sizeof(int) * (3 * pl->num_sms + 2));
+  const int64_t step = mx ? BK_MX : BK, kd = c.D / step, ki = c.I / step;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  // units: the shared expert's up/gate projections are cut here, the others when the
+  // experts are known, into at most so many pieces (fewer for more tokens, whose sums are larger)
+  L.q_s = dec_unit_steps((int)(c.I_s / 128 * 2 * (c.D / BK)), pl->num_sms, (int)ncap);
+  const int64_t most = T <= 8 ? 16 : 128 / T;
+  L.most_u = (int)(most < up(kd, 4) ? most : up(kd, 4));
+  L.most_d = (int)(most < up(ki, 4) ? most : up(ki, 4));
+  L.q_ds = (int)up(c.I_s / BK, most);
+  L.counters = take(sizeof(int) * DEC_COUNTERS);
   L.logits = take(sizeof(float2) * T * c.E);
   L.topk_idx = take(sizeof(int) * R);
   L.topk_w = take(sizeof(float) * R);
@@ -930,8 +1041,10 @@ DecodeLayout decode_layout(const moe_plan* pl, int64_t T) {
   L.h = take((size_t)R * c.I * (mx ? 1 : 2));
   L.hs = take(mx ? R * (c.I / 32) : 0);
   L.h_s = take((size_t)DEC_MAX_T * c.I_s * 2);
-  L.slots = take(sizeof(float) * 256 * ncap * DEC_SLOTS * pl->num_sms);
-  L.slots_s = take(c.I_s ? sizeof(float) * 256 * ncap * DEC_SLOTS * pl->num_sms : 0);
+  L.sums_s = take((size_t)(c.I_s / 128) * 2 * up(c.D / BK, L.q_s) * T * 512);
+  L.sums_u = take((size_t)(c.I / 128) * 2 * L.most_u * R * 512);
+  L.sums_d = take((size_t)(c.D / 128) * L.most_d * R * 512);
+  L.sums_ds = take((size_t)(c.D / 128) * (c.I_s ? most : 0) * T * 512);
   L.total = at;
   return L;
 }
@@ -993,7 +1106,9 @@ int decode(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, c
   p.xq = ws + L.xq, p.xs = ws + L.xs;
   p.h = ws + L.h, p.hs = ws + L.hs;
   p.h_s = reinterpret_cast<bf16*>(ws + L.h_s);
-  p.slots = reinterpret_cast<float*>(ws + L.slots), p.slots_s = reinterpret_cast<float*>(ws + L.slots_s);
+  p.sums_s = reinterpret_cast<float*>(ws + L.sums_s), p.sums_u = reinterpret_cast<float*>(ws + L.sums_u);
+  p.sums_d = reinterpret_cast<float*>(ws + L.sums_d), p.sums_ds = reinterpret_cast<float*>(ws + L.sums_ds);
+  p.q_s = L.q_s, p.q_ds = L.q_ds, p.most_u = L.most_u, p.most_d = L.most_d;
   p.sf_up = w->W_up_scale, p.sf_gate = w->W_gate_scale, p.sf_down = w->W_down_scale;
 
   DecodeMaps m;
