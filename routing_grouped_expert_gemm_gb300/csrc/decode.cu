@@ -45,6 +45,7 @@ constexpr int DEC_MAX_STAGES = 12;
 constexpr int DEC_THREADS = 256;
 constexpr int DEC_A_BYTES = 128 * 128;              // weights of a step
 enum : int { CTR_TOPK = 0, CTR_CLAIMS, CTR_UP /* units done */, CTR_H /* CTAs whose share of h is written */, CTR_DOWN, DEC_COUNTERS };
+constexpr int DEC_OWN_TOPK = 4;                     // up to so many tokens every CTA makes all tokens' selection itself
 constexpr int DEC_EARLY = 5;                        // steps loaded before the grid's barrier
 constexpr int DEC_QUEUE = 4;                        // claimed units on their way to the roles of a CTA
 
@@ -64,6 +65,7 @@ __host__ __device__ inline int dec_unit_steps(int total, int ctas, int ncap) {
 struct DecodeParams {
   int T, D, I, E, k, I_s;
   int score_fn, given, mx;
+  int inv_k;      // ceil(2^16 / k)
   int ncap;       // columns of a step's tokens (T rounded up to 16)
   int n_stages, stage_bytes;
   long long timeout_ns;
@@ -237,7 +239,7 @@ __device__ void router_logits(const DecodeParams& p, float* red /* [2][4][RT_E R
   const int groups = (p.T + RT_T - 1) / RT_T, chunks = p.D / 256;
   const int per = p.E * groups <= 4 * (int)gridDim.x ? 1 : RT_E, items = (p.E + per - 1) / per * groups;
   for (int first = blockIdx.x; first < items; first += 2 * gridDim.x) {
-    const int item = first + team * (int)gridDim.x;
+    const int item = first + (1 - team) * (int)gridDim.x;  // (a thread of team 0 starts the loads first)
     const bool on = item < items;
     const int e0 = on ? item / groups * per : 0, t0 = on ? item % groups * RT_T : 0;
     const int ne = min(per, p.E - e0), nt = min(RT_T, p.T - t0);
@@ -305,11 +307,24 @@ __device__ __forceinline__ uint32_t dec_key(float f) {  // order of floats as un
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// The undecided experts of a token (bit i of `und` in lane l: expert l + 32 i)
-// ranked in fp64; the `want` first are added to `sel`.
-__device__ __noinline__ uint32_t decide_fp64(const DecodeParams& p, int t, uint32_t und, uint32_t sel, int want) {
+// The selection of token t where fp32 left it open, by one warp: `words` are the
+// selected so far (bit e % 32 of word e / 32); those that may be in or out, given what
+// every logit may be off by, are ranked by their logits in fp64.
+__device__ __noinline__ void decide_fp64(const DecodeParams& p, int t, float lo, float hi, uint32_t* words) {
   const int lane = threadIdx.x & 31;
   double v[E_MAX / 32];
+  uint32_t und = 0u, sel = 0u;  // bit i: expert lane + 32 i
+  int want = 0;
+  for (int i = 0; i * 32 < p.E; ++i) {
+    const int e = lane + 32 * i;
+    if (e >= p.E) continue;
+    const float2 q = __ldcg(p.logits + (size_t)t * p.E + e);
+    const bool in = words[i] >> lane & 1;
+    const bool open = in ? q.x - q.y <= hi : q.x + q.y >= lo;
+    if (open) und |= 1u << i, want += in;
+    else if (in) sel |= 1u << i;
+  }
+  want = (int)__reduce_add_sync(0xffffffffu, (unsigned)want);
   for (int i = 0; i * 32 < p.E; ++i) {
     uint32_t who = __ballot_sync(0xffffffffu, und >> i & 1);
     while (who) {
@@ -335,45 +350,64 @@ __device__ __noinline__ uint32_t decide_fp64(const DecodeParams& p, int t, uint3
     }
     if (id != 1 << 20 && (id & 31) == lane) und &= ~(1u << (id >> 5)), sel |= 1u << (id >> 5);
   }
-  return sel;
+  for (int i = 0; i * 32 < p.E; ++i) {
+    const uint32_t w = __ballot_sync(0xffffffffu, sel >> i & 1);
+    if (lane == 0) words[i] = w;
+  }
 }
 
-// Experts and weights of token t, one warp
-__device__ void token_topk(const DecodeParams& p, int t, float* logit /* [k], shared memory of the warp */) {
-  const int lane = threadIdx.x & 31, k = p.k;
-  float v[E_MAX / 32], err[E_MAX / 32];
-  uint32_t left = 0u, key[E_MAX / 32];
+struct TopkScratch {
+  uint32_t key[E_MAX];
+  uint32_t words[E_MAX / 32];
+  float range[3][4];
+  float logit[TOPK_MAX];
+  int idx[TOPK_MAX];
+};
+static_assert(sizeof(TopkScratch) <= sizeof(DecodeSched::mask), "scratch of the selection lies where the masks come to lie");
+
+// Experts and weights of token t, by the epilogue's 128 threads (thread i has
+// experts i + 128 j): an expert's rank is the number of keys before its own, counted
+// in a short loop over all of them (selecting the largest k times over took 15 us of a
+// call at 256 experts; this takes 2).
+__device__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s, int* idx, float* wt) {
+  const int lane = tid & 31, ew = tid >> 5, k = p.k;
+  constexpr int NI = E_MAX / 128;
+  float v[NI], err[NI];
+  uint32_t key[NI];
   float most = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E_MAX / 32; ++i) {
-    const int e = lane + 32 * i;
+  for (int i = 0; i < NI; ++i) {
+    const int e = tid + 128 * i;
     v[i] = err[i] = 0.0f, key[i] = 0u;
     if (e < p.E) {
       const float2 q = __ldcg(p.logits + (size_t)t * p.E + e);
       v[i] = q.x, err[i] = q.y, key[i] = dec_key(q.x);
       most = fmaxf(most, q.y);
-      left |= 1u << i;
     }
+    s.key[e] = key[i];
   }
-  uint32_t sel = 0u;
-  for (int n = 0; n < k; ++n) {
-    uint32_t b = 0u;
-    int id = 1 << 20;
+  named_bar_sync(3, 128);
+  int rank[NI] = {0, 0, 0, 0};
+#pragma unroll 1
+  for (int j = 0; j < p.E; j += 4) {  // (keys past the last expert are 0 and behind it in every tie)
+    const uint4 q = *reinterpret_cast<const uint4*>(s.key + j);
 #pragma unroll
-    for (int i = 0; i < E_MAX / 32; ++i) {
-      if (32 * i >= p.E) break;
-      if ((left >> i & 1) && (id == 1 << 20 || key[i] > b)) b = key[i], id = lane + 32 * i;
+    for (int i = 0; i < NI; ++i) {
+      if (128 * i >= p.E) break;
+      const int e = tid + 128 * i - j;  // ties: the lower id is before
+      rank[i] += (q.x > key[i] || (q.x == key[i] && 0 < e)) + (q.y > key[i] || (q.y == key[i] && 1 < e)) +
+                 (q.z > key[i] || (q.z == key[i] && 2 < e)) + (q.w > key[i] || (q.w == key[i] && 3 < e));
     }
-    const uint32_t m = __reduce_max_sync(0xffffffffu, b);
-    id = (int)__reduce_min_sync(0xffffffffu, b == m ? (unsigned)id : 1u << 20);
-    if ((id & 31) == lane) left &= ~(1u << (id >> 5)), sel |= 1u << (id >> 5);
   }
   // lowest that a selected logit may be, highest that another may be
   float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < E_MAX / 32; ++i) {
-    if (sel >> i & 1) lo = fminf(lo, v[i] - err[i]);
-    else if (left >> i & 1) hi = fmaxf(hi, v[i] + err[i]);
+  for (int i = 0; i < NI; ++i) {
+    const bool there = tid + 128 * i < p.E, in = there && rank[i] < k;
+    if (in) lo = fminf(lo, v[i] - err[i]);
+    else if (there) hi = fmaxf(hi, v[i] + err[i]);
+    const uint32_t w = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) s.words[4 * i + ew] = w;
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
@@ -381,68 +415,69 @@ __device__ void token_topk(const DecodeParams& p, int t, float* logit /* [k], sh
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
   }
+  if (lane == 0) s.range[0][ew] = lo, s.range[1][ew] = hi, s.range[2][ew] = most;
+  named_bar_sync(3, 128);
+  lo = fminf(fminf(s.range[0][0], s.range[0][1]), fminf(s.range[0][2], s.range[0][3]));
+  hi = fmaxf(fmaxf(s.range[1][0], s.range[1][1]), fmaxf(s.range[1][2], s.range[1][3]));
+  most = fmaxf(fmaxf(s.range[2][0], s.range[2][1]), fmaxf(s.range[2][2], s.range[2][3]));
   if (most > 0.0f && lo <= hi) {  // (exact logits that are equal are ties, decided above)
-    uint32_t und = 0u;
-    int want = 0;
-#pragma unroll
-    for (int i = 0; i < E_MAX / 32; ++i) {
-      const bool in = sel >> i & 1;
-      if (in ? v[i] - err[i] <= hi : (left >> i & 1) && v[i] + err[i] >= lo) und |= 1u << i, want += in;
-    }
-    want = (int)__reduce_add_sync(0xffffffffu, (unsigned)want);
-    sel = decide_fp64(p, t, und, sel & ~und, want);
+    if (ew == 0) decide_fp64(p, t, lo, hi, s.words);
+    named_bar_sync(3, 128);
   }
-  // the selected in ascending order: slot = number of selected experts below
-  int slot = 0;
+  // slots in ascending order: the selected experts below
 #pragma unroll
-  for (int i = 0; i < E_MAX / 32; ++i) {
-    if (32 * i >= p.E) break;
-    const uint32_t row = __ballot_sync(0xffffffffu, sel >> i & 1);
-    if (sel >> i & 1) {
-      const int s = slot + __popc(row & ((1u << lane) - 1u));
-      p.topk_idx[(size_t)t * k + s] = lane + 32 * i;
-      logit[s] = v[i];
-      if (p.out_idx) p.out_idx[(size_t)t * k + s] = lane + 32 * i;
-    }
-    slot += __popc(row);
+  for (int i = 0; i < NI; ++i) {
+    if (!(s.words[4 * i + ew] >> lane & 1)) continue;
+    int slot = __popc(s.words[4 * i + ew] & ((1u << lane) - 1u));
+    for (int w = 0; w < 4 * i + ew; ++w) slot += __popc(s.words[w]);
+    s.logit[slot] = v[i];
+    idx[slot] = tid + 128 * i;
+    if (p.out_idx && (int)blockIdx.x == t % (int)gridDim.x) p.out_idx[(size_t)t * k + slot] = tid + 128 * i;
   }
-  __syncwarp();
+  named_bar_sync(3, 128);
   // weights over their sum.  Softmax: exp(l - m); sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)), both factors scaled so
   // that the largest is near 1 (logits far below 0 leave fp32's range otherwise)
-  const float l = lane < k ? logit[lane] : -INFINITY;
-  const bool soft = p.score_fn == MOE_SCORE_SOFTMAX;
-  const float a = soft ? l : fminf(l, 0.0f);
-  float m = a;
+  if (ew == 0) {
+    const float l = lane < k ? s.logit[lane] : -INFINITY;
+    const bool soft = p.score_fn == MOE_SCORE_SOFTMAX;
+    const float a = soft ? l : fminf(l, 0.0f);
+    float m = a;
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float s = lane < k ? expf(a - m) : 0.0f;
-  if (!soft && lane < k) s /= 1.0f + expf(-fabsf(l));
-  float sum = s;
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float w = lane < k ? expf(a - m) : 0.0f;
+    if (!soft && lane < k) w /= 1.0f + expf(-fabsf(l));
+    float sum = w;
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane < k) {
-    p.topk_w[(size_t)t * k + lane] = s / sum;
-    if (p.out_w) p.out_w[(size_t)t * k + lane] = s / sum;
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane < k) {
+      wt[lane] = w / sum;
+      if (p.out_w && (int)blockIdx.x == t % (int)gridDim.x) p.out_w[(size_t)t * k + lane] = w / sum;
+    }
   }
 }
+
+// r / k for a route r, by a reciprocal: r (k ceil(2^16 / k) - 2^16) < 2^16 for r < 1024
+__device__ __forceinline__ int token_of(const DecodeParams& p, int r) { return (int)((unsigned)r * (unsigned)p.inv_k >> 16); }
 
 // The routing into shared memory, by the 128 threads of the epilogue warps
 __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
   const int R = p.T * p.k;
-  const int* idx = p.given ? p.in_idx : p.topk_idx;
-  const float* wt = p.given ? p.in_w : p.topk_w;
   for (int e = tid; e < p.E; e += 128) s.mask[e] = 0ull;
-  for (int r = tid; r < R; r += 128) {
-    const int e = __ldcg(idx + r);
-    const bool ok = e >= 0 && e < p.E;
-    if (!ok && e != -1 && blockIdx.x == 0) atomicOr(p.status + 1, FLAG_ROUTES_INVALID);
-    s.idx[r] = ok ? (uint16_t)e : (uint16_t)0xffffu;
-    s.w[r] = __ldcg(wt + r);
+  if (p.given || p.T > DEC_OWN_TOPK) {
+    const int* idx = p.given ? p.in_idx : p.topk_idx;
+    const float* wt = p.given ? p.in_w : p.topk_w;
+    for (int r = tid; r < R; r += 128) {
+      const int e = __ldcg(idx + r);
+      s.w[r] = __ldcg(wt + r);
+      const bool ok = e >= 0 && e < p.E;
+      if (!ok && e != -1 && blockIdx.x == 0) atomicOr(p.status + 1, FLAG_ROUTES_INVALID);
+      s.idx[r] = ok ? (uint16_t)e : (uint16_t)0xffffu;
+    }
   }
   named_bar_sync(3, 128);
   if (p.given) {  // a second slot of a token with the same expert is an empty one
     for (int r = tid; r < R; r += 128) {
-      const int t = r / p.k;
+      const int t = token_of(p, r);
       const uint16_t e = s.idx[r];
       bool twice = false;
       for (int q = t * p.k; q < r; ++q) twice |= e != 0xffffu && s.idx[q] == e;
@@ -454,7 +489,7 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
     for (int r = tid; r < R; r += 128)
       if (s.row[r]) s.idx[r] = 0xffffu;
   } else {
-    for (int r = tid; r < R; r += 128) atomicOr(&s.mask[s.idx[r]], 1ull << (r / p.k));
+    for (int r = tid; r < R; r += 128) atomicOr(&s.mask[s.idx[r]], 1ull << token_of(p, r));
   }
   named_bar_sync(3, 128);
   // rows and active experts before every expert: thread i takes experts 4 i .. 4 i + 3
@@ -506,7 +541,7 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
   named_bar_sync(3, 128);
   for (int r = tid; r < R; r += 128) {
     const uint16_t e = s.idx[r];
-    if (e != 0xffffu) s.row[s.off[e] + __popcll(s.mask[e] & ((1ull << (r / p.k)) - 1ull))] = (uint16_t)r;
+    if (e != 0xffffu) s.row[s.off[e] + __popcll(s.mask[e] & ((1ull << token_of(p, r)) - 1ull))] = (uint16_t)r;
   }
 }
 
@@ -530,7 +565,7 @@ __device__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) 
     const float* su = (shared ? p.sums_s : p.sums_u) + ((size_t)tile * 2 * m * rows + r) * 128 + 4 * lane;
     const float* sg = su + (size_t)m * rows * 128;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), g = a;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < m; ++c) {
       add4(a, ldcg4(su + c * rows * 128));
       add4(g, ldcg4(sg + c * rows * 128));
@@ -570,15 +605,41 @@ __device__ void finish_down(const DecodeParams& p, const DecodeSched& sc, int ew
   for (int it = blockIdx.x + ew * gridDim.x; it < p.T * tiles; it += 4 * gridDim.x) {
     const int t = it / tiles, tile = it % tiles;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < sc.m_ds; ++c) add4(s, ldcg4(p.sums_ds + ((size_t)(tile * sc.m_ds + c) * p.T + t) * 128 + 4 * lane));
 #pragma unroll 4
-    for (int j = 0; j < p.k; ++j) {
-      const int r = t * p.k + j, e = sc.idx[r];
-      if (e == 0xffff) continue;
-      const int row = sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull));
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = 0; c < sc.m_d; ++c) add4(y, ldcg4(p.sums_d + ((size_t)(tile * sc.m_d + c) * R + row) * 128 + 4 * lane));
-      fma4(s, sc.w[r], y);
+    for (int c = 0; c < sc.m_ds; ++c) add4(s, ldcg4(p.sums_ds + ((size_t)(tile * sc.m_ds + c) * p.T + t) * 128 + 4 * lane));
+    // four slots and four pieces on their way at once
+    for (int j0 = 0; j0 < p.k; j0 += 4) {
+      const float* from[4];
+      float g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = t * p.k + j0 + j, e = j0 + j < p.k ? sc.idx[r] : 0xffff;
+        from[j] = nullptr, g[j] = 0.0f;
+        if (e != 0xffff) {
+          const int row = sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull));
+          from[j] = p.sums_d + ((size_t)tile * sc.m_d * R + row) * 128 + 4 * lane;
+          g[j] = sc.w[r];
+        }
+      }
+      float4 y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c0 = 0; c0 < sc.m_d; c0 += 4) {
+        float4 q[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            q[j][c] = from[j] && c0 + c < sc.m_d ? ldcg4(from[j] + (size_t)(c0 + c) * R * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c0 + c < sc.m_d) add4(y[j], q[j][c]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (from[j]) fma4(s, g[j], y[j]);
     }
     *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + tile * 128 + 4 * lane) =
         make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
@@ -620,20 +681,13 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     }
     fence_barrier_init();
   }
-  if (warp == 1) {
-    tmem_alloc<256>(tmem_slot);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  // Loads of one step: 128 rows of weights; the rows of x or h of the unit's tokens
+  // Loads of one step: 128 rows of weights; the rows of x or h of the unit's tokens.  Weights are read once: they are
+  // the first to leave L2, and do not push out what is used again (tokens, sums, the kernel's own code)
+  const uint64_t once = l2_policy_evict_first();
   auto load_weights = [&](const Unit& u, int k, int stage, const CUtensorMap* m, int row, const uint8_t* scales) {
     const bool mx = MX && scales;
     mbar_arrive_expect_tx(&full[stage], DEC_A_BYTES + (mx ? SF_BLOCK_BYTES : 0));
-    tma_load_2d(smem + stage * p.stage_bytes, m, &full[stage], k * (mx ? BK_MX : BK), row);
+    tma_load_2d_hint(smem + stage * p.stage_bytes, m, &full[stage], k * (mx ? BK_MX : BK), row, once);
     if (mx) bulk_load(sf + stage * 2 * SF_BLOCK_BYTES, scales + (size_t)k * SF_BLOCK_BYTES, SF_BLOCK_BYTES, &full[stage]);
   };
   auto load_x = [&](int k, int stage) {
@@ -641,8 +695,11 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     tma_load_2d(smem + stage * p.stage_bytes + DEC_A_BYTES, &maps.x, &full[stage], k * BK, 0);
   };
 
-  // ---- before the grid's barrier: the first loads of the shared expert's weights (they wait for nothing);
+  // ---- before the grid's barrier: the first loads of the shared expert's weights (they wait for nothing; the other
+  // warps are at the router's weights meanwhile);
   // counters and status to zero, logits, x as codes
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + (int)(sizeof(DecodeMaps) / sizeof(CUtensorMap)))
+    prefetch_tensormap(reinterpret_cast<const CUtensorMap*>(&maps) + (threadIdx.x - 128));
   const int n_shared = shared_units(p), early_most = min(NST, DEC_EARLY);
   if (threadIdx.x == 0) {
     int stage = 0;
@@ -669,9 +726,16 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     }
     fence_proxy_async_global();  // read by TMA
   }
+  if (warp == 1) {
+    tmem_alloc<256>(tmem_slot);
+    tmem_relinquish();
+  }
   __syncwarp();
   if (!p.given) router_logits(p, reinterpret_cast<float*>(&sched));
-  cooperative_groups::this_grid().sync();
+  tc_fence_before();
+  cooperative_groups::this_grid().sync();  // (of this CTA's threads too)
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   if (MX) fence_proxy_async_global();
 
   // the epilogue's 128 threads go on together or not at all
@@ -786,7 +850,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
       if (u.phase == PH_UP) {
         loads = (u.n + 3) / 4, bytes = (uint32_t)loads * 512;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t[j] = sched.row[u.off + min(4 * lane + j, u.n - 1)] / p.k;
+        for (int j = 0; j < 4; ++j) t[j] = token_of(p, sched.row[u.off + min(4 * lane + j, u.n - 1)]);
       } else {
         loads = (u.n + 15) / 16, bytes = (uint32_t)loads * 2048;
       }
@@ -845,7 +909,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
           for (int j = 0; j < 2; ++j) {
             const int r = lane + 32 * j;
             if (r < u.n)
-              src[j] = reinterpret_cast<const uint32_t*>(u.phase == PH_UP ? p.xs + (size_t)(sched.row[u.off + r] / p.k) * (p.D / 32)
+              src[j] = reinterpret_cast<const uint32_t*>(u.phase == PH_UP ? p.xs + (size_t)token_of(p, sched.row[u.off + r]) * (p.D / 32)
                                                                          : p.hs + (size_t)(u.off + r) * (p.I / 32));
           }
         }
@@ -926,13 +990,23 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     const int ew = warp - 4, tid = threadIdx.x - 128;
     bool ok = true;
     if (!p.given) {
-      for (int t = blockIdx.x + ew * gridDim.x; t < p.T; t += 4 * gridDim.x) {
-        token_topk(p, t, sched.w + ew * 32);
-        __syncwarp();
-        if (lane == 0) red_release_add_gpu(p.counters + CTR_TOPK, 1);
+      TopkScratch& scratch = *reinterpret_cast<TopkScratch*>(sched.mask);
+      if (p.T <= DEC_OWN_TOPK) {
+        for (int t = 0; t < p.T; ++t) {
+          token_topk(p, t, tid, scratch, scratch.idx, sched.w + t * p.k);
+          if (tid < p.k) sched.idx[t * p.k + tid] = (uint16_t)scratch.idx[tid];  // (written before the last barrier)
+          named_bar_sync(3, 128);
+        }
+      } else {
+        int mine = 0;
+        for (int t = blockIdx.x; t < p.T; t += gridDim.x, ++mine) {
+          token_topk(p, t, tid, scratch, p.topk_idx + (size_t)t * p.k, p.topk_w + (size_t)t * p.k);
+          named_bar_sync(3, 128);
+        }
+        if (tid == 0 && mine) red_release_add_gpu(p.counters + CTR_TOPK, mine);
+        // (one thread asks: the others' loads would be in the way of those that work)
+        ok = agree(tid != 0 || wait_counter_ge(p.counters + CTR_TOPK, p.T, p.status, p.timeout_ns));
       }
-      // (one thread asks: the others' loads would be in the way of those that work)
-      ok = agree(tid != 0 || wait_counter_ge(p.counters + CTR_TOPK, p.T, p.status, p.timeout_ns));
     }
     if (ok) build_schedule(p, sched, tid);
     named_bar_sync(3, 128);
@@ -1083,6 +1157,7 @@ int decode(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, c
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeParams p{};
   p.T = (int)T, p.D = (int)c.D, p.I = (int)c.I, p.E = (int)c.E, p.k = (int)c.k, p.I_s = shared ? (int)c.I_s : 0;
+  p.inv_k = (65536 + p.k - 1) / p.k;
   p.score_fn = c.score_fn;
   p.given = given;
   p.mx = mx;
