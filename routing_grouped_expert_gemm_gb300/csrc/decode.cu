@@ -124,88 +124,111 @@ struct DecodeSched {
   int n_rows;           // rows: routes that are not empty
 };
 
-constexpr int dec_smem_fixed() { return (int)sizeof(DecodeSched) + 1024 /* alignment */ + 512 /* barriers */; }
-
 enum : int { PH_SHARED = 0, PH_UP = 1, PH_DOWN = 2 };
 
+// A unit as the role that loads weights hands it to the others
 struct Unit {
-  int phase;
-  int tile;    // 128 rows: of the expert's up/gate matrices, or of the output
-  int part;    // up/gate: 0 up rows, 1 gate rows
-  int piece;
-  int act;     // index of the active expert, -1: the shared expert
-  int e;       // that expert
+  int phase;   // PH_*, or -1: no more
+  int routed;  // 0: the shared expert
   int k0, k1;  // steps
   int n, off;  // its tokens and their first row
+  int m, row;  // weights: tensor map (order of DecodeMaps) and first row
+  float* sums; // where its sums go: [n][128]
+  const uint8_t* scales;  // MXFP8: the weights' scale blocks of these rows
 };
+enum : int { M_X = 0, M_X_ROWS, M_UP, M_GATE, M_DOWN, M_S_UP, M_S_GATE, M_S_DOWN, M_H, M_H_S };
 
-__device__ __forceinline__ void unit_expert(const DecodeParams& p, const DecodeSched& s, Unit& u) {
-  if (u.act >= 0) {
-    u.e = s.act_e[u.act];
-    u.n = __popcll(s.mask[u.e]);
-    u.off = s.off[u.e];
-  } else {
-    u.e = u.off = 0;
-    u.n = p.T;
-  }
-}
-// Unit i of the shared expert's up/gate phase
 __device__ __forceinline__ int shared_pieces(const DecodeParams& p) { return (p.D / BK + p.q_s - 1) / p.q_s; }
 __device__ __forceinline__ int shared_units(const DecodeParams& p) { return p.I_s / 128 * 2 * shared_pieces(p); }
-__device__ __forceinline__ Unit shared_unit(const DecodeParams& p, int i) {
-  const int m = shared_pieces(p);
-  Unit u;
+// Unit i of the shared expert's up/gate phase
+__device__ __forceinline__ void shared_unit(const DecodeParams& p, int i, Unit& u) {
+  const int m = shared_pieces(p), piece = i % m, tp = i / m;  // tp: tile and part
   u.phase = PH_SHARED;
-  u.piece = i % m;
-  u.part = i / m & 1;
-  u.tile = i / (2 * m);
-  u.act = -1, u.e = 0, u.n = p.T, u.off = 0;
-  u.k0 = u.piece * p.q_s;
+  u.routed = 0;
+  u.n = p.T, u.off = 0;
+  u.m = tp & 1 ? M_S_GATE : M_S_UP;
+  u.row = (tp >> 1) * 128;
+  u.k0 = piece * p.q_s;
   u.k1 = min(p.D / BK, u.k0 + p.q_s);
-  return u;
+  u.sums = p.sums_s + (size_t)i * p.T * 128;
+  u.scales = nullptr;
 }
 // Claimed unit i
-__device__ __forceinline__ Unit claimed_unit(const DecodeParams& p, const DecodeSched& s, int i) {
-  Unit u;
-  if (i < s.n_u) {
+__device__ __noinline__ void claimed_unit(const DecodeParams& p, const DecodeSched& s, int i, Unit& u) {
+  const size_t R = (size_t)p.T * p.k;
+  int act = -1, kd;
+  if (i < s.n_u) {  // (active expert, tile, part, piece)
     u.phase = PH_UP;
-    u.piece = i % s.m_u;
-    i /= s.m_u;
-    u.part = i & 1;
-    i >>= 1;
-    u.tile = i % (p.I / 128);
-    u.act = i / (p.I / 128);
-    u.k0 = u.piece * s.q_u;
-    u.k1 = min(p.D / (p.mx ? BK_MX : BK), u.k0 + s.q_u);
-  } else {
+    const int piece = i % s.m_u, tp = i / s.m_u % (p.I / 64), tile = tp >> 1;
+    act = i / s.m_u / (p.I / 64);
+    kd = p.D;
+    u.k0 = piece * s.q_u, u.k1 = u.k0 + s.q_u;
+    u.m = tp & 1 ? M_GATE : M_UP;
+    u.row = s.act_e[act] * p.I + tile * 128;
+    u.scales = tp & 1 ? p.sf_gate : p.sf_up;
+    u.sums = p.sums_u + (size_t)(tp * s.m_u + piece) * R * 128;
+  } else {  // (output tile, shared expert's pieces, (active expert, piece))
     i -= s.n_u;
-    const int per = s.m_ds + s.n_act * s.m_d;
     u.phase = PH_DOWN;
-    u.part = 0;
-    u.tile = i / per;
-    i -= u.tile * per;
-    int k;
+    const int per = s.m_ds + s.n_act * s.m_d, tile = i / per;
+    i -= tile * per;
+    int piece = i;
     if (i < s.m_ds) {
-      u.act = -1, u.piece = i;
-      k = p.I_s / BK;
+      kd = p.I_s;
+      u.m = M_S_DOWN, u.row = tile * 128;
+      u.sums = p.sums_ds + (size_t)(tile * s.m_ds + piece) * p.T * 128;
     } else {
       i -= s.m_ds;
-      u.act = i / s.m_d, u.piece = i % s.m_d;
-      k = p.I / (p.mx ? BK_MX : BK);
+      act = i / s.m_d, piece = i % s.m_d;
+      kd = p.I;
+      u.m = M_DOWN, u.row = s.act_e[act] * p.D + tile * 128;
+      u.sums = p.sums_d + (size_t)(tile * s.m_d + piece) * R * 128;
     }
-    u.k0 = u.piece * s.q_d;
-    u.k1 = min(k, u.k0 + s.q_d);
+    u.scales = p.sf_down;
+    u.k0 = piece * s.q_d, u.k1 = u.k0 + s.q_d;
   }
-  unit_expert(p, s, u);
-  return u;
+  u.routed = act >= 0;
+  const int step = p.mx && u.routed ? BK_MX : BK;
+  u.k1 = min(u.k1, kd / step);
+  if (u.routed) {
+    const int e = s.act_e[act];
+    u.n = __popcll(s.mask[e]);
+    u.off = s.off[e];
+    u.sums += (size_t)u.off * 128;
+    u.scales = p.mx ? u.scales + (size_t)(u.row / 128) * (kd / BK_MX) * SF_BLOCK_BYTES : nullptr;
+  } else {
+    u.n = p.T, u.off = 0;
+    u.scales = nullptr;
+  }
 }
-// Where a unit's sums go: [n][128] floats
-__device__ __forceinline__ float* unit_sums(const DecodeParams& p, const DecodeSched& s, const Unit& u) {
-  const size_t R = (size_t)p.T * p.k;
-  if (u.phase == PH_SHARED) return p.sums_s + ((size_t)((u.tile * 2 + u.part) * shared_pieces(p) + u.piece) * p.T) * 128;
-  if (u.phase == PH_UP) return p.sums_u + ((size_t)((u.tile * 2 + u.part) * s.m_u + u.piece) * R + u.off) * 128;
-  if (u.act < 0) return p.sums_ds + ((size_t)(u.tile * s.m_ds + u.piece) * p.T) * 128;
-  return p.sums_d + ((size_t)(u.tile * s.m_d + u.piece) * R + u.off) * 128;
+
+// Everything of a CTA in shared memory but the stages
+struct DecodeShared {
+  DecodeSched sched;
+  DecodeParams p;  // (here its fields cost 30 cycles, not a miss of the constant cache each)
+  Unit queue[DEC_QUEUE];
+  uint64_t full[DEC_MAX_STAGES], empty[DEC_MAX_STAGES], acc_full[2], acc_empty[2], ready, q_full[DEC_QUEUE], q_empty[DEC_QUEUE];
+  uint32_t tmem;
+};
+constexpr int dec_smem_fixed() { return (int)sizeof(DecodeShared) + 1024 /* alignment */; }
+
+// Bounded waits (as in common.cuh), out of line: a launch runs most of this kernel's
+// code once, and what it costs then is fetching it
+__device__ __noinline__ bool dec_wait_slow(uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  return mbar_wait(bar, parity, p.status, p.timeout_ns);
+}
+__device__ __forceinline__ bool dec_wait(uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  return mbar_try_wait(bar, parity) || dec_wait_slow(bar, parity, p);
+}
+__device__ __noinline__ bool dec_wait_count(int ctr, int need, const DecodeParams& p) {
+  return wait_counter_ge(p.counters + ctr, need, p.status, p.timeout_ns);
+}
+// the epilogue's 128 threads go on together or not at all
+__device__ __forceinline__ bool agree(bool v) {
+  uint32_t all;
+  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.and.pred b, 3, 128, a;\n selp.u32 %0, 1, 0, b;\n}\n"
+               : "=r"(all) : "r"((uint32_t)v) : "memory");
+  return all != 0;
 }
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -219,13 +242,13 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 
 // ------------------------------------------------------------------ router
 // Logits of all tokens: a team of four warps takes four experts (so that x comes from
-// L2 once for them; one where that leaves teams without work) and 8 tokens, each warp a quarter of D in chunks
+// L2 once for them; one where that leaves teams without work) and 4 tokens, each warp a quarter of D in chunks
 // of 256 (8 elements a lane).  Beside a logit what fp32 may be off by: a product
 // passes through at most `depth` additions, each of half an ulp (2^-24) of a sum that
 // is at most the sum of magnitudes, which is at most |x| |w|; and the bias through one.
 // (1 + 2^-8 covers the norms' own roundings.)
-constexpr int RT_E = 4, RT_T = 8;
-__device__ __forceinline__ float dec_depth(int D) { return (float)((D / 256 + 3) / 4 * 8 + 8 + 4); }
+constexpr int RT_E = 4, RT_T = 4, RT_N = RT_E * RT_T + RT_E + RT_T;
+__device__ __forceinline__ float dec_depth(int D) { return (float)((D / 256 + 3) / 4 * 8 + 16 + 4); }
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -233,11 +256,13 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
   for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
 
-__device__ void router_logits(const DecodeParams& p, float* red /* [2][4][RT_E RT_T + RT_E + RT_T] */) {
-  constexpr int NV = RT_E * RT_T + RT_E + RT_T;
+__device__ __noinline__ void router_logits(const DecodeParams& p, float* part /* [8 warps][RT_N][33] */, float* red /* [8][RT_N] */) {
+  constexpr int NV = RT_N, AHEAD = 3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp >> 2, quarter = warp & 3;
   const int groups = (p.T + RT_T - 1) / RT_T, chunks = p.D / 256;
   const int per = p.E * groups <= 4 * (int)gridDim.x ? 1 : RT_E, items = (p.E + per - 1) / per * groups;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
   for (int first = blockIdx.x; first < items; first += 2 * gridDim.x) {
     const int item = first + (1 - team) * (int)gridDim.x;  // (a thread of team 0 starts the loads first)
     const bool on = item < items;
@@ -246,42 +271,62 @@ __device__ void router_logits(const DecodeParams& p, float* red /* [2][4][RT_E R
     float v[NV];  // logits, then |w|^2, then |x|^2
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = 0.0f;
-    if (on) {
-      const uint4* w = reinterpret_cast<const uint4*>(p.w_router + (size_t)e0 * p.D) + lane;
-      const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)t0 * p.D) + lane;
-#pragma unroll 4
-      for (int c = quarter; c < chunks; c += 4) {
-        float wf[RT_E][8];
+    const uint4* w = reinterpret_cast<const uint4*>(p.w_router + (size_t)e0 * p.D) + lane;
+    const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)t0 * p.D) + lane;
+    const int d8 = p.D / 8;
+    uint4 wq[AHEAD][RT_E], xq[RT_T];  // weights three chunks ahead, tokens one
+    auto get = [&](int c, uint4 (&q)[RT_E]) {
 #pragma unroll
-        for (int e = 0; e < RT_E; ++e) {
-          unpack8(e < ne ? __ldg(w + (size_t)e * (p.D / 8) + c * 32) : make_uint4(0u, 0u, 0u, 0u), wf[e]);
+      for (int e = 0; e < RT_E; ++e) q[e] = on && c < chunks && e < ne ? __ldg(w + (size_t)e * d8 + c * 32) : none;
+    };
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[RT_E * RT_T + e] = fmaf(wf[e][j], wf[e][j], v[RT_E * RT_T + e]);
-        }
+    for (int a = 0; a < AHEAD; ++a) get(quarter + 4 * a, wq[a]);
 #pragma unroll
-        for (int t = 0; t < RT_T; ++t) {
-          if (t >= nt) break;
-          float xf[8];
-          unpack8(__ldg(x + (size_t)t * (p.D / 8) + c * 32), xf);
+    for (int t = 0; t < RT_T; ++t) xq[t] = on && quarter < chunks && t < nt ? __ldg(x + (size_t)t * d8 + quarter * 32) : none;
+#pragma unroll 1
+    for (int c = quarter; on && c < chunks; c += 4) {
+      float wf[RT_E][8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[RT_E * RT_T + RT_E + t] = fmaf(xf[j], xf[j], v[RT_E * RT_T + RT_E + t]);
+      for (int e = 0; e < RT_E; ++e) {
+        unpack8(wq[0][e], wf[e]);
 #pragma unroll
-            for (int e = 0; e < RT_E; ++e) v[t * RT_E + e] = fmaf(xf[j], wf[e][j], v[t * RT_E + e]);
-          }
+        for (int a = 0; a + 1 < AHEAD; ++a) wq[a][e] = wq[a + 1][e];
+      }
+      get(c + 4 * AHEAD, wq[AHEAD - 1]);
+#pragma unroll
+      for (int e = 0; e < RT_E; ++e)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[RT_E * RT_T + e] = fmaf(wf[e][j], wf[e][j], v[RT_E * RT_T + e]);
+#pragma unroll
+      for (int t = 0; t < RT_T; ++t) {
+        if (t >= nt) break;
+        float xf[8];
+        unpack8(xq[t], xf);
+        if (c + 4 < chunks) xq[t] = __ldg(x + (size_t)t * d8 + (c + 4) * 32);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[RT_E * RT_T + RT_E + t] = fmaf(xf[j], xf[j], v[RT_E * RT_T + RT_E + t]);
+#pragma unroll
+          for (int e = 0; e < RT_E; ++e) v[t * RT_E + e] = fmaf(xf[j], wf[e][j], v[t * RT_E + e]);
         }
       }
     }
-    float* mine = red + (team * 4 + quarter) * NV;
+    // the lanes' sums through shared memory: lane l adds those of value l
+    float* mine = part + warp * (NV * 33);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (i < RT_E * RT_T && i / RT_E >= nt) continue;  // (of tokens past the end)
+    for (int i = 0; i < NV; ++i) mine[i * 33 + lane] = v[i];
+    __syncwarp();
+    if (lane < NV) {
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int l = 0; l < 32; l += 4)
 #pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
-      if (lane == 0) mine[i] = v[i];
+        for (int i = 0; i < 4; ++i) sum[i] += mine[lane * 33 + l + i];
+      red[warp * NV + lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
+    __syncwarp();
     named_bar_sync(1 + team, 128);
-    if (quarter == 0 && on && lane / RT_E < nt && lane % RT_E < ne) {  // lane: a token and an expert
+    if (quarter == 0 && on && lane < RT_E * RT_T && lane / RT_E < nt && lane % RT_E < ne) {  // lane: a token and an expert
       const int t = lane / RT_E, e = lane % RT_E;
       const float* r = red + team * 4 * NV;
       float2 s = make_float2(0.0f, 0.0f);
@@ -368,48 +413,34 @@ static_assert(sizeof(TopkScratch) <= sizeof(DecodeSched::mask), "scratch of the 
 // Experts and weights of token t, by the epilogue's 128 threads (thread i has
 // experts i + 128 j): an expert's rank is the number of keys before its own, counted
 // in a short loop over all of them (selecting the largest k times over took 15 us of a
-// call at 256 experts; this takes 2).
-__device__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s, int* idx, float* wt) {
+// call at 256 experts).  Loops stay rolled: every line of code is a miss.
+__device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s, int* idx, float* wt) {
   const int lane = tid & 31, ew = tid >> 5, k = p.k;
-  constexpr int NI = E_MAX / 128;
-  float v[NI], err[NI];
-  uint32_t key[NI];
-  float most = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int e = tid + 128 * i;
-    v[i] = err[i] = 0.0f, key[i] = 0u;
-    if (e < p.E) {
-      const float2 q = __ldcg(p.logits + (size_t)t * p.E + e);
-      v[i] = q.x, err[i] = q.y, key[i] = dec_key(q.x);
-      most = fmaxf(most, q.y);
-    }
-    s.key[e] = key[i];
-  }
-  named_bar_sync(3, 128);
-  int rank[NI] = {0, 0, 0, 0};
+  const float2* from = p.logits + (size_t)t * p.E;
 #pragma unroll 1
-  for (int j = 0; j < p.E; j += 4) {  // (keys past the last expert are 0 and behind it in every tie)
-    const uint4 q = *reinterpret_cast<const uint4*>(s.key + j);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (128 * i >= p.E) break;
-      const int e = tid + 128 * i - j;  // ties: the lower id is before
-      rank[i] += (q.x > key[i] || (q.x == key[i] && 0 < e)) + (q.y > key[i] || (q.y == key[i] && 1 < e)) +
-                 (q.z > key[i] || (q.z == key[i] && 2 < e)) + (q.w > key[i] || (q.w == key[i] && 3 < e));
-    }
-  }
+  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) s.key[e] = e < p.E ? dec_key(__ldcg(&from[e].x)) : 0u;
+  named_bar_sync(3, 128);
   // lowest that a selected logit may be, highest that another may be
-  float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const bool there = tid + 128 * i < p.E, in = there && rank[i] < k;
-    if (in) lo = fminf(lo, v[i] - err[i]);
-    else if (there) hi = fmaxf(hi, v[i] + err[i]);
+  float lo = INFINITY, hi = -INFINITY, most = 0.0f;
+#pragma unroll 1
+  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) {
+    const uint32_t key = s.key[e];
+    const float2 q = e < p.E ? __ldcg(from + e) : make_float2(0.0f, 0.0f);
+    int rank = 0;
+#pragma unroll 2
+    for (int j = 0; j < p.E; j += 4) {  // (keys past the last expert are 0 and behind it in every tie)
+      const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
+      const int d = e - j;  // ties: the lower id is before
+      rank += (o.x >= key + (d <= 0)) + (o.y >= key + (d <= 1)) + (o.z >= key + (d <= 2)) + (o.w >= key + (d <= 3));
+    }
+    const bool in = e < p.E && rank < k;
+    if (in) lo = fminf(lo, q.x - q.y);
+    else if (e < p.E) hi = fmaxf(hi, q.x + q.y);
+    most = fmaxf(most, q.y);
     const uint32_t w = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) s.words[4 * i + ew] = w;
+    if (lane == 0) s.words[e >> 5] = w;
   }
-#pragma unroll
+#pragma unroll 1
   for (int d = 16; d >= 1; d >>= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
@@ -417,22 +448,22 @@ __device__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s
   }
   if (lane == 0) s.range[0][ew] = lo, s.range[1][ew] = hi, s.range[2][ew] = most;
   named_bar_sync(3, 128);
-  lo = fminf(fminf(s.range[0][0], s.range[0][1]), fminf(s.range[0][2], s.range[0][3]));
-  hi = fmaxf(fmaxf(s.range[1][0], s.range[1][1]), fmaxf(s.range[1][2], s.range[1][3]));
-  most = fmaxf(fmaxf(s.range[2][0], s.range[2][1]), fmaxf(s.range[2][2], s.range[2][3]));
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) lo = fminf(lo, s.range[0][w]), hi = fmaxf(hi, s.range[1][w]), most = fmaxf(most, s.range[2][w]);
   if (most > 0.0f && lo <= hi) {  // (exact logits that are equal are ties, decided above)
     if (ew == 0) decide_fp64(p, t, lo, hi, s.words);
     named_bar_sync(3, 128);
   }
   // slots in ascending order: the selected experts below
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    if (!(s.words[4 * i + ew] >> lane & 1)) continue;
-    int slot = __popc(s.words[4 * i + ew] & ((1u << lane) - 1u));
-    for (int w = 0; w < 4 * i + ew; ++w) slot += __popc(s.words[w]);
-    s.logit[slot] = v[i];
-    idx[slot] = tid + 128 * i;
-    if (p.out_idx && (int)blockIdx.x == t % (int)gridDim.x) p.out_idx[(size_t)t * k + slot] = tid + 128 * i;
+#pragma unroll 1
+  for (int e = tid; e < p.E; e += 128) {
+    if (!(s.words[e >> 5] >> lane & 1)) continue;
+    int slot = __popc(s.words[e >> 5] & ((1u << lane) - 1u));
+#pragma unroll 1
+    for (int w = 0; w < e >> 5; ++w) slot += __popc(s.words[w]);
+    s.logit[slot] = __ldcg(&from[e].x);
+    idx[slot] = e;
+    if (p.out_idx && (int)blockIdx.x == t % (int)gridDim.x) p.out_idx[(size_t)t * k + slot] = e;
   }
   named_bar_sync(3, 128);
   // weights over their sum.  Softmax: exp(l - m); sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)), both factors scaled so
@@ -442,12 +473,12 @@ __device__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s
     const bool soft = p.score_fn == MOE_SCORE_SOFTMAX;
     const float a = soft ? l : fminf(l, 0.0f);
     float m = a;
-#pragma unroll
+#pragma unroll 1
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     float w = lane < k ? expf(a - m) : 0.0f;
     if (!soft && lane < k) w /= 1.0f + expf(-fabsf(l));
     float sum = w;
-#pragma unroll
+#pragma unroll 1
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane < k) {
       wt[lane] = w / sum;
@@ -460,12 +491,14 @@ __device__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s
 __device__ __forceinline__ int token_of(const DecodeParams& p, int r) { return (int)((unsigned)r * (unsigned)p.inv_k >> 16); }
 
 // The routing into shared memory, by the 128 threads of the epilogue warps
-__device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
+__device__ __noinline__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
   const int R = p.T * p.k;
+#pragma unroll 1
   for (int e = tid; e < p.E; e += 128) s.mask[e] = 0ull;
   if (p.given || p.T > DEC_OWN_TOPK) {
     const int* idx = p.given ? p.in_idx : p.topk_idx;
     const float* wt = p.given ? p.in_w : p.topk_w;
+#pragma unroll 1
     for (int r = tid; r < R; r += 128) {
       const int e = __ldcg(idx + r);
       s.w[r] = __ldcg(wt + r);
@@ -476,25 +509,29 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
   }
   named_bar_sync(3, 128);
   if (p.given) {  // a second slot of a token with the same expert is an empty one
+#pragma unroll 1
     for (int r = tid; r < R; r += 128) {
       const int t = token_of(p, r);
       const uint16_t e = s.idx[r];
       bool twice = false;
+#pragma unroll 1
       for (int q = t * p.k; q < r; ++q) twice |= e != 0xffffu && s.idx[q] == e;
       if (twice && blockIdx.x == 0) atomicOr(p.status + 1, FLAG_ROUTES_INVALID);
       if (!twice && e != 0xffffu) atomicOr(&s.mask[e], 1ull << t);
       s.row[r] = twice;  // (marked; the slots before it still have to be seen)
     }
     named_bar_sync(3, 128);
+#pragma unroll 1
     for (int r = tid; r < R; r += 128)
       if (s.row[r]) s.idx[r] = 0xffffu;
   } else {
+#pragma unroll 1
     for (int r = tid; r < R; r += 128) atomicOr(&s.mask[s.idx[r]], 1ull << token_of(p, r));
   }
   named_bar_sync(3, 128);
   // rows and active experts before every expert: thread i takes experts 4 i .. 4 i + 3
   int rows = 0, act = 0;
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < 4; ++j) {
     const int e = 4 * tid + j;
     const int n = e < p.E ? __popcll(s.mask[e]) : 0;
@@ -512,7 +549,7 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
   int before = sum - (rows | act << 16);
   for (int i = 0; i < w; ++i) before += s.scan[i];
   rows = before & 0xffff, act = before >> 16;
-#pragma unroll
+#pragma unroll 1
   for (int j = 0; j < 4; ++j) {
     const int e = 4 * tid + j;
     if (e < p.E) {
@@ -539,6 +576,7 @@ __device__ void build_schedule(const DecodeParams& p, DecodeSched& s, int tid) {
     s.n_d = p.D / 128 * (s.m_ds + act * s.m_d);
   }
   named_bar_sync(3, 128);
+#pragma unroll 1
   for (int r = tid; r < R; r += 128) {
     const uint16_t e = s.idx[r];
     if (e != 0xffffu) s.row[s.off[e] + __popcll(s.mask[e] & ((1ull << token_of(p, r)) - 1ull))] = (uint16_t)r;
@@ -554,7 +592,7 @@ __device__ __forceinline__ void fma4(float4& a, float g, const float4& b) {
 
 // h of all rows, this CTA's share: an item is a row (token) and 128 columns, a warp
 // takes an item, a lane 4 columns: the sums of its pieces in order, SwiGLU.
-__device__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) {
+__device__ __noinline__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) {
   const int lane = threadIdx.x & 31, tiles_s = p.I_s / 128, tiles_u = p.I / 128;
   const int of_s = p.T * tiles_s, items = of_s + sc.n_rows * tiles_u;
   for (int it = blockIdx.x + ew * gridDim.x; it < items; it += 4 * gridDim.x) {
@@ -565,10 +603,17 @@ __device__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) 
     const float* su = (shared ? p.sums_s : p.sums_u) + ((size_t)tile * 2 * m * rows + r) * 128 + 4 * lane;
     const float* sg = su + (size_t)m * rows * 128;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), g = a;
-#pragma unroll 8
-    for (int c = 0; c < m; ++c) {
-      add4(a, ldcg4(su + c * rows * 128));
-      add4(g, ldcg4(sg + c * rows * 128));
+#pragma unroll 1
+    for (int c0 = 0; c0 < m; c0 += 4) {  // four pieces of both on their way at once
+      float4 q[2][4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool in = c0 + c < m;
+        q[0][c] = in ? ldcg4(su + (c0 + c) * rows * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+        q[1][c] = in ? ldcg4(sg + (c0 + c) * rows * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) add4(a, q[0][c]), add4(g, q[1][c]);  // (a sum of zeros stays what it is)
     }
     const float h[4] = {silu_f32(g.x) * a.x, silu_f32(g.y) * a.y, silu_f32(g.z) * a.z, silu_f32(g.w) * a.w};
     if (shared || !p.mx) {
@@ -599,47 +644,52 @@ __device__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) 
 
 // The output, this CTA's share: a token's outputs of the shared expert and of its
 // slots, in that order, weighted.  An item is a token and 128 columns.
-__device__ void finish_down(const DecodeParams& p, const DecodeSched& sc, int ew) {
+__device__ __noinline__ void finish_down(const DecodeParams& p, const DecodeSched& sc, int ew) {
   const int lane = threadIdx.x & 31, tiles = p.D / 128;
   const size_t R = (size_t)p.T * p.k;
   for (int it = blockIdx.x + ew * gridDim.x; it < p.T * tiles; it += 4 * gridDim.x) {
     const int t = it / tiles, tile = it % tiles;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = 0; c < sc.m_ds; ++c) add4(s, ldcg4(p.sums_ds + ((size_t)(tile * sc.m_ds + c) * p.T + t) * 128 + 4 * lane));
-    // four slots and four pieces on their way at once
-    for (int j0 = 0; j0 < p.k; j0 += 4) {
-      const float* from[4];
-      float g[4];
+    // the terms in order: the shared expert's pieces, then every slot's; four on their way at once
+    const int terms = sc.m_ds + p.k * sc.m_d;
+    float4 y = s;
+    int j = -1, c = sc.m_d - 1;  // slot and piece of the term last looked at
+    const float* from = p.sums_ds + ((size_t)tile * sc.m_ds * p.T + t) * 128 + 4 * lane;
+    float g = 0.0f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < terms; i0 += 4) {
+      float4 q[4];
+      float w[4];          // weight with which y is added
+      uint32_t ends = 0u;  // behind these terms
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = t * p.k + j0 + j, e = j0 + j < p.k ? sc.idx[r] : 0xffff;
-        from[j] = nullptr, g[j] = 0.0f;
-        if (e != 0xffff) {
-          const int row = sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull));
-          from[j] = p.sums_d + ((size_t)tile * sc.m_d * R + row) * 128 + 4 * lane;
-          g[j] = sc.w[r];
+      for (int i = 0; i < 4; ++i) {
+        const int term = i0 + i;
+        q[i] = make_float4(0.f, 0.f, 0.f, 0.f), w[i] = 0.0f;
+        if (term < sc.m_ds) {
+          q[i] = ldcg4(from + (size_t)term * p.T * 128);
+          w[i] = 1.0f, ends |= 1u << i;
+        } else if (term < terms) {
+          if (++c == sc.m_d) {
+            c = 0, ++j;
+            const int r = t * p.k + j, e = sc.idx[r];
+            g = 0.0f, from = nullptr;
+            if (e != 0xffff) {
+              g = sc.w[r];
+              from = p.sums_d + ((size_t)tile * sc.m_d * R + sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull))) * 128 + 4 * lane;
+            }
+          }
+          if (from) q[i] = ldcg4(from + (size_t)c * R * 128);
+          if (from && c == sc.m_d - 1) w[i] = g, ends |= 1u << i;
         }
       }
-      float4 y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c0 = 0; c0 < sc.m_d; c0 += 4) {
-        float4 q[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            q[j][c] = from[j] && c0 + c < sc.m_d ? ldcg4(from[j] + (size_t)(c0 + c) * R * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c0 + c < sc.m_d) add4(y[j], q[j][c]);
+      for (int i = 0; i < 4; ++i) {
+        add4(y, q[i]);
+        if (ends >> i & 1) {
+          fma4(s, w[i], y);
+          y = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (from[j]) fma4(s, g[j], y[j]);
     }
     *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + tile * 128 + 4 * lane) =
         make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
@@ -647,72 +697,75 @@ __device__ void finish_down(const DecodeParams& p, const DecodeSched& sc, int ew
 }
 
 // ------------------------------------------------------------------ the kernel
+static_assert(3 * (DEC_A_BYTES + DEC_MAX_T * 128) >= 8 * RT_N * 33 * 4, "the router's sums fit into the stages without early loads");
 template <bool MX>
 __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid_constant__ DecodeMaps maps,
-                                                                   const __grid_constant__ DecodeParams p) {
+                                                                   const __grid_constant__ DecodeParams params) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int NST = p.n_stages;
-  uint8_t* after = smem + NST * p.stage_bytes;
-  uint8_t* sf = after;  // MXFP8: per stage the scale blocks of the weights and of the tokens
-  if (MX) after += NST * 2 * SF_BLOCK_BYTES;
-  DecodeSched& sched = *reinterpret_cast<DecodeSched*>(after);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(after + sizeof(DecodeSched));
-  uint64_t *full = bars, *empty = bars + DEC_MAX_STAGES, *acc_full = bars + 2 * DEC_MAX_STAGES,
-           *acc_empty = acc_full + 2, *ready = acc_empty + 2, *q_full = ready + 1, *q_empty = q_full + DEC_QUEUE;
-  int* queue = reinterpret_cast<int*>(q_empty + DEC_QUEUE);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + DEC_QUEUE);
+  const int NST = params.n_stages, stage_bytes = params.stage_bytes;
+  uint8_t* sf = smem + NST * stage_bytes;  // MXFP8: per stage the scale blocks of the weights and of the tokens
+  DecodeShared& sh = *reinterpret_cast<DecodeShared*>(sf + (MX ? NST * 2 * SF_BLOCK_BYTES : 0));
+  DecodeSched& sched = sh.sched;
+  const DecodeParams& p = sh.p;
+  const CUtensorMap* const map = &maps.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int FULL_ARRIVALS = MX ? 3 : 2;  // weights, tokens (and the tokens' scales)
 
+  // ---- before the grid's barrier
+  if (threadIdx.x < sizeof(DecodeParams) / 4)
+    reinterpret_cast<uint32_t*>(&sh.p)[threadIdx.x] = reinterpret_cast<const uint32_t*>(&params)[threadIdx.x];
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + (int)(sizeof(DecodeMaps) / sizeof(CUtensorMap))) prefetch_tensormap(map + (threadIdx.x - 128));
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], FULL_ARRIVALS);
-      mbar_init(&empty[i], 1);
+      mbar_init(&sh.full[i], FULL_ARRIVALS);
+      mbar_init(&sh.empty[i], 1);
+    }
+#pragma unroll 1
+    for (int i = 0; i < DEC_QUEUE; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 128 + (MX ? 3 : 2));  // epilogue, tokens, (scales,) products
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&sh.acc_full[i], 1);
+      mbar_init(&sh.acc_empty[i], 128);
     }
-    mbar_init(ready, 128);
-    for (int i = 0; i < DEC_QUEUE; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], MX ? 4 : 3);  // tokens, (scales,) products, epilogue
-    }
+    mbar_init(&sh.ready, 128);
     fence_barrier_init();
   }
+  __syncthreads();
   // Loads of one step: 128 rows of weights; the rows of x or h of the unit's tokens.  Weights are read once: they are
   // the first to leave L2, and do not push out what is used again (tokens, sums, the kernel's own code)
   const uint64_t once = l2_policy_evict_first();
-  auto load_weights = [&](const Unit& u, int k, int stage, const CUtensorMap* m, int row, const uint8_t* scales) {
-    const bool mx = MX && scales;
-    mbar_arrive_expect_tx(&full[stage], DEC_A_BYTES + (mx ? SF_BLOCK_BYTES : 0));
-    tma_load_2d_hint(smem + stage * p.stage_bytes, m, &full[stage], k * (mx ? BK_MX : BK), row, once);
-    if (mx) bulk_load(sf + stage * 2 * SF_BLOCK_BYTES, scales + (size_t)k * SF_BLOCK_BYTES, SF_BLOCK_BYTES, &full[stage]);
+  auto load_weights = [&](const Unit& u, int k, int stage) {
+    const bool mx = MX && u.routed;
+    mbar_arrive_expect_tx(&sh.full[stage], DEC_A_BYTES + (mx ? SF_BLOCK_BYTES : 0));
+    tma_load_2d_hint(smem + stage * stage_bytes, map + u.m, &sh.full[stage], k * (mx ? BK_MX : BK), u.row, once);
+    if (mx) bulk_load(sf + stage * 2 * SF_BLOCK_BYTES, u.scales + (size_t)k * SF_BLOCK_BYTES, SF_BLOCK_BYTES, &sh.full[stage]);
   };
   auto load_x = [&](int k, int stage) {
-    mbar_arrive_expect_tx(&full[stage], (uint32_t)p.ncap * 128);
-    tma_load_2d(smem + stage * p.stage_bytes + DEC_A_BYTES, &maps.x, &full[stage], k * BK, 0);
+    mbar_arrive_expect_tx(&sh.full[stage], (uint32_t)p.ncap * 128);
+    tma_load_2d(smem + stage * stage_bytes + DEC_A_BYTES, map + M_X, &sh.full[stage], k * BK, 0);
   };
-
-  // ---- before the grid's barrier: the first loads of the shared expert's weights (they wait for nothing; the other
-  // warps are at the router's weights meanwhile);
-  // counters and status to zero, logits, x as codes
-  if (threadIdx.x >= 128 && threadIdx.x < 128 + (int)(sizeof(DecodeMaps) / sizeof(CUtensorMap)))
-    prefetch_tensormap(reinterpret_cast<const CUtensorMap*>(&maps) + (threadIdx.x - 128));
-  const int n_shared = shared_units(p), early_most = min(NST, DEC_EARLY);
+  // The first loads of the shared expert's weights, which wait for nothing, by one thread while the others are at the
+  // router's weights; counters and status to zero, logits, x as codes
+  const int n_shared = shared_units(p);
   if (threadIdx.x == 0) {
     int stage = 0;
-    for (int i = blockIdx.x; i < n_shared && stage < early_most; i += gridDim.x) {
-      const Unit u = shared_unit(p, i);
-      for (int k = u.k0; k < u.k1 && stage < early_most; ++k, ++stage) {
-        load_weights(u, k, stage, u.part ? &maps.ws_gate : &maps.ws_up, u.tile * 128, nullptr);
+#pragma unroll 1
+    for (int i = blockIdx.x; i < n_shared && stage < DEC_EARLY; i += gridDim.x) {
+      Unit u;
+      shared_unit(p, i, u);
+#pragma unroll 1
+      for (int k = u.k0; k < u.k1 && stage < DEC_EARLY; ++k, ++stage) {
+        load_weights(u, k, stage);
         load_x(k, stage);
       }
     }
   }
   if (blockIdx.x == 0 && threadIdx.x < 2) p.status[threadIdx.x] = 0;
-  for (int i = blockIdx.x * DEC_THREADS + threadIdx.x; i < DEC_COUNTERS; i += gridDim.x * DEC_THREADS) p.counters[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < DEC_COUNTERS) p.counters[threadIdx.x] = 0;
   if (MX) {
     const int blocks = p.T * (p.D / 32);
     for (int b = blockIdx.x * DEC_THREADS + threadIdx.x; b < blocks; b += gridDim.x * DEC_THREADS) {
@@ -727,184 +780,139 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     fence_proxy_async_global();  // read by TMA
   }
   if (warp == 1) {
-    tmem_alloc<256>(tmem_slot);
+    tmem_alloc<256>(&sh.tmem);
     tmem_relinquish();
   }
   __syncwarp();
-  if (!p.given) router_logits(p, reinterpret_cast<float*>(&sched));
+  if (!p.given) {  // (its sums in stages that have no loads yet)
+    router_logits(p, reinterpret_cast<float*>(smem + DEC_EARLY * stage_bytes), reinterpret_cast<float*>(&sched));
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   cooperative_groups::this_grid().sync();  // (of this CTA's threads too)
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = sh.tmem;
   if (MX) fence_proxy_async_global();
 
-  // the epilogue's 128 threads go on together or not at all
-  auto agree = [](bool v) {
-    uint32_t all;
-    asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.and.pred b, 3, 128, a;\n selp.u32 %0, 1, 0, b;\n}\n"
-                 : "=r"(all) : "r"((uint32_t)v) : "memory");
-    return all != 0;
-  };
-  auto wait_bar = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, p.status, p.timeout_ns); };
-  // the next claimed unit (one thread of a role; others are told by it); -1 at the end, -2 when waiting was given up
-  auto pop = [&](int i) {
-    if (!wait_bar(&q_full[i % DEC_QUEUE], (uint32_t)(i / DEC_QUEUE) & 1u)) return -2;
-    const int v = queue[i % DEC_QUEUE];
-    mbar_arrive(&q_empty[i % DEC_QUEUE]);
-    return v;
-  };
-  // position in the ring of stages
-  int stage = 0;
+  // position in the ring of stages, and in the queue of units
+  int stage = 0, at = 0;
   uint32_t parity = 0;
   auto advance = [&]() {
     if (++stage == NST) stage = 0, parity ^= 1u;
   };
+  auto q_slot = [&]() { return at % DEC_QUEUE; };
+  auto q_parity = [&]() { return (uint32_t)(at / DEC_QUEUE) & 1u; };
 
   if (warp == 0) {
-    // ---------------- weights, and claims
+    // ---------------- units and their weights: the shared expert's up/gate units by number, then claimed ones
     if (elect_one()) {
       bool ok = true;
-      int early = 0;  // steps issued before the barrier
-      for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) {
-        const Unit u = shared_unit(p, i);
-        for (int k = u.k0; k < u.k1; ++k, advance()) {
-          if (early < early_most) { ++early; continue; }
-          if (!(ok = wait_bar(&empty[stage], parity ^ 1u))) break;
-          load_weights(u, k, stage, u.part ? &maps.ws_gate : &maps.ws_up, u.tile * 128, nullptr);
+      int mine = blockIdx.x, next = 0, early = 0, units = 0;
+      bool claiming = false;
+#pragma unroll 1
+      for (; ok; ++at) {
+        const bool shared = mine < n_shared;
+        if (!shared && !claiming) {
+          if (!dec_wait(&sh.ready, 0, p)) break;
+          claiming = true;
+          units = sched.n_u + sched.n_d;
+          next = atomicAdd(p.counters + CTR_CLAIMS, 1);
         }
-      }
-      ok = ok && wait_bar(ready, 0);
-      if (ok) {
-        const int units = sched.n_u + sched.n_d;
-        int next = atomicAdd(p.counters + CTR_CLAIMS, 1);
-        for (int i = 0;; ++i) {
-          const int id = next < units ? next : -1;
-          if (id >= 0) next = atomicAdd(p.counters + CTR_CLAIMS, 1);  // (its answer is not needed before this unit's loads are issued)
-          if (!wait_bar(&q_empty[i % DEC_QUEUE], ((uint32_t)(i / DEC_QUEUE) & 1u) ^ 1u)) break;
-          queue[i % DEC_QUEUE] = id;
-          mbar_arrive(&q_full[i % DEC_QUEUE]);
-          if (id < 0) break;
-          const Unit u = claimed_unit(p, sched, id);
-          const CUtensorMap* m;
-          const uint8_t* scales = nullptr;
-          int row;
-          if (u.phase == PH_UP) {
-            m = u.part ? &maps.w_gate : &maps.w_up;
-            row = u.e * p.I + u.tile * 128;
-            if (MX) scales = (u.part ? p.sf_gate : p.sf_up) + (size_t)(row / 128) * (p.D / BK_MX) * SF_BLOCK_BYTES;
-          } else if (u.act < 0) {
-            m = &maps.ws_down, row = u.tile * 128;
-          } else {
-            m = &maps.w_down, row = u.e * p.D + u.tile * 128;
-            if (MX) scales = p.sf_down + (size_t)(row / 128) * (p.I / BK_MX) * SF_BLOCK_BYTES;
-          }
-          for (int k = u.k0; k < u.k1; ++k, advance()) {
-            if (!(ok = wait_bar(&empty[stage], parity ^ 1u))) break;
-            load_weights(u, k, stage, m, row, scales);
-          }
-          if (!ok) break;
+        if (!dec_wait(&sh.q_empty[q_slot()], q_parity() ^ 1u, p)) break;
+        Unit& u = sh.queue[q_slot()];
+        if (shared) {
+          shared_unit(p, mine, u);
+          mine += gridDim.x;
+        } else if (next < units) {
+          const int id = next;
+          next = atomicAdd(p.counters + CTR_CLAIMS, 1);  // (the answer is not needed before this unit's loads are issued)
+          claimed_unit(p, sched, id, u);
+        } else {
+          u.phase = -1;
+        }
+        mbar_arrive(&sh.q_full[q_slot()]);
+        if (u.phase < 0) break;
+        const Unit v = u;
+#pragma unroll 1
+        for (int k = v.k0; k < v.k1; ++k, advance()) {
+          if (shared && early < DEC_EARLY) { ++early; continue; }
+          if (!(ok = dec_wait(&sh.empty[stage], parity ^ 1u, p))) break;
+          load_weights(v, k, stage);
         }
       }
     }
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- tokens
-    bool ok = true;
+    bool ok = true, have_h = false;
     int early = 0;
-    for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) {
-      const Unit u = shared_unit(p, i);
-      for (int k = u.k0; k < u.k1; ++k, advance()) {
-        if (early < early_most) { ++early; continue; }
-        int go = 1;
-        if (lane == 0) {
-          go = wait_bar(&empty[stage], parity ^ 1u);
-          if (go) load_x(k, stage);
-        }
-        if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
-      }
-    }
-    int go = ok ? 1 : 0;
-    if (lane == 0 && ok) go = wait_bar(ready, 0);
-    ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-    __syncwarp();
-    bool have_h = false;
-    for (int i = 0; ok; ++i) {
-      int id = 0;
-      if (lane == 0) id = pop(i);
-      id = __shfl_sync(0xffffffffu, id, 0);
-      if (id < 0) break;
-      const Unit u = claimed_unit(p, sched, id);
-      if (u.phase == PH_DOWN && !have_h) {
-        go = 1;
-        if (lane == 0) go = wait_counter_ge(p.counters + CTR_H, (int)gridDim.x, p.status, p.timeout_ns);
-        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-        __syncwarp();
-        if (!ok) break;
-        fence_proxy_async_global();
-        have_h = true;
-      }
+#pragma unroll 1
+    for (; ok; ++at) {
+      int go = 1;
+      if (lane == 0) go = dec_wait(&sh.q_full[q_slot()], q_parity(), p);
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      __syncwarp();
+      const Unit u = sh.queue[q_slot()];
       // lane l: the l-th load of every step
-      const bool routed = u.act >= 0, mx = MX && routed;
-      int t[4] = {0, 0, 0, 0}, loads;
-      uint32_t bytes;
+      int t[4] = {0, 0, 0, 0}, loads = 1;
+      uint32_t bytes = (uint32_t)p.ncap * 128;
       if (u.phase == PH_UP) {
         loads = (u.n + 3) / 4, bytes = (uint32_t)loads * 512;
 #pragma unroll
         for (int j = 0; j < 4; ++j) t[j] = token_of(p, sched.row[u.off + min(4 * lane + j, u.n - 1)]);
-      } else {
+      } else if (u.phase == PH_DOWN) {
         loads = (u.n + 15) / 16, bytes = (uint32_t)loads * 2048;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_empty[q_slot()]);
+      if (u.phase < 0) break;
+      if (u.phase == PH_DOWN && !have_h) {
+        if (lane == 0) go = dec_wait_count(CTR_H, (int)gridDim.x, p);
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        __syncwarp();
+        fence_proxy_async_global();
+        have_h = true;
+      }
+      const bool mx = MX && u.routed;
+#pragma unroll 1
       for (int k = u.k0; k < u.k1; ++k, advance()) {
-        go = 1;
+        if (u.phase == PH_SHARED && early < DEC_EARLY) { ++early; continue; }
         if (lane == 0) {
-          go = wait_bar(&empty[stage], parity ^ 1u);
-          if (go) mbar_arrive_expect_tx(&full[stage], bytes);
+          go = dec_wait(&sh.empty[stage], parity ^ 1u, p);
+          if (go) mbar_arrive_expect_tx(&sh.full[stage], bytes);
         }
         if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
-        uint8_t* b = smem + stage * p.stage_bytes + DEC_A_BYTES;
+        uint8_t* b = smem + stage * stage_bytes + DEC_A_BYTES;
         const int kc = k * (mx ? BK_MX : BK);
         if (lane < loads) {
-          if (u.phase == PH_UP) tma_gather4(b + lane * 512, &maps.x_rows, &full[stage], kc, t[0], t[1], t[2], t[3]);
-          else tma_load_2d(b + lane * 2048, routed ? &maps.h : &maps.h_s, &full[stage], kc, u.off + lane * 16);
+          if (u.phase == PH_UP) tma_gather4(b + lane * 512, map + M_X_ROWS, &sh.full[stage], kc, t[0], t[1], t[2], t[3]);
+          else tma_load_2d(b + lane * 2048, map + (u.phase == PH_SHARED ? M_X : u.routed ? M_H : M_H_S), &sh.full[stage], kc, u.off + lane * 16);
         }
         __syncwarp();
       }
     }
   } else if (warp == 3) {
-    // ---------------- MXFP8: the scale block of a step's tokens, lane l rows l and l + 32
+    // ---------------- MXFP8: the scale block of a step's tokens, lane l rows l and l + 32 (for other steps only the arrival)
     if (MX) {
-      bool ok = true;
-      int go = 1;
-      for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) {  // no scales: only the arrivals
-        const Unit u = shared_unit(p, i);
-        for (int k = u.k0; k < u.k1; ++k, advance()) {
-          if (lane == 0) {
-            go = wait_bar(&empty[stage], parity ^ 1u);
-            if (go) mbar_arrive(&full[stage]);
-          }
-          if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
-        }
-      }
-      if (lane == 0 && ok) go = wait_bar(ready, 0);
-      ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-      __syncwarp();
-      bool have_h = false;
-      for (int i = 0; ok; ++i) {
-        int id = 0;
-        if (lane == 0) id = pop(i);
-        id = __shfl_sync(0xffffffffu, id, 0);
-        if (id < 0) break;
-        const Unit u = claimed_unit(p, sched, id);
+      bool ok = true, have_h = false;
+#pragma unroll 1
+      for (; ok; ++at) {
+        int go = 1;
+        if (lane == 0) go = dec_wait(&sh.q_full[q_slot()], q_parity(), p);
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        __syncwarp();
+        const Unit u = sh.queue[q_slot()];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_empty[q_slot()]);
+        if (u.phase < 0) break;
         if (u.phase == PH_DOWN && !have_h) {
-          go = 1;
-          if (lane == 0) go = wait_counter_ge(p.counters + CTR_H, (int)gridDim.x, p.status, p.timeout_ns);
-          ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+          if (lane == 0) go = dec_wait_count(CTR_H, (int)gridDim.x, p);
+          if (!__shfl_sync(0xffffffffu, go, 0)) break;
           __syncwarp();
-          if (!ok) break;
           have_h = true;
         }
         const uint32_t* src[2] = {nullptr, nullptr};
-        if (u.act >= 0) {
+        if (u.routed) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int r = lane + 32 * j;
@@ -918,24 +926,21 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
         for (int d = 0; d < 4; ++d)
 #pragma unroll
           for (int j = 0; j < 2; ++j) ahead[d][j] = src[j] && u.k0 + d < u.k1 ? __ldcg(src[j] + u.k0 + d) : 0u;
-        for (int k = u.k0; ok && k < u.k1; k += 4) {
+#pragma unroll 1
+        for (int k = u.k0; k < u.k1; ++k, advance()) {
+          if (lane == 0) go = dec_wait(&sh.empty[stage], parity ^ 1u, p);
+          if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+          uint8_t* to = sf + stage * 2 * SF_BLOCK_BYTES + SF_BLOCK_BYTES + lane * 16;
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            if (k + d >= u.k1 || !ok) break;
-            go = 1;
-            if (lane == 0) go = wait_bar(&empty[stage], parity ^ 1u);
-            if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
-            uint8_t* to = sf + stage * 2 * SF_BLOCK_BYTES + SF_BLOCK_BYTES + lane * 16;
+          for (int j = 0; j < 2; ++j) {
+            if (u.routed) *reinterpret_cast<uint32_t*>(to + 4 * j) = ahead[0][j];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              *reinterpret_cast<uint32_t*>(to + 4 * j) = ahead[d][j];
-              ahead[d][j] = src[j] && k + d + 4 < u.k1 ? __ldcg(src[j] + k + d + 4) : 0u;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[stage]);
-            advance();
+            for (int d = 0; d < 3; ++d) ahead[d][j] = ahead[d + 1][j];
+            ahead[3][j] = src[j] && k + 4 < u.k1 ? __ldcg(src[j] + k + 4) : 0u;
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[stage]);
         }
       }
     }
@@ -944,17 +949,25 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     if (elect_one()) {
       int acc = 0;
       uint32_t acc_parity = 1;
-      auto multiply = [&](const Unit& u) {
-        const bool mx = MX && u.act >= 0;
-        const uint32_t n = (uint32_t)(u.n + 15) & ~15u;
+      bool ok = true;
+#pragma unroll 1
+      for (; ok; ++at) {
+        if (!dec_wait(&sh.q_full[q_slot()], q_parity(), p)) break;
+        const Unit& q = sh.queue[q_slot()];
+        const int phase = q.phase, k0 = q.k0, k1 = q.k1;
+        const bool mx = MX && q.routed;
+        const uint32_t n = (uint32_t)(q.n + 15) & ~15u;
+        mbar_arrive(&sh.q_empty[q_slot()]);
+        if (phase < 0) break;
         const uint32_t idesc = mx ? idesc_mxf8_e4m3(128, n) : idesc_bf16_f32(128, n);
-        if (!wait_bar(&acc_empty[acc], acc_parity)) return false;
+        if (!dec_wait(&sh.acc_empty[acc], acc_parity, p)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * DEC_MAX_T, sfa = tmem + 2 * DEC_MAX_T, sfb = sfa + 4;
-        for (int k = u.k0; k < u.k1; ++k, advance()) {
-          if (!wait_bar(&full[stage], parity)) return false;
+#pragma unroll 1
+        for (int k = k0; k < k1; ++k, advance()) {
+          if (!(ok = dec_wait(&sh.full[stage], parity, p))) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + stage * p.stage_bytes), b = a + DEC_A_BYTES;
+          const uint32_t a = smem_u32(smem + stage * stage_bytes), b = a + DEC_A_BYTES;
           if (mx) {
             const uint32_t f = smem_u32(sf + stage * 2 * SF_BLOCK_BYTES);
             tmem_cp_32x128b_warpx4(sfa, sdesc_sf_block(f));
@@ -962,26 +975,18 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_mxf8_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32),
-                          idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), sfa, sfb, k != u.k0 || kk ? 1u : 0u);
+                          idesc | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), sfa, sfb, k != k0 || kk ? 1u : 0u);
           } else {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32), idesc, k != u.k0 || kk ? 1u : 0u);
+              mma_bf16_ss(d, sdesc_kmajor_sw128(a + kk * 32), sdesc_kmajor_sw128(b + kk * 32), idesc, k != k0 || kk ? 1u : 0u);
           }
-          mma_commit(&empty[stage]);
+          mma_commit(&sh.empty[stage]);
         }
-        mma_commit(&acc_full[acc]);
+        if (!ok) break;
+        mma_commit(&sh.acc_full[acc]);
         acc ^= 1;
         if (!acc) acc_parity ^= 1u;
-        return true;
-      };
-      bool ok = true;
-      for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x) ok = multiply(shared_unit(p, i));
-      ok = ok && wait_bar(ready, 0);
-      for (int i = 0; ok; ++i) {
-        const int id = pop(i);
-        if (id < 0) break;
-        ok = multiply(claimed_unit(p, sched, id));
       }
     }
     __syncwarp();
@@ -991,80 +996,70 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
     bool ok = true;
     if (!p.given) {
       TopkScratch& scratch = *reinterpret_cast<TopkScratch*>(sched.mask);
-      if (p.T <= DEC_OWN_TOPK) {
-        for (int t = 0; t < p.T; ++t) {
-          token_topk(p, t, tid, scratch, scratch.idx, sched.w + t * p.k);
-          if (tid < p.k) sched.idx[t * p.k + tid] = (uint16_t)scratch.idx[tid];  // (written before the last barrier)
-          named_bar_sync(3, 128);
-        }
-      } else {
-        int mine = 0;
-        for (int t = blockIdx.x; t < p.T; t += gridDim.x, ++mine) {
-          token_topk(p, t, tid, scratch, p.topk_idx + (size_t)t * p.k, p.topk_w + (size_t)t * p.k);
-          named_bar_sync(3, 128);
-        }
-        if (tid == 0 && mine) red_release_add_gpu(p.counters + CTR_TOPK, mine);
+      const bool own = p.T <= DEC_OWN_TOPK;
+      int done = 0;
+#pragma unroll 1
+      for (int t = own ? 0 : blockIdx.x; t < p.T; t += own ? 1 : gridDim.x, ++done) {
+        token_topk(p, t, tid, scratch, own ? scratch.idx : p.topk_idx + (size_t)t * p.k, own ? sched.w + t * p.k : p.topk_w + (size_t)t * p.k);
+        if (own && tid < p.k) sched.idx[t * p.k + tid] = (uint16_t)scratch.idx[tid];  // (written before the last barrier)
+        named_bar_sync(3, 128);
+      }
+      if (!own) {
+        if (tid == 0 && done) red_release_add_gpu(p.counters + CTR_TOPK, done);
         // (one thread asks: the others' loads would be in the way of those that work)
-        ok = agree(tid != 0 || wait_counter_ge(p.counters + CTR_TOPK, p.T, p.status, p.timeout_ns));
+        ok = agree(tid != 0 || dec_wait_count(CTR_TOPK, p.T, p));
       }
     }
     if (ok) build_schedule(p, sched, tid);
     named_bar_sync(3, 128);
-    if (ok) mbar_arrive(ready);
+    if (ok) mbar_arrive(&sh.ready);
 
-    int acc = 0;
-    uint32_t acc_parity = 0;
-    // one unit's sums out of TMEM; the last of a tile finishes it
-    auto take = [&](const Unit& u) {
-      float* to = unit_sums(p, sched, u) + tid;
-      if (!agree(wait_bar(&acc_full[acc], acc_parity))) return false;
-      tc_fence_after();
-      const uint32_t taddr = tmem + acc * DEC_MAX_T + ((uint32_t)(32 * ew) << 16);
-      for (int n0 = 0; n0 < u.n; n0 += 16) {
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(taddr + n0, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (n0 + j < u.n) to[(n0 + j) * 128] = __uint_as_float(v[j]);
-      }
-      tc_fence_before();
-      mbar_arrive(&acc_empty[acc]);
-      acc ^= 1;
-      if (!acc) acc_parity ^= 1u;
-      return true;
-    };
     // all units of a phase are done: `mine` of them here.  (One thread asks.)
     auto all_done = [&](int ctr, int mine, int all) {
       named_bar_sync(3, 128);
       if (tid == 0) red_release_add_gpu(p.counters + ctr, mine);
-      return agree(tid != 0 || wait_counter_ge(p.counters + ctr, all, p.status, p.timeout_ns));
+      return agree(tid != 0 || dec_wait_count(ctr, all, p));
     };
-    int up_units = 0, down_units = 0;
+    int acc = 0, units[2] = {0, 0};  // up/gate and down units
+    uint32_t acc_parity = 0;
     bool have_h = false;
-    for (int i = blockIdx.x; ok && i < n_shared; i += gridDim.x, ++up_units) ok = take(shared_unit(p, i));
-    for (int i = 0; ok; ++i) {
-      // thread 0 takes the unit from the queue and tells the others
-      if (tid == 0) sched.scan[0] = pop(i);
-      named_bar_sync(3, 128);
-      const int id = sched.scan[0];
-      if (id == -2) ok = false;
-      if (ok && !have_h && (id < 0 || id >= sched.n_u)) {  // the last of this CTA's up/gate units is done
-        ok = all_done(CTR_UP, up_units, n_shared + sched.n_u);
-        if (!ok) break;
+#pragma unroll 1
+    for (; ok; ++at) {
+      if (!(ok = agree(dec_wait(&sh.q_full[q_slot()], q_parity(), p)))) break;
+      const Unit& q = sh.queue[q_slot()];
+      const int phase = q.phase, n = q.n;
+      float* to = q.sums + tid;
+      mbar_arrive(&sh.q_empty[q_slot()]);
+      if (!have_h && (phase < 0 || phase == PH_DOWN)) {  // the last of this CTA's up/gate units is done
+        if (!(ok = all_done(CTR_UP, units[0], n_shared + sched.n_u))) break;
         finish_up(p, sched, ew);
         fence_proxy_async_global();  // h is read by TMA
         named_bar_sync(3, 128);
         if (tid == 0) red_release_add_gpu(p.counters + CTR_H, 1);
         have_h = true;
       }
-      if (id < 0) break;
-      ok = take(claimed_unit(p, sched, id));
-      if (id < sched.n_u) ++up_units;
-      else ++down_units;
+      if (phase < 0) break;
+      ++units[phase == PH_DOWN];
+      if (!(ok = agree(dec_wait(&sh.acc_full[acc], acc_parity, p)))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + acc * DEC_MAX_T + ((uint32_t)(32 * ew) << 16);
+#pragma unroll 1
+      for (int n0 = 0; n0 < n; n0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + n0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (n0 + j >= n) break;
+          to[(n0 + j) * 128] = __uint_as_float(v[j]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sh.acc_empty[acc]);
+      acc ^= 1;
+      if (!acc) acc_parity ^= 1u;
     }
-    if (ok) ok = all_done(CTR_DOWN, down_units, sched.n_d);
-    if (ok) finish_down(p, sched, ew);  // (without any expert: zeros)
+    if (ok && all_done(CTR_DOWN, units[1], sched.n_d)) finish_down(p, sched, ew);  // (without any expert: zeros)
   }
   tc_fence_before();
   __syncthreads();
