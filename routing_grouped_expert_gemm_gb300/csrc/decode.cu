@@ -31,6 +31,7 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstring>
 
 #include "../../include/moe.h"
@@ -46,7 +47,7 @@ constexpr int DEC_THREADS = 256;
 constexpr int DEC_A_BYTES = 128 * 128;              // weights of a step
 enum : int { CTR_TOPK = 0, CTR_CLAIMS, CTR_UP /* units done */, CTR_H /* CTAs whose share of h is written */, CTR_DOWN, DEC_COUNTERS };
 constexpr int DEC_OWN_TOPK = 4;                     // up to so many tokens every CTA makes all tokens' selection itself
-constexpr int DEC_EARLY = 5;                        // steps loaded before the grid's barrier
+constexpr int DEC_EARLY = 2;                        // steps loaded before the grid's barrier
 constexpr int DEC_QUEUE = 4;                        // claimed units on their way to the roles of a CTA
 
 // Steps of a unit, for `total` steps on `ctas` CTAs: a CTA's share in 32 units,
@@ -248,7 +249,7 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 // is at most the sum of magnitudes, which is at most |x| |w|; and the bias through one.
 // (1 + 2^-8 covers the norms' own roundings.)
 constexpr int RT_E = 4, RT_T = 4, RT_N = RT_E * RT_T + RT_E + RT_T;
-__device__ __forceinline__ float dec_depth(int D) { return (float)((D / 256 + 3) / 4 * 8 + 16 + 4); }
+__device__ __forceinline__ float dec_depth(int D) { return (float)((D / 256 + 3) / 4 + 8 + 10 + 4); }
 
 __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -300,15 +301,17 @@ __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /*
 #pragma unroll
       for (int t = 0; t < RT_T; ++t) {
         if (t >= nt) break;
-        float xf[8];
+        float xf[8], of[RT_E];  // (a chunk's sum by itself: fewer additions behind one another)
         unpack8(xq[t], xf);
         if (c + 4 < chunks) xq[t] = __ldg(x + (size_t)t * d8 + (c + 4) * 32);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[RT_E * RT_T + RT_E + t] = fmaf(xf[j], xf[j], v[RT_E * RT_T + RT_E + t]);
 #pragma unroll
-          for (int e = 0; e < RT_E; ++e) v[t * RT_E + e] = fmaf(xf[j], wf[e][j], v[t * RT_E + e]);
+          for (int e = 0; e < RT_E; ++e) of[e] = j ? fmaf(xf[j], wf[e][j], of[e]) : xf[0] * wf[e][0];
         }
+#pragma unroll
+        for (int e = 0; e < RT_E; ++e) v[t * RT_E + e] += of[e];
       }
     }
     // the lanes' sums through shared memory: lane l adds those of value l
@@ -352,93 +355,124 @@ __device__ __forceinline__ uint32_t dec_key(float f) {  // order of floats as un
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// The selection of token t where fp32 left it open, by one warp: `words` are the
-// selected so far (bit e % 32 of word e / 32); those that may be in or out, given what
-// every logit may be off by, are ranked by their logits in fp64.
-__device__ __noinline__ void decide_fp64(const DecodeParams& p, int t, float lo, float hi, uint32_t* words) {
-  const int lane = threadIdx.x & 31;
-  double v[E_MAX / 32];
-  uint32_t und = 0u, sel = 0u;  // bit i: expert lane + 32 i
-  int want = 0;
-  for (int i = 0; i * 32 < p.E; ++i) {
-    const int e = lane + 32 * i;
-    if (e >= p.E) continue;
-    const float2 q = __ldcg(p.logits + (size_t)t * p.E + e);
-    const bool in = words[i] >> lane & 1;
-    const bool open = in ? q.x - q.y <= hi : q.x + q.y >= lo;
-    if (open) und |= 1u << i, want += in;
-    else if (in) sel |= 1u << i;
-  }
-  want = (int)__reduce_add_sync(0xffffffffu, (unsigned)want);
-  for (int i = 0; i * 32 < p.E; ++i) {
-    uint32_t who = __ballot_sync(0xffffffffu, und >> i & 1);
-    while (who) {
-      const int l = __ffs(who) - 1, e = l + 32 * i;
-      who &= who - 1;
-      double s = 0.0;
-      const bf16 *x = p.x + (size_t)t * p.D, *w = p.w_router + (size_t)e * p.D;
-      for (int d = lane; d < p.D; d += 32) s = fma((double)__bfloat162float(x[d]), (double)__bfloat162float(w[d]), s);
-      for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (p.b_router) s += (double)p.b_router[e];
-      if (lane == l) v[i] = s;
-    }
-  }
-  for (int n = 0; n < want; ++n) {
-    double best = 0.0;
-    int id = 1 << 20;
-    for (int i = 0; i * 32 < p.E; ++i)
-      if ((und >> i & 1) && (id == 1 << 20 || v[i] > best)) best = v[i], id = lane + 32 * i;
-    for (int m = 16; m >= 1; m >>= 1) {
-      const double b = __shfl_xor_sync(0xffffffffu, best, m);
-      const int j = __shfl_xor_sync(0xffffffffu, id, m);
-      if (j != 1 << 20 && (id == 1 << 20 || b > best || (b == best && j < id))) best = b, id = j;
-    }
-    if (id != 1 << 20 && (id & 31) == lane) und &= ~(1u << (id >> 5)), sel |= 1u << (id >> 5);
-  }
-  for (int i = 0; i * 32 < p.E; ++i) {
-    const uint32_t w = __ballot_sync(0xffffffffu, sel >> i & 1);
-    if (lane == 0) words[i] = w;
-  }
-}
-
 struct TopkScratch {
   uint32_t key[E_MAX];
-  uint32_t words[E_MAX / 32];
+  uint32_t words[E_MAX / 32], open[E_MAX / 32];  // a bit an expert
   float range[3][4];
   float logit[TOPK_MAX];
-  int idx[TOPK_MAX];
+  int idx[DEC_OWN_TOPK * TOPK_MAX];
+  float w[DEC_OWN_TOPK * TOPK_MAX];
 };
+static_assert(offsetof(DecodeSched, scan) - offsetof(DecodeSched, row) >= E_MAX * sizeof(float2), "the logits lie where rows and experts come to lie");
+static_assert(sizeof(DecodeSched::w) >= E_MAX * 8, "keys in fp64 lie where the weights come to lie");
+static_assert(DEC_OWN_TOPK * TOPK_MAX <= 128, "a thread a route");
 static_assert(sizeof(TopkScratch) <= sizeof(DecodeSched::mask), "scratch of the selection lies where the masks come to lie");
+
+// The selection of token t where fp32 left it open, by the epilogue's 128 threads:
+// the experts that may be in or out, given what every logit may be off by, are ranked
+// by their logits in fp64 (as integers of the same order, NaN lowest).
+__device__ __noinline__ void decide_fp64(const DecodeParams& p, int t, int tid, float lo, float hi, TopkScratch& s, const float2* val,
+                                         unsigned long long* dkey /* [E], shared memory */) {
+  const int lane = tid & 31, ew = tid >> 5, words = (p.E + 31) / 32;
+#pragma unroll 1
+  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) {
+    const bool in = s.words[e >> 5] >> lane & 1;
+    const float2 q = val[e];
+    const bool open = e < p.E && (in ? q.x - q.y <= hi : q.x + q.y >= lo);
+    const uint32_t o = __ballot_sync(0xffffffffu, open), w = __ballot_sync(0xffffffffu, in && !open);
+    if (lane == 0) s.open[e >> 5] = o, s.words[e >> 5] = w;
+  }
+  named_bar_sync(3, 128);
+  int n = 0, want = p.k;
+#pragma unroll 1
+  for (int w = 0; w < words; ++w) {
+    want -= __popc(s.words[w]);
+    uint32_t who = s.open[w];
+#pragma unroll 1
+    for (; who; who &= who - 1, ++n) {  // a warp every fourth
+      if ((n & 3) != ew) continue;
+      const int e = 32 * w + __ffs(who) - 1;
+      const bf16 *x = p.x + (size_t)t * p.D + 8 * lane, *v = p.w_router + (size_t)e * p.D + 8 * lane;
+      double sum = 0.0;
+#pragma unroll 2
+      for (int d = 0; d < p.D; d += 256) {
+        float a[8], b[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(x + d)), a);
+        unpack8(__ldg(reinterpret_cast<const uint4*>(v + d)), b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fma((double)a[j], (double)b[j], sum);
+      }
+#pragma unroll 1
+      for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      if (p.b_router) sum += (double)p.b_router[e];
+      const long long bits = __double_as_longlong(sum + 0.0);
+      if (lane == 0) dkey[e] = sum != sum ? 0ull : (unsigned long long)(bits ^ (bits >> 63 | (long long)0x8000000000000000ull));
+    }
+  }
+  named_bar_sync(3, 128);
+#pragma unroll 1
+  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) {
+    bool in = s.words[e >> 5] >> lane & 1;
+    if (s.open[e >> 5] >> lane & 1) {
+      const unsigned long long key = dkey[e];
+      int rank = 0;
+#pragma unroll 1
+      for (int w = 0; w < words; ++w)
+#pragma unroll 1
+        for (uint32_t who = s.open[w]; who; who &= who - 1) {
+          const int f = 32 * w + __ffs(who) - 1;
+          rank += dkey[f] > key || (dkey[f] == key && f < e);
+        }
+      in = rank < want;
+    }
+    const uint32_t w = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) s.words[e >> 5] = w;  // (this warp alone reads this word here)
+  }
+  named_bar_sync(3, 128);
+}
 
 // Experts and weights of token t, by the epilogue's 128 threads (thread i has
 // experts i + 128 j): an expert's rank is the number of keys before its own, counted
 // in a short loop over all of them (selecting the largest k times over took 15 us of a
 // call at 256 experts).  Loops stay rolled: every line of code is a miss.
-__device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s, int* idx, float* wt) {
+__device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, TopkScratch& s, float2* val /* [E], shared memory */,
+                                       unsigned long long* dkey, int* idx, float* wt) {
   const int lane = tid & 31, ew = tid >> 5, k = p.k;
   const float2* from = p.logits + (size_t)t * p.E;
 #pragma unroll 1
-  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) s.key[e] = e < p.E ? dec_key(__ldcg(&from[e].x)) : 0u;
+  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) {
+    const float2 q = e < p.E ? __ldcg(from + e) : make_float2(0.0f, 0.0f);
+    val[e] = q;
+    s.key[e] = e < p.E ? dec_key(q.x) : 0u;
+  }
   named_bar_sync(3, 128);
+  // the rank of an expert among all: four keys a look, two experts at once
   // lowest that a selected logit may be, highest that another may be
   float lo = INFINITY, hi = -INFINITY, most = 0.0f;
 #pragma unroll 1
-  for (int e = tid; e < ((p.E + 127) & ~127); e += 128) {
-    const uint32_t key = s.key[e];
-    const float2 q = e < p.E ? __ldcg(from + e) : make_float2(0.0f, 0.0f);
-    int rank = 0;
+  for (int e = tid; e < ((p.E + 127) & ~127); e += 256) {
+    const int e2 = e + 128;
+    const bool two = e2 < ((p.E + 127) & ~127);
+    const uint32_t key = s.key[e], key2 = two ? s.key[e2] : 0u;
+    int rank = 0, rank2 = 0;
 #pragma unroll 2
     for (int j = 0; j < p.E; j += 4) {  // (keys past the last expert are 0 and behind it in every tie)
       const uint4 o = *reinterpret_cast<const uint4*>(s.key + j);
-      const int d = e - j;  // ties: the lower id is before
+      const int d = e - j, d2 = e2 - j;  // ties: the lower id is before
       rank += (o.x >= key + (d <= 0)) + (o.y >= key + (d <= 1)) + (o.z >= key + (d <= 2)) + (o.w >= key + (d <= 3));
+      rank2 += (o.x >= key2 + (d2 <= 0)) + (o.y >= key2 + (d2 <= 1)) + (o.z >= key2 + (d2 <= 2)) + (o.w >= key2 + (d2 <= 3));
     }
-    const bool in = e < p.E && rank < k;
-    if (in) lo = fminf(lo, q.x - q.y);
-    else if (e < p.E) hi = fmaxf(hi, q.x + q.y);
-    most = fmaxf(most, q.y);
-    const uint32_t w = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) s.words[e >> 5] = w;
+#pragma unroll 1
+    for (int i = 0; i < (two ? 2 : 1); ++i) {
+      const int at = i ? e2 : e;
+      const float2 q = val[at];
+      const bool in = at < p.E && (i ? rank2 : rank) < k;
+      if (in) lo = fminf(lo, q.x - q.y);
+      else if (at < p.E) hi = fmaxf(hi, q.x + q.y);
+      most = fmaxf(most, q.y);
+      const uint32_t w = __ballot_sync(0xffffffffu, in);
+      if (lane == 0) s.words[at >> 5] = w;
+    }
   }
 #pragma unroll 1
   for (int d = 16; d >= 1; d >>= 1) {
@@ -451,8 +485,7 @@ __device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, T
 #pragma unroll 1
   for (int w = 0; w < 4; ++w) lo = fminf(lo, s.range[0][w]), hi = fmaxf(hi, s.range[1][w]), most = fmaxf(most, s.range[2][w]);
   if (most > 0.0f && lo <= hi) {  // (exact logits that are equal are ties, decided above)
-    if (ew == 0) decide_fp64(p, t, lo, hi, s.words);
-    named_bar_sync(3, 128);
+    decide_fp64(p, t, tid, lo, hi, s, val, dkey);
   }
   // slots in ascending order: the selected experts below
 #pragma unroll 1
@@ -461,7 +494,7 @@ __device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, T
     int slot = __popc(s.words[e >> 5] & ((1u << lane) - 1u));
 #pragma unroll 1
     for (int w = 0; w < e >> 5; ++w) slot += __popc(s.words[w]);
-    s.logit[slot] = __ldcg(&from[e].x);
+    s.logit[slot] = val[e].x;
     idx[slot] = e;
     if (p.out_idx && (int)blockIdx.x == t % (int)gridDim.x) p.out_idx[(size_t)t * k + slot] = e;
   }
@@ -590,36 +623,61 @@ __device__ __forceinline__ void fma4(float4& a, float g, const float4& b) {
   a.x = fmaf(g, b.x, a.x), a.y = fmaf(g, b.y, a.y), a.z = fmaf(g, b.z, a.z), a.w = fmaf(g, b.w, a.w);
 }
 
-// h of all rows, this CTA's share: an item is a row (token) and 128 columns, a warp
-// takes an item, a lane 4 columns: the sums of its pieces in order, SwiGLU.
+// The sums that follow are a few rows of 512 bytes out of L2 an output, and what they
+// cost is the trips there, each with up to four rows on its way.  A warp takes 128
+// columns, a lane 4; or, where that makes fewer trips (few items, many rows each), 32
+// columns: 8 lanes a row of 128 bytes, each quarter of the warp every fourth row, and
+// the quarters are added in the end (one token's last sums 10 -> 3 us; 64 tokens' h the
+// other way round, 13 -> 48).
+struct Split {
+  int quarter, of, lane, blocks;  // this lane's quarter, quarters, lane in it, items' columns
+  __device__ __forceinline__ Split(int items /* of 128 columns */, int rows) {
+    const int l = threadIdx.x & 31, warps = 4 * gridDim.x;
+    const bool split = (4 * items + warps - 1) / warps * ((rows + 15) / 16) < (items + warps - 1) / warps * ((rows + 3) / 4);
+    quarter = split ? l >> 3 : 0, of = split ? 4 : 1, lane = split ? l & 7 : l, blocks = split ? 32 : 128;
+  }
+};
+__device__ __forceinline__ float4 quarters(float4 a) {
+#pragma unroll
+  for (int d = 8; d <= 16; d <<= 1) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, d), a.y += __shfl_xor_sync(0xffffffffu, a.y, d);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, d), a.w += __shfl_xor_sync(0xffffffffu, a.w, d);
+  }
+  return a;
+}
+
+// h of all rows, this CTA's share: an item is a row (token) and 32 or 128 columns: the
+// sums of its pieces, SwiGLU.
 __device__ __noinline__ void finish_up(const DecodeParams& p, const DecodeSched& sc, int ew) {
-  const int lane = threadIdx.x & 31, tiles_s = p.I_s / 128, tiles_u = p.I / 128;
-  const int of_s = p.T * tiles_s, items = of_s + sc.n_rows * tiles_u;
+  const Split sp(p.T * (p.I_s / 128) + sc.n_rows * (p.I / 128), max(shared_pieces(p), sc.m_u));
+  const int blocks_s = p.I_s / sp.blocks, blocks_u = p.I / sp.blocks, of_s = p.T * blocks_s, items = of_s + sc.n_rows * blocks_u;
+#pragma unroll 1
   for (int it = blockIdx.x + ew * gridDim.x; it < items; it += 4 * gridDim.x) {
     const bool shared = it < of_s;
-    const int tiles = shared ? tiles_s : tiles_u, r = (shared ? it : it - of_s) / tiles, tile = (shared ? it : it - of_s) % tiles;
-    const int m = shared ? shared_pieces(p) : sc.m_u, col = tile * 128 + 4 * lane;
+    const int blocks = shared ? blocks_s : blocks_u, r = (shared ? it : it - of_s) / blocks, block = (shared ? it : it - of_s) % blocks;
+    const int m = shared ? shared_pieces(p) : sc.m_u, col = block * sp.blocks + 4 * sp.lane, tile = col >> 7;
     const size_t rows = shared ? p.T : (size_t)p.T * p.k;
-    const float* su = (shared ? p.sums_s : p.sums_u) + ((size_t)tile * 2 * m * rows + r) * 128 + 4 * lane;
+    const float* su = (shared ? p.sums_s : p.sums_u) + ((size_t)tile * 2 * m * rows + r) * 128 + (col & 127);
     const float* sg = su + (size_t)m * rows * 128;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), g = a;
 #pragma unroll 1
-    for (int c0 = 0; c0 < m; c0 += 4) {  // four pieces of both on their way at once
+    for (int c0 = sp.quarter; c0 < m; c0 += 4 * sp.of) {
       float4 q[2][4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const bool in = c0 + c < m;
-        q[0][c] = in ? ldcg4(su + (c0 + c) * rows * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
-        q[1][c] = in ? ldcg4(sg + (c0 + c) * rows * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool in = c0 + sp.of * c < m;
+        q[0][c] = in ? ldcg4(su + (c0 + sp.of * c) * rows * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+        q[1][c] = in ? ldcg4(sg + (c0 + sp.of * c) * rows * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) add4(a, q[0][c]), add4(g, q[1][c]);  // (a sum of zeros stays what it is)
+      for (int c = 0; c < 4; ++c) add4(a, q[0][c]), add4(g, q[1][c]);
     }
+    if (sp.of > 1) a = quarters(a), g = quarters(g);
     const float h[4] = {silu_f32(g.x) * a.x, silu_f32(g.y) * a.y, silu_f32(g.z) * a.z, silu_f32(g.w) * a.w};
     if (shared || !p.mx) {
       bf16* to = shared ? p.h_s + (size_t)r * p.I_s + col : static_cast<bf16*>(p.h) + (size_t)r * p.I + col;
-      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
-    } else {  // MX blocks of 32 columns = 8 lanes
+      if (sp.quarter == 0) *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+    } else {  // an MX block is 8 lanes
       float most = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
 #pragma unroll
       for (int d = 4; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
@@ -636,63 +694,51 @@ __device__ __noinline__ void finish_up(const DecodeParams& p, const DecodeSched&
         code = lo | hi << 16;
         scale = (uint32_t)(se + 127);
       }
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.h) + (size_t)r * p.I + col) = code;
-      if ((lane & 7) == 0) p.hs[(size_t)r * (p.I / 32) + col / 32] = (uint8_t)scale;
+      if (sp.quarter == 0) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.h) + (size_t)r * p.I + col) = code;
+      if (sp.quarter == 0 && (sp.lane & 7) == 0) p.hs[(size_t)r * (p.I / 32) + col / 32] = (uint8_t)scale;
     }
   }
 }
 
-// The output, this CTA's share: a token's outputs of the shared expert and of its
-// slots, in that order, weighted.  An item is a token and 128 columns.
+// The output, this CTA's share: an item is a token and 32 or 128 columns; its terms are the
+// pieces of the shared expert's output and of its slots' outputs, these times the slot's weight.
 __device__ __noinline__ void finish_down(const DecodeParams& p, const DecodeSched& sc, int ew) {
-  const int lane = threadIdx.x & 31, tiles = p.D / 128;
+  const int terms = sc.m_ds + p.k * sc.m_d;
+  const Split sp(p.T * (p.D / 128), terms);
+  const int blocks = p.D / sp.blocks;
   const size_t R = (size_t)p.T * p.k;
-  for (int it = blockIdx.x + ew * gridDim.x; it < p.T * tiles; it += 4 * gridDim.x) {
-    const int t = it / tiles, tile = it % tiles;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the terms in order: the shared expert's pieces, then every slot's; four on their way at once
-    const int terms = sc.m_ds + p.k * sc.m_d;
-    float4 y = s;
-    int j = -1, c = sc.m_d - 1;  // slot and piece of the term last looked at
-    const float* from = p.sums_ds + ((size_t)tile * sc.m_ds * p.T + t) * 128 + 4 * lane;
-    float g = 0.0f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < terms; i0 += 4) {
+  for (int it = blockIdx.x + ew * gridDim.x; it < p.T * blocks; it += 4 * gridDim.x) {
+    const int t = it / blocks, at = it % blocks * sp.blocks + 4 * sp.lane, tile = at >> 7, col = at & 127;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i0 = sp.quarter; i0 < terms; i0 += 4 * sp.of) {
       float4 q[4];
-      float w[4];          // weight with which y is added
-      uint32_t ends = 0u;  // behind these terms
+      float w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int term = i0 + i;
-        q[i] = make_float4(0.f, 0.f, 0.f, 0.f), w[i] = 0.0f;
+        const int term = i0 + sp.of * i;
+        const float* from = nullptr;
+        w[i] = 1.0f;
         if (term < sc.m_ds) {
-          q[i] = ldcg4(from + (size_t)term * p.T * 128);
-          w[i] = 1.0f, ends |= 1u << i;
+          from = p.sums_ds + ((size_t)(tile * sc.m_ds + term) * p.T + t) * 128;
         } else if (term < terms) {
-          if (++c == sc.m_d) {
-            c = 0, ++j;
-            const int r = t * p.k + j, e = sc.idx[r];
-            g = 0.0f, from = nullptr;
-            if (e != 0xffff) {
-              g = sc.w[r];
-              from = p.sums_d + ((size_t)tile * sc.m_d * R + sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull))) * 128 + 4 * lane;
-            }
+          const int j = (term - sc.m_ds) / sc.m_d, c = term - sc.m_ds - j * sc.m_d, r = t * p.k + j, e = sc.idx[r];
+          if (e != 0xffff) {
+            from = p.sums_d + ((size_t)(tile * sc.m_d + c) * R + sc.off[e] + __popcll(sc.mask[e] & ((1ull << t) - 1ull))) * 128;
+            w[i] = sc.w[r];
           }
-          if (from) q[i] = ldcg4(from + (size_t)c * R * 128);
-          if (from && c == sc.m_d - 1) w[i] = g, ends |= 1u << i;
         }
+        q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (from) q[i] = ldcg4(from + col);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        add4(y, q[i]);
-        if (ends >> i & 1) {
-          fma4(s, w[i], y);
-          y = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
+      for (int i = 0; i < 4; ++i) fma4(s, w[i], q[i]);
     }
-    *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + tile * 128 + 4 * lane) =
-        make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    if (sp.of > 1) s = quarters(s);
+    if (sp.quarter == 0)
+      *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + at) =
+          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
@@ -1000,8 +1046,12 @@ __global__ void __launch_bounds__(DEC_THREADS, 1) moe_decode_kernel(const __grid
       int done = 0;
 #pragma unroll 1
       for (int t = own ? 0 : blockIdx.x; t < p.T; t += own ? 1 : gridDim.x, ++done) {
-        token_topk(p, t, tid, scratch, own ? scratch.idx : p.topk_idx + (size_t)t * p.k, own ? sched.w + t * p.k : p.topk_w + (size_t)t * p.k);
-        if (own && tid < p.k) sched.idx[t * p.k + tid] = (uint16_t)scratch.idx[tid];  // (written before the last barrier)
+        token_topk(p, t, tid, scratch, reinterpret_cast<float2*>(sched.row), reinterpret_cast<unsigned long long*>(sched.w),
+                   own ? scratch.idx + t * p.k : p.topk_idx + (size_t)t * p.k, own ? scratch.w + t * p.k : p.topk_w + (size_t)t * p.k);
+        named_bar_sync(3, 128);
+      }
+      if (own) {
+        if (tid < p.T * p.k) sched.idx[tid] = (uint16_t)scratch.idx[tid], sched.w[tid] = scratch.w[tid];
         named_bar_sync(3, 128);
       }
       if (!own) {
