@@ -1,0 +1,251 @@
+// Backward of the norms around a block, rows in whole vectors (norm.cuh has the
+// formulas).  16384 x 7168 in bf16: BWDTIME, BWDSHARE of the copy rate.
+//
+// A CTA keeps to its own rows, a thread to its own columns: the sums over the rows (dw
+// and dc of both norms, dg) and the norms' weights stay in its registers, and leave
+// the CTA once, at the end.
+#include "norm.cuh"
+
+namespace moe {
+
+// First half of one norm's backward: from the gradient d of its output and the
+// normalised input n, the sums for dw and dc, u = d w in d, and the row's sums.
+template <int NV, bool LN>
+struct NormBack {
+  F2 aw[NV][4], ac[LN ? NV : 1][4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        aw[j][i] = f2(0.0f);
+        if constexpr (LN) ac[j][i] = f2(0.0f);
+      }
+  }
+};
+
+template <int NV, bool LN, bool GATE, int S, int B>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
+  constexpr bool KEEP = NV <= 2;  // the weights in registers
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float red[2 * 2 * NORM_MAX_WARPS];
+  const int tid = threadIdx.x;
+  const Mine<NV> mine(tid, blockDim.x, p.nvec);
+  Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
+  // order in the ring: y, dh, dy, o; the gate's rows are read when they are needed
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t at_h = p.pre ? p.D * esize(S) : 0, at_d = at_h + (p.pre ? p.D * esize(B) : 0), at_o = at_d + (p.dy ? p.D * esize(S) : 0);
+  const int64_t row0 = blockIdx.x, step = gridDim.x;
+  const int rows = (int)((p.T - row0 + step - 1) / step);
+  auto at_row = [&](const void* v, int64_t ld, int size) { return v ? static_cast<const char*>(v) + row0 * ld * size : nullptr; };
+  const char *ya = at_row(p.y, p.y_ld, esize(S)), *ha = at_row(p.dh, p.dh_ld, esize(B)), *da = at_row(p.dy, p.dy_ld, esize(S)),
+             *oa = at_row(p.o, p.o_ld, esize(B));
+  const char* gate = static_cast<const char*>(p.gate) + (p.gate_rows ? row0 * p.gate_ld * esize(B) : 0);
+  char *dx = const_cast<char*>(at_row(p.dx, p.dx_ld, esize(S))), *d_o = const_cast<char*>(at_row(p.d_o, p.do_ld, esize(B))),
+       *dgate = const_cast<char*>(at_row(p.dgate, p.dgate_ld, esize(B)));
+  const int64_t y_step = step * p.y_ld * esize(S), h_step = step * p.dh_ld * esize(B), d_step = step * p.dy_ld * esize(S),
+                o_step = step * p.o_ld * esize(B);
+  grid_dependency_wait();
+  auto fetch = [&](bool on, uint32_t stage) {
+    if (on) {
+      if (p.pre) {
+        mine.template fetch<S>(stage, ya);
+        mine.template fetch<B>(stage + at_h, ha);
+        ya += y_step, ha += h_step;
+      }
+      if (p.dy) {
+        mine.template fetch<S>(stage + at_d, da);
+        da += d_step;
+      }
+      if (p.o) {
+        mine.template fetch<B>(stage + at_o, oa);
+        oa += o_step;
+      }
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s + 1 < p.stages; ++s) fetch(s < rows, ring + s * p.stage_bytes);
+  F2 w1[KEEP ? NV : 1][4], w2[KEEP ? NV : 1][4];
+  if constexpr (KEEP)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (p.post) mine.weight(j, p.w1, p.pdt, p.w_off, w1[j]);
+      if (p.pre) mine.weight(j, p.w2, p.pdt, p.w_off, w2[j]);
+    }
+  NormBack<NV, LN> b1, b2;
+  b1.clear(), b2.clear();
+  F2 ag[GATE ? NV : 1][4];
+  if constexpr (GATE)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ag[j][i] = f2(0.0f);
+  // the row's means of u n and of u
+  auto means = [&](F2 (&q)[2], F2 e, float& c, float& m) {
+    m = 0.0f;
+    if constexpr (LN) {
+      const float2 b = split(e);
+      float s[2] = {both(q[0], q[1]), b.x + b.y};
+      group_sums(s, grp);
+      c = s[0] * p.inv_d, m = s[1] * p.inv_d;
+    } else {
+      float s[1] = {both(q[0], q[1])};
+      group_sums(s, grp);
+      c = s[0] * p.inv_d;
+    }
+  };
+  int stage = 0;
+#pragma unroll 1
+  for (int i = 0; i < rows; ++i) {
+    const uint32_t at = ring + stage * p.stage_bytes;
+    {
+      int next = stage + p.stages - 1;
+      next = next >= p.stages ? next - p.stages : next;
+      fetch(i + p.stages - 1 < rows, ring + next * p.stage_bytes);
+    }
+    float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.stats) {
+      const float* sp = p.stats + 4 * (row0 + i * step);
+      st = make_float4(sp[0], sp[1], sp[2], sp[3]);
+    }
+    cp_async_wait(p.stages - 1);
+    F2 d[NV][4], n[NV][4];
+    float c, m;
+    if (p.pre) {
+      F2 u[NV][4], q[2] = {f2(0.0f), f2(0.0f)}, e = f2(0.0f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        F2 w[4];
+        mine.template take<S>(j, at, st.z, n[j]);
+        mine.template take<B>(j, at + at_h, 0.0f, u[j]);
+        if constexpr (!KEEP) mine.weight(j, p.w2, p.pdt, p.w_off, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          n[j][k] = (LN ? n[j][k] + f2(-st.z) : n[j][k]) * f2(st.w);
+          b2.aw[j][k] = fma2(u[j][k], n[j][k], b2.aw[j][k]);
+          if constexpr (LN) b2.ac[j][k] = b2.ac[j][k] + u[j][k];
+          u[j][k] = u[j][k] * (KEEP ? w2[KEEP ? j : 0][k] : w[k]);
+          q[k & 1] = fma2(u[j][k], n[j][k], q[k & 1]);
+          if constexpr (LN) e = e + u[j][k];
+        }
+      }
+      means(q, e, c, m);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        if (p.dy) {
+          mine.template take<S>(j, at + at_d, 0.0f, d[j]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) d[j][k] = f2(0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[j][k] = fma2(f2(st.w), fma2(n[j][k], f2(-c), LN ? u[j][k] + f2(-m) : u[j][k]), d[j][k]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) mine.template take<S>(j, at + at_d, 0.0f, d[j]);
+    }
+    F2 q[2] = {f2(0.0f), f2(0.0f)}, e = f2(0.0f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      F2 t[4], w[4];
+      if (p.dx) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = f2(p.x_scale) * d[j][k];
+        mine.template put<S>(j, dx, t);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[j][k] = d[j][k] * f2(p.o_scale);
+      if (p.o) {
+        mine.template take<B>(j, at + at_o, p.post ? st.x : 0.0f, n[j]);
+        if (p.post)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) n[j][k] = (LN ? n[j][k] + f2(-st.x) : n[j][k]) * f2(st.y);
+      }
+      if constexpr (!KEEP)
+        if (p.post) mine.weight(j, p.w1, p.pdt, p.w_off, w);
+      if (p.gate) {
+        if (GATE || dgate) {  // z again, from the normalised output
+          F2 z[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[k] = p.post ? n[j][k] * (KEEP ? w1[KEEP ? j : 0][k] : w[k]) : n[j][k];
+          if (LN && p.post && p.c1) {
+            mine.global(j, p.c1, p.pdt, 0.0f, t);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] = z[k] + t[k];
+          }
+          if constexpr (GATE) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ag[j][k] = fma2(d[j][k], z[k], ag[j][k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] = z[k] * d[j][k];
+            mine.template put<B>(j, dgate, z);
+          }
+        }
+        mine.global(j, gate, p.gate_rows ? B : p.pdt, 0.0f, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[j][k] = d[j][k] * t[k];
+      }
+      if (p.post) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          b1.aw[j][k] = fma2(d[j][k], n[j][k], b1.aw[j][k]);
+          if constexpr (LN) b1.ac[j][k] = b1.ac[j][k] + d[j][k];
+          d[j][k] = d[j][k] * (KEEP ? w1[KEEP ? j : 0][k] : w[k]);
+          q[k & 1] = fma2(d[j][k], n[j][k], q[k & 1]);
+          if constexpr (LN) e = e + d[j][k];
+        }
+      }
+    }
+    if (p.post) {
+      means(q, e, c, m);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[j][k] = f2(st.y) * fma2(n[j][k], f2(-c), LN ? d[j][k] + f2(-m) : d[j][k]);
+    }
+    if (d_o) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) mine.template put<B>(j, d_o, d[j]);
+      d_o += step * p.do_ld * esize(B);
+    }
+    if (dx) dx += step * p.dx_ld * esize(S);
+    if (dgate) dgate += step * p.dgate_ld * esize(B);
+    if (p.gate_rows) gate += step * p.gate_ld * esize(B);
+    stage = stage + 1 >= p.stages ? 0 : stage + 1;
+  }
+  if (!p.sums) return;
+  auto leave = [&](int which, F2 (&a)[NV][4]) {
+    char* to = reinterpret_cast<char*>(p.sums + ((size_t)blockIdx.x * NORM_SUMS + which) * p.D);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) mine.template put<MOE_DTYPE_FP32>(j, to, a[j]);
+  };
+  if (p.post) leave(0, b1.aw);
+  if (p.pre) leave(2, b2.aw);
+  if constexpr (LN) {
+    if (p.post) leave(1, b1.ac);
+    if (p.pre) leave(3, b2.ac);
+  }
+  if constexpr (GATE) leave(4, ag);
+}
+
+cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
+  auto by_type = [&](auto s, auto b) {
+    constexpr int S = decltype(s)::value, B = decltype(b)::value;
+    auto kernel = p.D <= 8192
+                      ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B> : norm_bwd_kernel<2, true, false, S, B>)
+                                 : (gate_sum ? norm_bwd_kernel<2, false, true, S, B> : norm_bwd_kernel<2, false, false, S, B>))
+                      : (p.layer ? (gate_sum ? norm_bwd_kernel<4, true, true, S, B> : norm_bwd_kernel<4, true, false, S, B>)
+                                 : (gate_sum ? norm_bwd_kernel<4, false, true, S, B> : norm_bwd_kernel<4, false, false, S, B>));
+    return norm_launch(kernel, dim3(grid), threads, smem, st, p);
+  };
+  constexpr std::integral_constant<int, MOE_DTYPE_FP32> f32{};
+  constexpr std::integral_constant<int, MOE_DTYPE_BF16> b16{};
+  constexpr std::integral_constant<int, MOE_DTYPE_FP16> f16{};
+  if (p.sdt == MOE_DTYPE_BF16) return by_type(b16, b16);
+  if (p.sdt == MOE_DTYPE_FP16) return by_type(f16, f16);
+  return p.bdt == MOE_DTYPE_FP32 ? by_type(f32, f32) : p.bdt == MOE_DTYPE_BF16 ? by_type(f32, b16) : by_type(f32, f16);
+}
+
+}  // namespace moe
