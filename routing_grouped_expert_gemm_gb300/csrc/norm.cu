@@ -347,12 +347,13 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
     p.smem_w = need >= 2 * rows;
     while (rows > 1 && rows * row_bytes + p.smem_w * w_bytes > NORM_SMEM) --rows;
     if (rows * row_bytes + p.smem_w * w_bytes > NORM_SMEM) p.smem_w = 0;
-    // rows ahead that fit, up to three
+    // rows ahead that fit
     int64_t fit = (NORM_SMEM - p.smem_w * w_bytes) / (rows * row_bytes);
     const int64_t use = (need + rows - 1) / rows;
     fit = fit < use ? fit : use;
-    p.stages = (int)(fit < 3 ? fit : 3);
+    p.stages = (int)(fit < NORM_FWD_STAGES ? fit : NORM_FWD_STAGES);
     p.stage_bytes = (int)row_bytes;
+    p.whole = p.stages == NORM_FWD_STAGES && c.D <= 8192 && p.smem_w && c.post && c.pre && x && o && y && !p.gate;
     const int64_t ctas = (T + rows - 1) / rows, grid = ctas < pl->num_sms ? ctas : pl->num_sms;
     err = launch_norm_fwd(p, (unsigned)grid, (unsigned)(rows * p.group), rows * p.stages * p.stage_bytes + p.smem_w * w_bytes,
                           (cudaStream_t)stream);
@@ -436,12 +437,13 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
   const int64_t row_bytes = c.D * ((c.pre ? norm_size(sd) + norm_size(bd) : 0) + (dy ? norm_size(sd) : 0) + (use_o ? norm_size(bd) : 0));
   cudaError_t err;
   if (vec && row_bytes <= NORM_SMEM) {
-    // rows of the ring, up to four
+    // rows of the ring
     const int64_t per_sm = (grid + pl->num_sms - 1) / pl->num_sms, fit = NORM_SMEM / (per_sm * row_bytes), rows = (T + grid - 1) / grid;
-    p.stages = (int)(fit < 4 ? fit : 4);
+    p.stages = (int)(fit < NORM_BWD_STAGES ? fit : NORM_BWD_STAGES);
     if (p.stages > rows) p.stages = (int)rows;
     if (p.stages < 1) p.stages = 1;
     p.stage_bytes = (int)row_bytes;
+    p.whole = p.stages == NORM_BWD_STAGES && c.D <= 8192 && c.post && c.pre && dy && dx && d_o && (!p.gate || gate_sum);
     err = launch_norm_bwd(p, gate_sum, (unsigned)grid, (unsigned)norm_threads(c.D), (size_t)p.stages * row_bytes, stream);
   } else {
     cudaLaunchConfig_t lc = {};

@@ -29,6 +29,12 @@ constexpr int NORM_SUMS = 5;        // dw and dc of both norms, dg
 // threads of the forward's CTA: 64 registers each suffice for two vectors a thread
 constexpr int norm_fwd_threads(int nv) { return nv <= 2 ? 1024 : 512; }
 
+// Most of a row's instructions are not its arithmetic: looking at what a call has and
+// has not costs more than a hundred of them.  So the kernels have a form (`whole`) for
+// the call between two blocks of a large batch: all rows there, both norms, no gate, as many
+// rows in the ring as these constants say; and one that looks.
+constexpr int NORM_FWD_STAGES = 2, NORM_BWD_STAGES = 3;
+
 struct NormParams {
   int64_t T;
   int D, nvec;     // nvec: vectors of 8 elements in a row
@@ -36,6 +42,7 @@ struct NormParams {
   int group;       // forward: threads that share a row (a CTA's are that many times its rows at a time)
   int smem_w;      // forward: the weights in shared memory
   int stages;      // rows in the ring
+  int whole;
   int stage_bytes; // of a row in the ring
   float inv_d, eps, w_off, x_scale, o_scale;
   const void *w1, *c1, *w2, *c2, *gate;
@@ -211,10 +218,10 @@ struct Mine {
       for (int i = 0; i < 4; ++i) v[i] = f2(none);
     }
   }
-  template <int DT>
+  template <int DT, bool THERE>
   __device__ __forceinline__ void put(int j, char* row, F2 (&v)[4]) const {
     const Raw<DT> r = pack<DT>(v);
-    if (row && in[j]) {
+    if ((THERE || row) && in[j]) {
       uint4* to = reinterpret_cast<uint4*>(row + (DT == MOE_DTYPE_FP32 ? 2 * off[j] : off[j]));
       to[0] = r.q[0];
       if constexpr (DT == MOE_DTYPE_FP32) to[1] = r.q[1];

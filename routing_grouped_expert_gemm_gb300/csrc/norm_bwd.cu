@@ -24,8 +24,11 @@ struct NormBack {
   }
 };
 
-template <int NV, bool LN, bool GATE, int S, int B>
+template <int NV, bool LN, bool GATE, int S, int B, bool W>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
+  const bool pre = W || p.pre, post = W || p.post, has_dy = W || p.dy, has_o = W || p.o, gated = GATE || (!W && p.gate),
+             gate_rows = !W && p.gate_rows, has_dx = W || p.dx, has_do = W || p.d_o, has_dgate = !W && p.dgate;
+  const int stages = W ? NORM_BWD_STAGES : p.stages, stage_bytes = p.stage_bytes;
   constexpr bool KEEP = NV <= 2;  // the weights in registers
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2 * 2 * NORM_MAX_WARPS];
@@ -34,43 +37,45 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
   // order in the ring: y, dh, dy, o; the gate's rows are read when they are needed
   const uint32_t ring = smem_u32(smem);
-  const uint32_t at_h = p.pre ? p.D * esize(S) : 0, at_d = at_h + (p.pre ? p.D * esize(B) : 0), at_o = at_d + (p.dy ? p.D * esize(S) : 0);
+  const uint32_t at_h = pre ? p.D * esize(S) : 0, at_d = at_h + (pre ? p.D * esize(B) : 0), at_o = at_d + (has_dy ? p.D * esize(S) : 0);
   const int64_t row0 = blockIdx.x, step = gridDim.x;
   const int rows = (int)((p.T - row0 + step - 1) / step);
   auto at_row = [&](const void* v, int64_t ld, int size) { return v ? static_cast<const char*>(v) + row0 * ld * size : nullptr; };
   const char *ya = at_row(p.y, p.y_ld, esize(S)), *ha = at_row(p.dh, p.dh_ld, esize(B)), *da = at_row(p.dy, p.dy_ld, esize(S)),
              *oa = at_row(p.o, p.o_ld, esize(B));
-  const char* gate = static_cast<const char*>(p.gate) + (p.gate_rows ? row0 * p.gate_ld * esize(B) : 0);
+  const char* gate = static_cast<const char*>(p.gate) + (gate_rows ? row0 * p.gate_ld * esize(B) : 0);
   char *dx = const_cast<char*>(at_row(p.dx, p.dx_ld, esize(S))), *d_o = const_cast<char*>(at_row(p.d_o, p.do_ld, esize(B))),
        *dgate = const_cast<char*>(at_row(p.dgate, p.dgate_ld, esize(B)));
   const int64_t y_step = step * p.y_ld * esize(S), h_step = step * p.dh_ld * esize(B), d_step = step * p.dy_ld * esize(S),
-                o_step = step * p.o_ld * esize(B);
+                o_step = step * p.o_ld * esize(B), dx_step = step * p.dx_ld * esize(S), do_step = step * p.do_ld * esize(B),
+                dgate_step = step * p.dgate_ld * esize(B), gate_step = step * p.gate_ld * esize(B);
+  const float* stat = p.stats ? p.stats + 4 * row0 : nullptr;
   grid_dependency_wait();
   auto fetch = [&](bool on, uint32_t stage) {
     if (on) {
-      if (p.pre) {
+      if (pre) {
         mine.template fetch<S>(stage, ya);
         mine.template fetch<B>(stage + at_h, ha);
         ya += y_step, ha += h_step;
       }
-      if (p.dy) {
+      if (has_dy) {
         mine.template fetch<S>(stage + at_d, da);
         da += d_step;
       }
-      if (p.o) {
+      if (has_o) {
         mine.template fetch<B>(stage + at_o, oa);
         oa += o_step;
       }
     }
     cp_async_commit();
   };
-  for (int s = 0; s + 1 < p.stages; ++s) fetch(s < rows, ring + s * p.stage_bytes);
+  for (int s = 0; s + 1 < stages; ++s) fetch(s < rows, ring + s * stage_bytes);
   F2 w1[KEEP ? NV : 1][4], w2[KEEP ? NV : 1][4];
   if constexpr (KEEP)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (p.post) mine.weight(j, p.w1, p.pdt, p.w_off, w1[j]);
-      if (p.pre) mine.weight(j, p.w2, p.pdt, p.w_off, w2[j]);
+      if (post) mine.weight(j, p.w1, p.pdt, p.w_off, w1[j]);
+      if (pre) mine.weight(j, p.w2, p.pdt, p.w_off, w2[j]);
     }
   NormBack<NV, LN> b1, b2;
   b1.clear(), b2.clear();
@@ -97,21 +102,21 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   int stage = 0;
 #pragma unroll 1
   for (int i = 0; i < rows; ++i) {
-    const uint32_t at = ring + stage * p.stage_bytes;
+    const uint32_t at = ring + stage * stage_bytes;
     {
-      int next = stage + p.stages - 1;
-      next = next >= p.stages ? next - p.stages : next;
-      fetch(i + p.stages - 1 < rows, ring + next * p.stage_bytes);
+      int next = stage + stages - 1;
+      next = next >= stages ? next - stages : next;
+      fetch(i + stages - 1 < rows, ring + next * stage_bytes);
     }
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (p.stats) {
-      const float* sp = p.stats + 4 * (row0 + i * step);
-      st = make_float4(sp[0], sp[1], sp[2], sp[3]);
+    if (W || stat) {
+      st = make_float4(stat[0], stat[1], stat[2], stat[3]);
+      stat += 4 * step;
     }
-    cp_async_wait(p.stages - 1);
+    cp_async_wait(stages - 1);
     F2 d[NV][4], n[NV][4];
     float c, m;
-    if (p.pre) {
+    if (pre) {
       F2 u[NV][4], q[2] = {f2(0.0f), f2(0.0f)}, e = f2(0.0f);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
       means(q, e, c, m);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        if (p.dy) {
+        if (has_dy) {
           mine.template take<S>(j, at + at_d, 0.0f, d[j]);
         } else {
 #pragma unroll
@@ -149,27 +154,27 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       F2 t[4], w[4];
-      if (p.dx) {
+      if (has_dx) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) t[k] = f2(p.x_scale) * d[j][k];
-        mine.template put<S>(j, dx, t);
+        mine.template put<S, true>(j, dx, t);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[j][k] = d[j][k] * f2(p.o_scale);
-      if (p.o) {
-        mine.template take<B>(j, at + at_o, p.post ? st.x : 0.0f, n[j]);
-        if (p.post)
+      if (has_o) {
+        mine.template take<B>(j, at + at_o, post ? st.x : 0.0f, n[j]);
+        if (post)
 #pragma unroll
           for (int k = 0; k < 4; ++k) n[j][k] = (LN ? n[j][k] + f2(-st.x) : n[j][k]) * f2(st.y);
       }
       if constexpr (!KEEP)
-        if (p.post) mine.weight(j, p.w1, p.pdt, p.w_off, w);
-      if (p.gate) {
-        if (GATE || dgate) {  // z again, from the normalised output
+        if (post) mine.weight(j, p.w1, p.pdt, p.w_off, w);
+      if (gated) {
+        if (GATE || has_dgate) {  // z again, from the normalised output
           F2 z[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) z[k] = p.post ? n[j][k] * (KEEP ? w1[KEEP ? j : 0][k] : w[k]) : n[j][k];
-          if (LN && p.post && p.c1) {
+          for (int k = 0; k < 4; ++k) z[k] = post ? n[j][k] * (KEEP ? w1[KEEP ? j : 0][k] : w[k]) : n[j][k];
+          if (LN && post && p.c1) {
             mine.global(j, p.c1, p.pdt, 0.0f, t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) z[k] = z[k] + t[k];
@@ -180,14 +185,14 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) z[k] = z[k] * d[j][k];
-            mine.template put<B>(j, dgate, z);
+            mine.template put<B, true>(j, dgate, z);
           }
         }
-        mine.global(j, gate, p.gate_rows ? B : p.pdt, 0.0f, t);
+        mine.global(j, gate, gate_rows ? B : p.pdt, 0.0f, t);
 #pragma unroll
         for (int k = 0; k < 4; ++k) d[j][k] = d[j][k] * t[k];
       }
-      if (p.post) {
+      if (post) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           b1.aw[j][k] = fma2(d[j][k], n[j][k], b1.aw[j][k]);
@@ -198,34 +203,34 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
         }
       }
     }
-    if (p.post) {
+    if (post) {
       means(q, e, c, m);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) d[j][k] = f2(st.y) * fma2(n[j][k], f2(-c), LN ? d[j][k] + f2(-m) : d[j][k]);
     }
-    if (d_o) {
+    if (has_do) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) mine.template put<B>(j, d_o, d[j]);
-      d_o += step * p.do_ld * esize(B);
+      for (int j = 0; j < NV; ++j) mine.template put<B, true>(j, d_o, d[j]);
+      d_o += do_step;
     }
-    if (dx) dx += step * p.dx_ld * esize(S);
-    if (dgate) dgate += step * p.dgate_ld * esize(B);
-    if (p.gate_rows) gate += step * p.gate_ld * esize(B);
-    stage = stage + 1 >= p.stages ? 0 : stage + 1;
+    if (has_dx) dx += dx_step;
+    if (has_dgate) dgate += dgate_step;
+    if (gate_rows) gate += gate_step;
+    stage = stage + 1 >= stages ? 0 : stage + 1;
   }
   if (!p.sums) return;
   auto leave = [&](int which, F2 (&a)[NV][4]) {
     char* to = reinterpret_cast<char*>(p.sums + ((size_t)blockIdx.x * NORM_SUMS + which) * p.D);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) mine.template put<MOE_DTYPE_FP32>(j, to, a[j]);
+    for (int j = 0; j < NV; ++j) mine.template put<MOE_DTYPE_FP32, true>(j, to, a[j]);
   };
-  if (p.post) leave(0, b1.aw);
-  if (p.pre) leave(2, b2.aw);
+  if (post) leave(0, b1.aw);
+  if (pre) leave(2, b2.aw);
   if constexpr (LN) {
-    if (p.post) leave(1, b1.ac);
-    if (p.pre) leave(3, b2.ac);
+    if (post) leave(1, b1.ac);
+    if (pre) leave(3, b2.ac);
   }
   if constexpr (GATE) leave(4, ag);
 }
@@ -233,11 +238,13 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
 cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
   auto by_type = [&](auto s, auto b) {
     constexpr int S = decltype(s)::value, B = decltype(b)::value;
-    auto kernel = p.D <= 8192
-                      ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B> : norm_bwd_kernel<2, true, false, S, B>)
-                                 : (gate_sum ? norm_bwd_kernel<2, false, true, S, B> : norm_bwd_kernel<2, false, false, S, B>))
-                      : (p.layer ? (gate_sum ? norm_bwd_kernel<4, true, true, S, B> : norm_bwd_kernel<4, true, false, S, B>)
-                                 : (gate_sum ? norm_bwd_kernel<4, false, true, S, B> : norm_bwd_kernel<4, false, false, S, B>));
+    auto kernel = p.whole ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, true> : norm_bwd_kernel<2, true, false, S, B, true>)
+                                     : (gate_sum ? norm_bwd_kernel<2, false, true, S, B, true> : norm_bwd_kernel<2, false, false, S, B, true>))
+                  : p.D <= 8192
+                      ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, false> : norm_bwd_kernel<2, true, false, S, B, false>)
+                                 : (gate_sum ? norm_bwd_kernel<2, false, true, S, B, false> : norm_bwd_kernel<2, false, false, S, B, false>))
+                      : (p.layer ? (gate_sum ? norm_bwd_kernel<4, true, true, S, B, false> : norm_bwd_kernel<4, true, false, S, B, false>)
+                                 : (gate_sum ? norm_bwd_kernel<4, false, true, S, B, false> : norm_bwd_kernel<4, false, false, S, B, false>));
     return norm_launch(kernel, dim3(grid), threads, smem, st, p);
   };
   constexpr std::integral_constant<int, MOE_DTYPE_FP32> f32{};

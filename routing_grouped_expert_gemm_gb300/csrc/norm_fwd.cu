@@ -11,28 +11,31 @@
 
 namespace moe {
 
-template <int NV, bool LN, int S, int B>
+template <int NV, bool LN, int S, int B, bool W>
 __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const NormParams p) {
+  const bool has_x = W || p.x, has_o = W || p.o, post = W || p.post, pre = W || p.pre, has_y = W || p.y, smem_w = W || p.smem_w,
+             gated = !W && p.gate, gate_rows = !W && p.gate_rows;
+  const int stages = W ? NORM_FWD_STAGES : p.stages, stage_bytes = p.stage_bytes;
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[16 * 2 * 2 * NORM_MAX_WARPS];  // of groups of two warps and more
   const int g = threadIdx.x / p.group, groups = blockDim.x / p.group, tid = threadIdx.x - g * p.group;
   const Mine<NV> mine(tid, p.group, p.nvec);
   Group grp{red + (g & 15) * (2 * 2 * NORM_MAX_WARPS), g, p.group >> 5, tid >> 5, 0};
-  const uint32_t base = smem_u32(smem), ring = base + (uint32_t)(g * p.stages * p.stage_bytes);
-  const uint32_t at_o = p.x ? p.D * esize(S) : 0, at_g = at_o + (p.o ? p.D * esize(B) : 0);
+  const uint32_t base = smem_u32(smem), ring = base + (uint32_t)(g * stages * stage_bytes);
+  const uint32_t at_o = has_x ? p.D * esize(S) : 0, at_g = at_o + (has_o ? p.D * esize(B) : 0);
   // this group's rows, and the pointers that go along with them (`a`: to what is fetched ahead)
   const int64_t row0 = (int64_t)g * gridDim.x + blockIdx.x, step = (int64_t)groups * gridDim.x;
   const int rows = row0 < p.T ? (int)((p.T - row0 + step - 1) / step) : 0;
   const char* xa = static_cast<const char*>(p.x) + row0 * p.x_ld * esize(S);
   const char* oa = static_cast<const char*>(p.o) + row0 * p.o_ld * esize(B);
-  const char* ga = static_cast<const char*>(p.gate) + (p.gate_rows ? row0 * p.gate_ld * esize(B) : 0);
-  char* y = p.y ? static_cast<char*>(p.y) + row0 * p.y_ld * esize(S) : nullptr;
+  const char* ga = static_cast<const char*>(p.gate) + (gate_rows ? row0 * p.gate_ld * esize(B) : 0);
+  char* y = has_y ? static_cast<char*>(p.y) + row0 * p.y_ld * esize(S) : nullptr;
   char* h = static_cast<char*>(p.h) + row0 * p.h_ld * esize(B);
   const int64_t xs = step * p.x_ld * esize(S), os = step * p.o_ld * esize(B), gs = step * p.gate_ld * esize(B),
-                ys = p.y ? step * p.y_ld * esize(S) : 0, hs = step * p.h_ld * esize(B);
+                ys = has_y ? step * p.y_ld * esize(S) : 0, hs = step * p.h_ld * esize(B);
   grid_dependency_wait();
   auto fetch_o = [&](bool on, uint32_t stage) {
-    if (on && p.o) {
+    if (on && has_o) {
       mine.template fetch<B>(stage + at_o, oa);
       oa += os;
     }
@@ -40,31 +43,31 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   };
   auto fetch_x = [&](bool on, uint32_t stage) {
     if (on) {
-      if (p.x) {
+      if (has_x) {
         mine.template fetch<S>(stage, xa);
         xa += xs;
       }
-      if (p.gate_rows) {
+      if (gate_rows) {
         mine.template fetch<B>(stage + at_g, ga);
         ga += gs;
       }
     }
     cp_async_commit();
   };
-  for (int s = 0; s < p.stages; ++s) {
-    fetch_o(s < rows, ring + s * p.stage_bytes);
-    fetch_x(s < rows, ring + s * p.stage_bytes);
+  for (int s = 0; s < stages; ++s) {
+    fetch_o(s < rows, ring + s * stage_bytes);
+    fetch_x(s < rows, ring + s * stage_bytes);
   }
   // the norms' weights as fp32, once per CTA
   uint32_t sw1 = 0, sw2 = 0;
-  if (p.smem_w) {
-    sw1 = sw2 = base + groups * p.stages * p.stage_bytes;
-    if (p.post) sw2 += p.D * 4;
+  if (smem_w) {
+    sw1 = sw2 = base + groups * stages * stage_bytes;
+    if (post) sw2 += p.D * 4;
 #pragma unroll 1
     for (int i = threadIdx.x; i < 2 * p.nvec; i += blockDim.x) {
       const bool second = i >= p.nvec;
       const int v = second ? i - p.nvec : i;
-      if (!(second ? p.pre : p.post)) continue;
+      if (!(second ? pre : post)) continue;
       const Mine<1> one(v, 0, p.nvec);
       F2 w[4];
       one.weight(0, second ? p.w2 : p.w1, p.pdt, p.w_off, w);
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   // vector j of (v - m) r w + c in place
   auto apply = [&](int j, F2 (&v)[4], float m, float r, uint32_t sw, const void* w, const void* c) {
     F2 t[4];
-    if (p.smem_w) mine.template take<MOE_DTYPE_FP32>(j, sw, 0.0f, t);
+    if (smem_w) mine.template take<MOE_DTYPE_FP32>(j, sw, 0.0f, t);
     else mine.weight(j, w, p.pdt, p.w_off, t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (LN ? v[i] + f2(-m) : v[i]) * f2(r) * t[i];
@@ -89,70 +92,72 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
     }
   };
   int stage = 0;
+  float* stat = p.stats ? p.stats + 4 * row0 : nullptr;
 #pragma unroll 1
   for (int i = 0; i < rows; ++i) {
-    const uint32_t at = ring + stage * p.stage_bytes;
-    const bool more = i + p.stages < rows;
+    const uint32_t at = ring + stage * stage_bytes;
+    const bool more = i + stages < rows;
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     F2 v[NV][4];
-    cp_async_wait(2 * p.stages - 1);  // o
+    cp_async_wait(2 * stages - 1);  // o
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (p.o) {
+      if (has_o) {
         mine.template take<B>(j, at + at_o, 0.0f, v[j]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = f2(0.0f);
       }
     }
-    if (p.post) {
+    if (post) {
       row_stats<NV, LN>(mine, v, p.inv_d, p.eps, grp, st.x, st.y);
       fetch_o(more, at);  // the sums have used every element of o
     }
-    cp_async_wait(2 * p.stages - (p.post ? 1 : 2));  // x and the gate
+    cp_async_wait(2 * stages - (post ? 1 : 2));  // x and the gate
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       F2 t[4];
-      if (p.post) apply(j, v[j], st.x, st.y, sw1, p.w1, p.c1);
-      if (p.gate) {
-        if (p.gate_rows) mine.template take<B>(j, at + at_g, 0.0f, t);
+      if (post) apply(j, v[j], st.x, st.y, sw1, p.w1, p.c1);
+      if (gated) {
+        if (gate_rows) mine.template take<B>(j, at + at_g, 0.0f, t);
         else mine.global(j, p.gate, p.pdt, 0.0f, t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = v[j][e] * t[e];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[j][e] = v[j][e] * f2(p.o_scale);
-      if (p.x) {
+      if (has_x) {
         mine.template take<S>(j, at, 0.0f, t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = fma2(f2(p.x_scale), t[e], v[j][e]);
       }
-      mine.template put<S>(j, y, v[j]);
+      mine.template put<S, W>(j, y, v[j]);
     }
-    if (p.pre) row_stats<NV, LN>(mine, v, p.inv_d, p.eps, grp, st.z, st.w);
-    if (!p.post) fetch_o(more, at);
+    if (pre) row_stats<NV, LN>(mine, v, p.inv_d, p.eps, grp, st.z, st.w);
+    if (!post) fetch_o(more, at);
     fetch_x(more, at);
-    if (p.pre) {
+    if (pre) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         apply(j, v[j], st.z, st.w, sw2, p.w2, p.c2);
-        mine.template put<B>(j, h, v[j]);
+        mine.template put<B, true>(j, h, v[j]);
       }
     }
-    if (p.stats && tid == 0) {
-      float* s = p.stats + 4 * (row0 + i * step);
-      s[0] = st.x, s[1] = st.y, s[2] = st.z, s[3] = st.w;
+    if (stat) {
+      if (tid == 0) stat[0] = st.x, stat[1] = st.y, stat[2] = st.z, stat[3] = st.w;
+      stat += 4 * step;
     }
     y += ys, h += hs;
-    stage = stage + 1 >= p.stages ? 0 : stage + 1;
+    stage = stage + 1 >= stages ? 0 : stage + 1;
   }
 }
 
 cudaError_t launch_norm_fwd(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
   auto by_type = [&](auto s, auto b) {
     constexpr int S = decltype(s)::value, B = decltype(b)::value;
-    auto kernel = p.D <= 8192 ? (p.layer ? norm_fwd_kernel<2, true, S, B> : norm_fwd_kernel<2, false, S, B>)
-                              : (p.layer ? norm_fwd_kernel<4, true, S, B> : norm_fwd_kernel<4, false, S, B>);
+    auto kernel = p.whole       ? (p.layer ? norm_fwd_kernel<2, true, S, B, true> : norm_fwd_kernel<2, false, S, B, true>)
+                  : p.D <= 8192 ? (p.layer ? norm_fwd_kernel<2, true, S, B, false> : norm_fwd_kernel<2, false, S, B, false>)
+                                : (p.layer ? norm_fwd_kernel<4, true, S, B, false> : norm_fwd_kernel<4, false, S, B, false>);
     return norm_launch(kernel, dim3(grid), threads, smem, st, p);
   };
   constexpr std::integral_constant<int, MOE_DTYPE_FP32> f32{};
