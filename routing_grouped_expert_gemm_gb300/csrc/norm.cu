@@ -1,162 +1,11 @@
 // Norms around a block and their gradients (moe_norm, moe_norm_bwd in
-// include/moe.h): the C entries, the sums over the rows, and the kernels for rows
-// that are not whole vectors on 16-byte boundaries (or do not fit the fast kernels'
-// shared memory).  norm.cuh has the formulas.
+// include/moe.h): the C entries and the sums over the rows.  norm.cuh has the formulas.
 #include <new>
 #include <type_traits>
 
 #include "norm.cuh"
 
 namespace moe {
-
-// ------------------------------------------------------------------ any rows
-// A CTA per row; thread i takes elements i, i + NT, ... one by one, so that whatever
-// the alignment a warp's accesses lie together.  Values wait in shared memory as fp32
-// between the passes over a row, loops stay loops.
-__device__ __forceinline__ float load1(const void* p, int dt, int64_t i) {
-  if (dt == MOE_DTYPE_FP32) return static_cast<const float*>(p)[i];
-  if (dt == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const bf16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-// rounds to the type, stores unless p is null, returns what was rounded
-__device__ __forceinline__ float store1(void* p, int dt, int64_t i, float v) {
-  if (dt == MOE_DTYPE_FP32) {
-    if (p) static_cast<float*>(p)[i] = v;
-    return v;
-  }
-  if (dt == MOE_DTYPE_BF16) {
-    const bf16 w = __float2bfloat16_rn(v);
-    if (p) static_cast<bf16*>(p)[i] = w;
-    return __bfloat162float(w);
-  }
-  const __half w = __float2half_rn(v);
-  if (p) static_cast<__half*>(p)[i] = w;
-  return __half2float(w);
-}
-__device__ __forceinline__ float weight1(const NormParams& p, const void* w, int e) { return w ? load1(w, p.pdt, e) + p.w_off : 1.0f; }
-
-// mean and 1 / sqrt(variance + eps) of the row in shared memory
-__device__ __forceinline__ void any_stats(const NormParams& p, const float* v, float first /* this thread's sum */, Group& grp, float& m, float& r) {
-  float s[1] = {first};
-  m = 0.0f;
-  if (p.layer) {
-    group_sums(s, grp);
-    m = s[0] * p.inv_d;
-  }
-  s[0] = 0.0f;
-  for (int e = threadIdx.x; e < p.D; e += blockDim.x) s[0] = fmaf(v[e] - m, v[e] - m, s[0]);
-  group_sums(s, grp);
-  r = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
-}
-
-__global__ void __launch_bounds__(512) norm_fwd_any_kernel(const NormParams p) {
-  extern __shared__ __align__(16) float row_v[];  // [D]
-  __shared__ float red[2 * 2 * NORM_MAX_WARPS];
-  Group grp{red, 0, (int)blockDim.x >> 5, (int)threadIdx.x >> 5, 0};
-  grid_dependency_wait();
-#pragma unroll 1
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    float m[2] = {0.0f, 0.0f}, r[2] = {0.0f, 0.0f}, s = 0.0f;
-    if (p.post) {
-#pragma unroll 4
-      for (int e = threadIdx.x; e < p.D; e += blockDim.x) s += row_v[e] = load1(p.o, p.bdt, t * p.o_ld + e);
-      any_stats(p, row_v, s, grp, m[0], r[0]);
-    }
-    s = 0.0f;
-#pragma unroll 4
-    for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
-      float v = p.post ? (row_v[e] - m[0]) * r[0] * weight1(p, p.w1, e) + (p.c1 ? load1(p.c1, p.pdt, e) : 0.0f)
-                : p.o  ? load1(p.o, p.bdt, t * p.o_ld + e)
-                       : 0.0f;
-      if (p.gate) v *= p.gate_rows ? load1(p.gate, p.bdt, t * p.gate_ld + e) : load1(p.gate, p.pdt, e);
-      v *= p.o_scale;
-      if (p.x) v = fmaf(p.x_scale, load1(p.x, p.sdt, t * p.x_ld + e), v);
-      s += row_v[e] = store1(p.y, p.sdt, t * p.y_ld + e, v);
-    }
-    if (p.pre) {
-      any_stats(p, row_v, s, grp, m[1], r[1]);
-#pragma unroll 4
-      for (int e = threadIdx.x; e < p.D; e += blockDim.x)
-        store1(p.h, p.bdt, t * p.h_ld + e, (row_v[e] - m[1]) * r[1] * weight1(p, p.w2, e) + (p.c2 ? load1(p.c2, p.pdt, e) : 0.0f));
-    }
-    if (p.stats && threadIdx.x == 0) {
-      float* st = p.stats + 4 * t;
-      st[0] = m[0], st[1] = r[0], st[2] = m[1], st[3] = r[1];
-    }
-  }
-}
-
-// The sums over the rows are kept in the CTA's part of the workspace, an element by its own thread.
-__global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormParams p, int gate_sum) {
-  extern __shared__ __align__(16) float row_d[];  // [D] the gradient, then [D] the normalised input
-  __shared__ float red[2 * 2 * NORM_MAX_WARPS];
-  float* const row_n = row_d + p.D;
-  Group grp{red, 0, (int)blockDim.x >> 5, (int)threadIdx.x >> 5, 0};
-  grid_dependency_wait();
-  float* sums = p.sums ? p.sums + (size_t)blockIdx.x * NORM_SUMS * p.D : nullptr;
-  auto add = [&](int which, int e, float v, bool first) {
-    float* at = sums + (size_t)which * p.D + e;
-    *at = first ? v : *at + v;
-  };
-#pragma unroll 1
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    const bool first = t == blockIdx.x;
-    float st[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.stats)
-      for (int i = 0; i < 4; ++i) st[i] = p.stats[4 * t + i];
-    float s[2] = {0.0f, 0.0f};
-    if (p.pre) {
-#pragma unroll 4
-      for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
-        const float d = load1(p.dh, p.bdt, t * p.dh_ld + e), n = (load1(p.y, p.sdt, t * p.y_ld + e) - st[2]) * st[3];
-        if (sums) {
-          add(2, e, d * n, first);
-          if (p.layer) add(3, e, d, first);
-        }
-        const float u = d * weight1(p, p.w2, e);
-        s[0] = fmaf(u, n, s[0]), s[1] += u;
-        row_d[e] = u, row_n[e] = n;
-      }
-      group_sums(s, grp);
-    }
-    const float c2 = s[0] * p.inv_d, m2 = p.layer ? s[1] * p.inv_d : 0.0f;
-    s[0] = s[1] = 0.0f;
-#pragma unroll 4
-    for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
-      float d = p.dy ? load1(p.dy, p.sdt, t * p.dy_ld + e) : 0.0f;
-      if (p.pre) d = fmaf(st[3], row_d[e] - row_n[e] * c2 - m2, d);
-      if (p.dx) store1(p.dx, p.sdt, t * p.dx_ld + e, p.x_scale * d);
-      d *= p.o_scale;
-      float n = p.o ? load1(p.o, p.bdt, t * p.o_ld + e) : 0.0f;
-      if (p.post) n = (n - st[0]) * st[1];
-      const float w = p.post ? weight1(p, p.w1, e) : 1.0f;
-      if (p.gate) {
-        const float z = n * w + (p.post && p.c1 ? load1(p.c1, p.pdt, e) : 0.0f);
-        if (gate_sum && sums) add(4, e, d * z, first);
-        if (p.dgate) store1(p.dgate, p.bdt, t * p.dgate_ld + e, d * z);
-        d *= p.gate_rows ? load1(p.gate, p.bdt, t * p.gate_ld + e) : load1(p.gate, p.pdt, e);
-      }
-      if (p.post) {
-        if (sums) {
-          add(0, e, d * n, first);
-          if (p.layer) add(1, e, d, first);
-        }
-        d *= w;
-        s[0] = fmaf(d, n, s[0]), s[1] += d;
-        row_d[e] = d, row_n[e] = n;
-      } else if (p.d_o) {
-        store1(p.d_o, p.bdt, t * p.do_ld + e, d);
-      }
-    }
-    if (p.post) {
-      group_sums(s, grp);
-      const float c1 = s[0] * p.inv_d, m1 = p.layer ? s[1] * p.inv_d : 0.0f;
-      if (p.d_o)
-#pragma unroll 4
-        for (int e = threadIdx.x; e < p.D; e += blockDim.x) store1(p.d_o, p.bdt, t * p.do_ld + e, st[1] * (row_d[e] - row_n[e] * c1 - m1));
-    }
-  }
-}
 
 struct NormSums {
   const float* part;
@@ -173,6 +22,7 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const NormSums p) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (col < p.D)
+#pragma unroll 8
     for (int c = w; c < p.ctas; c += 8) s += p.part[((size_t)c * NORM_SUMS + blockIdx.y) * p.D + col];
   part[w][lane] = s;
   __syncthreads();
@@ -359,8 +209,11 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
                           (cudaStream_t)stream);
   } else {
     const int nt = any_threads(c.D);
-    const int64_t most = (int64_t)pl->num_sms * (1536 / nt), grid = T < most ? T : most;
-    err = norm_launch(norm_fwd_any_kernel, dim3((unsigned)grid), (unsigned)nt, (size_t)c.D * 4, (cudaStream_t)stream, p);
+    int64_t per_sm = 1536 / nt;
+    const int64_t by_smem = NORM_SMEM / (12 * c.D);
+    per_sm = per_sm < by_smem ? per_sm : by_smem < 1 ? 1 : by_smem;
+    const int64_t most = per_sm * pl->num_sms, grid = T < most ? T : most;
+    err = launch_norm_fwd_any(p, (unsigned)grid, (unsigned)nt, (cudaStream_t)stream);
   }
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -444,21 +297,15 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
     if (p.stages < 1) p.stages = 1;
     p.stage_bytes = (int)row_bytes;
     p.whole = p.stages == NORM_BWD_STAGES && c.D <= 8192 && c.post && c.pre && dy && dx && d_o && (!p.gate || gate_sum);
-    err = launch_norm_bwd(p, gate_sum, (unsigned)grid, (unsigned)norm_threads(c.D), (size_t)p.stages * row_bytes, stream);
+    size_t smem = (size_t)p.stages * row_bytes;
+    if (p.whole && c.kind == MOE_NORM_RMS && c.D > 4096 && T >= 4 * grid && 2 * row_bytes + 8 * c.D <= NORM_SMEM) {
+      p.whole = 2;  // two rows at a time, with the weights
+      smem = (size_t)(2 * row_bytes + 8 * c.D);
+    }
+    err = launch_norm_bwd(p, gate_sum, (unsigned)grid, (unsigned)norm_threads(c.D), smem, stream);
   } else {
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)grid);
-    lc.blockDim = dim3((unsigned)any_threads(c.D));
-    lc.dynamicSmemBytes = (size_t)c.D * 8;
-    lc.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    err = lc.dynamicSmemBytes > 40 * 1024 ? cudaFuncSetAttribute(norm_bwd_any_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lc.dynamicSmemBytes)
-                                          : cudaSuccess;
-    if (err == cudaSuccess) err = cudaLaunchKernelEx(&lc, norm_bwd_any_kernel, (const NormParams)p, (int)gate_sum);
+    p.gate_sum = gate_sum;
+    err = launch_norm_bwd_any(p, (unsigned)grid, (unsigned)any_threads(c.D), stream);
   }
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   if (sums) {

@@ -1,5 +1,5 @@
-// Shared by the kernels of the norms around a block (norm.cu, norm_fwd.cu,
-// norm_bwd.cu): parameters, packed fp32 arithmetic, rows in vectors, sums.
+// Shared by the kernels of the norms around a block (norm.cu, norm_fwd.cu, norm_bwd.cu,
+// norm_any.cu): parameters, packed fp32 arithmetic, rows in vectors, sums.
 //
 //   z = N(o),  y = a x + b g z,  h = N(y),   N(v) = (v - m) r w + c,
 //   r = 1 / sqrt(mean((v - m)^2) + eps),  m = mean(v) or 0.
@@ -17,6 +17,8 @@
 // else reads them) and meets the others only for the row's sums, one barrier each.
 #pragma once
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "common.cuh"
@@ -42,7 +44,7 @@ struct NormParams {
   int group;       // forward: threads that share a row (a CTA's are that many times its rows at a time)
   int smem_w;      // forward: the weights in shared memory
   int stages;      // rows in the ring
-  int whole;
+  int whole, gate_sum;
   int stage_bytes; // of a row in the ring
   float inv_d, eps, w_off, x_scale, o_scale;
   const void *w1, *c1, *w2, *c2, *gate;
@@ -58,6 +60,9 @@ struct NormParams {
 // Fast kernels: rows in whole vectors on 16-byte boundaries
 cudaError_t launch_norm_fwd(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
+// Any rows (norm_any.cu)
+cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st);
+cudaError_t launch_norm_bwd_any(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st);
 
 template <typename P>
 cudaError_t norm_launch(void (*kernel)(P), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const P& p) {

@@ -235,10 +235,196 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   if constexpr (GATE) leave(4, ag);
 }
 
+// The whole call's rms form for long rows, of which an SM has room for one CTA: two rows
+// at a time, so that one's arithmetic fills the other's barriers, the weights in shared
+// memory to make registers for them.  One place a tensor and row in the ring, filled
+// again as soon as it has been read.
+template <bool GATE, int S, int B>
+__global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p) {
+  constexpr int NV = 2;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ float red[2 * 2 * NORM_MAX_WARPS];
+  const int tid = threadIdx.x;
+  const Mine<NV> mine(tid, blockDim.x, p.nvec);
+  Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t at_h = p.D * esize(S), at_d = at_h + p.D * esize(B), at_o = at_d + p.D * esize(S), row_bytes = at_o + p.D * esize(B);
+  const uint32_t sw1 = ring + 2 * row_bytes, sw2 = sw1 + p.D * 4;
+  const int64_t row0 = 2 * (int64_t)blockIdx.x, step = 2 * (int64_t)gridDim.x;
+  const int pairs = (int)(((p.T + 1) / 2 - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  const char* in[4] = {static_cast<const char*>(p.y) + row0 * p.y_ld * esize(S), static_cast<const char*>(p.dh) + row0 * p.dh_ld * esize(B),
+                       static_cast<const char*>(p.dy) + row0 * p.dy_ld * esize(S), static_cast<const char*>(p.o) + row0 * p.o_ld * esize(B)};
+  const int64_t ld[4] = {p.y_ld * esize(S), p.dh_ld * esize(B), p.dy_ld * esize(S), p.o_ld * esize(B)};
+  char *dx = static_cast<char*>(p.dx) + row0 * p.dx_ld * esize(S), *d_o = static_cast<char*>(p.d_o) + row0 * p.do_ld * esize(B);
+  const int64_t dx_ld = p.dx_ld * esize(S), do_ld = p.do_ld * esize(B);
+  const float* stat = p.stats + 4 * row0;
+  grid_dependency_wait();
+  // both rows of a tensor for the next pair (the batch's last may have one)
+  int64_t left = p.T - row0;  // rows from this pair's first on
+  auto fetch = [&](auto which, bool on, bool two) {
+    constexpr int K = decltype(which)::value, DT = K == 0 || K == 2 ? S : B;
+    const uint32_t at = ring + (K == 0 ? 0 : K == 1 ? at_h : K == 2 ? at_d : at_o);
+    if (on) {
+      mine.template fetch<DT>(at, in[K]);
+      if (two) mine.template fetch<DT>(at + row_bytes, in[K] + ld[K]);
+      in[K] += (int64_t)step * ld[K];
+    }
+    cp_async_commit();
+  };
+  constexpr std::integral_constant<int, 0> k0{};
+  constexpr std::integral_constant<int, 1> k1{};
+  constexpr std::integral_constant<int, 2> k2{};
+  constexpr std::integral_constant<int, 3> k3{};
+  fetch(k0, pairs > 0, left > 1);
+  fetch(k1, pairs > 0, left > 1);
+  fetch(k2, pairs > 0, left > 1);
+  fetch(k3, pairs > 0, left > 1);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (mine.in[j]) {  // a thread's own weights into its own places
+      F2 w[4];
+      mine.weight(j, p.w1, p.pdt, p.w_off, w);
+      Raw<MOE_DTYPE_FP32> r = pack<MOE_DTYPE_FP32>(w);
+      char* to = smem + 2 * row_bytes + mine.off[j];
+      *reinterpret_cast<uint4*>(to) = r.q[0], *reinterpret_cast<uint4*>(to + mine.plane) = r.q[1];
+      mine.weight(j, p.w2, p.pdt, p.w_off, w);
+      r = pack<MOE_DTYPE_FP32>(w);
+      to += p.D * 4;
+      *reinterpret_cast<uint4*>(to) = r.q[0], *reinterpret_cast<uint4*>(to + mine.plane) = r.q[1];
+    }
+  F2 a1[NV][4], a2[NV][4], ag[GATE ? NV : 1][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a1[j][k] = a2[j][k] = f2(0.0f);
+      if constexpr (GATE) ag[j][k] = f2(0.0f);
+    }
+#pragma unroll 1
+  for (int i = 0; i < pairs; ++i) {
+    const bool two = left > 1, more = i + 1 < pairs, more_two = left - step > 1;
+    left -= step;
+    float r1[2], r2[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float* st = stat + (two ? 4 * r : 0);
+      r1[r] = st[1], r2[r] = st[3];
+    }
+    stat += 4 * step;
+    F2 d[2][NV][4], n[2][NV][4];
+    float s[2];
+    cp_async_wait(2);  // y and dh
+    {
+      F2 q[2] = {f2(0.0f), f2(0.0f)};
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        F2 w[4];
+        mine.template take<MOE_DTYPE_FP32>(j, sw2, 0.0f, w);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (r && !two) break;
+          mine.template take<S>(j, ring + r * row_bytes, 0.0f, n[r][j]);
+          mine.template take<B>(j, ring + r * row_bytes + at_h, 0.0f, d[r][j]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            n[r][j][k] = n[r][j][k] * f2(r2[r]);
+            a2[j][k] = fma2(d[r][j][k], n[r][j][k], a2[j][k]);
+            d[r][j][k] = d[r][j][k] * w[k];
+            q[r] = fma2(d[r][j][k], n[r][j][k], q[r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 a = split(q[r]);
+        s[r] = a.x + a.y;
+      }
+    }
+    group_sums(s, grp);
+    fetch(k0, more, more_two);  // (the sums have used them)
+    fetch(k1, more, more_two);
+    cp_async_wait(3);  // dy
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float c = s[r] * p.inv_d;
+      if (r && !two) break;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        F2 t[4];
+        mine.template take<S>(j, ring + r * row_bytes + at_d, 0.0f, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          d[r][j][k] = fma2(f2(r2[r]), fma2(n[r][j][k], f2(-c), d[r][j][k]), t[k]);
+          t[k] = f2(p.x_scale) * d[r][j][k];
+          d[r][j][k] = d[r][j][k] * f2(p.o_scale);
+        }
+        mine.template put<S, true>(j, dx + r * dx_ld, t);
+      }
+    }
+    dx += step * dx_ld;
+    cp_async_wait(2);  // o
+    {
+      F2 q[2] = {f2(0.0f), f2(0.0f)};
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        F2 w[4], g[GATE ? 4 : 1];
+        mine.template take<MOE_DTYPE_FP32>(j, sw1, 0.0f, w);
+        if constexpr (GATE) mine.global(j, p.gate, p.pdt, 0.0f, g);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (r && !two) break;
+          mine.template take<B>(j, ring + r * row_bytes + at_o, 0.0f, n[r][j]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            n[r][j][k] = n[r][j][k] * f2(r1[r]);
+            if constexpr (GATE) {
+              ag[j][k] = fma2(d[r][j][k], n[r][j][k] * w[k], ag[j][k]);
+              d[r][j][k] = d[r][j][k] * g[k];
+            }
+            a1[j][k] = fma2(d[r][j][k], n[r][j][k], a1[j][k]);
+            d[r][j][k] = d[r][j][k] * w[k];
+            q[r] = fma2(d[r][j][k], n[r][j][k], q[r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 a = split(q[r]);
+        s[r] = a.x + a.y;
+      }
+    }
+    group_sums(s, grp);
+    fetch(k2, more, more_two);
+    fetch(k3, more, more_two);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float c = s[r] * p.inv_d;
+      if (r && !two) break;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[r][j][k] = f2(r1[r]) * fma2(n[r][j][k], f2(-c), d[r][j][k]);
+        mine.template put<B, true>(j, d_o + r * do_ld, d[r][j]);
+      }
+    }
+    d_o += step * do_ld;
+  }
+  if (!p.sums) return;
+  auto leave = [&](int which, F2 (&a)[NV][4]) {
+    char* to = reinterpret_cast<char*>(p.sums + ((size_t)blockIdx.x * NORM_SUMS + which) * p.D);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) mine.template put<MOE_DTYPE_FP32, true>(j, to, a[j]);
+  };
+  leave(0, a1);
+  leave(2, a2);
+  if constexpr (GATE) leave(4, ag);
+}
+
 cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
   auto by_type = [&](auto s, auto b) {
     constexpr int S = decltype(s)::value, B = decltype(b)::value;
-    auto kernel = p.whole ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, true> : norm_bwd_kernel<2, true, false, S, B, true>)
+    auto kernel = p.whole == 2 ? (gate_sum ? norm_bwd_pairs_kernel<true, S, B> : norm_bwd_pairs_kernel<false, S, B>)
+                  : p.whole ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, true> : norm_bwd_kernel<2, true, false, S, B, true>)
                                      : (gate_sum ? norm_bwd_kernel<2, false, true, S, B, true> : norm_bwd_kernel<2, false, false, S, B, true>))
                   : p.D <= 8192
                       ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, false> : norm_bwd_kernel<2, true, false, S, B, false>)

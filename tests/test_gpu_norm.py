@@ -263,6 +263,14 @@ def test_backward_parts(T, D, kw):
     check_backward(c, backward(c))
 
 
+@pytest.mark.parametrize("T,D,kw", [(1001, 4104, dict()), (1000, 8192, dict(gate="vector")), (777, 6144, dict(stream="fp32", gate="vector")),
+                                    (2001, 7168, dict(stream="fp16", branch="fp16", param="fp16", pad=8, x_scale=0.5)),
+                                    (913, 7168, dict(kind="layer", bias=True, gate="vector")), (1500, 4096, dict(stream="fp32", branch="fp32"))])
+def test_many_rows(T, D, kw):
+    c = Case(T, D, seed=T, **kw)
+    check_backward(c, backward(c))
+
+
 def test_backward_without_dy():
     c = Case(70, 512, seed=6)
     check_backward(c, backward(c, dy=False))
