@@ -203,7 +203,7 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
     fit = fit < use ? fit : use;
     p.stages = (int)(fit < NORM_FWD_STAGES ? fit : NORM_FWD_STAGES);
     p.stage_bytes = (int)row_bytes;
-    p.whole = p.stages == NORM_FWD_STAGES && c.D <= 8192 && p.smem_w && c.post && c.pre && x && o && y && !p.gate;
+    p.whole = p.stages == NORM_FWD_STAGES && c.D <= 8192 && c.D % 512 == 0 && p.smem_w && c.post && c.pre && x && o && y && !p.gate;
     const int64_t ctas = (T + rows - 1) / rows, grid = ctas < pl->num_sms ? ctas : pl->num_sms;
     err = launch_norm_fwd(p, (unsigned)grid, (unsigned)(rows * p.group), rows * p.stages * p.stage_bytes + p.smem_w * w_bytes,
                           (cudaStream_t)stream);
@@ -296,7 +296,7 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
     if (p.stages > rows) p.stages = (int)rows;
     if (p.stages < 1) p.stages = 1;
     p.stage_bytes = (int)row_bytes;
-    p.whole = p.stages == NORM_BWD_STAGES && c.D <= 8192 && c.post && c.pre && dy && dx && d_o && (!p.gate || gate_sum);
+    p.whole = p.stages == NORM_BWD_STAGES && c.D <= 8192 && c.D % 512 == 0 && c.post && c.pre && dy && dx && d_o && (!p.gate || gate_sum);
     size_t smem = (size_t)p.stages * row_bytes;
     if (p.whole && c.kind == MOE_NORM_RMS && c.D > 4096 && T >= 4 * grid && 2 * row_bytes + 8 * c.D <= NORM_SMEM) {
       p.whole = 2;  // two rows at a time, with the weights

@@ -33,8 +33,8 @@ constexpr int norm_fwd_threads(int nv) { return nv <= 2 ? 1024 : 512; }
 
 // Most of a row's instructions are not its arithmetic: looking at what a call has and
 // has not costs more than a hundred of them.  So the kernels have a form (`whole`) for
-// the call between two blocks of a large batch: all rows there, both norms, no gate, as many
-// rows in the ring as these constants say; and one that looks.
+// the call between two blocks of a large batch: all rows there, both norms, no gate (backward:
+// none or one per channel), D a multiple of 512, as many rows in the ring as these constants say; and one that looks.
 constexpr int NORM_FWD_STAGES = 2, NORM_BWD_STAGES = 3;
 
 struct NormParams {
@@ -166,8 +166,8 @@ __device__ __forceinline__ Raw<DT> pack(F2 (&v)[4]) {
   return r;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+__device__ __forceinline__ void cp_async16(char* smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(g) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the `n` newest groups of this thread have landed (n up to 5)
@@ -179,29 +179,27 @@ __device__ __forceinline__ void cp_async_wait(int n) {
   else if (n == 4) asm volatile("cp.async.wait_group 4;" ::: "memory");
   else asm volatile("cp.async.wait_group 5;" ::: "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 q;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
-  return q;
-}
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A thread's vectors: offsets of 16 bytes a vector, and whether they lie in the row.
 // In shared memory vectors of fp32 lie in two planes of 16 bytes each (no bank conflicts).
-template <int NV>
+// ALL: all of all threads' vectors do (choosing between a value and 0 for every element
+// is a third of the instructions otherwise).
+template <int NV, bool ALL>
 struct Mine {
   uint32_t off[NV], plane;
-  bool in[NV];
+  bool in_[NV];
+  __device__ __forceinline__ bool in(int j) const { return ALL || in_[j]; }
   __device__ __forceinline__ Mine(int tid, int nt, int nvec) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) off[j] = (uint32_t)(tid + j * nt) * 16u, in[j] = tid + j * nt < nvec;
+    for (int j = 0; j < NV; ++j) off[j] = (uint32_t)(tid + j * nt) * 16u, in_[j] = tid + j * nt < nvec;
     plane = (uint32_t)nvec * 16u;
   }
   template <int DT>
-  __device__ __forceinline__ void fetch(uint32_t smem, const char* row) const {
+  __device__ __forceinline__ void fetch(char* smem, const char* row) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (in[j]) {
+      if (in(j)) {
         if constexpr (DT == MOE_DTYPE_FP32) {
           cp_async16(smem + off[j], row + 2 * off[j]);
           cp_async16(smem + off[j] + plane, row + 2 * off[j] + 16);
@@ -212,11 +210,11 @@ struct Mine {
   }
   // vector j out of shared memory; outside the row `none`
   template <int DT>
-  __device__ __forceinline__ void take(int j, uint32_t smem, float none, F2 (&v)[4]) const {
-    if (in[j]) {
+  __device__ __forceinline__ void take(int j, const char* smem, float none, F2 (&v)[4]) const {
+    if (in(j)) {
       Raw<DT> r;
-      r.q[0] = lds128(smem + off[j]);
-      if constexpr (DT == MOE_DTYPE_FP32) r.q[1] = lds128(smem + off[j] + plane);
+      r.q[0] = *reinterpret_cast<const uint4*>(smem + off[j]);
+      if constexpr (DT == MOE_DTYPE_FP32) r.q[1] = *reinterpret_cast<const uint4*>(smem + off[j] + plane);
       unpack<DT>(r, v);
     } else {
 #pragma unroll
@@ -226,7 +224,7 @@ struct Mine {
   template <int DT, bool THERE>
   __device__ __forceinline__ void put(int j, char* row, F2 (&v)[4]) const {
     const Raw<DT> r = pack<DT>(v);
-    if ((THERE || row) && in[j]) {
+    if ((THERE || row) && in(j)) {
       uint4* to = reinterpret_cast<uint4*>(row + (DT == MOE_DTYPE_FP32 ? 2 * off[j] : off[j]));
       to[0] = r.q[0];
       if constexpr (DT == MOE_DTYPE_FP32) to[1] = r.q[1];
@@ -234,7 +232,7 @@ struct Mine {
   }
   // vector j in global memory, of a type known now (parameters, a gate's rows)
   __device__ __forceinline__ void global(int j, const void* row, int dt, float none, F2 (&v)[4]) const {
-    if (!in[j]) {
+    if (!in(j)) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = f2(none);
     } else if (dt == MOE_DTYPE_FP32) {
@@ -257,7 +255,7 @@ struct Mine {
       for (int i = 0; i < 4; ++i) v[i] = v[i] + f2(offset);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = f2(in[j] ? 1.0f : 0.0f);
+      for (int i = 0; i < 4; ++i) v[i] = f2(in(j) ? 1.0f : 0.0f);
     }
   }
 };
@@ -301,8 +299,8 @@ __device__ __forceinline__ float both(F2 a, F2 b) {
 // mean (or 0) and 1 / sqrt(mean((v - m)^2) + eps) of one row whose elements
 // outside the row are 0 in v; two passes over the registers, so that a large
 // mean does not cancel
-template <int NV, bool LN>
-__device__ __forceinline__ void row_stats(const Mine<NV>& mine, const F2 (&v)[NV][4], float inv_d, float eps, Group& grp,
+template <int NV, bool LN, bool ALL>
+__device__ __forceinline__ void row_stats(const Mine<NV, ALL>& mine, const F2 (&v)[NV][4], float inv_d, float eps, Group& grp,
                                           float& m, float& r) {
   float s[1];
   F2 q[2] = {f2(0.0f), f2(0.0f)};
@@ -319,7 +317,7 @@ __device__ __forceinline__ void row_stats(const Mine<NV>& mine, const F2 (&v)[NV
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (!LN || mine.in[j])
+    if (!LN || mine.in(j))
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const F2 d = LN ? v[j][i] + f2(-m) : v[j][i];

@@ -33,10 +33,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2 * 2 * NORM_MAX_WARPS];
   const int tid = threadIdx.x;
-  const Mine<NV> mine(tid, blockDim.x, p.nvec);
+  const Mine<NV, W> mine(tid, blockDim.x, p.nvec);
   Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
   // order in the ring: y, dh, dy, o; the gate's rows are read when they are needed
-  const uint32_t ring = smem_u32(smem);
+  char* const ring = smem;
   const uint32_t at_h = pre ? p.D * esize(S) : 0, at_d = at_h + (pre ? p.D * esize(B) : 0), at_o = at_d + (has_dy ? p.D * esize(S) : 0);
   const int64_t row0 = blockIdx.x, step = gridDim.x;
   const int rows = (int)((p.T - row0 + step - 1) / step);
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
                 dgate_step = step * p.dgate_ld * esize(B), gate_step = step * p.gate_ld * esize(B);
   const float* stat = p.stats ? p.stats + 4 * row0 : nullptr;
   grid_dependency_wait();
-  auto fetch = [&](bool on, uint32_t stage) {
+  auto fetch = [&](bool on, char* stage) {
     if (on) {
       if (pre) {
         mine.template fetch<S>(stage, ya);
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   int stage = 0;
 #pragma unroll 1
   for (int i = 0; i < rows; ++i) {
-    const uint32_t at = ring + stage * stage_bytes;
+    char* const at = ring + stage * stage_bytes;
     {
       int next = stage + stages - 1;
       next = next >= stages ? next - stages : next;
@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2 * 2 * NORM_MAX_WARPS];
   const int tid = threadIdx.x;
-  const Mine<NV> mine(tid, blockDim.x, p.nvec);
+  const Mine<NV, true> mine(tid, blockDim.x, p.nvec);
   Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
-  const uint32_t ring = smem_u32(smem);
+  char* const ring = smem;
   const uint32_t at_h = p.D * esize(S), at_d = at_h + p.D * esize(B), at_o = at_d + p.D * esize(S), row_bytes = at_o + p.D * esize(B);
-  const uint32_t sw1 = ring + 2 * row_bytes, sw2 = sw1 + p.D * 4;
+  char *const sw1 = ring + 2 * row_bytes, *const sw2 = sw1 + p.D * 4;
   const int64_t row0 = 2 * (int64_t)blockIdx.x, step = 2 * (int64_t)gridDim.x;
   const int pairs = (int)(((p.T + 1) / 2 - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const char* in[4] = {static_cast<const char*>(p.y) + row0 * p.y_ld * esize(S), static_cast<const char*>(p.dh) + row0 * p.dh_ld * esize(B),
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
   int64_t left = p.T - row0;  // rows from this pair's first on
   auto fetch = [&](auto which, bool on, bool two) {
     constexpr int K = decltype(which)::value, DT = K == 0 || K == 2 ? S : B;
-    const uint32_t at = ring + (K == 0 ? 0 : K == 1 ? at_h : K == 2 ? at_d : at_o);
+    char* const at = ring + (K == 0 ? 0 : K == 1 ? at_h : K == 2 ? at_d : at_o);
     if (on) {
       mine.template fetch<DT>(at, in[K]);
       if (two) mine.template fetch<DT>(at + row_bytes, in[K] + ld[K]);
@@ -281,11 +281,11 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
   fetch(k3, pairs > 0, left > 1);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (mine.in[j]) {  // a thread's own weights into its own places
+    if (mine.in(j)) {  // a thread's own weights into its own places
       F2 w[4];
       mine.weight(j, p.w1, p.pdt, p.w_off, w);
       Raw<MOE_DTYPE_FP32> r = pack<MOE_DTYPE_FP32>(w);
-      char* to = smem + 2 * row_bytes + mine.off[j];
+      char* to = sw1 + mine.off[j];
       *reinterpret_cast<uint4*>(to) = r.q[0], *reinterpret_cast<uint4*>(to + mine.plane) = r.q[1];
       mine.weight(j, p.w2, p.pdt, p.w_off, w);
       r = pack<MOE_DTYPE_FP32>(w);

@@ -19,9 +19,9 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[16 * 2 * 2 * NORM_MAX_WARPS];  // of groups of two warps and more
   const int g = threadIdx.x / p.group, groups = blockDim.x / p.group, tid = threadIdx.x - g * p.group;
-  const Mine<NV> mine(tid, p.group, p.nvec);
+  const Mine<NV, W> mine(tid, p.group, p.nvec);
   Group grp{red + (g & 15) * (2 * 2 * NORM_MAX_WARPS), g, p.group >> 5, tid >> 5, 0};
-  const uint32_t base = smem_u32(smem), ring = base + (uint32_t)(g * stages * stage_bytes);
+  char* const ring = smem + g * stages * stage_bytes;
   const uint32_t at_o = has_x ? p.D * esize(S) : 0, at_g = at_o + (has_o ? p.D * esize(B) : 0);
   // this group's rows, and the pointers that go along with them (`a`: to what is fetched ahead)
   const int64_t row0 = (int64_t)g * gridDim.x + blockIdx.x, step = (int64_t)groups * gridDim.x;
@@ -34,14 +34,14 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   const int64_t xs = step * p.x_ld * esize(S), os = step * p.o_ld * esize(B), gs = step * p.gate_ld * esize(B),
                 ys = has_y ? step * p.y_ld * esize(S) : 0, hs = step * p.h_ld * esize(B);
   grid_dependency_wait();
-  auto fetch_o = [&](bool on, uint32_t stage) {
+  auto fetch_o = [&](bool on, char* stage) {
     if (on && has_o) {
       mine.template fetch<B>(stage + at_o, oa);
       oa += os;
     }
     cp_async_commit();
   };
-  auto fetch_x = [&](bool on, uint32_t stage) {
+  auto fetch_x = [&](bool on, char* stage) {
     if (on) {
       if (has_x) {
         mine.template fetch<S>(stage, xa);
@@ -59,27 +59,27 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
     fetch_x(s < rows, ring + s * stage_bytes);
   }
   // the norms' weights as fp32, once per CTA
-  uint32_t sw1 = 0, sw2 = 0;
+  char *sw1 = nullptr, *sw2 = nullptr;
   if (smem_w) {
-    sw1 = sw2 = base + groups * stages * stage_bytes;
+    sw1 = sw2 = smem + groups * stages * stage_bytes;
     if (post) sw2 += p.D * 4;
 #pragma unroll 1
     for (int i = threadIdx.x; i < 2 * p.nvec; i += blockDim.x) {
       const bool second = i >= p.nvec;
       const int v = second ? i - p.nvec : i;
       if (!(second ? pre : post)) continue;
-      const Mine<1> one(v, 0, p.nvec);
+      const Mine<1, true> one(v, 0, p.nvec);
       F2 w[4];
       one.weight(0, second ? p.w2 : p.w1, p.pdt, p.w_off, w);
       const Raw<MOE_DTYPE_FP32> r = pack<MOE_DTYPE_FP32>(w);
-      char* to = smem + ((second ? sw2 : sw1) - base) + one.off[0];
+      char* to = (second ? sw2 : sw1) + one.off[0];
       *reinterpret_cast<uint4*>(to) = r.q[0];
       *reinterpret_cast<uint4*>(to + one.plane) = r.q[1];
     }
     __syncthreads();
   }
   // vector j of (v - m) r w + c in place
-  auto apply = [&](int j, F2 (&v)[4], float m, float r, uint32_t sw, const void* w, const void* c) {
+  auto apply = [&](int j, F2 (&v)[4], float m, float r, const char* sw, const void* w, const void* c) {
     F2 t[4];
     if (smem_w) mine.template take<MOE_DTYPE_FP32>(j, sw, 0.0f, t);
     else mine.weight(j, w, p.pdt, p.w_off, t);
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   float* stat = p.stats ? p.stats + 4 * row0 : nullptr;
 #pragma unroll 1
   for (int i = 0; i < rows; ++i) {
-    const uint32_t at = ring + stage * stage_bytes;
+    char* const at = ring + stage * stage_bytes;
     const bool more = i + stages < rows;
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     F2 v[NV][4];
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
       }
     }
     if (post) {
-      row_stats<NV, LN>(mine, v, p.inv_d, p.eps, grp, st.x, st.y);
+      row_stats<NV, LN, W>(mine, v, p.inv_d, p.eps, grp, st.x, st.y);
       fetch_o(more, at);  // the sums have used every element of o
     }
     cp_async_wait(2 * stages - (post ? 1 : 2));  // x and the gate
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
       }
       mine.template put<S, W>(j, y, v[j]);
     }
-    if (pre) row_stats<NV, LN>(mine, v, p.inv_d, p.eps, grp, st.z, st.w);
+    if (pre) row_stats<NV, LN, W>(mine, v, p.inv_d, p.eps, grp, st.z, st.w);
     if (!post) fetch_o(more, at);
     fetch_x(more, at);
     if (pre) {
