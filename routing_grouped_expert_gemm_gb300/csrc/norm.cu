@@ -55,16 +55,21 @@ int norm_threads(int64_t D) {
   const int64_t per = 8 * norm_nv(D);
   return (int)(((D + per - 1) / per + 31) / 32 * 32);
 }
-// The backward's CTAs (resident by threads and registers; rows are handed out evenly)
+// The backward's CTAs: resident by threads and registers, but each leaves sums for
+// every column, so not so many that those outweigh the rows (8 a CTA)
 int64_t norm_grid(const moe_norm_plan* pl, int64_t T) {
   int64_t per_sm = 512 / norm_threads(pl->cfg.D);
   per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
+  const int64_t enough = (T + 8 * pl->num_sms - 1) / (8 * pl->num_sms);
+  per_sm = per_sm < enough ? per_sm : enough;
   const int64_t most = per_sm * pl->num_sms;
   return T < most ? T : most;
 }
-// Threads of a CTA where elements are taken one by one: about eight elements each
-int any_threads(int64_t D) {
-  const int64_t n = (D / 8 + 31) / 32 * 32;
+// ... where elements are taken one by one and a row takes longer: two an SM
+int64_t any_grid(const moe_norm_plan* pl, int64_t T) { return T < 2 * pl->num_sms ? T : 2 * pl->num_sms; }
+// Threads of a CTA where elements are taken one by one, `per` elements each
+int any_threads(int64_t D, int per) {
+  const int64_t n = (D / per + 31) / 32 * 32;
   return (int)(n < 64 ? 64 : n > 512 ? 512 : n);
 }
 constexpr int NORM_SMEM = 200 * 1024;  // of an SM's shared memory for the rings
@@ -208,7 +213,7 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
     err = launch_norm_fwd(p, (unsigned)grid, (unsigned)(rows * p.group), rows * p.stages * p.stage_bytes + p.smem_w * w_bytes,
                           (cudaStream_t)stream);
   } else {
-    const int nt = any_threads(c.D);
+    const int nt = any_threads(c.D, 8);
     int64_t per_sm = 1536 / nt;
     const int64_t by_smem = NORM_SMEM / (12 * c.D);
     per_sm = per_sm < by_smem ? per_sm : by_smem < 1 ? 1 : by_smem;
@@ -221,7 +226,8 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
 size_t moe_norm_workspace_bytes(const moe_norm_plan* plan, int64_t T) {
   if (!plan || T < 0) return 0;
   if (T == 0) return 256;
-  return ((size_t)norm_grid(plan, T) * NORM_SUMS * plan->cfg.D * 4 + 255) / 256 * 256;
+  const int64_t a = norm_grid(plan, T), b = any_grid(plan, T);
+  return ((size_t)(a > b ? a : b) * NORM_SUMS * plan->cfg.D * 4 + 255) / 256 * 256;
 }
 
 int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, const float* stats, const void* o,
@@ -286,7 +292,7 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
   p.d_o = d_o, p.do_ld = d_o_stride;
   p.stats = const_cast<float*>(stats);
   p.sums = sums ? static_cast<float*>(workspace) : nullptr;
-  const int64_t grid = norm_grid(pl, T);
+  int64_t grid = norm_grid(pl, T);
   const int64_t row_bytes = c.D * ((c.pre ? norm_size(sd) + norm_size(bd) : 0) + (dy ? norm_size(sd) : 0) + (use_o ? norm_size(bd) : 0));
   cudaError_t err;
   if (vec && row_bytes <= NORM_SMEM) {
@@ -304,8 +310,11 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
     }
     err = launch_norm_bwd(p, gate_sum, (unsigned)grid, (unsigned)norm_threads(c.D), smem, stream);
   } else {
+    grid = any_grid(pl, T);
     p.gate_sum = gate_sum;
-    err = launch_norm_bwd_any(p, (unsigned)grid, (unsigned)any_threads(c.D), stream);
+    p.stages = c.D <= 5120;  // rows of 100 KB in shared memory
+    p.smem_w = c.D <= 2048;  // the sums there too: 80 KB in all
+    err = launch_norm_bwd_any(p, (unsigned)grid, (unsigned)any_threads(c.D, 4), stream);
   }
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   if (sums) {

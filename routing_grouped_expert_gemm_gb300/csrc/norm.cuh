@@ -35,7 +35,7 @@ constexpr int norm_fwd_threads(int nv) { return nv <= 2 ? 1024 : 512; }
 // has not costs more than a hundred of them.  So the kernels have a form (`whole`) for
 // the call between two blocks of a large batch: all rows there, both norms, no gate (backward:
 // none or one per channel), D a multiple of 512, as many rows in the ring as these constants say; and one that looks.
-constexpr int NORM_FWD_STAGES = 2, NORM_BWD_STAGES = 3;
+constexpr int NORM_FWD_STAGES = 2, NORM_BWD_STAGES = 2;
 
 struct NormParams {
   int64_t T;

@@ -95,17 +95,22 @@ __global__ void __launch_bounds__(512) norm_fwd_any_kernel(const NormParams p) {
   }
 }
 
-// The sums over the rows are kept in the CTA's part of the workspace, an element by its own thread.
+// Short rows (p.stages) are fetched whole before anything else; of long ones only the
+// gradient and the normalised input wait in shared memory.  The sums over the rows are
+// kept by the element's own thread: in shared memory where they fit beside the row
+// (p.smem_w), else in the CTA's part of the workspace.
 template <int S, int B, int P>
 __global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormParams p) {
-  extern __shared__ __align__(16) float any_smem[];  // [D] the gradient, then [D] the normalised input
+  extern __shared__ __align__(16) float any_smem[];  // gradient, normalised input, dy, o, gate of the row; sums
   __shared__ float red[2 * 2 * NORM_MAX_WARPS];
-  float *const row_d = any_smem, *const row_n = row_d + p.D;
+  float *const row_d = any_smem, *const row_n = row_d + p.D, *const row_y = row_n + p.D, *const row_o = row_y + p.D,
+        *const row_g = row_o + p.D;
   Group grp{red, 0, (int)blockDim.x >> 5, (int)threadIdx.x >> 5, 0};
   grid_dependency_wait();
-  float* sums = p.sums ? p.sums + (size_t)blockIdx.x * NORM_SUMS * p.D : nullptr;
+  float* const out = p.sums ? p.sums + (size_t)blockIdx.x * NORM_SUMS * p.D : nullptr;
+  float* const sums = out && p.smem_w ? any_smem + 5 * p.D : out;
   auto add = [&](int which, int e, float v, bool first) {
-    float* at = sums + (size_t)which * p.D + e;
+    float* at = sums + which * p.D + e;
     *at = first ? v : *at + v;
   };
 #pragma unroll 1
@@ -114,16 +119,27 @@ __global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormParams p) {
     float st[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (p.stats)
       for (int i = 0; i < 4; ++i) st[i] = p.stats[4 * t + i];
+    // the whole row on its way at once
+    if (p.stages) {
+#pragma unroll 4
+      for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
+        if (p.pre) row_d[e] = load1<B>(p.dh, t * p.dh_ld + e), row_n[e] = load1<S>(p.y, t * p.y_ld + e);
+        if (p.dy) row_y[e] = load1<S>(p.dy, t * p.dy_ld + e);
+        if (p.o) row_o[e] = load1<B>(p.o, t * p.o_ld + e);
+        if (p.gate) row_g[e] = p.gate_rows ? load1<B>(p.gate, t * p.gate_ld + e) : load1<P>(p.gate, e);
+      }
+    }
     float s[2] = {0.0f, 0.0f};
     if (p.pre) {
 #pragma unroll 4
       for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
-        const float d = load1<B>(p.dh, t * p.dh_ld + e), n = (load1<S>(p.y, t * p.y_ld + e) - st[2]) * st[3];
+        const float d = p.stages ? row_d[e] : load1<B>(p.dh, t * p.dh_ld + e);
+        const float n = ((p.stages ? row_n[e] : load1<S>(p.y, t * p.y_ld + e)) - st[2]) * st[3];
+        const float u = d * (p.w2 ? load1<P>(p.w2, e) + p.w_off : 1.0f);
         if (sums) {
           add(2, e, d * n, first);
           if (p.layer) add(3, e, d, first);
         }
-        const float u = d * (p.w2 ? load1<P>(p.w2, e) + p.w_off : 1.0f);
         s[0] = fmaf(u, n, s[0]), s[1] += u;
         row_d[e] = u, row_n[e] = n;
       }
@@ -133,18 +149,18 @@ __global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormParams p) {
     s[0] = s[1] = 0.0f;
 #pragma unroll 4
     for (int e = threadIdx.x; e < p.D; e += blockDim.x) {
-      float d = p.dy ? load1<S>(p.dy, t * p.dy_ld + e) : 0.0f;
+      float d = !p.dy ? 0.0f : p.stages ? row_y[e] : load1<S>(p.dy, t * p.dy_ld + e);
       if (p.pre) d = fmaf(st[3], row_d[e] - row_n[e] * c2 - m2, d);
       if (p.dx) store1<S>(p.dx, t * p.dx_ld + e, p.x_scale * d);
       d *= p.o_scale;
-      float n = p.o ? load1<B>(p.o, t * p.o_ld + e) : 0.0f;
+      float n = !p.o ? 0.0f : p.stages ? row_o[e] : load1<B>(p.o, t * p.o_ld + e);
       if (p.post) n = (n - st[0]) * st[1];
       const float w = p.post && p.w1 ? load1<P>(p.w1, e) + p.w_off : 1.0f;
       if (p.gate) {
         const float z = n * w + (p.post && p.c1 ? load1<P>(p.c1, e) : 0.0f);
         if (p.gate_sum && sums) add(4, e, d * z, first);
         if (p.dgate) store1<B>(p.dgate, t * p.dgate_ld + e, d * z);
-        d *= p.gate_rows ? load1<B>(p.gate, t * p.gate_ld + e) : load1<P>(p.gate, e);
+        d *= p.stages ? row_g[e] : p.gate_rows ? load1<B>(p.gate, t * p.gate_ld + e) : load1<P>(p.gate, e);
       }
       if (p.post) {
         if (sums) {
@@ -166,6 +182,13 @@ __global__ void __launch_bounds__(512) norm_bwd_any_kernel(const NormParams p) {
         for (int e = threadIdx.x; e < p.D; e += blockDim.x) store1<B>(p.d_o, t * p.do_ld + e, st[1] * (row_d[e] - row_n[e] * c1 - m1));
     }
   }
+  if (out && p.smem_w)
+#pragma unroll 1
+    for (int k = 0; k < NORM_SUMS; ++k) {
+      if (k == 4 ? !p.gate_sum : (k & 1 && !p.layer) || !(k < 2 ? p.post : p.pre)) continue;
+#pragma unroll 4
+      for (int e = threadIdx.x; e < p.D; e += blockDim.x) out[(size_t)k * p.D + e] = sums[k * p.D + e];
+    }
 }
 
 namespace {
@@ -193,7 +216,7 @@ cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned thr
 cudaError_t launch_norm_bwd_any(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st) {
   return any_by_type(p, [&](auto s, auto b, auto q) {
     return norm_launch(norm_bwd_any_kernel<decltype(s)::value, decltype(b)::value, decltype(q)::value>, dim3(grid), threads,
-                       (size_t)p.D * 8, st, p);
+                       (size_t)p.D * 4 * (p.smem_w ? 5 + NORM_SUMS : p.stages ? 5 : 2), st, p);
   });
 }
 
