@@ -3,7 +3,7 @@
 #include <new>
 #include <type_traits>
 
-#include "norm.cuh"
+#include "norm_any.cuh"
 
 namespace moe {
 
@@ -65,14 +65,43 @@ int64_t norm_grid(const moe_norm_plan* pl, int64_t T) {
   const int64_t most = per_sm * pl->num_sms;
   return T < most ? T : most;
 }
-// ... where elements are taken one by one and a row takes longer: two an SM
-int64_t any_grid(const moe_norm_plan* pl, int64_t T) { return T < 2 * pl->num_sms ? T : 2 * pl->num_sms; }
-// Threads of a CTA where elements are taken one by one, `per` elements each
-int any_threads(int64_t D, int per) {
-  const int64_t n = (D / per + 31) / 32 * 32;
-  return (int)(n < 64 ? 64 : n > 512 ? 512 : n);
-}
 constexpr int NORM_SMEM = 200 * 1024;  // of an SM's shared memory for the rings
+
+// Rows off vectors: threads of a CTA (`per` elements each), CTAs of the backward at most
+// (each leaves sums, so eight rows a CTA where there are more than two CTAs an SM), and a
+// call's threads, ring and grid
+int any_threads(int64_t D, int per) { return (int)(((D + per - 1) / per + 31) / 32 * 32); }
+int64_t any_bwd_grid(const moe_norm_plan* pl, int64_t T) {
+  const int64_t n = T / 8 > 2 * pl->num_sms ? T / 8 : 2 * pl->num_sms, all = (int64_t)ANY_MAX_CTAS * pl->num_sms;
+  const int64_t most = n < all ? n : all;
+  return most < T ? most : T;
+}
+struct AnyCall {
+  int64_t grid;
+  int threads;
+  size_t smem;
+};
+// row_bytes: of a row's tensors in the ring; params: vectors of parameters
+AnyCall any_call(const moe_norm_plan* pl, NormParams& p, int per, int64_t row_bytes, int params, int64_t most) {
+  const int threads = any_threads(p.D, per);
+  const int64_t need = (p.T + pl->num_sms - 1) / pl->num_sms, w = params * 4 * (int64_t)p.D;
+  int64_t per_sm = ANY_RESIDENT / threads;  // 0: too wide
+  per_sm = per_sm < ANY_MAX_CTAS ? per_sm : ANY_MAX_CTAS;
+  per_sm = per_sm < need ? per_sm : need;
+  p.stage_bytes = (int)row_bytes;
+  for (; per_sm >= 1; --per_sm) {
+    int64_t grid = per_sm * pl->num_sms;
+    grid = grid < most ? grid : most;
+    const int64_t rows = (p.T + grid - 1) / grid, room = NORM_SMEM / per_sm - 1024;
+    int64_t fit = room > w ? (room - w) / row_bytes : 0;
+    if (fit < (rows < 2 ? rows : 2)) continue;
+    fit = fit < rows ? fit : rows;
+    p.stages = (int)(fit < ANY_STAGES ? fit : ANY_STAGES);
+    return {grid, threads, (size_t)(p.stages * row_bytes + w)};
+  }
+  p.stages = 0;
+  return {pl->num_sms < most ? pl->num_sms : most, any_threads(p.D, ANY_WIDE), 0};
+}
 
 // A row tensor of a call: elements aligned, strides in range
 bool norm_rows_ok(const void* p, int64_t& ld, int64_t D, int dt, int64_t T) {
@@ -213,12 +242,10 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
     err = launch_norm_fwd(p, (unsigned)grid, (unsigned)(rows * p.group), rows * p.stages * p.stage_bytes + p.smem_w * w_bytes,
                           (cudaStream_t)stream);
   } else {
-    const int nt = any_threads(c.D, 8);
-    int64_t per_sm = 1536 / nt;
-    const int64_t by_smem = NORM_SMEM / (12 * c.D);
-    per_sm = per_sm < by_smem ? per_sm : by_smem < 1 ? 1 : by_smem;
-    const int64_t most = per_sm * pl->num_sms, grid = T < most ? T : most;
-    err = launch_norm_fwd_any(p, (unsigned)grid, (unsigned)nt, (cudaStream_t)stream);
+    const int64_t slot = (o ? any_slot(c.D, c.branch_dtype) : 0) + (x ? any_slot(c.D, c.stream_dtype) : 0) +
+                         (p.gate_rows ? any_slot(c.D, c.branch_dtype) : 0);
+    const AnyCall a = any_call(pl, p, ANY_FWD, slot, c.post + c.pre + (p.c1 != nullptr) + (p.c2 != nullptr) + (p.gate && !p.gate_rows), T);
+    err = launch_norm_fwd_any(p, (unsigned)a.grid, (unsigned)a.threads, a.smem, (cudaStream_t)stream);
   }
   return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -226,7 +253,7 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
 size_t moe_norm_workspace_bytes(const moe_norm_plan* plan, int64_t T) {
   if (!plan || T < 0) return 0;
   if (T == 0) return 256;
-  const int64_t a = norm_grid(plan, T), b = any_grid(plan, T);
+  const int64_t a = norm_grid(plan, T), b = any_bwd_grid(plan, T);
   return ((size_t)(a > b ? a : b) * NORM_SUMS * plan->cfg.D * 4 + 255) / 256 * 256;
 }
 
@@ -310,11 +337,11 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
     }
     err = launch_norm_bwd(p, gate_sum, (unsigned)grid, (unsigned)norm_threads(c.D), smem, stream);
   } else {
-    grid = any_grid(pl, T);
-    p.gate_sum = gate_sum;
-    p.stages = c.D <= 5120;  // rows of 100 KB in shared memory
-    p.smem_w = c.D <= 2048;  // the sums there too: 80 KB in all
-    err = launch_norm_bwd_any(p, (unsigned)grid, (unsigned)any_threads(c.D, 4), stream);
+    const int64_t slot = (c.pre ? any_slot(c.D, sd) + any_slot(c.D, bd) : 0) + (dy ? any_slot(c.D, sd) : 0) +
+                         (use_o ? any_slot(c.D, bd) : 0) + (p.gate_rows ? any_slot(c.D, bd) : 0) + (stats ? any_slot(4, MOE_DTYPE_FP32) : 0);
+    const AnyCall a = any_call(pl, p, any_bwd_per(c.D), slot, c.post + c.pre + (p.gate ? (p.c1 != nullptr) + !p.gate_rows : 0), any_bwd_grid(pl, T));
+    grid = a.grid;
+    err = launch_norm_bwd_any(p, (unsigned)grid, (unsigned)a.threads, a.smem, stream);
   }
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   if (sums) {

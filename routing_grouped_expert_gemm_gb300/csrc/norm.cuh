@@ -1,5 +1,5 @@
 // Shared by the kernels of the norms around a block (norm.cu, norm_fwd.cu, norm_bwd.cu,
-// norm_any.cu): parameters, packed fp32 arithmetic, rows in vectors, sums.
+// norm_any_fwd.cu, norm_any_bwd.cu): parameters, packed fp32 arithmetic, rows in vectors, sums.
 //
 //   z = N(o),  y = a x + b g z,  h = N(y),   N(v) = (v - m) r w + c,
 //   r = 1 / sqrt(mean((v - m)^2) + eps),  m = mean(v) or 0.
@@ -60,9 +60,9 @@ struct NormParams {
 // Fast kernels: rows in whole vectors on 16-byte boundaries
 cudaError_t launch_norm_fwd(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
-// Any rows (norm_any.cu)
-cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st);
-cudaError_t launch_norm_bwd_any(const NormParams& p, unsigned grid, unsigned threads, cudaStream_t st);
+// Any rows (norm_any_fwd.cu, norm_any_bwd.cu)
+cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
+cudaError_t launch_norm_bwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 
 template <typename P>
 cudaError_t norm_launch(void (*kernel)(P), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const P& p) {
@@ -267,25 +267,25 @@ struct Group {
 };
 // Sums of N values over the group, every thread getting the same bits.  `red`
 // alternates between two buffers, so that one barrier a call is enough.
-template <int N>
+template <int N, int MAX_WARPS = NORM_MAX_WARPS>
 __device__ __forceinline__ void group_sums(float (&v)[N], Group& g) {
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
   if (g.warps == 1) return;
-  float* r = g.red + g.turn * (2 * NORM_MAX_WARPS);
+  float* r = g.red + g.turn * (2 * MAX_WARPS);
   g.turn ^= 1;
   const int lane = threadIdx.x & 31;
   if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i * NORM_MAX_WARPS + g.warp] = v[i];
+    for (int i = 0; i < N; ++i) r[i * MAX_WARPS + g.warp] = v[i];
   named_bar_sync(g.id, g.warps * 32);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < g.warps ? r[i * NORM_MAX_WARPS + lane] : 0.0f;
-  // (at most 16 warps: the upper half of the lanes adds zeros)
+  for (int i = 0; i < N; ++i) v[i] = lane < g.warps ? r[i * MAX_WARPS + lane] : 0.0f;
+  // (of at most 16 warps the upper half of the lanes would add zeros)
 #pragma unroll
-  for (int m = 8; m >= 1; m >>= 1)
+  for (int m = MAX_WARPS / 2; m >= 1; m >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
 #pragma unroll
