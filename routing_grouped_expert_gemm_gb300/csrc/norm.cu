@@ -55,6 +55,8 @@ int norm_threads(int64_t D) {
   const int64_t per = 8 * norm_nv(D);
   return (int)(((D + per - 1) / per + 31) / 32 * 32);
 }
+// ... and the vectors' places in a ring, as elements
+int64_t norm_places(int64_t D) { return (int64_t)norm_threads(D) * 8 * norm_nv(D); }
 // The backward's CTAs: resident by threads and registers, but each leaves sums for
 // every column, so not so many that those outweigh the rows (8 a CTA)
 int64_t norm_grid(const moe_norm_plan* pl, int64_t T) {
@@ -94,13 +96,17 @@ AnyCall any_call(const moe_norm_plan* pl, NormParams& p, int per, int64_t row_by
     grid = grid < most ? grid : most;
     const int64_t rows = (p.T + grid - 1) / grid, room = NORM_SMEM / per_sm - 1024;
     int64_t fit = room > w ? (room - w) / row_bytes : 0;
-    if (fit < (rows < 2 ? rows : 2)) continue;
+    p.smem_w = fit >= (rows < 2 ? rows : 2);
+    if (!p.smem_w) {
+      if (per_sm > 1) continue;
+      fit = room / row_bytes;  // at least 1: 8192 elements of 20 bytes
+    }
     fit = fit < rows ? fit : rows;
     p.stages = (int)(fit < ANY_STAGES ? fit : ANY_STAGES);
-    return {grid, threads, (size_t)(p.stages * row_bytes + w)};
+    return {grid, p.smem_w ? threads : any_threads(p.D, any_wide(ANY_ROWS)), (size_t)(p.stages * row_bytes + p.smem_w * w)};
   }
   p.stages = 0;
-  return {pl->num_sms < most ? pl->num_sms : most, any_threads(p.D, ANY_WIDE), 0};
+  return {pl->num_sms < most ? pl->num_sms : most, any_threads(p.D, any_wide(ANY_NONE)), 0};
 }
 
 // A row tensor of a call: elements aligned, strides in range
@@ -118,6 +124,7 @@ int norm_params(const moe_norm_plan* pl, const moe_norm_params* q, int64_t T, No
   p.T = T;
   p.D = (int)c.D;
   p.nvec = (int)(c.D / 8);
+  p.places = (int)norm_places(c.D);
   p.layer = c.kind == MOE_NORM_LAYER;
   p.post = c.post;
   p.pre = c.pre;
@@ -221,9 +228,9 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
   p.stats = stats;
   // rows at a time on a CTA, fewer where the rows' ring or the batch do not ask for them
   p.group = norm_threads(c.D);
-  const int64_t row_bytes = c.D * ((x ? norm_size(c.stream_dtype) : 0) + (o ? norm_size(c.branch_dtype) : 0) +
+  const int64_t row_bytes = norm_places(c.D) * ((x ? norm_size(c.stream_dtype) : 0) + (o ? norm_size(c.branch_dtype) : 0) +
                                    (p.gate_rows ? norm_size(c.branch_dtype) : 0));
-  const int64_t w_bytes = c.D * 4 * (c.post + c.pre);
+  const int64_t w_bytes = norm_places(c.D) * 4 * (c.post + c.pre);
   int64_t rows = norm_fwd_threads(norm_nv(c.D)) / p.group, need = (T + pl->num_sms - 1) / pl->num_sms;
   rows = rows < need ? rows : need;
   cudaError_t err;
@@ -237,7 +244,8 @@ int moe_norm(const moe_norm_plan* pl, int64_t T, const moe_norm_params* params, 
     fit = fit < use ? fit : use;
     p.stages = (int)(fit < NORM_FWD_STAGES ? fit : NORM_FWD_STAGES);
     p.stage_bytes = (int)row_bytes;
-    p.whole = p.stages == NORM_FWD_STAGES && c.D <= 8192 && c.D % 512 == 0 && p.smem_w && c.post && c.pre && x && o && y && !p.gate;
+    p.whole = p.stages == NORM_FWD_STAGES && c.D <= 8192 && p.smem_w && c.post && c.pre && x && o && y && !p.gate;
+    if (p.whole && c.D % 512 == 0) p.whole = 2;
     const int64_t ctas = (T + rows - 1) / rows, grid = ctas < pl->num_sms ? ctas : pl->num_sms;
     err = launch_norm_fwd(p, (unsigned)grid, (unsigned)(rows * p.group), rows * p.stages * p.stage_bytes + p.smem_w * w_bytes,
                           (cudaStream_t)stream);
@@ -320,7 +328,7 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
   p.stats = const_cast<float*>(stats);
   p.sums = sums ? static_cast<float*>(workspace) : nullptr;
   int64_t grid = norm_grid(pl, T);
-  const int64_t row_bytes = c.D * ((c.pre ? norm_size(sd) + norm_size(bd) : 0) + (dy ? norm_size(sd) : 0) + (use_o ? norm_size(bd) : 0));
+  const int64_t row_bytes = norm_places(c.D) * ((c.pre ? norm_size(sd) + norm_size(bd) : 0) + (dy ? norm_size(sd) : 0) + (use_o ? norm_size(bd) : 0));
   cudaError_t err;
   if (vec && row_bytes <= NORM_SMEM) {
     // rows of the ring
@@ -329,13 +337,16 @@ int moe_norm_bwd(const moe_norm_plan* pl, int64_t T, const moe_norm_params* para
     if (p.stages > rows) p.stages = (int)rows;
     if (p.stages < 1) p.stages = 1;
     p.stage_bytes = (int)row_bytes;
-    p.whole = p.stages == NORM_BWD_STAGES && c.D <= 8192 && c.D % 512 == 0 && c.post && c.pre && dy && dx && d_o && (!p.gate || gate_sum);
+    p.whole = p.stages == NORM_BWD_STAGES && c.D <= 8192 && c.post && c.pre && dy && dx && d_o && (!p.gate || gate_sum);
     size_t smem = (size_t)p.stages * row_bytes;
-    if (p.whole && c.kind == MOE_NORM_RMS && c.D > 4096 && T >= 4 * grid && 2 * row_bytes + 8 * c.D <= NORM_SMEM) {
-      p.whole = 2;  // two rows at a time, with the weights
-      smem = (size_t)(2 * row_bytes + 8 * c.D);
+    bool pairs = false;
+    const size_t pair_bytes = 2 * row_bytes + 8 * norm_places(c.D);
+    if (p.whole && c.kind == MOE_NORM_RMS && c.D > 4096 && T >= 4 * grid && pair_bytes <= NORM_SMEM) {
+      pairs = true;  // two rows at a time, with the weights
+      smem = pair_bytes;
     }
-    err = launch_norm_bwd(p, gate_sum, (unsigned)grid, (unsigned)norm_threads(c.D), smem, stream);
+    if (p.whole && c.D % 512 == 0) p.whole = 2;
+    err = launch_norm_bwd(p, gate_sum, pairs, (unsigned)grid, (unsigned)norm_threads(c.D), smem, stream);
   } else {
     const int64_t slot = (c.pre ? any_slot(c.D, sd) + any_slot(c.D, bd) : 0) + (dy ? any_slot(c.D, sd) : 0) +
                          (use_o ? any_slot(c.D, bd) : 0) + (p.gate_rows ? any_slot(c.D, bd) : 0) + (stats ? any_slot(4, MOE_DTYPE_FP32) : 0);

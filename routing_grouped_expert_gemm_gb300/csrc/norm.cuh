@@ -32,9 +32,11 @@ constexpr int NORM_SUMS = 5;        // dw and dc of both norms, dg
 constexpr int norm_fwd_threads(int nv) { return nv <= 2 ? 1024 : 512; }
 
 // Most of a row's instructions are not its arithmetic: looking at what a call has and
-// has not costs more than a hundred of them.  So the kernels have a form (`whole`) for
-// the call between two blocks of a large batch: all rows there, both norms, no gate (backward:
-// none or one per channel), D a multiple of 512, as many rows in the ring as these constants say; and one that looks.
+// has not costs more than a hundred of them.  So the kernels have a form (`whole` 1) for
+// the call between two blocks of a large batch: all rows there, both norms, no gate
+// (backward: none or one per channel), as many rows in the ring as these constants say;
+// one (2) where besides every thread's vectors lie in the row (D a multiple of 512); and
+// one that looks.
 constexpr int NORM_FWD_STAGES = 2, NORM_BWD_STAGES = 2;
 
 struct NormParams {
@@ -44,7 +46,7 @@ struct NormParams {
   int group;       // forward: threads that share a row (a CTA's are that many times its rows at a time)
   int smem_w;      // forward: the weights in shared memory
   int stages;      // rows in the ring
-  int whole, gate_sum;
+  int whole, places;  // places: elements of a row in the ring, 8 for every vector of every thread
   int stage_bytes; // of a row in the ring
   float inv_d, eps, w_off, x_scale, o_scale;
   const void *w1, *c1, *w2, *c2, *gate;
@@ -59,7 +61,7 @@ struct NormParams {
 
 // Fast kernels: rows in whole vectors on 16-byte boundaries
 cudaError_t launch_norm_fwd(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
-cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, bool pairs, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 // Any rows (norm_any_fwd.cu, norm_any_bwd.cu)
 cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 cudaError_t launch_norm_bwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
@@ -183,17 +185,25 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 
 // A thread's vectors: offsets of 16 bytes a vector, and whether they lie in the row.
 // In shared memory vectors of fp32 lie in two planes of 16 bytes each (no bank conflicts).
-// ALL: all of all threads' vectors do (choosing between a value and 0 for every element
-// is a third of the instructions otherwise).
+// Choosing between a value and 0 for every element would be a third of the instructions:
+// ALL: all of all threads' vectors lie in the row; else the ring has places for those
+// outside too, and they hold zeros.
 template <int NV, bool ALL>
 struct Mine {
   uint32_t off[NV], plane;
   bool in_[NV];
   __device__ __forceinline__ bool in(int j) const { return ALL || in_[j]; }
-  __device__ __forceinline__ Mine(int tid, int nt, int nvec) {
+  __device__ __forceinline__ Mine(int tid, int nt, int nvec, int places) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) off[j] = (uint32_t)(tid + j * nt) * 16u, in_[j] = tid + j * nt < nvec;
-    plane = (uint32_t)nvec * 16u;
+    plane = ALL ? (uint32_t)nvec * 16u : (uint32_t)places * 2u;
+  }
+  // once: zeros in this thread's places outside the row, in every 16 bytes of all vectors'
+  __device__ __forceinline__ void clear(char* stage, uint32_t stage_bytes) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (!in(j))
+        for (uint32_t at = off[j]; at < stage_bytes; at += plane) *reinterpret_cast<uint4*>(stage + at) = make_uint4(0, 0, 0, 0);
   }
   template <int DT>
   __device__ __forceinline__ void fetch(char* smem, const char* row) const {
@@ -208,18 +218,13 @@ struct Mine {
         }
       }
   }
-  // vector j out of shared memory; outside the row `none`
+  // vector j out of shared memory; 0 outside the row
   template <int DT>
-  __device__ __forceinline__ void take(int j, const char* smem, float none, F2 (&v)[4]) const {
-    if (in(j)) {
-      Raw<DT> r;
-      r.q[0] = *reinterpret_cast<const uint4*>(smem + off[j]);
-      if constexpr (DT == MOE_DTYPE_FP32) r.q[1] = *reinterpret_cast<const uint4*>(smem + off[j] + plane);
-      unpack<DT>(r, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = f2(none);
-    }
+  __device__ __forceinline__ void take(int j, const char* smem, F2 (&v)[4]) const {
+    Raw<DT> r;
+    r.q[0] = *reinterpret_cast<const uint4*>(smem + off[j]);
+    if constexpr (DT == MOE_DTYPE_FP32) r.q[1] = *reinterpret_cast<const uint4*>(smem + off[j] + plane);
+    unpack<DT>(r, v);
   }
   template <int DT, bool THERE>
   __device__ __forceinline__ void put(int j, char* row, F2 (&v)[4]) const {

@@ -1,5 +1,7 @@
 // Forward of the norms around a block for rows off vectors (norm_any.cuh).
-// 1003 x 2053 in fp16 with a gate per row: ANYFWD.
+// 1003 x 2053 layer norms in fp16 with a gate per row: 18.4 us; in
+// vectors, rows of 2056 take 70%.  An element's own instructions bound it, hence the elements of
+// a thread in arrays that are read and written without a branch between (22 us with them).
 #include "norm_any.cuh"
 
 namespace moe {
@@ -22,9 +24,8 @@ __device__ __forceinline__ void any_stats(const NormParams& p, const float (&v)[
   r = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
 }
 
-template <int NE, bool LN, int S, int B>
+template <int MODE, int NE, bool LN, int S, int B>
 __global__ void __launch_bounds__(1024) norm_fwd_any_kernel(const NormParams p) {
-  constexpr bool RING = NE != ANY_WIDE;
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2 * 2 * ANY_MAX_WARPS];
   const int tid = threadIdx.x, nt = blockDim.x;
@@ -33,14 +34,14 @@ __global__ void __launch_bounds__(1024) norm_fwd_any_kernel(const NormParams p) 
   const AnyRows ro(p.o, p.o_ld, p.D, B, end), rx(p.x, p.x_ld, p.D, S, end), rg(p.gate_rows ? p.gate : nullptr, p.gate_ld, p.D, B, end);
   auto fetch = [&](char* stage, int64_t t) { ro.fetch(stage, t), rx.fetch(stage, t), rg.fetch(stage, t); };
   grid_dependency_wait();
-  if (RING) any_first(p, smem, fetch);
+  if (MODE != ANY_NONE) any_first(p, smem, fetch);
   char* room = smem + p.stages * p.stage_bytes;
-  const AnyParam<RING> w1(p, p.w1, p.w_off, p.post, room), w2(p, p.w2, p.w_off, p.pre, room), c1(p, p.c1, 0.0f, false, room),
+  const AnyParam<MODE> w1(p, p.w1, p.w_off, p.post, room), w2(p, p.w2, p.w_off, p.pre, room), c1(p, p.c1, 0.0f, false, room),
       c2(p, p.c2, 0.0f, false, room), gate(p, p.gate_rows ? nullptr : p.gate, 0.0f, false, room);
-  any_rows<RING>(p, smem, fetch, [&](const char* stage, int64_t t) {
+  any_rows<MODE>(p, smem, fetch, [&](const char* stage, int64_t t) {
     float v[NE], a[NE], m[2] = {0.0f, 0.0f}, r[2] = {0.0f, 0.0f};
     // (v - m) r w + c
-    auto apply = [&](float m, float r, const AnyParam<RING>& w, const AnyParam<RING>& c, bool biased) {
+    auto apply = [&](float m, float r, const AnyParam<MODE>& w, const AnyParam<MODE>& c, bool biased) {
       w.mine(p.D, a);
 #pragma unroll
       for (int j = 0; j < NE; ++j) v[j] = (v[j] - m) * r * a[j];
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_any_kernel(const NormParams p) 
       }
     };
     if (p.o) {
-      load_mine<B>(ro.row<RING>(stage, t), p.D, v);
+      load_mine<B>(ro.row<MODE>(stage, t), p.D, v);
     } else {
 #pragma unroll
       for (int j = 0; j < NE; ++j) v[j] = 0.0f;
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_any_kernel(const NormParams p) 
       apply(m[0], r[0], w1, c1, p.c1);
     }
     if (p.gate) {
-      if (p.gate_rows) load_mine<B>(rg.row<RING>(stage, t), p.D, a);
+      if (p.gate_rows) load_mine<B>(rg.row<MODE>(stage, t), p.D, a);
       else gate.mine(p.D, a);
 #pragma unroll
       for (int j = 0; j < NE; ++j) v[j] *= a[j];
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_any_kernel(const NormParams p) 
 #pragma unroll
     for (int j = 0; j < NE; ++j) v[j] *= p.o_scale;
     if (p.x) {
-      load_mine<S>(rx.row<RING>(stage, t), p.D, a);
+      load_mine<S>(rx.row<MODE>(stage, t), p.D, a);
 #pragma unroll
       for (int j = 0; j < NE; ++j) v[j] = fmaf(p.x_scale, a[j], v[j]);
     }
@@ -93,9 +94,10 @@ __global__ void __launch_bounds__(1024) norm_fwd_any_kernel(const NormParams p) 
 cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
   return any_by_type(p, [&](auto s, auto b) {
     constexpr int S = decltype(s)::value, B = decltype(b)::value;
-    auto kernel = !p.stages ? norm_fwd_any_kernel<ANY_WIDE, true, S, B>
-                  : p.layer ? norm_fwd_any_kernel<ANY_FWD, true, S, B>
-                            : norm_fwd_any_kernel<ANY_FWD, false, S, B>;
+    auto kernel = !p.stages   ? norm_fwd_any_kernel<ANY_NONE, any_wide(ANY_NONE), true, S, B>
+                  : !p.smem_w ? norm_fwd_any_kernel<ANY_ROWS, any_wide(ANY_ROWS), true, S, B>
+                  : p.layer   ? norm_fwd_any_kernel<ANY_ALL, ANY_FWD, true, S, B>
+                              : norm_fwd_any_kernel<ANY_ALL, ANY_FWD, false, S, B>;
     return norm_launch(kernel, dim3(grid), threads, smem, st, p);
   });
 }

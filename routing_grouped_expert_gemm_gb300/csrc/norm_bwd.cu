@@ -1,5 +1,5 @@
 // Backward of the norms around a block, rows in whole vectors (norm.cuh has the
-// formulas).  16384 x 7168 in bf16: BWDTIME, BWDSHARE of the copy rate.
+// formulas).  16384 x 7168 in bf16: 230 us, 90% of the copy rate.
 //
 // A CTA keeps to its own rows, a thread to its own columns: the sums over the rows (dw
 // and dc of both norms, dg) and the norms' weights stay in its registers, and leave
@@ -24,7 +24,7 @@ struct NormBack {
   }
 };
 
-template <int NV, bool LN, bool GATE, int S, int B, bool W>
+template <int NV, bool LN, bool GATE, int S, int B, int W /* whole */>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   const bool pre = W || p.pre, post = W || p.post, has_dy = W || p.dy, has_o = W || p.o, gated = GATE || (!W && p.gate),
              gate_rows = !W && p.gate_rows, has_dx = W || p.dx, has_do = W || p.d_o, has_dgate = !W && p.dgate;
@@ -33,11 +33,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2 * 2 * NORM_MAX_WARPS];
   const int tid = threadIdx.x;
-  const Mine<NV, W> mine(tid, blockDim.x, p.nvec);
+  const int row = W == 2 ? p.D : p.places;  // elements of a row in the ring
+  const Mine<NV, W == 2> mine(tid, blockDim.x, p.nvec, row);
   Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
   // order in the ring: y, dh, dy, o; the gate's rows are read when they are needed
   char* const ring = smem;
-  const uint32_t at_h = pre ? p.D * esize(S) : 0, at_d = at_h + (pre ? p.D * esize(B) : 0), at_o = at_d + (has_dy ? p.D * esize(S) : 0);
+  const uint32_t at_h = pre ? row * esize(S) : 0, at_d = at_h + (pre ? row * esize(B) : 0), at_o = at_d + (has_dy ? row * esize(S) : 0);
   const int64_t row0 = blockIdx.x, step = gridDim.x;
   const int rows = (int)((p.T - row0 + step - 1) / step);
   auto at_row = [&](const void* v, int64_t ld, int size) { return v ? static_cast<const char*>(v) + row0 * ld * size : nullptr; };
@@ -69,6 +70,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
     }
     cp_async_commit();
   };
+  if constexpr (W != 2)
+    for (int s = 0; s < stages; ++s) mine.clear(ring + s * stage_bytes, stage_bytes);
   for (int s = 0; s + 1 < stages; ++s) fetch(s < rows, ring + s * stage_bytes);
   F2 w1[KEEP ? NV : 1][4], w2[KEEP ? NV : 1][4];
   if constexpr (KEEP)
@@ -121,8 +124,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         F2 w[4];
-        mine.template take<S>(j, at, st.z, n[j]);
-        mine.template take<B>(j, at + at_h, 0.0f, u[j]);
+        mine.template take<S>(j, at, n[j]);
+        mine.template take<B>(j, at + at_h, u[j]);
         if constexpr (!KEEP) mine.weight(j, p.w2, p.pdt, p.w_off, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (has_dy) {
-          mine.template take<S>(j, at + at_d, 0.0f, d[j]);
+          mine.template take<S>(j, at + at_d, d[j]);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) d[j][k] = f2(0.0f);
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) mine.template take<S>(j, at + at_d, 0.0f, d[j]);
+      for (int j = 0; j < NV; ++j) mine.template take<S>(j, at + at_d, d[j]);
     }
     F2 q[2] = {f2(0.0f), f2(0.0f)}, e = f2(0.0f);
 #pragma unroll
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) d[j][k] = d[j][k] * f2(p.o_scale);
       if (has_o) {
-        mine.template take<B>(j, at + at_o, post ? st.x : 0.0f, n[j]);
+        mine.template take<B>(j, at + at_o, n[j]);
         if (post)
 #pragma unroll
           for (int k = 0; k < 4; ++k) n[j][k] = (LN ? n[j][k] + f2(-st.x) : n[j][k]) * f2(st.y);
@@ -236,20 +239,21 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p) {
 }
 
 // The whole call's rms form for long rows, of which an SM has room for one CTA: two rows
-// at a time, so that one's arithmetic fills the other's barriers, the weights in shared
-// memory to make registers for them.  One place a tensor and row in the ring, filled
+// at a time, so that one's arithmetic fills the other's barriers (335 -> 291 us where it
+// was taken), the weights in shared memory to make registers for them.  One place a tensor and row in the ring, filled
 // again as soon as it has been read.
-template <bool GATE, int S, int B>
+template <bool GATE, int S, int B, bool ALL>
 __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p) {
   constexpr int NV = 2;
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[2 * 2 * NORM_MAX_WARPS];
   const int tid = threadIdx.x;
-  const Mine<NV, true> mine(tid, blockDim.x, p.nvec);
+  const int row = ALL ? p.D : p.places;
+  const Mine<NV, ALL> mine(tid, blockDim.x, p.nvec, row);
   Group grp{red, 0, (int)blockDim.x >> 5, tid >> 5, 0};
   char* const ring = smem;
-  const uint32_t at_h = p.D * esize(S), at_d = at_h + p.D * esize(B), at_o = at_d + p.D * esize(S), row_bytes = at_o + p.D * esize(B);
-  char *const sw1 = ring + 2 * row_bytes, *const sw2 = sw1 + p.D * 4;
+  const uint32_t at_h = row * esize(S), at_d = at_h + row * esize(B), at_o = at_d + row * esize(S), row_bytes = at_o + row * esize(B);
+  char *const sw1 = ring + 2 * row_bytes, *const sw2 = sw1 + row * 4;
   const int64_t row0 = 2 * (int64_t)blockIdx.x, step = 2 * (int64_t)gridDim.x;
   const int pairs = (int)(((p.T + 1) / 2 - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const char* in[4] = {static_cast<const char*>(p.y) + row0 * p.y_ld * esize(S), static_cast<const char*>(p.dh) + row0 * p.dh_ld * esize(B),
@@ -275,13 +279,14 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
   constexpr std::integral_constant<int, 1> k1{};
   constexpr std::integral_constant<int, 2> k2{};
   constexpr std::integral_constant<int, 3> k3{};
+  if constexpr (!ALL) mine.clear(ring, 2 * row_bytes);
   fetch(k0, pairs > 0, left > 1);
   fetch(k1, pairs > 0, left > 1);
   fetch(k2, pairs > 0, left > 1);
   fetch(k3, pairs > 0, left > 1);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
-    if (mine.in(j)) {  // a thread's own weights into its own places
+    {  // a thread's own weights into its own places
       F2 w[4];
       mine.weight(j, p.w1, p.pdt, p.w_off, w);
       Raw<MOE_DTYPE_FP32> r = pack<MOE_DTYPE_FP32>(w);
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
       *reinterpret_cast<uint4*>(to) = r.q[0], *reinterpret_cast<uint4*>(to + mine.plane) = r.q[1];
       mine.weight(j, p.w2, p.pdt, p.w_off, w);
       r = pack<MOE_DTYPE_FP32>(w);
-      to += p.D * 4;
+      to += row * 4;
       *reinterpret_cast<uint4*>(to) = r.q[0], *reinterpret_cast<uint4*>(to + mine.plane) = r.q[1];
     }
   F2 a1[NV][4], a2[NV][4], ag[GATE ? NV : 1][4];
@@ -319,12 +324,12 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         F2 w[4];
-        mine.template take<MOE_DTYPE_FP32>(j, sw2, 0.0f, w);
+        mine.template take<MOE_DTYPE_FP32>(j, sw2, w);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if (r && !two) break;
-          mine.template take<S>(j, ring + r * row_bytes, 0.0f, n[r][j]);
-          mine.template take<B>(j, ring + r * row_bytes + at_h, 0.0f, d[r][j]);
+          mine.template take<S>(j, ring + r * row_bytes, n[r][j]);
+          mine.template take<B>(j, ring + r * row_bytes + at_h, d[r][j]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             n[r][j][k] = n[r][j][k] * f2(r2[r]);
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         F2 t[4];
-        mine.template take<S>(j, ring + r * row_bytes + at_d, 0.0f, t);
+        mine.template take<S>(j, ring + r * row_bytes + at_d, t);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           d[r][j][k] = fma2(f2(r2[r]), fma2(n[r][j][k], f2(-c), d[r][j][k]), t[k]);
@@ -368,12 +373,12 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         F2 w[4], g[GATE ? 4 : 1];
-        mine.template take<MOE_DTYPE_FP32>(j, sw1, 0.0f, w);
+        mine.template take<MOE_DTYPE_FP32>(j, sw1, w);
         if constexpr (GATE) mine.global(j, p.gate, p.pdt, 0.0f, g);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if (r && !two) break;
-          mine.template take<B>(j, ring + r * row_bytes + at_o, 0.0f, n[r][j]);
+          mine.template take<B>(j, ring + r * row_bytes + at_o, n[r][j]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             n[r][j][k] = n[r][j][k] * f2(r1[r]);
@@ -420,17 +425,22 @@ __global__ void __launch_bounds__(512) norm_bwd_pairs_kernel(const NormParams p)
   if constexpr (GATE) leave(4, ag);
 }
 
-cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
+cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, bool pairs, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
   auto by_type = [&](auto s, auto b) {
     constexpr int S = decltype(s)::value, B = decltype(b)::value;
-    auto kernel = p.whole == 2 ? (gate_sum ? norm_bwd_pairs_kernel<true, S, B> : norm_bwd_pairs_kernel<false, S, B>)
-                  : p.whole ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, true> : norm_bwd_kernel<2, true, false, S, B, true>)
-                                     : (gate_sum ? norm_bwd_kernel<2, false, true, S, B, true> : norm_bwd_kernel<2, false, false, S, B, true>))
-                  : p.D <= 8192
-                      ? (p.layer ? (gate_sum ? norm_bwd_kernel<2, true, true, S, B, false> : norm_bwd_kernel<2, true, false, S, B, false>)
-                                 : (gate_sum ? norm_bwd_kernel<2, false, true, S, B, false> : norm_bwd_kernel<2, false, false, S, B, false>))
-                      : (p.layer ? (gate_sum ? norm_bwd_kernel<4, true, true, S, B, false> : norm_bwd_kernel<4, true, false, S, B, false>)
-                                 : (gate_sum ? norm_bwd_kernel<4, false, true, S, B, false> : norm_bwd_kernel<4, false, false, S, B, false>));
+    auto by_form = [&](auto gate) {
+      constexpr bool G = decltype(gate)::value;
+      if (pairs) return p.whole == 2 ? norm_bwd_pairs_kernel<G, S, B, true> : norm_bwd_pairs_kernel<G, S, B, false>;
+      if (p.D > 8192) return p.layer ? norm_bwd_kernel<4, true, G, S, B, 0> : norm_bwd_kernel<4, false, G, S, B, 0>;
+      if (p.layer)
+        return p.whole == 2 ? norm_bwd_kernel<2, true, G, S, B, 2>
+               : p.whole    ? norm_bwd_kernel<2, true, G, S, B, 1>
+                            : norm_bwd_kernel<2, true, G, S, B, 0>;
+      return p.whole == 2 ? norm_bwd_kernel<2, false, G, S, B, 2>
+             : p.whole    ? norm_bwd_kernel<2, false, G, S, B, 1>
+                          : norm_bwd_kernel<2, false, G, S, B, 0>;
+    };
+    auto kernel = gate_sum ? by_form(std::true_type{}) : by_form(std::false_type{});
     return norm_launch(kernel, dim3(grid), threads, smem, st, p);
   };
   constexpr std::integral_constant<int, MOE_DTYPE_FP32> f32{};

@@ -1,17 +1,17 @@
 // Forward of the norms around a block, rows in whole vectors (norm.cuh has the
-// formulas).  16384 x 7168 in bf16: FWDTIME, FWDSHARE of the copy rate.
+// formulas).  16384 x 7168 in bf16: 149 us, 93% of the copy rate.
 //
 // A CTA works on several rows at a time, each in a group of threads of its own, so
 // that one row's barriers are another's work; a thread takes two vectors (four past
 // 8192): with one, what a thread does besides its elements (sums, barriers, addresses)
 // is most of its instructions (194 us), with four too few warps hide a row's latency
-// (221 us).  The weights are in shared memory as fp32 where the CTA has rows enough
+// (221 us).  A group's rows are grid rows apart: with neighbouring rows 161 us.  The weights are in shared memory as fp32 where the CTA has rows enough
 // for that to pay.
 #include "norm.cuh"
 
 namespace moe {
 
-template <int NV, bool LN, int S, int B, bool W>
+template <int NV, bool LN, int S, int B, int W /* whole */>
 __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const NormParams p) {
   const bool has_x = W || p.x, has_o = W || p.o, post = W || p.post, pre = W || p.pre, has_y = W || p.y, smem_w = W || p.smem_w,
              gated = !W && p.gate, gate_rows = !W && p.gate_rows;
@@ -19,10 +19,11 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   extern __shared__ __align__(16) char smem[];
   __shared__ float red[16 * 2 * 2 * NORM_MAX_WARPS];  // of groups of two warps and more
   const int g = threadIdx.x / p.group, groups = blockDim.x / p.group, tid = threadIdx.x - g * p.group;
-  const Mine<NV, W> mine(tid, p.group, p.nvec);
+  const int row = W == 2 ? p.D : p.places;  // elements of a row in the ring
+  const Mine<NV, W == 2> mine(tid, p.group, p.nvec, row);
   Group grp{red + (g & 15) * (2 * 2 * NORM_MAX_WARPS), g, p.group >> 5, tid >> 5, 0};
   char* const ring = smem + g * stages * stage_bytes;
-  const uint32_t at_o = has_x ? p.D * esize(S) : 0, at_g = at_o + (has_o ? p.D * esize(B) : 0);
+  const uint32_t at_o = has_x ? row * esize(S) : 0, at_g = at_o + (has_o ? row * esize(B) : 0);
   // this group's rows, and the pointers that go along with them (`a`: to what is fetched ahead)
   const int64_t row0 = (int64_t)g * gridDim.x + blockIdx.x, step = (int64_t)groups * gridDim.x;
   const int rows = row0 < p.T ? (int)((p.T - row0 + step - 1) / step) : 0;
@@ -54,6 +55,8 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
     }
     cp_async_commit();
   };
+  if constexpr (W != 2)
+    for (int s = 0; s < stages; ++s) mine.clear(ring + s * stage_bytes, stage_bytes);
   for (int s = 0; s < stages; ++s) {
     fetch_o(s < rows, ring + s * stage_bytes);
     fetch_x(s < rows, ring + s * stage_bytes);
@@ -62,13 +65,14 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   char *sw1 = nullptr, *sw2 = nullptr;
   if (smem_w) {
     sw1 = sw2 = smem + groups * stages * stage_bytes;
-    if (post) sw2 += p.D * 4;
+    if (post) sw2 += row * 4;
+    const int vecs = W == 2 ? p.nvec : row / 8;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < 2 * p.nvec; i += blockDim.x) {
-      const bool second = i >= p.nvec;
-      const int v = second ? i - p.nvec : i;
+    for (int i = threadIdx.x; i < 2 * vecs; i += blockDim.x) {
+      const bool second = i >= vecs;
+      const int v = second ? i - vecs : i;
       if (!(second ? pre : post)) continue;
-      const Mine<1, true> one(v, 0, p.nvec);
+      const Mine<1, W == 2> one(v, 0, p.nvec, row);
       F2 w[4];
       one.weight(0, second ? p.w2 : p.w1, p.pdt, p.w_off, w);
       const Raw<MOE_DTYPE_FP32> r = pack<MOE_DTYPE_FP32>(w);
@@ -81,7 +85,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
   // vector j of (v - m) r w + c in place
   auto apply = [&](int j, F2 (&v)[4], float m, float r, const char* sw, const void* w, const void* c) {
     F2 t[4];
-    if (smem_w) mine.template take<MOE_DTYPE_FP32>(j, sw, 0.0f, t);
+    if (smem_w) mine.template take<MOE_DTYPE_FP32>(j, sw, t);
     else mine.weight(j, w, p.pdt, p.w_off, t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (LN ? v[i] + f2(-m) : v[i]) * f2(r) * t[i];
@@ -103,23 +107,20 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (has_o) {
-        mine.template take<B>(j, at + at_o, 0.0f, v[j]);
+        mine.template take<B>(j, at + at_o, v[j]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = f2(0.0f);
       }
     }
-    if (post) {
-      row_stats<NV, LN, W>(mine, v, p.inv_d, p.eps, grp, st.x, st.y);
-      fetch_o(more, at);  // the sums have used every element of o
-    }
-    cp_async_wait(2 * stages - (post ? 1 : 2));  // x and the gate
+    if (post) row_stats<NV, LN, W == 2>(mine, v, p.inv_d, p.eps, grp, st.x, st.y);
+    cp_async_wait(2 * stages - 2);  // x and the gate
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       F2 t[4];
       if (post) apply(j, v[j], st.x, st.y, sw1, p.w1, p.c1);
       if (gated) {
-        if (gate_rows) mine.template take<B>(j, at + at_g, 0.0f, t);
+        if (gate_rows) mine.template take<B>(j, at + at_g, t);
         else mine.global(j, p.gate, p.pdt, 0.0f, t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = v[j][e] * t[e];
@@ -127,15 +128,13 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[j][e] = v[j][e] * f2(p.o_scale);
       if (has_x) {
-        mine.template take<S>(j, at, 0.0f, t);
+        mine.template take<S>(j, at, t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[j][e] = fma2(f2(p.x_scale), t[e], v[j][e]);
       }
-      mine.template put<S, W>(j, y, v[j]);
+      mine.template put<S, (W > 0)>(j, y, v[j]);
     }
-    if (pre) row_stats<NV, LN, W>(mine, v, p.inv_d, p.eps, grp, st.z, st.w);
-    if (!post) fetch_o(more, at);
-    fetch_x(more, at);
+    if (pre) row_stats<NV, LN, W == 2>(mine, v, p.inv_d, p.eps, grp, st.z, st.w);
     if (pre) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -143,6 +142,8 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
         mine.template put<B, true>(j, h, v[j]);
       }
     }
+    fetch_o(more, at);  // (as soon as its place is free, between the row's writes, a row costs 6% more)
+    fetch_x(more, at);
     if (stat) {
       if (tid == 0) stat[0] = st.x, stat[1] = st.y, stat[2] = st.z, stat[3] = st.w;
       stat += 4 * step;
@@ -155,9 +156,10 @@ __global__ void __launch_bounds__(norm_fwd_threads(NV)) norm_fwd_kernel(const No
 cudaError_t launch_norm_fwd(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st) {
   auto by_type = [&](auto s, auto b) {
     constexpr int S = decltype(s)::value, B = decltype(b)::value;
-    auto kernel = p.whole       ? (p.layer ? norm_fwd_kernel<2, true, S, B, true> : norm_fwd_kernel<2, false, S, B, true>)
-                  : p.D <= 8192 ? (p.layer ? norm_fwd_kernel<2, true, S, B, false> : norm_fwd_kernel<2, false, S, B, false>)
-                                : (p.layer ? norm_fwd_kernel<4, true, S, B, false> : norm_fwd_kernel<4, false, S, B, false>);
+    auto kernel = p.whole == 2  ? (p.layer ? norm_fwd_kernel<2, true, S, B, 2> : norm_fwd_kernel<2, false, S, B, 2>)
+                  : p.whole     ? (p.layer ? norm_fwd_kernel<2, true, S, B, 1> : norm_fwd_kernel<2, false, S, B, 1>)
+                  : p.D <= 8192 ? (p.layer ? norm_fwd_kernel<2, true, S, B, 0> : norm_fwd_kernel<2, false, S, B, 0>)
+                                : (p.layer ? norm_fwd_kernel<4, true, S, B, 0> : norm_fwd_kernel<4, false, S, B, 0>);
     return norm_launch(kernel, dim3(grid), threads, smem, st, p);
   };
   constexpr std::integral_constant<int, MOE_DTYPE_FP32> f32{};
