@@ -690,7 +690,8 @@ int moe_norm_plan_destroy(moe_norm_plan* plan);
 
 /*
  * The forward (T = 0 does nothing).  Rows [T, D] lie `_stride` elements apart (0 = D);
- * what is between D and the stride is neither read nor written.
+ * what is between D and the stride is not written and has no effect (a row that does
+ * not start on 16 bytes may be fetched from that boundary on).
  *   x      the residual stream, or NULL: y = o_scale (gate * z)
  *   o      the block's output, or NULL: y = x_scale x (a plan without a post norm, no gate)
  *   y      the new residual stream, or NULL: not written (with a pre norm only).

@@ -28,6 +28,12 @@
 //     of its error beside every logit; where the k-th and the next logit are
 //     closer than fp32 sums can tell apart, the undecided experts are decided in
 //     fp64.
+//
+// D = 7168, I = 2048, 256 experts, k = 8, one shared: one token 137 us (117.6 at the copy
+// rate: 18 us until the routing is known, of which the shared expert's weights hide some,
+// 4 us each between the phases and at the end), 64 tokens 2.82 to 2.91 ms (all of the copy
+// rate); 8 tokens of MXFP8 experts 432 us (92%).  Evicting weights from L2 first: 158 -> 150 us
+// for one token, nothing for more.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -1,7 +1,8 @@
 // Forward of the norms around a block for rows off vectors (norm_any.cuh).
-// 1003 x 2053 layer norms in fp16 with a gate per row: 18.4 us; in
-// vectors, rows of 2056 take 70%.  An element's own instructions bound it, hence the elements of
-// a thread in arrays that are read and written without a branch between (22 us with them).
+// 1003 x 2053 layer norms in fp16 with a gate per row: 17.3 us (22 with
+// the row in shared memory between the passes).  An element's own instructions bound it
+// (2000 x 2056 layer norms take 25.8 us, in vectors 15), hence the elements of a thread in
+// arrays that are read without a branch between them.
 #include "norm_any.cuh"
 
 namespace moe {

@@ -271,6 +271,21 @@ def test_many_rows(T, D, kw):
     check_backward(c, backward(c))
 
 
+# several rows a CTA: vectors that do not fill the threads, one at a time and in pairs; elements one by one
+# with the parameters beside the ring, without them, and with a ring of one row
+@pytest.mark.parametrize("T,D", [(1300, 2056), (1300, 5952), (5000, 40), (5000, 42), (700, 3001), (400, 5951), (400, 8191)])
+@pytest.mark.parametrize("v", [0, 1, 2, 4])
+def test_many_rows_of_each_form(T, D, v):
+    test_forward(T, D, v)
+    test_backward(T, D, v)
+
+
+@pytest.mark.parametrize("T,D", [(400, 8191), (400, 5951), (3, 8193)])
+def test_wide_rows_of_every_tensor(T, D):
+    kw = dict(kind="layer", bias=True, gate="rows", stream="fp32", branch="fp32", x_scale=0.5)
+    check_backward(c := Case(T, D, seed=5, **kw), backward(c))
+
+
 def test_backward_without_dy():
     c = Case(70, 512, seed=6)
     check_backward(c, backward(c, dy=False))
