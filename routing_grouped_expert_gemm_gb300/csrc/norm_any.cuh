@@ -18,7 +18,8 @@
 namespace moe {
 
 // Elements a thread, of the forward and of the backward (which holds the sums besides),
-// at 64 registers each.
+// at 64 registers each.  The backward takes 8 where 4 would need too many threads: 8000 x
+// 4001 in bf16 takes 193 us with 4, 223 with 8; layer norms in fp16 239 and 377, spilled.
 constexpr int ANY_FWD = 8;
 constexpr int any_bwd_per(int64_t D) { return D <= 4096 ? 4 : 8; }
 constexpr int ANY_MAX_WARPS = 32, ANY_RESIDENT = 1024;  // (threads an SM)
