@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_any_kernel(const NormParams p) 
       for (int i = 0; i < 4; ++i) st[i] = from[i];
     }
     // outside the row gradients and weights are 0, and so is all that enters the sums
-    float v[NE], d[NE], n[NE], w[NE], s[2] = {0.0f, 0.0f};
+    float v[NE], d[NE], n[NE], w[NE], s[LN ? 2 : 1] = {0.0f};
     if (p.dy) {
       load_mine<S>(rd.row<MODE>(stage, t), p.D, v);
     } else {
@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(1024) norm_bwd_any_kernel(const NormParams p) 
         if constexpr (LN) ac2[j] += d[j];
         d[j] *= w[j];
         s[0] = fmaf(d[j], n[j], s[0]);
-        if (LN) s[1] += d[j];
+        if constexpr (LN) s[1] += d[j];
       }
-      group_sums<2, ANY_MAX_WARPS>(s, grp);
-      const float q = s[0] * p.inv_d, m = LN && p.layer ? s[1] * p.inv_d : 0.0f;
+      group_sums<LN ? 2 : 1, ANY_MAX_WARPS>(s, grp);
+      const float q = s[0] * p.inv_d, m = LN && p.layer ? s[LN ? 1 : 0] * p.inv_d : 0.0f;
 #pragma unroll
       for (int j = 0; j < NE; ++j) v[j] = fmaf(st[3], d[j] - n[j] * q - m, v[j]);
     }
@@ -98,17 +98,18 @@ __global__ void __launch_bounds__(1024) norm_bwd_any_kernel(const NormParams p) 
       }
     }
     if (p.post) {
-      s[0] = s[1] = 0.0f;
+#pragma unroll
+      for (float& a : s) a = 0.0f;
 #pragma unroll
       for (int j = 0; j < NE; ++j) {
         aw1[j] = fmaf(v[j], n[j], aw1[j]);
         if constexpr (LN) ac1[j] += v[j];
         v[j] *= w[j];
         s[0] = fmaf(v[j], n[j], s[0]);
-        if (LN) s[1] += v[j];
+        if constexpr (LN) s[1] += v[j];
       }
-      group_sums<2, ANY_MAX_WARPS>(s, grp);
-      const float q = s[0] * p.inv_d, m = LN && p.layer ? s[1] * p.inv_d : 0.0f;
+      group_sums<LN ? 2 : 1, ANY_MAX_WARPS>(s, grp);
+      const float q = s[0] * p.inv_d, m = LN && p.layer ? s[LN ? 1 : 0] * p.inv_d : 0.0f;
 #pragma unroll
       for (int j = 0; j < NE; ++j) v[j] = st[1] * (v[j] - n[j] * q - m);
     }
