@@ -629,26 +629,44 @@ def _row_stride(t) -> int:
     return t.stride(0)
 
 
-def _gate_stride(gate, D: int) -> int:
-    """0: one gate per channel; else the stride of a gate per row."""
-    if gate is None or isinstance(gate, int) or gate.dim() == 1:
+def _gate_stride(gate, D: int, T: int) -> int:
+    """0: one gate per channel, [D]; else the stride of a gate per row, [T, D] (its
+    rows may have further dimensions).  Any other shape is refused: read as
+    either, it would be read past its end."""
+    if gate is None or isinstance(gate, int):
         return 0
+    if gate.dim() == 1 and gate.shape[0] == D and gate.is_contiguous():
+        return 0
+    if gate.dim() < 2 or gate.shape[-1] != D or gate.numel() < T * D:
+        raise MoEError(MOE_ERR_INVALID_ARG, "a gate that is neither [D] nor [T, D]")
     return _row_stride(gate) or D
 
 
-def _norm_args(plan: NormPlan, params: dict) -> moe_norm_params:
+def _norm_args(plan: NormPlan, params: dict, gate_stride: int) -> moe_norm_params:
     get = params.get
-    gate = get("gate")
     return moe_norm_params(_ptr(get("post_weight")), _ptr(get("post_bias")), _ptr(get("pre_weight")), _ptr(get("pre_bias")),
-                           _ptr(gate), get("gate_stride") or _gate_stride(gate, plan.cfg.D))
+                           _ptr(get("gate")), get("gate_stride") or gate_stride)
+
+
+def _gate_grad_stride(grad, D: int, T: int, per_row: bool) -> int:
+    """The same of a gate's gradient: [T, D] for a gate per row, else [D]."""
+    if grad is None or isinstance(grad, int):
+        return 0
+    if not per_row:
+        if grad.numel() != D or not grad.is_contiguous():
+            raise MoEError(MOE_ERR_INVALID_ARG, "the gradient of a gate [D] that is not [D]")
+        return 0
+    if grad.numel() < T * D or (grad.dim() > 1 and grad.shape[-1] != D):
+        raise MoEError(MOE_ERR_INVALID_ARG, "the gradient of a gate [T, D] that is not [T, D]")
+    return _row_stride(grad) or D
 
 
 def moe_norm(plan: NormPlan, T: int, params: dict, x=None, o=None, y=None, h=None, stats=None, stream=None) -> None:
     """z = N(o), y = x_scale x + o_scale gate z, h = N(y).  ``params``: post_weight,
-    post_bias, pre_weight, pre_bias and gate ([D], or [T, D] for a gate per row),
-    each optional.  Rows may be further apart than D (a view of a wider tensor);
-    ``stats`` [T, 4] fp32 keeps what ``moe_norm_bwd`` needs."""
-    q = _norm_args(plan, params)
+    post_bias, pre_weight, pre_bias and gate ([D], or [T, D] for a gate per row; no
+    other shape), each optional.  Rows may be further apart than D (a view of a wider
+    tensor); ``stats`` [T, 4] fp32 keeps what ``moe_norm_bwd`` needs."""
+    q = _norm_args(plan, params, _gate_stride(params.get("gate"), plan.cfg.D, T))
     rc = lib().moe_norm(plan.handle, T, q, _ptr(x), _row_stride(x), _ptr(o), _row_stride(o), _ptr(y), _row_stride(y),
                         _ptr(h), _row_stride(h), _ptr(stats), _stream(stream))
     if rc != MOE_OK:
@@ -661,7 +679,8 @@ def moe_norm_bwd(plan: NormPlan, T: int, params: dict, stats, grads: dict, o=Non
     in ``grads`` (the keys of ``params``: fp32 [D]; a gate per row: [T, D] of the branch's type)."""
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    q, g = _norm_args(plan, params), _norm_args(plan, grads)
+    q = _norm_args(plan, params, _gate_stride(params.get("gate"), plan.cfg.D, T))
+    g = _norm_args(plan, grads, _gate_grad_stride(grads.get("gate"), plan.cfg.D, T, q.gate_stride != 0))
     rc = lib().moe_norm_bwd(plan.handle, T, q, _ptr(stats), _ptr(o), _row_stride(o), _ptr(y), _row_stride(y), _ptr(dy),
                             _row_stride(dy), _ptr(dh), _row_stride(dh), _ptr(dx), _row_stride(dx), _ptr(do),
                             _row_stride(do), g, _ptr(workspace), workspace_bytes, _stream(stream))

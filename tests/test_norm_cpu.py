@@ -42,3 +42,73 @@ def test_null_arguments(L):
     assert L.moe_norm_workspace_bytes(None, 4) == 0
     assert L.moe_norm(None, 1, None, *[None, 0] * 4, None, None) == rg.MOE_ERR_INVALID_ARG
     assert L.moe_norm_bwd(None, 1, None, None, *[None, 0] * 6, None, None, 0, None) == rg.MOE_ERR_INVALID_ARG
+
+
+class _Reached:
+    """Stands in for the library: says yes, and what the binding called."""
+
+    def __init__(self):
+        self.calls = []
+
+    def moe_error_string(self, code):
+        return b"refused"
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append((name, a)) or rg.MOE_OK
+
+
+T, D = 6, 8
+ZERO = torch.zeros
+
+
+def _calls(monkeypatch, gate, grad=None):
+    """The calls that reach the library with this gate (and gradient), or the refusal's code."""
+    stub = _Reached()
+    monkeypatch.setattr(rg, "lib", lambda: stub)
+    plan = rg.NormPlan(0, rg.moe_norm_config(D))
+    row = ZERO(T, D, dtype=torch.bfloat16)
+    try:
+        if grad is None:
+            rg.moe_norm(plan, T, {"gate": gate}, x=row, o=row, y=row, h=row, stream=0)
+        else:
+            rg.moe_norm_bwd(plan, T, {"gate": gate}, 0, {"gate": grad}, o=row, y=row, dy=row, dh=row, stream=0)
+    except rg.MoEError as e:
+        assert not stub.calls
+        return e.code
+    return stub.calls
+
+
+# read as [T, D] or as [D], each of these would be read past its end or by the wrong rows
+@pytest.mark.parametrize("gate", [
+    ZERO(T, 1), ZERO(1, D), ZERO(T - 1, D), ZERO(1), ZERO(D - 1), ZERO(D + 1), ZERO(2 * D)[::2], ZERO(T, D + 1), ZERO(T, D - 1), ZERO(1, D).expand(T, D),
+    ZERO(T, 1).expand(T, D), ZERO(2, T // 2, D - 1), ZERO(())], ids=lambda t: f"{tuple(t.shape)}_{tuple(t.stride())}")
+def test_gates_of_other_shapes_are_refused(monkeypatch, gate):
+    assert _calls(monkeypatch, gate) == rg.MOE_ERR_INVALID_ARG
+    assert _calls(monkeypatch, gate, ZERO(D)) == rg.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("gate,stride", [(None, 0), (ZERO(D), 0), (ZERO(T, D), D), (ZERO(T + 3, D), D), (ZERO(2, T // 2, D), D),
+                                         (ZERO(T, D + 5)[:, :D], D + 5), (4096, 0)])
+def test_gates_that_are_taken(monkeypatch, gate, stride):
+    (name, args), = _calls(monkeypatch, gate)
+    assert name == "moe_norm" and args[2].gate_stride == stride
+
+
+ROWS = torch.bfloat16
+
+
+@pytest.mark.parametrize("gate,grad,ok", [
+    (ZERO(D), ZERO(D), True), (ZERO(D), ZERO(1, D), True), (ZERO(D), ZERO(T, D), False), (ZERO(D), ZERO(1), False), (ZERO(D), ZERO(2 * D)[::2], False),
+    (ZERO(T, D, dtype=ROWS), ZERO(T, D, dtype=ROWS), True), (ZERO(T, D, dtype=ROWS), ZERO(T, D + 2, dtype=ROWS)[:, :D], True),
+    (ZERO(T, D, dtype=ROWS), ZERO(T * D, dtype=ROWS), True), (ZERO(T, D, dtype=ROWS), ZERO(D), False), (ZERO(T, D, dtype=ROWS), ZERO(1, D), False),
+    (ZERO(T, D, dtype=ROWS), ZERO(T, D + 2, dtype=ROWS), False), (ZERO(T, D, dtype=ROWS), ZERO(T, 1), False), (None, None, True), (4096, 4096, True)])
+def test_gradients_of_gates(monkeypatch, gate, grad, ok):
+    if grad is None:
+        grad = 0
+    got = _calls(monkeypatch, gate, grad)
+    if not ok:
+        assert got == rg.MOE_ERR_INVALID_ARG
+    else:
+        (name, args), = got
+        per_row = torch.is_tensor(gate) and gate.dim() > 1
+        assert name == "moe_norm_bwd" and args[16].gate_stride == (0 if not per_row else grad.stride(0) if grad.dim() > 1 else D)
