@@ -234,7 +234,7 @@ int moe_plan_create(const moe_config* cfg_in, moe_plan** out) {
   pl->device = dev;
   pl->num_sms = prop.multiProcessorCount;
   pl->grid = c.gather_ctas + gemm;
-  pl->encode = reinterpret_cast<encode_tiled_fn>(fn);
+  pl->encode = {reinterpret_cast<encode_tiled_fn>(fn), dev};
   pl->timed = false;
   pl->bwd_timed = false;
   *out = pl;

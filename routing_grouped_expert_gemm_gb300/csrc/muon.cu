@@ -1143,7 +1143,7 @@ struct moe_muon_plan {
   int device, num_sms;
   int64_t chunk;  // matrices in flight
   int small_cs, small_wc;  // the one-launch form: CTAs per matrix (0: not used) and columns per thread
-  encode_tiled_fn encode;
+  EncodeTiled encode;
 };
 
 namespace {
@@ -1357,7 +1357,7 @@ int moe_muon_plan_create(const moe_muon_config* cfg, moe_muon_plan** out) {
   pl->cfg = c;
   pl->device = dev;
   pl->num_sms = sms;
-  pl->encode = reinterpret_cast<encode_tiled_fn>(fn);
+  pl->encode = {reinterpret_cast<encode_tiled_fn>(fn), dev};
   // matrices in flight: the smallest product (A, half of m / 256 squared tiles)
   // fills the CTA pairs eight times over, so its last, part-filled round costs
   // little, and the workspace does not grow with the stack

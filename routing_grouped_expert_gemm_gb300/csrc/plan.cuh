@@ -10,6 +10,18 @@ typedef CUresult (*encode_tiled_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_
                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 namespace moe {
+// cuTensorMapEncodeTiled.  Unlike the runtime's calls it wants a current context, which
+// a host thread that has made none of those yet does not have: it gets the plan's then.
+struct EncodeTiled {
+  encode_tiled_fn fn;
+  int device;
+  template <typename... Args>
+  CUresult operator()(Args... args) const {
+    const CUresult r = fn(args...);
+    return r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(device) == cudaSuccess ? fn(args...) : r;
+  }
+};
+
 // A forward's routing and schedule inside its workspace (device pointers)
 struct FwdRoutingViews {
   const int* topk_idx;
@@ -28,7 +40,7 @@ struct moe_plan {
   int device;
   int num_sms;
   int grid;  // persistent kernel CTAs = gather + gemm
-  encode_tiled_fn encode;
+  moe::EncodeTiled encode;
   cudaEvent_t timing[4];  // optional, see moe_plan_set_timing_events
   bool timed;
   cudaEvent_t bwd_timing[5];  // optional, see moe_plan_set_bwd_timing_events
