@@ -55,6 +55,7 @@ enum : int { CTR_TOPK = 0, CTR_CLAIMS, CTR_UP /* units done */, CTR_H /* CTAs wh
 constexpr int DEC_OWN_TOPK = 4;                     // up to so many tokens every CTA makes all tokens' selection itself
 constexpr int DEC_EARLY = 2;                        // steps loaded before the grid's barrier
 constexpr int DEC_QUEUE = 4;                        // claimed units on their way to the roles of a CTA
+constexpr int DEC_SMEM = 227 * 1024;                // shared memory of a CTA: as many stages as fit
 
 // Steps of a unit, for `total` steps on `ctas` CTAs: a CTA's share in 32 units,
 // though not so many that a unit is below 12 steps (4.5 us of an SM's loads), or where
@@ -1214,7 +1215,7 @@ int decode(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, c
   p.mx = mx;
   p.ncap = (int)((T + 15) / 16 * 16);
   p.stage_bytes = DEC_A_BYTES + p.ncap * 128;
-  const int room = 227 * 1024 - dec_smem_fixed(), per = p.stage_bytes + (mx ? 2 * SF_BLOCK_BYTES : 0);
+  const int room = DEC_SMEM - dec_smem_fixed(), per = p.stage_bytes + (mx ? 2 * SF_BLOCK_BYTES : 0);
   p.n_stages = room / per < DEC_MAX_STAGES ? room / per : DEC_MAX_STAGES;
   const int smem = dec_smem_fixed() + p.n_stages * per;
   p.timeout_ns = (long long)c.timeout_ms * 1000000LL;
@@ -1254,7 +1255,8 @@ int decode(const moe_plan* pl, int64_t T, const void* x, const moe_weights* w, c
   if (rc != MOE_OK) return MOE_ERR_INVALID_ARG;
 
   auto kernel = mx ? moe_decode_kernel<true> : moe_decode_kernel<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ERR_CUDA;
+  // (the limit belongs to the kernel, not to the launch, and another thread's call may set it in between: the same for all)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, DEC_SMEM) != cudaSuccess) return MOE_ERR_CUDA;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)pl->num_sms);
   lc.blockDim = dim3(DEC_THREADS);

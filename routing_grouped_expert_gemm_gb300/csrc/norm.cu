@@ -67,7 +67,6 @@ int64_t norm_grid(const moe_norm_plan* pl, int64_t T) {
   const int64_t most = per_sm * pl->num_sms;
   return T < most ? T : most;
 }
-constexpr int NORM_SMEM = 200 * 1024;  // of an SM's shared memory for the rings
 
 // Rows off vectors: threads of a CTA (`per` elements each), CTAs of the backward at most
 // (each leaves sums, so eight rows a CTA where there are more than two CTAs an SM), and a

@@ -66,10 +66,14 @@ cudaError_t launch_norm_bwd(const NormParams& p, bool gate_sum, bool pairs, unsi
 cudaError_t launch_norm_fwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 cudaError_t launch_norm_bwd_any(const NormParams& p, unsigned grid, unsigned threads, size_t smem, cudaStream_t st);
 
+constexpr int NORM_SMEM = 200 * 1024;  // of an SM's shared memory for the rings: no launch asks for more
+
+// The limit of shared memory belongs to the kernel, not to the launch, and another
+// thread's call may set it in between: so every call sets the same.
 template <typename P>
 cudaError_t norm_launch(void (*kernel)(P), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const P& p) {
   if (smem > 40 * 1024) {  // 48 KB with what the kernel holds besides
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t lc = {};

@@ -343,9 +343,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ROUTER_THREADS, 1)
 
 // host-side launcher (called from api.cu)
 namespace moe {
+constexpr int ROUTER_STAGES_SMEM = 200 * 1024;  // of all stages, at most
 int router_smem_bytes(int ncols, int* stages_out) {
   const int stage_bytes = A_STAGE_BYTES + (ncols / 2) * 128;  // x tile + this CTA's half of W_r
-  int stages = (200 * 1024) / stage_bytes;
+  int stages = ROUTER_STAGES_SMEM / stage_bytes;
   if (stages > 8) stages = 8;
   if (stages < 2) stages = 2;
   *stages_out = stages;
@@ -357,7 +358,10 @@ cudaError_t launch_router(const RouterMaps& maps, const FwdParams& p, cudaStream
   const int smem = router_smem_bytes(p.n_router_cols, &stages);
   int tmem_cols = 32;
   while (tmem_cols < p.n_router_cols) tmem_cols <<= 1;
-  cudaError_t err = cudaFuncSetAttribute(router_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit belongs to the kernel, not to the launch, and another thread's call (of a plan with other
+  // experts) may set it in between: the same for all
+  cudaError_t err =
+      cudaFuncSetAttribute(router_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ROUTER_STAGES_SMEM + 1024);
   if (err != cudaSuccess) return err;
   router_topk_kernel<<<(p.n_chunks + 1) & ~1, ROUTER_THREADS, smem, stream>>>(maps, p, stages, tmem_cols);
   return cudaGetLastError();

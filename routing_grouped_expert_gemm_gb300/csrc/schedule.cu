@@ -416,14 +416,17 @@ __device__ void build_tasks(const FwdParams& p, const int* sS, int* dsm) {
 
 // dynamic shared memory of build_tasks: mb_tiles, mt_first, mb_ptiles and
 // mtp_first [n_mb] each, then step_off [n_mb + lag + 1]
-__host__ __device__ inline int sched_dyn_ints(int n_mb, int lag) { return 4 * n_mb + (n_mb + lag + 1); }
+__host__ __device__ constexpr int sched_dyn_ints(int n_mb, int lag) { return 4 * n_mb + (n_mb + lag + 1); }
 
 int schedule_smem_bytes(const FwdParams& p) { return (int)sizeof(int) * sched_dyn_ints(p.n_mb, p.lag); }
 
 cudaError_t launch_schedule(const FwdParams& p, cudaStream_t stream) {
   const int smem = schedule_smem_bytes(p);
   if (smem > 48 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // (the limit belongs to the kernel, not to the launch, and another thread's call may set it in between: the
+    // most that a plan may have, for all)
+    constexpr int most = (int)sizeof(int) * sched_dyn_ints(8192, 1);  // minibatches, lag
+    const cudaError_t err = cudaFuncSetAttribute(schedule_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (err != cudaSuccess) return err;
   }
   schedule_kernel<<<p.n_chunks, SCHED_THREADS, smem, stream>>>(p);
