@@ -597,7 +597,8 @@ int moe_muon_get_status(const moe_muon_plan* plan, const void* workspace, int* d
  */
 #define MOE_DECODE_MAX_TOKENS 64
 
-/* Device workspace of moe_decode and moe_decode_routed for T tokens (0 on bad input). */
+/* Device workspace of moe_decode and moe_decode_routed for T tokens (0 on bad
+ * input); what is enough for T is enough for fewer. */
 size_t moe_decode_workspace_bytes(const moe_plan* plan, int64_t T);
 
 /*

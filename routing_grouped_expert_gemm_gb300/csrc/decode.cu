@@ -1152,9 +1152,18 @@ DecodeLayout decode_layout(const moe_plan* pl, int64_t T) {
   const int64_t step = mx ? BK_MX : BK, kd = c.D / step, ki = c.I / step;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
   // units: the shared expert's up/gate projections are cut here, the others when the
-  // experts are known, into at most so many pieces (fewer for more tokens, whose sums are larger)
-  L.q_s = dec_unit_steps((int)(c.I_s / 128 * 2 * (c.D / BK)), pl->num_sms, (int)ncap);
-  const int64_t most = T <= 8 ? 16 : 128 / T;
+  // experts are known, into at most so many pieces (fewer for more tokens, whose sums are larger).
+  // Rows times pieces would now and then be fewer for one token more; the room for them is not, so
+  // that a workspace for some tokens does for any fewer
+  auto steps = [&](int64_t cap) { return dec_unit_steps((int)(c.I_s / 128 * 2 * (c.D / BK)), pl->num_sms, (int)cap); };
+  L.q_s = steps(ncap);
+  int64_t rows_s = 0;
+  for (int64_t cap = 16; cap <= ncap; cap += 16) {
+    const int64_t rows = (T < cap ? T : cap) * up(c.D / BK, steps(cap));
+    rows_s = rows > rows_s ? rows : rows_s;
+  }
+  const int64_t most = T <= 8 ? 16 : 128 / T, rows_most = T <= 8 ? 16 * T : 128;  // (at least T most)
+  auto rows_of = [&](int64_t pieces) { return T * pieces < rows_most ? T * pieces : rows_most; };
   L.most_u = (int)(most < up(kd, 4) ? most : up(kd, 4));
   L.most_d = (int)(most < up(ki, 4) ? most : up(ki, 4));
   L.q_ds = (int)up(c.I_s / BK, most);
@@ -1167,10 +1176,10 @@ DecodeLayout decode_layout(const moe_plan* pl, int64_t T) {
   L.h = take((size_t)R * c.I * (mx ? 1 : 2));
   L.hs = take(mx ? R * (c.I / 32) : 0);
   L.h_s = take((size_t)DEC_MAX_T * c.I_s * 2);
-  L.sums_s = take((size_t)(c.I_s / 128) * 2 * up(c.D / BK, L.q_s) * T * 512);
-  L.sums_u = take((size_t)(c.I / 128) * 2 * L.most_u * R * 512);
-  L.sums_d = take((size_t)(c.D / 128) * L.most_d * R * 512);
-  L.sums_ds = take((size_t)(c.D / 128) * (c.I_s ? most : 0) * T * 512);
+  L.sums_s = take((size_t)(c.I_s / 128) * 2 * rows_s * 512);
+  L.sums_u = take((size_t)(c.I / 128) * 2 * rows_of(up(kd, 4)) * c.k * 512);
+  L.sums_d = take((size_t)(c.D / 128) * rows_of(up(ki, 4)) * c.k * 512);
+  L.sums_ds = take((size_t)(c.D / 128) * (c.I_s ? rows_most : 0) * 512);
   L.total = at;
   return L;
 }

@@ -333,3 +333,30 @@ def test_refusals():
     refused(bad, rg.moe_decode_routed, c.plan, 4, c.x, c.w, idx, w.data_ptr() + 2, out, c.ws)
     m = Layer(4, precision="mxfp8")
     refused(bad, rg.moe_decode, m.plan, 4, m.x, {k: v for k, v in m.w.items() if k != "W_up_scale"}, out, m.ws)
+
+
+SIZES = [dict(D=4096, I=1536, E=128, k=8, I_s=0), dict(D=1024, I=1024, E=17, k=1, I_s=1024), dict(D=768, I=640, E=20, k=6, I_s=256),
+         dict(D=7168, I=2048, E=256, k=8, I_s=2048)]
+
+
+@pytest.mark.parametrize("precision", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("shape", range(len(SIZES)))
+def test_workspace_sizes_never_fall(shape, precision):
+    plan = rg.moe_plan_create(64, precision=precision, **SIZES[shape])
+    sizes = [rg.moe_decode_workspace_bytes(plan, T) for T in range(1, 65)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+@pytest.mark.parametrize("most", [48, 64])
+@pytest.mark.parametrize("shape,precision", [(0, "bf16"), (1, "bf16"), (2, "bf16"), (2, "mxfp8")])
+def test_one_workspace_for_every_batch(shape, precision, most):
+    """A server's workspace, made once for its largest batch."""
+    c = Layer(most, precision=precision, seed=shape, **SIZES[shape])
+    idx, w = c.route()
+    ref = c.oracle(idx, w)
+    c.ws = torch.cat([c.ws, torch.full((256,), 0x5A, dtype=torch.uint8, device="cuda")])
+    for T in range(1, most + 1):
+        out, got, _ = c.run(T, workspace_bytes=c.ws.numel() - 256)
+        assert torch.equal(got.long(), idx[:T])
+        close(out, ref[:T])
+    assert (c.ws[-256:] == 0x5A).all()
