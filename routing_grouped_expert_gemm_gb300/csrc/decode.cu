@@ -254,7 +254,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 // of 256 (8 elements a lane).  Beside a logit what fp32 may be off by: a product
 // passes through at most `depth` additions, each of half an ulp (2^-24) of a sum that
 // is at most the sum of magnitudes, which is at most |x| |w|; and the bias through one.
-// (1 + 2^-8 covers the norms' own roundings.)
+// (1 + 2^-8 covers the norms' own roundings.)  Below 2^-126 a rounding loses up to 2^-150
+// whatever the value: squares of elements below 2^-75 come to nothing, so a lane whose
+// elements are not all zeros adds 2^-149 for every one of them to the squares, which does
+// nothing to those of ordinary size; and a logit may lose as much with every product.
 constexpr int RT_E = 4, RT_T = 4, RT_N = RT_E * RT_T + RT_E + RT_T;
 __device__ __forceinline__ float dec_depth(int D) { return (float)((D / 256 + 3) / 4 + 8 + 10 + 4); }
 
@@ -263,6 +266,8 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
 }
+
+__device__ __forceinline__ uint32_t any_bits(const uint4& q) { return (q.x | q.y) | (q.z | q.w); }
 
 __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /* [8 warps][RT_N][33] */, float* red /* [8][RT_N] */) {
   constexpr int NV = RT_N, AHEAD = 3;
@@ -279,6 +284,9 @@ __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /*
     float v[NV];  // logits, then |w|^2, then |x|^2
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = 0.0f;
+    uint32_t bits[RT_E + RT_T];  // of this lane's elements of w and x: whether one of them is not zero
+#pragma unroll
+    for (int i = 0; i < RT_E + RT_T; ++i) bits[i] = 0u;
     const uint4* w = reinterpret_cast<const uint4*>(p.w_router + (size_t)e0 * p.D) + lane;
     const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)t0 * p.D) + lane;
     const int d8 = p.D / 8;
@@ -297,6 +305,7 @@ __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /*
 #pragma unroll
       for (int e = 0; e < RT_E; ++e) {
         unpack8(wq[0][e], wf[e]);
+        bits[e] |= any_bits(wq[0][e]);
 #pragma unroll
         for (int a = 0; a + 1 < AHEAD; ++a) wq[a][e] = wq[a + 1][e];
       }
@@ -310,6 +319,7 @@ __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /*
         if (t >= nt) break;
         float xf[8], of[RT_E];  // (a chunk's sum by itself: fewer additions behind one another)
         unpack8(xq[t], xf);
+        bits[RT_E + t] |= any_bits(xq[t]);
         if (c + 4 < chunks) xq[t] = __ldg(x + (size_t)t * d8 + (c + 4) * 32);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -321,6 +331,9 @@ __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /*
         for (int e = 0; e < RT_E; ++e) v[t * RT_E + e] += of[e];
       }
     }
+#pragma unroll
+    for (int i = 0; i < RT_E + RT_T; ++i)
+      if (bits[i] & 0x7fff7fffu) v[RT_E * RT_T + i] += __int_as_float(8 * ((chunks + 3) / 4));  // 2^-149 each
     // the lanes' sums through shared memory: lane l adds those of value l
     float* mine = part + warp * (NV * 33);
 #pragma unroll
@@ -343,7 +356,8 @@ __device__ __noinline__ void router_logits(const DecodeParams& p, float* part /*
       float ww = 0.0f, xx = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) s.x += r[q * NV + lane], ww += r[q * NV + RT_E * RT_T + e], xx += r[q * NV + RT_E * RT_T + RT_E + t];
-      s.y = sqrtf(ww) * sqrtf(xx) * dec_depth(p.D) * (257.0f / 256.0f / 16777216.0f);
+      s.y = 0.0f;  // (of zeros)
+      if (ww > 0.0f && xx > 0.0f) s.y = sqrtf(ww) * sqrtf(xx) * dec_depth(p.D) * (257.0f / 256.0f / 16777216.0f) + __int_as_float(p.D);
       if (p.b_router) {
         s.x += p.b_router[e0 + e];
         s.y += fabsf(s.x) * (1.0f / 16777216.0f);

@@ -360,3 +360,44 @@ def test_one_workspace_for_every_batch(shape, precision, most):
         assert torch.equal(got.long(), idx[:T])
         close(out, ref[:T])
     assert (c.ws[-256:] == 0x5A).all()
+
+
+def cancelling(seed, T=64, D=2048, E=16, k=4, **kw):
+    """Logits of about 1 that are what is left of parts of up to 10^5: columns in pairs of opposite
+    tokens and equal weights, at random places, so that a pair cancels neither in a product nor in a
+    chunk; one pair has weights that differ.  Every product is exact and so, nearly, are fp64 sums."""
+    c = Layer(T, D=D, E=E, k=k, seed=seed, **kw)
+    at = torch.randperm(D, generator=c.gen, device="cuda")
+    a = (torch.randn(T, D // 2, generator=c.gen, device="cuda") * 300).bfloat16()
+    base = (torch.randn(E, D // 2, generator=c.gen, device="cuda") * 16).bfloat16()
+    base[:, 0] = (torch.randn(E, generator=c.gen, device="cuda") * 2.0**-8).bfloat16()
+    c.x[:, at[0::2]], c.x[:, at[1::2]] = a, -a
+    c.w["W_router"][:, at[0::2]] = c.w["W_router"][:, at[1::2]] = base
+    c.w["W_router"][:, at[0]] = (torch.randn(E, generator=c.gen, device="cuda") * 2.0**-8).bfloat16()
+    return c
+
+
+@pytest.mark.parametrize("T", [3, 64])
+@pytest.mark.parametrize("of_x,of_w", [(0, 0), (-60, -60), (-80, 0), (-90, 0), (0, -95), (-90, -30), (-75, -75)])
+def test_selection_of_any_magnitude(T, of_x, of_w):
+    """Powers of two in front of the tokens or the router change no order: not where squares of the
+    elements, or even their products (the last two cases), are below what fp32 holds."""
+    c = cancelling(T, T=T)
+    want = c.route()[0]
+    c.x *= 2.0**of_x
+    c.w["W_router"] *= 2.0**of_w
+    ri, _ = c.route()
+    assert torch.equal(ri, want)  # (the scaling is exact)
+    assert torch.equal(c.run()[1].long(), ri)
+
+
+def test_tokens_of_zeros_among_small_ones():
+    """A token of zeros: a tie of all experts.  One element that is not zero decides."""
+    c = Layer(8, D=512, E=40, k=3, seed=12)
+    c.x[1], c.x[3], c.x[6] = 0.0, -0.0, 0.0
+    c.x[6, 400] = 2.0**-120
+    c.x[5] *= 2.0**-110
+    c.w["W_router"][7] = 0.0
+    out, idx, w = c.run()
+    assert torch.equal(idx.long(), c.route()[0])
+    assert torch.equal(idx[[1, 3]], torch.arange(3, dtype=torch.int32, device="cuda").expand(2, 3))
