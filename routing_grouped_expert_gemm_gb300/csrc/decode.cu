@@ -389,17 +389,24 @@ static_assert(sizeof(DecodeSched::w) >= E_MAX * 8, "keys in fp64 lie where the w
 static_assert(DEC_OWN_TOPK * TOPK_MAX <= 128, "a thread a route");
 static_assert(sizeof(TopkScratch) <= sizeof(DecodeSched::mask), "scratch of the selection lies where the masks come to lie");
 
+// What a selected logit may be off by besides its own rounding to fp32, and how much of
+// that its weight bears: 2^-9 in the logit is at most 2^-8 of the weight, half a step of the
+// bf16 output.  (Unit tokens and router rows of 7168: 10^-4 at most, in truth 10^-6.)
+constexpr float DEC_LOGIT_TOL = 1.0f / 512.0f;
+__device__ __forceinline__ bool too_far_off(float2 q) { return fmaf(fabsf(q.x), -1.0f / 16777216.0f, q.y) > DEC_LOGIT_TOL; }
+
 // The selection of token t where fp32 left it open, by the epilogue's 128 threads:
 // the experts that may be in or out, given what every logit may be off by, are ranked
-// by their logits in fp64 (as integers of the same order, NaN lowest).
-__device__ __noinline__ void decide_fp64(const DecodeParams& p, int t, int tid, float lo, float hi, TopkScratch& s, const float2* val,
+// by their logits in fp64 (as integers of the same order, NaN lowest), which take the
+// place of the fp32 ones; and so do those of experts that are in, but too far off.
+__device__ __noinline__ void decide_fp64(const DecodeParams& p, int t, int tid, float lo, float hi, TopkScratch& s, float2* val,
                                          unsigned long long* dkey /* [E], shared memory */) {
   const int lane = tid & 31, ew = tid >> 5, words = (p.E + 31) / 32;
 #pragma unroll 1
   for (int e = tid; e < ((p.E + 127) & ~127); e += 128) {
     const bool in = s.words[e >> 5] >> lane & 1;
     const float2 q = val[e];
-    const bool open = e < p.E && (in ? q.x - q.y <= hi : q.x + q.y >= lo);
+    const bool open = e < p.E && (in ? q.x - q.y <= hi || too_far_off(q) : q.x + q.y >= lo);
     const uint32_t o = __ballot_sync(0xffffffffu, open), w = __ballot_sync(0xffffffffu, in && !open);
     if (lane == 0) s.open[e >> 5] = o, s.words[e >> 5] = w;
   }
@@ -427,7 +434,10 @@ __device__ __noinline__ void decide_fp64(const DecodeParams& p, int t, int tid, 
       for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
       if (p.b_router) sum += (double)p.b_router[e];
       const long long bits = __double_as_longlong(sum + 0.0);
-      if (lane == 0) dkey[e] = sum != sum ? 0ull : (unsigned long long)(bits ^ (bits >> 63 | (long long)0x8000000000000000ull));
+      if (lane == 0) {
+        dkey[e] = sum != sum ? 0ull : (unsigned long long)(bits ^ (bits >> 63 | (long long)0x8000000000000000ull));
+        val[e].x = (float)sum;
+      }
     }
   }
   named_bar_sync(3, 128);
@@ -469,7 +479,7 @@ __device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, T
   named_bar_sync(3, 128);
   // the rank of an expert among all: four keys a look, two experts at once
   // lowest that a selected logit may be, highest that another may be
-  float lo = INFINITY, hi = -INFINITY, most = 0.0f;
+  float lo = INFINITY, hi = -INFINITY, most = 0.0f;  // (most: the error, infinite where a selected one is too far off)
 #pragma unroll 1
   for (int e = tid; e < ((p.E + 127) & ~127); e += 256) {
     const int e2 = e + 128;
@@ -490,7 +500,7 @@ __device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, T
       const bool in = at < p.E && (i ? rank2 : rank) < k;
       if (in) lo = fminf(lo, q.x - q.y);
       else if (at < p.E) hi = fmaxf(hi, q.x + q.y);
-      most = fmaxf(most, q.y);
+      most = fmaxf(most, in && too_far_off(q) ? INFINITY : q.y);
       const uint32_t w = __ballot_sync(0xffffffffu, in);
       if (lane == 0) s.words[at >> 5] = w;
     }
@@ -505,7 +515,7 @@ __device__ __noinline__ void token_topk(const DecodeParams& p, int t, int tid, T
   named_bar_sync(3, 128);
 #pragma unroll 1
   for (int w = 0; w < 4; ++w) lo = fminf(lo, s.range[0][w]), hi = fmaxf(hi, s.range[1][w]), most = fmaxf(most, s.range[2][w]);
-  if (most > 0.0f && lo <= hi) {  // (exact logits that are equal are ties, decided above)
+  if (most > 0.0f && (lo <= hi || most == INFINITY)) {  // (exact logits that are equal are ties, decided above)
     decide_fp64(p, t, tid, lo, hi, s, val, dkey);
   }
   // slots in ascending order: the selected experts below

@@ -401,3 +401,19 @@ def test_tokens_of_zeros_among_small_ones():
     out, idx, w = c.run()
     assert torch.equal(idx.long(), c.route()[0])
     assert torch.equal(idx[[1, 3]], torch.arange(3, dtype=torch.int32, device="cuda").expand(2, 3))
+
+
+@pytest.mark.parametrize("T", [3, 64])
+@pytest.mark.parametrize("score,bias", [("softmax", False), ("sigmoid", False), ("softmax", True)])
+def test_weights_where_parts_cancel(T, score, bias):
+    """The logits that decide are the weights', too: fp64 sums rounded once, off by 2^-24 of at most 10."""
+    c = cancelling(T + 1, T=T, score=score, bias=bias)
+    if bias:  # held out and forced by a large bias, as any others are
+        c.w["b_router"][2], c.w["b_router"][9] = -1e9, 3.0
+    check(c)
+
+
+def test_weights_of_few_experts_all_in():
+    """Nothing to select: weights alone."""
+    c = cancelling(5, T=6, E=4, k=4, score="softmax")
+    check(c)
