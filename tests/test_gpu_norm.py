@@ -441,3 +441,47 @@ def test_refusals():
     refused(bad, rg.moe_norm_bwd, c.plan, 4, w, st, {"pre_bias": st}, **bk)
     refused(bad, rg.moe_norm_bwd, c.plan, 4, {}, st, {"gate": st}, **bk)
     refused(rg.MOE_ERR_WORKSPACE_TOO_SMALL, rg.moe_norm_bwd, c.plan, 4, w, st, g, **bk, workspace_bytes=ws.numel() - 1)
+
+
+# rows enough for the forms that keep two of them a CTA ahead and the weights in shared memory:
+# whole vectors in all threads, not in all, elements with the parameters beside the rows and without
+LARGE = [(700, 7168), (1300, 5952), (1000, 8192), (2500, 2048), (1300, 2053), (400, 5951), (400, 8191), (700, 8200)]
+
+
+@pytest.mark.parametrize("T,D", LARGE)
+@pytest.mark.parametrize("kw", [dict(), dict(stream="fp32", branch="bf16", x_scale=0.75), dict(kind="layer", bias=True, stream="fp16", branch="fp16"),
+                                dict(gate="vector", o_scale=0.5), dict(kind="layer", bias=True, gate="rows")])
+def test_forward_of_large_batches_is_that_of_rows(T, D, kw):
+    """A batch's bits are those of its rows alone, of two calls, of a call in place and of one that does not write y."""
+    c = Case(T, D, seed=T, **kw)
+    want = forward(c)
+    assert torch.equal(forward(c, y=False)["h"], want["h"])
+    x, o = c.vx.clone(), c.vo.clone()
+    rg.moe_norm(c.plan, T, c.params, x=x, o=o, y=x, h=o)
+    assert torch.equal(x, want["y"]) and torch.equal(o, want["h"])
+    some = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    few = {n: torch.empty(5, *t.shape[1:], dtype=t.dtype, device="cuda") for n, t in want.items()}
+    p = {**c.params, "gate": c.params["gate"][some].contiguous()} if c.gate == "rows" else c.params
+    rg.moe_norm(c.plan, 5, p, x=c.vx[some].contiguous(), o=c.vo[some].contiguous(), **few)
+    for n in want:
+        assert torch.equal(few[n], want[n][some]), n
+    same = dict(kind=c.kind, stream_dtype=c.stream, branch_dtype=c.branch, eps=1e-5)
+    a = rg.moe_norm_plan_create(D, post=True, pre=False, x_scale=c.x_scale, o_scale=c.o_scale, **same)
+    b = rg.moe_norm_plan_create(D, post=False, pre=True, **same)
+    y, h = torch.empty_like(want["y"]), torch.empty_like(want["h"])
+    rg.moe_norm(a, T, {n: v for n, v in c.params.items() if not n.startswith("pre")}, x=c.vx, o=c.vo, y=y)
+    rg.moe_norm(b, T, {n: v for n, v in c.params.items() if n.startswith("pre")}, x=y, h=h)
+    assert torch.equal(y, want["y"]) and torch.equal(h, want["h"])
+
+
+@pytest.mark.parametrize("T,D", LARGE)
+@pytest.mark.parametrize("kw", [dict(), dict(gate="vector", stream="fp32", branch="bf16"), dict(kind="layer", bias=True)])
+def test_backward_of_large_batches_in_place(T, D, kw):
+    c = Case(T, D, seed=T, **kw)
+    state = c.gen.get_state()
+    a = backward(c)
+    c.gen.set_state(state)
+    b = backward(c, inplace=True)
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["do"], b["do"])
+    for n in a["grads"]:
+        assert torch.equal(a["grads"][n], b["grads"][n]), n
