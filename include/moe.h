@@ -611,8 +611,9 @@ size_t moe_decode_workspace_bytes(const moe_plan* plan, int64_t T);
  * The selection is that of exact logits (with the bias; ties to the lower id):
  * where fp32 sums cannot tell the k-th logit from the next, fp64 sums decide.
  * (Logits or partial sums of 2^128 and more are infinities or NaN here.)  The weights
- * are those of logits off by 2^-9 at most (10^-6 for unit tokens): where parts
- * cancel so far that fp32 sums may miss a selected one by more, fp64 sums take their place.
+ * are those of logits off by 2^-6 at most, in truth a small part of it (10^-6 for unit
+ * tokens): where parts cancel so far that fp32 sums may miss a selected one by more, fp64
+ * sums take their place.
  * The launch is cooperative.  Two calls on the same inputs give the same bits; a
  * token's last bits may depend on which other tokens are in the call.  moe_get_status reads
  * the call's status from `workspace` (MOE_STATUS_TIMEOUT: a wait inside ran out).

@@ -389,10 +389,12 @@ static_assert(sizeof(DecodeSched::w) >= E_MAX * 8, "keys in fp64 lie where the w
 static_assert(DEC_OWN_TOPK * TOPK_MAX <= 128, "a thread a route");
 static_assert(sizeof(TopkScratch) <= sizeof(DecodeSched::mask), "scratch of the selection lies where the masks come to lie");
 
-// What a selected logit may be off by besides its own rounding to fp32, and how much of
-// that its weight bears: 2^-9 in the logit is at most 2^-8 of the weight, half a step of the
-// bf16 output.  (Unit tokens and router rows of 7168: 10^-4 at most, in truth 10^-6.)
-constexpr float DEC_LOGIT_TOL = 1.0f / 512.0f;
+// What a selected logit may be off by, besides its own rounding to fp32, before fp64
+// sums take its place for the weight's sake.  The bound holds for any order of signs; sums
+// whose parts cancel from 10^5 to 1 are off by a 220th of it at most (2^14 of them), so
+// 2^-6 means weights within 10^-4.  Unit tokens and router rows have bounds of 10^-4.  At
+// 2^-9 rows of 16 times that length pay for it already (one token of 256 experts 136 -> 196 us).
+constexpr float DEC_LOGIT_TOL = 1.0f / 64.0f;
 __device__ __forceinline__ bool too_far_off(float2 q) { return fmaf(fabsf(q.x), -1.0f / 16777216.0f, q.y) > DEC_LOGIT_TOL; }
 
 // The selection of token t where fp32 left it open, by the epilogue's 128 threads:
