@@ -176,14 +176,14 @@ __device__ __forceinline__ void cp_async16(char* smem, const void* g) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(g) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the `n` newest groups of this thread have landed (n up to 5)
+// all but the `n` newest groups of this thread have landed (n up to 3)
+constexpr int CP_ASYNC_MOST = 3;
+static_assert(2 * NORM_FWD_STAGES - 1 <= CP_ASYNC_MOST && NORM_BWD_STAGES - 1 <= CP_ASYNC_MOST, "groups under way in a ring");
 __device__ __forceinline__ void cp_async_wait(int n) {
   if (n <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
   else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
   else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (n == 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (n == 4) asm volatile("cp.async.wait_group 4;" ::: "memory");
-  else asm volatile("cp.async.wait_group 5;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

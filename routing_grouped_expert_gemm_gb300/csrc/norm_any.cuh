@@ -24,6 +24,7 @@ constexpr int ANY_FWD = 8;
 constexpr int any_bwd_per(int64_t D) { return D <= 4096 ? 4 : 8; }
 constexpr int ANY_MAX_WARPS = 32, ANY_RESIDENT = 1024;  // (threads an SM)
 constexpr int ANY_STAGES = 4, ANY_MAX_CTAS = 32;
+static_assert(ANY_STAGES - 1 <= CP_ASYNC_MOST, "groups under way in a ring");
 __host__ __device__ constexpr int any_slot(int64_t D, int dt) { return (int)((D * esize(dt) + 31) & ~15); }
 
 __device__ __forceinline__ float load_any(const void* p, int e, int dt) {
