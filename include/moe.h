@@ -738,7 +738,7 @@ size_t moe_norm_workspace_bytes(const moe_norm_plan* plan, int64_t T);
  *   dx   or NULL: not written; it may be dy itself
  *   d_o  or NULL: not written; it may be dh itself
  *   workspace  at least moe_norm_workspace_bytes(plan, T) bytes, 256-byte aligned,
- *              no initialisation needed
+ *              no initialisation needed; not to be shared by calls that overlap
  * With T = 0 the summed gradients are zeros.  No floating-point atomics: two
  * calls give the same bits.  One launch, and a second one for the sums.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_WORKSPACE_TOO_SMALL, MOE_ERR_CUDA.

@@ -57,10 +57,12 @@ constexpr int DEC_EARLY = 2;                        // steps loaded before the g
 constexpr int DEC_QUEUE = 4;                        // claimed units on their way to the roles of a CTA
 constexpr int DEC_SMEM = 227 * 1024;                // shared memory of a CTA: as many stages as fit
 
-// Steps of a unit, for `total` steps on `ctas` CTAs: a CTA's share in 32 units,
+// Steps that a unit should have, for `total` steps on `ctas` CTAs: a CTA's share in 32 units,
 // though not so many that a unit is below 12 steps (4.5 us of an SM's loads), or where
-// the share is small, 8 units of at least 4; and its sums (ncap columns) stay below an
-// eighth of its weights.
+// the share is small, 8 units of at least 4; and sums (ncap columns) below an eighth of its
+// weights.  A projection is cut into equal units near that, so one may have down to half as
+// many, and no unit has more than its tile's projection (4 steps of 256 columns: sums of 64
+// tokens are then half of its weights).
 __host__ __device__ inline int dec_unit_steps(int total, int ctas, int ncap) {
   const int share = (total + ctas - 1) / ctas;
   int q = share / 8;

@@ -4,9 +4,10 @@
 // A CTA works on several rows at a time, each in a group of threads of its own, so
 // that one row's barriers are another's work; a thread takes two vectors (four past
 // 8192): with one, what a thread does besides its elements (sums, barriers, addresses)
-// is most of its instructions (194 us), with four too few warps hide a row's latency
-// (221 us).  A group's rows are grid rows apart: with neighbouring rows 161 us.  The weights are in shared memory as fp32 where the CTA has rows enough
-// for that to pay.
+// is most of its instructions (194 us, two then took 160), with four too few warps hide
+// a row's latency (221 us).  A group's rows are grid rows apart: with neighbouring rows 161
+// us, where this took 149.  The weights are in shared memory as fp32 where the CTA has rows
+// enough for that to pay.
 #include "norm.cuh"
 
 namespace moe {
